@@ -13,6 +13,10 @@ Functions mirror the C names:
 * :func:`mx_scale_relayout`, :func:`mx_scale_tiled_bytes` -- scale-factor relayout.
 * :func:`mx_quantize`, :func:`fp8_group_quantize`, :func:`fp8_block_quantize` -- the
   quantisers that make the GEMMs' operands from BF16 / FP32 tensors.
+* :func:`moe_route`, :func:`moe_route_backward`, :func:`moe_plan`, :func:`moe_combine`,
+  :func:`moe_combine_backward` -- the expert layer around the grouped GEMMs.
+* :func:`int8_quantize`, :func:`int8_gemm`, :func:`grouped_int8_gemm` -- INT8 products with
+  scales for each token and channel.
 * :func:`device_status`, :func:`reserve_workspace`, :func:`set_wait_limit_ns`,
   :func:`launch_count`, :func:`probe_wait_timeout`, :func:`status_string`.
 """
@@ -28,6 +32,9 @@ from .build import LIB_PATH, build
 
 __all__ = ["mx_gemm", "mx_gemm_tiled", "mx_gemm_noalloc", "grouped_fp8_gemm", "grouped_fp8_pack_weights",
            "grouped_bf16_gemm",
+           "moe_route", "moe_route_backward", "moe_plan", "moe_plan_workspace_bytes",
+           "moe_combine", "moe_combine_backward",
+           "int8_quantize", "int8_gemm", "grouped_int8_gemm",
            "mx_scale_relayout",
            "mx_quantize", "fp8_group_quantize", "fp8_block_quantize", "autotune_configure",
            "autotune_lookup",
@@ -95,6 +102,17 @@ def load(path: str | None = None):
         lib.mx_gemm_tiled_bias_act.argtypes = [p, p, p, p, p, i32, p, i64, i64, i64, i32, i32, i32, p]
         lib.fp8_group_quantize.argtypes = [p, i32, i64, i64, p, i32, p, p, p]
         lib.fp8_block_quantize.argtypes = [p, i32, i64, i64, i64, p, p, p]
+        f32 = ctypes.c_float
+        lib.moe_route.argtypes = [p, i32, i64, i32, i32, i32, p, i32, i32, i32, i32, f32, p, p, p]
+        lib.moe_route_backward.argtypes = [p, i32, i64, i32, i32, i32, i32, f32, p, p, p, p]
+        lib.moe_plan.argtypes = [p, i64, i32, i32, p, p, p, p]
+        lib.moe_plan_workspace_bytes.argtypes = [i64, i32, i32]
+        lib.moe_plan_workspace_bytes.restype = i64
+        lib.moe_combine.argtypes = [p, i32, i64, i64, p, p, i64, i32, p, p]
+        lib.moe_combine_backward.argtypes = [p, i32, i64, p, p, p, p, i64, i32, p, p, p]
+        lib.int8_quantize.argtypes = [p, i32, i64, i64, p, i32, i64, p, p, p]
+        lib.int8_gemm.argtypes = [p, p, p, p, p, p, i32, i64, i64, i64, p]
+        lib.grouped_int8_gemm.argtypes = [p, p, p, p, p, i32, p, i64, i32, i64, i64, p]
         for name in ("mx_gemm", "mx_gemm_tiled", "mx_gemm_noalloc", "grouped_fp8_gemm",
                      "grouped_fp8_gemm_packed", "grouped_fp8_pack_weights",
                      "mx_scale_relayout",
@@ -103,7 +121,9 @@ def load(path: str | None = None):
                      "grouped_bf16_gemm", "bsmma_set_grouped_variant",
                      "bsmma_probe_wait_timeout", "mx_quantize", "fp8_group_quantize",
                      "fp8_block_quantize", "mx_gemm_bias_act", "mx_gemm_tiled_bias_act",
-                     "bsmma_autotune_configure"):
+                     "bsmma_autotune_configure", "moe_route", "moe_route_backward", "moe_plan",
+                     "moe_combine", "moe_combine_backward", "int8_quantize", "int8_gemm",
+                     "grouped_int8_gemm"):
             getattr(lib, name).restype = i32
         _lib = lib
         return lib
@@ -350,6 +370,178 @@ def fp8_block_quantize(w, codes=None, scales=None, stream=None):
     _check(load().fp8_block_quantize(_ptr(w), _dtype_code(w), G, N, K, _ptr(codes), _ptr(scales),
                                      _stream(stream)), "fp8_block_quantize")
     return codes, scales
+
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _dtype_of(t, what: str) -> int:
+    if t.dtype not in DTYPES:
+        raise ValueError(f"{what} must be bfloat16 or float32")
+    return DTYPES[t.dtype]
+
+
+def _expect(t, dtype, shape, what: str):
+    """`t` (None passes) has this dtype and shape."""
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}, "
+                         f"not {t.dtype} of {tuple(t.shape)}")
+
+
+def moe_route(logits, k, score="softmax", bias=None, groups=1, topk_groups=1, group_top=1,
+              renormalize=True, scale=1.0, ids=None, weights=None, stream=None):
+    """Chooses k experts a token from logits [T, E] (BF16 or FP32) -> (ids int32 [T, k],
+    weights float32 [T, k]); see ``moe_route`` in bsmma.h.  ``score``: 'softmax' or
+    'sigmoid'; ``bias``: float32 [E], added to the scores for the choice alone."""
+    T, E = logits.shape
+    _expect(bias, torch.float32, (E,), "bias")
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    _expect(ids, torch.int32, (T, k), "ids")
+    _expect(weights, torch.float32, (T, k), "weights")
+    _check(load().moe_route(_ptr(logits), _dtype_of(logits, "logits"), T, E, k, SCORES[score],
+                            _ptr(bias), groups, topk_groups, group_top, int(bool(renormalize)),
+                            scale, _ptr(ids), _ptr(weights), _stream(stream)), "moe_route")
+    return ids, weights
+
+
+def moe_route_backward(logits, ids, dweights, score="softmax", renormalize=True, scale=1.0,
+                       dlogits=None, stream=None):
+    """The gradient of :func:`moe_route`'s weights in its logits, the choice held fixed ->
+    dlogits [T, E] of the logits' dtype."""
+    T, E = logits.shape
+    k = ids.shape[1]
+    _expect(ids, torch.int32, (T, k), "ids")
+    _expect(dweights, torch.float32, (T, k), "dweights")
+    if dlogits is None:
+        dlogits = torch.empty_like(logits)
+    _expect(dlogits, logits.dtype, (T, E), "dlogits")
+    _check(load().moe_route_backward(_ptr(logits), _dtype_of(logits, "logits"), T, E, k,
+                                     SCORES[score], int(bool(renormalize)), scale, _ptr(ids),
+                                     _ptr(dweights), _ptr(dlogits), _stream(stream)),
+           "moe_route_backward")
+    return dlogits
+
+
+def moe_plan_workspace_bytes(T: int, k: int, E: int) -> int:
+    """Workspace of :func:`moe_plan` (reserve it before a capture)."""
+    return int(load().moe_plan_workspace_bytes(T, k, E))
+
+
+def moe_plan(ids, experts, m_sizes=None, src=None, pos=None, stream=None):
+    """The expert order of the slots ids int32 [T, k] -> (m_sizes int64 [experts], src int32
+    [T * k], pos int32 [T, k]); see ``moe_plan`` in bsmma.h."""
+    T, k = ids.shape
+    _expect(ids, torch.int32, (T, k), "ids")
+    if m_sizes is None:
+        m_sizes = torch.empty(experts, dtype=torch.int64, device=ids.device)
+    if src is None:
+        src = torch.empty(T * k, dtype=torch.int32, device=ids.device)
+    if pos is None:
+        pos = torch.empty((T, k), dtype=torch.int32, device=ids.device)
+    _expect(m_sizes, torch.int64, (experts,), "m_sizes")
+    _expect(src, torch.int32, (T * k,), "src")
+    _expect(pos, torch.int32, (T, k), "pos")
+    _check(load().moe_plan(_ptr(ids), T, k, experts, _ptr(m_sizes), _ptr(src), _ptr(pos),
+                           _stream(stream)), "moe_plan")
+    return m_sizes, src, pos
+
+
+def moe_combine(Y, pos, weights=None, out=None, stream=None):
+    """out[t] = sum_j weights[t, j] * Y[pos[t, j]] -> [T, H] of Y's dtype (BF16 or FP32);
+    without weights, the plain sum.  See ``moe_combine`` in bsmma.h."""
+    R, H = Y.shape
+    T, k = pos.shape
+    _expect(pos, torch.int32, (T, k), "pos")
+    _expect(weights, torch.float32, (T, k), "weights")
+    if out is None:
+        out = torch.empty((T, H), dtype=Y.dtype, device=Y.device)
+    _expect(out, Y.dtype, (T, H), "out")
+    _check(load().moe_combine(_ptr(Y), _dtype_of(Y, "Y"), R, H, _ptr(pos), _ptr(weights), T, k,
+                              _ptr(out), _stream(stream)), "moe_combine")
+    return out
+
+
+def moe_combine_backward(dout, Y, src, pos, weights=None, dY=None, dweights=None, stream=None):
+    """The gradients of :func:`moe_combine` -> (dY [T * k, H], dweights float32 [T, k]);
+    without weights only dY (dweights None), and Y may be None."""
+    T, H = dout.shape
+    k = pos.shape[1]
+    _expect(pos, torch.int32, (T, k), "pos")
+    _expect(src, torch.int32, (T * k,), "src")
+    _expect(weights, torch.float32, (T, k), "weights")
+    _expect(Y, dout.dtype, (T * k, H), "Y")
+    if weights is not None and Y is None:
+        raise ValueError("Y is needed for the gradient of the weights")
+    if dY is None:
+        dY = torch.empty((T * k, H), dtype=dout.dtype, device=dout.device)
+    if weights is not None and dweights is None:
+        dweights = torch.empty((T, k), dtype=torch.float32, device=dout.device)
+    _expect(dY, dout.dtype, (T * k, H), "dY")
+    _expect(dweights, torch.float32, (T, k), "dweights")
+    _check(load().moe_combine_backward(_ptr(dout), _dtype_of(dout, "dout"), H, _ptr(Y), _ptr(src),
+                                       _ptr(pos), _ptr(weights), T, k, _ptr(dY), _ptr(dweights),
+                                       _stream(stream)), "moe_combine_backward")
+    return dY, dweights
+
+
+def int8_quantize(x, src=None, k=1, codes=None, scales=None, stream=None):
+    """Symmetric INT8 quantisation by row of x [rows, K] (BF16 or FP32) -> (codes int8,
+    scales float32).  With ``src`` (moe_plan's, int32) output row r is row src[r] // k of x,
+    or zeros where src[r] < 0.  See ``int8_quantize`` in bsmma.h."""
+    x_rows, K = x.shape
+    rows = x_rows if src is None else src.numel()
+    _expect(src, torch.int32, (rows,), "src")
+    if codes is None:
+        codes = torch.empty((rows, K), dtype=torch.int8, device=x.device)
+    if scales is None:
+        scales = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _expect(codes, torch.int8, (rows, K), "codes")
+    _expect(scales, torch.float32, (rows,), "scales")
+    _check(load().int8_quantize(_ptr(x), _dtype_of(x, "x"), x_rows, K, _ptr(src), k, rows,
+                                _ptr(codes), _ptr(scales), _stream(stream)), "int8_quantize")
+    return codes, scales
+
+
+def int8_gemm(A, sA, B, sB, bias=None, out=None, dtype=torch.bfloat16, stream=None):
+    """D[m, n] = sA[m] * sB[n] * (A . B^T)[m, n] (+ bias[n]) for A int8 [M, K], B int8 [N, K],
+    in ``dtype`` (BF16 or FP32).  See ``int8_gemm`` in bsmma.h."""
+    M, K = A.shape
+    N = B.shape[0]
+    _expect(A, torch.int8, (M, K), "A")
+    _expect(B, torch.int8, (N, K), "B")
+    _expect(sA, torch.float32, (M,), "sA")
+    _expect(sB, torch.float32, (N,), "sB")
+    _expect(bias, torch.bfloat16, (N,), "bias")
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=A.device)
+    _expect(out, out.dtype, (M, N), "out")
+    _check(load().int8_gemm(_ptr(A), _ptr(sA), _ptr(B), _ptr(sB), _ptr(bias), _ptr(out),
+                            _dtype_of(out, "out"), M, N, K, _stream(stream)), "int8_gemm")
+    return out
+
+
+def grouped_int8_gemm(X, sX, W, sW, m_sizes, out=None, dtype=torch.bfloat16, stream=None):
+    """:func:`int8_gemm` for each expert's rows: X int8 [total_M, K], sX float32 [total_M],
+    W int8 [G, N, K], sW float32 [G, N], m_sizes int64 [G] on the device (it may sum to less
+    than total_M; the rows past it are left as they are).  See ``grouped_int8_gemm``."""
+    total_M, K = X.shape
+    G, N, _ = W.shape
+    _expect(X, torch.int8, (total_M, K), "X")
+    _expect(W, torch.int8, (G, N, K), "W")
+    _expect(sX, torch.float32, (total_M,), "sX")
+    _expect(sW, torch.float32, (G, N), "sW")
+    _expect(m_sizes, torch.int64, (G,), "m_sizes")
+    if out is None:
+        out = torch.empty((total_M, N), dtype=dtype, device=W.device)
+    _expect(out, out.dtype, (total_M, N), "out")
+    _check(load().grouped_int8_gemm(_ptr(X) if total_M else None, _ptr(sX) if total_M else None,
+                                    _ptr(W), _ptr(sW), _ptr(out) if total_M else None,
+                                    _dtype_of(out, "out"), _ptr(m_sizes), total_M, G, N, K,
+                                    _stream(stream)), "grouped_int8_gemm")
+    return out
 
 
 def autotune_configure(enable=-1, cache_path=None):

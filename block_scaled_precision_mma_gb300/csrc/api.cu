@@ -525,6 +525,157 @@ bsmma_status fp8_block_quantize(const void* w, bsmma_dtype w_dtype, int64_t G, i
                                reinterpret_cast<cudaStream_t>(stream));
 }
 
+namespace {
+bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+bool known_dtype(bsmma_dtype d) { return d == BSMMA_BF16 || d == BSMMA_F32; }
+
+bsmma_status check_route(bsmma_dtype dtype, int64_t T, int E, int k, bsmma_moe_score score,
+                         int renormalize) {
+  if (!known_dtype(dtype) || (score != BSMMA_SOFTMAX && score != BSMMA_SIGMOID))
+    return BSMMA_ERR_INVALID_ARG;
+  if (T < 0 || T >= INT32_MAX || E < 1 || E > 1024 || k < 1 || k > 32 || k > E ||
+      (renormalize != 0 && renormalize != 1))
+    return BSMMA_ERR_INVALID_ARG;
+  return BSMMA_OK;
+}
+}  // namespace
+
+bsmma_status moe_route(const void* logits, bsmma_dtype logits_dtype, int64_t T, int E, int k,
+                       bsmma_moe_score score, const float* bias, int groups, int topk_groups,
+                       int group_top, int renormalize, float scale, int32_t* ids, float* weights,
+                       bsmma_stream stream) {
+  const bsmma_status st = check_route(logits_dtype, T, E, k, score, renormalize);
+  if (st != BSMMA_OK) return st;
+  if (groups < 1 || groups > 32 || E % groups != 0 || topk_groups < 1 || topk_groups > groups ||
+      group_top < 1 || group_top > 2 || k > topk_groups * (E / groups))
+    return BSMMA_ERR_INVALID_ARG;
+  if (T == 0) return BSMMA_OK;
+  if (!logits || !ids || !weights) return BSMMA_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned_to(ids, 4) || !aligned_to(weights, 4) || !aligned_to(bias, 4))
+    return BSMMA_ERR_MISALIGNED;
+  return launch_route(logits, logits_dtype == BSMMA_F32, T, E, k, score == BSMMA_SIGMOID, bias,
+                      groups, topk_groups, group_top, renormalize != 0, scale, ids, weights,
+                      reinterpret_cast<cudaStream_t>(stream));
+}
+
+bsmma_status moe_route_backward(const void* logits, bsmma_dtype logits_dtype, int64_t T, int E,
+                                int k, bsmma_moe_score score, int renormalize, float scale,
+                                const int32_t* ids, const float* dweights, void* dlogits,
+                                bsmma_stream stream) {
+  const bsmma_status st = check_route(logits_dtype, T, E, k, score, renormalize);
+  if (st != BSMMA_OK || T == 0) return st;
+  if (!logits || !ids || !dweights || !dlogits) return BSMMA_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(dlogits) || !aligned_to(ids, 4) || !aligned_to(dweights, 4))
+    return BSMMA_ERR_MISALIGNED;
+  return launch_route_backward(logits, logits_dtype == BSMMA_F32, T, E, k, score == BSMMA_SIGMOID,
+                               renormalize != 0, scale, ids, dweights, dlogits,
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+int64_t moe_plan_workspace_bytes(int64_t T, int k, int E) {
+  if (T <= 0 || k < 1 || E < 1 || T >= INT32_MAX) return 0;
+  return plan_workspace_bytes(T * k, E);
+}
+
+bsmma_status moe_plan(const int32_t* ids, int64_t T, int k, int E, int64_t* m_sizes, int32_t* src,
+                      int32_t* pos, bsmma_stream stream) {
+  if (T < 0 || T >= INT32_MAX || k < 1 || E < 1 || E > 1024 || T * k >= INT32_MAX - 4096)
+    return BSMMA_ERR_INVALID_ARG;
+  if (!m_sizes) return BSMMA_ERR_INVALID_ARG;
+  if (!aligned_to(m_sizes, 8)) return BSMMA_ERR_MISALIGNED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) return cuda_ok(cudaMemsetAsync(m_sizes, 0, static_cast<size_t>(E) * 8, s));
+  if (!ids || !src || !pos) return BSMMA_ERR_INVALID_ARG;
+  if (!aligned_to(ids, 4) || !aligned_to(src, 4) || !aligned_to(pos, 4)) return BSMMA_ERR_MISALIGNED;
+  void* ws = nullptr;
+  const int64_t bytes = plan_workspace_bytes(T * k, E);
+  if (bytes > 0) {
+    const bsmma_status st = get_workspace(bytes, s, &ws);
+    if (st != BSMMA_OK) return st;
+  }
+  return launch_plan(ids, T * k, E, m_sizes, src, pos, ws, s);
+}
+
+bsmma_status int8_quantize(const void* x, bsmma_dtype x_dtype, int64_t x_rows, int64_t K,
+                           const int32_t* src, int k, int64_t rows, int8_t* codes, float* scales,
+                           bsmma_stream stream) {
+  if (!known_dtype(x_dtype) || x_rows < 0 || rows < 0 || rows >= INT32_MAX || K <= 0 ||
+      K % 16 != 0 || K >= INT32_MAX || k < 1)
+    return BSMMA_ERR_INVALID_ARG;
+  if (!src && rows != x_rows) return BSMMA_ERR_INVALID_ARG;
+  if (rows == 0) return BSMMA_OK;
+  if ((x_rows > 0 && !x) || !codes || !scales) return BSMMA_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(codes) || !aligned_to(scales, 4) || !aligned_to(src, 4))
+    return BSMMA_ERR_MISALIGNED;
+  return launch_int8_quantize(x, x_dtype == BSMMA_F32, x_rows, rows, K, src, k, codes, scales,
+                              reinterpret_cast<cudaStream_t>(stream));
+}
+
+bsmma_status int8_gemm(const int8_t* A, const float* sA, const int8_t* B, const float* sB,
+                       const void* bias, void* D, bsmma_dtype d_dtype, int64_t M, int64_t N,
+                       int64_t K, bsmma_stream stream) {
+  if (!known_dtype(d_dtype) || M < 0 || N < 0 || K < 0 || K % 16 != 0) return BSMMA_ERR_INVALID_ARG;
+  if (M >= INT32_MAX || N >= INT32_MAX || K >= INT32_MAX) return BSMMA_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return BSMMA_OK;
+  if (!D || !sA || !sB || (K > 0 && (!A || !B))) return BSMMA_ERR_INVALID_ARG;
+  if (!aligned16(A) || !aligned16(B) || !aligned16(D) || !aligned_to(sA, 4) || !aligned_to(sB, 4) ||
+      !aligned_to(bias, 2))
+    return BSMMA_ERR_MISALIGNED;
+  return launch_int8_gemm(A, sA, B, sB, bias, D, d_dtype == BSMMA_F32, nullptr, M, 1, N, K,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+bsmma_status grouped_int8_gemm(const int8_t* X, const float* sX, const int8_t* W, const float* sW,
+                               void* D, bsmma_dtype d_dtype, const int64_t* m_sizes,
+                               int64_t total_M, int G, int64_t N, int64_t K, bsmma_stream stream) {
+  if (!known_dtype(d_dtype) || G < 1 || G > 1024 || total_M < 0 || N <= 0 || K <= 0 || K % 16 != 0)
+    return BSMMA_ERR_INVALID_ARG;
+  if (total_M >= INT32_MAX || K >= INT32_MAX || N >= INT32_MAX ||
+      static_cast<int64_t>(G) * N >= INT32_MAX)
+    return BSMMA_ERR_INVALID_ARG;
+  if (!W || !sW || !m_sizes) return BSMMA_ERR_INVALID_ARG;
+  if (total_M > 0 && (!X || !sX || !D)) return BSMMA_ERR_INVALID_ARG;
+  if (!aligned16(W) || !aligned_to(sW, 4) || !aligned_to(m_sizes, 8) || !aligned16(X) ||
+      !aligned_to(sX, 4) || !aligned16(D))
+    return BSMMA_ERR_MISALIGNED;
+  return launch_int8_gemm(X, sX, W, sW, nullptr, D, d_dtype == BSMMA_F32, m_sizes, total_M, G, N, K,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+namespace {
+bsmma_status check_combine(bsmma_dtype dtype, int64_t R, int64_t H, int64_t T, int k) {
+  if (!known_dtype(dtype) || H <= 0 || H >= INT32_MAX || T < 0 || T >= INT32_MAX || R < 0 ||
+      R >= INT32_MAX || k < 1 || k > 32 || T * k >= INT32_MAX)
+    return BSMMA_ERR_INVALID_ARG;
+  if (H % (dtype == BSMMA_F32 ? 4 : 8) != 0) return BSMMA_ERR_MISALIGNED;
+  return BSMMA_OK;
+}
+}  // namespace
+
+bsmma_status moe_combine(const void* Y, bsmma_dtype dtype, int64_t R, int64_t H, const int32_t* pos,
+                         const float* weights, int64_t T, int k, void* out, bsmma_stream stream) {
+  const bsmma_status st = check_combine(dtype, R, H, T, k);
+  if (st != BSMMA_OK || T == 0) return st;
+  if ((R > 0 && !Y) || !pos || !out) return BSMMA_ERR_INVALID_ARG;
+  if (!aligned16(Y) || !aligned16(out) || !aligned_to(pos, 4) || !aligned_to(weights, 4))
+    return BSMMA_ERR_MISALIGNED;
+  return launch_combine(Y, dtype == BSMMA_F32, R, H, pos, weights, T, k, out,
+                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+bsmma_status moe_combine_backward(const void* dout, bsmma_dtype dtype, int64_t H, const void* Y,
+                                  const int32_t* src, const int32_t* pos, const float* weights,
+                                  int64_t T, int k, void* dY, float* dweights, bsmma_stream stream) {
+  const bsmma_status st = check_combine(dtype, 0, H, T, k);
+  if (st != BSMMA_OK || T == 0) return st;
+  if (!dout || (dweights && !Y) || !src || !pos || !dY) return BSMMA_ERR_INVALID_ARG;
+  if (!aligned16(dout) || !aligned16(Y) || !aligned16(dY) || !aligned_to(src, 4) ||
+      !aligned_to(pos, 4) || !aligned_to(weights, 4) || !aligned_to(dweights, 4))
+    return BSMMA_ERR_MISALIGNED;
+  return launch_combine_backward(dout, dtype == BSMMA_F32, H, Y, src, pos, weights, T, k, dY,
+                                 dweights, reinterpret_cast<cudaStream_t>(stream));
+}
+
 bsmma_status bsmma_reserve_workspace(int64_t bytes, bsmma_stream stream) {
   if (bytes < 0) return BSMMA_ERR_INVALID_ARG;
   void* p = nullptr;

@@ -91,6 +91,32 @@ bsmma_status launch_group_quantize(const void* x, bool f32, int64_t total_M, int
 bsmma_status launch_block_quantize(const void* w, bool f32, int64_t G, int64_t N, int64_t K,
                                    uint8_t* codes, float* scales, cudaStream_t stream);
 
+// Expert layer (arguments already validated by the entry points).
+bsmma_status launch_route(const void* logits, bool f32, int64_t T, int E, int k, bool sigmoid,
+                          const float* bias, int groups, int topk_groups, int group_top,
+                          bool renormalize, float scale, int32_t* ids, float* weights,
+                          cudaStream_t stream);
+bsmma_status launch_route_backward(const void* logits, bool f32, int64_t T, int E, int k,
+                                   bool sigmoid, bool renormalize, float scale, const int32_t* ids,
+                                   const float* dweights, void* dlogits, cudaStream_t stream);
+int64_t plan_workspace_bytes(int64_t S, int E);
+bsmma_status launch_plan(const int32_t* ids, int64_t S, int E, int64_t* m_sizes, int32_t* src,
+                         int32_t* pos, void* workspace, cudaStream_t stream);
+bsmma_status launch_combine(const void* y, bool f32, int64_t R, int64_t H, const int32_t* pos,
+                            const float* weights, int64_t T, int k, void* out,
+                            cudaStream_t stream);
+bsmma_status launch_combine_backward(const void* dout, bool f32, int64_t H, const void* y,
+                                     const int32_t* src, const int32_t* pos, const float* weights,
+                                     int64_t T, int k, void* dy, float* dweights,
+                                     cudaStream_t stream);
+bsmma_status launch_int8_quantize(const void* x, bool f32, int64_t x_rows, int64_t rows, int64_t K,
+                                  const int32_t* src, int k, int8_t* codes, float* scales,
+                                  cudaStream_t stream);
+// m_sizes nullptr: one group of total_M rows (G == 1).
+bsmma_status launch_int8_gemm(const int8_t* A, const float* sA, const int8_t* B, const float* sB,
+                              const void* bias, void* D, bool f32, const int64_t* m_sizes,
+                              int64_t total_M, int G, int64_t N, int64_t K, cudaStream_t stream);
+
 // Autotuning (opt-in): the cached choice for `key`, else -- when tuning is enabled and the
 // stream is not capturing -- the fastest of `candidates` timed with `launch`, else
 // `fallback`.

@@ -366,6 +366,135 @@ bsmma_status fp8_group_quantize(const void* x, bsmma_dtype x_dtype, int64_t tota
 bsmma_status fp8_block_quantize(const void* w, bsmma_dtype w_dtype, int64_t G, int64_t N,
                                 int64_t K, uint8_t* codes, float* scales, bsmma_stream stream);
 
+/*
+ * Expert layer.  The operators around the experts' products: a router chooses k experts a
+ * token (moe_route), the chosen slots are put in expert order (moe_plan), the tokens' rows
+ * go into that order, quantised on the way (int8_quantize), each expert multiplies its rows
+ * (grouped_int8_gemm; the FP8 and BF16 grouped GEMMs take the same order), and a token's
+ * rows come back as their weighted sum (moe_combine).  The source pages have no
+ * counterpart; the order they feed is their grouped GEMM's (m_sizes, uneven and empty
+ * groups).  A slot is (token t, choice j), number t*k + j.
+ *
+ * moe_route -- for each token, with x its E logits (BF16 or FP32):
+ *   score  s_e = exp(x_e) / sum_i exp(x_i) (softmax) or 1 / (1 + exp(-x_e)) (sigmoid);
+ *   key    c_e = s_e + bias_e with a bias, else x_e (both scores increase with x);
+ *   groups of E / groups consecutive experts, when topk_groups < groups: a group's value is
+ *          the sum of its group_top (1 or 2) largest keys -- for group_top 2 without a bias,
+ *          of its largest scores -- and only the topk_groups groups of largest value are
+ *          open;
+ *   ids    the k open experts of largest key, in decreasing order;
+ *   weight w_j = scale * s_j, divided by the sum of the chosen scores when renormalize
+ *          (0 when that sum is 0).
+ *   Every choice between equal values takes the lower index.  A logit of -inf or NaN closes
+ *   its expert (score 0, never chosen); +inf counts as the largest finite FP32.  A key that
+ *   is NaN or -inf is never chosen either.  Where fewer than k experts can be chosen, the
+ *   rest of the ids is -1 with weight 0: a token whose logits are all -inf gets k of them.
+ *   logits [T][E] 16-byte aligned; bias FP32 [E] or NULL; ids int32 [T][k]; weights FP32
+ *   [T][k].  Scores and sums are FP32.
+ * Preconditions: 1 <= E <= 1024, 1 <= groups <= 32 dividing E, 1 <= topk_groups <= groups,
+ *   group_top 1 or 2, 1 <= k <= 32, k <= topk_groups * (E / groups), 0 <= T < 2^31.
+ *   One launch (none when T == 0).
+ */
+typedef enum { BSMMA_SOFTMAX = 0, BSMMA_SIGMOID = 1 } bsmma_moe_score;
+bsmma_status moe_route(const void* logits, bsmma_dtype logits_dtype, int64_t T, int E, int k,
+                       bsmma_moe_score score, const float* bias, int groups, int topk_groups,
+                       int group_top, int renormalize, float scale, int32_t* ids, float* weights,
+                       bsmma_stream stream);
+
+/*
+ * moe_route_backward -- the gradient of moe_route's weights in its logits, the choice held
+ *   fixed (the bias and the groups only choose, so they have none).  ids: moe_route's (a
+ *   token's ids differ; -1 and ids >= E count as no choice); dweights FP32 [T][k]; dlogits
+ *   [T][E] of the logits' type, every element written (0 where a logit has no influence).
+ *   score, renormalize and scale as given to moe_route.
+ * Preconditions: those of moe_route.  One launch (none when T == 0).
+ */
+bsmma_status moe_route_backward(const void* logits, bsmma_dtype logits_dtype, int64_t T, int E,
+                                int k, bsmma_moe_score score, int renormalize, float scale,
+                                const int32_t* ids, const float* dweights, void* dlogits,
+                                bsmma_stream stream);
+
+/*
+ * moe_plan -- the expert order of T*k slots with expert numbers ids (int32 [T][k]; -1 or
+ *   anything outside 0..E-1: the slot is not used):
+ *   m_sizes int64 [E]   rows of each expert, what the grouped GEMMs take;
+ *   src     int32 [T*k] the slot of each row; an expert's rows are in increasing order of
+ *                       their slots; -1 for the rows past the last used one;
+ *   pos     int32 [T][k] the row of each slot, -1 for one that is not used.
+ *   The result depends on nothing but ids.  With unused slots m_sizes sums to less than
+ *   T*k: grouped_int8_gemm takes that, the other grouped GEMMs want total_M equal to the sum.
+ * Preconditions: 1 <= E <= 1024, k >= 1, T >= 0, T*k < 2^31 - 4096.  Up to 4096 slots one
+ *   launch; more take three and moe_plan_workspace_bytes(T, k, E) bytes of the stream's
+ *   workspace (mx_gemm's; reserve it before a capture).  T == 0 only clears m_sizes.
+ */
+bsmma_status moe_plan(const int32_t* ids, int64_t T, int k, int E, int64_t* m_sizes, int32_t* src,
+                      int32_t* pos, bsmma_stream stream);
+int64_t moe_plan_workspace_bytes(int64_t T, int k, int E);
+
+/*
+ * int8_quantize -- symmetric INT8 quantisation by row (token), optionally of gathered rows:
+ *   row r of the output is row r of x (src NULL; rows == x_rows) or row src[r] / k of x
+ *   (src, k: moe_plan's); src[r] < 0 or past x gives a row of zeros.
+ *   s = amax * (1 / 127), both steps in FP32 (1 when that is 0), code = rint(x / s), the FP32 quotient rounded
+ *   half to even, within [-127, 127].
+ *   x [x_rows][K] BF16 or FP32; codes int8 [rows][K]; scales FP32 [rows].
+ * Preconditions: K > 0, K % 16 == 0, K < 2^31, k >= 1, rows < 2^31, 16-byte-aligned x and
+ *   codes.  Inputs must be finite.  One launch (none when rows == 0).
+ */
+bsmma_status int8_quantize(const void* x, bsmma_dtype x_dtype, int64_t x_rows, int64_t K,
+                           const int32_t* src, int k, int64_t rows, int8_t* codes, float* scales,
+                           bsmma_stream stream);
+
+/*
+ * int8_gemm -- D[m][n] = sA[m] * sB[n] * sum_k A[m][k] * B[n][k] (+ bias[n]), the product of
+ *   8-bit integers with a scale for each token (row of A) and channel (row of B).
+ *   A int8 [M][K], B int8 [N][K], sA FP32 [M], sB FP32 [N], bias BF16 [N] or NULL, D [M][N]
+ *   BF16 or FP32 (d_dtype), rounded once.  sm_103a has no INT8 tcgen05 MMA; the operands are
+ *   widened to FP16, where an INT8 value and a product of two are exact, and summed in FP32:
+ *   the integer sum is exact while its partial sums stay below 2^24 (any K <= 1040; longer K
+ *   short of one-sided extremes), else rounded as FP32 sums are.  The order of the sum, and
+ *   so the result, is the same in every call with the same sizes.
+ * Preconditions: M, N, K >= 0, K % 16 == 0, M, N, K < 2^31 - 1, 16-byte-aligned A, B and D,
+ *   4-byte-aligned sA and sB, 2-byte-aligned bias.  N is not restricted.  M == 0 or N == 0
+ *   is a no-op; K == 0 writes the bias, or 0.
+ */
+bsmma_status int8_gemm(const int8_t* A, const float* sA, const int8_t* B, const float* sB,
+                       const void* bias, void* D, bsmma_dtype d_dtype, int64_t M, int64_t N,
+                       int64_t K, bsmma_stream stream);
+
+/*
+ * grouped_int8_gemm -- int8_gemm for each expert's rows:
+ *   D[r][n] = sX[r] * sW[g][n] * sum_k X[r][k] * W[g][n][k] for row r of group g.
+ *   X int8 [total_M][K], W int8 [G][N][K], sX FP32 [total_M], sW FP32 [G][N], m_sizes int64
+ *   [G] in DEVICE memory (the host never reads it).  m_sizes may sum to less than total_M:
+ *   rows past the sum are not written.  A negative entry or a larger sum writes nothing and
+ *   latches BSMMA_DEV_BAD_MSIZES.
+ * Preconditions: 1 <= G <= 1024, total_M >= 0, N > 0, K > 0, K % 16 == 0, total_M and G*N
+ *   below 2^31 - 1, alignments as for int8_gemm, 8-byte-aligned m_sizes.
+ */
+bsmma_status grouped_int8_gemm(const int8_t* X, const float* sX, const int8_t* W, const float* sW,
+                               void* D, bsmma_dtype d_dtype, const int64_t* m_sizes,
+                               int64_t total_M, int G, int64_t N, int64_t K, bsmma_stream stream);
+
+/*
+ * moe_combine -- out[t] = sum_j weights[t][j] * Y[pos[t][j]], in FP32 in the order of j,
+ *   rounded once.  pos (moe_plan's) outside 0..R-1 adds nothing; weights NULL counts as all
+ *   ones (the gradient of the gather that int8_quantize and a BF16 layer begin with).
+ *   Y [R][H] and out [T][H], both BF16 or both FP32; pos int32 [T][k]; weights FP32 [T][k].
+ * moe_combine_backward -- its gradients: dY[pos[t][j]] = weights[t][j] * dout[t] (0 in the
+ *   rows that src marks -1) and dweights[t][j] = sum_h dout[t][h] * Y[pos[t][j]][h] (0 where
+ *   pos is -1; not computed, and Y not read, when dweights is NULL).  dout [T][H], Y and dY
+ *   [T*k][H] of one type; src and pos moe_plan's.
+ * Preconditions: H > 0, rows of 16-byte multiples (H % 8 == 0 in BF16, H % 4 == 0 in FP32),
+ *   1 <= k <= 32, T >= 0, R and T*k < 2^31, 16-byte-aligned Y, out, dout and dY.  One launch
+ *   (none when T == 0).
+ */
+bsmma_status moe_combine(const void* Y, bsmma_dtype dtype, int64_t R, int64_t H, const int32_t* pos,
+                         const float* weights, int64_t T, int k, void* out, bsmma_stream stream);
+bsmma_status moe_combine_backward(const void* dout, bsmma_dtype dtype, int64_t H, const void* Y,
+                                  const int32_t* src, const int32_t* pos, const float* weights,
+                                  int64_t T, int k, void* dY, float* dweights, bsmma_stream stream);
+
 /* Grows the current (device, stream) scale workspace to at least `bytes` and allocates
  * the stream's split workspace if it has none (call before capturing mx_gemm or
  * mx_gemm_tiled into a CUDA graph).  The stream argument is this library's addition to
