@@ -13,7 +13,7 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libbsmma.so")
 SOURCES = ["api.cu", "relayout.cu", "mx_gemm.cu", "grouped_gemm.cu", "noalloc.cu",
            "mx_gemm_2sm.cu", "quantize.cu", "autotune.cu", "grouped_bf16.cu",
-           "moe.cu", "int8_gemm.cu"]
+           "moe.cu", "int8_gemm.cu", "int8_pair.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 

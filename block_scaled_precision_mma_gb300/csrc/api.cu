@@ -615,7 +615,8 @@ bsmma_status int8_gemm(const int8_t* A, const float* sA, const int8_t* B, const 
                        const void* bias, void* D, bsmma_dtype d_dtype, int64_t M, int64_t N,
                        int64_t K, bsmma_stream stream) {
   if (!known_dtype(d_dtype) || M < 0 || N < 0 || K < 0 || K % 16 != 0) return BSMMA_ERR_INVALID_ARG;
-  if (M >= INT32_MAX || N >= INT32_MAX || K >= INT32_MAX) return BSMMA_ERR_INVALID_ARG;
+  // tile coordinates past the last row stay within 32 bits
+  if (M >= INT32_MAX - 511 || N >= INT32_MAX - 511 || K >= INT32_MAX - 511) return BSMMA_ERR_INVALID_ARG;
   if (M == 0 || N == 0) return BSMMA_OK;
   if (!D || !sA || !sB || (K > 0 && (!A || !B))) return BSMMA_ERR_INVALID_ARG;
   if (!aligned16(A) || !aligned16(B) || !aligned16(D) || !aligned_to(sA, 4) || !aligned_to(sB, 4) ||
@@ -630,8 +631,8 @@ bsmma_status grouped_int8_gemm(const int8_t* X, const float* sX, const int8_t* W
                                int64_t total_M, int G, int64_t N, int64_t K, bsmma_stream stream) {
   if (!known_dtype(d_dtype) || G < 1 || G > 1024 || total_M < 0 || N <= 0 || K <= 0 || K % 16 != 0)
     return BSMMA_ERR_INVALID_ARG;
-  if (total_M >= INT32_MAX || K >= INT32_MAX || N >= INT32_MAX ||
-      static_cast<int64_t>(G) * N >= INT32_MAX)
+  if (total_M >= INT32_MAX - 511 || K >= INT32_MAX - 511 || N >= INT32_MAX - 511 ||
+      static_cast<int64_t>(G) * N >= INT32_MAX - 511)
     return BSMMA_ERR_INVALID_ARG;
   if (!W || !sW || !m_sizes) return BSMMA_ERR_INVALID_ARG;
   if (total_M > 0 && (!X || !sX || !D)) return BSMMA_ERR_INVALID_ARG;

@@ -13,11 +13,17 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "int8.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
 namespace bsmma {
 namespace {
+
+using int8::Int8Params;
+using int8::kMaxG;
+using int8::store_out;
+using int8::widen4;
 
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
@@ -164,33 +170,6 @@ bsmma_status launch_quantize_t(const QuantParams& p, cudaStream_t stream) {
 }
 
 // ---------------------------------------------------------------- products
-constexpr int kMaxG = 1024;   // groups per launch
-
-struct Int8Params {
-  const int8_t* A;
-  const float* sA;
-  const int8_t* B;
-  const float* sB;
-  const __nv_bfloat16* bias;
-  void* D;
-  const int64_t* m_sizes;   // nullptr: one group of total_M rows
-  int64_t total_M, N, K;
-  int G;
-  int* status;
-};
-
-// Four INT8 values as two FP16 pairs, exact: with u = x + 128 the FP16 bits 0x6400 | u are
-// the number 1024 + u.
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = w ^ 0x80808080u;
-  const __half2 bias = __half2half2(__ushort_as_half(0x6480));   // 1024 + 128
-  uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-  const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), bias);
-  const __half2 y = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
-  lo = *reinterpret_cast<const uint32_t*>(&x);
-  hi = *reinterpret_cast<const uint32_t*>(&y);
-}
-
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                           uint32_t b1) {
   asm volatile(
@@ -198,14 +177,6 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-template <bool F32>
-__device__ __forceinline__ void store_out(void* D, int64_t i, float v) {
-  if constexpr (F32)
-    static_cast<float*>(D)[i] = v;
-  else
-    static_cast<__nv_bfloat16*>(D)[i] = __float2bfloat16_rn(v);
 }
 
 // Row block `y` (blocks of R rows of one group, groups in order) -> group, its first row
@@ -429,6 +400,7 @@ bsmma_status launch_int8_gemm(const int8_t* A, const float* sA, const int8_t* B,
   p.G = G;
   p.status = dev->status;
   const int64_t per_group = (total_M + G - 1) / G;
+  if (per_group > 8 && K > 0) return int8::launch_pair(p, f32, dev, stream);
   if (per_group <= 8) return launch_rows<1>(p, f32, stream);
   if (per_group <= 16) return launch_rows<2>(p, f32, stream);
   return launch_rows<4>(p, f32, stream);

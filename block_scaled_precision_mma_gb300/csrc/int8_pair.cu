@@ -1,0 +1,655 @@
+// int8_pair.cu -- INT8 products on SM pairs: the tensor-core kernel of int8_gemm and
+// grouped_int8_gemm for more rows than the few-row kernel takes.
+//
+// The accumulator holds D transposed: its rows are 256 channels (128 a CTA), its columns up
+// to TN rows of A ("tokens").  Both operands arrive as INT8 by TMA and are widened to FP16
+// on the SM, where they are exact: the channels' values go from registers into tensor
+// memory, the A operand of tcgen05.mma, and the tokens' into shared memory, its B operand.
+// So DRAM and L2 carry one byte a value, and of the 4 bytes of shared-memory traffic that
+// the widened values would cost per channel value only the INT8 ones remain.
+//
+// One persistent launch over 2-CTA clusters, 512 threads a CTA:
+//   warp 0       TMA producer: 128 K of the CTA's 128 channels and of its half of the tokens
+//                (8- and 32-row boxes, as many as the unit has tokens) into a ring;
+//   warp 1       in the leader, lane 0 issues the M = 256 FP16 MMAs, four per 64 K;
+//   warps 4-11   two widening warpgroups, one for each 64-K half of a stage: a thread widens
+//                one channel's 64 values into its tensor-memory lane and its share of the
+//                tokens into the 128-byte-swizzled shared-memory tile;
+//   warps 12-15  output: accumulator columns out of tensor memory, times the scales, plus
+//                the bias, rounded and stored, 32 channels of a token per warp store.
+// Units (a token block of one group x 256 channels) are dealt round robin; the last wave's
+// are split along K over the pairs that would idle (stream_k.cuh), the partial sums added in
+// K order by the last pair to finish.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "int8.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+#include "stream_k.cuh"
+
+namespace bsmma {
+namespace int8 {
+namespace {
+
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+constexpr int kThreads = 512;
+constexpr int kWideWarp0 = 4, kOutWarp0 = 12;
+constexpr int kSlots = 4;                     // widened 64-K slots: two per widening warpgroup
+constexpr int kSlotCols = 32;                 // tensor-memory columns of 64 FP16 values
+constexpr uint16_t kPairMask = 3;
+
+struct Table {
+  int32_t start[kMaxG + 1];    // first row of each group
+  int32_t tile0[kMaxG + 1];    // its first token block
+  int32_t warp_sum[2][kThreads / 32];
+  int bad;
+};
+
+template <int TN>
+struct Cfg {
+  static constexpr int kHalf = TN / 2;                        // tokens of a CTA
+  static constexpr int kRawBytes = 128 * 128 + kHalf * 128;   // a stage: 128 K in INT8
+  static constexpr int kWideBytes = kHalf * 128;              // a slot: 64 K of the tokens in FP16
+  static constexpr int kBufs = 2 * TN + kSlots * kSlotCols <= 512 ? 2 : 1;   // accumulators
+  static constexpr int kTail = 1024 + static_cast<int>(sizeof(Table)) + 512;
+  static constexpr int kFit = (232448 - kTail - kSlots * kWideBytes) / kRawBytes;
+  static constexpr int kStages = kFit > 12 ? 12 : kFit;
+  static constexpr int kSmemBytes = kTail + kSlots * kWideBytes + kStages * kRawBytes;
+  static_assert(kStages >= 3, "shared memory budget");
+  static_assert(kBufs * TN + kSlots * kSlotCols <= 512, "tensor memory budget");
+};
+
+struct PairParams {
+  Int8Params a;
+  int tn, num_n_tiles, stages_k, halves_k;
+  float* part;
+  int* arrivals;
+  uint64_t limit_ns;
+};
+
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// mbar_wait for a barrier that the peer CTA's threads arrive on as well.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                                  volatile int* abort, int* status) {
+  if (!mbar_wait(bar, parity, limit_ns, abort, status)) return false;
+  return try_wait_cluster(bar, parity);
+}
+
+// D(tmem) (+)= A(tmem) x B(smem) over the pair, FP16 operands, FP32 accumulation.
+__device__ __forceinline__ void mma_f16_pair_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                                uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// 32 registers into 32 lanes x 32 consecutive columns of tensor memory.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async_proxy() {
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// Fills the group table (every thread of the block); blocks of tn rows.
+__device__ __forceinline__ void build_table(Table& t, const PairParams& p) {
+  const int G = p.a.G, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (!p.a.m_sizes) {
+    if (tid == 0) {
+      t.start[0] = 0;
+      t.tile0[0] = 0;
+      t.start[1] = static_cast<int32_t>(p.a.total_M);
+      t.tile0[1] = static_cast<int32_t>((p.a.total_M + p.tn - 1) / p.tn);
+      t.bad = 0;
+    }
+    __syncthreads();
+    return;
+  }
+  constexpr int kPer = kMaxG / kThreads;
+  int64_t rows = 0;
+  int32_t m[kPer], blocks = 0;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int g = tid * kPer + i;
+    const int64_t v = g < G ? p.a.m_sizes[g] : 0;
+    const bool out = v < 0 || v > p.a.total_M;
+    bad |= out;
+    m[i] = out ? 0 : static_cast<int32_t>(v);
+    rows += m[i];
+    blocks += (m[i] + p.tn - 1) / p.tn;
+  }
+  // sums of up to 1024 sizes below 2^31 each can pass 32 bits: checked in 64 first
+  int64_t all = rows;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(kFull, all, o);
+  bad |= all > p.a.total_M;
+  bad = __syncthreads_or(bad);
+  int32_t ir = static_cast<int32_t>(bad ? 0 : rows), ib = bad ? 0 : blocks;
+  const int32_t r_own = ir, b_own = ib;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t a = __shfl_up_sync(kFull, ir, o), b = __shfl_up_sync(kFull, ib, o);
+    if (lane >= o) {
+      ir += a;
+      ib += b;
+    }
+  }
+  if (lane == 31) {
+    t.warp_sum[0][warp] = ir;
+    t.warp_sum[1][warp] = ib;
+  }
+  __syncthreads();
+  int32_t r0 = ir - r_own, b0 = ib - b_own;
+  int64_t total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) {
+      r0 += t.warp_sum[0][w];
+      b0 += t.warp_sum[1][w];
+    }
+    total += t.warp_sum[0][w];
+  }
+  bad |= total > p.a.total_M;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int g = tid * kPer + i;
+    if (g <= G) {
+      t.start[g] = r0;
+      t.tile0[g] = b0;
+    }
+    r0 += m[i];
+    b0 += (m[i] + p.tn - 1) / p.tn;
+    if (g == G - 1) {
+      t.start[G] = r0;
+      t.tile0[G] = b0;
+    }
+  }
+  if (tid == 0) {
+    t.bad = bad;
+    if (bad && blockIdx.x == 0) report_status(p.a.status, kDevBadMSizes);
+  }
+  __syncthreads();
+}
+
+// A unit: its group, first token, tokens, and first channel.
+struct Unit {
+  int g, row0, rows, n0;
+};
+constexpr int kBand = 16;   // token blocks walked together over all channels, for L2
+__device__ __forceinline__ Unit find_unit(const Table& t, const PairParams& p, int u) {
+  const int NT = p.num_n_tiles, blocks = t.tile0[p.a.G];
+  const int b = u / (kBand * NT), first = b * kBand;
+  const int h = blocks - first < kBand ? blocks - first : kBand;
+  const int v = u - b * kBand * NT;
+  const int mt = first + v % h;
+  int lo = 0, hi = p.a.G - 1;   // the last group whose first block is not after mt
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.tile0[mid] <= mt) lo = mid;
+    else hi = mid - 1;
+  }
+  Unit r;
+  r.g = lo;
+  const int off = (mt - t.tile0[lo]) * p.tn;
+  const int left = t.start[lo + 1] - t.start[lo] - off;
+  r.row0 = t.start[lo] + off;
+  r.rows = left < p.tn ? left : p.tn;
+  r.n0 = v / h * 256;
+  return r;
+}
+// Columns of the unit's MMAs: its tokens, rounded up to 16 (8 for each CTA).
+__device__ __forceinline__ int unit_cols(const Unit& u) { return (u.rows + 15) & ~15; }
+
+// The worker's units in turn, whole ones and then its share of the split ones.
+struct Walk {
+  int dp, it, end;
+  __device__ __forceinline__ Walk(const DSched& s, int c) {
+    dp = c;
+    it = c < s.P ? dsk_begin(s, c) : 0;
+    end = c < s.P ? dsk_begin(s, c + 1) : 0;
+  }
+  __device__ __forceinline__ bool next(const DSched& s, int workers, int& u, int& k0, int& k1) {
+    if (dp < s.t_dp) {
+      u = dp;
+      k0 = 0;
+      k1 = s.KS;
+      dp += workers;
+      return true;
+    }
+    if (it >= end) return false;
+    const int v = it / s.gpu;
+    k0 = it - v * s.gpu;
+    k1 = s.gpu - k0 <= end - it ? s.gpu : k0 + (end - it);
+    it += k1 - k0;
+    u = s.t_dp + v;
+    return true;
+  }
+};
+
+template <int TN, bool F32>
+__global__ void __launch_bounds__(kThreads, 1)
+    int8_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA8,
+                     const __grid_constant__ CUtensorMap tmA32, const PairParams p) {
+  using C = Cfg<TN>;
+  constexpr int kStages = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* raw = smem;
+  uint8_t* wide = raw + kStages * C::kRawBytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(wide + kSlots * C::kWideBytes);
+  uint64_t* empty = full + kStages;
+  uint64_t* wide_full = empty + kStages;        // in the leader: widening warps of both CTAs
+  uint64_t* wide_empty = wide_full + kSlots;    // in both: the MMAs' commit
+  uint64_t* acc_full = wide_empty + kSlots;     // [2] in both
+  uint64_t* acc_empty = acc_full + 2;           // [2] in the leader: output warps of both CTAs
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  Table& table = *reinterpret_cast<Table*>(reinterpret_cast<uint8_t*>(full) + 512);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 8);       // the CTA's widening warps
+    }
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&wide_full[s], 8);   // one warpgroup of each CTA
+      mbar_init(&wide_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&acc_full[s], 1);
+      mbar_init(&acc_empty[s], 8);   // output warps of both CTAs
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmB);
+    prefetch_tmap(&tmA8);
+    prefetch_tmap(&tmA32);
+  }
+  build_table(table, p);
+  // both CTAs read the same sizes, so a bad table stops the whole cluster here
+  if (table.bad) return;
+
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem_wide = tmem + 512 - kSlots * kSlotCols;
+  const int worker = static_cast<int>(blockIdx.x >> 1), workers = static_cast<int>(gridDim.x >> 1);
+  const DSched sched = make_dsched(table.tile0[p.a.G] * p.num_n_tiles, p.stages_k, 1, workers,
+                                   p.part != nullptr, 6, 4);
+  Walk walk(sched, worker);
+  int u, k0, k1;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // -------------------------------------------------------------- producer
+      int stage = 0;
+      uint32_t phase = 0, armed = 0, armed_parity = 0;
+      bool ok = true;
+      while (ok && walk.next(sched, workers, u, k0, k1)) {
+        const Unit un = find_unit(table, p, u);
+        const int half = unit_cols(un) / 2;
+        const int row = un.row0 + rank * half;
+        const int chan = static_cast<int>(un.g * p.a.N) + un.n0 + rank * 128;
+        for (int k = k0; k < k1; ++k) {
+          if (!mbar_wait(&empty[stage], phase ^ 1, p.limit_ns, abort_flag, p.a.status)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[stage], 128 * 128 + half * 128);
+          armed |= 1u << stage;
+          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+          uint8_t* dst = raw + stage * C::kRawBytes;
+          tma_load_2d(&tmB, &full[stage], dst, k * 128, chan);
+          dst += 128 * 128;
+          int r = 0;
+          for (; r + 32 <= half; r += 32) tma_load_2d(&tmA32, &full[stage], dst + r * 128, k * 128, row + r);
+          for (; r < half; r += 8) tma_load_2d(&tmA8, &full[stage], dst + r * 128, k * 128, row + r);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // no copy may land after the block has finished
+      for (int s = 0; s < kStages; ++s)
+        if (armed & (1u << s)) {
+          volatile int no_abort = 0;
+          mbar_wait(&full[s], (armed_parity >> s) & 1u, p.limit_ns / 4 + 1, &no_abort, nullptr);
+        }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // -------------------------------------------------------------- MMA issuer (leader)
+      uint32_t tcount = 0, cnt[2] = {0, 0};
+      bool ok = true;
+      while (ok && walk.next(sched, workers, u, k0, k1)) {
+        const Unit un = find_unit(table, p, u);
+        const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(unit_cols(un) >> 3) << 17) |
+                               ((256u >> 4) << 24);   // FP32 accumulator, FP16 operands, M = 256
+        const uint32_t buf = tcount % C::kBufs;
+        if (!mbar_wait_cluster(&acc_empty[buf], ((tcount / C::kBufs) & 1) ^ 1, p.limit_ns, abort_flag,
+                               p.a.status))
+          break;
+        ++tcount;
+        tc_fence_after();
+        const uint32_t d = tmem + buf * TN;
+        const int h1 = 2 * k1 < p.halves_k ? 2 * k1 : p.halves_k;
+        for (int h = 2 * k0; h < h1; ++h) {
+          const int wg = h & 1;
+          const uint32_t slot = 2 * (cnt[wg] & 1) + wg, parity = (cnt[wg] >> 1) & 1;
+          ++cnt[wg];
+          if (!mbar_wait_cluster(&wide_full[slot], parity, p.limit_ns, abort_flag, p.a.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t b_base = smem_u32(wide + slot * C::kWideBytes);
+          const uint32_t a_base = tmem_wide + slot * kSlotCols;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_f16_pair_ts(d, a_base + j * 8, make_sdesc(b_base + j * 32, 16, 1024, kSwizzle128B),
+                            idesc, h != 2 * k0 || j != 0);
+          tc_commit_pair(&wide_empty[slot], kPairMask);
+        }
+        if (!ok) break;
+        tc_commit_pair(&acc_full[buf], kPairMask);
+      }
+      // every MMA must be finished before tensor memory is freed
+      tc_commit_pair(drain, 1);
+      volatile int no_abort = 0;
+      mbar_wait(drain, 0, p.limit_ns, &no_abort, nullptr);
+    }
+  } else if (warp >= kWideWarp0 && warp < kOutWarp0) {
+    // ---------------------------------------------------------------- widening (both CTAs)
+    const int wg = (warp - kWideWarp0) >> 2, tid = threadIdx.x & 127;
+    const uint32_t taddr = tmem_wide + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t chan_off = static_cast<uint32_t>(tid) * 128, chan_x = tid & 7;
+    int stage = 0;
+    uint32_t phase = 0, cnt = 0;
+    bool ok = true;
+    while (ok && walk.next(sched, workers, u, k0, k1)) {
+      const Unit un = find_unit(table, p, u);
+      const int half = unit_cols(un) / 2;
+      // the tokens' 16-byte pieces: piece i of a thread is token (i * 128 + tid) % half,
+      // piece (i * 128 + tid) / half of the row's four
+      for (int k = k0; k < k1; ++k) {
+        if (!mbar_wait(&full[stage], phase, p.limit_ns, abort_flag, p.a.status)) {
+          ok = false;
+          break;
+        }
+        const uint32_t base = smem_u32(raw + stage * C::kRawBytes);
+        const bool work = 2 * k + wg < p.halves_k;
+        uint4 c[4], x[C::kHalf / 32 + 1];
+        if (work) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            c[j] = lds128(base + chan_off + (((4 * wg + j) ^ chan_x) << 4));
+#pragma unroll
+          for (int i = 0; i < (C::kHalf + 31) / 32; ++i) {
+            const int e = i * 128 + tid;
+            if (e < 4 * half) {
+              const int r = e % half, piece = e / half;
+              x[i] = lds128(base + 128 * 128 + r * 128 + (((4 * wg + piece) ^ (r & 7)) << 4));
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[stage]);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+        if (!work) continue;
+        uint32_t w[32];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          widen4(c[j].x, w[8 * j], w[8 * j + 1]);
+          widen4(c[j].y, w[8 * j + 2], w[8 * j + 3]);
+          widen4(c[j].z, w[8 * j + 4], w[8 * j + 5]);
+          widen4(c[j].w, w[8 * j + 6], w[8 * j + 7]);
+        }
+        const uint32_t slot = 2 * (cnt & 1) + wg, parity = ((cnt >> 1) & 1) ^ 1;
+        ++cnt;
+        if (!mbar_wait(&wide_empty[slot], parity, p.limit_ns, abort_flag, p.a.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        tmem_st32(taddr + slot * kSlotCols, w);
+        const uint32_t out = smem_u32(wide + slot * C::kWideBytes);
+#pragma unroll
+        for (int i = 0; i < (C::kHalf + 31) / 32; ++i) {
+          const int e = i * 128 + tid;
+          if (e < 4 * half) {
+            const int r = e % half, piece = e / half;
+            uint32_t v[8];
+            widen4(x[i].x, v[0], v[1]);
+            widen4(x[i].y, v[2], v[3]);
+            widen4(x[i].z, v[4], v[5]);
+            widen4(x[i].w, v[6], v[7]);
+            const uint32_t row = out + r * 128;
+            sts128(row + (((2 * piece) ^ (r & 7)) << 4), v[0], v[1], v[2], v[3]);
+            sts128(row + (((2 * piece + 1) ^ (r & 7)) << 4), v[4], v[5], v[6], v[7]);
+          }
+        }
+        tmem_st_wait();
+        fence_async_proxy();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&wide_full[slot]), 0));
+      }
+    }
+  } else if (warp >= kOutWarp0) {
+    // ---------------------------------------------------------------- output (both CTAs)
+    const int q = warp & 3;
+    const uint32_t acc_empty_leader = map_to_cta(smem_u32(acc_empty), 0);
+    uint32_t tcount = 0;
+    while (walk.next(sched, workers, u, k0, k1)) {
+      const Unit un = find_unit(table, p, u);
+      const int cols = unit_cols(un);
+      const int64_t n = un.n0 + rank * 128 + q * 32 + lane;
+      const bool ok = n < p.a.N;
+      const float sb = ok ? p.a.sB[un.g * p.a.N + n] : 0.f;
+      const float bias = ok && p.a.bias ? __bfloat162float(p.a.bias[n]) : 0.f;
+      const uint32_t buf = tcount % C::kBufs;
+      if (!mbar_wait(&acc_full[buf], (tcount / C::kBufs) & 1, p.limit_ns, abort_flag, p.a.status)) break;
+      ++tcount;
+      tc_fence_after();
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * TN;
+      const bool whole = k1 - k0 == p.stages_k;
+      // 32 tokens of the lane's channel
+      auto finish = [&](int c, const uint32_t (&r)[32]) {
+        const float sa = c + lane < un.rows ? p.a.sA[un.row0 + c + lane] : 0.f;
+        const int left = un.rows - c;
+        const int64_t at = static_cast<int64_t>(un.row0 + c) * p.a.N + n;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float s = __shfl_sync(kFull, sa, i);
+          if (ok && i < left)
+            store_out<F32>(p.a.D, at + i * p.a.N, fmaf(__uint_as_float(r[i]), s * sb, bias));
+        }
+      };
+      const int v = u - sched.t_dp;
+      // a slot of partial sums: [quarter][token][32 channels]
+      auto slot_of = [&](int c) {
+        return p.part + static_cast<int64_t>((c * 2 + dsk_slot(sched, c, v)) * 2 + rank) * (128 * 256) +
+               q * (32 * 256) + lane;
+      };
+      float* mine = whole ? nullptr : slot_of(worker);
+      for (int c = 0; c < cols; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(taddr + c, r);
+        tmem_ld_wait(r);
+        if (c + 32 >= cols) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(acc_empty_leader + buf * 8);
+        }
+        if (whole) {
+          finish(c, r);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i < un.rows) __stcg(mine + (c + i) * 32, __uint_as_float(r[i]));
+        }
+      }
+      if (whole) continue;
+      __threadfence();
+      __syncwarp();
+      const int c_lo = dsk_first_worker(sched, v), c_hi = dsk_last_worker(sched, v);
+      int last = 0;
+      if (lane == 0) {
+        int* ctr = p.arrivals + (v * 2 + rank) * 8 + q;
+        last = atomicAdd(ctr, 1) + 1 == c_hi - c_lo + 1;
+        if (last) *ctr = 0;   // every contributor has counted itself in
+      }
+      if (!__shfl_sync(kFull, last, 0)) continue;
+      __threadfence();
+      for (int c = 0; c < cols; c += 32) {
+        float sum[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum[i] = 0.f;
+        for (int cc = c_lo; cc <= c_hi; ++cc) {
+          const float* from = slot_of(cc) + c * 32;
+          float y[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = c + i < un.rows ? __ldcg(from + i * 32) : 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[i] += y[i];
+        }
+        uint32_t r[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(sum[i]);
+        finish(c, r);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // both CTAs are done with tensor memory and with each other's barriers
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+  cluster_sync();
+}
+
+template <int TN, bool F32>
+bsmma_status launch_tn(PairParams p, const DeviceInfo* dev, cudaStream_t stream) {
+  using C = Cfg<TN>;
+  auto kern = int8_pair_kernel<TN, F32>;
+  static int max_clusters = -1;   // benign race: every thread computes the same value
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (max_clusters < 0) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) !=
+        cudaSuccess)
+      return BSMMA_ERR_CUDA;
+    cfg.gridDim = dim3(2 * (dev->sm_count / 2), 1, 1);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) return BSMMA_ERR_CUDA;
+    max_clusters = n < dev->sm_count / 2 ? n : dev->sm_count / 2;
+  }
+  CUtensorMap tb, ta8, ta32;
+  const Int8Params& a = p.a;
+  bsmma_status st = encode_tmap_u8(&tb, a.B, a.K, static_cast<uint64_t>(a.G) * a.N, a.K, 128, 128);
+  if (st != BSMMA_OK) return st;
+  // with no rows there is no tile of A to load; B's address stands in for the map
+  const void* A = a.total_M > 0 ? a.A : a.B;
+  const uint64_t rows = a.total_M > 0 ? a.total_M : 1;
+  st = encode_tmap_u8(&ta8, A, a.K, rows, a.K, 128, 8);
+  if (st != BSMMA_OK) return st;
+  st = encode_tmap_u8(&ta32, A, a.K, rows, a.K, 128, 32);
+  if (st != BSMMA_OK) return st;
+  p.part = nullptr;
+  p.arrivals = nullptr;
+  st = split_workspace(stream, &p.part, &p.arrivals);
+  if (st == BSMMA_ERR_WORKSPACE) {   // captured on a stream without one: no unit is split
+    p.part = nullptr;
+    p.arrivals = nullptr;
+  } else if (st != BSMMA_OK) {
+    return st;
+  }
+  p.tn = TN;
+  p.num_n_tiles = static_cast<int>((a.N + 255) / 256);
+  p.stages_k = static_cast<int>((a.K + 127) / 128);
+  p.halves_k = static_cast<int>((a.K + 63) / 64);
+  p.limit_ns = wait_limit_ns();
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * max_clusters), 1, 1);
+  cfg.stream = stream;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tb, ta8, ta32, p);
+  count_launches(1);
+  return cuda_ok(e == cudaSuccess ? cudaGetLastError() : e);
+}
+
+}  // namespace
+
+bsmma_status launch_pair(const Int8Params& a, bool f32, const DeviceInfo* dev, cudaStream_t stream) {
+  PairParams p;
+  p.a = a;
+  const int64_t per_group = (a.total_M + a.G - 1) / a.G;
+#define BSMMA_INT8_TN(T) (f32 ? launch_tn<T, true>(p, dev, stream) : launch_tn<T, false>(p, dev, stream))
+  if (per_group <= 32) return BSMMA_INT8_TN(64);
+  if (per_group <= 128) return BSMMA_INT8_TN(128);
+  return BSMMA_INT8_TN(256);
+#undef BSMMA_INT8_TN
+}
+
+}  // namespace int8
+}  // namespace bsmma

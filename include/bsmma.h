@@ -454,7 +454,7 @@ bsmma_status int8_quantize(const void* x, bsmma_dtype x_dtype, int64_t x_rows, i
  *   the integer sum is exact while its partial sums stay below 2^24 (any K <= 1040; longer K
  *   short of one-sided extremes), else rounded as FP32 sums are.  The order of the sum, and
  *   so the result, is the same in every call with the same sizes.
- * Preconditions: M, N, K >= 0, K % 16 == 0, M, N, K < 2^31 - 1, 16-byte-aligned A, B and D,
+ * Preconditions: M, N, K >= 0, K % 16 == 0, M, N, K < 2^31 - 512, 16-byte-aligned A, B and D,
  *   4-byte-aligned sA and sB, 2-byte-aligned bias.  N is not restricted.  M == 0 or N == 0
  *   is a no-op; K == 0 writes the bias, or 0.
  */
@@ -469,8 +469,8 @@ bsmma_status int8_gemm(const int8_t* A, const float* sA, const int8_t* B, const 
  *   [G] in DEVICE memory (the host never reads it).  m_sizes may sum to less than total_M:
  *   rows past the sum are not written.  A negative entry or a larger sum writes nothing and
  *   latches BSMMA_DEV_BAD_MSIZES.
- * Preconditions: 1 <= G <= 1024, total_M >= 0, N > 0, K > 0, K % 16 == 0, total_M and G*N
- *   below 2^31 - 1, alignments as for int8_gemm, 8-byte-aligned m_sizes.
+ * Preconditions: 1 <= G <= 1024, total_M >= 0, N > 0, K > 0, K % 16 == 0, total_M, K and
+ *   G*N below 2^31 - 512, alignments as for int8_gemm, 8-byte-aligned m_sizes.
  */
 bsmma_status grouped_int8_gemm(const int8_t* X, const float* sX, const int8_t* W, const float* sW,
                                void* D, bsmma_dtype d_dtype, const int64_t* m_sizes,
