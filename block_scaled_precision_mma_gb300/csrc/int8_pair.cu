@@ -38,6 +38,7 @@ constexpr int kWideWarp0 = 4, kOutWarp0 = 12;
 constexpr int kSlots = 4;                     // widened 64-K slots: two per widening warpgroup
 constexpr int kSlotCols = 32;                 // tensor-memory columns of 64 FP16 values
 constexpr uint16_t kPairMask = 3;
+constexpr uint32_t kNone = 0xFFFFFFFFu;
 
 struct Table {
   int32_t start[kMaxG + 1];    // first row of each group
@@ -86,6 +87,15 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   return try_wait_cluster(bar, parity);
 }
 
+// Arrives on the leader's barrier, releasing at CTA scope: what it announces (values in this
+// CTA's shared and tensor memory, or accumulator columns read) concerns this CTA's own tensor
+// core.  Release at cluster scope waits for every earlier store of the warp to be visible to
+// the cluster: 800 to 1100 cycles a slot for the widening warps, and all of a tile's output
+// stores for the output warps (4096 x 14336 x 4096: 605 -> 345 us without).
+__device__ __forceinline__ void arrive_leader(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
 // D(tmem) (+)= A(tmem) x B(smem) over the pair, FP16 operands, FP32 accumulation.
 __device__ __forceinline__ void mma_f16_pair_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
                                                 uint32_t acc) {
@@ -113,7 +123,7 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void fence_async_proxy() {
-  asm volatile("fence.proxy.async;" ::: "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
@@ -410,15 +420,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- widening (both CTAs)
     const int wg = (warp - kWideWarp0) >> 2, tid = threadIdx.x & 127;
     const uint32_t taddr = tmem_wide + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t chan_off = static_cast<uint32_t>(tid) * 128, chan_x = tid & 7;
+    // 16-byte piece j of the thread's channel is at chan ^ (j << 4) of the stage (the
+    // 128-byte swizzle exchanges pieces by the row's number modulo 8)
+    const uint32_t chan = static_cast<uint32_t>(tid) * 128 + (((4 * wg) ^ (tid & 7)) << 4);
+    constexpr int kPieces = (C::kHalf + 31) / 32;   // of the tokens, a thread
     int stage = 0;
     uint32_t phase = 0, cnt = 0;
     bool ok = true;
     while (ok && walk.next(sched, workers, u, k0, k1)) {
       const Unit un = find_unit(table, p, u);
       const int half = unit_cols(un) / 2;
-      // the tokens' 16-byte pieces: piece i of a thread is token (i * 128 + tid) % half,
-      // piece (i * 128 + tid) / half of the row's four
+      // the thread's i-th 16-byte piece of the tokens is that of token e % half, piece
+      // e / half of its four, e = i * 128 + tid: where it is in a stage, and where its first
+      // eight FP16 values go in a slot (the others 16 bytes on, before the swizzle)
+      uint32_t from[kPieces], to[kPieces];
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int e = i * 128 + tid, piece = e / half, r = e - piece * half;
+        from[i] = piece < 4 ? 128 * 128 + r * 128 + (((4 * wg + piece) ^ (r & 7)) << 4) : kNone;
+        to[i] = r * 128 + (((2 * piece) ^ (r & 7)) << 4);
+      }
       for (int k = k0; k < k1; ++k) {
         if (!mbar_wait(&full[stage], phase, p.limit_ns, abort_flag, p.a.status)) {
           ok = false;
@@ -426,19 +447,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t base = smem_u32(raw + stage * C::kRawBytes);
         const bool work = 2 * k + wg < p.halves_k;
-        uint4 c[4], x[C::kHalf / 32 + 1];
+        uint4 c[4], x[kPieces];
         if (work) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            c[j] = lds128(base + chan_off + (((4 * wg + j) ^ chan_x) << 4));
+            c[j] = lds128(base + (chan ^ (j << 4)));
 #pragma unroll
-          for (int i = 0; i < (C::kHalf + 31) / 32; ++i) {
-            const int e = i * 128 + tid;
-            if (e < 4 * half) {
-              const int r = e % half, piece = e / half;
-              x[i] = lds128(base + 128 * 128 + r * 128 + (((4 * wg + piece) ^ (r & 7)) << 4));
-            }
-          }
+          for (int i = 0; i < kPieces; ++i)
+            if (from[i] != kNone) x[i] = lds128(base + from[i]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
@@ -465,25 +481,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st32(taddr + slot * kSlotCols, w);
         const uint32_t out = smem_u32(wide + slot * C::kWideBytes);
 #pragma unroll
-        for (int i = 0; i < (C::kHalf + 31) / 32; ++i) {
-          const int e = i * 128 + tid;
-          if (e < 4 * half) {
-            const int r = e % half, piece = e / half;
+        for (int i = 0; i < kPieces; ++i) {
+          if (from[i] != kNone) {
             uint32_t v[8];
             widen4(x[i].x, v[0], v[1]);
             widen4(x[i].y, v[2], v[3]);
             widen4(x[i].z, v[4], v[5]);
             widen4(x[i].w, v[6], v[7]);
-            const uint32_t row = out + r * 128;
-            sts128(row + (((2 * piece) ^ (r & 7)) << 4), v[0], v[1], v[2], v[3]);
-            sts128(row + (((2 * piece + 1) ^ (r & 7)) << 4), v[4], v[5], v[6], v[7]);
+            sts128(out + to[i], v[0], v[1], v[2], v[3]);
+            sts128(out + (to[i] ^ 16), v[4], v[5], v[6], v[7]);
           }
         }
         tmem_st_wait();
         fence_async_proxy();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&wide_full[slot]), 0));
+        if (lane == 0) arrive_leader(map_to_cta(smem_u32(&wide_full[slot]), 0));
       }
     }
   } else if (warp >= kOutWarp0) {
@@ -530,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c + 32 >= cols) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(acc_empty_leader + buf * 8);
+          if (lane == 0) arrive_leader(acc_empty_leader + buf * 8);
         }
         if (whole) {
           finish(c, r);
