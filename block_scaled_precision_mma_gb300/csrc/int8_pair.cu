@@ -38,6 +38,7 @@ constexpr int kWideWarp0 = 4, kOutWarp0 = 12;
 constexpr int kSlots = 4;                     // widened 64-K slots: two per widening warpgroup
 constexpr int kSlotCols = 32;                 // tensor-memory columns of 64 FP16 values
 constexpr uint16_t kPairMask = 3;
+constexpr int kOutBarrier = 1;                // named barrier of the output warps
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 
 struct Table {
@@ -47,13 +48,17 @@ struct Table {
   int bad;
 };
 
-template <int TN>
+template <int TN, bool F32>
 struct Cfg {
   static constexpr int kHalf = TN / 2;                        // tokens of a CTA
   static constexpr int kRawBytes = 128 * 128 + kHalf * 128;   // a stage: 128 K in INT8
   static constexpr int kWideBytes = kHalf * 128;              // a slot: 64 K of the tokens in FP16
   static constexpr int kBufs = 2 * TN + kSlots * kSlotCols <= 512 ? 2 : 1;   // accumulators
-  static constexpr int kTail = 1024 + static_cast<int>(sizeof(Table)) + 512;
+  // output tile: 32 tokens x 128 channels, rows padded so that two rows' halves of the banks
+  // do not meet
+  static constexpr int kOutRow = F32 ? 512 : 256 + 64;
+  static constexpr int kOutBytes = 32 * kOutRow;
+  static constexpr int kTail = 1024 + static_cast<int>(sizeof(Table)) + 512 + 2 * kOutBytes;
   static constexpr int kFit = (232448 - kTail - kSlots * kWideBytes) / kRawBytes;
   static constexpr int kStages = kFit > 12 ? 12 : kFit;
   static constexpr int kSmemBytes = kTail + kSlots * kWideBytes + kStages * kRawBytes;
@@ -272,18 +277,39 @@ struct Walk {
   }
 };
 
+// True on all 128 output threads if `mine` is on all of them.
+__device__ __forceinline__ bool out_agree(bool mine) {
+  uint32_t all;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "barrier.cta.red.and.pred p, %2, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(all)
+      : "r"(static_cast<uint32_t>(mine)), "n"(kOutBarrier)
+      : "memory");
+  return all != 0;
+}
+
+// Moves a register array on by one place.
+template <int N>
+__device__ __forceinline__ void rotate(float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i + 1 < N; ++i) v[i] = v[i + 1];
+}
+
 template <int TN, bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
     int8_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA8,
                      const __grid_constant__ CUtensorMap tmA32, const PairParams p) {
-  using C = Cfg<TN>;
+  using C = Cfg<TN, F32>;
   constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* raw = smem;
   uint8_t* wide = raw + kStages * C::kRawBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(wide + kSlots * C::kWideBytes);
+  uint8_t* stage_out = wide + kSlots * C::kWideBytes;   // two output tiles
+  uint64_t* full = reinterpret_cast<uint64_t*>(stage_out + 2 * C::kOutBytes);
   uint64_t* empty = full + kStages;
   uint64_t* wide_full = empty + kStages;        // in the leader: widening warps of both CTAs
   uint64_t* wide_empty = wide_full + kSlots;    // in both: the MMAs' commit
@@ -501,9 +527,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kOutWarp0) {
     // ---------------------------------------------------------------- output (both CTAs)
-    const int q = warp & 3;
+    // A lane has a channel's tokens, a row of D wants a token's channels: 32 tokens at a time
+    // pass through shared memory ([token][128 channels]) and leave in 16-byte pieces, a
+    // token's 128 channels contiguous.  The four warps move together: every step that could
+    // give up or that only one of them would take is agreed on at a barrier first, so none
+    // is left waiting.
+    const int q = warp & 3, tid = threadIdx.x & 127;
     const uint32_t acc_empty_leader = map_to_cta(smem_u32(acc_empty), 0);
-    uint32_t tcount = 0;
+    const bool vec = p.a.N % (F32 ? 4 : 8) == 0;   // rows of D are 16-byte aligned
+    uint32_t tcount = 0, flip = 0;
     while (walk.next(sched, workers, u, k0, k1)) {
       const Unit un = find_unit(table, p, u);
       const int cols = unit_cols(un);
@@ -511,22 +543,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool ok = n < p.a.N;
       const float sb = ok ? p.a.sB[un.g * p.a.N + n] : 0.f;
       const float bias = ok && p.a.bias ? __bfloat162float(p.a.bias[n]) : 0.f;
+      // loaded ahead of the accumulator: lane l has the scales of tokens l, l + 32, ...
+      float sa[TN / 32];
+#pragma unroll
+      for (int i = 0; i < TN / 32; ++i)
+        sa[i] = 32 * i + lane < un.rows ? p.a.sA[un.row0 + 32 * i + lane] : 0.f;
       const uint32_t buf = tcount % C::kBufs;
-      if (!mbar_wait(&acc_full[buf], (tcount / C::kBufs) & 1, p.limit_ns, abort_flag, p.a.status)) break;
+      const bool got = mbar_wait(&acc_full[buf], (tcount / C::kBufs) & 1, p.limit_ns, abort_flag, p.a.status);
+      if (!out_agree(got)) break;
       ++tcount;
       tc_fence_after();
       const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * TN;
       const bool whole = k1 - k0 == p.stages_k;
-      // 32 tokens of the lane's channel
-      auto finish = [&](int c, const uint32_t (&r)[32]) {
-        const float sa = c + lane < un.rows ? p.a.sA[un.row0 + c + lane] : 0.f;
-        const int left = un.rows - c;
-        const int64_t at = static_cast<int64_t>(un.row0 + c) * p.a.N + n;
+      // 32 tokens of the lane's channel: scaled, turned and stored
+      auto finish = [&](int c, float scale_a, const uint32_t (&r)[32]) {
+        uint8_t* tile = stage_out + flip * C::kOutBytes;
+        flip ^= 1;
+        float y[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float s = __shfl_sync(kFull, sa, i);
-          if (ok && i < left)
-            store_out<F32>(p.a.D, at + i * p.a.N, fmaf(__uint_as_float(r[i]), s * sb, bias));
+        for (int i = 0; i < 32; ++i)
+          y[i] = fmaf(__uint_as_float(r[i]), __shfl_sync(kFull, scale_a, i) * sb, bias);
+        if constexpr (F32) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            *reinterpret_cast<float*>(tile + i * C::kOutRow + (q * 32 + lane) * 4) = y[i];
+        } else {
+          // neighbouring lanes pair up their channels: the even one takes the even token
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const bool odd = lane & 1;
+            const float theirs = __shfl_xor_sync(kFull, odd ? y[i] : y[i + 1], 1);
+            *reinterpret_cast<uint32_t*>(tile + (i + odd) * C::kOutRow + (q * 32 + (lane & ~1)) * 2) =
+                odd ? pack_bf16x2(theirs, y[i + 1]) : pack_bf16x2(y[i], theirs);
+          }
+        }
+        named_barrier_sync(kOutBarrier, 128);
+        const int tokens = un.rows - c < 32 ? un.rows - c : 32;
+        const int64_t left = p.a.N - un.n0 - rank * 128;   // channels of this CTA from its first
+        const int64_t at = static_cast<int64_t>(un.row0 + c) * p.a.N + un.n0 + rank * 128;
+        constexpr int kSize = F32 ? 4 : 2, kPer = 16 / kSize, kRow = 128 / kPer;
+        if (vec) {
+#pragma unroll
+          for (int i = 0; i < 32 * kRow / 128; ++i) {
+            const int e = i * 128 + tid, t = e / kRow, v = e % kRow;
+            if (t < tokens && v * kPer < left)
+              __stcs(reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.a.D) +
+                                              (at + t * p.a.N + v * kPer) * kSize),
+                     *reinterpret_cast<const uint4*>(tile + t * C::kOutRow + v * 16));
+          }
+        } else if (tid < left) {
+          for (int t = 0; t < tokens; ++t) {
+            const uint8_t* from = tile + t * C::kOutRow + tid * kSize;
+            if constexpr (F32)
+              static_cast<float*>(p.a.D)[at + t * p.a.N + tid] = *reinterpret_cast<const float*>(from);
+            else
+              static_cast<__nv_bfloat16*>(p.a.D)[at + t * p.a.N + tid] =
+                  *reinterpret_cast<const __nv_bfloat16*>(from);
+          }
         }
       };
       const int v = u - sched.t_dp;
@@ -536,6 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                q * (32 * 256) + lane;
       };
       float* mine = whole ? nullptr : slot_of(worker);
+#pragma unroll 1
       for (int c = 0; c < cols; c += 32) {
         uint32_t r[32];
         tmem_ld32(taddr + c, r);
@@ -546,25 +620,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) arrive_leader(acc_empty_leader + buf * 8);
         }
         if (whole) {
-          finish(c, r);
+          finish(c, sa[0], r);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             if (c + i < un.rows) __stcg(mine + (c + i) * 32, __uint_as_float(r[i]));
         }
+        if (whole) rotate(sa);
       }
       if (whole) continue;
       __threadfence();
-      __syncwarp();
+      named_barrier_sync(kOutBarrier, 128);
       const int c_lo = dsk_first_worker(sched, v), c_hi = dsk_last_worker(sched, v);
       int last = 0;
-      if (lane == 0) {
-        int* ctr = p.arrivals + (v * 2 + rank) * 8 + q;
+      if (tid == 0) {
+        int* ctr = p.arrivals + (v * 2 + rank) * 8;
         last = atomicAdd(ctr, 1) + 1 == c_hi - c_lo + 1;
         if (last) *ctr = 0;   // every contributor has counted itself in
       }
-      if (!__shfl_sync(kFull, last, 0)) continue;
+      if (!out_agree(tid != 0 || last)) continue;
       __threadfence();
+#pragma unroll 1
       for (int c = 0; c < cols; c += 32) {
         float sum[32];
 #pragma unroll
@@ -580,7 +656,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t r[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(sum[i]);
-        finish(c, r);
+        finish(c, sa[0], r);
+        rotate(sa);
       }
     }
   }
@@ -597,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int TN, bool F32>
 bsmma_status launch_tn(PairParams p, const DeviceInfo* dev, cudaStream_t stream) {
-  using C = Cfg<TN>;
+  using C = Cfg<TN, F32>;
   auto kern = int8_pair_kernel<TN, F32>;
   static int max_clusters = -1;   // benign race: every thread computes the same value
   cudaLaunchConfig_t cfg = {};
