@@ -235,6 +235,10 @@ int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
 }  // namespace
 
+bsmma_status stream_workspace(int64_t bytes, cudaStream_t stream, void** out) {
+  return get_workspace(bytes, stream, out);
+}
+
 bsmma_status split_workspace(cudaStream_t stream, float** part, int** arrivals) {
   bsmma_status st;
   const DeviceInfo* dev = current_device(&st);

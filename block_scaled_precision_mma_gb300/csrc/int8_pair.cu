@@ -10,8 +10,8 @@
 //
 // One persistent launch over 2-CTA clusters, 512 threads a CTA:
 //   warp 0       TMA producer: 128 K of the CTA's 128 channels and of its half of the tokens
-//                (8- and 32-row boxes, as many as the unit has tokens) into a ring;
-//   warp 1       in the leader, lane 0 issues the M = 256 FP16 MMAs, four per 64 K;
+//                (one box for a full half, else boxes of 32 and 8 rows) into a ring;
+//   warp 1       in the leader, issues the M = 256 FP16 MMAs, four per 64 K;
 //   warps 4-11   two widening warpgroups, one for each 64-K half of a stage: a thread widens
 //                one channel's 64 values into its tensor-memory lane and its share of the
 //                tokens into the 128-byte-swizzled shared-memory tile;
@@ -48,20 +48,25 @@ struct Table {
   int bad;
 };
 
-template <int TN, bool F32>
+// PRE: the tokens are FP16 already (a widening pass before the launch).
+template <int TN, bool PRE, bool F32>
 struct Cfg {
   static constexpr int kHalf = TN / 2;                        // tokens of a CTA
-  static constexpr int kRawBytes = 128 * 128 + kHalf * 128;   // a stage: 128 K in INT8
+  // a stage: 128 K in INT8, of the channels alone with PRE
+  static constexpr int kRawBytes = 128 * 128 + (PRE ? 0 : kHalf * 128);
   static constexpr int kWideBytes = kHalf * 128;              // a slot: 64 K of the tokens in FP16
+  static constexpr int kTokSlots = PRE ? 10 : kSlots;
   static constexpr int kBufs = 2 * TN + kSlots * kSlotCols <= 512 ? 2 : 1;   // accumulators
   // output tile: 32 tokens x 128 channels, rows padded so that two rows' halves of the banks
   // do not meet
   static constexpr int kOutRow = F32 ? 512 : 256 + 64;
   static constexpr int kOutBytes = 32 * kOutRow;
   static constexpr int kTail = 1024 + static_cast<int>(sizeof(Table)) + 512 + 2 * kOutBytes;
-  static constexpr int kFit = (232448 - kTail - kSlots * kWideBytes) / kRawBytes;
+  static constexpr int kFit = (232448 - kTail - kTokSlots * kWideBytes) / kRawBytes;
   static constexpr int kStages = kFit > 12 ? 12 : kFit;
-  static constexpr int kSmemBytes = kTail + kSlots * kWideBytes + kStages * kRawBytes;
+  static constexpr int kSmemBytes = kTail + kTokSlots * kWideBytes + kStages * kRawBytes;
+  static_assert((2 * kStages + 2 * kSlots + 5 + (PRE ? 2 * kTokSlots : 0)) * 8 + 8 <= 512,
+                "barriers fit below the group table");
   static_assert(kStages >= 3, "shared memory budget");
   static_assert(kBufs * TN + kSlots * kSlotCols <= 512, "tensor memory budget");
 };
@@ -109,6 +114,18 @@ __device__ __forceinline__ void mma_f16_pair_ts(uint32_t d, uint32_t a, uint64_t
       "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
+}
+
+// True in one lane of the (whole) warp, the same one every time.  A role that issues copies or
+// MMAs runs its loop on all lanes and elects the issuing one at the instruction, so that loop
+// state and descriptors are warp-uniform for the compiler; under a divergent `lane == 0` each
+// MMA cost its issuer about 180 cycles.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r != 0;
 }
 
 // 32 registers into 32 lanes x 32 consecutive columns of tensor memory.
@@ -297,18 +314,19 @@ __device__ __forceinline__ void rotate(float (&v)[N]) {
   for (int i = 0; i + 1 < N; ++i) v[i] = v[i + 1];
 }
 
-template <int TN, bool F32>
+template <int TN, bool PRE, bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
     int8_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA8,
-                     const __grid_constant__ CUtensorMap tmA32, const PairParams p) {
-  using C = Cfg<TN, F32>;
+                     const __grid_constant__ CUtensorMap tmA32,
+                     const __grid_constant__ CUtensorMap tmAll, const PairParams p) {
+  using C = Cfg<TN, PRE, F32>;
   constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* raw = smem;
   uint8_t* wide = raw + kStages * C::kRawBytes;
-  uint8_t* stage_out = wide + kSlots * C::kWideBytes;   // two output tiles
+  uint8_t* stage_out = wide + C::kTokSlots * C::kWideBytes;   // two output tiles
   uint64_t* full = reinterpret_cast<uint64_t*>(stage_out + 2 * C::kOutBytes);
   uint64_t* empty = full + kStages;
   uint64_t* wide_full = empty + kStages;        // in the leader: widening warps of both CTAs
@@ -316,7 +334,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* acc_full = wide_empty + kSlots;     // [2] in both
   uint64_t* acc_empty = acc_full + 2;           // [2] in the leader: output warps of both CTAs
   uint64_t* drain = acc_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* tok_full = drain + 1;               // PRE: in the leader, both CTAs' bytes
+  uint64_t* tok_empty = tok_full + C::kTokSlots;   // PRE: in both, the MMAs' commit
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1 + (PRE ? 2 * C::kTokSlots : 0));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   Table& table = *reinterpret_cast<Table*>(reinterpret_cast<uint8_t*>(full) + 512);
 
@@ -336,11 +356,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&acc_empty[s], 8);   // output warps of both CTAs
     }
     mbar_init(drain, 1);
+    if constexpr (PRE)
+      for (int s = 0; s < C::kTokSlots; ++s) {
+        mbar_init(&tok_full[s], 1);
+        mbar_init(&tok_empty[s], 1);
+      }
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tmB);
     prefetch_tmap(&tmA8);
     prefetch_tmap(&tmA32);
+    prefetch_tmap(&tmAll);
   }
   build_table(table, p);
   // both CTAs read the same sizes, so a bad table stops the whole cluster here
@@ -363,47 +389,102 @@ __global__ void __launch_bounds__(kThreads, 1)
   int u, k0, k1;
 
   if (warp == 0) {
-    if (lane == 0) {
-      // -------------------------------------------------------------- producer
-      int stage = 0;
-      uint32_t phase = 0, armed = 0, armed_parity = 0;
-      bool ok = true;
-      while (ok && walk.next(sched, workers, u, k0, k1)) {
-        const Unit un = find_unit(table, p, u);
-        const int half = unit_cols(un) / 2;
-        const int row = un.row0 + rank * half;
-        const int chan = static_cast<int>(un.g * p.a.N) + un.n0 + rank * 128;
-        for (int k = k0; k < k1; ++k) {
-          if (!mbar_wait(&empty[stage], phase ^ 1, p.limit_ns, abort_flag, p.a.status)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&full[stage], 128 * 128 + half * 128);
-          armed |= 1u << stage;
-          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+    // ---------------------------------------------------------------- producer, channels
+    // (and, without PRE, the tokens on the same barrier)
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, armed_parity = 0;
+    bool ok = true;
+    while (ok && walk.next(sched, workers, u, k0, k1)) {
+      const Unit un = find_unit(table, p, u);
+      const int half = unit_cols(un) / 2;
+      const int row = un.row0 + rank * half;
+      const int chan = static_cast<int>(un.g * p.a.N) + un.n0 + rank * 128;
+      for (int k = k0; k < k1; ++k) {
+        if (!mbar_wait(&empty[stage], phase ^ 1, p.limit_ns, abort_flag, p.a.status)) {
+          ok = false;
+          break;
+        }
+        armed |= 1u << stage;
+        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&full[stage], 128 * 128 + (PRE ? 0 : half * 128));
           uint8_t* dst = raw + stage * C::kRawBytes;
           tma_load_2d(&tmB, &full[stage], dst, k * 128, chan);
-          dst += 128 * 128;
-          int r = 0;
-          for (; r + 32 <= half; r += 32) tma_load_2d(&tmA32, &full[stage], dst + r * 128, k * 128, row + r);
-          for (; r < half; r += 8) tma_load_2d(&tmA8, &full[stage], dst + r * 128, k * 128, row + r);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1;
+          if constexpr (!PRE) {
+            dst += 128 * 128;
+            int r = 0;
+            if (half == C::kHalf) {
+              tma_load_2d(&tmAll, &full[stage], dst, k * 128, row);
+              r = half;
+            }
+            for (; r + 32 <= half; r += 32)
+              tma_load_2d(&tmA32, &full[stage], dst + r * 128, k * 128, row + r);
+            for (; r < half; r += 8) tma_load_2d(&tmA8, &full[stage], dst + r * 128, k * 128, row + r);
           }
         }
-      }
-      // no copy may land after the block has finished
-      for (int s = 0; s < kStages; ++s)
-        if (armed & (1u << s)) {
-          volatile int no_abort = 0;
-          mbar_wait(&full[s], (armed_parity >> s) & 1u, p.limit_ns / 4 + 1, &no_abort, nullptr);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
         }
+      }
     }
+    // no copy may land after the block has finished
+    for (int s = 0; s < kStages; ++s)
+      if (armed & (1u << s)) {
+        volatile int no_abort = 0;
+        mbar_wait(&full[s], (armed_parity >> s) & 1u, p.limit_ns / 4 + 1, &no_abort, nullptr);
+      }
+  } else if (PRE && warp == 2) {
+    // ---------------------------------------------------------------- producer, FP16 tokens
+    // A warp of its own: with both on one warp the issuing itself (some 1100 cycles for a
+    // stage's three copies) was longer than the stage's MMAs.
+    int tok = 0;
+    uint32_t phase = 0, armed = 0, armed_parity = 0;
+    bool ok = true;
+    while (ok && walk.next(sched, workers, u, k0, k1)) {
+      const Unit un = find_unit(table, p, u);
+      const int half = unit_cols(un) / 2;
+      const int row = un.row0 + rank * half;
+      const int h1 = 2 * k1 < p.halves_k ? 2 * k1 : p.halves_k;
+      for (int h = 2 * k0; h < h1; ++h) {
+        if (!mbar_wait(&tok_empty[tok], phase ^ 1, p.limit_ns, abort_flag, p.a.status)) {
+          ok = false;
+          break;
+        }
+        if (rank == 0) {
+          armed |= 1u << tok;
+          armed_parity = (armed_parity & ~(1u << tok)) | (phase << tok);
+        }
+        if (elect_one()) {
+          const uint32_t bar = map_to_cta(smem_u32(&tok_full[tok]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&tok_full[tok], 2 * half * 128);
+          uint8_t* dst = wide + tok * C::kWideBytes;
+          int r = 0;
+          if (half == C::kHalf) {
+            tma_load_2d_pair(&tmAll, bar, dst, h * 128, row);
+            r = half;
+          }
+          for (; r + 32 <= half; r += 32)
+            tma_load_2d_pair(&tmA32, bar, dst + r * 128, h * 128, row + r);
+          for (; r < half; r += 8) tma_load_2d_pair(&tmA8, bar, dst + r * 128, h * 128, row + r);
+        }
+        if (++tok == C::kTokSlots) {
+          tok = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    // both CTAs' copies complete on the leader's barriers
+    for (int s = 0; s < C::kTokSlots; ++s)
+      if (armed & (1u << s)) {
+        volatile int no_abort = 0;
+        mbar_wait(&tok_full[s], (armed_parity >> s) & 1u, p.limit_ns / 4 + 1, &no_abort, nullptr);
+      }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // -------------------------------------------------------------- MMA issuer (leader)
-      uint32_t tcount = 0, cnt[2] = {0, 0};
+      uint32_t tcount = 0, cnt = 0, tok = 0, tok_phase = 0;   // cnt: slots of each warpgroup
+      const uint64_t b_desc = make_sdesc(smem_u32(wide), 16, 1024, kSwizzle128B);
       bool ok = true;
       while (ok && walk.next(sched, workers, u, k0, k1)) {
         const Unit un = find_unit(table, p, u);
@@ -414,31 +495,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                                p.a.status))
           break;
         ++tcount;
-        tc_fence_after();
         const uint32_t d = tmem + buf * TN;
-        const int h1 = 2 * k1 < p.halves_k ? 2 * k1 : p.halves_k;
-        for (int h = 2 * k0; h < h1; ++h) {
-          const int wg = h & 1;
-          const uint32_t slot = 2 * (cnt[wg] & 1) + wg, parity = (cnt[wg] >> 1) & 1;
-          ++cnt[wg];
-          if (!mbar_wait_cluster(&wide_full[slot], parity, p.limit_ns, abort_flag, p.a.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t b_base = smem_u32(wide + slot * C::kWideBytes);
-          const uint32_t a_base = tmem_wide + slot * kSlotCols;
+        uint32_t acc = 0;
+        for (int k = k0; ok && k < k1; ++k) {
+          const int halves = p.halves_k - 2 * k < 2 ? 1 : 2;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_f16_pair_ts(d, a_base + j * 8, make_sdesc(b_base + j * 32, 16, 1024, kSwizzle128B),
-                            idesc, h != 2 * k0 || j != 0);
-          tc_commit_pair(&wide_empty[slot], kPairMask);
+          for (int wg = 0; wg < 2; ++wg) {
+            if (wg >= halves) break;
+            // (a second half missing at the end of K leaves its warpgroup a slot behind)
+            const uint32_t use = wg == 0 ? cnt & 0xFFFFu : cnt >> 16;
+            const uint32_t slot = 2 * (use & 1) + wg;
+            cnt += wg == 0 ? 1 : 0x10000;
+            if (!mbar_wait_cluster(&wide_full[slot], (use >> 1) & 1, p.limit_ns, abort_flag, p.a.status)) {
+              ok = false;
+              break;
+            }
+            if constexpr (PRE) {
+              if (!mbar_wait(&tok_full[tok], tok_phase, p.limit_ns, abort_flag, p.a.status)) {
+                ok = false;
+                break;
+              }
+            }
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t b = b_desc + ((PRE ? tok : slot) * C::kWideBytes >> 4);
+              const uint32_t a = tmem_wide + slot * kSlotCols;
+              mma_f16_pair_ts(d, a, b, idesc, acc);
+#pragma unroll
+              for (int j = 1; j < 4; ++j) mma_f16_pair_ts(d, a + j * 8, b + 2 * j, idesc, 1);
+              tc_commit_pair(&wide_empty[slot], kPairMask);
+              if constexpr (PRE) tc_commit_pair(&tok_empty[tok], kPairMask);
+            }
+            acc = 1;
+            if constexpr (PRE) {
+              if (++tok == C::kTokSlots) {
+                tok = 0;
+                tok_phase ^= 1;
+              }
+            }
+          }
         }
         if (!ok) break;
-        tc_commit_pair(&acc_full[buf], kPairMask);
+        if (elect_one()) tc_commit_pair(&acc_full[buf], kPairMask);
       }
       // every MMA must be finished before tensor memory is freed
-      tc_commit_pair(drain, 1);
+      __syncwarp();
+      if (elect_one()) tc_commit_pair(drain, 1);
       volatile int no_abort = 0;
       mbar_wait(drain, 0, p.limit_ns, &no_abort, nullptr);
     }
@@ -449,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 16-byte piece j of the thread's channel is at chan ^ (j << 4) of the stage (the
     // 128-byte swizzle exchanges pieces by the row's number modulo 8)
     const uint32_t chan = static_cast<uint32_t>(tid) * 128 + (((4 * wg) ^ (tid & 7)) << 4);
-    constexpr int kPieces = (C::kHalf + 31) / 32;   // of the tokens, a thread
+    constexpr int kPieces = PRE ? 0 : (C::kHalf + 31) / 32;   // of the tokens, a thread
     int stage = 0;
     uint32_t phase = 0, cnt = 0;
     bool ok = true;
@@ -459,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the thread's i-th 16-byte piece of the tokens is that of token e % half, piece
       // e / half of its four, e = i * 128 + tid: where it is in a stage, and where its first
       // eight FP16 values go in a slot (the others 16 bytes on, before the swizzle)
-      uint32_t from[kPieces], to[kPieces];
+      uint32_t from[kPieces + 1], to[kPieces + 1];
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int e = i * 128 + tid, piece = e / half, r = e - piece * half;
@@ -473,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t base = smem_u32(raw + stage * C::kRawBytes);
         const bool work = 2 * k + wg < p.halves_k;
-        uint4 c[4], x[kPieces];
+        uint4 c[4], x[kPieces + 1];
         if (work) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -672,10 +774,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();
 }
 
-template <int TN, bool F32>
-bsmma_status launch_tn(PairParams p, const DeviceInfo* dev, cudaStream_t stream) {
-  using C = Cfg<TN, F32>;
-  auto kern = int8_pair_kernel<TN, F32>;
+// tok16: the tokens in FP16 ([total_M][K]) with PRE.
+template <int TN, bool PRE, bool F32>
+bsmma_status launch_tn(PairParams p, const void* tok16, const DeviceInfo* dev, cudaStream_t stream) {
+  using C = Cfg<TN, PRE, F32>;
+  auto kern = int8_pair_kernel<TN, PRE, F32>;
   static int max_clusters = -1;   // benign race: every thread computes the same value
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
@@ -696,16 +799,18 @@ bsmma_status launch_tn(PairParams p, const DeviceInfo* dev, cudaStream_t stream)
     if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) return BSMMA_ERR_CUDA;
     max_clusters = n < dev->sm_count / 2 ? n : dev->sm_count / 2;
   }
-  CUtensorMap tb, ta8, ta32;
+  CUtensorMap tb, ta8, ta32, tall;
   const Int8Params& a = p.a;
   bsmma_status st = encode_tmap_u8(&tb, a.B, a.K, static_cast<uint64_t>(a.G) * a.N, a.K, 128, 128);
   if (st != BSMMA_OK) return st;
   // with no rows there is no tile of A to load; B's address stands in for the map
-  const void* A = a.total_M > 0 ? a.A : a.B;
-  const uint64_t rows = a.total_M > 0 ? a.total_M : 1;
-  st = encode_tmap_u8(&ta8, A, a.K, rows, a.K, 128, 8);
+  const void* A = a.total_M > 0 ? (PRE ? tok16 : a.A) : a.B;
+  const uint64_t rows = a.total_M > 0 ? a.total_M : 1, row_bytes = PRE ? 2 * a.K : a.K;
+  st = encode_tmap_u8(&ta8, A, row_bytes, rows, row_bytes, 128, 8);
   if (st != BSMMA_OK) return st;
-  st = encode_tmap_u8(&ta32, A, a.K, rows, a.K, 128, 32);
+  st = encode_tmap_u8(&ta32, A, row_bytes, rows, row_bytes, 128, 32);
+  if (st != BSMMA_OK) return st;
+  st = encode_tmap_u8(&tall, A, row_bytes, rows, row_bytes, 128, C::kHalf);
   if (st != BSMMA_OK) return st;
   p.part = nullptr;
   p.arrivals = nullptr;
@@ -723,21 +828,47 @@ bsmma_status launch_tn(PairParams p, const DeviceInfo* dev, cudaStream_t stream)
   p.limit_ns = wait_limit_ns();
   cfg.gridDim = dim3(static_cast<unsigned>(2 * max_clusters), 1, 1);
   cfg.stream = stream;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tb, ta8, ta32, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tb, ta8, ta32, tall, p);
   count_launches(1);
   return cuda_ok(e == cudaSuccess ? cudaGetLastError() : e);
 }
 
 }  // namespace
 
+namespace {
+// int8 [n16 * 16] -> FP16, 16 values a thread and step.
+__global__ void __launch_bounds__(256) widen_kernel(const uint4* __restrict__ in,
+                                                    uint4* __restrict__ out, int64_t n16) {
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n16; i += gridDim.x * 256ll) {
+    const uint4 v = __ldcs(in + i);
+    uint4 a, b;
+    widen4(v.x, a.x, a.y);
+    widen4(v.y, a.z, a.w);
+    widen4(v.z, b.x, b.y);
+    widen4(v.w, b.z, b.w);
+    out[2 * i] = a;
+    out[2 * i + 1] = b;
+  }
+}
+}  // namespace
+
 bsmma_status launch_pair(const Int8Params& a, bool f32, const DeviceInfo* dev, cudaStream_t stream) {
   PairParams p;
   p.a = a;
   const int64_t per_group = (a.total_M + a.G - 1) / a.G;
-#define BSMMA_INT8_TN(T) (f32 ? launch_tn<T, true>(p, dev, stream) : launch_tn<T, false>(p, dev, stream))
-  if (per_group <= 32) return BSMMA_INT8_TN(64);
-  if (per_group <= 128) return BSMMA_INT8_TN(128);
-  return BSMMA_INT8_TN(256);
+#define BSMMA_INT8_TN(T, PRE, X) \
+  (f32 ? launch_tn<T, PRE, true>(p, X, dev, stream) : launch_tn<T, PRE, false>(p, X, dev, stream))
+  if (per_group <= 32) return BSMMA_INT8_TN(64, false, nullptr);
+  if (per_group <= 128) return BSMMA_INT8_TN(128, false, nullptr);
+  void* tok16 = nullptr;
+  const bsmma_status st = stream_workspace(a.total_M * a.K * 2, stream, &tok16);
+  if (st == BSMMA_ERR_WORKSPACE) return BSMMA_INT8_TN(256, false, nullptr);
+  if (st != BSMMA_OK) return st;
+  const int64_t n16 = a.total_M * a.K / 16, blocks = (n16 + 255) / 256;
+  widen_kernel<<<static_cast<unsigned>(blocks < dev->sm_count * 8 ? blocks : dev->sm_count * 8), 256, 0,
+                 stream>>>(reinterpret_cast<const uint4*>(a.A), static_cast<uint4*>(tok16), n16);
+  count_launches(1);
+  return BSMMA_INT8_TN(192, true, tok16);
 #undef BSMMA_INT8_TN
 }
 

@@ -51,6 +51,10 @@ bsmma_status launch_wide_relayout(const uint8_t* sa, int64_t rows_a, uint8_t* ou
                                   const uint8_t* sb, int64_t rows_b, uint8_t* out_b,
                                   int64_t kblocks, cudaStream_t stream);
 
+// The (current device, stream) workspace, grown to at least `bytes` (BSMMA_ERR_WORKSPACE
+// during a capture that would have to grow it).
+bsmma_status stream_workspace(int64_t bytes, cudaStream_t stream, void** out);
+
 // The dense SM-pair kernel's split workspace for (current device, stream): arrival
 // counters [#SMs][8 epilogue warps] (zero between launches) and partial-sum slots
 // [2 * #SMs][128 x 256 FP32].
