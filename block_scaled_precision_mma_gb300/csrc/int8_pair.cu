@@ -11,10 +11,11 @@
 // One persistent launch over 2-CTA clusters, 512 threads a CTA:
 //   warp 0       TMA producer: 128 K of the CTA's 128 channels and of its half of the tokens
 //                (one box for a full half, else boxes of 32 and 8 rows) into a ring;
-//   warp 1       in the leader, issues the M = 256 FP16 MMAs, four per 64 K;
+//   warp 1       in the leader, issues the M = 256 FP16 MMAs, eight per stage;
 //   warps 4-11   two widening warpgroups, one for each 64-K half of a stage: a thread widens
 //                one channel's 64 values into its tensor-memory lane and its share of the
-//                tokens into the 128-byte-swizzled shared-memory tile;
+//                tokens into the 128-byte-swizzled shared-memory tile (with PRE the tokens
+//                come as FP16, by warp 2);
 //   warps 12-15  output: accumulator columns out of tensor memory, times the scales, plus
 //                the bias, rounded and stored, 32 channels of a token per warp store.
 // Units (a token block of one group x 256 channels) are dealt round robin; the last wave's
@@ -35,8 +36,7 @@ namespace {
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kThreads = 512;
 constexpr int kWideWarp0 = 4, kOutWarp0 = 12;
-constexpr int kSlots = 4;                     // widened 64-K slots: two per widening warpgroup
-constexpr int kSlotCols = 32;                 // tensor-memory columns of 64 FP16 values
+constexpr int kSlotCols = 64;                 // tensor-memory columns of a slot's 128 FP16 values
 constexpr uint16_t kPairMask = 3;
 constexpr int kOutBarrier = 1;                // named barrier of the output warps
 constexpr uint32_t kNone = 0xFFFFFFFFu;
@@ -54,9 +54,12 @@ struct Cfg {
   static constexpr int kHalf = TN / 2;                        // tokens of a CTA
   // a stage: 128 K in INT8, of the channels alone with PRE
   static constexpr int kRawBytes = 128 * 128 + (PRE ? 0 : kHalf * 128);
-  static constexpr int kWideBytes = kHalf * 128;              // a slot: 64 K of the tokens in FP16
-  static constexpr int kTokSlots = PRE ? 10 : kSlots;
-  static constexpr int kBufs = 2 * TN + kSlots * kSlotCols <= 512 ? 2 : 1;   // accumulators
+  static constexpr int kWideBytes = kHalf * 256;              // a slot: 128 K of the tokens in FP16
+  // accumulators, and slots of widened channels in the rest of tensor memory
+  static constexpr int kBufs = 2 * TN + 2 * kSlotCols <= 512 ? 2 : 1;
+  static constexpr int kFree = (512 - kBufs * TN) / kSlotCols;
+  static constexpr int kSlots = PRE ? (kFree < 4 ? kFree : 4) : TN > 128 ? 2 : 3;
+  static constexpr int kTokSlots = PRE ? (TN > 192 ? 4 : 5) : kSlots;
   // output tile: 32 tokens x 128 channels, rows padded so that two rows' halves of the banks
   // do not meet
   static constexpr int kOutRow = F32 ? 512 : 256 + 64;
@@ -93,8 +96,8 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
 // mbar_wait for a barrier that the peer CTA's threads arrive on as well.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
                                                   volatile int* abort, int* status) {
-  if (!mbar_wait(bar, parity, limit_ns, abort, status)) return false;
-  return try_wait_cluster(bar, parity);
+  if (try_wait_cluster(bar, parity)) return true;
+  return mbar_wait(bar, parity, limit_ns, abort, status) && try_wait_cluster(bar, parity);
 }
 
 // Arrives on the leader's barrier, releasing at CTA scope: what it announces (values in this
@@ -320,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap tmA32,
                      const __grid_constant__ CUtensorMap tmAll, const PairParams p) {
   using C = Cfg<TN, PRE, F32>;
-  constexpr int kStages = C::kStages;
+  constexpr int kStages = C::kStages, kSlots = C::kSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -348,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&empty[s], 8);       // the CTA's widening warps
     }
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&wide_full[s], 8);   // one warpgroup of each CTA
+      mbar_init(&wide_full[s], 16);  // the widening warps of both CTAs
       mbar_init(&wide_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -445,8 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Unit un = find_unit(table, p, u);
       const int half = unit_cols(un) / 2;
       const int row = un.row0 + rank * half;
-      const int h1 = 2 * k1 < p.halves_k ? 2 * k1 : p.halves_k;
-      for (int h = 2 * k0; h < h1; ++h) {
+      for (int k = k0; k < k1; ++k) {
         if (!mbar_wait(&tok_empty[tok], phase ^ 1, p.limit_ns, abort_flag, p.a.status)) {
           ok = false;
           break;
@@ -457,16 +459,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (elect_one()) {
           const uint32_t bar = map_to_cta(smem_u32(&tok_full[tok]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&tok_full[tok], 2 * half * 128);
-          uint8_t* dst = wide + tok * C::kWideBytes;
-          int r = 0;
-          if (half == C::kHalf) {
-            tma_load_2d_pair(&tmAll, bar, dst, h * 128, row);
-            r = half;
+          const int halves = p.halves_k - 2 * k < 2 ? 1 : 2;
+          if (rank == 0) mbar_arrive_expect_tx(&tok_full[tok], halves * 2 * half * 128);
+          for (int h = 0; h < halves; ++h) {
+            uint8_t* dst = wide + tok * C::kWideBytes + h * (C::kWideBytes / 2);
+            const int x = (2 * k + h) * 128;
+            int r = 0;
+            if (half == C::kHalf) {
+              tma_load_2d_pair(&tmAll, bar, dst, x, row);
+              r = half;
+            }
+            for (; r + 32 <= half; r += 32) tma_load_2d_pair(&tmA32, bar, dst + r * 128, x, row + r);
+            for (; r < half; r += 8) tma_load_2d_pair(&tmA8, bar, dst + r * 128, x, row + r);
           }
-          for (; r + 32 <= half; r += 32)
-            tma_load_2d_pair(&tmA32, bar, dst + r * 128, h * 128, row + r);
-          for (; r < half; r += 8) tma_load_2d_pair(&tmA8, bar, dst + r * 128, h * 128, row + r);
         }
         if (++tok == C::kTokSlots) {
           tok = 0;
@@ -483,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (rank == 0) {
       // -------------------------------------------------------------- MMA issuer (leader)
-      uint32_t tcount = 0, cnt = 0, tok = 0, tok_phase = 0;   // cnt: slots of each warpgroup
+      uint32_t tcount = 0, slot = 0, slot_phase = 0, tok = 0, tok_phase = 0;
       const uint64_t b_desc = make_sdesc(smem_u32(wide), 16, 1024, kSwizzle128B);
       bool ok = true;
       while (ok && walk.next(sched, workers, u, k0, k1)) {
@@ -496,42 +501,40 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         ++tcount;
         const uint32_t d = tmem + buf * TN;
-        uint32_t acc = 0;
-        for (int k = k0; ok && k < k1; ++k) {
-          const int halves = p.halves_k - 2 * k < 2 ? 1 : 2;
-#pragma unroll
-          for (int wg = 0; wg < 2; ++wg) {
-            if (wg >= halves) break;
-            // (a second half missing at the end of K leaves its warpgroup a slot behind)
-            const uint32_t use = wg == 0 ? cnt & 0xFFFFu : cnt >> 16;
-            const uint32_t slot = 2 * (use & 1) + wg;
-            cnt += wg == 0 ? 1 : 0x10000;
-            if (!mbar_wait_cluster(&wide_full[slot], (use >> 1) & 1, p.limit_ns, abort_flag, p.a.status)) {
+        for (int k = k0; k < k1; ++k) {
+          if (!mbar_wait_cluster(&wide_full[slot], slot_phase, p.limit_ns, abort_flag, p.a.status)) {
+            ok = false;
+            break;
+          }
+          if constexpr (PRE) {
+            if (!mbar_wait_cluster(&tok_full[tok], tok_phase, p.limit_ns, abort_flag, p.a.status)) {
               ok = false;
               break;
             }
-            if constexpr (PRE) {
-              if (!mbar_wait(&tok_full[tok], tok_phase, p.limit_ns, abort_flag, p.a.status)) {
-                ok = false;
-                break;
-              }
-            }
-            tc_fence_after();
-            if (elect_one()) {
-              const uint64_t b = b_desc + ((PRE ? tok : slot) * C::kWideBytes >> 4);
-              const uint32_t a = tmem_wide + slot * kSlotCols;
-              mma_f16_pair_ts(d, a, b, idesc, acc);
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t b = b_desc + ((PRE ? tok : slot) * C::kWideBytes >> 4);
+            const uint32_t a = tmem_wide + slot * kSlotCols;
+            mma_f16_pair_ts(d, a, b, idesc, k != k0);
 #pragma unroll
-              for (int j = 1; j < 4; ++j) mma_f16_pair_ts(d, a + j * 8, b + 2 * j, idesc, 1);
-              tc_commit_pair(&wide_empty[slot], kPairMask);
-              if constexpr (PRE) tc_commit_pair(&tok_empty[tok], kPairMask);
+            for (int j = 1; j < 4; ++j) mma_f16_pair_ts(d, a + j * 8, b + 2 * j, idesc, 1);
+            if (2 * k + 1 < p.halves_k) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                mma_f16_pair_ts(d, a + 32 + j * 8, b + (C::kWideBytes / 2 >> 4) + 2 * j, idesc, 1);
             }
-            acc = 1;
-            if constexpr (PRE) {
-              if (++tok == C::kTokSlots) {
-                tok = 0;
-                tok_phase ^= 1;
-              }
+            tc_commit_pair(&wide_empty[slot], kPairMask);
+            if constexpr (PRE) tc_commit_pair(&tok_empty[tok], kPairMask);
+          }
+          if (++slot == kSlots) {
+            slot = 0;
+            slot_phase ^= 1;
+          }
+          if constexpr (PRE) {
+            if (++tok == C::kTokSlots) {
+              tok = 0;
+              tok_phase ^= 1;
             }
           }
         }
@@ -547,13 +550,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kWideWarp0 && warp < kOutWarp0) {
     // ---------------------------------------------------------------- widening (both CTAs)
     const int wg = (warp - kWideWarp0) >> 2, tid = threadIdx.x & 127;
-    const uint32_t taddr = tmem_wide + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t taddr = tmem_wide + (static_cast<uint32_t>((warp & 3) * 32) << 16) + wg * 32;
     // 16-byte piece j of the thread's channel is at chan ^ (j << 4) of the stage (the
     // 128-byte swizzle exchanges pieces by the row's number modulo 8)
     const uint32_t chan = static_cast<uint32_t>(tid) * 128 + (((4 * wg) ^ (tid & 7)) << 4);
     constexpr int kPieces = PRE ? 0 : (C::kHalf + 31) / 32;   // of the tokens, a thread
     int stage = 0;
-    uint32_t phase = 0, cnt = 0;
+    uint32_t phase = 0, slot = 0, slot_phase = 0;
     bool ok = true;
     while (ok && walk.next(sched, workers, u, k0, k1)) {
       const Unit un = find_unit(table, p, u);
@@ -590,7 +593,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           stage = 0;
           phase ^= 1;
         }
-        if (!work) continue;
         uint32_t w[32];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -599,18 +601,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           widen4(c[j].z, w[8 * j + 4], w[8 * j + 5]);
           widen4(c[j].w, w[8 * j + 6], w[8 * j + 7]);
         }
-        const uint32_t slot = 2 * (cnt & 1) + wg, parity = ((cnt >> 1) & 1) ^ 1;
-        ++cnt;
-        if (!mbar_wait(&wide_empty[slot], parity, p.limit_ns, abort_flag, p.a.status)) {
+        if (!mbar_wait(&wide_empty[slot], slot_phase ^ 1, p.limit_ns, abort_flag, p.a.status)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        tmem_st32(taddr + slot * kSlotCols, w);
-        const uint32_t out = smem_u32(wide + slot * C::kWideBytes);
+        if (work) tmem_st32(taddr + slot * kSlotCols, w);
+        const uint32_t out = smem_u32(wide + slot * C::kWideBytes + wg * (C::kWideBytes / 2));
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) {
-          if (from[i] != kNone) {
+          if (work && from[i] != kNone) {
             uint32_t v[8];
             widen4(x[i].x, v[0], v[1]);
             widen4(x[i].y, v[2], v[3]);
@@ -625,6 +625,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_leader(map_to_cta(smem_u32(&wide_full[slot]), 0));
+        if (++slot == kSlots) {
+          slot = 0;
+          slot_phase ^= 1;
+        }
       }
     }
   } else if (warp >= kOutWarp0) {
