@@ -38,7 +38,9 @@ constexpr int kThreads = 512;
 constexpr int kWideWarp0 = 4, kOutWarp0 = 12;
 constexpr int kSlotCols = 64;                 // tensor-memory columns of a slot's 128 FP16 values
 constexpr uint16_t kPairMask = 3;
-constexpr int kOutBarrier = 1;                // named barrier of the output warps
+constexpr int kOutBarrier = 1;                // named barriers: the output warps,
+constexpr int kFixBarrier = 2;                // the output and widening warps (3-5: each warpgroup)
+constexpr int kSetupBarrier = 6;              // all but the channel producer
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 
 struct Table {
@@ -46,6 +48,7 @@ struct Table {
   int32_t tile0[kMaxG + 1];    // its first token block
   int32_t warp_sum[2][kThreads / 32];
   int bad;
+  int fixes, fix[2];           // split units whose parts this CTA adds (two at most)
 };
 
 // PRE: the tokens are FP16 already (a widening pass before the launch).
@@ -70,7 +73,7 @@ struct Cfg {
   static constexpr int kSmemBytes = kTail + kTokSlots * kWideBytes + kStages * kRawBytes;
   static_assert((2 * kStages + 2 * kSlots + 5 + (PRE ? 2 * kTokSlots : 0)) * 8 + 8 <= 512,
                 "barriers fit below the group table");
-  static_assert(kStages >= 3, "shared memory budget");
+  static_assert(kStages >= 3 && 4 * kOutBytes <= kStages * kRawBytes, "shared memory budget");
   static_assert(kBufs * TN + kSlots * kSlotCols <= 512, "tensor memory budget");
 };
 
@@ -117,6 +120,14 @@ __device__ __forceinline__ void mma_f16_pair_ts(uint32_t d, uint32_t a, uint64_t
       "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
+}
+
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // True in one lane of the (whole) warp, the same one every time.  A role that issues copies or
@@ -317,6 +328,65 @@ __device__ __forceinline__ void rotate(float (&v)[N]) {
   for (int i = 0; i + 1 < N; ++i) v[i] = v[i + 1];
 }
 
+// 32 tokens (from the unit's token c) of the lane's channel: scaled, turned and stored by a
+// warpgroup.  A lane has a channel's tokens, a row of D wants a token's channels: the tile
+// passes through shared memory ([token][128 channels], two such tiles in turn) and leaves in
+// 16-byte pieces, a token's 128 channels contiguous.  n: the lane's channel; sa: the scale of
+// token c + lane.
+template <bool F32, int ROW>
+__device__ __forceinline__ void emit_tile(const Int8Params& a, const Unit& un, int chan0, int c,
+                                          float sa, float sb, float bias, const uint32_t (&r)[32],
+                                          uint8_t* tile, int barrier) {
+  const int tid = threadIdx.x & 127, q = tid >> 5, lane = tid & 31;
+  float y[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    y[i] = fmaf(__uint_as_float(r[i]), __shfl_sync(kFull, sa, i) * sb, bias);
+  if constexpr (F32) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      *reinterpret_cast<float*>(tile + i * ROW + (q * 32 + lane) * 4) = y[i];
+  } else {
+    // neighbouring lanes pair up their channels: the even one takes the even token
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const bool odd = lane & 1;
+      const float theirs = __shfl_xor_sync(kFull, odd ? y[i] : y[i + 1], 1);
+      *reinterpret_cast<uint32_t*>(tile + (i + odd) * ROW + (q * 32 + (lane & ~1)) * 2) =
+          odd ? pack_bf16x2(theirs, y[i + 1]) : pack_bf16x2(y[i], theirs);
+    }
+  }
+  named_barrier_sync(barrier, 128);
+  const int tokens = un.rows - c < 32 ? un.rows - c : 32;
+  const int64_t left = a.N - chan0;   // channels of this CTA from its first
+  const int64_t at = static_cast<int64_t>(un.row0 + c) * a.N + chan0;
+  constexpr int kSize = F32 ? 4 : 2, kPer = 16 / kSize, kRow = 128 / kPer;
+  if (a.N % kPer == 0) {              // rows of D are 16-byte aligned
+#pragma unroll
+    for (int i = 0; i < 32 * kRow / 128; ++i) {
+      const int e = i * 128 + tid, t = e / kRow, v = e % kRow;
+      if (t < tokens && v * kPer < left)
+        __stcs(reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.D) + (at + t * a.N + v * kPer) * kSize),
+               *reinterpret_cast<const uint4*>(tile + t * ROW + v * 16));
+    }
+  } else if (tid < left) {
+    for (int t = 0; t < tokens; ++t) {
+      const uint8_t* from = tile + t * ROW + tid * kSize;
+      if constexpr (F32)
+        static_cast<float*>(a.D)[at + t * a.N + tid] = *reinterpret_cast<const float*>(from);
+      else
+        static_cast<__nv_bfloat16*>(a.D)[at + t * a.N + tid] =
+            *reinterpret_cast<const __nv_bfloat16*>(from);
+    }
+  }
+}
+
+// Worker c's part of split unit v, this CTA's half: [token][128 channels].
+__device__ __forceinline__ float* part_slot(const PairParams& p, const DSched& s, int c, int v,
+                                            int rank) {
+  return p.part + static_cast<int64_t>((c * 2 + dsk_slot(s, c, v)) * 2 + rank) * (128 * 256);
+}
+
 template <int TN, bool PRE, bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
     int8_pair_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmA8,
@@ -365,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&tok_empty[s], 1);
       }
     *abort_flag = 0;
+    table.fixes = 0;
     fence_mbar_init();
     prefetch_tmap(&tmB);
     prefetch_tmap(&tmA8);
@@ -375,15 +446,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   // both CTAs read the same sizes, so a bad table stops the whole cluster here
   if (table.bad) return;
 
-  if (warp == 1) {
-    tmem_alloc_pair(tmem_slot, 512);
-    tmem_relinquish_pair();
+  // warp 0 starts loading at once: its copies complete on barriers of this CTA alone
+  uint32_t tmem = 0;
+  if (warp == 0) {
+    cluster_arrive();
+  } else {
+    if (warp == 1) {
+      tmem_alloc_pair(tmem_slot, 512);
+      tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    named_barrier_sync(kSetupBarrier, kThreads - 32);
+    cluster_arrive();
+    cluster_wait();
+    tc_fence_after();
+    tmem = *tmem_slot;
   }
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
   const uint32_t tmem_wide = tmem + 512 - kSlots * kSlotCols;
   const int worker = static_cast<int>(blockIdx.x >> 1), workers = static_cast<int>(gridDim.x >> 1);
   const DSched sched = make_dsched(table.tile0[p.a.G] * p.num_n_tiles, p.stages_k, 1, workers,
@@ -437,6 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         volatile int no_abort = 0;
         mbar_wait(&full[s], (armed_parity >> s) & 1u, p.limit_ns / 4 + 1, &no_abort, nullptr);
       }
+    __syncwarp();
+    cluster_wait();
   } else if (PRE && warp == 2) {
     // ---------------------------------------------------------------- producer, FP16 tokens
     // A warp of its own: with both on one warp the issuing itself (some 1100 cycles for a
@@ -633,19 +713,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kOutWarp0) {
     // ---------------------------------------------------------------- output (both CTAs)
-    // A lane has a channel's tokens, a row of D wants a token's channels: 32 tokens at a time
-    // pass through shared memory ([token][128 channels]) and leave in 16-byte pieces, a
-    // token's 128 channels contiguous.  The four warps move together: every step that could
-    // give up or that only one of them would take is agreed on at a barrier first, so none
-    // is left waiting.
+    // The four warps move together: every step that could give up is agreed on at a barrier
+    // first, so none is left waiting.
     const int q = warp & 3, tid = threadIdx.x & 127;
     const uint32_t acc_empty_leader = map_to_cta(smem_u32(acc_empty), 0);
-    const bool vec = p.a.N % (F32 ? 4 : 8) == 0;   // rows of D are 16-byte aligned
     uint32_t tcount = 0, flip = 0;
     while (walk.next(sched, workers, u, k0, k1)) {
       const Unit un = find_unit(table, p, u);
-      const int cols = unit_cols(un);
-      const int64_t n = un.n0 + rank * 128 + q * 32 + lane;
+      const int cols = unit_cols(un), chan0 = un.n0 + rank * 128;
+      const int64_t n = chan0 + tid;
       const bool ok = n < p.a.N;
       const float sb = ok ? p.a.sB[un.g * p.a.N + n] : 0.f;
       const float bias = ok && p.a.bias ? __bfloat162float(p.a.bias[n]) : 0.f;
@@ -661,60 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * TN;
       const bool whole = k1 - k0 == p.stages_k;
-      // 32 tokens of the lane's channel: scaled, turned and stored
-      auto finish = [&](int c, float scale_a, const uint32_t (&r)[32]) {
-        uint8_t* tile = stage_out + flip * C::kOutBytes;
-        flip ^= 1;
-        float y[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          y[i] = fmaf(__uint_as_float(r[i]), __shfl_sync(kFull, scale_a, i) * sb, bias);
-        if constexpr (F32) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            *reinterpret_cast<float*>(tile + i * C::kOutRow + (q * 32 + lane) * 4) = y[i];
-        } else {
-          // neighbouring lanes pair up their channels: the even one takes the even token
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const bool odd = lane & 1;
-            const float theirs = __shfl_xor_sync(kFull, odd ? y[i] : y[i + 1], 1);
-            *reinterpret_cast<uint32_t*>(tile + (i + odd) * C::kOutRow + (q * 32 + (lane & ~1)) * 2) =
-                odd ? pack_bf16x2(theirs, y[i + 1]) : pack_bf16x2(y[i], theirs);
-          }
-        }
-        named_barrier_sync(kOutBarrier, 128);
-        const int tokens = un.rows - c < 32 ? un.rows - c : 32;
-        const int64_t left = p.a.N - un.n0 - rank * 128;   // channels of this CTA from its first
-        const int64_t at = static_cast<int64_t>(un.row0 + c) * p.a.N + un.n0 + rank * 128;
-        constexpr int kSize = F32 ? 4 : 2, kPer = 16 / kSize, kRow = 128 / kPer;
-        if (vec) {
-#pragma unroll
-          for (int i = 0; i < 32 * kRow / 128; ++i) {
-            const int e = i * 128 + tid, t = e / kRow, v = e % kRow;
-            if (t < tokens && v * kPer < left)
-              __stcs(reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.a.D) +
-                                              (at + t * p.a.N + v * kPer) * kSize),
-                     *reinterpret_cast<const uint4*>(tile + t * C::kOutRow + v * 16));
-          }
-        } else if (tid < left) {
-          for (int t = 0; t < tokens; ++t) {
-            const uint8_t* from = tile + t * C::kOutRow + tid * kSize;
-            if constexpr (F32)
-              static_cast<float*>(p.a.D)[at + t * p.a.N + tid] = *reinterpret_cast<const float*>(from);
-            else
-              static_cast<__nv_bfloat16*>(p.a.D)[at + t * p.a.N + tid] =
-                  *reinterpret_cast<const __nv_bfloat16*>(from);
-          }
-        }
-      };
       const int v = u - sched.t_dp;
-      // a slot of partial sums: [quarter][token][32 channels]
-      auto slot_of = [&](int c) {
-        return p.part + static_cast<int64_t>((c * 2 + dsk_slot(sched, c, v)) * 2 + rank) * (128 * 256) +
-               q * (32 * 256) + lane;
-      };
-      float* mine = whole ? nullptr : slot_of(worker);
+      float* mine = whole ? nullptr : part_slot(p, sched, worker, v, rank) + tid;
 #pragma unroll 1
       for (int c = 0; c < cols; c += 32) {
         uint32_t r[32];
@@ -726,44 +750,74 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) arrive_leader(acc_empty_leader + buf * 8);
         }
         if (whole) {
-          finish(c, sa[0], r);
+          emit_tile<F32, C::kOutRow>(p.a, un, chan0, c, sa[0], sb, bias, r,
+                                     stage_out + flip * C::kOutBytes, kOutBarrier);
+          flip ^= 1;
+          rotate(sa);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            if (c + i < un.rows) __stcg(mine + (c + i) * 32, __uint_as_float(r[i]));
+            if (c + i < un.rows) __stcg(mine + (c + i) * 128, __uint_as_float(r[i]));
         }
-        if (whole) rotate(sa);
       }
       if (whole) continue;
+      // counted in; the last contributor's CTA adds the parts when its walk is over
       __threadfence();
       named_barrier_sync(kOutBarrier, 128);
-      const int c_lo = dsk_first_worker(sched, v), c_hi = dsk_last_worker(sched, v);
-      int last = 0;
       if (tid == 0) {
         int* ctr = p.arrivals + (v * 2 + rank) * 8;
-        last = atomicAdd(ctr, 1) + 1 == c_hi - c_lo + 1;
-        if (last) *ctr = 0;   // every contributor has counted itself in
+        if (atomicAdd(ctr, 1) + 1 == dsk_last_worker(sched, v) - dsk_first_worker(sched, v) + 1) {
+          *ctr = 0;   // every contributor has counted itself in
+          table.fix[table.fixes++] = u;
+        }
       }
-      if (!out_agree(tid != 0 || last)) continue;
-      __threadfence();
+    }
+  }
+  if (sched.P > 0 && warp >= kWideWarp0) {
+    // ---------------------------------------------------------------- split units' sums
+    // By the output and the widening warpgroups together, 32 tokens each in turn: the sum is
+    // bound by the latency of the parts' loads, so what counts is how many are in flight.
+    // The parts are added in K order, whoever came last.
+    named_barrier_sync(kFixBarrier, 384);
+    const int wg = (warp - kWideWarp0) >> 2, tid = threadIdx.x & 127;
+    uint8_t* tiles = wg == 2 ? stage_out : raw + wg * 2 * C::kOutBytes;   // the ring is idle now
+    uint32_t flip = 0;
+    if (table.fixes > 0) __threadfence();
+    for (int f = 0; f < table.fixes; ++f) {
+      const int v = table.fix[f] - sched.t_dp;
+      const Unit un = find_unit(table, p, table.fix[f]);
+      const int chan0 = un.n0 + rank * 128;
+      const int64_t n = chan0 + tid;
+      const bool ok = n < p.a.N;
+      const float sb = ok ? p.a.sB[un.g * p.a.N + n] : 0.f;
+      const float bias = ok && p.a.bias ? __bfloat162float(p.a.bias[n]) : 0.f;
+      const int c_lo = dsk_first_worker(sched, v), c_hi = dsk_last_worker(sched, v);
 #pragma unroll 1
-      for (int c = 0; c < cols; c += 32) {
+      for (int c = wg * 32; c < un.rows; c += 96) {
+        const float sa = c + lane < un.rows ? p.a.sA[un.row0 + c + lane] : 0.f;
         float sum[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) sum[i] = 0.f;
-        for (int cc = c_lo; cc <= c_hi; ++cc) {
-          const float* from = slot_of(cc) + c * 32;
-          float y[32];
+#pragma unroll 1
+        for (int cc = c_lo; cc <= c_hi; cc += 2) {
+          const bool two = cc < c_hi;
+          const float* x = part_slot(p, sched, cc, v, rank) + tid + c * 128;
+          const float* y = part_slot(p, sched, two ? cc + 1 : cc, v, rank) + tid + c * 128;
+          float xs[32], ys[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = c + i < un.rows ? __ldcg(from + i * 32) : 0.f;
+          for (int i = 0; i < 32; ++i) {
+            xs[i] = c + i < un.rows ? __ldcg(x + i * 128) : 0.f;
+            ys[i] = two && c + i < un.rows ? __ldcg(y + i * 128) : 0.f;
+          }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) sum[i] += y[i];
+          for (int i = 0; i < 32; ++i) sum[i] = sum[i] + xs[i] + ys[i];
         }
         uint32_t r[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(sum[i]);
-        finish(c, sa[0], r);
-        rotate(sa);
+        emit_tile<F32, C::kOutRow>(p.a, un, chan0, c, sa, sb, bias, r, tiles + flip * C::kOutBytes,
+                                   kOutBarrier + 2 + wg);
+        flip ^= 1;
       }
     }
   }
