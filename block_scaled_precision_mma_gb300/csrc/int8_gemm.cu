@@ -400,7 +400,8 @@ bsmma_status launch_int8_gemm(const int8_t* A, const float* sA, const int8_t* B,
   p.G = G;
   p.status = dev->status;
   const int64_t per_group = (total_M + G - 1) / G;
-  if (per_group > 8 && K > 0) return int8::launch_pair(p, f32, dev, stream);
+  if ((per_group > 8 || static_cast<int64_t>(G) * N * K > (8 << 20)) && K > 0)
+    return int8::launch_pair(p, f32, dev, stream);
   if (per_group <= 8) return launch_rows<1>(p, f32, stream);
   if (per_group <= 16) return launch_rows<2>(p, f32, stream);
   return launch_rows<4>(p, f32, stream);

@@ -24,6 +24,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
+
 #include "int8.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -62,7 +64,7 @@ struct Cfg {
   static constexpr int kBufs = 2 * TN + 2 * kSlotCols <= 512 ? 2 : 1;
   static constexpr int kFree = (512 - kBufs * TN) / kSlotCols;
   static constexpr int kSlots = PRE ? (kFree < 4 ? kFree : 4) : TN > 128 ? 2 : 3;
-  static constexpr int kTokSlots = PRE ? (TN > 192 ? 4 : 5) : kSlots;
+  static constexpr int kTokSlots = PRE ? (TN > 192 ? (F32 ? 3 : 4) : 5) : kSlots;
   // output tile: 32 tokens x 128 channels, rows padded so that two rows' halves of the banks
   // do not meet
   static constexpr int kOutRow = F32 ? 512 : 256 + 64;
@@ -465,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_wide = tmem + 512 - kSlots * kSlotCols;
   const int worker = static_cast<int>(blockIdx.x >> 1), workers = static_cast<int>(gridDim.x >> 1);
   const DSched sched = make_dsched(table.tile0[p.a.G] * p.num_n_tiles, p.stages_k, 1, workers,
-                                   p.part != nullptr, 6, 4);
+                                   p.part != nullptr, 14, 4);
   Walk walk(sched, worker);
   int u, k0, k1;
 
@@ -910,23 +912,74 @@ __global__ void __launch_bounds__(256) widen_kernel(const uint4* __restrict__ in
 }
 }  // namespace
 
+// Which tile a launch takes: the cheapest by an estimate in SM cycles that the host can make
+// from the sizes alone (rows a group as if evenly spread).
+//   - A 128-K stage costs its eight MMAs, 37 / 45 / 73 / 105 / 137 cycles each at 16 / 64 / 128 /
+//     192 / 256 columns (measured, one instruction stream), or the 16 KB of channels it
+//     streams, 760 cycles when every SM streams.
+//   - A wave of units that leaves pairs idle is split over them when that is shorter; a
+//     split costs about 14 stages (parts written, counted, read back).  Measured at 14336 x
+//     4096, 128 rows: 27 us unsplit, 35 us split at 56 units on 76 pairs.
+//   - Tokens that come as FP16 cost a pass over them first.  At 4096 x 14336 x 4096: 272 us
+//     with it (TN 192), 312 us without (TN 256); the latter wins for short or narrow products.
+struct Choice {
+  int tn;
+  bool pre;
+};
+double estimate(const Int8Params& a, int tn, bool pre, int pairs) {
+  const double active = a.total_M < a.G ? static_cast<double>(a.total_M) : a.G;
+  const double rows = active > 0 ? a.total_M / active : 0;
+  // uneven groups end in a part-filled block each
+  const double blocks_g = a.G == 1 ? std::ceil(rows / tn) : rows <= tn / 2.0 ? 1 : rows / tn + 0.5;
+  double cols = rows / blocks_g;
+  if (a.G > 1 && cols < tn) cols = std::fmin(tn, cols * 1.25);
+  const double mma = cols <= 64 ? 36 + cols * 0.14 : cols * 0.5 + 9;
+  // without PRE, a stage's tokens are widened too, and shared memory carries them thrice
+  const double stage = std::fmax(760, 8 * mma * (pre ? 1.05 : tn > 128 ? 1.2 : 1.1));
+  const double ks = static_cast<double>((a.K + 127) / 128);
+  const double units = blocks_g * active * ((a.N + 255) / 256);
+  const double full = std::floor(units / pairs), rem = units - full * pairs;
+  const double tail = rem > 0 ? std::fmin(ks, ks * rem / pairs + 14) : 0;
+  const double drain = tn > 192 ? full * 5000 : 0;   // one accumulator: not overlapped
+  return (full * ks + tail) * stage + drain + (pre ? 8000 + a.total_M * a.K * 0.9e-3 : 0);
+}
+Choice choose(const Int8Params& a, int pairs) {
+  const Choice all[] = {{64, false}, {128, false}, {256, false}, {192, true}, {256, true}};
+  Choice best = all[0];
+  double least = 0;
+  for (const Choice& c : all) {
+    const double t = estimate(a, c.tn, c.pre, pairs);
+    if (least == 0 || t < least) {
+      least = t;
+      best = c;
+    }
+  }
+  return best;
+}
+
 bsmma_status launch_pair(const Int8Params& a, bool f32, const DeviceInfo* dev, cudaStream_t stream) {
   PairParams p;
   p.a = a;
-  const int64_t per_group = (a.total_M + a.G - 1) / a.G;
-#define BSMMA_INT8_TN(T, PRE, X) \
-  (f32 ? launch_tn<T, PRE, true>(p, X, dev, stream) : launch_tn<T, PRE, false>(p, X, dev, stream))
-  if (per_group <= 32) return BSMMA_INT8_TN(64, false, nullptr);
-  if (per_group <= 128) return BSMMA_INT8_TN(128, false, nullptr);
+  Choice c = choose(a, dev->sm_count / 2);
   void* tok16 = nullptr;
-  const bsmma_status st = stream_workspace(a.total_M * a.K * 2, stream, &tok16);
-  if (st == BSMMA_ERR_WORKSPACE) return BSMMA_INT8_TN(256, false, nullptr);
-  if (st != BSMMA_OK) return st;
-  const int64_t n16 = a.total_M * a.K / 16, blocks = (n16 + 255) / 256;
-  widen_kernel<<<static_cast<unsigned>(blocks < dev->sm_count * 8 ? blocks : dev->sm_count * 8), 256, 0,
-                 stream>>>(reinterpret_cast<const uint4*>(a.A), static_cast<uint4*>(tok16), n16);
-  count_launches(1);
-  return BSMMA_INT8_TN(192, true, tok16);
+  if (c.pre) {
+    const bsmma_status st = stream_workspace(a.total_M * a.K * 2, stream, &tok16);
+    if (st == BSMMA_ERR_WORKSPACE)   // captured without one: widened in the kernel
+      c = Choice{256, false};
+    else if (st != BSMMA_OK)
+      return st;
+  }
+  if (c.pre) {
+    const int64_t n16 = a.total_M * a.K / 16, blocks = (n16 + 255) / 256;
+    widen_kernel<<<static_cast<unsigned>(blocks < dev->sm_count * 8 ? blocks : dev->sm_count * 8), 256, 0,
+                   stream>>>(reinterpret_cast<const uint4*>(a.A), static_cast<uint4*>(tok16), n16);
+    count_launches(1);
+  }
+#define BSMMA_INT8_TN(T, PRE) \
+  (f32 ? launch_tn<T, PRE, true>(p, tok16, dev, stream) : launch_tn<T, PRE, false>(p, tok16, dev, stream))
+  if (c.pre) return c.tn == 192 ? BSMMA_INT8_TN(192, true) : BSMMA_INT8_TN(256, true);
+  return c.tn == 64 ? BSMMA_INT8_TN(64, false) : c.tn == 128 ? BSMMA_INT8_TN(128, false)
+                                                             : BSMMA_INT8_TN(256, false);
 #undef BSMMA_INT8_TN
 }
 
