@@ -65,6 +65,8 @@ class BsmmaError(RuntimeError):
 def load(path: str | None = None):
     """Loads libbsmma.so (built in-tree by ``build()``) and declares its ABI."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -130,8 +132,11 @@ def load(path: str | None = None):
 
 
 def _stream(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return int(s.cuda_stream) if hasattr(s, "cuda_stream") else int(s)
+    if stream is None:
+        # the handle of torch.cuda.current_stream() without building the Stream object,
+        # which costs as much host time as a kernel launch
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _ptr(t) -> int | None:
@@ -382,10 +387,18 @@ def _dtype_of(t, what: str) -> int:
 
 
 def _expect(t, dtype, shape, what: str):
-    """`t` (None passes) has this dtype and shape."""
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)}, "
+    """`t` (None passes) has this dtype and shape (a tuple)."""
+    if t is not None and (t.dtype != dtype or t.shape != shape):
+        raise ValueError(f"{what} must be {dtype} of shape {shape}, "
                          f"not {t.dtype} of {tuple(t.shape)}")
+
+
+def _output(t, dtype, shape, like, what: str):
+    """The output to write: `t` if it has this dtype and shape (a tuple), or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _expect(t, dtype, shape, what)
+    return t
 
 
 def moe_route(logits, k, score="softmax", bias=None, groups=1, topk_groups=1, group_top=1,
@@ -395,12 +408,8 @@ def moe_route(logits, k, score="softmax", bias=None, groups=1, topk_groups=1, gr
     'sigmoid'; ``bias``: float32 [E], added to the scores for the choice alone."""
     T, E = logits.shape
     _expect(bias, torch.float32, (E,), "bias")
-    if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    if weights is None:
-        weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    _expect(ids, torch.int32, (T, k), "ids")
-    _expect(weights, torch.float32, (T, k), "weights")
+    ids = _output(ids, torch.int32, (T, k), logits, "ids")
+    weights = _output(weights, torch.float32, (T, k), logits, "weights")
     _check(load().moe_route(_ptr(logits), _dtype_of(logits, "logits"), T, E, k, SCORES[score],
                             _ptr(bias), groups, topk_groups, group_top, int(bool(renormalize)),
                             scale, _ptr(ids), _ptr(weights), _stream(stream)), "moe_route")
@@ -415,9 +424,7 @@ def moe_route_backward(logits, ids, dweights, score="softmax", renormalize=True,
     k = ids.shape[1]
     _expect(ids, torch.int32, (T, k), "ids")
     _expect(dweights, torch.float32, (T, k), "dweights")
-    if dlogits is None:
-        dlogits = torch.empty_like(logits)
-    _expect(dlogits, logits.dtype, (T, E), "dlogits")
+    dlogits = _output(dlogits, logits.dtype, (T, E), logits, "dlogits")
     _check(load().moe_route_backward(_ptr(logits), _dtype_of(logits, "logits"), T, E, k,
                                      SCORES[score], int(bool(renormalize)), scale, _ptr(ids),
                                      _ptr(dweights), _ptr(dlogits), _stream(stream)),
@@ -435,15 +442,9 @@ def moe_plan(ids, experts, m_sizes=None, src=None, pos=None, stream=None):
     [T * k], pos int32 [T, k]); see ``moe_plan`` in bsmma.h."""
     T, k = ids.shape
     _expect(ids, torch.int32, (T, k), "ids")
-    if m_sizes is None:
-        m_sizes = torch.empty(experts, dtype=torch.int64, device=ids.device)
-    if src is None:
-        src = torch.empty(T * k, dtype=torch.int32, device=ids.device)
-    if pos is None:
-        pos = torch.empty((T, k), dtype=torch.int32, device=ids.device)
-    _expect(m_sizes, torch.int64, (experts,), "m_sizes")
-    _expect(src, torch.int32, (T * k,), "src")
-    _expect(pos, torch.int32, (T, k), "pos")
+    m_sizes = _output(m_sizes, torch.int64, (experts,), ids, "m_sizes")
+    src = _output(src, torch.int32, (T * k,), ids, "src")
+    pos = _output(pos, torch.int32, (T, k), ids, "pos")
     _check(load().moe_plan(_ptr(ids), T, k, experts, _ptr(m_sizes), _ptr(src), _ptr(pos),
                            _stream(stream)), "moe_plan")
     return m_sizes, src, pos
@@ -456,9 +457,7 @@ def moe_combine(Y, pos, weights=None, out=None, stream=None):
     T, k = pos.shape
     _expect(pos, torch.int32, (T, k), "pos")
     _expect(weights, torch.float32, (T, k), "weights")
-    if out is None:
-        out = torch.empty((T, H), dtype=Y.dtype, device=Y.device)
-    _expect(out, Y.dtype, (T, H), "out")
+    out = _output(out, Y.dtype, (T, H), Y, "out")
     _check(load().moe_combine(_ptr(Y), _dtype_of(Y, "Y"), R, H, _ptr(pos), _ptr(weights), T, k,
                               _ptr(out), _stream(stream)), "moe_combine")
     return out
@@ -473,14 +472,11 @@ def moe_combine_backward(dout, Y, src, pos, weights=None, dY=None, dweights=None
     _expect(src, torch.int32, (T * k,), "src")
     _expect(weights, torch.float32, (T, k), "weights")
     _expect(Y, dout.dtype, (T * k, H), "Y")
-    if weights is not None and Y is None:
+    if (weights is not None or dweights is not None) and Y is None:
         raise ValueError("Y is needed for the gradient of the weights")
-    if dY is None:
-        dY = torch.empty((T * k, H), dtype=dout.dtype, device=dout.device)
-    if weights is not None and dweights is None:
-        dweights = torch.empty((T, k), dtype=torch.float32, device=dout.device)
-    _expect(dY, dout.dtype, (T * k, H), "dY")
-    _expect(dweights, torch.float32, (T, k), "dweights")
+    dY = _output(dY, dout.dtype, (T * k, H), dout, "dY")
+    if weights is not None or dweights is not None:
+        dweights = _output(dweights, torch.float32, (T, k), dout, "dweights")
     _check(load().moe_combine_backward(_ptr(dout), _dtype_of(dout, "dout"), H, _ptr(Y), _ptr(src),
                                        _ptr(pos), _ptr(weights), T, k, _ptr(dY), _ptr(dweights),
                                        _stream(stream)), "moe_combine_backward")
@@ -494,12 +490,8 @@ def int8_quantize(x, src=None, k=1, codes=None, scales=None, stream=None):
     x_rows, K = x.shape
     rows = x_rows if src is None else src.numel()
     _expect(src, torch.int32, (rows,), "src")
-    if codes is None:
-        codes = torch.empty((rows, K), dtype=torch.int8, device=x.device)
-    if scales is None:
-        scales = torch.empty(rows, dtype=torch.float32, device=x.device)
-    _expect(codes, torch.int8, (rows, K), "codes")
-    _expect(scales, torch.float32, (rows,), "scales")
+    codes = _output(codes, torch.int8, (rows, K), x, "codes")
+    scales = _output(scales, torch.float32, (rows,), x, "scales")
     _check(load().int8_quantize(_ptr(x), _dtype_of(x, "x"), x_rows, K, _ptr(src), k, rows,
                                 _ptr(codes), _ptr(scales), _stream(stream)), "int8_quantize")
     return codes, scales
@@ -515,9 +507,7 @@ def int8_gemm(A, sA, B, sB, bias=None, out=None, dtype=torch.bfloat16, stream=No
     _expect(sA, torch.float32, (M,), "sA")
     _expect(sB, torch.float32, (N,), "sB")
     _expect(bias, torch.bfloat16, (N,), "bias")
-    if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=A.device)
-    _expect(out, out.dtype, (M, N), "out")
+    out = _output(out, dtype if out is None else out.dtype, (M, N), A, "out")
     _check(load().int8_gemm(_ptr(A), _ptr(sA), _ptr(B), _ptr(sB), _ptr(bias), _ptr(out),
                             _dtype_of(out, "out"), M, N, K, _stream(stream)), "int8_gemm")
     return out
@@ -534,9 +524,7 @@ def grouped_int8_gemm(X, sX, W, sW, m_sizes, out=None, dtype=torch.bfloat16, str
     _expect(sX, torch.float32, (total_M,), "sX")
     _expect(sW, torch.float32, (G, N), "sW")
     _expect(m_sizes, torch.int64, (G,), "m_sizes")
-    if out is None:
-        out = torch.empty((total_M, N), dtype=dtype, device=W.device)
-    _expect(out, out.dtype, (total_M, N), "out")
+    out = _output(out, dtype if out is None else out.dtype, (total_M, N), W, "out")
     _check(load().grouped_int8_gemm(_ptr(X) if total_M else None, _ptr(sX) if total_M else None,
                                     _ptr(W), _ptr(sW), _ptr(out) if total_M else None,
                                     _dtype_of(out, "out"), _ptr(m_sizes), total_M, G, N, K,

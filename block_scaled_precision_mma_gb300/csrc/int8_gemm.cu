@@ -31,10 +31,10 @@ constexpr uint32_t kFull = 0xFFFFFFFFu;
 // One row per TPR threads, kept in registers between the maximum and the codes (V 16-byte
 // pieces a thread), or read twice when it is longer than that (V == 0).
 //   s = amax * (1 / 127), both steps in FP32 (1 when that is zero), code = rint(x / s) within [-127, 127].
-// The code is that of the correctly rounded quotient x / s.  t = x * (1 / s) is within
-// 2^-14 of it for |t| <= 127 (two roundings of relative size 2^-24, and the quotient's own),
-// so rint(t) is already the code unless t is that close to a half; only there is the
-// quotient computed.
+// The code is that of the correctly rounded quotient x / s.  With y = RN(1 / s), x * y is
+// within 127 * 2^-24 of x / s, and the rounded quotient is within 2^-18: together below
+// 2^-16.  So rint(x * y), from one fused step, is already the code unless x * y is that close
+// to a half (2^-15 is taken); only there is the quotient computed.
 struct QuantParams {
   const void* x;
   const int32_t* src;    // nullptr: row r is row r of x
@@ -75,7 +75,7 @@ __device__ __forceinline__ void codes_of(const float (&x)[N], float s, float inv
   for (int i = 0; i < N; ++i) {
     const float y = fmaf(x[i], inv, kMagic);
     const float f = fmaf(x[i], inv, -(y - kMagic));
-    near_half |= fabsf(f) > 0.5f - 0x1p-13f;
+    near_half |= fabsf(f) > 0.5f - 0x1p-15f;
     b[i] = __float_as_uint(y);
   }
   if (near_half) {
@@ -105,11 +105,19 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) int8_quantize_kernel(co
   constexpr int kHeld = V > 0 ? V : 1;
   uint4 held[kHeld];
   uint32_t amax = 0;
+  // BF16: the maximum of two magnitudes at a time, kept in a pair
   auto fold = [&](const uint4& v) {
-    float f[kN];
-    unpack<F32>(v, f);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < kN; ++i) amax = max(amax, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (F32) {
+        amax = max(amax, w[i] & 0x7FFFFFFFu);
+      } else {
+        __nv_bfloat162 a = *reinterpret_cast<__nv_bfloat162*>(&amax);
+        a = __hmax2(a, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+        amax = *reinterpret_cast<uint32_t*>(&a);
+      }
+    }
   };
   if constexpr (V > 0) {
 #pragma unroll
@@ -123,6 +131,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) int8_quantize_kernel(co
   } else if (xr >= 0) {
     for (int v = tid; v < p.vecs; v += TPR) fold(x[v]);
   }
+  if constexpr (!F32) amax = max(amax << 16, amax & 0xFFFF0000u);
   amax = __reduce_max_sync(kFull, amax);
   if constexpr (TPR > 32) {
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;

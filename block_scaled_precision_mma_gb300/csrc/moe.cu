@@ -10,6 +10,7 @@
 
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -59,37 +60,134 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // ------------------------------------------------------------------------- routing
-// One warp per token; lane l holds experts l, l + 32, ... (V of them).  The k choices are
-// k rounds of a warp-wide maximum over (key, lowest index): each lane keeps the best of
-// its own V keys and only the round's winner looks for its next one.
+// One warp per token, V experts a lane.  The k choices are k rounds of a warp-wide maximum.
+// Instructions bound it, not its bytes (a token of 128 experts is 256 bytes), so a round is
+// kept short: each lane holds the best of its own keys, and only what the round took changes.
 struct RouteParams {
   const void* logits;
   const float* bias;
   int64_t T;
   int E, k, groups, topk_groups, group_top;
+  uint32_t per_magic;   // e * per_magic >> 32 is e / (E / groups) for e < 1024
   int sigmoid, renormalize;
   float scale;
   int32_t* ids;
   float* weights;
 };
 
+// The weights of the chosen: lane j has the j-th's logit x (id -1: none).
+__device__ __forceinline__ void write_choice(const RouteParams& p, int64_t t, int id, float x,
+                                             float mx, float denom) {
+  const int lane = threadIdx.x & 31;
+  float s = 0.f;
+  if (id >= 0) s = p.sigmoid ? sigmoid(x) : expf(x - mx) / denom;
+  if (p.renormalize) {
+    const float sum = warp_sum(s);
+    s = sum > 0.f ? s / sum : 0.f;
+  }
+  if (lane < p.k) {
+    p.ids[t * p.k + lane] = id;
+    p.weights[t * p.k + lane] = s * p.scale;
+  }
+}
+
 // Both score functions increase with the logit, so without a bias the keys are the logits
-// themselves and no rounding of a score can reorder the choice.
-template <bool F32, int V>
-__global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
+// themselves and no rounding of a score can reorder the choice.  A BF16 logit's ordered 16
+// bits and the complement of its index make one 32-bit key: one reduction finds the largest
+// and, among equals, the lowest index.  Lane l holds experts 64 j + 2 l + {0, 1} (E even: pairs
+// are 4-byte loads) or 32 j + l.
+template <int V, bool PAIRS>
+__global__ void __launch_bounds__(128) route_bf16_kernel(const RouteParams p) {
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= p.T) return;
-  float key[V];
-  float mx = -INFINITY;
+  const uint16_t* row = static_cast<const uint16_t*>(p.logits) + t * p.E;
+  uint32_t key[V];   // 0: closed or taken
+#pragma unroll
+  for (int i = 0; i < V; ++i) key[i] = 0;
+  auto key_of = [](uint32_t bits, int e) {
+    if ((bits & 0x7FFFu) > 0x7F80u || bits == 0xFF80u) return 0u;   // NaN, -inf
+    if (bits == 0x8000u) bits = 0;                                  // -0 and +0 are one key
+    const uint32_t o = (bits & 0x8000u) ? ~bits & 0xFFFFu : bits | 0x8000u;
+    return o << 16 | static_cast<uint32_t>(0xFFFF - e);
+  };
+  if constexpr (PAIRS) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const int e = 32 * i + 2 * lane;
+      if (e < p.E) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(row + e);
+        key[i] = key_of(w & 0xFFFFu, e);
+        key[i + 1] = key_of(w >> 16, e + 1);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (32 * i + lane < p.E) key[i] = key_of(row[32 * i + lane], 32 * i + lane);
+  }
+  auto logit = [](uint32_t k) {
+    const uint32_t o = k >> 16;
+    return fminf(__uint_as_float((o & 0x8000u ? o & 0x7FFFu : ~o & 0xFFFFu) << 16), FLT_MAX);
+  };
+  uint32_t best = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) best = max(best, key[i]);
+  uint32_t mine = 0, first = 0;   // lane j keeps the j-th choice
+  for (int j = 0; j < p.k; ++j) {
+    const uint32_t top = __reduce_max_sync(kFull, best);
+    if (top == 0) break;
+    if (j == 0) first = top;
+    if (lane == j) mine = top;
+    if (best == top) {
+      best = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (key[i] == top) key[i] = 0;
+        best = max(best, key[i]);
+      }
+    }
+  }
+  const float mx = first ? logit(first) : 0.f;
+  float denom = 1.f;
+  if (!p.sigmoid && !p.renormalize) {
+    float sum = 0.f;   // the chosen are 0 in key[] by now: theirs come from `mine`
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (key[i]) sum += expf(logit(key[i]) - mx);
+    if (mine) sum += expf(logit(mine) - mx);
+    sum = warp_sum(sum);
+    denom = sum > 0.f ? sum : 1.f;
+  }
+  write_choice(p, t, mine ? 0xFFFF - static_cast<int>(mine & 0xFFFFu) : -1, mine ? logit(mine) : 0.f, mx,
+               denom);
+}
+
+// FP32 logits, a bias or groups: 32-bit keys, lane l holding experts 32 i + l.
+template <bool F32, int V>
+__global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
+  extern __shared__ float smem[];
+  const int lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (t >= p.T) return;
+  float x[V], key[V], bias[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int e = lane + 32 * i;
-    key[i] = e < p.E ? clean_logit(load_elem<F32>(p.logits, t * p.E + e)) : -INFINITY;
-    mx = fmaxf(mx, key[i]);
+    x[i] = -INFINITY;
+    bias[i] = 0.f;
+    if (e < p.E) {
+      x[i] = load_elem<F32>(p.logits, t * p.E + e);
+      if (p.bias) bias[i] = p.bias[e];
+    }
   }
-  const bool summed_groups = p.groups > 1 && p.group_top > 1;
-  const bool all_scores = p.bias || summed_groups;
+  float mx = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    key[i] = x[i] = clean_logit(x[i]);
+    mx = fmaxf(mx, x[i]);
+  }
+  const bool all_scores = p.bias || (p.groups > 1 && p.group_top > 1);
   float denom = 1.f;
   if (!p.sigmoid) {
     mx = warp_max(mx);
@@ -97,57 +195,38 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
     if (all_scores || !p.renormalize) {
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum += expf(key[i] - mx);
+      for (int i = 0; i < V; ++i) sum += expf(x[i] - mx);
       sum = warp_sum(sum);
       denom = sum > 0.f ? sum : 1.f;
     }
   }
-  auto score = [&](float x) { return p.sigmoid ? sigmoid(x) : expf(x - mx) / denom; };
-
-  float of[V];   // what a group is valued by
+  float* row = smem + (threadIdx.x >> 5) * p.E;   // what a group is valued by (groups only)
 #pragma unroll
-  for (int i = 0; i < V; ++i) of[i] = key[i];
-  if (all_scores) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane + 32 * i;
-      if (e < p.E) {
-        float s = -INFINITY;
-        if (key[i] != -INFINITY) {
-          s = score(key[i]);
-          if (p.bias) {
-            s += p.bias[e];
-            if (s != s) s = -INFINITY;
-            key[i] = s;
-          }
-        }
-        of[i] = s;
-      }
+  for (int i = 0; i < V; ++i) {
+    const int e = lane + 32 * i;
+    float value = x[i];
+    if (all_scores && x[i] != -INFINITY) {
+      value = (p.sigmoid ? sigmoid(x[i]) : expf(x[i] - mx) / denom) + bias[i];
+      if (value != value) value = -INFINITY;
+      if (p.bias) key[i] = value;
     }
+    if (p.groups > 1 && e < p.E) row[e] = value;
   }
   if (p.groups > 1) {
-    // value of a group: the sum of its group_top largest keys (of its scores without a bias)
-    const int per = p.E / p.groups;
-    extern __shared__ float smem[];
-    float* row = smem + (threadIdx.x >> 5) * p.E;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane + 32 * i < p.E) row[lane + 32 * i] = of[i];
+    // value of a group: the sum of its group_top largest; `width` lanes (a power of two)
+    // share a group
     __syncwarp();
-    // `width` lanes (a power of two) share a group
+    const int per = p.E / p.groups;
     int width = 32;
     while (width * p.groups > 32) width >>= 1;
     const int g = lane / width;
     float a = -INFINITY, b = -INFINITY;   // the group's largest and second largest
     if (g < p.groups)
+#pragma unroll 4
       for (int i = lane % width; i < per; i += width) {
         const float v = row[g * per + i];
-        if (v > a) {
-          b = a;
-          a = v;
-        } else if (v > b) {
-          b = v;
-        }
+        b = fmaxf(b, fminf(a, v));
+        a = fmaxf(a, v);
       }
     for (int o = 1; o < width; o <<= 1) {
       const float a2 = __shfl_xor_sync(kFull, a, o), b2 = __shfl_xor_sync(kFull, b, o);
@@ -165,32 +244,41 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
     const uint32_t open = __ballot_sync(kFull, g < p.groups && ahead < p.topk_groups);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = lane + 32 * i;
-      if (e < p.E && !((open >> ((e / per) * width)) & 1u)) key[i] = -INFINITY;
+      const uint32_t e = lane + 32 * i;
+      const int of = per == 1 ? static_cast<int>(e) : static_cast<int>(__umulhi(e, p.per_magic));
+      if (e < p.E && !((open >> (of * width)) & 1u)) key[i] = -INFINITY;
     }
   }
 
-  float best = -INFINITY;
+  uint32_t best = 0;    // of the lane's keys, in an order of unsigned integers
   int at = 0;
+  float best_x = 0.f;   // its logit
   auto rescan = [&] {
-    best = -INFINITY;
+    float k = -INFINITY;
     at = 0;
+    best_x = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (key[i] > best) {
-        best = key[i];
+      if (key[i] > k) {
+        k = key[i];
         at = i;
+        best_x = x[i];
       }
+    best = k == -INFINITY ? 0u : ordered(k);
   };
   rescan();
-  int mine = -1;   // lane j keeps the j-th choice
+  int mine = -1;   // lane j keeps the j-th choice, and its logit
+  float mine_x = 0.f;
   for (int j = 0; j < p.k; ++j) {
-    const uint32_t o = ordered(best);
-    const uint32_t top = __reduce_max_sync(kFull, o);
-    if (top == ordered(-INFINITY)) break;
-    const uint32_t e = __reduce_min_sync(kFull, o == top ? static_cast<uint32_t>(lane + 32 * at)
-                                                         : 0xFFFFFFFFu);
-    if (lane == j) mine = static_cast<int>(e);
+    const uint32_t top = __reduce_max_sync(kFull, best);
+    if (top == 0) break;
+    const uint32_t e = __reduce_min_sync(kFull, best == top ? static_cast<uint32_t>(lane + 32 * at)
+                                                            : 0xFFFFFFFFu);
+    const float chosen = __shfl_sync(kFull, best_x, e & 31);
+    if (lane == j) {
+      mine = static_cast<int>(e);
+      mine_x = chosen;
+    }
     if (static_cast<int>(e & 31u) == lane) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
@@ -198,17 +286,7 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
       rescan();
     }
   }
-  // the chosen experts' logits are read again from the row (cached)
-  float s = 0.f;
-  if (mine >= 0) s = score(clean_logit(load_elem<F32>(p.logits, t * p.E + mine)));
-  if (p.renormalize) {
-    const float sum = warp_sum(s);
-    s = sum > 0.f ? s / sum : 0.f;
-  }
-  if (lane < p.k) {
-    p.ids[t * p.k + lane] = mine;
-    p.weights[t * p.k + lane] = s * p.scale;
-  }
+  write_choice(p, t, mine, mine_x, mx, denom);
 }
 
 // ------------------------------------------------------------------- routing, gradient
@@ -218,8 +296,8 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
 //   softmax:                dx_i = q_i (d_i - sum_m q_m d_m)             (every expert)
 //   sigmoid, renormalised:  dx_j = q_j (1 - q_j) (d_j - sum p d) / S     (chosen only)
 //   sigmoid:                dx_j = q_j (1 - q_j) d_j                     (chosen only)
-// A warp builds its token's row in shared memory and writes it in 16-byte pieces where
-// rows are 16-byte aligned.
+// A warp builds its token's row in shared memory, in the logits' type, and writes it in
+// 16-byte pieces where rows are 16-byte aligned.
 struct RouteGradParams {
   const void* logits;
   const int32_t* ids;
@@ -231,28 +309,49 @@ struct RouteGradParams {
   void* dlogits;
 };
 
-template <bool F32, bool VEC>
+// EVERY: the second form, which reads the whole row; the others read the chosen logits.
+template <bool F32, bool EVERY>
 __global__ void __launch_bounds__(128) route_grad_kernel(const RouteGradParams p) {
-  extern __shared__ __align__(16) float smem[];
+  extern __shared__ __align__(16) uint8_t smem_b[];
+  using Elem = typename std::conditional<F32, float, __nv_bfloat16>::type;
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= p.T) return;
-  const int ld = (p.E + 7) & ~7;
-  float* row = smem + (threadIdx.x >> 5) * ld;
+  constexpr int kPer = 16 / sizeof(Elem);
+  const int pieces = (p.E + kPer - 1) / kPer;   // of the row, 16 bytes each
+  Elem* row = reinterpret_cast<Elem*>(smem_b + (threadIdx.x >> 5) * pieces * 16);
   int id = lane < p.k ? p.ids[t * p.k + lane] : -1;
   if (id >= p.E) id = -1;
-  const float d = id >= 0 ? p.scale * p.dweights[t * p.k + lane] : 0.f;
-  const float x = id >= 0 ? clean_logit(load_elem<F32>(p.logits, t * p.E + id)) : -INFINITY;
+  float d = 0.f, x = -INFINITY;
+  if (id >= 0) {
+    d = p.scale * p.dweights[t * p.k + lane];
+    x = clean_logit(load_elem<F32>(p.logits, t * p.E + id));
+  }
+  for (int v = lane; v < pieces; v += 32) reinterpret_cast<uint4*>(row)[v] = make_uint4(0, 0, 0, 0);
   float out = 0.f;
-  const bool every = !p.sigmoid && !p.renormalize;
-  if (!p.sigmoid && p.renormalize) {
+  __syncwarp();
+  if constexpr (EVERY) {
+    float mx = -INFINITY, sum = 0.f;
+    for (int e = lane; e < p.E; e += 32) mx = fmaxf(mx, clean_logit(load_elem<F32>(p.logits, t * p.E + e)));
+    mx = warp_max(mx);
+    if (mx == -INFINITY) mx = 0.f;
+    for (int e = lane; e < p.E; e += 32) sum += expf(clean_logit(load_elem<F32>(p.logits, t * p.E + e)) - mx);
+    sum = warp_sum(sum);
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float q = x == -INFINITY ? 0.f : expf(x - mx) * inv;
+    const float dot = warp_sum(q * d);
+    out = q * (d - dot);
+    for (int e = lane; e < p.E; e += 32)
+      store_elem<F32>(row, e, -expf(clean_logit(load_elem<F32>(p.logits, t * p.E + e)) - mx) * inv * dot);
+    __syncwarp();
+  } else if (!p.sigmoid) {
     float mx = warp_max(x);
     if (mx == -INFINITY) mx = 0.f;
     float e = expf(x - mx);
     const float sum = warp_sum(e);
     e = sum > 0.f ? e / sum : 0.f;
     out = e * (d - warp_sum(e * d));
-  } else if (p.sigmoid) {
+  } else {
     const float q = x == -INFINITY ? 0.f : sigmoid(x);
     float g = d;
     if (p.renormalize) {
@@ -262,48 +361,14 @@ __global__ void __launch_bounds__(128) route_grad_kernel(const RouteGradParams p
     // 1 - q as 1 / (1 + e^x): no cancellation for large logits
     out = x == -INFINITY ? 0.f : q * sigmoid(-x) * g;
   }
-  if (every) {
-    float mx = -INFINITY;
-    for (int e = lane; e < p.E; e += 32) {
-      const float v = clean_logit(load_elem<F32>(p.logits, t * p.E + e));
-      row[e] = v;
-      mx = fmaxf(mx, v);
-    }
-    mx = warp_max(mx);
-    if (mx == -INFINITY) mx = 0.f;
-    float sum = 0.f;
-    for (int e = lane; e < p.E; e += 32) {
-      const float v = expf(row[e] - mx);
-      row[e] = v;
-      sum += v;
-    }
-    sum = warp_sum(sum);
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const float q = x == -INFINITY ? 0.f : expf(x - mx) * inv;
-    const float dot = warp_sum(q * d);
-    out = q * (d - dot);
-    for (int e = lane; e < p.E; e += 32) row[e] = -row[e] * inv * dot;
-  } else {
-    for (int e = lane; e < ld; e += 32) row[e] = 0.f;
-  }
+  if (id >= 0) store_elem<F32>(row, id, out);
   __syncwarp();
-  if (id >= 0) row[id] = out;
-  __syncwarp();
-  if constexpr (VEC) {
-    if constexpr (F32) {
-      float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.dlogits) + t * p.E);
-      for (int v = lane; v < p.E / 4; v += 32) o[v] = reinterpret_cast<const float4*>(row)[v];
-    } else {
-      uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dlogits) + t * p.E);
-      for (int v = lane; v < p.E / 8; v += 32) {
-        const float4 a = reinterpret_cast<const float4*>(row)[2 * v];
-        const float4 b = reinterpret_cast<const float4*>(row)[2 * v + 1];
-        o[v] = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
-                          pack_bf16x2(b.z, b.w));
-      }
-    }
+  Elem* to = static_cast<Elem*>(p.dlogits) + t * p.E;
+  if (p.E % kPer == 0) {
+    for (int v = lane; v < pieces; v += 32)
+      reinterpret_cast<uint4*>(to)[v] = reinterpret_cast<const uint4*>(row)[v];
   } else {
-    for (int e = lane; e < p.E; e += 32) store_elem<F32>(p.dlogits, t * p.E + e, row[e]);
+    for (int e = lane; e < p.E; e += 32) to[e] = row[e];
   }
 }
 
@@ -635,13 +700,25 @@ __global__ void __launch_bounds__(256) combine_grad_kernel(const CombineParams p
   }
 }
 
+// A few tokens: one warp per block, so that they spread over the SMs.
+int route_warps(int64_t T) { return T >= 1024 ? 4 : 1; }
+
 template <bool F32, int V>
 bsmma_status launch_route_v(const RouteParams& p, cudaStream_t stream) {
-  // a few tokens: one warp per block, so that they spread over the SMs
-  const int warps = p.T >= 1024 ? 4 : 1;
-  const bool staged = p.groups > 1;
-  route_kernel<F32, V><<<static_cast<unsigned>((p.T + warps - 1) / warps), warps * 32,
-                         staged ? warps * p.E * 4 : 0, stream>>>(p);
+  const int warps = route_warps(p.T);
+  const unsigned grid = static_cast<unsigned>((p.T + warps - 1) / warps);
+  if (!F32 && !p.bias && p.groups == 1) {
+    if constexpr (V >= 2) {
+      if (p.E % 2 == 0)
+        route_bf16_kernel<V, true><<<grid, warps * 32, 0, stream>>>(p);
+      else
+        route_bf16_kernel<V, false><<<grid, warps * 32, 0, stream>>>(p);
+    } else {
+      route_bf16_kernel<V, false><<<grid, warps * 32, 0, stream>>>(p);
+    }
+  } else {
+    route_kernel<F32, V><<<grid, warps * 32, p.groups > 1 ? warps * p.E * 4 : 0, stream>>>(p);
+  }
   count_launches(1);
   return cuda_ok(cudaGetLastError());
 }
@@ -676,6 +753,8 @@ bsmma_status launch_route(const void* logits, bool f32, int64_t T, int E, int k,
   p.groups = topk_groups < groups ? groups : 1;   // every group open: no group step
   p.topk_groups = topk_groups;
   p.group_top = group_top;
+  const uint64_t per = E / p.groups;
+  p.per_magic = static_cast<uint32_t>(per > 1 ? ((uint64_t(1) << 32) + per - 1) / per : 0);
   p.sigmoid = sigmoid;
   p.renormalize = renormalize;
   p.scale = scale;
@@ -698,17 +777,17 @@ bsmma_status launch_route_backward(const void* logits, bool f32, int64_t T, int 
   p.renormalize = renormalize;
   p.scale = scale;
   p.dlogits = dlogits;
-  const int warps = T >= 1024 ? 4 : 1;
+  const int warps = route_warps(T);
   const unsigned grid = static_cast<unsigned>((T + warps - 1) / warps);
-  const int smem = warps * ((E + 7) & ~7) * 4;
-  const bool vec = E % (f32 ? 4 : 8) == 0;
+  const int per = f32 ? 4 : 8, smem = warps * ((E + per - 1) / per) * 16;
+  const bool every = !sigmoid && !renormalize;
   if (f32) {
-    if (vec)
+    if (every)
       route_grad_kernel<true, true><<<grid, warps * 32, smem, stream>>>(p);
     else
       route_grad_kernel<true, false><<<grid, warps * 32, smem, stream>>>(p);
   } else {
-    if (vec)
+    if (every)
       route_grad_kernel<false, true><<<grid, warps * 32, smem, stream>>>(p);
     else
       route_grad_kernel<false, false><<<grid, warps * 32, smem, stream>>>(p);
