@@ -445,8 +445,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmAll);
   }
   build_table(table, p);
-  // both CTAs read the same sizes, so a bad table stops the whole cluster here
-  if (table.bad) return;
+  // both CTAs read the same sizes, so a bad table stops the whole cluster here.  (With PRE
+  // the launch may have started before the widening pass has ended: one warp of every CTA
+  // waits for that, so that this grid's end is the pass's too.)
+  if (table.bad) {
+    if (PRE && warp == 2) grid_dependency_wait();
+    return;
+  }
 
   // warp 0 starts loading at once: its copies complete on barriers of this CTA alone
   uint32_t tmem = 0;
@@ -523,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- producer, FP16 tokens
     // A warp of its own: with both on one warp the issuing itself (some 1100 cycles for a
     // stage's three copies) was longer than the stage's MMAs.
+    grid_dependency_wait();   // for the widening pass that wrote the tokens
     int tok = 0;
     uint32_t phase = 0, armed = 0, armed_parity = 0;
     bool ok = true;
@@ -841,11 +847,13 @@ bsmma_status launch_tn(PairParams p, const void* tok16, const DeviceInfo* dev, c
   auto kern = int8_pair_kernel<TN, PRE, F32>;
   static int max_clusters = -1;   // benign race: every thread computes the same value
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.attrs = attr;
@@ -888,6 +896,7 @@ bsmma_status launch_tn(PairParams p, const void* tok16, const DeviceInfo* dev, c
   p.limit_ns = wait_limit_ns();
   cfg.gridDim = dim3(static_cast<unsigned>(2 * max_clusters), 1, 1);
   cfg.stream = stream;
+  cfg.numAttrs = PRE ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tb, ta8, ta32, tall, p);
   count_launches(1);
   return cuda_ok(e == cudaSuccess ? cudaGetLastError() : e);
@@ -896,18 +905,27 @@ bsmma_status launch_tn(PairParams p, const void* tok16, const DeviceInfo* dev, c
 }  // namespace
 
 namespace {
-// int8 [n16 * 16] -> FP16, 16 values a thread and step.
+// int8 [n16 * 16] -> FP16: four 16-byte loads in flight a thread.
+constexpr int kWidenSteps = 4;
 __global__ void __launch_bounds__(256) widen_kernel(const uint4* __restrict__ in,
                                                     uint4* __restrict__ out, int64_t n16) {
-  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n16; i += gridDim.x * 256ll) {
-    const uint4 v = __ldcs(in + i);
+  grid_launch_dependents();
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (256 * kWidenSteps) + threadIdx.x;
+  uint4 v[kWidenSteps];
+#pragma unroll
+  for (int j = 0; j < kWidenSteps; ++j)
+    if (i0 + j * 256 < n16) v[j] = __ldcs(in + i0 + j * 256);
+#pragma unroll
+  for (int j = 0; j < kWidenSteps; ++j) {
     uint4 a, b;
-    widen4(v.x, a.x, a.y);
-    widen4(v.y, a.z, a.w);
-    widen4(v.z, b.x, b.y);
-    widen4(v.w, b.z, b.w);
-    out[2 * i] = a;
-    out[2 * i + 1] = b;
+    widen4(v[j].x, a.x, a.y);
+    widen4(v[j].y, a.z, a.w);
+    widen4(v[j].z, b.x, b.y);
+    widen4(v[j].w, b.z, b.w);
+    if (i0 + j * 256 < n16) {
+      out[2 * (i0 + j * 256)] = a;
+      out[2 * (i0 + j * 256) + 1] = b;
+    }
   }
 }
 }  // namespace
@@ -970,10 +988,11 @@ bsmma_status launch_pair(const Int8Params& a, bool f32, const DeviceInfo* dev, c
       return st;
   }
   if (c.pre) {
-    const int64_t n16 = a.total_M * a.K / 16, blocks = (n16 + 255) / 256;
-    widen_kernel<<<static_cast<unsigned>(blocks < dev->sm_count * 8 ? blocks : dev->sm_count * 8), 256, 0,
-                   stream>>>(reinterpret_cast<const uint4*>(a.A), static_cast<uint4*>(tok16), n16);
+    const int64_t n16 = a.total_M * a.K / 16, per = 256 * kWidenSteps;
+    widen_kernel<<<static_cast<unsigned>((n16 + per - 1) / per), 256, 0, stream>>>(
+        reinterpret_cast<const uint4*>(a.A), static_cast<uint4*>(tok16), n16);
     count_launches(1);
+    if (cudaGetLastError() != cudaSuccess) return BSMMA_ERR_CUDA;
   }
 #define BSMMA_INT8_TN(T, PRE) \
   (f32 ? launch_tn<T, PRE, true>(p, tok16, dev, stream) : launch_tn<T, PRE, false>(p, tok16, dev, stream))

@@ -130,6 +130,24 @@ int autotune_cached(const std::string& key);
 int autotune_pick(const std::string& key, const std::vector<int>& candidates, int fallback,
                   cudaStream_t stream, const std::function<bsmma_status(int)>& launch);
 
+// Launches `kernel`, letting it start while the kernel before it on the stream still runs: the
+// kernel calls grid_dependency_wait() before it touches what that one reads or writes.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                             cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 inline bsmma_status cuda_ok(cudaError_t e) { return e == cudaSuccess ? BSMMA_OK : BSMMA_ERR_CUDA; }
 
 }  // namespace bsmma

@@ -163,6 +163,106 @@ __global__ void __launch_bounds__(128) route_bf16_kernel(const RouteParams p) {
                denom);
 }
 
+// The same keys for many tokens: four lanes a token, eight tokens a warp, when k <= 8 and the
+// rows are whole 64-byte pieces.  A lane keeps the eight largest keys of its experts in
+// order: it sorts eight new ones (19 exchanges of a maximum and a minimum) and merges them in
+// (eight maxima, 12 exchanges); two more merges across the four lanes leave all of them with
+// the token's eight.  About 80 warp instructions a token at 128 experts against 440 for the
+// rounds above, which at 65536 tokens took 34 us, issue-bound.
+__device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b) {
+  const uint32_t hi = max(a, b);
+  b = min(a, b);
+  a = hi;
+}
+__device__ __forceinline__ void sort8(uint32_t (&v)[8]) {
+  exchange(v[0], v[1]); exchange(v[2], v[3]); exchange(v[4], v[5]); exchange(v[6], v[7]);
+  exchange(v[0], v[2]); exchange(v[1], v[3]); exchange(v[4], v[6]); exchange(v[5], v[7]);
+  exchange(v[1], v[2]); exchange(v[5], v[6]);
+  exchange(v[0], v[4]); exchange(v[1], v[5]); exchange(v[2], v[6]); exchange(v[3], v[7]);
+  exchange(v[2], v[4]); exchange(v[3], v[5]);
+  exchange(v[1], v[2]); exchange(v[3], v[4]); exchange(v[5], v[6]);
+}
+// v: first rising then falling or the other way round -> in falling order.
+__device__ __forceinline__ void merge8(uint32_t (&v)[8]) {
+#pragma unroll
+  for (int d = 4; d; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & d)) exchange(v[i], v[i + d]);
+}
+
+__global__ void __launch_bounds__(128) route_quad_kernel(const RouteParams p) {
+  const int lane = threadIdx.x & 31, q = lane & 3;
+  const int64_t t = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) >> 2;
+  const bool in = t < p.T;
+  const uint4* row =
+      reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.logits) + (in ? t : 0) * p.E);
+  uint32_t top[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top[i] = 0;
+#pragma unroll 4
+  for (int b = q; b < p.E / 8; b += 4) {
+    const uint4 w4 = row[b];
+    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+    const uint32_t low = 0xFFFF - 8 * b;
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // NaN becomes -inf, -0 becomes +0
+      const float f = fmaxf(__uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16), -INFINITY) + 0.f;
+      const uint32_t bits = __float_as_uint(f);
+      const uint32_t o = bits ^ (static_cast<uint32_t>(static_cast<int32_t>(bits) >> 31) | 0x80000000u);
+      v[i] = (o & 0xFFFF0000u) | (low - i);
+    }
+    sort8(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top[i] = max(top[i], v[7 - i]);
+    merge8(top);
+  }
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = max(top[i], __shfl_xor_sync(kFull, top[7 - i], o));
+    merge8(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top[i] = v[i];
+  }
+  constexpr uint32_t kClosed = 0x00800000u;   // keys of -inf are below
+  auto logit = [](uint32_t k) {
+    const uint32_t o = k >> 16;
+    return fminf(__uint_as_float((o & 0x8000u ? o & 0x7FFFu : ~o & 0xFFFFu) << 16), FLT_MAX);
+  };
+  // lane q finishes choices q and q + 4
+  const float mx = top[0] >= kClosed ? logit(top[0]) : 0.f;
+  uint32_t c[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = q & 1 ? top[4 * h + 1] : top[4 * h], hi = q & 1 ? top[4 * h + 3] : top[4 * h + 2];
+    c[h] = q & 2 ? hi : lo;
+    if (q + 4 * h >= p.k || c[h] < kClosed) c[h] = 0;
+  }
+  float s[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float x = logit(c[h]);
+    s[h] = c[h] ? (p.sigmoid ? sigmoid(x) : expf(x - mx)) : 0.f;
+  }
+  if (p.renormalize) {
+    float sum = s[0] + s[1];
+    sum += __shfl_xor_sync(kFull, sum, 1);
+    sum += __shfl_xor_sync(kFull, sum, 2);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) s[h] = sum > 0.f ? s[h] / sum : 0.f;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (in && q + 4 * h < p.k) {
+      p.ids[t * p.k + q + 4 * h] = c[h] ? 0xFFFF - static_cast<int>(c[h] & 0xFFFFu) : -1;
+      p.weights[t * p.k + q + 4 * h] = s[h] * p.scale;
+    }
+}
+
 // FP32 logits, a bias or groups: 32-bit keys, lane l holding experts 32 i + l.
 template <bool F32, int V>
 __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
@@ -310,16 +410,30 @@ struct RouteGradParams {
 };
 
 // EVERY: the second form, which reads the whole row; the others read the chosen logits.
-template <bool F32, bool EVERY>
+// LANES of a warp share a token: 8 where k <= 8 and there are many tokens, else 32.
+template <int LANES>
+__device__ __forceinline__ float part_sum(float v) {
+#pragma unroll
+  for (int o = LANES / 2; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ float part_max(float v) {
+#pragma unroll
+  for (int o = LANES / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+template <bool F32, bool EVERY, int LANES>
 __global__ void __launch_bounds__(128) route_grad_kernel(const RouteGradParams p) {
   extern __shared__ __align__(16) uint8_t smem_b[];
   using Elem = typename std::conditional<F32, float, __nv_bfloat16>::type;
-  const int lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (t >= p.T) return;
+  const int lane = threadIdx.x % LANES;
+  const int64_t t_of = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / LANES;
+  const bool in = t_of < p.T;   // (a warp's other tokens may still be)
+  const int64_t t = in ? t_of : p.T - 1;
   constexpr int kPer = 16 / sizeof(Elem);
   const int pieces = (p.E + kPer - 1) / kPer;   // of the row, 16 bytes each
-  Elem* row = reinterpret_cast<Elem*>(smem_b + (threadIdx.x >> 5) * pieces * 16);
+  Elem* row = reinterpret_cast<Elem*>(smem_b + (threadIdx.x / LANES) * pieces * 16);
   int id = lane < p.k ? p.ids[t * p.k + lane] : -1;
   if (id >= p.E) id = -1;
   float d = 0.f, x = -INFINITY;
@@ -327,48 +441,73 @@ __global__ void __launch_bounds__(128) route_grad_kernel(const RouteGradParams p
     d = p.scale * p.dweights[t * p.k + lane];
     x = clean_logit(load_elem<F32>(p.logits, t * p.E + id));
   }
-  for (int v = lane; v < pieces; v += 32) reinterpret_cast<uint4*>(row)[v] = make_uint4(0, 0, 0, 0);
+  if constexpr (!EVERY)
+    for (int v = lane; v < pieces; v += LANES) reinterpret_cast<uint4*>(row)[v] = make_uint4(0, 0, 0, 0);
   float out = 0.f;
-  __syncwarp();
   if constexpr (EVERY) {
     float mx = -INFINITY, sum = 0.f;
-    for (int e = lane; e < p.E; e += 32) mx = fmaxf(mx, clean_logit(load_elem<F32>(p.logits, t * p.E + e)));
-    mx = warp_max(mx);
+    for (int e = lane; e < p.E; e += LANES)
+      mx = fmaxf(mx, clean_logit(load_elem<F32>(p.logits, t * p.E + e)));
+    mx = part_max<LANES>(mx);
     if (mx == -INFINITY) mx = 0.f;
-    for (int e = lane; e < p.E; e += 32) sum += expf(clean_logit(load_elem<F32>(p.logits, t * p.E + e)) - mx);
-    sum = warp_sum(sum);
+    for (int e = lane; e < p.E; e += LANES)
+      sum += expf(clean_logit(load_elem<F32>(p.logits, t * p.E + e)) - mx);
+    sum = part_sum<LANES>(sum);
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     const float q = x == -INFINITY ? 0.f : expf(x - mx) * inv;
-    const float dot = warp_sum(q * d);
+    const float dot = part_sum<LANES>(q * d);
     out = q * (d - dot);
-    for (int e = lane; e < p.E; e += 32)
+    for (int e = lane; e < p.E; e += LANES)
       store_elem<F32>(row, e, -expf(clean_logit(load_elem<F32>(p.logits, t * p.E + e)) - mx) * inv * dot);
-    __syncwarp();
   } else if (!p.sigmoid) {
-    float mx = warp_max(x);
+    float mx = part_max<LANES>(x);
     if (mx == -INFINITY) mx = 0.f;
     float e = expf(x - mx);
-    const float sum = warp_sum(e);
+    const float sum = part_sum<LANES>(e);
     e = sum > 0.f ? e / sum : 0.f;
-    out = e * (d - warp_sum(e * d));
+    out = e * (d - part_sum<LANES>(e * d));
   } else {
     const float q = x == -INFINITY ? 0.f : sigmoid(x);
     float g = d;
     if (p.renormalize) {
-      const float sum = warp_sum(q);
-      g = sum > 0.f ? (d - warp_sum(q / sum * d)) / sum : 0.f;
+      // (the sums outside the condition: a warp's tokens may differ in it)
+      const float sum = part_sum<LANES>(q), inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float dot = part_sum<LANES>(q * inv * d);
+      g = (d - dot) * inv;
     }
     // 1 - q as 1 / (1 + e^x): no cancellation for large logits
     out = x == -INFINITY ? 0.f : q * sigmoid(-x) * g;
   }
+  __syncwarp();
   if (id >= 0) store_elem<F32>(row, id, out);
   __syncwarp();
+  if (!in) return;
   Elem* to = static_cast<Elem*>(p.dlogits) + t * p.E;
   if (p.E % kPer == 0) {
-    for (int v = lane; v < pieces; v += 32)
+    for (int v = lane; v < pieces; v += LANES)
       reinterpret_cast<uint4*>(to)[v] = reinterpret_cast<const uint4*>(row)[v];
   } else {
-    for (int e = lane; e < p.E; e += 32) to[e] = row[e];
+    for (int e = lane; e < p.E; e += LANES) to[e] = row[e];
+  }
+}
+
+template <bool F32>
+void launch_route_grad(const RouteGradParams& p, cudaStream_t stream) {
+  const int per = F32 ? 4 : 8, row_bytes = (p.E + per - 1) / per * 16;
+  const bool every = !p.sigmoid && !p.renormalize;
+  const int warps = p.T >= 1024 ? 4 : 1;
+  if (p.k <= 8 && p.T >= 1024 && 16 * row_bytes <= 48 * 1024) {
+    const unsigned grid = static_cast<unsigned>((p.T + 15) / 16);
+    if (every)
+      route_grad_kernel<F32, true, 8><<<grid, 128, 16 * row_bytes, stream>>>(p);
+    else
+      route_grad_kernel<F32, false, 8><<<grid, 128, 16 * row_bytes, stream>>>(p);
+  } else {
+    const unsigned grid = static_cast<unsigned>((p.T + warps - 1) / warps);
+    if (every)
+      route_grad_kernel<F32, true, 32><<<grid, warps * 32, warps * row_bytes, stream>>>(p);
+    else
+      route_grad_kernel<F32, false, 32><<<grid, warps * 32, warps * row_bytes, stream>>>(p);
   }
 }
 
@@ -509,6 +648,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_one_kernel(const PlanParams
 
 __global__ void __launch_bounds__(kPlanThreads) plan_rank_kernel(const PlanParams p) {
   extern __shared__ int32_t smem_i[];
+  grid_launch_dependents();
   rank_slots(
       p, static_cast<int64_t>(blockIdx.x) * kPlanSlots, smem_i,
       [&](int e, int32_t n) { p.block_hist[static_cast<int64_t>(e) * p.blocks + blockIdx.x] = n; },
@@ -519,6 +659,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_rank_kernel(const PlanParam
 __global__ void __launch_bounds__(128) plan_scan_kernel(const PlanParams p) {
   const int lane = threadIdx.x & 31;
   const int e = blockIdx.x * 4 + (threadIdx.x >> 5);
+  grid_launch_dependents();
+  grid_dependency_wait();
   if (e >= p.E) return;
   int32_t* h = p.block_hist + static_cast<int64_t>(e) * p.blocks;
   int32_t base = 0;
@@ -540,27 +682,54 @@ __global__ void __launch_bounds__(128) plan_scan_kernel(const PlanParams p) {
   }
 }
 
+// A block's slots are put in expert order in shared memory first, so that what it writes to
+// src is a run per expert and not a word here and there (1 M slots, 128 experts: 21 us with
+// the words scattered and the loads in turn, 8 us so).
 __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanParams p) {
-  __shared__ int32_t start[1024];
+  constexpr int kPer = kPlanSlots / kPlanThreads;
+  __shared__ int32_t start[1024];     // first row of the expert in the block's run
+  __shared__ int32_t local[1024];     // its place among the block's slots
+  __shared__ int32_t order[kPlanSlots], row[kPlanSlots];
   __shared__ int32_t warp_sums[kPlanWarps];
+  const int64_t s0 = static_cast<int64_t>(blockIdx.x) * kPlanSlots;
+  int32_t id[kPer], rank[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int64_t s = s0 + i * kPlanThreads + threadIdx.x;
+    const int32_t e = s < p.S ? p.ids[s] : -1;
+    id[i] = e < 0 || e >= p.E ? -1 : e;
+  }
+  grid_dependency_wait();
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int64_t s = s0 + i * kPlanThreads + threadIdx.x;
+    rank[i] = s < p.S ? p.pos[s] : -1;
+  }
+  const int b = blockIdx.x;
   for (int e = threadIdx.x; e < p.E; e += kPlanThreads) start[e] = p.totals[e];
   __syncthreads();
   const int32_t total = block_prefix(start, p.E, warp_sums);
-  for (int e = threadIdx.x; e < p.E; e += kPlanThreads)
-    start[e] += p.block_hist[static_cast<int64_t>(e) * p.blocks + blockIdx.x];
-  __syncthreads();
-  const int64_t s0 = static_cast<int64_t>(blockIdx.x) * kPlanSlots;
-  for (int i = threadIdx.x; i < kPlanSlots; i += kPlanThreads) {
-    const int64_t s = s0 + i;
-    if (s >= p.S) break;
-    const int id = p.ids[s];
-    if (id >= 0 && id < p.E) {
-      const int32_t at = start[id] + p.pos[s];
-      p.pos[s] = at;
-      p.src[at] = static_cast<int32_t>(s);
-    }
-    if (s >= total) p.src[s] = -1;
+  for (int e = threadIdx.x; e < p.E; e += kPlanThreads) {
+    const int32_t* h = p.block_hist + static_cast<int64_t>(e) * p.blocks;
+    const int32_t before = h[b];
+    start[e] += before;
+    local[e] = (b + 1 < p.blocks ? h[b + 1] : p.totals[e]) - before;
   }
+  __syncthreads();
+  const int32_t used = block_prefix(local, p.E, warp_sums);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int64_t s = s0 + i * kPlanThreads + threadIdx.x;
+    if (id[i] >= 0) {
+      const int32_t at = start[id[i]] + rank[i], l = local[id[i]] + rank[i];
+      p.pos[s] = at;
+      order[l] = static_cast<int32_t>(s);
+      row[l] = at;
+    }
+    if (s < p.S && s >= total) p.src[s] = -1;
+  }
+  __syncthreads();
+  for (int l = threadIdx.x; l < used; l += kPlanThreads) p.src[row[l]] = order[l];
 }
 
 // ------------------------------------------------------------------------ weighted sum
@@ -635,9 +804,10 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
 }
 
 // One block per token: dY of its rows is w * dout, dw the dot product of dout and the row.
-// The token's dout pieces are read once per kSlots slots.
+// The token's dout pieces are read once per kSlots slots.  Four blocks an SM: at the 120
+// registers that ptxas takes by itself two fit, and 8192 x 8 rows of 4096 took 197 us, not 165.
 template <bool F32>
-__global__ void __launch_bounds__(256) combine_grad_kernel(const CombineParams p) {
+__global__ void __launch_bounds__(256, 4) combine_grad_kernel(const CombineParams p) {
   constexpr int kN = Vec<F32>::kN, kSlots = 8;
   __shared__ float part[8][kSlots];
   const int64_t t = blockIdx.x;
@@ -707,7 +877,10 @@ template <bool F32, int V>
 bsmma_status launch_route_v(const RouteParams& p, cudaStream_t stream) {
   const int warps = route_warps(p.T);
   const unsigned grid = static_cast<unsigned>((p.T + warps - 1) / warps);
-  if (!F32 && !p.bias && p.groups == 1) {
+  if (!F32 && !p.bias && p.groups == 1 && p.k <= 8 && p.E % 32 == 0 && p.T >= 1024 &&
+      (p.sigmoid || p.renormalize)) {
+    route_quad_kernel<<<static_cast<unsigned>((p.T + 31) / 32), 128, 0, stream>>>(p);
+  } else if (!F32 && !p.bias && p.groups == 1) {
     if constexpr (V >= 2) {
       if (p.E % 2 == 0)
         route_bf16_kernel<V, true><<<grid, warps * 32, 0, stream>>>(p);
@@ -777,21 +950,10 @@ bsmma_status launch_route_backward(const void* logits, bool f32, int64_t T, int 
   p.renormalize = renormalize;
   p.scale = scale;
   p.dlogits = dlogits;
-  const int warps = route_warps(T);
-  const unsigned grid = static_cast<unsigned>((T + warps - 1) / warps);
-  const int per = f32 ? 4 : 8, smem = warps * ((E + per - 1) / per) * 16;
-  const bool every = !sigmoid && !renormalize;
-  if (f32) {
-    if (every)
-      route_grad_kernel<true, true><<<grid, warps * 32, smem, stream>>>(p);
-    else
-      route_grad_kernel<true, false><<<grid, warps * 32, smem, stream>>>(p);
-  } else {
-    if (every)
-      route_grad_kernel<false, true><<<grid, warps * 32, smem, stream>>>(p);
-    else
-      route_grad_kernel<false, false><<<grid, warps * 32, smem, stream>>>(p);
-  }
+  if (f32)
+    launch_route_grad<true>(p, stream);
+  else
+    launch_route_grad<false>(p, stream);
   count_launches(1);
   return cuda_ok(cudaGetLastError());
 }
@@ -821,10 +983,11 @@ bsmma_status launch_plan(const int32_t* ids, int64_t S, int E, int64_t* m_sizes,
     return cuda_ok(cudaGetLastError());
   }
   plan_rank_kernel<<<p.blocks, kPlanThreads, kPlanWarps * E * 4, stream>>>(p);
-  plan_scan_kernel<<<(E + 3) / 4, 128, 0, stream>>>(p);
-  plan_place_kernel<<<p.blocks, kPlanThreads, 0, stream>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = launch_dependent(plan_scan_kernel, (E + 3) / 4, 128, 0, stream, p);
+  if (e == cudaSuccess) e = launch_dependent(plan_place_kernel, p.blocks, kPlanThreads, 0, stream, p);
   count_launches(3);
-  return cuda_ok(cudaGetLastError());
+  return cuda_ok(e);
 }
 
 bsmma_status launch_combine(const void* y, bool f32, int64_t R, int64_t H, const int32_t* pos,

@@ -345,6 +345,18 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// ---------------------------------------------------------------- dependent launches
+// Waits until the kernels this launch programmatically depends on have finished and their
+// writes are visible (nothing to wait for in an ordinary launch).
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// Lets a dependent launch start its blocks (its grid_dependency_wait still waits for the end
+// of this grid).
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- per-thread async copies
 // 4-byte global -> shared copy (LDGSTS); src_bytes 0 writes zero and reads nothing.
 __device__ __forceinline__ void cp_async_4(void* dst_smem, const void* src, uint32_t src_bytes) {

@@ -125,7 +125,32 @@ def test_route_masks_and_specials(score, bias):
 
 @pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
-@pytest.mark.parametrize("T,E,k,dtype", [(1, 1, 1, "f32"), (6, 33, 4, "f32"), (1030, 64, 8, "bf16"),
+@pytest.mark.parametrize("E,k", [(32, 8), (128, 1), (160, 5), (1024, 8), (64, 12), (65, 8), (2, 2), (1023, 3)])
+def test_route_bf16_many_tokens(E, k, score, renorm):
+    """BF16 logits over enough tokens for every kernel: few distinct values (ties in almost
+    every token), zeros of both signs, NaN, infinities, the lowest value, closed experts."""
+    T = 1037
+    g = np.random.default_rng([78, E, k])
+    x = np.round(g.standard_normal((T, E)) * 4) / 2
+    pick = g.random((T, E))
+    for i, v in enumerate((np.nan, -np.inf, np.inf, -0.0, float(torch.finfo(torch.bfloat16).min))):
+        x[(pick >= i * 0.02) & (pick < i * 0.02 + 0.02)] = v
+    x[5] = -np.inf
+    x[6] = np.nan
+    x[7] = -0.0
+    x[8, 1:] = -np.inf
+    xt = torch.from_numpy(x).bfloat16()
+    ids, w = bs.moe_route(xt.cuda(), k, score=score, renormalize=renorm, scale=0.5)
+    torch.cuda.synchronize()
+    x64 = xt.double().numpy()
+    ids_ref, w_ref = ref.route(x64, k, score, renormalize=renorm, scale=0.5)
+    assert np.array_equal(ids.cpu().numpy(), ids_ref)
+    assert np.all(np.abs(w.cpu().numpy() - w_ref) <= W_TOL * np.abs(w_ref) + 1e-37)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,dtype", [(1, 1, 1, "f32"), (1101, 33, 3, "f32"), (1029, 1024, 7, "bf16"), (6, 33, 4, "f32"), (1030, 64, 8, "bf16"),
                                          (3, 1024, 32, "f32"), (5, 20, 20, "bf16")])
 def test_route_backward(T, E, k, dtype, score, renorm):
     g = np.random.default_rng([72, T, E, k])
