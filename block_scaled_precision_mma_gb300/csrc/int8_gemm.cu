@@ -64,6 +64,20 @@ __device__ __forceinline__ uint32_t code_slow(float x, float s) {
   return static_cast<uint32_t>(static_cast<int>(q)) & 0xFFu;
 }
 
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // N (4 or 8) codes of x / s in bytes.  inv = 1 / s, or 0 where that is no FP32 number.
 template <int N>
 __device__ __forceinline__ void codes_of(const float (&x)[N], float s, float inv,
@@ -71,12 +85,20 @@ __device__ __forceinline__ void codes_of(const float (&x)[N], float s, float inv
   constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: adding it rounds to an integer
   uint32_t b[N];
   bool near_half = inv == 0.f;
+  const uint64_t inv2 = pack2(inv, inv), magic2 = pack2(kMagic, kMagic), minus2 = pack2(-1.f, -1.f);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float y = fmaf(x[i], inv, kMagic);
-    const float f = fmaf(x[i], inv, -(y - kMagic));
-    near_half |= fabsf(f) > 0.5f - 0x1p-15f;
-    b[i] = __float_as_uint(y);
+  for (int i = 0; i < N; i += 2) {   // two values an instruction
+    const uint64_t x2 = pack2(x[i], x[i + 1]);
+    const uint64_t y = fma2(x2, inv2, magic2);
+    const uint64_t f2 = fma2(x2, inv2, fma2(y, minus2, magic2));   // x * inv - the integer
+    float f0, f1;
+    unpack2(f2, f0, f1);
+    near_half |= fabsf(f0) > 0.5f - 0x1p-15f;
+    near_half |= fabsf(f1) > 0.5f - 0x1p-15f;
+    float y0, y1;
+    unpack2(y, y0, y1);
+    b[i] = __float_as_uint(y0);
+    b[i + 1] = __float_as_uint(y1);
   }
   if (near_half) {
 #pragma unroll

@@ -12,10 +12,10 @@
 //   warp 0       TMA producer: 128 K of the CTA's 128 channels and of its half of the tokens
 //                (one box for a full half, else boxes of 32 and 8 rows) into a ring;
 //   warp 1       in the leader, issues the M = 256 FP16 MMAs, eight per stage;
-//   warps 4-11   two widening warpgroups, one for each 64-K half of a stage: a thread widens
-//                one channel's 64 values into its tensor-memory lane and its share of the
-//                tokens into the 128-byte-swizzled shared-memory tile (with PRE the tokens
-//                come as FP16, by warp 2);
+//   warps 4-11   two widening warpgroups, stages in turn: a thread widens one channel's 128
+//                values into its tensor-memory lane and its share of the tokens into the
+//                128-byte-swizzled shared-memory tile (with PRE the tokens come as FP16, by
+//                warp 2);
 //   warps 12-15  output: accumulator columns out of tensor memory, times the scales, plus
 //                the bias, rounded and stored, 32 channels of a token per warp store.
 // Units (a token block of one group x 256 channels) are dealt round robin; the last wave's
@@ -63,7 +63,8 @@ struct Cfg {
   // accumulators, and slots of widened channels in the rest of tensor memory
   static constexpr int kBufs = 2 * TN + 2 * kSlotCols <= 512 ? 2 : 1;
   static constexpr int kFree = (512 - kBufs * TN) / kSlotCols;
-  static constexpr int kSlots = PRE ? (kFree < 4 ? kFree : 4) : TN > 128 ? 2 : 3;
+  static constexpr int kSlots = PRE ? (kFree < 4 ? kFree : 4) : 2;   // (three: 144 us, two: 138 us at
+                                                                      // 64 x 2048 x 7168, 256 rows)
   static constexpr int kTokSlots = PRE ? (TN > 192 ? (F32 ? 3 : 4) : 5) : kSlots;
   // output tile: 32 tokens x 128 channels, rows padded so that two rows' halves of the banks
   // do not meet
@@ -87,22 +88,45 @@ struct PairParams {
   uint64_t limit_ns;
 };
 
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+// The library's bounded wait (mbar_wait) with a suspend hint: a waiting warp stays off the
+// shared-memory pipe until the phase completes or 20 us have passed.  Without it a dozen
+// polling warps a CTA slow the widening warps' loads (64 experts x 2048 x 7168, 256 rows:
+// 152 us without, 144 us with).  CLUSTER: the peer CTA arrives on the barrier as well.
+template <bool CLUSTER>
+__device__ __forceinline__ bool try_wait_hint(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
+  if constexpr (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000)
+        : "memory");
   return ok != 0;
 }
-// mbar_wait for a barrier that the peer CTA's threads arrive on as well.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
-                                                  volatile int* abort, int* status) {
-  if (try_wait_cluster(bar, parity)) return true;
-  return mbar_wait(bar, parity, limit_ns, abort, status) && try_wait_cluster(bar, parity);
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                           volatile int* abort, int* status) {
+  if (try_wait_hint<CLUSTER>(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!try_wait_hint<CLUSTER>(bar, parity)) {
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > limit_ns) {
+      report_status(status, kDevTimeout);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
 }
 
 // Arrives on the leader's barrier, releasing at CTA scope: what it announces (values in this
@@ -420,10 +444,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 8);       // the CTA's widening warps
+      mbar_init(&empty[s], 4);       // a widening warpgroup
     }
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&wide_full[s], 16);  // the widening warps of both CTAs
+      mbar_init(&wide_full[s], 8);   // a widening warpgroup of each CTA
       mbar_init(&wide_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -488,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = un.row0 + rank * half;
       const int chan = static_cast<int>(un.g * p.a.N) + un.n0 + rank * 128;
       for (int k = k0; k < k1; ++k) {
-        if (!mbar_wait(&empty[stage], phase ^ 1, p.limit_ns, abort_flag, p.a.status)) {
+        if (!wait_phase(&empty[stage], phase ^ 1, p.limit_ns, abort_flag, p.a.status)) {
           ok = false;
           break;
         }
@@ -501,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (!PRE) {
             dst += 128 * 128;
             int r = 0;
-            if (half == C::kHalf) {
+            if (half == p.tn / 2) {
               tma_load_2d(&tmAll, &full[stage], dst, k * 128, row);
               r = half;
             }
@@ -520,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kStages; ++s)
       if (armed & (1u << s)) {
         volatile int no_abort = 0;
-        mbar_wait(&full[s], (armed_parity >> s) & 1u, p.limit_ns / 4 + 1, &no_abort, nullptr);
+        wait_phase(&full[s], (armed_parity >> s) & 1u, p.limit_ns / 4 + 1, &no_abort, nullptr);
       }
     __syncwarp();
     cluster_wait();
@@ -537,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int half = unit_cols(un) / 2;
       const int row = un.row0 + rank * half;
       for (int k = k0; k < k1; ++k) {
-        if (!mbar_wait(&tok_empty[tok], phase ^ 1, p.limit_ns, abort_flag, p.a.status)) {
+        if (!wait_phase(&tok_empty[tok], phase ^ 1, p.limit_ns, abort_flag, p.a.status)) {
           ok = false;
           break;
         }
@@ -553,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* dst = wide + tok * C::kWideBytes + h * (C::kWideBytes / 2);
             const int x = (2 * k + h) * 128;
             int r = 0;
-            if (half == C::kHalf) {
+            if (half == p.tn / 2) {
               tma_load_2d_pair(&tmAll, bar, dst, x, row);
               r = half;
             }
@@ -571,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < C::kTokSlots; ++s)
       if (armed & (1u << s)) {
         volatile int no_abort = 0;
-        mbar_wait(&tok_full[s], (armed_parity >> s) & 1u, p.limit_ns / 4 + 1, &no_abort, nullptr);
+        wait_phase(&tok_full[s], (armed_parity >> s) & 1u, p.limit_ns / 4 + 1, &no_abort, nullptr);
       }
   } else if (warp == 1) {
     if (rank == 0) {
@@ -584,18 +608,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(unit_cols(un) >> 3) << 17) |
                                ((256u >> 4) << 24);   // FP32 accumulator, FP16 operands, M = 256
         const uint32_t buf = tcount % C::kBufs;
-        if (!mbar_wait_cluster(&acc_empty[buf], ((tcount / C::kBufs) & 1) ^ 1, p.limit_ns, abort_flag,
+        if (!wait_phase<true>(&acc_empty[buf], ((tcount / C::kBufs) & 1) ^ 1, p.limit_ns, abort_flag,
                                p.a.status))
           break;
         ++tcount;
         const uint32_t d = tmem + buf * TN;
         for (int k = k0; k < k1; ++k) {
-          if (!mbar_wait_cluster(&wide_full[slot], slot_phase, p.limit_ns, abort_flag, p.a.status)) {
+          if (!wait_phase<true>(&wide_full[slot], slot_phase, p.limit_ns, abort_flag, p.a.status)) {
             ok = false;
             break;
           }
           if constexpr (PRE) {
-            if (!mbar_wait_cluster(&tok_full[tok], tok_phase, p.limit_ns, abort_flag, p.a.status)) {
+            if (!wait_phase<true>(&tok_full[tok], tok_phase, p.limit_ns, abort_flag, p.a.status)) {
               ok = false;
               break;
             }
@@ -633,17 +657,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (elect_one()) tc_commit_pair(drain, 1);
       volatile int no_abort = 0;
-      mbar_wait(drain, 0, p.limit_ns, &no_abort, nullptr);
+      wait_phase(drain, 0, p.limit_ns, &no_abort, nullptr);
     }
   } else if (warp >= kWideWarp0 && warp < kOutWarp0) {
     // ---------------------------------------------------------------- widening (both CTAs)
+    // The warpgroups take stages in turn: a stage is a chain of waits and latencies, and a
+    // whole stage a warpgroup has half as many of them as half of every stage.
     const int wg = (warp - kWideWarp0) >> 2, tid = threadIdx.x & 127;
-    const uint32_t taddr = tmem_wide + (static_cast<uint32_t>((warp & 3) * 32) << 16) + wg * 32;
-    // 16-byte piece j of the thread's channel is at chan ^ (j << 4) of the stage (the
-    // 128-byte swizzle exchanges pieces by the row's number modulo 8)
-    const uint32_t chan = static_cast<uint32_t>(tid) * 128 + (((4 * wg) ^ (tid & 7)) << 4);
-    constexpr int kPieces = PRE ? 0 : (C::kHalf + 31) / 32;   // of the tokens, a thread
-    int stage = 0;
+    const uint32_t taddr = tmem_wide + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    // 16-byte piece j of a 64-K half of the thread's channel is at chan ^ (j << 4) of the
+    // stage, ^ 64 for the second half (the 128-byte swizzle exchanges pieces by the row's
+    // number modulo 8)
+    const uint32_t chan = static_cast<uint32_t>(tid) * 128 + ((tid & 7) << 4);
+    constexpr int kPieces = PRE ? 0 : (C::kHalf + 31) / 32;   // of a half's tokens, a thread
+    int stage = 0, turn = 0;
     uint32_t phase = 0, slot = 0, slot_phase = 0;
     bool ok = true;
     while (ok && walk.next(sched, workers, u, k0, k1)) {
@@ -656,63 +683,90 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int e = i * 128 + tid, piece = e / half, r = e - piece * half;
-        from[i] = piece < 4 ? 128 * 128 + r * 128 + (((4 * wg + piece) ^ (r & 7)) << 4) : kNone;
+        from[i] = piece < 4 ? 128 * 128 + r * 128 + ((piece ^ (r & 7)) << 4) : kNone;
         to[i] = r * 128 + (((2 * piece) ^ (r & 7)) << 4);
       }
-      for (int k = k0; k < k1; ++k) {
-        if (!mbar_wait(&full[stage], phase, p.limit_ns, abort_flag, p.a.status)) {
-          ok = false;
-          break;
-        }
-        const uint32_t base = smem_u32(raw + stage * C::kRawBytes);
-        const bool work = 2 * k + wg < p.halves_k;
-        uint4 c[4], x[kPieces + 1];
-        if (work) {
+      for (int k = k0; k < k1; ++k, turn ^= 1) {
+        if (turn == wg) {
+          if (!wait_phase(&full[stage], phase, p.limit_ns, abort_flag, p.a.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t base = smem_u32(raw + stage * C::kRawBytes);
+          const uint32_t out = smem_u32(wide + slot * C::kWideBytes);
+          const int halves = 2 * k + 1 < p.halves_k ? 2 : 1;
+          auto widen16 = [](const uint4 (&c)[4], uint32_t (&w)[32]) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            c[j] = lds128(base + (chan ^ (j << 4)));
+            for (int j = 0; j < 4; ++j) {
+              widen4(c[j].x, w[8 * j], w[8 * j + 1]);
+              widen4(c[j].y, w[8 * j + 2], w[8 * j + 3]);
+              widen4(c[j].z, w[8 * j + 4], w[8 * j + 5]);
+              widen4(c[j].w, w[8 * j + 6], w[8 * j + 7]);
+            }
+          };
+          auto slot_free = [&] {
+            ok = wait_phase(&wide_empty[slot], slot_phase ^ 1, p.limit_ns, abort_flag, p.a.status);
+            tc_fence_after();
+            return ok;
+          };
+          if constexpr (PRE) {
+            // both halves are ready before the slot is: only the stores follow its release
+            uint4 c[4], d[4];
+            uint32_t w[32], y[32];
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i)
-            if (from[i] != kNone) x[i] = lds128(base + from[i]);
+            for (int j = 0; j < 4; ++j) c[j] = lds128(base + (chan ^ (j << 4)));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[j] = lds128(base + (chan ^ 64 ^ (j << 4)));
+            widen16(c, w);
+            widen16(d, y);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[stage]);
+            if (!slot_free()) break;
+            tmem_st32(taddr + slot * kSlotCols, w);
+            if (halves == 2) tmem_st32(taddr + slot * kSlotCols + 32, y);
+          } else {
+#pragma unroll 1
+            for (int h = 0; h < halves; ++h) {
+              uint4 c[4], x[kPieces + 1];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) c[j] = lds128(base + (chan ^ (h << 6) ^ (j << 4)));
+#pragma unroll
+              for (int i = 0; i < kPieces; ++i)
+                if (from[i] != kNone) x[i] = lds128(base + (from[i] ^ (h << 6)));
+              if (h == halves - 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[stage]);
+              }
+              uint32_t w[32];
+              widen16(c, w);
+              if (h == 0 && !slot_free()) break;
+              tmem_st32(taddr + slot * kSlotCols + h * 32, w);
+#pragma unroll
+              for (int i = 0; i < kPieces; ++i) {
+                if (from[i] != kNone) {
+                  uint32_t v[8];
+                  widen4(x[i].x, v[0], v[1]);
+                  widen4(x[i].y, v[2], v[3]);
+                  widen4(x[i].z, v[4], v[5]);
+                  widen4(x[i].w, v[6], v[7]);
+                  const uint32_t dst = out + h * (C::kWideBytes / 2);
+                  sts128(dst + to[i], v[0], v[1], v[2], v[3]);
+                  sts128(dst + (to[i] ^ 16), v[4], v[5], v[6], v[7]);
+                }
+              }
+            }
+          }
+          if (!ok) break;
+          tmem_st_wait();
+          fence_async_proxy();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_leader(map_to_cta(smem_u32(&wide_full[slot]), 0));
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[stage]);
         if (++stage == kStages) {
           stage = 0;
           phase ^= 1;
         }
-        uint32_t w[32];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          widen4(c[j].x, w[8 * j], w[8 * j + 1]);
-          widen4(c[j].y, w[8 * j + 2], w[8 * j + 3]);
-          widen4(c[j].z, w[8 * j + 4], w[8 * j + 5]);
-          widen4(c[j].w, w[8 * j + 6], w[8 * j + 7]);
-        }
-        if (!mbar_wait(&wide_empty[slot], slot_phase ^ 1, p.limit_ns, abort_flag, p.a.status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (work) tmem_st32(taddr + slot * kSlotCols, w);
-        const uint32_t out = smem_u32(wide + slot * C::kWideBytes + wg * (C::kWideBytes / 2));
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          if (work && from[i] != kNone) {
-            uint32_t v[8];
-            widen4(x[i].x, v[0], v[1]);
-            widen4(x[i].y, v[2], v[3]);
-            widen4(x[i].z, v[4], v[5]);
-            widen4(x[i].w, v[6], v[7]);
-            sts128(out + to[i], v[0], v[1], v[2], v[3]);
-            sts128(out + (to[i] ^ 16), v[4], v[5], v[6], v[7]);
-          }
-        }
-        tmem_st_wait();
-        fence_async_proxy();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_leader(map_to_cta(smem_u32(&wide_full[slot]), 0));
         if (++slot == kSlots) {
           slot = 0;
           slot_phase ^= 1;
@@ -739,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < TN / 32; ++i)
         sa[i] = 32 * i + lane < un.rows ? p.a.sA[un.row0 + 32 * i + lane] : 0.f;
       const uint32_t buf = tcount % C::kBufs;
-      const bool got = mbar_wait(&acc_full[buf], (tcount / C::kBufs) & 1, p.limit_ns, abort_flag, p.a.status);
+      const bool got = wait_phase(&acc_full[buf], (tcount / C::kBufs) & 1, p.limit_ns, abort_flag, p.a.status);
       if (!out_agree(got)) break;
       ++tcount;
       tc_fence_after();
@@ -878,7 +932,13 @@ bsmma_status launch_tn(PairParams p, const void* tok16, const DeviceInfo* dev, c
   if (st != BSMMA_OK) return st;
   st = encode_tmap_u8(&ta32, A, row_bytes, rows, row_bytes, 128, 32);
   if (st != BSMMA_OK) return st;
-  st = encode_tmap_u8(&tall, A, row_bytes, rows, row_bytes, 128, C::kHalf);
+  // blocks of tn tokens: a single group's are made equally large
+  p.tn = TN;
+  if (a.G == 1 && a.total_M > 0) {
+    const int64_t blocks = (a.total_M + TN - 1) / TN;
+    p.tn = static_cast<int>(((a.total_M + blocks - 1) / blocks + 15) / 16 * 16);
+  }
+  st = encode_tmap_u8(&tall, A, row_bytes, rows, row_bytes, 128, p.tn / 2);
   if (st != BSMMA_OK) return st;
   p.part = nullptr;
   p.arrivals = nullptr;
@@ -889,7 +949,6 @@ bsmma_status launch_tn(PairParams p, const void* tok16, const DeviceInfo* dev, c
   } else if (st != BSMMA_OK) {
     return st;
   }
-  p.tn = TN;
   p.num_n_tiles = static_cast<int>((a.N + 255) / 256);
   p.stages_k = static_cast<int>((a.K + 127) / 128);
   p.halves_k = static_cast<int>((a.K + 63) / 64);
@@ -930,16 +989,22 @@ __global__ void __launch_bounds__(256) widen_kernel(const uint4* __restrict__ in
 }
 }  // namespace
 
-// Which tile a launch takes: the cheapest by an estimate in SM cycles that the host can make
-// from the sizes alone (rows a group as if evenly spread).
-//   - A 128-K stage costs its eight MMAs, 37 / 45 / 73 / 105 / 137 cycles each at 16 / 64 / 128 /
-//     192 / 256 columns (measured, one instruction stream), or the 16 KB of channels it
-//     streams, 760 cycles when every SM streams.
+// Which tile a launch takes: the cheapest by an estimate in SM cycles that the host makes from
+// the sizes alone.
+//   - A 128-K stage takes about 740 + 2.6 cycles a column with the tokens widened in the
+//     kernel (a fit to 32 to 256 columns, dense and grouped).  With FP16 tokens it takes its
+//     eight MMAs, 9 + 0.5 cycles a column each and 14% more, or the channels' arrival: the
+//     ring is five stages then, and without other blocks that bring the same channels to L2 a
+//     stage waits some 1200 cycles for DRAM.
+//   - Units are what the groups' blocks make: of one group exactly, of several on average
+//     over groups 0.6 to 1.4 times as large as their mean.
 //   - A wave of units that leaves pairs idle is split over them when that is shorter; a
 //     split costs about 14 stages (parts written, counted, read back).  Measured at 14336 x
-//     4096, 128 rows: 27 us unsplit, 35 us split at 56 units on 76 pairs.
-//   - Tokens that come as FP16 cost a pass over them first.  At 4096 x 14336 x 4096: 272 us
-//     with it (TN 192), 312 us without (TN 256); the latter wins for short or narrow products.
+//     4096, 128 rows: 27 us unsplit, 35 us split, 56 units on 76 pairs.
+//   - Each block reads its channels from DRAM, at 3.1 KB a cycle; FP16 tokens cost a pass over
+//     them first and twice the bytes.
+// At 4096 x 14336 x 4096: 268 us with FP16 tokens (192 columns), 312 us without (256); 64
+// experts of 2048 x 7168 with 192 rows each: 369 and 289 us.
 struct Choice {
   int tn;
   bool pre;
@@ -947,22 +1012,26 @@ struct Choice {
 double estimate(const Int8Params& a, int tn, bool pre, int pairs) {
   const double active = a.total_M < a.G ? static_cast<double>(a.total_M) : a.G;
   const double rows = active > 0 ? a.total_M / active : 0;
-  // uneven groups end in a part-filled block each
-  const double blocks_g = a.G == 1 ? std::ceil(rows / tn) : rows <= tn / 2.0 ? 1 : rows / tn + 0.5;
-  double cols = rows / blocks_g;
-  if (a.G > 1 && cols < tn) cols = std::fmin(tn, cols * 1.25);
-  const double mma = cols <= 64 ? 36 + cols * 0.14 : cols * 0.5 + 9;
-  // without PRE, a stage's tokens are widened too, and shared memory carries them thrice
-  const double stage = std::fmax(760, 8 * mma * (pre ? 1.05 : tn > 128 ? 1.2 : 1.1));
+  double blocks = std::ceil(rows / tn);
+  if (a.G > 1) {
+    blocks = 0;
+    for (const double f : {0.6, 0.8, 1.0, 1.2, 1.4}) blocks += std::ceil(f * rows / tn) / 5;
+  }
+  if (blocks < 1) blocks = 1;
+  const double cols = std::fmax(16, rows / blocks);
+  const double stage = pre ? std::fmax(900 + 300 / std::fmax(1, blocks - 1), 8 * 1.14 * (9 + 0.5 * cols))
+                           : 740 + 2.6 * cols;
   const double ks = static_cast<double>((a.K + 127) / 128);
-  const double units = blocks_g * active * ((a.N + 255) / 256);
+  const double units = blocks * active * ((a.N + 255) / 256);
   const double full = std::floor(units / pairs), rem = units - full * pairs;
   const double tail = rem > 0 ? std::fmin(ks, ks * rem / pairs + 14) : 0;
   const double drain = tn > 192 ? full * 5000 : 0;   // one accumulator: not overlapped
-  return (full * ks + tail) * stage + drain + (pre ? 8000 + a.total_M * a.K * 0.9e-3 : 0);
+  const double size = static_cast<double>(a.K) * (pre ? 5 : 1);
+  const double dram = (blocks * active * a.N * a.K + a.total_M * (size + 2 * a.N)) / 3100;
+  return std::fmax((full * ks + tail) * stage + drain + (pre ? 8000 + a.total_M * a.K * 0.9e-3 : 0), dram);
 }
 Choice choose(const Int8Params& a, int pairs) {
-  const Choice all[] = {{64, false}, {128, false}, {256, false}, {192, true}, {256, true}};
+  const Choice all[] = {{32, false}, {64, false}, {128, false}, {256, false}, {192, true}, {256, true}};
   Choice best = all[0];
   double least = 0;
   for (const Choice& c : all) {
@@ -997,7 +1066,7 @@ bsmma_status launch_pair(const Int8Params& a, bool f32, const DeviceInfo* dev, c
 #define BSMMA_INT8_TN(T, PRE) \
   (f32 ? launch_tn<T, PRE, true>(p, tok16, dev, stream) : launch_tn<T, PRE, false>(p, tok16, dev, stream))
   if (c.pre) return c.tn == 192 ? BSMMA_INT8_TN(192, true) : BSMMA_INT8_TN(256, true);
-  return c.tn == 64 ? BSMMA_INT8_TN(64, false) : c.tn == 128 ? BSMMA_INT8_TN(128, false)
+  return c.tn == 32 ? BSMMA_INT8_TN(32, false) : c.tn == 64 ? BSMMA_INT8_TN(64, false) : c.tn == 128 ? BSMMA_INT8_TN(128, false)
                                                              : BSMMA_INT8_TN(256, false);
 #undef BSMMA_INT8_TN
 }

@@ -519,7 +519,7 @@ void launch_route_grad(const RouteGradParams& p, cudaStream_t stream) {
 // arrival enters a rank.
 constexpr int kPlanThreads = 256;
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kPlanSlots = 4096;
+constexpr int kPlanSlots = 2048;
 
 struct PlanParams {
   const int32_t* ids;

@@ -423,7 +423,7 @@ bsmma_status moe_route_backward(const void* logits, bsmma_dtype logits_dtype, in
  *   pos     int32 [T][k] the row of each slot, -1 for one that is not used.
  *   The result depends on nothing but ids.  With unused slots m_sizes sums to less than
  *   T*k: grouped_int8_gemm takes that, the other grouped GEMMs want total_M equal to the sum.
- * Preconditions: 1 <= E <= 1024, k >= 1, T >= 0, T*k < 2^31 - 4096.  Up to 4096 slots one
+ * Preconditions: 1 <= E <= 1024, k >= 1, T >= 0, T*k < 2^31 - 4096.  Up to 2048 slots one
  *   launch; more take three and moe_plan_workspace_bytes(T, k, E) bytes of the stream's
  *   workspace (mx_gemm's; reserve it before a capture).  T == 0 only clears m_sizes.
  */

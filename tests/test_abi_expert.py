@@ -62,8 +62,8 @@ def test_plan_refusals(lib, args, expect):
 
 def test_plan_workspace(lib):
     assert lib.moe_plan_workspace_bytes(0, 8, 64) == 0
-    assert lib.moe_plan_workspace_bytes(512, 8, 64) == 0
-    assert lib.moe_plan_workspace_bytes(513, 8, 64) > 0
+    assert lib.moe_plan_workspace_bytes(256, 8, 64) == 0
+    assert lib.moe_plan_workspace_bytes(257, 8, 64) > 0
 
 
 @pytest.mark.parametrize("args,expect", [
