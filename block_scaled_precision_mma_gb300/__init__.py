@@ -39,7 +39,7 @@ __all__ = ["mx_gemm", "mx_gemm_tiled", "mx_gemm_noalloc", "grouped_fp8_gemm", "g
            "mx_quantize", "fp8_group_quantize", "fp8_block_quantize", "autotune_configure",
            "autotune_lookup",
            "mx_scale_tiled_bytes", "device_status", "reserve_workspace", "set_wait_limit_ns",
-           "set_dense_variant", "set_grouped_tile_width", "set_grouped_variant",
+           "set_dense_variant", "set_grouped_tile_width", "set_grouped_variant", "set_int8_variant",
            "launch_count", "probe_wait_timeout", "status_string", "BsmmaError", "load",
            "LAYOUTS", "FORMATS", "ROLES", "build", "LIB_PATH"]
 
@@ -91,6 +91,8 @@ def load(path: str | None = None):
         lib.bsmma_set_dense_variant.argtypes = [i32]
         lib.bsmma_set_grouped_tile_width.argtypes = [i32]
         lib.bsmma_set_grouped_variant.argtypes = [i32]
+        lib.bsmma_set_int8_variant.argtypes = [i32, i32]
+        lib.bsmma_set_int8_variant.restype = i32
         lib.bsmma_status_string.argtypes = [i32]
         lib.bsmma_status_string.restype = ctypes.c_char_p
         lib.bsmma_launch_count.argtypes = []
@@ -308,6 +310,12 @@ def set_grouped_tile_width(width: int):
 def set_grouped_variant(variant: int):
     """Grouped BF16 tiles: 0 automatic, 1 one CTA per tile, 3 SM-pair 256 x 256 tiles."""
     _check(load().bsmma_set_grouped_variant(int(variant)), "bsmma_set_grouped_variant")
+
+
+def set_int8_variant(tile: int, fp16_tokens: bool = False):
+    """INT8 products: 0 automatic, 1 few-row kernel, or SM-pair tiles of 32, 64, 128 or 256
+    rows, or of 192 or 256 rows widened to FP16 beforehand (``fp16_tokens``)."""
+    _check(load().bsmma_set_int8_variant(int(tile), int(bool(fp16_tokens))), "bsmma_set_int8_variant")
 
 
 def launch_count() -> int:

@@ -36,6 +36,8 @@ std::atomic<uint64_t> g_wait_limit_ns{2000000000ull};
 std::atomic<int> g_dense_variant{0};
 std::atomic<int> g_grouped_width{0};
 std::atomic<int> g_grouped_variant{0};
+std::atomic<int> g_int8_tile{0};
+std::atomic<bool> g_int8_fp16_tokens{false};
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -95,6 +97,8 @@ uint64_t wait_limit_ns() { return g_wait_limit_ns.load(); }
 int dense_variant() { return g_dense_variant.load(); }
 int grouped_tile_width() { return g_grouped_width.load(); }
 int grouped_variant() { return g_grouped_variant.load(); }
+int int8_tile() { return g_int8_tile.load(); }
+bool int8_fp16_tokens() { return g_int8_fp16_tokens.load(); }
 void count_launches(int n) { g_launches += n; }
 
 bsmma_status encode_tmap_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
@@ -734,6 +738,16 @@ bsmma_status bsmma_set_grouped_tile_width(int width) {
 bsmma_status bsmma_set_grouped_variant(int variant) {
   if (variant != 0 && variant != 1 && variant != 3) return BSMMA_ERR_INVALID_ARG;
   g_grouped_variant = variant;
+  return BSMMA_OK;
+}
+
+bsmma_status bsmma_set_int8_variant(int tile, int fp16_tokens) {
+  const bool wide = fp16_tokens == 1 && (tile == 192 || tile == 256);
+  const bool plain = fp16_tokens == 0 && (tile == 0 || tile == 1 || tile == 32 || tile == 64 ||
+                                          tile == 128 || tile == 256);
+  if (!wide && !plain) return BSMMA_ERR_INVALID_ARG;
+  g_int8_tile = tile;
+  g_int8_fp16_tokens = wide;
   return BSMMA_OK;
 }
 

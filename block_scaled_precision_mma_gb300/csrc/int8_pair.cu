@@ -1047,7 +1047,8 @@ Choice choose(const Int8Params& a, int pairs) {
 bsmma_status launch_pair(const Int8Params& a, bool f32, const DeviceInfo* dev, cudaStream_t stream) {
   PairParams p;
   p.a = a;
-  Choice c = choose(a, dev->sm_count / 2);
+  Choice c = int8_tile() > 1 ? Choice{int8_tile(), int8_fp16_tokens()} : choose(a, dev->sm_count / 2);
+  if (a.total_M == 0) c = Choice{32, false};   // no rows to widen; the sizes are still checked
   void* tok16 = nullptr;
   if (c.pre) {
     const bsmma_status st = stream_workspace(a.total_M * a.K * 2, stream, &tok16);

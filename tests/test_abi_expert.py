@@ -140,6 +140,14 @@ def test_combine_backward_refusals(lib, args, expect):
     assert lib.moe_combine_backward(*args, None) == expect
 
 
+@pytest.mark.parametrize("tile,fp16,expect", [(0, 0, 0), (1, 0, 0), (64, 0, 0), (256, 1, 0), (192, 1, 0), (0, 0, 0),
+                                              (192, 0, INVALID), (64, 1, INVALID), (0, 1, INVALID),
+                                              (-1, 0, INVALID), (2, 0, INVALID), (32, 2, INVALID)])
+def test_int8_variant_refusals(lib, tile, fp16, expect):
+    assert lib.bsmma_set_int8_variant(tile, fp16) == expect
+    assert lib.bsmma_set_int8_variant(0, 0) == 0
+
+
 def test_python_side_refusals():
     """Types and shapes are checked before pointers are taken (CPU tensors suffice)."""
     i8, f = torch.zeros((4, 32), dtype=torch.int8), torch.zeros(4)

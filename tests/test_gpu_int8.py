@@ -74,6 +74,15 @@ def test_quantize_near_halves_bit_exact():
     assert np.array_equal(codes.cpu().numpy(), c_ref)
 
 
+@pytest.fixture(params=[(0, 0), (1, 0), (32, 0), (64, 0), (128, 0), (256, 0), (192, 1), (256, 1)],
+                ids=["auto", "few", "t32", "t64", "t128", "t256", "f192", "f256"])
+def variant(request):
+    """Runs the test with each of the kernels."""
+    bs.set_int8_variant(*request.param)
+    yield request.param
+    bs.set_int8_variant(0)
+
+
 def codes(g, *shape):
     return g.integers(-128, 128, shape).astype(np.int8)
 
@@ -102,7 +111,7 @@ SHAPES = [(1, 1, 16), (1, 257, 48), (3, 130, 4096), (8, 100, 144), (9, 64, 1040)
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
-def test_dense_product_is_exact(M, N, K):
+def test_dense_product_is_exact(M, N, K, variant):
     g = np.random.default_rng([83, M, N, K])
     a, b = codes(g, M, K), codes(g, N, K)
     one = lambda n: np.ones(n, dtype=np.float32)  # noqa: E731
@@ -110,7 +119,7 @@ def test_dense_product_is_exact(M, N, K):
 
 
 @pytest.mark.parametrize("M", [2, 40, 300])
-def test_dense_largest_values_are_exact(M):
+def test_dense_largest_values_are_exact(M, variant):
     """Every product +-2^14: partial sums of 2^24 at K = 1024, the longest that must be exact."""
     K, N = 1024, 160
     a = np.full((M, K), -128, dtype=np.int8)
@@ -121,7 +130,7 @@ def test_dense_largest_values_are_exact(M):
 
 
 @pytest.mark.parametrize("M", [5, 200])
-def test_dense_one_sided_sums_round_as_fp32(M):
+def test_dense_one_sided_sums_round_as_fp32(M, variant):
     """Partial sums past 2^24: each of at most K / 16 accumulator steps may round (or cut) at
     2^-23 of the sum."""
     K, N = 14336, 96
@@ -136,7 +145,7 @@ def test_dense_one_sided_sums_round_as_fp32(M):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("bias", [True, False])
 @pytest.mark.parametrize("M,N,K", [(1, 130, 256), (12, 77, 512), (70, 513, 4096), (300, 600, 2064)])
-def test_dense_scales_and_bias(M, N, K, bias, dtype):
+def test_dense_scales_and_bias(M, N, K, bias, dtype, variant):
     g = np.random.default_rng([84, M, N, K])
     a, b = codes(g, M, K), codes(g, N, K)
     sa, sb = (g.random(n).astype(np.float32) * 0.02 + 0.001 for n in (M, N))
@@ -157,6 +166,27 @@ def test_dense_of_no_k(M):
     assert not dense(z[0], one(M), z[1], one(24)).any()
 
 
+@pytest.mark.parametrize("M,N,K", [(7, 4096, 8192), (100, 2304, 8208), (260, 1300, 4112), (600, 3000, 2064)])
+def test_dense_split_units_are_exact(M, N, K, variant):
+    """Few units of a long K: the last wave is split over the idle SM pairs."""
+    g = np.random.default_rng([90, M, N, K])
+    a, b = codes(g, M, K), codes(g, N, K)
+    one = lambda n: np.ones(n, dtype=np.float32)  # noqa: E731
+    assert np.array_equal(dense(a, one(M), b, one(N)), product(a, b))
+
+
+@pytest.mark.slow
+def test_dense_many_units(variant):
+    """More units than SM pairs, with a split remainder, both accumulators in turn."""
+    M, N, K = 1543, 9000, 1072
+    g = np.random.default_rng([91])
+    a, b = codes(g, M, K), codes(g, N, K)
+    one = lambda n: np.ones(n, dtype=np.float32)  # noqa: E731
+    got = dense(a, one(M), b, one(N))
+    want = (torch.from_numpy(a).cuda().double() @ torch.from_numpy(b).cuda().double().T).cpu().numpy()
+    assert np.array_equal(got, want)
+
+
 def grouped(a, sa, b, sb, sizes, dtype="f32"):
     T, N = len(a), b.shape[1]
     buf = torch.full((T * N + 128,), float("nan"), dtype=DT[dtype], device="cuda")
@@ -175,7 +205,7 @@ SPLITS = [[5], [0, 0, 3, 0], [1, 0, 7, 9, 0, 2, 64, 11], [3, 0, 300, 1, 0, 129, 
 
 @pytest.mark.parametrize("extra", [0, 5], ids=["full", "rows_left"])
 @pytest.mark.parametrize("sizes", SPLITS, ids=lambda s: f"G{len(s)}_T{sum(s)}")
-def test_grouped_product_is_exact(sizes, extra):
+def test_grouped_product_is_exact(sizes, extra, variant):
     g = np.random.default_rng([85, len(sizes), sum(sizes)])
     G, T, N, K = len(sizes), sum(sizes), 200, 144
     a, b = codes(g, T + extra, K), codes(g, G, N, K)
@@ -192,7 +222,7 @@ def test_grouped_product_is_exact(sizes, extra):
 
 @pytest.mark.parametrize("T,N,K,G", [(20, 1000, 1552, 6), (900, 769, 1552, 6), (2200, 384, 80, 3)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_grouped_types_and_tails(T, N, K, G, dtype):
+def test_grouped_types_and_tails(T, N, K, G, dtype, variant):
     g = np.random.default_rng([86, T, N, K])
     sizes = g.multinomial(T, np.arange(G) / (G * (G - 1) / 2)).tolist()
     a, b = codes(g, T, K), codes(g, G, N, K)
@@ -209,7 +239,7 @@ def test_grouped_types_and_tails(T, N, K, G, dtype):
 
 @pytest.mark.parametrize("T", [24, 900])
 @pytest.mark.parametrize("bad", [[10, -1, 5, 0], [10, 900, 0, 0], [1 << 40, 0, 0, 0], [0, 0, 0, -(1 << 62)]])
-def test_grouped_bad_sizes_write_nothing(bad, T):
+def test_grouped_bad_sizes_write_nothing(bad, T, variant):
     D = torch.full((T, 256), 5.0, device="cuda")
     X = torch.ones((T, 128), dtype=torch.int8, device="cuda")
     W = torch.ones((4, 256, 128), dtype=torch.int8, device="cuda")
@@ -219,7 +249,7 @@ def test_grouped_bad_sizes_write_nothing(bad, T):
     assert bool((D == 5).all())
 
 
-def test_grouped_without_rows():
+def test_grouped_without_rows(variant):
     W = torch.ones((4, 256, 128), dtype=torch.int8, device="cuda")
     D = bs.grouped_int8_gemm(torch.empty((0, 128), dtype=torch.int8, device="cuda"),
                              torch.empty(0, device="cuda"), W, torch.ones((4, 256), device="cuda"),
@@ -228,14 +258,14 @@ def test_grouped_without_rows():
 
 
 @pytest.mark.parametrize("M,N,K", [(3, 512, 8192), (100, 1000, 4096), (1000, 1000, 1040)])
-def test_same_call_same_bits(M, N, K):
+def test_same_call_same_bits(M, N, K, variant):
     g = np.random.default_rng([87, M])
     a, b = codes(g, M, K), codes(g, N, K)
     sa, sb = g.random(M).astype(np.float32), g.random(N).astype(np.float32)
     assert np.array_equal(dense(a, sa, b, sb), dense(a, sa, b, sb))
 
 
-def test_products_in_a_graph_on_a_stream():
+def test_products_in_a_graph_on_a_stream(variant):
     """Captured without a reservation and replayed on new inputs and a new split."""
     G, N, K, T = 5, 300, 272, 90
     stream = torch.cuda.Stream()

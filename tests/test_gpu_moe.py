@@ -181,7 +181,7 @@ def test_route_backward_ignores_foreign_ids():
     assert np.allclose(dx, want, atol=1e-6)
 
 
-@pytest.mark.parametrize("T,k,E", [(1, 1, 1), (5, 3, 2), (31, 1, 1024), (512, 8, 256), (4097, 1, 7),
+@pytest.mark.parametrize("T,k,E", [(1, 1, 1), (5, 3, 2), (31, 1, 1024), (256, 8, 256), (512, 8, 256), (2049, 1, 7),
                                    (2050, 2, 1024), (10001, 5, 60)])
 @pytest.mark.parametrize("unused", [0.0, 0.3, 1.0])
 def test_plan(T, k, E, unused):
