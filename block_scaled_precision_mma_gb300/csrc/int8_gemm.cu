@@ -7,7 +7,7 @@
 // twelfth of the FP16 tensor rate.  An INT8 value is exact in FP16 and a product of two
 // (at most 2^14) is exact in the FP32 accumulator, so the kernels widen both operands to
 // FP16 on the way to the tensor core.  The sum is exact as long as its partial sums stay
-// below 2^24 (any K <= 1040, and larger K unless almost all products have one sign), and
+// below 2^24 (any K <= 1024, and larger K unless almost all products have one sign), and
 // is rounded as an FP32 sum beyond.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -31,10 +31,13 @@ constexpr uint32_t kFull = 0xFFFFFFFFu;
 // One row per TPR threads, kept in registers between the maximum and the codes (V 16-byte
 // pieces a thread), or read twice when it is longer than that (V == 0).
 //   s = amax * (1 / 127), both steps in FP32 (1 when that is zero), code = rint(x / s) within [-127, 127].
-// The code is that of the correctly rounded quotient x / s.  With y = RN(1 / s), x * y is
-// within 127 * 2^-24 of x / s, and the rounded quotient is within 2^-18: together below
-// 2^-16.  So rint(x * y), from one fused step, is already the code unless x * y is that close
-// to a half (2^-15 is taken); only there is the quotient computed.
+// The code is that of the correctly rounded quotient x / s, which comes from the reciprocal
+// without a division a value, by the corrections that the FP8 quantisers use (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", IBM J. Res.
+// Dev. 34(1), 1990): with y = RN(1 / s), q0 = RN(x y) is within 1.5 ulp of x / s, one
+// correction q + (x - s q) y by fused steps makes it one of the two neighbours, a second
+// RN(x / s).  That needs s well inside the exponent range: 2^-88 to 2^100 here, where only
+// quotients below 2^-11 lose anything, whose code is 0 either way; other rows divide.
 struct QuantParams {
   const void* x;
   const int32_t* src;    // nullptr: row r is row r of x
@@ -78,29 +81,28 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-// N (4 or 8) codes of x / s in bytes.  inv = 1 / s, or 0 where that is no FP32 number.
+// N (4 or 8) codes of x / s in bytes, two values an instruction.  inv = 1 / s, or 0 where the
+// reciprocal does not serve.
 template <int N>
 __device__ __forceinline__ void codes_of(const float (&x)[N], float s, float inv,
                                          uint32_t (&out)[N / 4]) {
   constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: adding it rounds to an integer
   uint32_t b[N];
-  bool near_half = inv == 0.f;
-  const uint64_t inv2 = pack2(inv, inv), magic2 = pack2(kMagic, kMagic), minus2 = pack2(-1.f, -1.f);
+  if (inv != 0.f) {
+    const uint64_t inv2 = pack2(inv, inv), minus_s = pack2(-s, -s), zero = pack2(0.f, 0.f),
+                   one = pack2(1.f, 1.f), magic2 = pack2(kMagic, kMagic);
 #pragma unroll
-  for (int i = 0; i < N; i += 2) {   // two values an instruction
-    const uint64_t x2 = pack2(x[i], x[i + 1]);
-    const uint64_t y = fma2(x2, inv2, magic2);
-    const uint64_t f2 = fma2(x2, inv2, fma2(y, minus2, magic2));   // x * inv - the integer
-    float f0, f1;
-    unpack2(f2, f0, f1);
-    near_half |= fabsf(f0) > 0.5f - 0x1p-15f;
-    near_half |= fabsf(f1) > 0.5f - 0x1p-15f;
-    float y0, y1;
-    unpack2(y, y0, y1);
-    b[i] = __float_as_uint(y0);
-    b[i + 1] = __float_as_uint(y1);
-  }
-  if (near_half) {
+    for (int i = 0; i < N; i += 2) {
+      const uint64_t x2 = pack2(x[i], x[i + 1]);
+      const uint64_t q0 = fma2(x2, inv2, zero);
+      const uint64_t q1 = fma2(fma2(minus_s, q0, x2), inv2, q0);
+      const uint64_t q = fma2(fma2(minus_s, q1, x2), inv2, q1);
+      float y0, y1;
+      unpack2(fma2(q, one, magic2), y0, y1);
+      b[i] = __float_as_uint(y0);
+      b[i + 1] = __float_as_uint(y1);
+    }
+  } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) b[i] = code_slow(x[i], s);
   }
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) int8_quantize_kernel(co
   float s = __fmul_rn(__uint_as_float(amax), 1.f / 127.f);
   if (s == 0.f) s = 1.f;
   if (tid == 0) p.scales[r] = s;
-  const float inv = s >= 0x1p-100f && s <= 0x1p100f ? __fdiv_rn(1.f, s) : 0.f;
+  const float inv = s >= 0x1p-88f && s <= 0x1p100f ? __fdiv_rn(1.f, s) : 0.f;
   uint32_t* out = reinterpret_cast<uint32_t*>(p.codes) + r * p.vecs * (kN / 4);
   auto emit = [&](int v, const uint4& h) {
     float f[kN];

@@ -76,7 +76,7 @@ struct Cfg {
   static constexpr int kSmemBytes = kTail + kTokSlots * kWideBytes + kStages * kRawBytes;
   static_assert((2 * kStages + 2 * kSlots + 5 + (PRE ? 2 * kTokSlots : 0)) * 8 + 8 <= 512,
                 "barriers fit below the group table");
-  static_assert(kStages >= 3 && 4 * kOutBytes <= kStages * kRawBytes, "shared memory budget");
+  static_assert(kStages >= 3 && kSlots % 2 == 0 && 4 * kOutBytes <= kStages * kRawBytes, "shared memory budget");
   static_assert(kBufs * TN + kSlots * kSlotCols <= 512, "tensor memory budget");
 };
 
@@ -670,9 +670,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     // number modulo 8)
     const uint32_t chan = static_cast<uint32_t>(tid) * 128 + ((tid & 7) << 4);
     constexpr int kPieces = PRE ? 0 : (C::kHalf + 31) / 32;   // of a half's tokens, a thread
-    int stage = 0, turn = 0;
-    uint32_t phase = 0, slot = 0, slot_phase = 0;
+    // (both halves of a stage at once where the registers allow: one latency, and only the
+    // stores left to do when the slot is free)
+    constexpr bool kWhole = PRE || kPieces <= 1;
+    int stage = wg, slot = wg % kSlots, k_off = wg;
+    uint32_t phase = 0, slot_phase = 0;
     bool ok = true;
+    auto widen16 = [](const uint4 (&c)[4], uint32_t (&w)[32]) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        widen4(c[j].x, w[8 * j], w[8 * j + 1]);
+        widen4(c[j].y, w[8 * j + 2], w[8 * j + 3]);
+        widen4(c[j].z, w[8 * j + 4], w[8 * j + 5]);
+        widen4(c[j].w, w[8 * j + 6], w[8 * j + 7]);
+      }
+    };
+    auto store_tokens = [](const uint4& x, uint32_t dst) {
+      uint32_t v[8];
+      widen4(x.x, v[0], v[1]);
+      widen4(x.y, v[2], v[3]);
+      widen4(x.z, v[4], v[5]);
+      widen4(x.w, v[6], v[7]);
+      sts128(dst, v[0], v[1], v[2], v[3]);
+      sts128(dst ^ 16, v[4], v[5], v[6], v[7]);
+    };
     while (ok && walk.next(sched, workers, u, k0, k1)) {
       const Unit un = find_unit(table, p, u);
       const int half = unit_cols(un) / 2;
@@ -686,92 +707,81 @@ __global__ void __launch_bounds__(kThreads, 1)
         from[i] = piece < 4 ? 128 * 128 + r * 128 + ((piece ^ (r & 7)) << 4) : kNone;
         to[i] = r * 128 + (((2 * piece) ^ (r & 7)) << 4);
       }
-      for (int k = k0; k < k1; ++k, turn ^= 1) {
-        if (turn == wg) {
-          if (!wait_phase(&full[stage], phase, p.limit_ns, abort_flag, p.a.status)) {
-            ok = false;
-            break;
+      int k = k0 + k_off;
+      for (; k < k1; k += 2) {
+        if (!wait_phase(&full[stage], phase, p.limit_ns, abort_flag, p.a.status)) {
+          ok = false;
+          break;
+        }
+        const uint32_t base = smem_u32(raw + stage * C::kRawBytes);
+        const uint32_t out = smem_u32(wide + slot * C::kWideBytes);
+        const uint32_t tslot = taddr + slot * kSlotCols;
+        const int halves = 2 * k + 1 < p.halves_k ? 2 : 1;
+        auto release_stage = [&] {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[stage]);
+        };
+        auto slot_free = [&] {
+          ok = wait_phase(&wide_empty[slot], slot_phase ^ 1, p.limit_ns, abort_flag, p.a.status);
+          tc_fence_after();
+          return ok;
+        };
+        if constexpr (kWhole) {
+          uint4 c[4], d[4], x[2];
+          uint32_t w[32], y[32];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) c[j] = lds128(base + (chan ^ (j << 4)));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) d[j] = lds128(base + (chan ^ 64 ^ (j << 4)));
+          if (kPieces > 0 && from[0] != kNone) {
+            x[0] = lds128(base + from[0]);
+            x[1] = lds128(base + (from[0] ^ 64));
           }
-          const uint32_t base = smem_u32(raw + stage * C::kRawBytes);
-          const uint32_t out = smem_u32(wide + slot * C::kWideBytes);
-          const int halves = 2 * k + 1 < p.halves_k ? 2 : 1;
-          auto widen16 = [](const uint4 (&c)[4], uint32_t (&w)[32]) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              widen4(c[j].x, w[8 * j], w[8 * j + 1]);
-              widen4(c[j].y, w[8 * j + 2], w[8 * j + 3]);
-              widen4(c[j].z, w[8 * j + 4], w[8 * j + 5]);
-              widen4(c[j].w, w[8 * j + 6], w[8 * j + 7]);
-            }
-          };
-          auto slot_free = [&] {
-            ok = wait_phase(&wide_empty[slot], slot_phase ^ 1, p.limit_ns, abort_flag, p.a.status);
-            tc_fence_after();
-            return ok;
-          };
-          if constexpr (PRE) {
-            // both halves are ready before the slot is: only the stores follow its release
-            uint4 c[4], d[4];
-            uint32_t w[32], y[32];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) c[j] = lds128(base + (chan ^ (j << 4)));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) d[j] = lds128(base + (chan ^ 64 ^ (j << 4)));
-            widen16(c, w);
-            widen16(d, y);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[stage]);
-            if (!slot_free()) break;
-            tmem_st32(taddr + slot * kSlotCols, w);
-            if (halves == 2) tmem_st32(taddr + slot * kSlotCols + 32, y);
-          } else {
+          widen16(c, w);
+          widen16(d, y);
+          release_stage();
+          if (!slot_free()) break;
+          tmem_st32(tslot, w);
+          if (halves == 2) tmem_st32(tslot + 32, y);
+          if (kPieces > 0 && from[0] != kNone) {
+            store_tokens(x[0], out + to[0]);
+            store_tokens(x[1], out + C::kWideBytes / 2 + to[0]);
+          }
+        } else {
 #pragma unroll 1
-            for (int h = 0; h < halves; ++h) {
-              uint4 c[4], x[kPieces + 1];
+          for (int h = 0; h < halves; ++h) {
+            uint4 c[4], x[kPieces + 1];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) c[j] = lds128(base + (chan ^ (h << 6) ^ (j << 4)));
+            for (int j = 0; j < 4; ++j) c[j] = lds128(base + (chan ^ (h << 6) ^ (j << 4)));
 #pragma unroll
-              for (int i = 0; i < kPieces; ++i)
-                if (from[i] != kNone) x[i] = lds128(base + (from[i] ^ (h << 6)));
-              if (h == halves - 1) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[stage]);
-              }
-              uint32_t w[32];
-              widen16(c, w);
-              if (h == 0 && !slot_free()) break;
-              tmem_st32(taddr + slot * kSlotCols + h * 32, w);
+            for (int i = 0; i < kPieces; ++i)
+              if (from[i] != kNone) x[i] = lds128(base + (from[i] ^ (h << 6)));
+            if (h == halves - 1) release_stage();
+            uint32_t w[32];
+            widen16(c, w);
+            if (h == 0 && !slot_free()) break;
+            tmem_st32(tslot + h * 32, w);
 #pragma unroll
-              for (int i = 0; i < kPieces; ++i) {
-                if (from[i] != kNone) {
-                  uint32_t v[8];
-                  widen4(x[i].x, v[0], v[1]);
-                  widen4(x[i].y, v[2], v[3]);
-                  widen4(x[i].z, v[4], v[5]);
-                  widen4(x[i].w, v[6], v[7]);
-                  const uint32_t dst = out + h * (C::kWideBytes / 2);
-                  sts128(dst + to[i], v[0], v[1], v[2], v[3]);
-                  sts128(dst + (to[i] ^ 16), v[4], v[5], v[6], v[7]);
-                }
-              }
-            }
+            for (int i = 0; i < kPieces; ++i)
+              if (from[i] != kNone) store_tokens(x[i], out + h * (C::kWideBytes / 2) + to[i]);
           }
           if (!ok) break;
-          tmem_st_wait();
-          fence_async_proxy();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_leader(map_to_cta(smem_u32(&wide_full[slot]), 0));
         }
-        if (++stage == kStages) {
-          stage = 0;
+        tmem_st_wait();
+        fence_async_proxy();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_leader(map_to_cta(smem_u32(&wide_full[slot]), 0));
+        if ((stage += 2) >= kStages) {
+          stage -= kStages;
           phase ^= 1;
         }
-        if (++slot == kSlots) {
-          slot = 0;
+        if ((slot += 2) >= kSlots) {
+          slot -= kSlots;
           slot_phase ^= 1;
         }
       }
+      k_off = k - k1;
     }
   } else if (warp >= kOutWarp0) {
     // ---------------------------------------------------------------- output (both CTAs)
@@ -1051,11 +1061,14 @@ bsmma_status launch_pair(const Int8Params& a, bool f32, const DeviceInfo* dev, c
   if (a.total_M == 0) c = Choice{32, false};   // no rows to widen; the sizes are still checked
   void* tok16 = nullptr;
   if (c.pre) {
-    const bsmma_status st = stream_workspace(a.total_M * a.K * 2, stream, &tok16);
-    if (st == BSMMA_ERR_WORKSPACE)   // captured without one: widened in the kernel
+    // captured without a workspace, or no memory for one, or rows of more bytes than a copy's
+    // coordinate counts: widened in the kernel
+    const bsmma_status st = a.K < (int64_t(1) << 30) ? stream_workspace(a.total_M * a.K * 2, stream, &tok16)
+                                                     : BSMMA_ERR_WORKSPACE;
+    if (st != BSMMA_OK) {
+      cudaGetLastError();
       c = Choice{256, false};
-    else if (st != BSMMA_OK)
-      return st;
+    }
   }
   if (c.pre) {
     const int64_t n16 = a.total_M * a.K / 16, per = 256 * kWidenSteps;

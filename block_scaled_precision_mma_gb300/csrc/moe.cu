@@ -524,7 +524,7 @@ constexpr int kPlanSlots = 2048;
 struct PlanParams {
   const int32_t* ids;
   int64_t S;
-  int E, bits, blocks;
+  int E, blocks;
   int32_t* block_hist;   // [E][blocks]: counts, then their exclusive prefix over blocks
   int32_t* totals;       // [E]
   int64_t* m_sizes;
@@ -534,7 +534,7 @@ struct PlanParams {
 
 // Ranks the block's slots; each thread's ranks go through `emit(slot, id, rank)` after the
 // warps' histograms have been prefix-summed.  hist: [kPlanWarps][E] counters.
-template <typename Count, typename Emit>
+template <int BITS, typename Count, typename Emit>
 __device__ __forceinline__ void rank_slots(const PlanParams& p, int64_t s0, int32_t* hist,
                                            Count count, Emit emit) {
   constexpr int kRows = kPlanSlots / kPlanWarps / 32;
@@ -552,7 +552,8 @@ __device__ __forceinline__ void rank_slots(const PlanParams& p, int64_t s0, int3
 #pragma unroll
   for (int r = 0; r < kRows; ++r) {
     uint32_t peers = __ballot_sync(kFull, id[r] >= 0);
-    for (int b = 0; b < p.bits; ++b) {
+#pragma unroll
+    for (int b = 0; b < BITS; ++b) {
       const bool bit = (id[r] >> b) & 1;
       const uint32_t v = __ballot_sync(kFull, bit);
       peers &= bit ? v : ~v;
@@ -620,13 +621,14 @@ __device__ __forceinline__ int32_t block_prefix(int32_t* v, int n, int32_t* warp
 }
 
 // All of it in one block (S <= kPlanSlots).
+template <int BITS>
 __global__ void __launch_bounds__(kPlanThreads) plan_one_kernel(const PlanParams p) {
   extern __shared__ int32_t smem_i[];
   int32_t* start = smem_i + kPlanWarps * p.E;
   __shared__ int32_t warp_sums[kPlanWarps];
   int32_t total = 0;
   // the expert starts are known only after the counts, before the ranks are emitted
-  rank_slots(
+  rank_slots<BITS>(
       p, 0, smem_i,
       [&](int e, int32_t n) {
         start[e] = n;
@@ -646,10 +648,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_one_kernel(const PlanParams
   }
 }
 
+template <int BITS>
 __global__ void __launch_bounds__(kPlanThreads) plan_rank_kernel(const PlanParams p) {
   extern __shared__ int32_t smem_i[];
   grid_launch_dependents();
-  rank_slots(
+  rank_slots<BITS>(
       p, static_cast<int64_t>(blockIdx.x) * kPlanSlots, smem_i,
       [&](int e, int32_t n) { p.block_hist[static_cast<int64_t>(e) * p.blocks + blockIdx.x] = n; },
       [&](int64_t s, int, int32_t rank) { p.pos[s] = rank; });
@@ -663,18 +666,28 @@ __global__ void __launch_bounds__(128) plan_scan_kernel(const PlanParams p) {
   grid_dependency_wait();
   if (e >= p.E) return;
   int32_t* h = p.block_hist + static_cast<int64_t>(e) * p.blocks;
+  // eight loads in flight a lane: the scan is nothing but their latency
+  constexpr int kAhead = 8;
   int32_t base = 0;
-  for (int b0 = 0; b0 < p.blocks; b0 += 32) {
-    const int b = b0 + lane;
-    const int32_t c = b < p.blocks ? h[b] : 0;
-    int32_t inc = c;
+  for (int b0 = 0; b0 < p.blocks; b0 += 32 * kAhead) {
+    int32_t c[kAhead];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t y = __shfl_up_sync(kFull, inc, o);
-      if (lane >= o) inc += y;
+    for (int i = 0; i < kAhead; ++i) {
+      const int b = b0 + i * 32 + lane;
+      c[i] = b < p.blocks ? h[b] : 0;
     }
-    if (b < p.blocks) h[b] = base + inc - c;
-    base += __shfl_sync(kFull, inc, 31);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int b = b0 + i * 32 + lane;
+      int32_t inc = c[i];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t y = __shfl_up_sync(kFull, inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (b < p.blocks) h[b] = base + inc - c[i];
+      base += __shfl_sync(kFull, inc, 31);
+    }
   }
   if (lane == 0) {
     p.totals[e] = base;
@@ -905,10 +918,19 @@ bsmma_status launch_route_t(const RouteParams& p, cudaStream_t stream) {
   return launch_route_v<F32, 32>(p, stream);
 }
 
-int bits_for(int E) {
-  int b = 0;
-  while ((1 << b) < E) ++b;
-  return b;
+template <int BITS>
+bsmma_status launch_plan_bits(const PlanParams& p, cudaStream_t stream) {
+  if (p.S <= kPlanSlots) {
+    plan_one_kernel<BITS><<<1, kPlanThreads, (kPlanWarps + 1) * p.E * 4, stream>>>(p);
+    count_launches(1);
+    return cuda_ok(cudaGetLastError());
+  }
+  plan_rank_kernel<BITS><<<p.blocks, kPlanThreads, kPlanWarps * p.E * 4, stream>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = launch_dependent(plan_scan_kernel, (p.E + 3) / 4, 128, 0, stream, p);
+  if (e == cudaSuccess) e = launch_dependent(plan_place_kernel, p.blocks, kPlanThreads, 0, stream, p);
+  count_launches(3);
+  return cuda_ok(e);
 }
 
 }  // namespace
@@ -970,24 +992,16 @@ bsmma_status launch_plan(const int32_t* ids, int64_t S, int E, int64_t* m_sizes,
   p.ids = ids;
   p.S = S;
   p.E = E;
-  p.bits = bits_for(E);
   p.blocks = static_cast<int>((S + kPlanSlots - 1) / kPlanSlots);
   p.totals = static_cast<int32_t*>(workspace);
   p.block_hist = p.totals ? p.totals + E : nullptr;
   p.m_sizes = m_sizes;
   p.src = src;
   p.pos = pos;
-  if (S <= kPlanSlots) {
-    plan_one_kernel<<<1, kPlanThreads, (kPlanWarps + 1) * E * 4, stream>>>(p);
-    count_launches(1);
-    return cuda_ok(cudaGetLastError());
-  }
-  plan_rank_kernel<<<p.blocks, kPlanThreads, kPlanWarps * E * 4, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = launch_dependent(plan_scan_kernel, (E + 3) / 4, 128, 0, stream, p);
-  if (e == cudaSuccess) e = launch_dependent(plan_place_kernel, p.blocks, kPlanThreads, 0, stream, p);
-  count_launches(3);
-  return cuda_ok(e);
+  // one ballot a bit of the expert's number
+  if (E <= 16) return launch_plan_bits<4>(p, stream);
+  if (E <= 128) return launch_plan_bits<7>(p, stream);
+  return launch_plan_bits<10>(p, stream);
 }
 
 bsmma_status launch_combine(const void* y, bool f32, int64_t R, int64_t H, const int32_t* pos,

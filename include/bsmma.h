@@ -451,9 +451,13 @@ bsmma_status int8_quantize(const void* x, bsmma_dtype x_dtype, int64_t x_rows, i
  *   A int8 [M][K], B int8 [N][K], sA FP32 [M], sB FP32 [N], bias BF16 [N] or NULL, D [M][N]
  *   BF16 or FP32 (d_dtype), rounded once.  sm_103a has no INT8 tcgen05 MMA; the operands are
  *   widened to FP16, where an INT8 value and a product of two are exact, and summed in FP32:
- *   the integer sum is exact while its partial sums stay below 2^24 (any K <= 1040; longer K
- *   short of one-sided extremes), else rounded as FP32 sums are.  The order of the sum, and
- *   so the result, is the same in every call with the same sizes.
+ *   the integer sum is exact while its partial sums stay below 2^24 (any K <= 1024; longer K
+ *   short of one-sided extremes), else rounded as FP32 sums are, in an order that depends on
+ *   the sizes alone (and on whether a captured stream has the workspaces below).
+ *   One launch; two where many rows of A are widened to FP16 first, in the stream's workspace
+ *   (mx_gemm's; 2 * M * K bytes).  The last wave's units may be split along K, as mx_gemm's
+ *   are, in the stream's split workspace.  A call captured on a stream without these
+ *   workspaces needs no reservation: it widens in the kernel and splits nothing.
  * Preconditions: M, N, K >= 0, K % 16 == 0, M, N, K < 2^31 - 512, 16-byte-aligned A, B and D,
  *   4-byte-aligned sA and sB, 2-byte-aligned bias.  N is not restricted.  M == 0 or N == 0
  *   is a no-op; K == 0 writes the bias, or 0.
