@@ -30,6 +30,7 @@ constexpr uint32_t kFull = 0xFFFFFFFFu;
 // ---------------------------------------------------------------- quantiser
 // One row per TPR threads, kept in registers between the maximum and the codes (V 16-byte
 // pieces a thread), or read twice when it is longer than that (V == 0).
+// Bound by DRAM: 16384 rows of 7168 BF16 take 54 us, 352 MB at 6.6 TB/s.
 //   s = amax * (1 / 127), both steps in FP32 (1 when that is zero), code = rint(x / s) within [-127, 127].
 // The code is that of the correctly rounded quotient x / s, which comes from the reciprocal
 // without a division a value, by the corrections that the FP8 quantisers use (Markstein,

@@ -5,8 +5,17 @@
 // to TN rows of A ("tokens").  Both operands arrive as INT8 by TMA and are widened to FP16
 // on the SM, where they are exact: the channels' values go from registers into tensor
 // memory, the A operand of tcgen05.mma, and the tokens' into shared memory, its B operand.
-// So DRAM and L2 carry one byte a value, and of the 4 bytes of shared-memory traffic that
-// the widened values would cost per channel value only the INT8 ones remain.
+// So DRAM and L2 carry one byte a value, and the channels' widened values never cross shared
+// memory, which the MMAs' own reads of the tokens fill (an FP16 tile by TMA would write and
+// read two bytes each).
+//
+// What bounds it, as measured (graph replays, L2 flushed): many rows the tensor pipe, 4096 x
+// 14336 x 4096 265 us with the widening pass, 1.82 PFLOP/s, and 8 experts of 7168 x 2304 with
+// 16384 rows 320 us, 1.69 PFLOP/s (tensor pipe 76% busy under ncu at the clock it holds there);
+// few rows the streaming of the channels, 64 experts of 2048 x 7168 with 256 rows 128 us,
+// 5.8 TB/s; in between (192 rows an expert) the widening warps' latencies, tensor pipe and
+// DRAM both near half.  A single short product is launch, setup and pipeline start: 4 x 14336 x
+// 4096 takes about 18 us of which its bytes are 9.
 //
 // One persistent launch over 2-CTA clusters, 512 threads a CTA:
 //   warp 0       TMA producer: 128 K of the CTA's 128 channels and of its half of the tokens
@@ -17,7 +26,7 @@
 //                128-byte-swizzled shared-memory tile (with PRE the tokens come as FP16, by
 //                warp 2);
 //   warps 12-15  output: accumulator columns out of tensor memory, times the scales, plus
-//                the bias, rounded and stored, 32 channels of a token per warp store.
+//                the bias, rounded, turned through shared memory and stored by rows of D.
 // Units (a token block of one group x 256 channels) are dealt round robin; the last wave's
 // are split along K over the pairs that would idle (stream_k.cuh), the partial sums added in
 // K order by the last pair to finish.
@@ -63,8 +72,9 @@ struct Cfg {
   // accumulators, and slots of widened channels in the rest of tensor memory
   static constexpr int kBufs = 2 * TN + 2 * kSlotCols <= 512 ? 2 : 1;
   static constexpr int kFree = (512 - kBufs * TN) / kSlotCols;
-  static constexpr int kSlots = PRE ? (kFree < 4 ? kFree : 4) : 2;   // (three: 144 us, two: 138 us at
-                                                                      // 64 x 2048 x 7168, 256 rows)
+  static constexpr int kSlots = PRE ? (kFree < 4 ? kFree : 4) : 2;   // (three: a shorter ring,
+                                                                      // 144 us for 138 at 64 x
+                                                                      // 2048 x 7168, 256 rows)
   static constexpr int kTokSlots = PRE ? (TN > 192 ? (F32 ? 3 : 4) : 5) : kSlots;
   // output tile: 32 tokens x 128 channels, rows padded so that two rows' halves of the banks
   // do not meet
@@ -133,7 +143,7 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint6
 // CTA's shared and tensor memory, or accumulator columns read) concerns this CTA's own tensor
 // core.  Release at cluster scope waits for every earlier store of the warp to be visible to
 // the cluster: 800 to 1100 cycles a slot for the widening warps, and all of a tile's output
-// stores for the output warps (4096 x 14336 x 4096: 605 -> 345 us without).
+// stores for the output warps (4096 x 14336 x 4096 at that time: 605 us with it, 486 without).
 __device__ __forceinline__ void arrive_leader(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
@@ -159,7 +169,8 @@ __device__ __forceinline__ void cluster_wait() {
 // True in one lane of the (whole) warp, the same one every time.  A role that issues copies or
 // MMAs runs its loop on all lanes and elects the issuing one at the instruction, so that loop
 // state and descriptors are warp-uniform for the compiler; under a divergent `lane == 0` each
-// MMA cost its issuer about 180 cycles.
+// MMA cost its issuer about 180 cycles, longer than the MMA itself (4096 x 14336 x 4096: 550
+// us with it, 392 without).
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile(
@@ -670,8 +681,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // number modulo 8)
     const uint32_t chan = static_cast<uint32_t>(tid) * 128 + ((tid & 7) << 4);
     constexpr int kPieces = PRE ? 0 : (C::kHalf + 31) / 32;   // of a half's tokens, a thread
-    // (both halves of a stage at once where the registers allow: one latency, and only the
-    // stores left to do when the slot is free)
+    // Loads of both halves first, one latency for all; where the registers allow, both halves
+    // are widened before the slot is free, and only the stores are left then.
     constexpr bool kWhole = PRE || kPieces <= 1;
     int stage = wg, slot = wg % kSlots, k_off = wg;
     uint32_t phase = 0, slot_phase = 0;
@@ -748,24 +759,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             store_tokens(x[1], out + C::kWideBytes / 2 + to[0]);
           }
         } else {
-#pragma unroll 1
-          for (int h = 0; h < halves; ++h) {
-            uint4 c[4], x[kPieces + 1];
+          // everything is loaded and the stage handed back first, the registers then freed half
+          // by half
+          uint4 c[8], x[2][kPieces + 1];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) c[j] = lds128(base + (chan ^ (h << 6) ^ (j << 4)));
+          for (int j = 0; j < 8; ++j) c[j] = lds128(base + (chan ^ (j << 4)));
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < kPieces; ++i)
-              if (from[i] != kNone) x[i] = lds128(base + (from[i] ^ (h << 6)));
-            if (h == halves - 1) release_stage();
+              if (from[i] != kNone) x[h][i] = lds128(base + (from[i] ^ (h << 6)));
+          release_stage();
+          if (!slot_free()) break;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h == halves) break;
             uint32_t w[32];
-            widen16(c, w);
-            if (h == 0 && !slot_free()) break;
+            const uint4 half_c[4] = {c[4 * h], c[4 * h + 1], c[4 * h + 2], c[4 * h + 3]};
+            widen16(half_c, w);
             tmem_st32(tslot + h * 32, w);
 #pragma unroll
             for (int i = 0; i < kPieces; ++i)
-              if (from[i] != kNone) store_tokens(x[i], out + h * (C::kWideBytes / 2) + to[i]);
+              if (from[i] != kNone) store_tokens(x[h][i], out + h * (C::kWideBytes / 2) + to[i]);
           }
-          if (!ok) break;
         }
         tmem_st_wait();
         fence_async_proxy();

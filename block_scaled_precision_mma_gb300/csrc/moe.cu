@@ -167,8 +167,9 @@ __global__ void __launch_bounds__(128) route_bf16_kernel(const RouteParams p) {
 // rows are whole 64-byte pieces.  A lane keeps the eight largest keys of its experts in
 // order: it sorts eight new ones (19 exchanges of a maximum and a minimum) and merges them in
 // (eight maxima, 12 exchanges); two more merges across the four lanes leave all of them with
-// the token's eight.  About 80 warp instructions a token at 128 experts against 440 for the
-// rounds above, which at 65536 tokens took 34 us, issue-bound.
+// the token's eight.  96 warp instructions a token at 128 experts against 440 for the rounds
+// above: 65536 tokens 13 us against 34, both bound by issuing (56% of the slots; the 21 MB are
+// 3 us).
 __device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b) {
   const uint32_t hi = max(a, b);
   b = min(a, b);
@@ -263,7 +264,9 @@ __global__ void __launch_bounds__(128) route_quad_kernel(const RouteParams p) {
     }
 }
 
-// FP32 logits, a bias or groups: 32-bit keys, lane l holding experts 32 i + l.
+// FP32 logits, a bias or groups: 32-bit keys, lane l holding experts 32 i + l.  A decoding
+// step is its chain of latencies: 32 tokens of 256 experts with a bias and groups take 8.3 us
+// a launch, one after another.
 template <bool F32, int V>
 __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
   extern __shared__ float smem[];
@@ -696,8 +699,9 @@ __global__ void __launch_bounds__(128) plan_scan_kernel(const PlanParams p) {
 }
 
 // A block's slots are put in expert order in shared memory first, so that what it writes to
-// src is a run per expert and not a word here and there (1 M slots, 128 experts: 21 us with
-// the words scattered and the loads in turn, 8 us so).
+// src is a run per expert and not a word here and there, and its loads are all in flight at
+// once (1 M slots, 128 experts under ncu: 21 us with the words scattered and the loads in
+// turn, 10 us so; the three kernels together 17.5 us, chains of latencies each, for 12.6 MB).
 __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanParams p) {
   constexpr int kPer = kPlanSlots / kPlanThreads;
   __shared__ int32_t start[1024];     // first row of the expert in the block's run
@@ -782,7 +786,8 @@ struct CombineParams {
 };
 
 // A thread owns one 16-byte piece of one token's output and has up to kUnroll rows' pieces
-// in flight; the sum runs over the token's slots in order.
+// in flight; the sum runs over the token's slots in order.  Bound by DRAM: 8192 tokens of 8
+// rows of 4096 BF16 take 85 us, 604 MB at 7.1 TB/s.
 template <bool F32>
 __global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
   constexpr int kUnroll = 8, kN = Vec<F32>::kN;
@@ -818,7 +823,8 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
 
 // One block per token: dY of its rows is w * dout, dw the dot product of dout and the row.
 // The token's dout pieces are read once per kSlots slots.  Four blocks an SM: at the 120
-// registers that ptxas takes by itself two fit, and 8192 x 8 rows of 4096 took 197 us, not 165.
+// registers that ptxas takes by itself two fit, and 8192 x 8 rows of 4096 BF16 took 197 us, not 170 (1.14 GB: 6.7
+// TB/s, DRAM 81% busy).
 template <bool F32>
 __global__ void __launch_bounds__(256, 4) combine_grad_kernel(const CombineParams p) {
   constexpr int kN = Vec<F32>::kN, kSlots = 8;
