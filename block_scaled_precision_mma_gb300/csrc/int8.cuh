@@ -1,5 +1,5 @@
 // int8.cuh -- what the INT8 product kernels share: their arguments, the widening of INT8
-// values to FP16 and the output store.
+// values to FP16, the output store and the table of the groups' rows.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace bsmma {
 namespace int8 {
@@ -45,6 +46,110 @@ __device__ __forceinline__ void store_out(void* D, int64_t i, float v) {
     static_cast<float*>(D)[i] = v;
   else
     static_cast<__nv_bfloat16*>(D)[i] = __float2bfloat16_rn(v);
+}
+
+// Where each group's rows and blocks of rows begin, for blocks of THREADS threads.
+template <int THREADS>
+struct GroupTable {
+  int32_t start[kMaxG + 1];    // first row of each group
+  int32_t tile0[kMaxG + 1];    // its first row block
+  int32_t warp_sum[2][THREADS / 32];
+  int bad;
+};
+
+// Fills the table (every thread of the block); blocks of tn rows.  Sizes that are negative or
+// sum to more than total_M set `bad` and latch the status once.
+template <int THREADS>
+__device__ __forceinline__ void build_table(GroupTable<THREADS>& t, const Int8Params& p, int tn) {
+  constexpr uint32_t kFull = 0xFFFFFFFFu, kThreads = THREADS;
+  const int G = p.G, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (!p.m_sizes) {
+    if (tid == 0) {
+      t.start[0] = 0;
+      t.tile0[0] = 0;
+      t.start[1] = static_cast<int32_t>(p.total_M);
+      t.tile0[1] = static_cast<int32_t>((p.total_M + tn - 1) / tn);
+      t.bad = 0;
+    }
+    __syncthreads();
+    return;
+  }
+  constexpr int kPer = kMaxG / kThreads;
+  int64_t rows = 0;
+  int32_t m[kPer], blocks = 0;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int g = tid * kPer + i;
+    const int64_t v = g < G ? p.m_sizes[g] : 0;
+    const bool out = v < 0 || v > p.total_M;
+    bad |= out;
+    m[i] = out ? 0 : static_cast<int32_t>(v);
+    rows += m[i];
+    blocks += (m[i] + tn - 1) / tn;
+  }
+  // sums of up to 1024 sizes below 2^31 each can pass 32 bits: checked in 64 first
+  int64_t all = rows;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(kFull, all, o);
+  bad |= all > p.total_M;
+  bad = __syncthreads_or(bad);
+  int32_t ir = static_cast<int32_t>(bad ? 0 : rows), ib = bad ? 0 : blocks;
+  const int32_t r_own = ir, b_own = ib;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t a = __shfl_up_sync(kFull, ir, o), b = __shfl_up_sync(kFull, ib, o);
+    if (lane >= o) {
+      ir += a;
+      ib += b;
+    }
+  }
+  if (lane == 31) {
+    t.warp_sum[0][warp] = ir;
+    t.warp_sum[1][warp] = ib;
+  }
+  __syncthreads();
+  int32_t r0 = ir - r_own, b0 = ib - b_own;
+  int64_t total = 0;
+  for (int w = 0; w < static_cast<int>(kThreads) / 32; ++w) {
+    if (w < warp) {
+      r0 += t.warp_sum[0][w];
+      b0 += t.warp_sum[1][w];
+    }
+    total += t.warp_sum[0][w];
+  }
+  bad |= total > p.total_M;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int g = tid * kPer + i;
+    if (g <= G) {
+      t.start[g] = r0;
+      t.tile0[g] = b0;
+    }
+    r0 += m[i];
+    b0 += (m[i] + tn - 1) / tn;
+    if (g == G - 1) {
+      t.start[G] = r0;
+      t.tile0[G] = b0;
+    }
+  }
+  if (tid == 0) {
+    t.bad = bad;
+    if (bad && blockIdx.x == 0) report_status(p.status, kDevBadMSizes);
+  }
+  __syncthreads();
+}
+
+// The group of row block mt: the last one whose first block is not after it.
+template <int THREADS>
+__device__ __forceinline__ int find_group(const GroupTable<THREADS>& t, int G, int mt) {
+  int lo = 0, hi = G - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.tile0[mid] <= mt) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
 }
 
 // SM-pair kernel (int8_pair.cu).

@@ -213,130 +213,141 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Row block `y` (blocks of R rows of one group, groups in order) -> group, its first row
-// and its rows left.  Called by every thread of a 256-thread block; false past the last
-// block or when the sizes are negative or exceed total_M.
-struct RowBlock {
-  int64_t row0;
-  int g, rows, state;   // state: 1 found, 0 past the end, -1 bad sizes
-};
-__device__ __forceinline__ bool find_row_block(const Int8Params& p, int64_t y, int R,
-                                               RowBlock& rb) {
-  if (!p.m_sizes) {
-    rb.g = 0;
-    rb.row0 = y * R;
-    const int64_t left = p.total_M - rb.row0;
-    rb.rows = left < R ? static_cast<int>(left) : R;
-    return left > 0;
-  }
-  constexpr int kPer = kMaxG / 256;
-  __shared__ RowBlock found;
-  __shared__ int64_t warp_rows[8], warp_blocks[8];
-  __syncthreads();
-  if (threadIdx.x == 0) found.state = 0;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t m[kPer], rows = 0, blocks = 0;
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int g = threadIdx.x * kPer + i;
-    m[i] = g < p.G ? p.m_sizes[g] : 0;
-    if (m[i] < 0 || m[i] > p.total_M) {
-      bad = true;
-      m[i] = 0;
-    }
-    rows += m[i];
-    blocks += (m[i] + R - 1) / R;
-  }
-  int64_t ir = rows, ib = blocks;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t a = __shfl_up_sync(kFull, ir, o), b = __shfl_up_sync(kFull, ib, o);
-    if (lane >= o) {
-      ir += a;
-      ib += b;
-    }
-  }
-  if (lane == 31) {
-    warp_rows[warp] = ir;
-    warp_blocks[warp] = ib;
-  }
-  bad = __syncthreads_or(bad);
-  int64_t r0 = ir - rows, b0 = ib - blocks, all = 0;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    if (w < warp) {
-      r0 += warp_rows[w];
-      b0 += warp_blocks[w];
-    }
-    all += warp_rows[w];
-  }
-  bad = bad || all > p.total_M;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int64_t nb = (m[i] + R - 1) / R;
-    if (!bad && y >= b0 && y < b0 + nb) {
-      found.g = threadIdx.x * kPer + i;
-      found.row0 = r0 + (y - b0) * R;
-      const int64_t left = m[i] - (y - b0) * R;
-      found.rows = left < R ? static_cast<int>(left) : R;
-      found.state = 1;
-    }
-    r0 += m[i];
-    b0 += nb;
-  }
-  if (bad && threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0)
-    report_status(p.status, kDevBadMSizes);
-  __syncthreads();
-  rb = found;
-  return rb.state == 1;
+__device__ __forceinline__ void cp_async_16(uint32_t dst_smem, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src),
+               "r"(in ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
 }
 
-// Products of few rows: bound by reading B once.  A block of 8 warps takes 32 channels and
-// up to 8 * NT rows of A; its warps share out K in pieces of 128 and add their sums through
-// shared memory.  A lane reads 16 consecutive K of a channel straight into registers and
-// uses the same 16 K of A, so the order of K inside an MMA step (the same for both
-// operands) needs no shuffle.
+// Products of few rows: bound by reading B once, so everything is arranged to keep its bytes
+// in flight.  One block of 8 warps an SM takes units of 32 channels x up to 8 * NT rows in
+// turn; its warps share out K in pieces of 128, each warp with a ring of kStages pieces of its
+// own (160 KB in flight an SM) that runs on across units, and their sums meet in shared memory
+// at a unit's end.  A lane copies and reads back its own 16 consecutive K of a channel and uses
+// the same 16 K of A, so no barrier is needed inside a unit and the order of K inside an MMA
+// step (the same for both operands) needs no shuffle.
+template <int NT>
+struct RowsCfg {
+  static constexpr int kPieceBytes = (8 + 2 * NT) * 512;   // a warp's 128 K: 32 channels, 8 NT rows
+  static constexpr int kStages = NT == 1 ? 5 : 4;
+  static constexpr int kRingBytes = 8 * kStages * kPieceBytes;
+  static constexpr int kSumBytes = 8 * 32 * 8 * NT * 4;
+  static constexpr int kSmemBytes = kRingBytes + kSumBytes + static_cast<int>(sizeof(int8::GroupTable<256>));
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
 template <int NT, bool F32>
-__global__ void __launch_bounds__(256) int8_rows_kernel(const Int8Params p) {
-  constexpr int R = 8 * NT;
-  __shared__ float sums[8][32 * R];
+__global__ void __launch_bounds__(256, 1) int8_rows_kernel(const Int8Params p) {
+  using C = RowsCfg<NT>;
+  constexpr int R = 8 * NT, S = C::kStages;
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* sums = reinterpret_cast<float*>(smem + C::kRingBytes);   // [warp][row][channel]
+  int8::GroupTable<256>& table =
+      *reinterpret_cast<int8::GroupTable<256>*>(smem + C::kRingBytes + C::kSumBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q = lane >> 2, t = lane & 3;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 32;
-  for (int64_t y = blockIdx.y;; y += gridDim.y) {
-    RowBlock rb;
-    if (!find_row_block(p, y, R, rb)) return;
-    const int8_t* B = p.B + static_cast<int64_t>(rb.g) * p.N * p.K;
-    const int8_t* wrow[4];
-    bool wok[4];
+  int8::build_table(table, p, R);
+  if (table.bad) return;
+  const int tiles = static_cast<int>((p.N + 31) / 32), units = table.tile0[p.G] * tiles;
+  const int pieces = static_cast<int>((p.K + 127) / 128);
+  const int mine = pieces > warp ? (pieces - warp + 7) / 8 : 0;   // of every unit
+  const uint32_t ring = smem_u32(smem) + warp * (S * C::kPieceBytes) + lane * 16;
+
+  struct Place {
+    int g, row0, rows;
+    int64_t n0;
+  };
+  auto place = [&](int u) {
+    Place r;
+    const int mt = u / tiles;
+    r.n0 = static_cast<int64_t>(u - mt * tiles) * 32;
+    r.g = int8::find_group(table, p.G, mt);
+    const int off = (mt - table.tile0[r.g]) * R;
+    r.row0 = table.start[r.g] + off;
+    const int left = table.start[r.g + 1] - r.row0;
+    r.rows = left < R ? left : R;
+    return r;
+  };
+
+  // the copies run kStages - 1 pieces ahead of the products
+  int pu = mine > 0 ? static_cast<int>(blockIdx.x) : units, pi = 0, pslot = 0;
+  const int8_t *wsrc = nullptr, *asrc = nullptr;
+  uint32_t ok = 0;   // bits 0-3: the lane's channels exist; 4..: its rows
+  auto issue = [&] {
+    if (pu < units) {
+      if (pi == 0) {
+        const Place u = place(pu);
+        ok = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t n = n0 + q + 8 * i;
-      wok[i] = n < p.N;
-      wrow[i] = B + (wok[i] ? n : 0) * p.K + 16 * t;
+        for (int i = 0; i < 4; ++i) ok |= (u.n0 + q + 8 * i < p.N ? 1u : 0u) << i;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) ok |= (q + 8 * i < u.rows ? 1u : 0u) << (4 + i);
+        wsrc = p.B + (static_cast<int64_t>(u.g) * p.N + u.n0 + q) * p.K + 16 * t + warp * 128;
+        asrc = p.A + static_cast<int64_t>(u.row0 + q) * p.K + 16 * t + warp * 128;
+      }
+      const int64_t k = static_cast<int64_t>(pi) * 1024, k_lane = k + warp * 128 + 16 * t;
+      const uint32_t dst = ring + pslot * C::kPieceBytes;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const bool in = k_lane + 64 * c < p.K;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool some = in && (ok >> i & 1u);
+          cp_async_16(dst + (c * 4 + i) * 512, some ? wsrc + k + 64 * c + 8 * i * p.K : p.B, some);
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const bool some = in && (ok >> (4 + i) & 1u);
+          cp_async_16(dst + (8 + c * NT + i) * 512, some ? asrc + k + 64 * c + 8 * i * p.K : p.B, some);
+        }
+      }
+      if (++pi == mine) {
+        pi = 0;
+        pu += gridDim.x;
+      }
     }
-    const int8_t* arow[NT];
-    bool aok[NT];
+    cp_async_commit();
+    if (++pslot == S) pslot = 0;
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue();
+
+  int slot = 0;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const Place un = place(u);
+    // the scales of this thread's outputs, loaded ahead of the sums
+    float scale[NT], bias[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      aok[i] = q + 8 * i < rb.rows;
-      arow[i] = p.A + (rb.row0 + (aok[i] ? q + 8 * i : 0)) * p.K + 16 * t;
+      const int o = i * 256 + threadIdx.x;
+      const int64_t n = un.n0 + (o & 31);
+      scale[i] = bias[i] = 0.f;
+      if (n < p.N && (o >> 5) < un.rows) {
+        scale[i] = p.sA[un.row0 + (o >> 5)] * p.sB[un.g * p.N + n];
+        if (p.bias) bias[i] = __bfloat162float(p.bias[n]);
+      }
     }
     float acc[2][NT][4] = {};
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int64_t k0 = warp * 128; k0 < p.K; k0 += 8 * 128) {
+    for (int it = 0; it < mine; ++it) {
+      cp_async_wait<S - 2>();
+      const uint32_t from = ring + slot * C::kPieceBytes;
+      if (++slot == S) slot = 0;
       uint4 w[2][4], a[2][NT];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const bool in = k0 + 64 * c + 16 * t < p.K;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[c][i] = in && wok[i] ? __ldcs(reinterpret_cast<const uint4*>(wrow[i] + k0 + 64 * c)) : zero;
+        for (int i = 0; i < 4; ++i) w[c][i] = lds16(from + (c * 4 + i) * 512);
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-          a[c][i] = in && aok[i] ? *reinterpret_cast<const uint4*>(arow[i] + k0 + 64 * c) : zero;
+        for (int i = 0; i < NT; ++i) a[c][i] = lds16(from + (8 + c * NT + i) * 512);
       }
+      issue();   // into the slot that the piece before this one was read from
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -358,41 +369,47 @@ __global__ void __launch_bounds__(256) int8_rows_kernel(const Int8Params p) {
         }
     }
     // accumulator element: channel q (+8) of half h, rows 2t, 2t+1 of row tile i
-    __syncthreads();
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          sums[warp][(8 * i + 2 * t + (e & 1)) * 32 + 16 * h + q + 8 * (e >> 1)] = acc[h][i][e];
+          sums[(warp * R + 8 * i + 2 * t + (e & 1)) * 32 + 16 * h + q + 8 * (e >> 1)] = acc[h][i][e];
     __syncthreads();
-    for (int o = threadIdx.x; o < 32 * rb.rows; o += 256) {
-      const int64_t n = n0 + (o & 31), m = rb.row0 + (o >> 5);
-      if (n < p.N) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int o = i * 256 + threadIdx.x;
+      const int64_t n = un.n0 + (o & 31);
+      if (n < p.N && (o >> 5) < un.rows) {
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) s += sums[w][o];
-        s *= p.sA[m] * p.sB[static_cast<int64_t>(rb.g) * p.N + n];
-        if (p.bias) s += __bfloat162float(p.bias[n]);
-        store_out<F32>(p.D, m * p.N + n, s);
+        for (int w = 0; w < 8; ++w) s += sums[w * R * 32 + o];
+        store_out<F32>(p.D, static_cast<int64_t>(un.row0 + (o >> 5)) * p.N + n,
+                       fmaf(s, scale[i], bias[i]));
       }
     }
-    if (!p.m_sizes && (y + gridDim.y) * R >= p.total_M) return;
+    __syncthreads();
   }
+  cp_async_wait_all();
 }
 
-template <int NT>
-bsmma_status launch_rows(const Int8Params& p, bool f32, cudaStream_t stream) {
+template <int NT, bool F32>
+bsmma_status launch_rows(const Int8Params& p, const DeviceInfo* dev, cudaStream_t stream) {
+  using C = RowsCfg<NT>;
+  static bool attr_set = false;   // benign race: setting the attribute twice is harmless
+  if (!attr_set) {
+    if (cudaFuncSetAttribute(int8_rows_kernel<NT, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::kSmemBytes) != cudaSuccess)
+      return BSMMA_ERR_CUDA;
+    attr_set = true;
+  }
   int64_t blocks = (p.total_M + 8 * NT - 1) / (8 * NT);
   if (p.m_sizes) blocks += p.G < p.total_M ? p.G : p.total_M;
   if (blocks < 1) blocks = 1;   // the sizes are still checked
-  const dim3 grid(static_cast<unsigned>((p.N + 31) / 32),
-                  static_cast<unsigned>(blocks < 32768 ? blocks : 32768));
-  if (f32)
-    int8_rows_kernel<NT, true><<<grid, 256, 0, stream>>>(p);
-  else
-    int8_rows_kernel<NT, false><<<grid, 256, 0, stream>>>(p);
+  const int64_t units = blocks * ((p.N + 31) / 32);
+  const int64_t grid = units < dev->sm_count ? units : dev->sm_count;
+  int8_rows_kernel<NT, F32><<<static_cast<unsigned>(grid), 256, C::kSmemBytes, stream>>>(p);
   count_launches(1);
   return cuda_ok(cudaGetLastError());
 }
@@ -440,9 +457,9 @@ bsmma_status launch_int8_gemm(const int8_t* A, const float* sA, const int8_t* B,
   const bool few = tile == 1 || (tile == 0 && per_group <= 8 &&
                                  static_cast<int64_t>(G) * N * K <= (int64_t(8) << 20));
   if (!few && K > 0) return int8::launch_pair(p, f32, dev, stream);
-  if (per_group <= 8) return launch_rows<1>(p, f32, stream);
-  if (per_group <= 16) return launch_rows<2>(p, f32, stream);
-  return launch_rows<4>(p, f32, stream);
+  if (per_group <= 8)
+    return f32 ? launch_rows<1, true>(p, dev, stream) : launch_rows<1, false>(p, dev, stream);
+  return f32 ? launch_rows<2, true>(p, dev, stream) : launch_rows<2, false>(p, dev, stream);
 }
 
 }  // namespace bsmma

@@ -55,10 +55,7 @@ constexpr int kSetupBarrier = 6;              // all but the channel producer
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 
 struct Table {
-  int32_t start[kMaxG + 1];    // first row of each group
-  int32_t tile0[kMaxG + 1];    // its first token block
-  int32_t warp_sum[2][kThreads / 32];
-  int bad;
+  GroupTable<kThreads> groups;
   int fixes, fix[2];           // split units whose parts this CTA adds (two at most)
 };
 
@@ -210,103 +207,18 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
                : "memory");
 }
 
-// Fills the group table (every thread of the block); blocks of tn rows.
-__device__ __forceinline__ void build_table(Table& t, const PairParams& p) {
-  const int G = p.a.G, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (!p.a.m_sizes) {
-    if (tid == 0) {
-      t.start[0] = 0;
-      t.tile0[0] = 0;
-      t.start[1] = static_cast<int32_t>(p.a.total_M);
-      t.tile0[1] = static_cast<int32_t>((p.a.total_M + p.tn - 1) / p.tn);
-      t.bad = 0;
-    }
-    __syncthreads();
-    return;
-  }
-  constexpr int kPer = kMaxG / kThreads;
-  int64_t rows = 0;
-  int32_t m[kPer], blocks = 0;
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int g = tid * kPer + i;
-    const int64_t v = g < G ? p.a.m_sizes[g] : 0;
-    const bool out = v < 0 || v > p.a.total_M;
-    bad |= out;
-    m[i] = out ? 0 : static_cast<int32_t>(v);
-    rows += m[i];
-    blocks += (m[i] + p.tn - 1) / p.tn;
-  }
-  // sums of up to 1024 sizes below 2^31 each can pass 32 bits: checked in 64 first
-  int64_t all = rows;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(kFull, all, o);
-  bad |= all > p.a.total_M;
-  bad = __syncthreads_or(bad);
-  int32_t ir = static_cast<int32_t>(bad ? 0 : rows), ib = bad ? 0 : blocks;
-  const int32_t r_own = ir, b_own = ib;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int32_t a = __shfl_up_sync(kFull, ir, o), b = __shfl_up_sync(kFull, ib, o);
-    if (lane >= o) {
-      ir += a;
-      ib += b;
-    }
-  }
-  if (lane == 31) {
-    t.warp_sum[0][warp] = ir;
-    t.warp_sum[1][warp] = ib;
-  }
-  __syncthreads();
-  int32_t r0 = ir - r_own, b0 = ib - b_own;
-  int64_t total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) {
-      r0 += t.warp_sum[0][w];
-      b0 += t.warp_sum[1][w];
-    }
-    total += t.warp_sum[0][w];
-  }
-  bad |= total > p.a.total_M;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int g = tid * kPer + i;
-    if (g <= G) {
-      t.start[g] = r0;
-      t.tile0[g] = b0;
-    }
-    r0 += m[i];
-    b0 += (m[i] + p.tn - 1) / p.tn;
-    if (g == G - 1) {
-      t.start[G] = r0;
-      t.tile0[G] = b0;
-    }
-  }
-  if (tid == 0) {
-    t.bad = bad;
-    if (bad && blockIdx.x == 0) report_status(p.a.status, kDevBadMSizes);
-  }
-  __syncthreads();
-}
-
 // A unit: its group, first token, tokens, and first channel.
 struct Unit {
   int g, row0, rows, n0;
 };
 constexpr int kBand = 16;   // token blocks walked together over all channels, for L2
-__device__ __forceinline__ Unit find_unit(const Table& t, const PairParams& p, int u) {
+__device__ __forceinline__ Unit find_unit(const GroupTable<kThreads>& t, const PairParams& p, int u) {
   const int NT = p.num_n_tiles, blocks = t.tile0[p.a.G];
   const int b = u / (kBand * NT), first = b * kBand;
   const int h = blocks - first < kBand ? blocks - first : kBand;
   const int v = u - b * kBand * NT;
   const int mt = first + v % h;
-  int lo = 0, hi = p.a.G - 1;   // the last group whose first block is not after mt
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (t.tile0[mid] <= mt) lo = mid;
-    else hi = mid - 1;
-  }
+  const int lo = find_group(t, p.a.G, mt);
   Unit r;
   r.g = lo;
   const int off = (mt - t.tile0[lo]) * p.tn;
@@ -479,11 +391,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmA32);
     prefetch_tmap(&tmAll);
   }
-  build_table(table, p);
+  build_table(table.groups, p.a, p.tn);
   // both CTAs read the same sizes, so a bad table stops the whole cluster here.  (With PRE
   // the launch may have started before the widening pass has ended: one warp of every CTA
   // waits for that, so that this grid's end is the pass's too.)
-  if (table.bad) {
+  if (table.groups.bad) {
     if (PRE && warp == 2) grid_dependency_wait();
     return;
   }
@@ -506,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const uint32_t tmem_wide = tmem + 512 - kSlots * kSlotCols;
   const int worker = static_cast<int>(blockIdx.x >> 1), workers = static_cast<int>(gridDim.x >> 1);
-  const DSched sched = make_dsched(table.tile0[p.a.G] * p.num_n_tiles, p.stages_k, 1, workers,
+  const DSched sched = make_dsched(table.groups.tile0[p.a.G] * p.num_n_tiles, p.stages_k, 1, workers,
                                    p.part != nullptr, 14, 4);
   Walk walk(sched, worker);
   int u, k0, k1;
@@ -518,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0, armed = 0, armed_parity = 0;
     bool ok = true;
     while (ok && walk.next(sched, workers, u, k0, k1)) {
-      const Unit un = find_unit(table, p, u);
+      const Unit un = find_unit(table.groups, p, u);
       const int half = unit_cols(un) / 2;
       const int row = un.row0 + rank * half;
       const int chan = static_cast<int>(un.g * p.a.N) + un.n0 + rank * 128;
@@ -568,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0, armed = 0, armed_parity = 0;
     bool ok = true;
     while (ok && walk.next(sched, workers, u, k0, k1)) {
-      const Unit un = find_unit(table, p, u);
+      const Unit un = find_unit(table.groups, p, u);
       const int half = unit_cols(un) / 2;
       const int row = un.row0 + rank * half;
       for (int k = k0; k < k1; ++k) {
@@ -615,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t b_desc = make_sdesc(smem_u32(wide), 16, 1024, kSwizzle128B);
       bool ok = true;
       while (ok && walk.next(sched, workers, u, k0, k1)) {
-        const Unit un = find_unit(table, p, u);
+        const Unit un = find_unit(table.groups, p, u);
         const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(unit_cols(un) >> 3) << 17) |
                                ((256u >> 4) << 24);   // FP32 accumulator, FP16 operands, M = 256
         const uint32_t buf = tcount % C::kBufs;
@@ -706,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sts128(dst ^ 16, v[4], v[5], v[6], v[7]);
     };
     while (ok && walk.next(sched, workers, u, k0, k1)) {
-      const Unit un = find_unit(table, p, u);
+      const Unit un = find_unit(table.groups, p, u);
       const int half = unit_cols(un) / 2;
       // the thread's i-th 16-byte piece of the tokens is that of token e % half, piece
       // e / half of its four, e = i * 128 + tid: where it is in a stage, and where its first
@@ -807,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t acc_empty_leader = map_to_cta(smem_u32(acc_empty), 0);
     uint32_t tcount = 0, flip = 0;
     while (walk.next(sched, workers, u, k0, k1)) {
-      const Unit un = find_unit(table, p, u);
+      const Unit un = find_unit(table.groups, p, u);
       const int cols = unit_cols(un), chan0 = un.n0 + rank * 128;
       const int64_t n = chan0 + tid;
       const bool ok = n < p.a.N;
@@ -873,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (table.fixes > 0) __threadfence();
     for (int f = 0; f < table.fixes; ++f) {
       const int v = table.fix[f] - sched.t_dp;
-      const Unit un = find_unit(table, p, table.fix[f]);
+      const Unit un = find_unit(table.groups, p, table.fix[f]);
       const int chan0 = un.n0 + rank * 128;
       const int64_t n = chan0 + tid;
       const bool ok = n < p.a.N;
