@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 
 #include "internal.h"
@@ -152,7 +153,22 @@ __device__ __forceinline__ int find_group(const GroupTable<THREADS>& t, int G, i
   return lo;
 }
 
-// SM-pair kernel (int8_pair.cu).
+// Blocks of `tn` rows that a group's rows make on the host's estimate: of one group exactly, of
+// several on average over groups 0.6 to 1.4 times as large as their mean.
+inline double blocks_per_group(const Int8Params& a, double rows, int tn) {
+  double blocks = std::ceil(rows / tn);
+  if (a.G > 1) {
+    blocks = 0;
+    for (const double f : {0.6, 0.8, 1.0, 1.2, 1.4}) blocks += std::ceil(f * rows / tn) / 5;
+  }
+  return blocks < 1 ? 1 : blocks;
+}
+inline double groups_with_rows(const Int8Params& a) {
+  return a.total_M < a.G ? static_cast<double>(a.total_M) : a.G;
+}
+
+// SM-pair kernel (int8_pair.cu), and the SM cycles it is expected to take.
+double pair_cycles(const Int8Params& p, const DeviceInfo* dev);
 bsmma_status launch_pair(const Int8Params& p, bool f32, const DeviceInfo* dev, cudaStream_t stream);
 
 }  // namespace int8

@@ -414,6 +414,22 @@ bsmma_status launch_rows(const Int8Params& p, const DeviceInfo* dev, cudaStream_
   return cuda_ok(cudaGetLastError());
 }
 
+// SM cycles that the few-row kernel is expected to take: its units in turn, each the pieces of
+// its slowest warp at 24 bytes a cycle (15.5 with 16 rows) or, where units are short, 1000 a
+// piece and 2600 for the sums and the next unit's start; 5000 for the launch; 15% for uneven
+// groups, some of which take a second block.  It wins where one or two row blocks read B once
+// or B is small: 4 x 14336 x 4096 17 against 23 us on SM-pair tiles, 4 x 4096 x 4096 11 and 21,
+// 32 x 4096 x 4096 17 and 25; but 32 x 14336 x 4096 33 and 21, 128 experts of 1408 x 2048 with 4
+// rows each 109 and 74.
+double rows_cycles(const Int8Params& p, const DeviceInfo* dev) {
+  const double active = int8::groups_with_rows(p), rows = active > 0 ? p.total_M / active : 0;
+  const int nt = (p.total_M + p.G - 1) / p.G <= 8 ? 1 : 2;
+  const double units = int8::blocks_per_group(p, rows, 8 * nt) * active * ((p.N + 31) / 32);
+  const double pieces = static_cast<double>((p.K + 1023) / 1024);   // of a warp
+  const double unit = std::fmax(pieces * 32 * 1024 / (nt == 1 ? 24 : 15.5), 2600 + 1000 * pieces) + 300;
+  return (std::ceil(units / dev->sm_count) * unit + 5000) * (p.G > 1 ? 1.15 : 1);
+}
+
 }  // namespace
 
 bsmma_status launch_int8_quantize(const void* x, bool f32, int64_t x_rows, int64_t rows, int64_t K,
@@ -452,10 +468,7 @@ bsmma_status launch_int8_gemm(const int8_t* A, const float* sA, const int8_t* B,
   p.status = dev->status;
   const int64_t per_group = (total_M + G - 1) / G;
   const int tile = int8_tile();
-  // The few-row kernel has the shorter start (1 x 1024 x 1024: 10.7 against 12.8 us), the
-  // SM-pair kernel streams faster (4 x 14336 x 4096: 35.3 against 23.0 us).
-  const bool few = tile == 1 || (tile == 0 && per_group <= 8 &&
-                                 static_cast<int64_t>(G) * N * K <= (int64_t(8) << 20));
+  const bool few = tile == 1 || (tile == 0 && rows_cycles(p, dev) < int8::pair_cycles(p, dev));
   if (!few && K > 0) return int8::launch_pair(p, f32, dev, stream);
   if (per_group <= 8)
     return f32 ? launch_rows<1, true>(p, dev, stream) : launch_rows<1, false>(p, dev, stream);

@@ -33,8 +33,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <cmath>
-
 #include "int8.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -929,17 +927,15 @@ __global__ void __launch_bounds__(256) widen_kernel(const uint4* __restrict__ in
 
 // Which tile a launch takes: the cheapest by an estimate in SM cycles that the host makes from
 // the sizes alone.
-//   - A 128-K stage takes about 740 + 2.6 cycles a column with the tokens widened in the
+//   - A 128-K stage takes about 660 + 2.75 cycles a column with the tokens widened in the
 //     kernel (a fit to 32 to 256 columns, dense and grouped).  With FP16 tokens it takes its
 //     eight MMAs, 9 + 0.5 cycles a column each and 14% more, or the channels' arrival: the
 //     ring is five stages then, and without other blocks that bring the same channels to L2 a
 //     stage waits some 1200 cycles for DRAM.
-//   - Units are what the groups' blocks make: of one group exactly, of several on average
-//     over groups 0.6 to 1.4 times as large as their mean.
 //   - A wave of units that leaves pairs idle is split over them when that is shorter; a
-//     split costs about 14 stages (parts written, counted, read back).  Measured at 14336 x
+//     split costs 14 to 18 stages (parts written, counted, read back).  Measured at 14336 x
 //     4096, 128 rows: 27 us unsplit, 35 us split, 56 units on 76 pairs.
-//   - Each block reads its channels from DRAM, at 3.1 KB a cycle; FP16 tokens cost a pass over
+//   - Each block reads its channels from DRAM, at 3.3 KB a cycle; FP16 tokens cost a pass over
 //     them first and twice the bytes.
 // At 4096 x 14336 x 4096: 268 us with FP16 tokens (192 columns), 312 us without (256); 64
 // experts of 2048 x 7168 with 192 rows each: 369 and 289 us.
@@ -948,38 +944,41 @@ struct Choice {
   bool pre;
 };
 double estimate(const Int8Params& a, int tn, bool pre, int pairs) {
-  const double active = a.total_M < a.G ? static_cast<double>(a.total_M) : a.G;
+  const double active = groups_with_rows(a);
   const double rows = active > 0 ? a.total_M / active : 0;
-  double blocks = std::ceil(rows / tn);
-  if (a.G > 1) {
-    blocks = 0;
-    for (const double f : {0.6, 0.8, 1.0, 1.2, 1.4}) blocks += std::ceil(f * rows / tn) / 5;
-  }
-  if (blocks < 1) blocks = 1;
+  const double blocks = blocks_per_group(a, rows, tn);
   const double cols = std::fmax(16, rows / blocks);
   const double stage = pre ? std::fmax(900 + 300 / std::fmax(1, blocks - 1), 8 * 1.14 * (9 + 0.5 * cols))
-                           : 740 + 2.6 * cols;
+                           : 660 + 2.75 * cols;
   const double ks = static_cast<double>((a.K + 127) / 128);
   const double units = blocks * active * ((a.N + 255) / 256);
   const double full = std::floor(units / pairs), rem = units - full * pairs;
-  const double tail = rem > 0 ? std::fmin(ks, ks * rem / pairs + 14) : 0;
+  const double tail = rem > 0 ? std::fmin(ks, ks * rem / pairs + 18) : 0;
   const double drain = tn > 192 ? full * 5000 : 0;   // one accumulator: not overlapped
   const double size = static_cast<double>(a.K) * (pre ? 5 : 1);
-  const double dram = (blocks * active * a.N * a.K + a.total_M * (size + 2 * a.N)) / 3100;
+  const double dram = (blocks * active * a.N * a.K + a.total_M * (size + 2 * a.N)) / 3300;
   return std::fmax((full * ks + tail) * stage + drain + (pre ? 8000 + a.total_M * a.K * 0.9e-3 : 0), dram);
 }
-Choice choose(const Int8Params& a, int pairs) {
+Choice choose(const Int8Params& a, int pairs, double* cycles = nullptr) {
   const Choice all[] = {{32, false}, {64, false}, {128, false}, {256, false}, {192, true}, {256, true}};
   Choice best = all[0];
-  double least = 0;
+  double least = -1;
   for (const Choice& c : all) {
     const double t = estimate(a, c.tn, c.pre, pairs);
-    if (least == 0 || t < least) {
+    if (least < 0 || t < least) {
       least = t;
       best = c;
     }
   }
+  if (cycles) *cycles = least;
   return best;
+}
+
+// (9500: launch, setup and the start of the pipeline)
+double pair_cycles(const Int8Params& a, const DeviceInfo* dev) {
+  double t = 0;
+  choose(a, dev->sm_count / 2, &t);
+  return t + 9500;
 }
 
 bsmma_status launch_pair(const Int8Params& a, bool f32, const DeviceInfo* dev, cudaStream_t stream) {

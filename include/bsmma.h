@@ -536,8 +536,8 @@ bsmma_status bsmma_set_grouped_tile_width(int width);
 bsmma_status bsmma_set_grouped_variant(int variant);
 
 /* Selects the kernel of later int8_gemm and grouped_int8_gemm calls: tile 0 automatic
- * (default: the few-row kernel for weights of up to 8 M values and at most 8 rows a group,
- * else the tile that an estimate from the sizes finds cheapest), 1 the few-row kernel, or
+ * (default: the kernel and tile that an estimate from the sizes finds cheapest), 1 the
+ * few-row kernel, or
  * SM-pair tiles of 256 channels x 32, 64, 128 or 256 rows (fp16_tokens 0: INT8 rows widened in
  * the kernel) or x 192 or 256 rows (fp16_tokens 1: widened to FP16 by a pass before it).  Any
  * other pair returns BSMMA_ERR_INVALID_ARG.  Same result while sums are exact (int8_gemm); a
