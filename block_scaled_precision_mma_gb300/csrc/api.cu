@@ -653,7 +653,7 @@ bsmma_status grouped_int8_gemm(const int8_t* X, const float* sX, const int8_t* W
 
 namespace {
 bsmma_status check_combine(bsmma_dtype dtype, int64_t R, int64_t H, int64_t T, int k) {
-  if (!known_dtype(dtype) || H <= 0 || H >= INT32_MAX || T < 0 || T >= INT32_MAX || R < 0 ||
+  if (!known_dtype(dtype) || H <= 0 || H > (1 << 24) || T < 0 || T >= INT32_MAX || R < 0 ||
       R >= INT32_MAX || k < 1 || k > 32 || T * k >= INT32_MAX)
     return BSMMA_ERR_INVALID_ARG;
   if (H % (dtype == BSMMA_F32 ? 4 : 8) != 0) return BSMMA_ERR_MISALIGNED;

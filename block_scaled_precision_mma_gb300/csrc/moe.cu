@@ -669,28 +669,30 @@ __global__ void __launch_bounds__(128) plan_scan_kernel(const PlanParams p) {
   grid_dependency_wait();
   if (e >= p.E) return;
   int32_t* h = p.block_hist + static_cast<int64_t>(e) * p.blocks;
-  // eight loads in flight a lane: the scan is nothing but their latency
-  constexpr int kAhead = 8;
+  // a lane scans 16 consecutive counts by itself, their loads in flight together, so that one
+  // scan across the warp serves 512: what it takes is latency alone
+  constexpr int kRun = 16;
   int32_t base = 0;
-  for (int b0 = 0; b0 < p.blocks; b0 += 32 * kAhead) {
-    int32_t c[kAhead];
+  for (int b0 = 0; b0 < p.blocks; b0 += 32 * kRun) {
+    const int first = b0 + lane * kRun;
+    int32_t c[kRun], sum = 0;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int b = b0 + i * 32 + lane;
-      c[i] = b < p.blocks ? h[b] : 0;
+    for (int i = 0; i < kRun; ++i) c[i] = first + i < p.blocks ? h[first + i] : 0;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) sum += c[i];
+    int32_t inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(kFull, inc, o);
+      if (lane >= o) inc += y;
     }
+    int32_t at = base + inc - sum;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int b = b0 + i * 32 + lane;
-      int32_t inc = c[i];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int32_t y = __shfl_up_sync(kFull, inc, o);
-        if (lane >= o) inc += y;
-      }
-      if (b < p.blocks) h[b] = base + inc - c[i];
-      base += __shfl_sync(kFull, inc, 31);
+    for (int i = 0; i < kRun; ++i) {
+      if (first + i < p.blocks) h[first + i] = at;
+      at += c[i];
     }
+    base += __shfl_sync(kFull, inc, 31);
   }
   if (lane == 0) {
     p.totals[e] = base;

@@ -489,7 +489,7 @@ bsmma_status grouped_int8_gemm(const int8_t* X, const float* sX, const int8_t* W
  *   rows that src marks -1) and dweights[t][j] = sum_h dout[t][h] * Y[pos[t][j]][h] (0 where
  *   pos is -1; not computed, and Y not read, when dweights is NULL).  dout [T][H], Y and dY
  *   [T*k][H] of one type; src and pos moe_plan's.
- * Preconditions: H > 0, rows of 16-byte multiples (H % 8 == 0 in BF16, H % 4 == 0 in FP32),
+ * Preconditions: 0 < H <= 2^24, rows of 16-byte multiples (H % 8 == 0 in BF16, H % 4 == 0 in FP32),
  *   1 <= k <= 32, T >= 0, R and T*k < 2^31, 16-byte-aligned Y, out, dout and dY.  One launch
  *   (none when T == 0).
  */

@@ -118,7 +118,7 @@ def test_grouped_int8_gemm_refusals(lib, args, expect):
 @pytest.mark.parametrize("args,expect", [
     # (Y, dtype, R, H, pos, weights, T, k, out)
     ((FAKE, 0, 8, 12, FAKE, FAKE, 4, 2, FAKE), MISALIGNED), ((FAKE, 1, 8, 6, FAKE, FAKE, 4, 2, FAKE), MISALIGNED),
-    ((FAKE, 0, 8, 0, FAKE, FAKE, 4, 2, FAKE), INVALID), ((FAKE, 0, 8, 16, FAKE, FAKE, 4, 33, FAKE), INVALID),
+    ((FAKE, 0, 8, 0, FAKE, FAKE, 4, 2, FAKE), INVALID), ((FAKE, 0, 8, (1 << 24) + 8, FAKE, FAKE, 4, 2, FAKE), INVALID), ((FAKE, 0, 8, 16, FAKE, FAKE, 4, 33, FAKE), INVALID),
     ((FAKE, 3, 8, 16, FAKE, FAKE, 4, 2, FAKE), INVALID), ((None, 0, 8, 16, FAKE, FAKE, 4, 2, FAKE), INVALID),
     ((FAKE, 0, 8, 16, None, FAKE, 4, 2, FAKE), INVALID), ((ODD, 0, 8, 16, FAKE, FAKE, 4, 2, FAKE), MISALIGNED),
     ((None, 0, 0, 16, None, None, 0, 2, None), 0),

@@ -182,7 +182,8 @@ def test_route_backward_ignores_foreign_ids():
 
 
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (5, 3, 2), (31, 1, 1024), (256, 8, 256), (512, 8, 256), (2049, 1, 7),
-                                   (2050, 2, 1024), (10001, 5, 60)])
+                                   (2050, 2, 1024), (10001, 5, 60),
+                                   (300001, 4, 3)])
 @pytest.mark.parametrize("unused", [0.0, 0.3, 1.0])
 def test_plan(T, k, E, unused):
     g = np.random.default_rng([73, T, k, E])
