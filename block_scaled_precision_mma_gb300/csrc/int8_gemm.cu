@@ -119,9 +119,9 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) int8_quantize_kernel(co
   __shared__ uint32_t part[kThreads / 32];
   const int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / TPR) + threadIdx.x / TPR;
   const int tid = threadIdx.x % TPR;
-  if (r >= p.rows) return;   // whole warps only: TPR < 128 is 32, else one row per block
-  int64_t xr = r;
-  if (p.src) {
+  const bool in = r < p.rows;   // (a warp's other rows may still be)
+  int64_t xr = in ? r : -1;
+  if (p.src && in) {
     const int32_t slot = p.src[r];
     xr = slot < 0 ? -1 : slot / p.k;
     if (xr >= p.x_rows) xr = -1;
@@ -157,7 +157,12 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) int8_quantize_kernel(co
     for (int v = tid; v < p.vecs; v += TPR) fold(x[v]);
   }
   if constexpr (!F32) amax = max(amax << 16, amax & 0xFFFF0000u);
-  amax = __reduce_max_sync(kFull, amax);
+  if constexpr (TPR < 32) {
+#pragma unroll
+    for (int o = TPR / 2; o; o >>= 1) amax = max(amax, __shfl_xor_sync(kFull, amax, o));
+  } else {
+    amax = __reduce_max_sync(kFull, amax);
+  }
   if constexpr (TPR > 32) {
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
     __syncthreads();
@@ -166,6 +171,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) int8_quantize_kernel(co
   }
   float s = __fmul_rn(__uint_as_float(amax), 1.f / 127.f);
   if (s == 0.f) s = 1.f;
+  if (!in) return;
   if (tid == 0) p.scales[r] = s;
   const float inv = s >= 0x1p-88f && s <= 0x1p100f ? __fdiv_rn(1.f, s) : 0.f;
   uint32_t* out = reinterpret_cast<uint32_t*>(p.codes) + r * p.vecs * (kN / 4);
@@ -190,9 +196,15 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) int8_quantize_kernel(co
 
 template <bool F32>
 bsmma_status launch_quantize_t(const QuantParams& p, cudaStream_t stream) {
+  // short rows share a warp, and rows of up to 256 pieces take one warp each (no barrier)
   constexpr int V = 8;
-  if (p.vecs <= 32 * 4)
-    int8_quantize_kernel<F32, 32, 4><<<static_cast<unsigned>((p.rows + 3) / 4), 128, 0, stream>>>(p);
+  const unsigned blocks4 = static_cast<unsigned>((p.rows + 3) / 4);
+  if (p.vecs <= 8 * 4)
+    int8_quantize_kernel<F32, 8, 4><<<static_cast<unsigned>((p.rows + 15) / 16), 128, 0, stream>>>(p);
+  else if (p.vecs <= 32 * 4)
+    int8_quantize_kernel<F32, 32, 4><<<blocks4, 128, 0, stream>>>(p);
+  else if (p.vecs <= 32 * V)
+    int8_quantize_kernel<F32, 32, V><<<blocks4, 128, 0, stream>>>(p);
   else if (p.vecs <= 128 * V)
     int8_quantize_kernel<F32, 128, V><<<static_cast<unsigned>(p.rows), 128, 0, stream>>>(p);
   else if (p.vecs <= 512 * V)
@@ -416,18 +428,18 @@ bsmma_status launch_rows(const Int8Params& p, const DeviceInfo* dev, cudaStream_
 
 // SM cycles that the few-row kernel is expected to take: its units in turn, each the pieces of
 // its slowest warp at 24 bytes a cycle (15.5 with 16 rows) or, where units are short, 1000 a
-// piece and 2600 for the sums and the next unit's start; 5000 for the launch; 15% for uneven
-// groups, some of which take a second block.  It wins where one or two row blocks read B once
-// or B is small: 4 x 14336 x 4096 17 against 23 us on SM-pair tiles, 4 x 4096 x 4096 11 and 21,
-// 32 x 4096 x 4096 17 and 25; but 32 x 14336 x 4096 33 and 21, 128 experts of 1408 x 2048 with 4
-// rows each 109 and 74.
+// piece and 2600 for the sums and the next unit's start; a fifth more for uneven groups, some of
+// which take several blocks; 5000 for the launch.  It wins where one or two row blocks read B
+// once or B is small: 4 x 14336 x 4096 17 against 23 us on SM-pair tiles, 4 x 4096 x 4096 11 and
+// 21, 32 x 4096 x 4096 17 and 25; but 32 x 14336 x 4096 33 and 21, 128 experts of 1408 x 2048 with
+// 4 rows each 109 and 74.
 double rows_cycles(const Int8Params& p, const DeviceInfo* dev) {
   const double active = int8::groups_with_rows(p), rows = active > 0 ? p.total_M / active : 0;
   const int nt = (p.total_M + p.G - 1) / p.G <= 8 ? 1 : 2;
   const double units = int8::blocks_per_group(p, rows, 8 * nt) * active * ((p.N + 31) / 32);
   const double pieces = static_cast<double>((p.K + 1023) / 1024);   // of a warp
   const double unit = std::fmax(pieces * 32 * 1024 / (nt == 1 ? 24 : 15.5), 2600 + 1000 * pieces) + 300;
-  return (std::ceil(units / dev->sm_count) * unit + 5000) * (p.G > 1 ? 1.15 : 1);
+  return std::ceil(units / dev->sm_count) * unit * (p.G > 1 ? 1.2 : 1) + 5000;
 }
 
 }  // namespace

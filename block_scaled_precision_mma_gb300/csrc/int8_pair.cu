@@ -33,6 +33,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "int8.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -71,9 +73,7 @@ struct Cfg {
                                                                       // 144 us for 138 at 64 x
                                                                       // 2048 x 7168, 256 rows)
   static constexpr int kTokSlots = PRE ? (TN > 192 ? (F32 ? 3 : 4) : 5) : kSlots;
-  // output tile: 32 tokens x 128 channels, rows padded so that two rows' halves of the banks
-  // do not meet
-  static constexpr int kOutRow = F32 ? 512 : 256 + 64;
+  static constexpr int kOutRow = F32 ? 512 + 16 : 256 + 64;   // output tile: 32 tokens x 128 channels
   static constexpr int kOutBytes = 32 * kOutRow;
   static constexpr int kTail = 1024 + static_cast<int>(sizeof(Table)) + 512 + 2 * kOutBytes;
   static constexpr int kFit = (232448 - kTail - kTokSlots * kWideBytes) / kRawBytes;
@@ -81,7 +81,8 @@ struct Cfg {
   static constexpr int kSmemBytes = kTail + kTokSlots * kWideBytes + kStages * kRawBytes;
   static_assert((2 * kStages + 2 * kSlots + 5 + (PRE ? 2 * kTokSlots : 0)) * 8 + 8 <= 512,
                 "barriers fit below the group table");
-  static_assert(kStages >= 3 && kSlots % 2 == 0 && 4 * kOutBytes <= kStages * kRawBytes, "shared memory budget");
+  static_assert(kStages >= 3 && kSlots % 2 == 0 && 4 * kOutBytes <= kStages * kRawBytes + kTokSlots * kWideBytes,
+                "shared memory budget");
   static_assert(kBufs * TN + kSlots * kSlotCols <= 512, "tensor memory budget");
 };
 
@@ -268,62 +269,75 @@ __device__ __forceinline__ bool out_agree(bool mine) {
   return all != 0;
 }
 
-// Moves a register array on by one place.
-template <int N>
-__device__ __forceinline__ void rotate(float (&v)[N]) {
-#pragma unroll
-  for (int i = 0; i + 1 < N; ++i) v[i] = v[i + 1];
-}
-
 // 32 tokens (from the unit's token c) of the lane's channel: scaled, turned and stored by a
 // warpgroup.  A lane has a channel's tokens, a row of D wants a token's channels: the tile
 // passes through shared memory ([token][128 channels], two such tiles in turn) and leaves in
-// 16-byte pieces, a token's 128 channels contiguous.  n: the lane's channel; sa: the scale of
-// token c + lane.
+// 16-byte pieces, a token's 128 channels contiguous.  Where rows of D are not 16-byte aligned
+// (N not a multiple of 16 bytes) a token's channels are put at the offset that its row has in
+// D, so that the tile's pieces are D's aligned ones all the same, and the elements before the
+// first and after the last whole one follow by themselves.
+// sa: the scale of token c + lane; sb, bias: the lane's channel's.
 template <bool F32, int ROW>
 __device__ __forceinline__ void emit_tile(const Int8Params& a, const Unit& un, int chan0, int c,
                                           float sa, float sb, float bias, const uint32_t (&r)[32],
                                           uint8_t* tile, int barrier) {
-  const int tid = threadIdx.x & 127, q = tid >> 5, lane = tid & 31;
+  using Elem = typename std::conditional<F32, float, __nv_bfloat16>::type;
+  constexpr int kPer = 16 / sizeof(Elem), kRow = 128 / kPer;
+  const int tid = threadIdx.x & 127;
+  const int64_t at = static_cast<int64_t>(un.row0 + c) * a.N + chan0;
+  const int step = static_cast<int>(a.N & (kPer - 1)), off0 = static_cast<int>(at & (kPer - 1));
+  Elem* mine = reinterpret_cast<Elem*>(tile) + tid;
   float y[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i)
     y[i] = fmaf(__uint_as_float(r[i]), __shfl_sync(kFull, sa, i) * sb, bias);
-  if constexpr (F32) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      *reinterpret_cast<float*>(tile + i * ROW + (q * 32 + lane) * 4) = y[i];
-  } else {
-    // neighbouring lanes pair up their channels: the even one takes the even token
+  if (!F32 && step == 0) {
+    // neighbouring lanes pair up their channels, the even one taking the even token: half the
+    // stores, which share the banks with the MMAs' operands
+    const bool odd = tid & 1;
+    uint8_t* pair = tile + (tid & ~1) * 2 + odd * ROW;
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-      const bool odd = lane & 1;
       const float theirs = __shfl_xor_sync(kFull, odd ? y[i] : y[i + 1], 1);
-      *reinterpret_cast<uint32_t*>(tile + (i + odd) * ROW + (q * 32 + (lane & ~1)) * 2) =
+      *reinterpret_cast<uint32_t*>(pair + i * ROW) =
           odd ? pack_bf16x2(theirs, y[i + 1]) : pack_bf16x2(y[i], theirs);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      store_out<F32>(mine, i * (ROW / static_cast<int>(sizeof(Elem))) + ((off0 + i * step) & (kPer - 1)), y[i]);
   }
   named_barrier_sync(barrier, 128);
   const int tokens = un.rows - c < 32 ? un.rows - c : 32;
-  const int64_t left = a.N - chan0;   // channels of this CTA from its first
-  const int64_t at = static_cast<int64_t>(un.row0 + c) * a.N + chan0;
-  constexpr int kSize = F32 ? 4 : 2, kPer = 16 / kSize, kRow = 128 / kPer;
-  if (a.N % kPer == 0) {              // rows of D are 16-byte aligned
+  const int left = a.N - chan0 < 128 ? static_cast<int>(a.N - chan0) : 128;   // channels here
+  Elem* D = static_cast<Elem*>(a.D) + at;
+  if (step == 0) {
 #pragma unroll
     for (int i = 0; i < 32 * kRow / 128; ++i) {
-      const int e = i * 128 + tid, t = e / kRow, v = e % kRow;
-      if (t < tokens && v * kPer < left)
-        __stcs(reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.D) + (at + t * a.N + v * kPer) * kSize),
-               *reinterpret_cast<const uint4*>(tile + t * ROW + v * 16));
+      const int e = i * 128 + tid, t = e / kRow, v = e % kRow * kPer;
+      if (t < tokens && v < left)
+        __stcs(reinterpret_cast<uint4*>(D + t * a.N + v),
+               *reinterpret_cast<const uint4*>(tile + t * ROW + v * sizeof(Elem)));
     }
-  } else if (tid < left) {
-    for (int t = 0; t < tokens; ++t) {
-      const uint8_t* from = tile + t * ROW + tid * kSize;
-      if constexpr (F32)
-        static_cast<float*>(a.D)[at + t * a.N + tid] = *reinterpret_cast<const float*>(from);
-      else
-        static_cast<__nv_bfloat16*>(a.D)[at + t * a.N + tid] =
-            *reinterpret_cast<const __nv_bfloat16*>(from);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 32 * kRow / 128; ++i) {
+    const int e = i * 128 + tid, t = e / kRow, v = e % kRow * kPer;
+    const int off = (off0 + t * step) & (kPer - 1);
+    if (t < tokens && v >= off && v + kPer <= off + left)
+      __stcs(reinterpret_cast<uint4*>(D + t * a.N + v - off),
+             *reinterpret_cast<const uint4*>(tile + t * ROW + v * sizeof(Elem)));
+  }
+  // four threads a token: the elements of the pieces that its row cuts
+  const int t = tid >> 2, off = (off0 + t * step) & (kPer - 1), end = off + left;
+  const Elem* from = reinterpret_cast<const Elem*>(tile + t * ROW);
+  if (t < tokens) {
+#pragma unroll
+    for (int j = tid & 3; j < kPer; j += 4) {
+      const int tail = (end & ~(kPer - 1)) + j;
+      if (j >= off && j < end && (off > 0 || end < kPer)) D[t * a.N + j - off] = from[j];
+      if (tail >= kPer && tail >= off && tail < end) D[t * a.N + tail - off] = from[tail];
     }
   }
 }
@@ -751,7 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           emit_tile<F32, C::kOutRow>(p.a, un, chan0, c, sa[0], sb, bias, r,
                                      stage_out + flip * C::kOutBytes, kOutBarrier);
           flip ^= 1;
-          rotate(sa);
+#pragma unroll
+          for (int i = 0; i + 1 < TN / 32; ++i) sa[i] = sa[i + 1];
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
@@ -778,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The parts are added in K order, whoever came last.
     named_barrier_sync(kFixBarrier, 384);
     const int wg = (warp - kWideWarp0) >> 2, tid = threadIdx.x & 127;
-    uint8_t* tiles = wg == 2 ? stage_out : raw + wg * 2 * C::kOutBytes;   // the ring is idle now
+    uint8_t* tiles = wg == 2 ? stage_out : raw + wg * 2 * C::kOutBytes;   // the rings are idle now
     uint32_t flip = 0;
     if (table.fixes > 0) __threadfence();
     for (int f = 0; f < table.fixes; ++f) {
@@ -933,8 +948,8 @@ __global__ void __launch_bounds__(256) widen_kernel(const uint4* __restrict__ in
 //     ring is five stages then, and without other blocks that bring the same channels to L2 a
 //     stage waits some 1200 cycles for DRAM.
 //   - A wave of units that leaves pairs idle is split over them when that is shorter; a
-//     split costs 14 to 18 stages (parts written, counted, read back).  Measured at 14336 x
-//     4096, 128 rows: 27 us unsplit, 35 us split, 56 units on 76 pairs.
+//     split costs some 14 stages and more with many parts (written, counted, read back).
+//     Measured at 14336 x 4096, 128 rows: 27 us unsplit, 35 us split, 56 units on 76 pairs.
 //   - Each block reads its channels from DRAM, at 3.3 KB a cycle; FP16 tokens cost a pass over
 //     them first and twice the bytes.
 // At 4096 x 14336 x 4096: 268 us with FP16 tokens (192 columns), 312 us without (256); 64
@@ -953,7 +968,10 @@ double estimate(const Int8Params& a, int tn, bool pre, int pairs) {
   const double ks = static_cast<double>((a.K + 127) / 128);
   const double units = blocks * active * ((a.N + 255) / 256);
   const double full = std::floor(units / pairs), rem = units - full * pairs;
-  const double tail = rem > 0 ? std::fmin(ks, ks * rem / pairs + 18) : 0;
+  // parts of a unit, read back two at a time for each 96 tokens
+  const double parts = rem > 0 ? std::ceil(pairs / rem) + 1 : 0;
+  const double join = 9000 + std::ceil(cols / 96) * std::ceil(parts / 2) * 1300;
+  const double tail = rem > 0 ? std::fmin(ks, ks * rem / pairs + join / stage) : 0;
   const double drain = tn > 192 ? full * 5000 : 0;   // one accumulator: not overlapped
   const double size = static_cast<double>(a.K) * (pre ? 5 : 1);
   const double dram = (blocks * active * a.N * a.K + a.total_M * (size + 2 * a.N)) / 3300;

@@ -353,6 +353,30 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
     }
   }
 
+  if constexpr (V == 1) {
+    // up to 32 experts: every lane counts the keys ahead of its own, which is its place
+    int ahead = 0;
+    for (int j = 0; j < p.E; ++j) {
+      const float other = __shfl_sync(kFull, key[0], j);
+      ahead += other > key[0] || (other == key[0] && j < lane);
+    }
+    const bool chosen = key[0] != -INFINITY && ahead < p.k;
+    float s = 0.f;
+    if (chosen) s = p.sigmoid ? sigmoid(x[0]) : expf(x[0] - mx) / denom;
+    if (p.renormalize) {
+      const float sum = warp_sum(s);
+      s = sum > 0.f ? s / sum : 0.f;
+    }
+    if (chosen) {
+      p.ids[t * p.k + ahead] = lane;
+      p.weights[t * p.k + ahead] = s * p.scale;
+    }
+    if (lane >= __popc(__ballot_sync(kFull, chosen)) && lane < p.k) {
+      p.ids[t * p.k + lane] = -1;
+      p.weights[t * p.k + lane] = 0.f;
+    }
+    return;
+  }
   uint32_t best = 0;    // of the lane's keys, in an order of unsigned integers
   int at = 0;
   float best_x = 0.f;   // its logit
@@ -790,11 +814,20 @@ struct CombineParams {
 // A thread owns one 16-byte piece of one token's output and has up to kUnroll rows' pieces
 // in flight; the sum runs over the token's slots in order.  Bound by DRAM: 8192 tokens of 8
 // rows of 4096 BF16 take 85 us, 604 MB at 7.1 TB/s.
-template <bool F32>
+// PACK: rows of fewer than 128 pieces, threads numbered over (token, piece).
+template <bool F32, bool PACK>
 __global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
   constexpr int kUnroll = 8, kN = Vec<F32>::kN;
-  const int64_t t = blockIdx.x;
-  const int v = blockIdx.y * 128 + threadIdx.x;
+  int64_t t = blockIdx.x;
+  int v = blockIdx.y * 128 + threadIdx.x;
+  if constexpr (PACK) {
+    // (a block's 128 threads begin at piece v0 of token t0, in 64 bits; the rest is in 32)
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * 128, t0 = first / p.vecs;
+    const int e = static_cast<int>(first - t0 * p.vecs) + threadIdx.x, dt = e / p.vecs;
+    t = t0 + dt;
+    v = e - dt * p.vecs;
+    if (t >= p.T) return;
+  }
   if (v >= p.vecs) return;
   const uint4* y = static_cast<const uint4*>(p.y);
   float acc[kN];
@@ -823,16 +856,18 @@ __global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
   static_cast<uint4*>(p.out)[t * p.vecs + v] = pack_vec<F32>(acc);
 }
 
-// One block per token: dY of its rows is w * dout, dw the dot product of dout and the row.
+// THREADS (a block of 256, or a warp for short rows) per token: dY of its rows is w * dout, dw
+// the dot product of dout and the row.
 // The token's dout pieces are read once per kSlots slots.  Four blocks an SM: at the 120
 // registers that ptxas takes by itself two fit, and 8192 x 8 rows of 4096 BF16 took 197 us, not 170 (1.14 GB: 6.7
 // TB/s, DRAM 81% busy).
-template <bool F32>
+template <bool F32, int THREADS>
 __global__ void __launch_bounds__(256, 4) combine_grad_kernel(const CombineParams p) {
   constexpr int kN = Vec<F32>::kN, kSlots = 8;
   __shared__ float part[8][kSlots];
-  const int64_t t = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (256 / THREADS) + threadIdx.x / THREADS;
+  if (t >= p.T) return;   // whole warps, or no block at all
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x % THREADS;
   const uint4* y = static_cast<const uint4*>(p.y);
   const uint4* dout = static_cast<const uint4*>(p.dout) + t * p.vecs;
   uint4* dy = static_cast<uint4*>(p.out);
@@ -847,7 +882,7 @@ __global__ void __launch_bounds__(256, 4) combine_grad_kernel(const CombineParam
       w[u] = r[u] >= 0 ? (p.weights ? p.weights[t * p.k + j] : 1.f) : 0.f;
       dot[u] = 0.f;
     }
-    for (int v = threadIdx.x; v < p.vecs; v += 256) {
+    for (int v = tid; v < p.vecs; v += THREADS) {
       Vec<F32> d;
       d.r = dout[v];
       Vec<F32> x[kSlots];
@@ -871,8 +906,14 @@ __global__ void __launch_bounds__(256, 4) combine_grad_kernel(const CombineParam
 #pragma unroll
       for (int u = 0; u < kSlots; ++u) {
         const float s = warp_sum(dot[u]);
-        if (lane == 0) part[warp][u] = s;
+        if constexpr (THREADS == 32) {
+          if (lane == u && j0 + u < p.k) p.dweights[t * p.k + j0 + u] = s;
+        } else {
+          if (lane == 0) part[warp][u] = s;
+        }
       }
+    }
+    if (THREADS > 32 && p.dweights) {
       __syncthreads();
       if (threadIdx.x < kSlots && j0 + static_cast<int>(threadIdx.x) < p.k) {
         float s = 0.f;
@@ -887,7 +928,7 @@ __global__ void __launch_bounds__(256, 4) combine_grad_kernel(const CombineParam
   for (int j = 0; j < p.k; ++j) {
     const int64_t row = t * p.k + j;
     if (p.src[row] < 0)
-      for (int v = threadIdx.x; v < p.vecs; v += 256) dy[row * p.vecs + v] = make_uint4(0, 0, 0, 0);
+      for (int v = tid; v < p.vecs; v += THREADS) dy[row * p.vecs + v] = make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -1025,10 +1066,17 @@ bsmma_status launch_combine(const void* y, bool f32, int64_t R, int64_t H, const
   p.k = k;
   p.vecs = static_cast<int>(H / (f32 ? 4 : 8));
   const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>((p.vecs + 127) / 128));
-  if (f32)
-    combine_kernel<true><<<grid, 128, 0, stream>>>(p);
-  else
-    combine_kernel<false><<<grid, 128, 0, stream>>>(p);
+  const int64_t packed = (T * p.vecs + 127) / 128;
+  if (p.vecs < 128) {
+    if (f32)
+      combine_kernel<true, true><<<static_cast<unsigned>(packed), 128, 0, stream>>>(p);
+    else
+      combine_kernel<false, true><<<static_cast<unsigned>(packed), 128, 0, stream>>>(p);
+  } else if (f32) {
+    combine_kernel<true, false><<<grid, 128, 0, stream>>>(p);
+  } else {
+    combine_kernel<false, false><<<grid, 128, 0, stream>>>(p);
+  }
   count_launches(1);
   return cuda_ok(cudaGetLastError());
 }
@@ -1049,10 +1097,17 @@ bsmma_status launch_combine_backward(const void* dout, bool f32, int64_t H, cons
   p.R = T * k;
   p.k = k;
   p.vecs = static_cast<int>(H / (f32 ? 4 : 8));
-  if (f32)
-    combine_grad_kernel<true><<<static_cast<unsigned>(T), 256, 0, stream>>>(p);
-  else
-    combine_grad_kernel<false><<<static_cast<unsigned>(T), 256, 0, stream>>>(p);
+  const unsigned warps = static_cast<unsigned>((T + 7) / 8);
+  if (p.vecs <= 128) {
+    if (f32)
+      combine_grad_kernel<true, 32><<<warps, 256, 0, stream>>>(p);
+    else
+      combine_grad_kernel<false, 32><<<warps, 256, 0, stream>>>(p);
+  } else if (f32) {
+    combine_grad_kernel<true, 256><<<static_cast<unsigned>(T), 256, 0, stream>>>(p);
+  } else {
+    combine_grad_kernel<false, 256><<<static_cast<unsigned>(T), 256, 0, stream>>>(p);
+  }
   count_launches(1);
   return cuda_ok(cudaGetLastError());
 }

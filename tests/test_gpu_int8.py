@@ -34,7 +34,8 @@ def rows_of(g, rows, K, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,K", [(1, 16), (9, 48), (130, 512), (33, 1040), (7, 7168), (6, 16400),
-                                    (6, 40000)])
+                                    (6, 40000), (21, 256), (50, 128), (37, 144),
+                                    (19, 1664)])
 def test_quantize_bit_exact(rows, K, dtype):
     x = rows_of(np.random.default_rng([80, rows, K]), rows, K, dtype)
     codes, scales = bs.int8_quantize(x.cuda())

@@ -60,6 +60,8 @@ ROUTES = [
     (17, 96, 3, "sigmoid", False, 32, 1, 1, True, 1.0, "f32", 0.5),
     (12, 32, 4, "softmax", False, 32, 31, 2, True, 1.0, "f32", 0.0),
     (5, 300, 16, "softmax", False, 3, 3, 2, True, 1.0, "f32", 0.95),
+    (1100, 30, 16, "softmax", True, 1, 1, 1, False, 1.0, "f32", 0.6),
+    (6, 32, 16, "sigmoid", True, 4, 2, 2, True, 2.0, "bf16", 0.5),
 ]
 
 
@@ -252,7 +254,8 @@ def order(g, T, k, unused):
 
 COMBINES = [(1, 1, 8, "bf16", 0.0), (1, 1, 4, "f32", 0.0), (7, 3, 1000, "bf16", 0.2),
             (5, 9, 2056, "f32", 0.3), (33, 8, 4096, "bf16", 0.1), (3, 32, 1032, "bf16", 0.0),
-            (64, 2, 72, "f32", 0.5), (4, 8, 264, "bf16", 1.0)]
+            (64, 2, 72, "f32", 0.5), (4, 8, 264, "bf16", 1.0), (301, 3, 88, "bf16", 0.2),
+            (37, 17, 520, "f32", 0.1), (9, 2, 1016, "bf16", 0.0)]
 
 
 @pytest.mark.parametrize("weighted", [True, False])
