@@ -809,63 +809,93 @@ struct CombineParams {
   float* dweights;        // gradient only; may be nullptr
   int64_t T, R;
   int k, vecs;            // 16-byte pieces of a row
+  uint64_t vecs_magic64;  // of short rows, sum only: a * magic >> 64 is a / vecs (a * vecs < 2^64)
+  uint32_t vecs_magic;    // and a * magic >> 32 (a * vecs < 2^32)
 };
 
-// A thread owns one 16-byte piece of one token's output and has up to kUnroll rows' pieces
-// in flight; the sum runs over the token's slots in order.  Bound by DRAM: 8192 tokens of 8
-// rows of 4096 BF16 take 85 us, 604 MB at 7.1 TB/s.
-// PACK: rows of fewer than 128 pieces, threads numbered over (token, piece).
-template <bool F32, bool PACK>
-__global__ void __launch_bounds__(128) combine_kernel(const CombineParams p) {
-  constexpr int kUnroll = 8, kN = Vec<F32>::kN;
-  int64_t t = blockIdx.x;
-  int v = blockIdx.y * 128 + threadIdx.x;
-  if constexpr (PACK) {
-    // (a block's 128 threads begin at piece v0 of token t0, in 64 bits; the rest is in 32)
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * 128, t0 = first / p.vecs;
-    const int e = static_cast<int>(first - t0 * p.vecs) + threadIdx.x, dt = e / p.vecs;
-    t = t0 + dt;
-    v = e - dt * p.vecs;
-    if (t >= p.T) return;
-  }
-  if (v >= p.vecs) return;
-  const uint4* y = static_cast<const uint4*>(p.y);
-  float acc[kN];
+// A thread owns PIECES 16-byte pieces of the output, 128 apart, and has the pieces of SLOTS rows
+// in flight for each; the sum runs over the token's slots in order.  Bound by DRAM where a thread
+// has enough in flight and few enough registers (eight blocks an SM): 8192 tokens of 8 rows of
+// 4096 BF16 take 84 us, 604 MB at 7.2 TB/s (eight slots at once 88; FP32, half the arithmetic a
+// byte, 170 with eight and 174 with four).  One or two slots a token leave room for two pieces:
+// 16384 x 2 rows of 4096 BF16 62 us, 64 with one piece, 70 with four.
+// FLAT: rows of fewer than 512 pieces that would leave threads idle, threads numbered over
+// (token, piece): 65536 x 1 rows of 520 FP32 52 us, 109 with a block a row.
+template <bool F32, bool FLAT, int PIECES, int SLOTS>
+__global__ void __launch_bounds__(128, 8) combine_kernel(const CombineParams p) {
+  constexpr int kSlots = SLOTS, kN = Vec<F32>::kN;
+  int64_t t[PIECES];
+  int v[PIECES];
+  if constexpr (FLAT) {
+    // (a block begins at piece first - t0 * vecs of token t0, in 64 bits; the rest is in 32)
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * (128 * PIECES);
+    const int64_t t0 = __umul64hi(first, p.vecs_magic64);
+    const uint32_t from = static_cast<uint32_t>(first - t0 * p.vecs) + threadIdx.x;
 #pragma unroll
-  for (int i = 0; i < kN; ++i) acc[i] = 0.f;
-  for (int j0 = 0; j0 < p.k; j0 += kUnroll) {
-    Vec<F32> x[kUnroll];
-    float w[kUnroll];
-    bool used[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int j = j0 + u;
-      const int32_t r = j < p.k ? p.pos[t * p.k + j] : -1;
-      used[u] = r >= 0 && r < p.R;
-      if (used[u]) {
-        w[u] = p.weights ? p.weights[t * p.k + j] : 1.f;
-        x[u].r = __ldcs(y + static_cast<int64_t>(r) * p.vecs + v);
-      }
+    for (int q = 0; q < PIECES; ++q) {
+      const uint32_t e = from + q * 128, dt = __umulhi(e, p.vecs_magic);
+      t[q] = t0 + dt;
+      v[q] = static_cast<int>(e - dt * p.vecs);
     }
+  } else {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (used[u])
-#pragma unroll
-        for (int i = 0; i < kN; ++i) acc[i] = fmaf(w[u], x[u].get(i), acc[i]);
+    for (int q = 0; q < PIECES; ++q) {
+      t[q] = blockIdx.x;
+      v[q] = (blockIdx.y * PIECES + q) * 128 + threadIdx.x;
+    }
   }
-  static_cast<uint4*>(p.out)[t * p.vecs + v] = pack_vec<F32>(acc);
+  const uint4* y = static_cast<const uint4*>(p.y);
+  float acc[PIECES][kN];
+#pragma unroll
+  for (int q = 0; q < PIECES; ++q)
+#pragma unroll
+    for (int i = 0; i < kN; ++i) acc[q][i] = 0.f;
+  for (int j0 = 0; j0 < p.k; j0 += kSlots) {
+    Vec<F32> x[PIECES][kSlots];
+    float w[PIECES][kSlots];
+    int32_t r[PIECES][kSlots];
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q)
+#pragma unroll
+      for (int u = 0; u < kSlots; ++u) {
+        const int j = j0 + u;
+        r[q][u] = j < p.k && t[q] < p.T && v[q] < p.vecs ? p.pos[t[q] * p.k + j] : -1;
+        if (r[q][u] >= p.R) r[q][u] = -1;
+      }
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q)
+#pragma unroll
+      for (int u = 0; u < kSlots; ++u)
+        if (r[q][u] >= 0) {
+          w[q][u] = p.weights ? p.weights[t[q] * p.k + j0 + u] : 1.f;
+          x[q][u].r = __ldcs(y + static_cast<int64_t>(r[q][u]) * p.vecs + v[q]);
+        }
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q)
+#pragma unroll
+      for (int u = 0; u < kSlots; ++u)
+        if (r[q][u] >= 0)
+#pragma unroll
+          for (int i = 0; i < kN; ++i) acc[q][i] = fmaf(w[q][u], x[q][u].get(i), acc[q][i]);
+  }
+#pragma unroll
+  for (int q = 0; q < PIECES; ++q)
+    if (t[q] < p.T && v[q] < p.vecs)
+      static_cast<uint4*>(p.out)[t[q] * p.vecs + v[q]] = pack_vec<F32>(acc[q]);
 }
 
-// THREADS (a block of 256, or a warp for short rows) per token: dY of its rows is w * dout, dw
-// the dot product of dout and the row.
-// The token's dout pieces are read once per kSlots slots.  Four blocks an SM: at the 120
-// registers that ptxas takes by itself two fit, and 8192 x 8 rows of 4096 BF16 took 197 us, not 170 (1.14 GB: 6.7
-// TB/s, DRAM 81% busy).
-template <bool F32, int THREADS>
-__global__ void __launch_bounds__(256, 4) combine_grad_kernel(const CombineParams p) {
-  constexpr int kN = Vec<F32>::kN, kSlots = 8;
+// THREADS (a block, or a warp for short rows) per token: dY of its rows is w * dout, dw the dot
+// product of dout and the row.  65536 x 1 rows of 520 FP32: 90 us with 64 threads, 277 with 256.
+// The token's dout pieces are read once per SLOTS slots; with one or two slots two of them are
+// in flight (16384 x 2 rows of 4096 BF16 101 us, 138 with one).  1024 threads an SM: at the 120
+// registers that ptxas takes by itself 512 fit, and 8192 x 8 rows of 4096 BF16 took 197 us, not
+// 170 (1.14 GB: 6.7 TB/s, DRAM 81% busy).
+template <bool F32, int THREADS, int SLOTS>
+__global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS, THREADS == 32 ? 4 : 1024 / THREADS)
+    combine_grad_kernel(const CombineParams p) {
+  constexpr int kN = Vec<F32>::kN, kSlots = SLOTS, kPieces = SLOTS == 2 ? 2 : 1;
   __shared__ float part[8][kSlots];
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (256 / THREADS) + threadIdx.x / THREADS;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (blockDim.x / THREADS) + threadIdx.x / THREADS;
   if (t >= p.T) return;   // whole warps, or no block at all
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x % THREADS;
   const uint4* y = static_cast<const uint4*>(p.y);
@@ -882,25 +912,34 @@ __global__ void __launch_bounds__(256, 4) combine_grad_kernel(const CombineParam
       w[u] = r[u] >= 0 ? (p.weights ? p.weights[t * p.k + j] : 1.f) : 0.f;
       dot[u] = 0.f;
     }
-    for (int v = tid; v < p.vecs; v += THREADS) {
-      Vec<F32> d;
-      d.r = dout[v];
-      Vec<F32> x[kSlots];
-      if (p.dweights)
+    for (int v0 = tid; v0 < p.vecs; v0 += kPieces * THREADS) {
+      Vec<F32> d[kPieces], x[kPieces][kSlots];
+#pragma unroll
+      for (int q = 0; q < kPieces; ++q) {
+        const int v = v0 + q * THREADS;
+        if (v >= p.vecs) break;
+        d[q].r = dout[v];
+        if (p.dweights)
+#pragma unroll
+          for (int u = 0; u < kSlots; ++u)
+            if (r[u] >= 0) x[q][u].r = __ldcs(y + static_cast<int64_t>(r[u]) * p.vecs + v);
+      }
+#pragma unroll
+      for (int q = 0; q < kPieces; ++q) {
+        const int v = v0 + q * THREADS;
+        if (v >= p.vecs) break;
 #pragma unroll
         for (int u = 0; u < kSlots; ++u)
-          if (r[u] >= 0) x[u].r = __ldcs(y + static_cast<int64_t>(r[u]) * p.vecs + v);
+          if (r[u] >= 0) {
+            float o[kN];
 #pragma unroll
-      for (int u = 0; u < kSlots; ++u)
-        if (r[u] >= 0) {
-          float o[kN];
+            for (int i = 0; i < kN; ++i) o[i] = w[u] * d[q].get(i);
+            __stcs(dy + static_cast<int64_t>(r[u]) * p.vecs + v, pack_vec<F32>(o));
+            if (p.dweights)
 #pragma unroll
-          for (int i = 0; i < kN; ++i) o[i] = w[u] * d.get(i);
-          __stcs(dy + static_cast<int64_t>(r[u]) * p.vecs + v, pack_vec<F32>(o));
-          if (p.dweights)
-#pragma unroll
-            for (int i = 0; i < kN; ++i) dot[u] = fmaf(d.get(i), x[u].get(i), dot[u]);
-        }
+              for (int i = 0; i < kN; ++i) dot[u] = fmaf(d[q].get(i), x[q][u].get(i), dot[u]);
+          }
+      }
     }
     if (p.dweights) {
 #pragma unroll
@@ -918,7 +957,7 @@ __global__ void __launch_bounds__(256, 4) combine_grad_kernel(const CombineParam
       if (threadIdx.x < kSlots && j0 + static_cast<int>(threadIdx.x) < p.k) {
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += part[i][threadIdx.x];
+        for (int i = 0; i < THREADS / 32; ++i) s += part[i][threadIdx.x];
         p.dweights[t * p.k + j0 + threadIdx.x] = s;
       }
       __syncthreads();
@@ -980,6 +1019,49 @@ bsmma_status launch_plan_bits(const PlanParams& p, cudaStream_t stream) {
   if (e == cudaSuccess) e = launch_dependent(plan_place_kernel, p.blocks, kPlanThreads, 0, stream, p);
   count_launches(3);
   return cuda_ok(e);
+}
+
+template <bool F32, int PIECES, int SLOTS>
+void launch_combine_p(CombineParams p, cudaStream_t stream) {
+  constexpr int kBlock = 128 * PIECES;
+  if (p.vecs > 1 && p.vecs < 512 && p.vecs % kBlock != 0) {
+    p.vecs_magic64 = ~uint64_t(0) / p.vecs + 1;
+    p.vecs_magic = ~uint32_t(0) / p.vecs + 1;
+    combine_kernel<F32, true, PIECES, SLOTS>
+        <<<static_cast<unsigned>((p.T * p.vecs + kBlock - 1) / kBlock), 128, 0, stream>>>(p);
+  } else {
+    const dim3 grid(static_cast<unsigned>(p.T), static_cast<unsigned>((p.vecs + kBlock - 1) / kBlock));
+    combine_kernel<F32, false, PIECES, SLOTS><<<grid, 128, 0, stream>>>(p);
+  }
+}
+template <bool F32>
+void launch_combine_t(const CombineParams& p, cudaStream_t stream) {
+  if (p.k <= 2)
+    launch_combine_p<F32, 2, 2>(p, stream);
+  else if (p.k <= 4)
+    launch_combine_p<F32, 1, 4>(p, stream);
+  else
+    launch_combine_p<F32, 1, F32 ? 8 : 4>(p, stream);
+}
+
+template <bool F32, int SLOTS>
+void launch_combine_grad_s(const CombineParams& p, cudaStream_t stream) {
+  const unsigned T = static_cast<unsigned>(p.T);
+  if (p.vecs <= 128)
+    combine_grad_kernel<F32, 32, SLOTS><<<(T + 7) / 8, 256, 0, stream>>>(p);
+  else if (p.vecs <= 256)
+    combine_grad_kernel<F32, 64, SLOTS><<<T, 64, 0, stream>>>(p);
+  else if (p.vecs <= 512)
+    combine_grad_kernel<F32, 128, SLOTS><<<T, 128, 0, stream>>>(p);
+  else
+    combine_grad_kernel<F32, 256, SLOTS><<<T, 256, 0, stream>>>(p);
+}
+template <bool F32>
+void launch_combine_grad_t(const CombineParams& p, cudaStream_t stream) {
+  if (p.k <= 2)
+    launch_combine_grad_s<F32, 2>(p, stream);
+  else
+    launch_combine_grad_s<F32, 8>(p, stream);
 }
 
 }  // namespace
@@ -1065,18 +1147,10 @@ bsmma_status launch_combine(const void* y, bool f32, int64_t R, int64_t H, const
   p.R = R;
   p.k = k;
   p.vecs = static_cast<int>(H / (f32 ? 4 : 8));
-  const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>((p.vecs + 127) / 128));
-  const int64_t packed = (T * p.vecs + 127) / 128;
-  if (p.vecs < 128) {
-    if (f32)
-      combine_kernel<true, true><<<static_cast<unsigned>(packed), 128, 0, stream>>>(p);
-    else
-      combine_kernel<false, true><<<static_cast<unsigned>(packed), 128, 0, stream>>>(p);
-  } else if (f32) {
-    combine_kernel<true, false><<<grid, 128, 0, stream>>>(p);
-  } else {
-    combine_kernel<false, false><<<grid, 128, 0, stream>>>(p);
-  }
+  if (f32)
+    launch_combine_t<true>(p, stream);
+  else
+    launch_combine_t<false>(p, stream);
   count_launches(1);
   return cuda_ok(cudaGetLastError());
 }
@@ -1097,17 +1171,10 @@ bsmma_status launch_combine_backward(const void* dout, bool f32, int64_t H, cons
   p.R = T * k;
   p.k = k;
   p.vecs = static_cast<int>(H / (f32 ? 4 : 8));
-  const unsigned warps = static_cast<unsigned>((T + 7) / 8);
-  if (p.vecs <= 128) {
-    if (f32)
-      combine_grad_kernel<true, 32><<<warps, 256, 0, stream>>>(p);
-    else
-      combine_grad_kernel<false, 32><<<warps, 256, 0, stream>>>(p);
-  } else if (f32) {
-    combine_grad_kernel<true, 256><<<static_cast<unsigned>(T), 256, 0, stream>>>(p);
-  } else {
-    combine_grad_kernel<false, 256><<<static_cast<unsigned>(T), 256, 0, stream>>>(p);
-  }
+  if (f32)
+    launch_combine_grad_t<true>(p, stream);
+  else
+    launch_combine_grad_t<false>(p, stream);
   count_launches(1);
   return cuda_ok(cudaGetLastError());
 }
