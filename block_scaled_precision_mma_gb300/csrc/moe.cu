@@ -170,12 +170,21 @@ __global__ void __launch_bounds__(128) route_bf16_kernel(const RouteParams p) {
 // the token's eight.  96 warp instructions a token at 128 experts against 440 for the rounds
 // above: 65536 tokens 13 us against 34, both bound by issuing (56% of the slots; the 21 MB are
 // 3 us).
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
+__device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
 __device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b) {
   const uint32_t hi = max(a, b);
   b = min(a, b);
   a = hi;
 }
-__device__ __forceinline__ void sort8(uint32_t (&v)[8]) {
+__device__ __forceinline__ void exchange(uint64_t& a, uint64_t& b) {
+  const bool swap = b > a;
+  const uint64_t hi = swap ? b : a;
+  b = swap ? a : b;
+  a = hi;
+}
+template <typename Key>
+__device__ __forceinline__ void sort8(Key (&v)[8]) {
   exchange(v[0], v[1]); exchange(v[2], v[3]); exchange(v[4], v[5]); exchange(v[6], v[7]);
   exchange(v[0], v[2]); exchange(v[1], v[3]); exchange(v[4], v[6]); exchange(v[5], v[7]);
   exchange(v[1], v[2]); exchange(v[5], v[6]);
@@ -184,7 +193,8 @@ __device__ __forceinline__ void sort8(uint32_t (&v)[8]) {
   exchange(v[1], v[2]); exchange(v[3], v[4]); exchange(v[5], v[6]);
 }
 // v: first rising then falling or the other way round -> in falling order.
-__device__ __forceinline__ void merge8(uint32_t (&v)[8]) {
+template <typename Key>
+__device__ __forceinline__ void merge8(Key (&v)[8]) {
 #pragma unroll
   for (int d = 4; d; d >>= 1)
 #pragma unroll
@@ -264,7 +274,175 @@ __global__ void __launch_bounds__(128) route_quad_kernel(const RouteParams p) {
     }
 }
 
-// FP32 logits, a bias or groups: 32-bit keys, lane l holding experts 32 i + l.  A decoding
+// FP32 logits, a bias or groups, many tokens: the same with 64-bit keys, a key's 32 bits above the
+// complement of its index, and eight lanes a token.  Each lane's experts belong to one group
+// (1, 2, 4 or 8 of them, whole pieces of eight experts), so that the lanes of a group come to
+// its largest keys, which value it, before the other groups' lists are merged in and a closed
+// group's list is empty.  Bound by the integer pipe (a 64-bit exchange is two compares and four
+// selects): 65536 tokens of 256 experts with a bias and 8 groups 72 us, 105 with a warp a token
+// and rounds; 128 FP32 experts 39 and 52.  16384 tokens 26 and 33; at 8192 both take 19 to 21 and
+// below a token's longer chain shows, so the rounds keep those.
+struct Logits8 {
+  float x[8];
+};
+template <bool F32>
+__device__ __forceinline__ Logits8 load_logits8(const void* logits, int64_t at) {
+  Logits8 r;
+  if constexpr (F32) {
+    const float4* from = reinterpret_cast<const float4*>(static_cast<const float*>(logits) + at);
+    const float4 a = from[0], b = from[1];
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.x[i] = clean_logit(v[i]);
+  } else {
+    const uint4 w4 = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(logits) + at);
+    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      r.x[i] = clean_logit(__uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16));
+  }
+  return r;
+}
+__device__ __forceinline__ float of_key(uint64_t key) {
+  const uint32_t o = static_cast<uint32_t>(key >> 32);
+  return key == 0 ? -INFINITY : __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
+// The eight largest keys of the lane and its partner, o lanes away, in both.
+__device__ __forceinline__ void merge_lanes(uint64_t (&top)[8], int o) {
+  uint64_t v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = larger(top[i], __shfl_xor_sync(kFull, top[7 - i], o));
+  merge8(v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top[i] = v[i];
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(128) route_eight_kernel(const RouteParams p) {
+  const int q = threadIdx.x & 7;
+  const int64_t t_of = (static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x) >> 3;
+  const bool in = t_of < p.T;
+  const int64_t t = in ? t_of : p.T - 1;
+  const int per = p.E / p.groups, share = 8 / p.groups;   // a group's experts and lanes
+  const int g = q / share, e0 = g * per;
+  const int64_t row = t * p.E;
+  auto segment_max = [](float v) {
+#pragma unroll
+    for (int o = 4; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+  };
+  auto segment_sum = [](float v) {
+#pragma unroll
+    for (int o = 4; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+  };
+  float mx = -INFINITY, denom = 1.f;
+  // the scores' denominator, with mx known
+  auto sum_scores = [&] {
+    float sum = 0.f;
+    for (int e = e0 + 8 * (q % share); e < e0 + per; e += 8 * share) {
+      const Logits8 l = load_logits8<F32>(p.logits, row + e);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += expf(l.x[i] - mx);
+    }
+    sum = segment_sum(sum);
+    denom = sum > 0.f ? sum : 1.f;
+  };
+  auto score = [&](float x) { return p.sigmoid ? sigmoid(x) : expf(x - mx) / denom; };
+  const bool values = p.groups > 1 && p.group_top > 1;   // groups by the sum of two scores
+  const bool before = !p.sigmoid && (p.bias || values);
+  if (before) {
+    for (int e = e0 + 8 * (q % share); e < e0 + per; e += 8 * share) {
+      const Logits8 l = load_logits8<F32>(p.logits, row + e);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mx = fmaxf(mx, l.x[i]);
+    }
+    mx = segment_max(mx);
+    if (mx == -INFINITY) mx = 0.f;
+    sum_scores();
+  }
+
+  uint64_t top[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top[i] = 0;
+  for (int e = e0 + 8 * (q % share); e < e0 + per; e += 8 * share) {
+    const Logits8 l = load_logits8<F32>(p.logits, row + e);
+    float bias[8];
+    if (p.bias) {
+      const float4 a = *reinterpret_cast<const float4*>(p.bias + e), b = *reinterpret_cast<const float4*>(p.bias + e + 4);
+      bias[0] = a.x, bias[1] = a.y, bias[2] = a.z, bias[3] = a.w;
+      bias[4] = b.x, bias[5] = b.y, bias[6] = b.z, bias[7] = b.w;
+    }
+    uint64_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float key = l.x[i];
+      if (p.bias && key != -INFINITY) {
+        key = score(key) + bias[i];
+        if (key != key) key = -INFINITY;
+      }
+      v[i] = key == -INFINITY ? 0 : static_cast<uint64_t>(ordered(key)) << 32 | (0xFFFFFFFFu - (e + i));
+    }
+    sort8(v);
+    if (e < e0 + 8 * share) {   // the lane's first
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top[i] = v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top[i] = larger(top[i], v[7 - i]);
+      merge8(top);
+    }
+  }
+  for (int o = 1; o < share; o <<= 1) merge_lanes(top, o);
+  if (p.groups > 1) {
+    // value of a group: the sum of its group_top largest; open when fewer than topk_groups are
+    // ahead of it (ties: lower index first)
+    float value = of_key(top[0]), second = of_key(top[1]);
+    if (values) {
+      if (!p.bias) {
+        if (value != -INFINITY) value = score(value);
+        if (second != -INFINITY) second = score(second);
+      }
+      if (second != -INFINITY) value += second;
+    }
+    int ahead = 0;
+    for (int j = 0; j < p.groups; ++j) {
+      const float v = __shfl_sync(kFull, value, (threadIdx.x & 24) + j * share);
+      ahead += v > value || (v == value && j < g);
+    }
+    if (ahead >= p.topk_groups)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top[i] = 0;
+    for (int o = share; o < 8; o <<= 1) merge_lanes(top, o);
+  }
+
+  // lane q finishes choice q
+  uint64_t c = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i == q && i < p.k) c = top[i];
+  const int id = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(c));
+  float x = -INFINITY;
+  if (c) x = p.bias ? clean_logit(load_elem<F32>(p.logits, row + id)) : of_key(c);
+  if (!p.sigmoid && !before) {
+    // the first choice is the largest logit: without a bias, and with groups valued by their
+    // largest, its group is open
+    mx = segment_max(x);
+    if (mx == -INFINITY) mx = 0.f;
+    if (!p.renormalize) sum_scores();
+  }
+  float s = c ? score(x) : 0.f;
+  if (p.renormalize) {
+    const float sum = segment_sum(s);
+    s = sum > 0.f ? s / sum : 0.f;
+  }
+  if (in && q < p.k) {
+    p.ids[t * p.k + q] = c ? id : -1;
+    p.weights[t * p.k + q] = s * p.scale;
+  }
+}
+
+// FP32 logits, a bias or groups otherwise: 32-bit keys, lane l holding experts 32 i + l.  A decoding
 // step is its chain of latencies: 32 tokens of 256 experts with a bias and groups take 8.3 us
 // a launch, one after another.
 template <bool F32, int V>
@@ -981,6 +1159,9 @@ bsmma_status launch_route_v(const RouteParams& p, cudaStream_t stream) {
   if (!F32 && !p.bias && p.groups == 1 && p.k <= 8 && p.E % 32 == 0 && p.T >= 1024 &&
       (p.sigmoid || p.renormalize)) {
     route_quad_kernel<<<static_cast<unsigned>((p.T + 31) / 32), 128, 0, stream>>>(p);
+  } else if (p.k <= 8 && p.T >= 8192 && p.groups <= 8 && (p.groups & (p.groups - 1)) == 0 &&
+             p.E % (8 * p.groups) == 0 && (reinterpret_cast<uintptr_t>(p.bias) & 15) == 0 && (F32 || p.bias || p.groups > 1)) {
+    route_eight_kernel<F32><<<static_cast<unsigned>((p.T + 15) / 16), 128, 0, stream>>>(p);
   } else if (!F32 && !p.bias && p.groups == 1) {
     if constexpr (V >= 2) {
       if (p.E % 2 == 0)

@@ -62,6 +62,17 @@ ROUTES = [
     (5, 300, 16, "softmax", False, 3, 3, 2, True, 1.0, "f32", 0.95),
     (1100, 30, 16, "softmax", True, 1, 1, 1, False, 1.0, "f32", 0.6),
     (6, 32, 16, "sigmoid", True, 4, 2, 2, True, 2.0, "bf16", 0.5),
+    (8217, 256, 8, "sigmoid", True, 8, 4, 2, True, 2.5, "f32", 0.0),
+    (8223, 256, 8, "sigmoid", True, 8, 4, 2, True, 2.5, "bf16", 0.5),
+    (8222, 64, 6, "softmax", True, 4, 2, 2, False, 1.0, "f32", 0.2),
+    (8216, 128, 8, "softmax", False, 1, 1, 1, True, 1.0, "f32", 0.3),
+    (8216, 384, 7, "softmax", False, 1, 1, 1, False, 1.0, "f32", 0.0),
+    (8218, 48, 5, "sigmoid", False, 2, 1, 2, True, 1.0, "bf16", 0.9),
+    (8219, 1024, 8, "softmax", True, 1, 1, 1, True, 1.0, "f32", 0.0),
+    (8221, 24, 3, "softmax", False, 1, 1, 1, False, 3.0, "f32", 0.95),
+    (8225, 320, 4, "softmax", False, 8, 3, 1, False, 1.0, "bf16", 0.2),
+    (8216, 8, 8, "softmax", False, 1, 1, 1, True, 1.0, "f32", 0.5),
+    (8192, 64, 1, "softmax", False, 8, 1, 2, True, 1.0, "f32", 0.9),
 ]
 
 
@@ -123,6 +134,40 @@ def test_route_masks_and_specials(score, bias):
     assert ids[6][0] == (17 if bias and score == "sigmoid" else 32) and np.all(np.isfinite(w))
     if score == "softmax":
         assert np.allclose(w[3], 1 / 3) and np.allclose(w[4], [0.5, 0.5, 0]) and w[5].tolist() == [1, 0, 0]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("groups,topk_groups,group_top", [(1, 1, 1), (4, 2, 1), (8, 3, 2)])
+@pytest.mark.parametrize("score,bias,E,k", [("softmax", False, 64, 8), ("sigmoid", False, 192, 5),
+                                            ("sigmoid", True, 128, 8), ("sigmoid", True, 1024, 3)])
+def test_route_many_tokens_ties(score, bias, E, k, groups, topk_groups, group_top, dtype):
+    """Few distinct values, so ties in almost every token, of experts and of groups; zeros of
+    both signs, NaN, infinities, closed rows and groups; a NaN in the bias closes its expert."""
+    T = 8209
+    g = np.random.default_rng([79, E, k, groups])
+    x = np.round(g.standard_normal((T, E)) * 4) / 2
+    pick = g.random((T, E))
+    for i, v in enumerate((np.nan, -np.inf, np.inf, -0.0)):
+        x[(pick >= i * 0.02) & (pick < i * 0.02 + 0.02)] = v
+    x[5] = -np.inf
+    x[6] = np.nan
+    x[7] = -0.0
+    x[8, 1:] = -np.inf
+    x[9:60, E // 8:] = -np.inf
+    xt = torch.from_numpy(x).to(DT[dtype])
+    x64 = xt.double().numpy()
+    b = None
+    if bias:
+        b = (g.integers(0, 3, E) * 0.25).astype(np.float32)
+        b[3] = np.nan
+        x64[:, 3] = -np.inf
+    ids, w = bs.moe_route(xt.cuda(), k, score=score, bias=None if b is None else torch.from_numpy(b).cuda(),
+                          groups=groups, topk_groups=topk_groups, group_top=group_top)
+    torch.cuda.synchronize()
+    ids_ref, w_ref = ref.route(x64, k, score, None if b is None else np.nan_to_num(b), groups, topk_groups,
+                               group_top)
+    assert np.array_equal(ids.cpu().numpy(), ids_ref)
+    assert np.all(np.abs(w.cpu().numpy() - w_ref) <= W_TOL * np.abs(w_ref) + 1e-37)
 
 
 @pytest.mark.parametrize("renorm", [True, False])
