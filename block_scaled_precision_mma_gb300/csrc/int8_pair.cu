@@ -75,13 +75,22 @@ struct Cfg {
   static constexpr int kTokSlots = PRE ? (TN > 192 ? (F32 ? 3 : 4) : 5) : kSlots;
   static constexpr int kOutRow = F32 ? 512 + 16 : 256 + 64;   // output tile: 32 tokens x 128 channels
   static constexpr int kOutBytes = 32 * kOutRow;
-  static constexpr int kTail = 1024 + static_cast<int>(sizeof(Table)) + 512 + 2 * kOutBytes;
+  static constexpr int kOutTiles = F32 && TN > 192 && !PRE ? 1 : 2;   // one: room for a fourth stage
+  static constexpr int kTail = 1024 + static_cast<int>(sizeof(Table)) + 512 + kOutTiles * kOutBytes;
   static constexpr int kFit = (232448 - kTail - kTokSlots * kWideBytes) / kRawBytes;
-  static constexpr int kStages = kFit > 12 ? 12 : kFit;
+  static constexpr int kMost = kFit > 12 ? 12 : kFit;
+  // With an odd number of stages a stage goes back and forth between the two widening
+  // warpgroups, and each of them waits for every second load of it.  A wait by parity takes the
+  // load two before for the awaited one while the load between them is still under way, so that
+  // one must be known to have come: it is stage i - kStages when the warpgroup waits for stage
+  // i, and the slot of the warpgroup's last stage, i - 2, was freed by the MMAs of stage
+  // i - 2 - kSlots, which follow those of every stage before.
+  static constexpr int kStages = kMost % 2 == 0 || kMost >= kSlots + 2 ? kMost : kMost - 1;
   static constexpr int kSmemBytes = kTail + kTokSlots * kWideBytes + kStages * kRawBytes;
   static_assert((2 * kStages + 2 * kSlots + 5 + (PRE ? 2 * kTokSlots : 0)) * 8 + 8 <= 512,
                 "barriers fit below the group table");
-  static_assert(kStages >= 3 && kSlots % 2 == 0 && 4 * kOutBytes <= kStages * kRawBytes + kTokSlots * kWideBytes,
+  static_assert(kStages >= 4 && (kStages % 2 == 0 || kStages >= kSlots + 2), "a wait cannot be a load behind");
+  static_assert(kSlots % 2 == 0 && 2 * kOutTiles * kOutBytes <= kStages * kRawBytes + kTokSlots * kWideBytes,
                 "shared memory budget");
   static_assert(kBufs * TN + kSlots * kSlotCols <= 512, "tensor memory budget");
 };
@@ -276,8 +285,9 @@ __device__ __forceinline__ bool out_agree(bool mine) {
 // (N not a multiple of 16 bytes) a token's channels are put at the offset that its row has in
 // D, so that the tile's pieces are D's aligned ones all the same, and the elements before the
 // first and after the last whole one follow by themselves.
+// ONE: a single tile, free when all of the warpgroup have read it.
 // sa: the scale of token c + lane; sb, bias: the lane's channel's.
-template <bool F32, int ROW>
+template <bool F32, int ROW, bool ONE>
 __device__ __forceinline__ void emit_tile(const Int8Params& a, const Unit& un, int chan0, int c,
                                           float sa, float sb, float bias, const uint32_t (&r)[32],
                                           uint8_t* tile, int barrier) {
@@ -291,6 +301,7 @@ __device__ __forceinline__ void emit_tile(const Int8Params& a, const Unit& un, i
 #pragma unroll
   for (int i = 0; i < 32; ++i)
     y[i] = fmaf(__uint_as_float(r[i]), __shfl_sync(kFull, sa, i) * sb, bias);
+  if constexpr (ONE) named_barrier_sync(barrier, 128);
   if (!F32 && step == 0) {
     // neighbouring lanes pair up their channels, the even one taking the even token: half the
     // stores, which share the banks with the MMAs' operands
@@ -360,8 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* raw = smem;
   uint8_t* wide = raw + kStages * C::kRawBytes;
-  uint8_t* stage_out = wide + C::kTokSlots * C::kWideBytes;   // two output tiles
-  uint64_t* full = reinterpret_cast<uint64_t*>(stage_out + 2 * C::kOutBytes);
+  uint8_t* stage_out = wide + C::kTokSlots * C::kWideBytes;   // the output tiles
+  uint64_t* full = reinterpret_cast<uint64_t*>(stage_out + C::kOutTiles * C::kOutBytes);
   uint64_t* empty = full + kStages;
   uint64_t* wide_full = empty + kStages;        // in the leader: widening warps of both CTAs
   uint64_t* wide_empty = wide_full + kSlots;    // in both: the MMAs' commit
@@ -762,9 +773,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) arrive_leader(acc_empty_leader + buf * 8);
         }
         if (whole) {
-          emit_tile<F32, C::kOutRow>(p.a, un, chan0, c, sa[0], sb, bias, r,
-                                     stage_out + flip * C::kOutBytes, kOutBarrier);
-          flip ^= 1;
+          emit_tile<F32, C::kOutRow, C::kOutTiles == 1>(p.a, un, chan0, c, sa[0], sb, bias, r,
+                                                        stage_out + flip * C::kOutBytes, kOutBarrier);
+          flip ^= C::kOutTiles - 1;
 #pragma unroll
           for (int i = 0; i + 1 < TN / 32; ++i) sa[i] = sa[i + 1];
         } else {
@@ -793,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The parts are added in K order, whoever came last.
     named_barrier_sync(kFixBarrier, 384);
     const int wg = (warp - kWideWarp0) >> 2, tid = threadIdx.x & 127;
-    uint8_t* tiles = wg == 2 ? stage_out : raw + wg * 2 * C::kOutBytes;   // the rings are idle now
+    uint8_t* tiles = wg == 2 ? stage_out : raw + wg * C::kOutTiles * C::kOutBytes;   // the rings are idle now
     uint32_t flip = 0;
     if (table.fixes > 0) __threadfence();
     for (int f = 0; f < table.fixes; ++f) {
@@ -828,9 +839,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t r[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(sum[i]);
-        emit_tile<F32, C::kOutRow>(p.a, un, chan0, c, sa, sb, bias, r, tiles + flip * C::kOutBytes,
-                                   kOutBarrier + 2 + wg);
-        flip ^= 1;
+        emit_tile<F32, C::kOutRow, C::kOutTiles == 1>(p.a, un, chan0, c, sa, sb, bias, r,
+                                                      tiles + flip * C::kOutBytes, kOutBarrier + 2 + wg);
+        flip ^= C::kOutTiles - 1;
       }
     }
   }

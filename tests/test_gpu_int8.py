@@ -176,6 +176,18 @@ def test_dense_split_units_are_exact(M, N, K, variant):
     assert np.array_equal(dense(a, one(M), b, one(N)), product(a, b))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_dense_long_sums_repeat(dtype, variant):
+    """Hundreds of stages in a row, many launches: the loads of a ring may come in any order."""
+    g = np.random.default_rng([88])
+    a, b = (torch.from_numpy(g.integers(-15, 16, (n, 13776)).astype(np.int8)).cuda() for n in (1100, 520))
+    ones = [torch.ones(n, device="cuda") for n in (1100, 520)]
+    want = (a.double() @ b.double().T).to(DT[dtype])   # below 2^24: exact before the rounding
+    for _ in range(40):
+        out = bs.int8_gemm(a, ones[0], b, ones[1], dtype=DT[dtype])
+        assert torch.equal(out, want)
+
+
 @pytest.mark.slow
 def test_dense_many_units(variant):
     """More units than SM pairs, with a split remainder, both accumulators in turn."""
