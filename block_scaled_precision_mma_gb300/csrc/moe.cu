@@ -278,8 +278,8 @@ __global__ void __launch_bounds__(128) route_quad_kernel(const RouteParams p) {
 // complement of its index, and eight lanes a token.  Each lane's experts belong to one group
 // (1, 2, 4 or 8 of them, whole pieces of eight experts), so that the lanes of a group come to
 // its largest keys, which value it, before the other groups' lists are merged in and a closed
-// group's list is empty.  Bound by the integer pipe (a 64-bit exchange is two compares and four
-// selects): 65536 tokens of 256 experts with a bias and 8 groups 72 us, 105 with a warp a token
+// group's list is empty.  Bound by issuing, 66% of the slots, most of it to the integer pipe (a
+// 64-bit exchange is two compares and four selects): 65536 tokens of 256 experts with a bias and 8 groups 72 us, 105 with a warp a token
 // and rounds; 128 FP32 experts 39 and 52.  16384 tokens 26 and 33; at 8192 both take 19 to 21 and
 // below a token's longer chain shows, so the rounds keep those.
 struct Logits8 {
