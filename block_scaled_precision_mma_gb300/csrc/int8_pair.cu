@@ -69,28 +69,31 @@ struct Cfg {
   // accumulators, and slots of widened channels in the rest of tensor memory
   static constexpr int kBufs = 2 * TN + 2 * kSlotCols <= 512 ? 2 : 1;
   static constexpr int kFree = (512 - kBufs * TN) / kSlotCols;
-  static constexpr int kSlots = PRE ? (kFree < 4 ? kFree : 4) : 2;   // (three: a shorter ring,
-                                                                      // 144 us for 138 at 64 x
-                                                                      // 2048 x 7168, 256 rows)
-  static constexpr int kTokSlots = PRE ? (TN > 192 ? (F32 ? 3 : 4) : 5) : kSlots;
+  static constexpr int kSlots = kFree < 4 ? kFree : 4;
+  // slots of tokens in shared memory: two without PRE, half as many as of channels, so that a
+  // stage's channels are stored without a wait while the tokens' slot is still being read (64
+  // experts of 2048 x 7168: 192 rows 266 -> 257 us, 256 rows in tiles of 128 383 -> 346)
+  static constexpr int kTokSlots = PRE ? (TN > 192 ? (F32 ? 3 : 4) : 5) : 2;
   static constexpr int kOutRow = F32 ? 512 + 16 : 256 + 64;   // output tile: 32 tokens x 128 channels
   static constexpr int kOutBytes = 32 * kOutRow;
   static constexpr int kOutTiles = F32 && TN > 192 && !PRE ? 1 : 2;   // one: room for a fourth stage
   static constexpr int kTail = 1024 + static_cast<int>(sizeof(Table)) + 512 + kOutTiles * kOutBytes;
   static constexpr int kFit = (232448 - kTail - kTokSlots * kWideBytes) / kRawBytes;
+  // a widening warpgroup waits for the MMAs of as many stages before its own
+  static constexpr int kBehind = PRE ? kSlots : kTokSlots;
   static constexpr int kMost = kFit > 12 ? 12 : kFit;
   // With an odd number of stages a stage goes back and forth between the two widening
   // warpgroups, and each of them waits for every second load of it.  A wait by parity takes the
   // load two before for the awaited one while the load between them is still under way, so that
   // one must be known to have come: it is stage i - kStages when the warpgroup waits for stage
   // i, and the slot of the warpgroup's last stage, i - 2, was freed by the MMAs of stage
-  // i - 2 - kSlots, which follow those of every stage before.
-  static constexpr int kStages = kMost % 2 == 0 || kMost >= kSlots + 2 ? kMost : kMost - 1;
+  // i - 2 - kBehind, which follow those of every stage before.
+  static constexpr int kStages = kMost % 2 == 0 || kMost >= kBehind + 2 ? kMost : kMost - 1;
   static constexpr int kSmemBytes = kTail + kTokSlots * kWideBytes + kStages * kRawBytes;
   static_assert((2 * kStages + 2 * kSlots + 5 + (PRE ? 2 * kTokSlots : 0)) * 8 + 8 <= 512,
                 "barriers fit below the group table");
-  static_assert(kStages >= 4 && (kStages % 2 == 0 || kStages >= kSlots + 2), "a wait cannot be a load behind");
-  static_assert(kSlots % 2 == 0 && 2 * kOutTiles * kOutBytes <= kStages * kRawBytes + kTokSlots * kWideBytes,
+  static_assert(kStages >= 4 && (kStages % 2 == 0 || kStages >= kBehind + 2), "a wait cannot be a load behind");
+  static_assert(kSlots % 2 == 0 && (PRE || (kSlots == 4 && kTokSlots == 2)) && 2 * kOutTiles * kOutBytes <= kStages * kRawBytes + kTokSlots * kWideBytes,
                 "shared memory budget");
   static_assert(kBufs * TN + kSlots * kSlotCols <= 512, "tensor memory budget");
 };
@@ -572,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t b = b_desc + ((PRE ? tok : slot) * C::kWideBytes >> 4);
+            const uint64_t b = b_desc + ((PRE ? tok : slot & 1) * C::kWideBytes >> 4);
             const uint32_t a = tmem_wide + slot * kSlotCols;
             mma_f16_pair_ts(d, a, b, idesc, k != k0);
 #pragma unroll
@@ -616,8 +619,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // number modulo 8)
     const uint32_t chan = static_cast<uint32_t>(tid) * 128 + ((tid & 7) << 4);
     constexpr int kPieces = PRE ? 0 : (C::kHalf + 31) / 32;   // of a half's tokens, a thread
-    // Loads of both halves first, one latency for all; where the registers allow, both halves
-    // are widened before the slot is free, and only the stores are left then.
+    // Loads of both halves first, one latency for all.  With few tokens a thread everything is
+    // in registers then; else the channels are widened and stored half by half.
     constexpr bool kWhole = PRE || kPieces <= 1;
     int stage = wg, slot = wg % kSlots, k_off = wg;
     uint32_t phase = 0, slot_phase = 0;
@@ -660,15 +663,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         const uint32_t base = smem_u32(raw + stage * C::kRawBytes);
-        const uint32_t out = smem_u32(wide + slot * C::kWideBytes);
+        const uint32_t out = smem_u32(wide + (slot & 1) * C::kWideBytes);   // (not with PRE)
         const uint32_t tslot = taddr + slot * kSlotCols;
         const int halves = 2 * k + 1 < p.halves_k ? 2 : 1;
         auto release_stage = [&] {
           __syncwarp();
           if (lane == 0) mbar_arrive(&empty[stage]);
         };
+        // PRE: the channels' slot is free.  Else the tokens' is, once the MMAs of the stage
+        // two back are done; the warpgroup's last stage waited for those of four back, which
+        // had this one's slot of channels.
         auto slot_free = [&] {
-          ok = wait_phase(&wide_empty[slot], slot_phase ^ 1, p.limit_ns, abort_flag, p.a.status);
+          const int of = PRE ? slot : slot ^ 2;
+          const uint32_t parity = PRE || slot < 2 ? slot_phase ^ 1 : slot_phase;
+          ok = wait_phase(&wide_empty[of], parity, p.limit_ns, abort_flag, p.a.status);
           tc_fence_after();
           return ok;
         };
@@ -686,9 +694,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           widen16(c, w);
           widen16(d, y);
           release_stage();
-          if (!slot_free()) break;
+          if (PRE && !slot_free()) break;
           tmem_st32(tslot, w);
           if (halves == 2) tmem_st32(tslot + 32, y);
+          if (!PRE && !slot_free()) {
+            tmem_st_wait();
+            break;
+          }
           if (kPieces > 0 && from[0] != kNone) {
             store_tokens(x[0], out + to[0]);
             store_tokens(x[1], out + C::kWideBytes / 2 + to[0]);
@@ -705,7 +717,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kPieces; ++i)
               if (from[i] != kNone) x[h][i] = lds128(base + (from[i] ^ (h << 6)));
           release_stage();
-          if (!slot_free()) break;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (h == halves) break;
@@ -713,6 +724,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint4 half_c[4] = {c[4 * h], c[4 * h + 1], c[4 * h + 2], c[4 * h + 3]};
             widen16(half_c, w);
             tmem_st32(tslot + h * 32, w);
+          }
+          if (!slot_free()) {
+            tmem_st_wait();
+            break;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h == halves) break;
 #pragma unroll
             for (int i = 0; i < kPieces; ++i)
               if (from[i] != kNone) store_tokens(x[h][i], out + h * (C::kWideBytes / 2) + to[i]);
@@ -953,18 +972,20 @@ __global__ void __launch_bounds__(256) widen_kernel(const uint4* __restrict__ in
 
 // Which tile a launch takes: the cheapest by an estimate in SM cycles that the host makes from
 // the sizes alone.
-//   - A 128-K stage takes about 660 + 2.75 cycles a column with the tokens widened in the
-//     kernel (a fit to 32 to 256 columns, dense and grouped).  With FP16 tokens it takes its
-//     eight MMAs, 9 + 0.5 cycles a column each and 14% more, or the channels' arrival: the
-//     ring is five stages then, and without other blocks that bring the same channels to L2 a
+//   - A 128-K stage with the tokens widened in the kernel takes about 660 + 2.75 cycles a column
+//     in tiles of 32 and 64, 770 + 0.75 in tiles of 128 (two accumulators, half the registers a
+//     thread) and 700 + 2.7 in tiles of 256: fits to 32 to 256 columns, dense and grouped.  With
+//     FP16 tokens it takes its eight MMAs, 9 + 0.5 cycles a column each and 14% more, or the
+//     channels' arrival: the ring is four stages then, and without other blocks that bring the same channels to L2 a
 //     stage waits some 1200 cycles for DRAM.
 //   - A wave of units that leaves pairs idle is split over them when that is shorter; a
-//     split costs some 14 stages and more with many parts (written, counted, read back).
+//     split costs some 18000 cycles and more with many parts (written, counted, read back).
 //     Measured at 14336 x 4096, 128 rows: 27 us unsplit, 35 us split, 56 units on 76 pairs.
 //   - Each block reads its channels from DRAM, at 3.3 KB a cycle; FP16 tokens cost a pass over
 //     them first and twice the bytes.
 // At 4096 x 14336 x 4096: 268 us with FP16 tokens (192 columns), 312 us without (256); 64
-// experts of 2048 x 7168 with 192 rows each: 369 and 289 us.
+// experts of 2048 x 7168 with 192 rows each: 290 and 257 us, in tiles of 128 345; with 96 rows 185
+// in tiles of 128, 207 of 256.
 struct Choice {
   int tn;
   bool pre;
@@ -975,13 +996,15 @@ double estimate(const Int8Params& a, int tn, bool pre, int pairs) {
   const double blocks = blocks_per_group(a, rows, tn);
   const double cols = std::fmax(16, rows / blocks);
   const double stage = pre ? std::fmax(900 + 300 / std::fmax(1, blocks - 1), 8 * 1.14 * (9 + 0.5 * cols))
-                           : 660 + 2.75 * cols;
+                     : tn > 128 ? 700 + 2.7 * cols
+                     : tn > 64  ? 770 + 0.75 * cols
+                                : 660 + 2.75 * cols;
   const double ks = static_cast<double>((a.K + 127) / 128);
   const double units = blocks * active * ((a.N + 255) / 256);
   const double full = std::floor(units / pairs), rem = units - full * pairs;
   // parts of a unit, read back two at a time for each 96 tokens
   const double parts = rem > 0 ? std::ceil(pairs / rem) + 1 : 0;
-  const double join = 9000 + std::ceil(cols / 96) * std::ceil(parts / 2) * 1300;
+  const double join = 18000 + std::ceil(cols / 96) * std::ceil(parts / 2) * 2600;
   const double tail = rem > 0 ? std::fmin(ks, ks * rem / pairs + join / stage) : 0;
   const double drain = tn > 192 ? full * 5000 : 0;   // one accumulator: not overlapped
   const double size = static_cast<double>(a.K) * (pre ? 5 : 1);
