@@ -12,6 +12,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <deque>
 #include <mutex>
 #include <vector>
 
@@ -65,6 +66,15 @@ std::vector<SplitWorkspace> g_sws;
 // Buffers replaced by a larger one after a graph capture used them: a replay of that
 // graph still reads and writes them, so they stay allocated until the process exits.
 std::vector<void*> g_ws_kept;
+// One mutex for each (device, stream) that has used a workspace (StreamLock).  A deque: they
+// stay where they are.
+struct StreamMutex {
+  int device;
+  cudaStream_t stream;
+  std::mutex mu;
+  StreamMutex(int d, cudaStream_t s) : device(d), stream(s) {}
+};
+std::deque<StreamMutex> g_stream_mu;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -239,6 +249,19 @@ int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
 }  // namespace
 
+StreamLock::StreamLock(cudaStream_t stream) {
+  int dev = -1;
+  cudaGetDevice(&dev);   // (a failure is the lookup's to report)
+  std::mutex* mu = nullptr;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    for (auto& e : g_stream_mu)
+      if (e.device == dev && e.stream == stream) mu = &e.mu;
+    if (!mu) mu = &g_stream_mu.emplace_back(dev, stream).mu;
+  }
+  lk_ = std::unique_lock<std::mutex>(*mu);
+}
+
 bsmma_status stream_workspace(int64_t bytes, cudaStream_t stream, void** out) {
   return get_workspace(bytes, stream, out);
 }
@@ -380,6 +403,7 @@ bsmma_status mx_gemm(const void* A, const uint8_t* sA, const void* B, const uint
   if (K == 0) return cuda_ok(cudaMemsetAsync(D, 0, static_cast<size_t>(M * N * 2), s));
   const int64_t bytes_a = align_up(wide_scale_bytes(M, K / 32, 0), 256);
   const int64_t bytes_b = wide_scale_bytes(N, K / 32, 1);
+  const StreamLock lock(s);
   void* ws = nullptr;
   st = get_workspace(bytes_a + bytes_b, s, &ws);
   if (st != BSMMA_OK) return st;
@@ -416,6 +440,7 @@ bsmma_status mx_gemm_bias_act(const void* A, const uint8_t* sA, const void* B, c
   if (K == 0) return zero_k_epilogue(bias, act, D, M, N, s);
   const int64_t bytes_a = align_up(wide_scale_bytes(M, K / 32, 0), 256);
   const int64_t bytes_b = wide_scale_bytes(N, K / 32, 1);
+  const StreamLock lock(s);
   void* ws = nullptr;
   st = get_workspace(bytes_a + bytes_b, s, &ws);
   if (st != BSMMA_OK) return st;
@@ -595,12 +620,12 @@ bsmma_status moe_plan(const int32_t* ids, int64_t T, int k, int E, int64_t* m_si
   if (T == 0) return cuda_ok(cudaMemsetAsync(m_sizes, 0, static_cast<size_t>(E) * 8, s));
   if (!ids || !src || !pos) return BSMMA_ERR_INVALID_ARG;
   if (!aligned_to(ids, 4) || !aligned_to(src, 4) || !aligned_to(pos, 4)) return BSMMA_ERR_MISALIGNED;
-  void* ws = nullptr;
   const int64_t bytes = plan_workspace_bytes(T * k, E);
-  if (bytes > 0) {
-    const bsmma_status st = get_workspace(bytes, s, &ws);
-    if (st != BSMMA_OK) return st;
-  }
+  if (bytes == 0) return launch_plan(ids, T * k, E, m_sizes, src, pos, nullptr, s);
+  const StreamLock lock(s);
+  void* ws = nullptr;
+  const bsmma_status st = get_workspace(bytes, s, &ws);
+  if (st != BSMMA_OK) return st;
   return launch_plan(ids, T * k, E, m_sizes, src, pos, ws, s);
 }
 
@@ -687,6 +712,7 @@ bsmma_status moe_combine_backward(const void* dout, bsmma_dtype dtype, int64_t H
 
 bsmma_status bsmma_reserve_workspace(int64_t bytes, bsmma_stream stream) {
   if (bytes < 0) return BSMMA_ERR_INVALID_ARG;
+  const StreamLock lock(reinterpret_cast<cudaStream_t>(stream));
   void* p = nullptr;
   bsmma_status st = get_workspace(bytes, reinterpret_cast<cudaStream_t>(stream), &p);
   if (st != BSMMA_OK) return st;

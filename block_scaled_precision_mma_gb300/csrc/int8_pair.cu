@@ -33,6 +33,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <optional>
 #include <type_traits>
 
 #include "int8.cuh"
@@ -1039,7 +1040,9 @@ bsmma_status launch_pair(const Int8Params& a, bool f32, const DeviceInfo* dev, c
   Choice c = int8_tile() > 1 ? Choice{int8_tile(), int8_fp16_tokens()} : choose(a, dev->sm_count / 2);
   if (a.total_M == 0) c = Choice{32, false};   // no rows to widen; the sizes are still checked
   void* tok16 = nullptr;
+  std::optional<StreamLock> lock;   // from the widened tokens' lookup to the products
   if (c.pre) {
+    lock.emplace(stream);
     // captured without a workspace, or no memory for one, or rows of more bytes than a copy's
     // coordinate counts: widened in the kernel
     const bsmma_status st = a.K < (int64_t(1) << 30) ? stream_workspace(a.total_M * a.K * 2, stream, &tok16)

@@ -5,6 +5,7 @@
 
 #include <cstdint>
 #include <functional>
+#include <mutex>
 #include <string>
 #include <vector>
 
@@ -52,6 +53,18 @@ int64_t wide_scale_bytes(int64_t rows, int64_t kblocks, int role);
 bsmma_status launch_wide_relayout(const uint8_t* sa, int64_t rows_a, uint8_t* out_a,
                                   const uint8_t* sb, int64_t rows_b, uint8_t* out_b,
                                   int64_t kblocks, cudaStream_t stream);
+
+// Held from the lookup of the (current device, stream) workspace to the last launch that uses
+// it.  A call passes data from one launch to the next through the workspace; calls on a stream
+// run in the order of their launches, so with another host thread's launches between a call's own
+// it would read that thread's data, and growing the workspace in between would free it.
+class StreamLock {
+ public:
+  explicit StreamLock(cudaStream_t stream);
+
+ private:
+  std::unique_lock<std::mutex> lk_;
+};
 
 // The (current device, stream) workspace, grown to at least `bytes` (BSMMA_ERR_WORKSPACE
 // during a capture that would have to grow it).

@@ -62,6 +62,7 @@ bsmma_status mx_gemm_noalloc(const void* A, const uint8_t* sA, const void* B, co
   uint8_t* scratch = nullptr;
   st = noalloc_scratch(&scratch);
   if (st != BSMMA_OK) return st;
+  const StreamLock lock(s);   // both launches before another thread's on this stream
   // every byte of both tiled buffers (padding included) is rewritten here, so the
   // previous call's contents never leak into this one
   st = launch_wide_relayout(sA, M, scratch, sB, N, scratch + bytes_a, K / 32, s);

@@ -29,7 +29,9 @@
  *     are detected on the host before any launch and leave D untouched.  Errors
  *     detected on the device (a timed-out wait, inconsistent m_sizes) are latched
  *     in a per-device status word that bsmma_device_status reads and clears.
- *   - Entry points may be called from several host threads.
+ *   - Entry points may be called from several host threads, also on one stream: a call
+ *     that passes data between its launches through the stream's workspace enqueues all
+ *     of them before another thread's call on that stream.
  */
 #ifndef BSMMA_H
 #define BSMMA_H
