@@ -28,7 +28,6 @@ __device__ int g_device_status;
 
 namespace {
 
-constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 DeviceInfo g_dev[kMaxDevices];
 bool g_dev_ready[kMaxDevices];

@@ -507,34 +507,32 @@ __global__ void __launch_bounds__(PCfg::kThreads, 1)
 }
 
 bsmma_status launch_bf16_pair(const CUtensorMap& tx, const CUtensorMap& tw, Bf16Params p,
-                              int64_t total_M, int G, cudaStream_t stream) {
+                              int64_t total_M, int G, const DeviceInfo* dev, cudaStream_t stream) {
   using C = PCfg;
   p.num_n_tiles = static_cast<int>((p.N + 255) / 256);
   p.idesc = idesc_bf16(256, 256);
-  static int max_clusters = -1;   // benign race: every thread computes the same value
-  if (max_clusters < 0) {
+  static PerDevice clusters_fit;
+  int max_clusters = 0;
+  const bsmma_status st = clusters_fit.get(dev->device, &max_clusters, [&](int* fit) {
     if (cudaFuncSetAttribute(grouped_bf16_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::kSmemBytes) != cudaSuccess)
       return BSMMA_ERR_CUDA;
-    int dev = 0, sms = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(2 * sms, 1, 1);
+    cfg.gridDim = dim3(2 * dev->sm_count, 1, 1);
     cfg.blockDim = dim3(C::kThreads, 1, 1);
     cfg.dynamicSmemBytes = C::kSmemBytes;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, grouped_bf16_pair_kernel, &cfg) != cudaSuccess || n < 1)
+    if (cudaOccupancyMaxActiveClusters(fit, grouped_bf16_pair_kernel, &cfg) != cudaSuccess || *fit < 1)
       return BSMMA_ERR_CUDA;
-    max_clusters = n;
-  }
+    return BSMMA_OK;
+  });
+  if (st != BSMMA_OK) return st;
   const int64_t bound = ((total_M + 255) / 256 + G) * p.num_n_tiles;
   int64_t clusters = bound < max_clusters ? bound : max_clusters;
   if (clusters < 1) clusters = 1;
@@ -557,20 +555,16 @@ bsmma_status launch_bf16_pair(const CUtensorMap& tx, const CUtensorMap& tw, Bf16
 
 template <int BN>
 bsmma_status launch_bf16_bn(const CUtensorMap& tx, const CUtensorMap& tw, Bf16Params p,
-                            int64_t total_M, int G, int sm_count, cudaStream_t stream) {
+                            int64_t total_M, int G, const DeviceInfo* dev, cudaStream_t stream) {
   using C = BCfg<BN>;
   p.num_n_tiles = static_cast<int>((p.N + BN - 1) / BN);
   p.idesc = idesc_bf16(kBM, BN);
   const int64_t bound = ((total_M + kBM - 1) / kBM + G) * p.num_n_tiles;
-  int64_t grid = bound < sm_count ? bound : sm_count;
+  int64_t grid = bound < dev->sm_count ? bound : dev->sm_count;
   if (grid < 1) grid = 1;
-  static bool attr_set = false;   // benign race: setting the attribute twice is harmless
-  if (!attr_set) {
-    if (cudaFuncSetAttribute(grouped_bf16_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::kSmemBytes) != cudaSuccess)
-      return BSMMA_ERR_CUDA;
-    attr_set = true;
-  }
+  static PerDevice ready;
+  const bsmma_status st = ready.allow_smem(dev->device, grouped_bf16_kernel<BN>, C::kSmemBytes);
+  if (st != BSMMA_OK) return st;
   grouped_bf16_kernel<BN><<<static_cast<int>(grid), C::kThreads, C::kSmemBytes, stream>>>(tx, tw, p);
   count_launches(1);
   return cuda_ok(cudaGetLastError());
@@ -602,9 +596,9 @@ bsmma_status launch_bf16_width(const void* X, const void* W, void* D, const int6
   p.num_kb = static_cast<int>((K + 63) / 64);
   p.status = dev->status;
   p.limit_ns = wait_limit_ns();
-  if (bn == kPairTile) return launch_bf16_pair(tx, tw, p, total_M, G, stream);
-  if (bn == 256) return launch_bf16_bn<256>(tx, tw, p, total_M, G, dev->sm_count, stream);
-  return launch_bf16_bn<128>(tx, tw, p, total_M, G, dev->sm_count, stream);
+  if (bn == kPairTile) return launch_bf16_pair(tx, tw, p, total_M, G, dev, stream);
+  if (bn == 256) return launch_bf16_bn<256>(tx, tw, p, total_M, G, dev, stream);
+  return launch_bf16_bn<128>(tx, tw, p, total_M, G, dev, stream);
 }
 
 }  // namespace

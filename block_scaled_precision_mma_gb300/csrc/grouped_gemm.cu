@@ -383,20 +383,16 @@ __global__ void __launch_bounds__(384, 1)
 
 template <int BN, bool PACKED>
 bsmma_status launch_grouped_bn(const CUtensorMap& tx, const CUtensorMap& tw, GroupedParams p,
-                               int64_t total_M, int G, int sm_count, cudaStream_t stream) {
+                               int64_t total_M, int G, const DeviceInfo* dev, cudaStream_t stream) {
   using C = GCfg<BN>;
   p.num_n_tiles = static_cast<int>(p.N / BN);
   p.idesc = idesc_f8f6f4(0, 0, 0, 0, kBM, BN);
   const int64_t bound = ((total_M + kBM - 1) / kBM + G) * p.num_n_tiles;
-  int64_t grid = bound < sm_count ? bound : sm_count;
+  int64_t grid = bound < dev->sm_count ? bound : dev->sm_count;
   if (grid < 1) grid = 1;
-  static bool attr_set = false;   // benign race: setting the attribute twice is harmless
-  if (!attr_set) {
-    if (cudaFuncSetAttribute(grouped_fp8_kernel<BN, PACKED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::kSmemBytes) != cudaSuccess)
-      return BSMMA_ERR_CUDA;
-    attr_set = true;
-  }
+  static PerDevice ready;
+  const bsmma_status st = ready.allow_smem(dev->device, grouped_fp8_kernel<BN, PACKED>, C::kSmemBytes);
+  if (st != BSMMA_OK) return st;
   grouped_fp8_kernel<BN, PACKED><<<static_cast<int>(grid), C::kThreads, C::kSmemBytes, stream>>>(tx, tw, p);
   count_launches(1);
   return cuda_ok(cudaGetLastError());
@@ -502,11 +498,11 @@ bsmma_status launch_grouped_width(const uint8_t* X, const float* sX, const uint8
   p.status = dev->status;
   p.limit_ns = wait_limit_ns();
   if (packed) {
-    if (bn == 256) return launch_grouped_bn<256, true>(tx, tw, p, total_M, G, dev->sm_count, stream);
-    return launch_grouped_bn<128, true>(tx, tw, p, total_M, G, dev->sm_count, stream);
+    if (bn == 256) return launch_grouped_bn<256, true>(tx, tw, p, total_M, G, dev, stream);
+    return launch_grouped_bn<128, true>(tx, tw, p, total_M, G, dev, stream);
   }
-  if (bn == 256) return launch_grouped_bn<256, false>(tx, tw, p, total_M, G, dev->sm_count, stream);
-  return launch_grouped_bn<128, false>(tx, tw, p, total_M, G, dev->sm_count, stream);
+  if (bn == 256) return launch_grouped_bn<256, false>(tx, tw, p, total_M, G, dev, stream);
+  return launch_grouped_bn<128, false>(tx, tw, p, total_M, G, dev, stream);
 }
 }  // namespace
 

@@ -409,13 +409,9 @@ __global__ void __launch_bounds__(256, 1) int8_rows_kernel(const Int8Params p) {
 template <int NT, bool F32>
 bsmma_status launch_rows(const Int8Params& p, const DeviceInfo* dev, cudaStream_t stream) {
   using C = RowsCfg<NT>;
-  static bool attr_set = false;   // benign race: setting the attribute twice is harmless
-  if (!attr_set) {
-    if (cudaFuncSetAttribute(int8_rows_kernel<NT, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::kSmemBytes) != cudaSuccess)
-      return BSMMA_ERR_CUDA;
-    attr_set = true;
-  }
+  static PerDevice ready;
+  const bsmma_status st = ready.allow_smem(dev->device, int8_rows_kernel<NT, F32>, C::kSmemBytes);
+  if (st != BSMMA_OK) return st;
   int64_t blocks = (p.total_M + 8 * NT - 1) / (8 * NT);
   if (p.m_sizes) blocks += p.G < p.total_M ? p.G : p.total_M;
   if (blocks < 1) blocks = 1;   // the sizes are still checked

@@ -881,7 +881,7 @@ template <int TN, bool PRE, bool F32>
 bsmma_status launch_tn(PairParams p, const void* tok16, const DeviceInfo* dev, cudaStream_t stream) {
   using C = Cfg<TN, PRE, F32>;
   auto kern = int8_pair_kernel<TN, PRE, F32>;
-  static int max_clusters = -1;   // benign race: every thread computes the same value
+  static PerDevice clusters_fit;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -894,18 +894,20 @@ bsmma_status launch_tn(PairParams p, const void* tok16, const DeviceInfo* dev, c
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (max_clusters < 0) {
+  int max_clusters = 0;
+  bsmma_status st = clusters_fit.get(dev->device, &max_clusters, [&](int* fit) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) !=
         cudaSuccess)
       return BSMMA_ERR_CUDA;
     cfg.gridDim = dim3(2 * (dev->sm_count / 2), 1, 1);
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) return BSMMA_ERR_CUDA;
-    max_clusters = n < dev->sm_count / 2 ? n : dev->sm_count / 2;
-  }
+    if (cudaOccupancyMaxActiveClusters(fit, kern, &cfg) != cudaSuccess || *fit < 1) return BSMMA_ERR_CUDA;
+    if (*fit > dev->sm_count / 2) *fit = dev->sm_count / 2;
+    return BSMMA_OK;
+  });
+  if (st != BSMMA_OK) return st;
   CUtensorMap tb, ta8, ta32, tall;
   const Int8Params& a = p.a;
-  bsmma_status st = encode_tmap_u8(&tb, a.B, a.K, static_cast<uint64_t>(a.G) * a.N, a.K, 128, 128);
+  st = encode_tmap_u8(&tb, a.B, a.K, static_cast<uint64_t>(a.G) * a.N, a.K, 128, 128);
   if (st != BSMMA_OK) return st;
   // with no rows there is no tile of A to load; B's address stands in for the map
   const void* A = a.total_M > 0 ? (PRE ? tok16 : a.A) : a.B;

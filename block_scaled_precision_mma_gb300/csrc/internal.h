@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <functional>
 #include <mutex>
@@ -12,6 +13,41 @@
 #include "bsmma.h"
 
 namespace bsmma {
+
+constexpr int kMaxDevices = 64;
+
+// What setting a kernel up left on each device: CUDA keeps a kernel's attributes, and how many
+// of its blocks or clusters fit, per device, so a process that uses a second one sets up again.
+class PerDevice {
+ public:
+  // The value (not 0) on `device`: `set_up(&value)` makes it at the first call there.  (Two
+  // threads may both do so, to the same effect.)
+  template <typename SetUp>
+  bsmma_status get(int device, int* value, SetUp set_up) {
+    int v = v_[device].load(std::memory_order_acquire);
+    if (v == 0) {
+      const bsmma_status st = set_up(&v);
+      if (st != BSMMA_OK) return st;
+      v_[device].store(v, std::memory_order_release);
+    }
+    *value = v;
+    return BSMMA_OK;
+  }
+  // Lets `kern` launch with `bytes` of dynamic shared memory on `device`.
+  template <typename Kern>
+  bsmma_status allow_smem(int device, Kern* kern, int bytes) {
+    int v = 0;
+    return get(device, &v, [&](int* done) {
+      *done = 1;
+      return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess
+                 ? BSMMA_OK
+                 : BSMMA_ERR_CUDA;
+    });
+  }
+
+ private:
+  std::atomic<int> v_[kMaxDevices] = {};
+};
 
 // Per-device facts the launchers need.
 struct DeviceInfo {

@@ -344,19 +344,15 @@ __global__ void __maxnreg__(168)
 
 template <bool FP4, bool A_MN, bool B_MN, bool EPI>
 bsmma_status launch_dense(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tsa,
-                          const CUtensorMap& tsb, const DenseParams& p, int sm_count,
+                          const CUtensorMap& tsb, const DenseParams& p, const DeviceInfo* dev,
                           cudaStream_t stream) {
   using C = Cfg<FP4>;
   auto kern = mx_gemm_kernel<FP4, A_MN, B_MN, EPI>;
-  static bool attr_set = false;   // benign race: setting the attribute twice is harmless
-  if (!attr_set) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) !=
-        cudaSuccess)
-      return BSMMA_ERR_CUDA;
-    attr_set = true;
-  }
+  static PerDevice ready;
+  const bsmma_status st = ready.allow_smem(dev->device, kern, C::kSmemBytes);
+  if (st != BSMMA_OK) return st;
   const int64_t units = static_cast<int64_t>(p.num_m_tiles) * p.num_n_tiles;
-  const int grid = static_cast<int>(units < sm_count ? units : sm_count);
+  const int grid = static_cast<int>(units < dev->sm_count ? units : dev->sm_count);
   kern<<<grid, kThreads, C::kSmemBytes, stream>>>(ta, tb, tsa, tsb, p);
   count_launches(1);
   return cuda_ok(cudaGetLastError());
@@ -447,11 +443,10 @@ bsmma_status launch_mx_gemm_variant(const void* A, const uint8_t* sfa, const voi
   p.idesc = idesc_block_scaled(af, bf, layout == BSMMA_TN, layout != BSMMA_NT, kBM, kBN);
   p.status = dev->status;
   p.limit_ns = wait_limit_ns();
-  const int sms = dev->sm_count;
   const bool epi = bias != nullptr || act != 0;
 #define BSMMA_DENSE(F, A, B)                                                     \
-  (epi ? launch_dense<F, A, B, true>(ta, tb, tsa, tsb, p, sms, stream)           \
-       : launch_dense<F, A, B, false>(ta, tb, tsa, tsb, p, sms, stream))
+  (epi ? launch_dense<F, A, B, true>(ta, tb, tsa, tsb, p, dev, stream)           \
+       : launch_dense<F, A, B, false>(ta, tb, tsa, tsb, p, dev, stream))
   if (fp4) return BSMMA_DENSE(true, false, false);
   switch (layout) {
     case BSMMA_NT: return BSMMA_DENSE(false, false, false);

@@ -465,33 +465,31 @@ __global__ void __maxnreg__(168)
 template <bool FP4, bool A_MN, bool B_MN, int EPI>
 bsmma_status launch_2sm(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tsa,
                         const CUtensorMap& tsb, const CUtensorMap& td, const Pair2Params& p,
-                        cudaStream_t stream) {
+                        const DeviceInfo* dev, cudaStream_t stream) {
   using C = Cfg2<FP4>;
   auto kern = mx_gemm_2sm_kernel<FP4, A_MN, B_MN, EPI>;
-  static int max_clusters = -1;   // benign race: every thread computes the same value
-  if (max_clusters < 0) {
+  static PerDevice clusters_fit;
+  int max_clusters = 0;
+  const bsmma_status st = clusters_fit.get(dev->device, &max_clusters, [&](int* fit) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) !=
         cudaSuccess)
       return BSMMA_ERR_CUDA;
-    int dev = 0, sms = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(2 * sms, 1, 1);
+    cfg.gridDim = dim3(2 * dev->sm_count, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = C::kSmemBytes;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1)
+    if (cudaOccupancyMaxActiveClusters(fit, kern, &cfg) != cudaSuccess || *fit < 1)
       return BSMMA_ERR_CUDA;
-    max_clusters = n;
-  }
+    return BSMMA_OK;
+  });
+  if (st != BSMMA_OK) return st;
   const int64_t units = static_cast<int64_t>(p.num_unit_rows) * p.num_n_tiles;
   const int grid = static_cast<int>(2 * (units < max_clusters ? units : max_clusters));
   cudaLaunchConfig_t cfg = {};
@@ -572,11 +570,11 @@ bsmma_status launch_mx_gemm_2sm(const void* A, const uint8_t* sfa, const void* B
   // output stage: 0 plain, else 1 + the activation (bias applied when given)
   const int epi = bias == nullptr && act == 0 ? 0 : 1 + act;
 #define BSMMA_2SM(F, A, B)                                                       \
-  (epi == 0   ? launch_2sm<F, A, B, 0>(ta, tb, tsa, tsb, td, p, stream)          \
-   : epi == 1 ? launch_2sm<F, A, B, 1>(ta, tb, tsa, tsb, td, p, stream)          \
-   : epi == 2 ? launch_2sm<F, A, B, 2>(ta, tb, tsa, tsb, td, p, stream)          \
-   : epi == 3 ? launch_2sm<F, A, B, 3>(ta, tb, tsa, tsb, td, p, stream)          \
-              : launch_2sm<F, A, B, 4>(ta, tb, tsa, tsb, td, p, stream))
+  (epi == 0   ? launch_2sm<F, A, B, 0>(ta, tb, tsa, tsb, td, p, dev, stream)     \
+   : epi == 1 ? launch_2sm<F, A, B, 1>(ta, tb, tsa, tsb, td, p, dev, stream)     \
+   : epi == 2 ? launch_2sm<F, A, B, 2>(ta, tb, tsa, tsb, td, p, dev, stream)     \
+   : epi == 3 ? launch_2sm<F, A, B, 3>(ta, tb, tsa, tsb, td, p, dev, stream)     \
+              : launch_2sm<F, A, B, 4>(ta, tb, tsa, tsb, td, p, dev, stream))
   if (fp4) return BSMMA_2SM(true, false, false);
   switch (layout) {
     case BSMMA_NT: return BSMMA_2SM(false, false, false);

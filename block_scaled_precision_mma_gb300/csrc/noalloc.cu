@@ -17,7 +17,6 @@ namespace bsmma {
 namespace {
 
 constexpr int64_t kNoAllocScratchBytes = BSMMA_NOALLOC_SCRATCH_BYTES;
-constexpr int kMaxDevices = 64;
 
 // Scratch shared by every mx_gemm_noalloc call on a device; it lives as long as
 // the library is loaded, on every device that loads it.

@@ -602,19 +602,18 @@ bsmma_status encode_words(CUtensorMap* map, const void* base, int rank, const ui
 }
 
 // Resident CTAs per SM of a ring kernel (its ring takes much of shared memory); sets the
-// kernel's dynamic shared-memory limit on first use.  0 on failure.
+// kernel's dynamic shared-memory limit on the device's first use.  0 on failure.
 template <auto Kern>
-int ring_ctas_per_sm(int threads, int smem) {
-  static int n = -1;   // one per kernel; benign race: every thread computes the same value
-  if (n < 0) {
-    int k = 0;
-    if (cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-            cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&k, Kern, threads, smem) != cudaSuccess)
-      return 0;
-    n = k;
-  }
-  return n;
+int ring_ctas_per_sm(int device, int threads, int smem) {
+  static PerDevice blocks_fit;   // one per kernel
+  int n = 0;
+  const bsmma_status st = blocks_fit.get(device, &n, [&](int* fit) {
+    return cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess &&
+                   cudaOccupancyMaxActiveBlocksPerMultiprocessor(fit, Kern, threads, smem) == cudaSuccess
+               ? BSMMA_OK
+               : BSMMA_ERR_CUDA;
+  });
+  return st == BSMMA_OK ? n : 0;
 }
 
 int grid_for(int64_t work, int per_sm, int sm_count) {
@@ -669,8 +668,8 @@ bsmma_status launch_group_quantize(const void* x, bool f32, int64_t total_M, int
   const DeviceInfo* dev = current_device(&st);
   if (!dev) return st;
   const int64_t work = ((total_M + 63) / 64) * (K / 128);
-  const int per_sm = f32 ? ring_ctas_per_sm<group_quant_kernel<true>>(kXThreads, XRing<true>::kSmem)
-                         : ring_ctas_per_sm<group_quant_kernel<false>>(kXThreads, XRing<false>::kSmem);
+  const int per_sm = f32 ? ring_ctas_per_sm<group_quant_kernel<true>>(dev->device, kXThreads, XRing<true>::kSmem)
+                         : ring_ctas_per_sm<group_quant_kernel<false>>(dev->device, kXThreads, XRing<false>::kSmem);
   if (per_sm < 1) return BSMMA_ERR_CUDA;
   // X[total_M][K] as 32-bit words: K/2 (BF16) or K (FP32) words x total_M rows, one
   // 64 x 128-value tile per box.  An empty X has no tiles: the kernel only checks m_sizes
@@ -703,8 +702,8 @@ bsmma_status launch_block_quantize(const void* w, bool f32, int64_t G, int64_t N
   if (!dev) return st;
   const int64_t work = G * (N / 128) * (K / 128);
   if (work == 0) return BSMMA_OK;
-  const int per_sm = f32 ? ring_ctas_per_sm<block_quant_kernel<true>>(kBlockThreads, WRing<true>::kSmem)
-                         : ring_ctas_per_sm<block_quant_kernel<false>>(kBlockThreads, WRing<false>::kSmem);
+  const int per_sm = f32 ? ring_ctas_per_sm<block_quant_kernel<true>>(dev->device, kBlockThreads, WRing<true>::kSmem)
+                         : ring_ctas_per_sm<block_quant_kernel<false>>(dev->device, kBlockThreads, WRing<false>::kSmem);
   if (per_sm < 1) return BSMMA_ERR_CUDA;
   // W[G][N][K] as 32-bit words: K/2 (BF16) or K (FP32) words x N rows x G matrices,
   // one 128x128-value block per box
