@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -39,6 +40,21 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   const __half2 y = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
   lo = *reinterpret_cast<const uint32_t*>(&x);
   hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// sum * sa * sb + bias.  With the product of the scales first an element costs one multiplication
+// and one fused step, but a subnormal product has lost bits that the result may have, and an
+// infinite one makes a sum of 0 NaN.  There the smaller scale meets the sum first: a sum is an
+// integer, so a subnormal product with it is exact, and one that overflows does so beside a
+// scale at least as large, where the result does too.
+__device__ __forceinline__ bool normal_product(float lo, float hi, float s) {
+  return lo * s >= FLT_MIN && hi * s <= FLT_MAX;
+}
+__device__ __forceinline__ float scale_sum(float sum, float sa, float sb, float bias) {
+  const float p = sa * sb;
+  if (normal_product(fabsf(p), fabsf(p), 1.f)) return fmaf(sum, p, bias);
+  const bool a_first = fabsf(sa) < fabsf(sb);
+  return fmaf(sum * (a_first ? sa : sb), a_first ? sb : sa, bias);
 }
 
 template <bool F32>

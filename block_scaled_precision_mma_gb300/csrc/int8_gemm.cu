@@ -335,14 +335,15 @@ __global__ void __launch_bounds__(256, 1) int8_rows_kernel(const Int8Params p) {
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     const Place un = place(u);
     // the scales of this thread's outputs, loaded ahead of the sums
-    float scale[NT], bias[NT];
+    float sa[NT], sb[NT], bias[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int o = i * 256 + threadIdx.x;
       const int64_t n = un.n0 + (o & 31);
-      scale[i] = bias[i] = 0.f;
+      sa[i] = sb[i] = bias[i] = 0.f;
       if (n < p.N && (o >> 5) < un.rows) {
-        scale[i] = p.sA[un.row0 + (o >> 5)] * p.sB[un.g * p.N + n];
+        sa[i] = p.sA[un.row0 + (o >> 5)];
+        sb[i] = p.sB[un.g * p.N + n];
         if (p.bias) bias[i] = __bfloat162float(p.bias[n]);
       }
     }
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(256, 1) int8_rows_kernel(const Int8Params p) {
 #pragma unroll
         for (int w = 0; w < 8; ++w) s += sums[w * R * 32 + o];
         store_out<F32>(p.D, static_cast<int64_t>(un.row0 + (o >> 5)) * p.N + n,
-                       fmaf(s, scale[i], bias[i]));
+                       int8::scale_sum(s, sa[i], sb[i], bias[i]));
       }
     }
     __syncthreads();

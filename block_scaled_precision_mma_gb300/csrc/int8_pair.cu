@@ -302,9 +302,20 @@ __device__ __forceinline__ void emit_tile(const Int8Params& a, const Unit& un, i
   const int step = static_cast<int>(a.N & (kPer - 1)), off0 = static_cast<int>(at & (kPer - 1));
   Elem* mine = reinterpret_cast<Elem*>(tile) + tid;
   float y[32];
+  // the range of the tokens' scales (0 aside) decides for the warp whether all products of two
+  // scales are normal
+  const uint32_t size = __float_as_uint(fabsf(sa));
+  const float lo = __uint_as_float(__reduce_min_sync(kFull, size ? size : kNone));
+  const float hi = __uint_as_float(__reduce_max_sync(kFull, size));
+  if (__all_sync(kFull, sb == 0.f || normal_product(lo, hi, fabsf(sb)))) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
-    y[i] = fmaf(__uint_as_float(r[i]), __shfl_sync(kFull, sa, i) * sb, bias);
+    for (int i = 0; i < 32; ++i)
+      y[i] = fmaf(__uint_as_float(r[i]), __shfl_sync(kFull, sa, i) * sb, bias);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      y[i] = scale_sum(__uint_as_float(r[i]), __shfl_sync(kFull, sa, i), sb, bias);
+  }
   if constexpr (ONE) named_barrier_sync(barrier, 128);
   if (!F32 && step == 0) {
     // neighbouring lanes pair up their channels, the even one taking the even token: half the

@@ -456,6 +456,8 @@ bsmma_status int8_quantize(const void* x, bsmma_dtype x_dtype, int64_t x_rows, i
  *   the integer sum is exact while its partial sums stay below 2^24 (any K <= 1024; longer K
  *   short of one-sided extremes), else rounded as FP32 sums are, in an order that depends on
  *   the sizes alone (and on whether a captured stream has the workspaces below).
+ *   The scales and the bias are applied in FP32, without loss where the scales' product alone
+ *   would leave FP32's range: a sum of 0 gives the bias (or 0) with any finite scales.
  *   One launch; two where many rows of A are widened to FP16 first, in the stream's workspace
  *   (mx_gemm's; 2 * M * K bytes).  The last wave's units may be split along K, as mx_gemm's
  *   are, in the stream's split workspace.  A call captured on a stream without these

@@ -336,3 +336,56 @@ def test_the_expert_layer_end_to_end():
     assert not out[7].any()
     # weights within 2^-18, sums of three FP32 terms
     assert np.all(np.abs(out.cpu().numpy() - want) <= 2.0 ** -16 * np.abs(want).max())
+
+
+# Scales whose product leaves FP32's range, alone or with another's: subnormal and zero products,
+# overflowing ones, a huge scale beside a tiny or a subnormal one.
+TOKEN_SCALES = [1.3 * 2.0 ** -80, 1.3 * 2.0 ** 100, 1.1 * 2.0 ** 120, 1.1 * 2.0 ** -130, 0.0, 0.02, -2.0 ** 90]
+CHANNEL_SCALES = [1.7 * 2.0 ** -65, 1.7 * 2.0 ** 60, 1.2 * 2.0 ** -130, 1.2 * 2.0 ** 120, 0.003, 0.0, -0.5,
+                  1.9 * 2.0 ** -90, 1.4 * 2.0 ** -55]
+
+
+def check_wide(got, sums, sa, sb, bias, dtype):
+    """(sum * sA) * sB + bias in 64 bits, where no step leaves the range; what rounds past the
+    type's largest number is infinite.  Three FP32 roundings and the type's, each half a step of
+    a subnormal at least."""
+    with np.errstate(over="ignore"):
+        plain = sums * np.outer(sa.astype(np.float64), sb.astype(np.float64))
+        want = plain if bias is None else plain + bias
+        wide = np.abs(want) >= 2.0 ** 128 - 2.0 ** (119 if dtype == "bf16" else 103)
+    assert np.array_equal(got[wide], np.sign(want[wide]) * np.inf)
+    tol = 4 * 2.0 ** -24 * (np.abs(plain) + np.abs(want)) + 2.0 ** -147
+    if dtype == "bf16":
+        tol = tol + 2.0 ** -8 * np.abs(want) + 2.0 ** -133
+    assert np.all(np.abs(got[~wide] - want[~wide]) <= tol[~wide])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("M,N,K", [(5, 70, 144), (60, 300, 272), (7, 600, 4096), (900, 1030, 2064)])
+def test_dense_scales_of_any_size(M, N, K, bias, dtype, variant):
+    """Also units split along K; a row of zeros, whose sums are 0 whatever the scales."""
+    g = np.random.default_rng([92, M, N, K])
+    a, b = codes(g, M, K), codes(g, N, K)
+    a[0] = a[M // 2] = 0
+    sa = np.resize(np.float32(TOKEN_SCALES), M)
+    sb = np.resize(np.float32(CHANNEL_SCALES), N)
+    sa[0], sa[M // 2] = 1.1 * 2.0 ** 120, 1.3 * 2.0 ** 100
+    bb = torch.from_numpy(g.standard_normal(N).astype(np.float32)).bfloat16() if bias else None
+    check_wide(dense(a, sa, b, sb, bb, dtype), product(a, b), sa, sb, None if bb is None else bb.double().numpy(), dtype)
+
+
+@pytest.mark.parametrize("sizes", [[3, 0, 20, 1], [130, 0, 300, 5]], ids=lambda s: f"T{sum(s)}")
+def test_grouped_scales_of_any_size(sizes, variant):
+    g = np.random.default_rng([93, sum(sizes)])
+    G, T, N, K = len(sizes), sum(sizes), 200, 144
+    a, b = codes(g, T, K), codes(g, G, N, K)
+    a[2] = a[T // 2] = 0
+    sa = np.resize(np.float32(TOKEN_SCALES), T)
+    sb = np.resize(np.float32(CHANNEL_SCALES), G * N).reshape(G, N)
+    got = grouped(a, sa, b, sb, sizes)
+    assert bs.device_status() == 0
+    row = 0
+    for i, m in enumerate(sizes):
+        check_wide(got[row:row + m], product(a[row:row + m], b[i]), sa[row:row + m], sb[i], None, "f32")
+        row += m
