@@ -48,6 +48,17 @@ __device__ __forceinline__ float clean_logit(float x) {
 }
 __device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
 
+// A chosen expert's score over e^m (softmax) or over e^min(m, 0) (sigmoid), with m the largest
+// chosen logit: renormalised weights are quotients of these, so that scores below FP32's range
+// keep their ratios.  A sigmoid below 2^-1022 is 0, in 64 bits too: an expert masked by the
+// type's lowest value.
+constexpr float kVanished = -708.f;
+__device__ __forceinline__ float renorm_score(bool of_sigmoid, float x, float m) {
+  if (!of_sigmoid) return expf(x - m);
+  if (m >= 0.f) return sigmoid(x);
+  return x < kVanished ? 0.f : expf(x - m) / (1.f + expf(x));
+}
+
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
@@ -57,6 +68,12 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   return v;
+}
+
+// The largest x of the lanes that have one (not NaN), by one reduction.
+__device__ __forceinline__ float warp_largest(bool have, float x) {
+  const uint32_t o = __reduce_max_sync(kFull, have ? ordered(x) : 0u);
+  return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
 }
 
 // ------------------------------------------------------------------------- routing
@@ -80,10 +97,13 @@ __device__ __forceinline__ void write_choice(const RouteParams& p, int64_t t, in
                                              float mx, float denom) {
   const int lane = threadIdx.x & 31;
   float s = 0.f;
-  if (id >= 0) s = p.sigmoid ? sigmoid(x) : expf(x - mx) / denom;
   if (p.renormalize) {
+    const float m = warp_largest(id >= 0, x);
+    if (id >= 0) s = renorm_score(p.sigmoid, x, m);
     const float sum = warp_sum(s);
     s = sum > 0.f ? s / sum : 0.f;
+  } else if (id >= 0) {
+    s = p.sigmoid ? sigmoid(x) : expf(x - mx) / denom;
   }
   if (lane < p.k) {
     p.ids[t * p.k + lane] = id;
@@ -257,7 +277,7 @@ __global__ void __launch_bounds__(128) route_quad_kernel(const RouteParams p) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const float x = logit(c[h]);
-    s[h] = c[h] ? (p.sigmoid ? sigmoid(x) : expf(x - mx)) : 0.f;
+    s[h] = c[h] ? (p.renormalize ? renorm_score(p.sigmoid, x, mx) : sigmoid(x)) : 0.f;
   }
   if (p.renormalize) {
     float sum = s[0] + s[1];
@@ -424,15 +444,19 @@ __global__ void __launch_bounds__(128) route_eight_kernel(const RouteParams p) {
   const int id = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(c));
   float x = -INFINITY;
   if (c) x = p.bias ? clean_logit(load_elem<F32>(p.logits, row + id)) : of_key(c);
-  if (!p.sigmoid && !before) {
-    // the first choice is the largest logit: without a bias, and with groups valued by their
-    // largest, its group is open
-    mx = segment_max(x);
-    if (mx == -INFINITY) mx = 0.f;
-    if (!p.renormalize) sum_scores();
-  }
-  float s = c ? score(x) : 0.f;
-  if (p.renormalize) {
+  float s = 0.f;
+  if (!p.renormalize) {
+    if (!p.sigmoid && !before) {
+      // the first choice is the largest logit: without a bias, and with groups valued by their
+      // largest, its group is open
+      mx = segment_max(x);
+      if (mx == -INFINITY) mx = 0.f;
+      sum_scores();
+    }
+    if (c) s = score(x);
+  } else {
+    const float m = segment_max(x);
+    if (c) s = renorm_score(p.sigmoid, x, m);
     const float sum = segment_sum(s);
     s = sum > 0.f ? s / sum : 0.f;
   }
@@ -540,8 +564,11 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
     }
     const bool chosen = key[0] != -INFINITY && ahead < p.k;
     float s = 0.f;
-    if (chosen) s = p.sigmoid ? sigmoid(x[0]) : expf(x[0] - mx) / denom;
-    if (p.renormalize) {
+    if (!p.renormalize) {
+      if (chosen) s = p.sigmoid ? sigmoid(x[0]) : expf(x[0] - mx) / denom;
+    } else {
+      const float m = warp_largest(chosen, x[0]);
+      if (chosen) s = renorm_score(p.sigmoid, x[0], m);
       const float sum = warp_sum(s);
       s = sum > 0.f ? s / sum : 0.f;
     }

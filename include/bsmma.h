@@ -385,8 +385,10 @@ bsmma_status fp8_block_quantize(const void* w, bsmma_dtype w_dtype, int64_t G, i
  *          of its largest scores -- and only the topk_groups groups of largest value are
  *          open;
  *   ids    the k open experts of largest key, in decreasing order;
- *   weight w_j = scale * s_j, divided by the sum of the chosen scores when renormalize
- *          (0 when that sum is 0).
+ *   weight w_j = scale * s_j, divided by the sum of the chosen scores when renormalize.  The
+ *          quotients hold where the scores themselves leave FP32's range: with softmax they
+ *          are the softmax of the chosen logits.  A sigmoid score below 2^-1022 counts as 0,
+ *          and the weights are 0 where that leaves no score.
  *   Every choice between equal values takes the lower index.  A logit of -inf or NaN closes
  *   its expert (score 0, never chosen); +inf counts as the largest finite FP32.  A key that
  *   is NaN or -inf is never chosen either.  Where fewer than k experts can be chosen, the

@@ -388,3 +388,67 @@ def test_another_stream():
         out = bs.moe_combine(y, bs.moe_plan(ids, 64)[2], w)
     s.synchronize()
     assert torch.equal(ids, want_ids) and torch.equal(w, want_w) and torch.equal(out, want)
+
+
+# where each routing kernel runs: tokens, experts, the logits' type
+ROUTE_KERNELS = [(6, 24, "f32"), (6, 40, "bf16"), (7, 96, "f32"), (1025, 64, "bf16"), (1030, 160, "f32"),
+                 (8200, 64, "f32"), (8201, 128, "bf16"), (1031, 30, "f32")]
+
+
+def spread(g, shape, top, dtype):
+    """Logits between top - 20 and top."""
+    return torch.from_numpy((top - 20 * g.random(shape)).astype(np.float32)).to(DT[dtype])
+
+
+@pytest.mark.parametrize("T,E,dtype", ROUTE_KERNELS)
+@pytest.mark.parametrize("groups", [1, 2])
+def test_route_weights_of_experts_far_below_the_largest(T, E, dtype, groups):
+    """A bias chooses experts whose scores are 2^-150 and less of the row's largest: their
+    renormalised weights are those of the definition all the same, and sum to the scale."""
+    g = np.random.default_rng([94, T, E])
+    k = 5
+    x = spread(g, (T, E), -120.0, dtype)
+    x[:, 3] = 90.0
+    x[T // 2:, 3] = -20.0
+    b = np.zeros(E, dtype=np.float32)
+    chosen = np.arange(E - 10, E)
+    b[chosen] = 2 + 0.125 * np.arange(10)
+    ids, w = bs.moe_route(x.cuda(), k, bias=torch.from_numpy(b).cuda(), groups=groups, topk_groups=1, scale=2.0)
+    torch.cuda.synchronize()
+    ids_ref, w_ref = ref.route(x.double().numpy(), k, "softmax", b, groups, 1, 1, True, 2.0)
+    assert np.array_equal(ids.cpu().numpy(), ids_ref)
+    assert np.allclose(w_ref.sum(1), 2)
+    assert np.all(np.abs(w.cpu().numpy() - w_ref) <= W_TOL * np.abs(w_ref) + 1e-37)
+
+
+@pytest.mark.parametrize("T,E,dtype", ROUTE_KERNELS)
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("top", [-60.0, -84.0, -95.0, -400.0])
+def test_route_sigmoid_weights_of_small_scores(T, E, dtype, bias, top):
+    """All scores far below 1, and below FP32's range: the weights are still their shares."""
+    g = np.random.default_rng([95, T, E])
+    k = 4
+    x = spread(g, (T, E), top, dtype)
+    if T > 6:
+        x[T // 2:, 1::2] = 3.0      # rows with large scores among the small ones
+        x[T // 2:, 0] = 0.25
+    b = (0.125 * np.arange(E)).astype(np.float32) if bias else None
+    ids, w = bs.moe_route(x.cuda(), k, score="sigmoid", bias=None if b is None else torch.from_numpy(b).cuda())
+    torch.cuda.synchronize()
+    # (with a bias the keys are FP32 sums: a score below 2^-23 of it leaves it as it is)
+    ids_ref, w_ref = ref.route(x.double().numpy(), k, "sigmoid", b)
+    assert np.array_equal(ids.cpu().numpy(), ids_ref)
+    assert np.allclose(w_ref.sum(1), 1)
+    assert np.all(np.abs(w.cpu().numpy() - w_ref) <= W_TOL * np.abs(w_ref) + 1e-37)
+
+
+@pytest.mark.parametrize("T", [4, 1100, 8200])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("E", [16, 64])
+def test_route_sigmoid_weights_of_vanished_scores(T, E, dtype):
+    """Scores that vanish in 64 bits too (a mask of the type's lowest value) sum to 0: weights 0."""
+    x = torch.full((T, E), float(torch.finfo(DT[dtype]).min), dtype=DT[dtype])
+    x[T // 2:, 5] = -700.0
+    ids, w = bs.moe_route(x.cuda(), 3, score="sigmoid")
+    assert ids[0].tolist() == [0, 1, 2] and w[0].tolist() == [0, 0, 0]
+    assert ids[-1].tolist() == [5, 0, 1] and w[-1].tolist() == [1, 0, 0]
