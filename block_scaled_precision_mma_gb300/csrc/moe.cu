@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(128) route_kernel(const RouteParams p) {
 // w_j = scale * q_j / S with S the sum of the chosen scores and p_j = q_j / S:
 //   softmax, renormalised:  dx_j = d_j' p_j,  d_j' = d_j - sum p d       (chosen only)
 //   softmax:                dx_i = q_i (d_i - sum_m q_m d_m)             (every expert)
-//   sigmoid, renormalised:  dx_j = q_j (1 - q_j) (d_j - sum p d) / S     (chosen only)
+//   sigmoid, renormalised:  dx_j = p_j (1 - q_j) (d_j - sum p d)         (chosen only)
 //   sigmoid:                dx_j = q_j (1 - q_j) d_j                     (chosen only)
 // A warp builds its token's row in shared memory, in the logits' type, and writes it in
 // 16-byte pieces where rows are 16-byte aligned.
@@ -699,16 +699,18 @@ __global__ void __launch_bounds__(128) route_grad_kernel(const RouteGradParams p
     e = sum > 0.f ? e / sum : 0.f;
     out = e * (d - part_sum<LANES>(e * d));
   } else {
-    const float q = x == -INFINITY ? 0.f : sigmoid(x);
-    float g = d;
+    float q = x == -INFINITY ? 0.f : sigmoid(x);
     if (p.renormalize) {
+      // q becomes p, and no sum or reciprocal of the scores leaves the range
       // (the sums outside the condition: a warp's tokens may differ in it)
-      const float sum = part_sum<LANES>(q), inv = sum > 0.f ? 1.f / sum : 0.f;
-      const float dot = part_sum<LANES>(q * inv * d);
-      g = (d - dot) * inv;
+      const float m = part_max<LANES>(x);
+      if (x != -INFINITY) q = renorm_score(true, x, m);
+      const float sum = part_sum<LANES>(q);
+      q = sum > 0.f ? q / sum : 0.f;
+      d -= part_sum<LANES>(q * d);
     }
     // 1 - q as 1 / (1 + e^x): no cancellation for large logits
-    out = x == -INFINITY ? 0.f : q * sigmoid(-x) * g;
+    out = x == -INFINITY ? 0.f : q * sigmoid(-x) * d;
   }
   __syncwarp();
   if (id >= 0) store_elem<F32>(row, id, out);

@@ -452,3 +452,50 @@ def test_route_sigmoid_weights_of_vanished_scores(T, E, dtype):
     ids, w = bs.moe_route(x.cuda(), 3, score="sigmoid")
     assert ids[0].tolist() == [0, 1, 2] and w[0].tolist() == [0, 0, 0]
     assert ids[-1].tolist() == [5, 0, 1] and w[-1].tolist() == [1, 0, 0]
+
+
+def small_scores_gradient(x, ids, dw, scale):
+    """Of renormalised sigmoid weights, from the shares' logarithms: p_j (1 - q_j) (d_j - sum p d)."""
+    log_q = -np.logaddexp(0, -np.take_along_axis(x, np.maximum(ids, 0), 1))
+    log_q[ids < 0] = -np.inf
+    p = np.exp(log_q - np.logaddexp.reduce(log_q, axis=1, keepdims=True))
+    d = scale * np.where(ids < 0, 0, dw)
+    dx = np.zeros(x.shape)
+    grad = p * -np.expm1(log_q) * (d - (p * d).sum(1, keepdims=True))
+    for t, j in zip(*np.nonzero(ids >= 0)):
+        dx[t, ids[t, j]] = grad[t, j]
+    return dx
+
+
+@pytest.mark.parametrize("T,k", [(6, 5), (6, 20), (1100, 8), (1100, 12)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("top", [-60.0, -84.0, -95.0, -400.0])
+def test_route_backward_of_small_sigmoid_scores(T, k, dtype, top):
+    """Renormalised shares of scores far below 1, and below FP32's range: sums of the scores
+    and their reciprocals leave the range, the gradient does not."""
+    g = np.random.default_rng([96, T, k])
+    E = 40
+    x = spread(g, (T, E), top, dtype)
+    x[T // 2:, ::3] = 2.5           # rows with large scores among the chosen
+    ids = np.stack([g.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    ids[1, 1:] = -1
+    dw = torch.from_numpy(g.standard_normal((T, k)).astype(np.float32))
+    dx = bs.moe_route_backward(x.cuda(), torch.from_numpy(ids).cuda(), dw.cuda(), score="sigmoid", scale=2.5)
+    torch.cuda.synchronize()
+    want = small_scores_gradient(x.double().numpy(), ids, dw.double().numpy(), 2.5)
+    if top > -300:   # the Jacobians' squares of the sums are within the range of 64 bits
+        assert np.allclose(want, ref.route_backward(x.double().numpy(), ids, dw.numpy(), "sigmoid", True, 2.5),
+                           rtol=1e-9, atol=1e-12)
+    # as in test_route_backward
+    terms = 2.5 * np.abs(dw.numpy()).sum(1, keepdims=True)
+    tol = 2.0 ** -18 * terms + (2.0 ** -8 if dtype == "bf16" else 0) * np.abs(want)
+    assert np.all(np.abs(dx.double().cpu().numpy() - want) <= tol)
+
+
+@pytest.mark.parametrize("T", [4, 1100])
+def test_route_backward_of_vanished_sigmoid_scores(T):
+    """Weights that are 0 because no score is left have no gradient."""
+    x = torch.full((T, 16), float(np.finfo(np.float32).min))
+    ids = torch.arange(3, dtype=torch.int32).repeat(T, 1)
+    dx = bs.moe_route_backward(x.cuda(), ids.cuda(), torch.randn(T, 3).cuda(), score="sigmoid")
+    assert not dx.any()
