@@ -130,7 +130,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) int8_quantize_kernel(co
   constexpr int kHeld = V > 0 ? V : 1;
   uint4 held[kHeld];
   uint32_t amax = 0;
-  // BF16: the maximum of two magnitudes at a time, kept in a pair
+  // BF16: the maximum of two magnitudes at a time, kept in a pair.  NaN is above infinity in the
+  // order of the bits, and passes the pairs' maximum too.
   auto fold = [&](const uint4& v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) int8_quantize_kernel(co
         amax = max(amax, w[i] & 0x7FFFFFFFu);
       } else {
         __nv_bfloat162 a = *reinterpret_cast<__nv_bfloat162*>(&amax);
-        a = __hmax2(a, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+        a = __hmax2_nan(a, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
         amax = *reinterpret_cast<uint32_t*>(&a);
       }
     }

@@ -443,7 +443,9 @@ int64_t moe_plan_workspace_bytes(int64_t T, int k, int E);
  *   half to even, within [-127, 127].
  *   x [x_rows][K] BF16 or FP32; codes int8 [rows][K]; scales FP32 [rows].
  * Preconditions: K > 0, K % 16 == 0, K < 2^31, k >= 1, rows < 2^31, 16-byte-aligned x and
- *   codes.  Inputs must be finite.  One launch (none when rows == 0).
+ *   codes.  A row that holds a NaN gets a NaN
+ *   scale, else one that holds an infinity an infinite scale, in both types; its codes are
+ *   unspecified.  One launch (none when rows == 0).
  */
 bsmma_status int8_quantize(const void* x, bsmma_dtype x_dtype, int64_t x_rows, int64_t K,
                            const int32_t* src, int k, int64_t rows, int8_t* codes, float* scales,

@@ -389,3 +389,22 @@ def test_grouped_scales_of_any_size(sizes, variant):
     for i, m in enumerate(sizes):
         check_wide(got[row:row + m], product(a[row:row + m], b[i]), sa[row:row + m], sb[i], None, "f32")
         row += m
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [16, 64, 512, 2048, 7168, 40000])
+def test_quantize_shows_what_is_not_finite(K, dtype):
+    """A NaN in a row makes its scale NaN and an infinity makes it infinite, wherever in the row
+    they are; the rows beside it are as they would be alone."""
+    g = np.random.default_rng([97, K])
+    x = g.standard_normal((9, K)).astype(np.float32)
+    for r, (at, v) in enumerate([(0, np.nan), (K - 1, np.nan), (K // 2 + 1, -np.nan), (K // 2, np.inf), (1, -np.inf)]):
+        x[r, at] = v
+    x[5, [0, K - 1]] = np.inf, np.nan
+    xt = torch.from_numpy(x).to(DT[dtype])
+    c, s = bs.int8_quantize(xt.cuda())
+    torch.cuda.synchronize()
+    s = s.cpu().numpy()
+    assert np.isnan(s[[0, 1, 2, 5]]).all() and np.isposinf(s[[3, 4]]).all()
+    c_ref, s_ref = ref.int8_quantize(xt[6:].float().numpy())
+    assert np.array_equal(s[6:], s_ref) and np.array_equal(c[6:].cpu().numpy(), c_ref)
