@@ -61,7 +61,11 @@ def train_step(x, logits, k, w, dout):
     E = w.shape[0]
     ids, weights = bs.moe_route(logits, k)
     m_sizes, src, pos = bs.moe_plan(ids, E)
-    y = bs.grouped_bf16_gemm(x[src.long() // k], w, m_sizes)
+    # a padding token (all its logits -inf) leaves rows that no expert owns, and this product
+    # wants every row owned: the last expert takes them, and nothing reads what it makes of them
+    owned = m_sizes.clone()
+    owned[-1] += src.numel() - m_sizes.sum()
+    y = bs.grouped_bf16_gemm(x[src.long().clamp_min(0) // k], w, owned)
     out = bs.moe_combine(y, pos, weights)
     dy, dweights = bs.moe_combine_backward(dout, y, src, pos, weights)
     return out, dy, bs.moe_route_backward(logits, ids, dweights)

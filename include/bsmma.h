@@ -426,7 +426,10 @@ bsmma_status moe_route_backward(const void* logits, bsmma_dtype logits_dtype, in
  *                       their slots; -1 for the rows past the last used one;
  *   pos     int32 [T][k] the row of each slot, -1 for one that is not used.
  *   The result depends on nothing but ids.  With unused slots m_sizes sums to less than
- *   T*k: grouped_int8_gemm takes that, the other grouped GEMMs want total_M equal to the sum.
+ *   T*k: grouped_int8_gemm takes that.  The other grouped GEMMs and fp8_group_quantize want
+ *   total_M equal to the sum; for them add what is missing to the last expert's size and
+ *   gather any row for src -1: moe_combine does not read what becomes of those rows, and
+ *   moe_combine_backward's dY is 0 there.
  * Preconditions: 1 <= E <= 1024, k >= 1, T >= 0, T*k < 2^31 - 4096.  Up to 2048 slots one
  *   launch; more take three and moe_plan_workspace_bytes(T, k, E) bytes of the stream's
  *   workspace (mx_gemm's; reserve it before a capture).  T == 0 only clears m_sizes.
@@ -443,9 +446,9 @@ int64_t moe_plan_workspace_bytes(int64_t T, int k, int E);
  *   half to even, within [-127, 127].
  *   x [x_rows][K] BF16 or FP32; codes int8 [rows][K]; scales FP32 [rows].
  * Preconditions: K > 0, K % 16 == 0, K < 2^31, k >= 1, rows < 2^31, 16-byte-aligned x and
- *   codes.  A row that holds a NaN gets a NaN
- *   scale, else one that holds an infinity an infinite scale, in both types; its codes are
- *   unspecified.  One launch (none when rows == 0).
+ *   codes.  A row that holds a NaN gets a NaN scale, else one that holds an infinity an
+ *   infinite scale, in both types; its codes are unspecified.  One launch (none when
+ *   rows == 0).
  */
 bsmma_status int8_quantize(const void* x, bsmma_dtype x_dtype, int64_t x_rows, int64_t K,
                            const int32_t* src, int k, int64_t rows, int8_t* codes, float* scales,

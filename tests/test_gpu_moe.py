@@ -1,6 +1,9 @@
 """Routing, the expert order and the weighted sum on the GPU against their definitions in
 64 bits.  Choices and orders are whole numbers and must be equal; inputs whose choice would
 hang on the rounding of a sum (keys closer than 1e-6) are drawn again."""
+import importlib.util
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -499,3 +502,39 @@ def test_route_backward_of_vanished_sigmoid_scores(T):
     ids = torch.arange(3, dtype=torch.int32).repeat(T, 1)
     dx = bs.moe_route_backward(x.cuda(), ids.cuda(), torch.randn(T, 3).cuda(), score="sigmoid")
     assert not dx.any()
+
+
+def test_the_training_example_with_padding_tokens():
+    """Tokens that no expert takes leave rows that no expert owns; the BF16 product wants
+    every row owned.  Against the layer in 64 bits."""
+    spec = importlib.util.spec_from_file_location(
+        "expert_layer", os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "expert_layer.py"))
+    layer = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(layer)
+    g = np.random.default_rng([98])
+    T, E, k, H = 70, 6, 2, 128
+    x, dout = (filled(g, (T, H), "bf16") for _ in range(2))
+    w = (filled(g, (E, H, H), "f32") / 12).bfloat16()
+    xl = logits(g, T, E, "bf16")
+    pad = np.arange(0, T, 5)
+    xl[pad] = -np.inf
+    xl[3, 2:] = -np.inf                 # fewer experts than k: one slot unused
+    xl[3, 1] = -np.inf
+    out, dy, dx = layer.train_step(x.cuda(), xl.cuda(), k, w.cuda(), dout.cuda())
+    torch.cuda.synchronize()
+    assert bs.device_status() == 0
+    ids, wt = ref.route(xl.double().numpy(), k, "softmax")
+    rows = np.einsum("th,eoh->teo", x.double().numpy(), w.double().numpy())
+    want, dw = np.zeros((T, H)), np.zeros((T, k))
+    for t in range(T):
+        for j in range(k):
+            if ids[t, j] >= 0:
+                want[t] += wt[t, j] * rows[t, ids[t, j]]
+                dw[t, j] = rows[t, ids[t, j]] @ dout[t].double().numpy()
+    # BF16 rows of y (2^-9 of each of two terms) and of the result
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= 2.0 ** -7 * np.abs(rows).max(1))
+    assert not out[pad].any() and not dx[pad].any()
+    want = ref.route_backward(xl.double().numpy(), ids, dw, "softmax", True, 1.0)
+    # dw: a dot product of BF16 rows, 2^-9 of terms that sum to |rows| . |dout|; the gradient its differences
+    terms = np.einsum("teo,to->te", np.abs(rows), np.abs(dout.double().numpy())).max(1, keepdims=True)
+    assert np.all(np.abs(dx.double().cpu().numpy() - want) <= 2.0 ** -7 * terms)
