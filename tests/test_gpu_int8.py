@@ -408,3 +408,43 @@ def test_quantize_shows_what_is_not_finite(K, dtype):
     assert np.isnan(s[[0, 1, 2, 5]]).all() and np.isposinf(s[[3, 4]]).all()
     c_ref, s_ref = ref.int8_quantize(xt[6:].float().numpy())
     assert np.array_equal(s[6:], s_ref) and np.array_equal(c[6:].cpu().numpy(), c_ref)
+
+
+@pytest.mark.parametrize("M,N,K", [(100, 2304, 8208), (700, 1000, 4112)])
+def test_products_in_a_graph_with_reserved_workspaces(M, N, K, variant):
+    """With the workspaces reserved a captured call widens its rows by a pass of its own (two
+    launches, the second started early) and splits its units along K, as outside a graph."""
+    G = 3
+    stream = torch.cuda.Stream()
+    bs.reserve_workspace(2 * M * K, stream)
+    g = np.random.default_rng([100, M])
+    X = torch.zeros((M, K), dtype=torch.int8, device="cuda")
+    W = torch.from_numpy(codes(g, G, N, K)).cuda()
+    sX, sW = torch.ones(M, device="cuda"), torch.ones((G, N), device="cuda")
+    m = torch.zeros(G, dtype=torch.int64, device="cuda")
+    D, D2 = torch.empty((M, N), device="cuda"), torch.empty((M, N), device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    before = bs.launch_count()
+    with torch.cuda.graph(graph, stream=stream):
+        bs.int8_gemm(X, sX, W[1], sW[1], out=D2, stream=stream)
+        bs.grouped_int8_gemm(X, sX, W, sW, m, out=D, stream=stream)
+    if variant != (0, 0):
+        assert bs.launch_count() - before == (4 if variant[1] else 2)
+    w = W.double()
+    for sizes in ([M, 0, 0], [M - 33, 1, 32], [10, M - 90, 80]):
+        a = torch.from_numpy(codes(g, M, K)).cuda()
+        which = torch.repeat_interleave(torch.arange(G), torch.tensor(sizes)).cuda()
+        per_group = torch.stack([a.double() @ w[i].T for i in range(G)])
+        want = per_group[which, torch.arange(M, device="cuda")].float()
+        X.copy_(a)
+        m.copy_(torch.tensor(sizes))
+        for _ in range(3):   # one after another, the workspaces as the last left them
+            D.fill_(float("nan"))
+            D2.fill_(float("nan"))
+            graph.replay()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(D, want)
+            assert torch.equal(D2, per_group[1].float())
+    assert bs.device_status() == 0
