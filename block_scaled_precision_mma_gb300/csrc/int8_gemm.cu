@@ -428,9 +428,11 @@ bsmma_status launch_rows(const Int8Params& p, const DeviceInfo* dev, cudaStream_
 // its slowest warp at 24 bytes a cycle (15.5 with 16 rows) or, where units are short, 1000 a
 // piece and 2600 for the sums and the next unit's start; a fifth more for uneven groups, some of
 // which take several blocks; 5000 for the launch.  It wins where one or two row blocks read B
-// once or B is small: 4 x 14336 x 4096 17 against 23 us on SM-pair tiles, 4 x 4096 x 4096 11 and
-// 21, 32 x 4096 x 4096 17 and 25; but 32 x 14336 x 4096 33 and 21, 128 experts of 1408 x 2048 with
-// 4 rows each 109 and 74.
+// once or B is small.  Graph replays with L2 flushed, a replay's start of some 4 us among them,
+// against SM-pair tiles of 32: 4 x 14336 x 4096 16.9 and 23.0 us, 4 x 4096 x 4096 10.8 and 27.1,
+// 32 x 4096 x 4096 14.8 and 27.1; but 32 x 14336 x 4096 31.2 and 23.0, 128 experts of 1408 x 2048
+// with 4 rows each 92 and 84.  (One after another in a graph, B mostly in L2: 10.5 and 16.7, 5.2 and
+// 17.2, 10.2 and 19.9; 26.0 and 16.7, 89 and 79.)
 double rows_cycles(const Int8Params& p, const DeviceInfo* dev) {
   const double active = int8::groups_with_rows(p), rows = active > 0 ? p.total_M / active : 0;
   const int nt = (p.total_M + p.G - 1) / p.G <= 8 ? 1 : 2;

@@ -9,13 +9,14 @@
 // memory, which the MMAs' own reads of the tokens fill (an FP16 tile by TMA would write and
 // read two bytes each).
 //
-// What bounds it, as measured (graph replays, L2 flushed): many rows the tensor pipe, 4096 x
-// 14336 x 4096 265 us with the widening pass, 1.82 PFLOP/s, and 8 experts of 7168 x 2304 with
-// 16384 rows 320 us, 1.69 PFLOP/s (tensor pipe 76% busy under ncu at the clock it holds there);
-// few rows the streaming of the channels, 64 experts of 2048 x 7168 with 256 rows 128 us,
-// 5.8 TB/s; in between (192 rows an expert) the widening warps' latencies, tensor pipe and
-// DRAM both near half.  A single short product is launch, setup and pipeline start: 4 x 14336 x
-// 4096 takes about 18 us of which its bytes are 9.
+// What bounds it, as measured (graph replays, L2 flushed, each after a pause): many rows the
+// tensor pipe, 4096 x 14336 x 4096 268 us with the widening pass, 1.80 PFLOP/s, and 8 experts of
+// 7168 x 2304 with 16384 rows 322 us, 1.68 PFLOP/s (tensor pipe 76% busy under ncu at the clock it
+// holds there; one after another the power cap makes them 285 and 340 us); few rows the streaming
+// of the channels, 64 experts of 2048 x 7168 with 256 rows between them 131 us for 738 MB, 5.6
+// TB/s; in between (192 rows an expert) the widening warps' latencies, tensor pipe and DRAM both
+// near half.  A single short product is launch, setup and pipeline start: 4 x 14336 x 4096 takes
+// 23 us, of which its bytes are 9 (the few-row kernel, which gets it, 17 us).
 //
 // One persistent launch over 2-CTA clusters, 512 threads a CTA:
 //   warp 0       TMA producer: 128 K of the CTA's 128 channels and of its half of the tokens
@@ -997,9 +998,11 @@ __global__ void __launch_bounds__(256) widen_kernel(const uint4* __restrict__ in
 //     Measured at 14336 x 4096, 128 rows: 27 us unsplit, 35 us split, 56 units on 76 pairs.
 //   - Each block reads its channels from DRAM, at 3.3 KB a cycle; FP16 tokens cost a pass over
 //     them first and twice the bytes.
-// At 4096 x 14336 x 4096: 268 us with FP16 tokens (192 columns), 312 us without (256); 64
-// experts of 2048 x 7168 with 192 rows each: 290 and 257 us, in tiles of 128 345; with 96 rows 185
-// in tiles of 128, 207 of 256.
+// At 4096 x 14336 x 4096: 268 us with FP16 tokens (192 columns), 311 us without (256); 64
+// experts of 2048 x 7168 with 192 rows each: 293 and 260 us, in tiles of 128 351; with 96 rows each
+// 185 in tiles of 128, 208 of 256, which it takes all the same: it counts on uneven groups, some of
+// them with more than 128 rows.  512 x 14336 x 4096: 54 us in tiles of 128 (chosen), 66 of 256, 62
+// and 76 with FP16 tokens in tiles of 256 and 192.
 struct Choice {
   int tn;
   bool pre;

@@ -189,7 +189,11 @@ __global__ void __launch_bounds__(128) route_bf16_kernel(const RouteParams p) {
 // (eight maxima, 12 exchanges); two more merges across the four lanes leave all of them with
 // the token's eight.  96 warp instructions a token at 128 experts against 440 for the rounds
 // above: 65536 tokens 13 us against 34, both bound by issuing (56% of the slots; the 21 MB are
-// 3 us).
+// 3 us).  From 1024 tokens on: there 2.8 us against 3.3 in launches one after another, at 4096
+// 2.7 and 4.2; fewer take 2.4 to 2.8 us either way (64 experts, 64 tokens: 2.8 against 2.6).
+// Softmax without renormalisation needs the row's sum as well, k above 8 more keys kept, and
+// other E a ragged last piece: those stay with the rounds (65536 x 128 without renormalisation
+// 36 us, with k = 12 41 us, of 100 experts 34 us).
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max(a, b); }
 __device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
 __device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b) {
@@ -641,8 +645,12 @@ struct RouteGradParams {
   void* dlogits;
 };
 
-// EVERY: the second form, which reads the whole row; the others read the chosen logits.
-// LANES of a warp share a token: 8 where k <= 8 and there are many tokens, else 32.
+// EVERY: the second form, which reads the whole row, three times; the others read the chosen
+// logits (65536 x 128 BF16 21 us and 7).
+// LANES of a warp share a token: 8 where k <= 8, from 1024 tokens on, else 32.  128 experts, k = 8,
+// launches one after another: 1024 tokens 2.4 us with 8 lanes, 2.65 with 32 lanes and four warps a
+// block, 2.9 with one warp a block; 4096 tokens 2.45, 2.9 and 4.3; 64 tokens 2.05, 2.2 and 2.3,
+// where one warp a block is kept for spreading over the SMs beside other kernels.
 template <int LANES>
 __device__ __forceinline__ float part_sum(float v) {
 #pragma unroll
@@ -1096,7 +1104,9 @@ __global__ void __launch_bounds__(128, 8) combine_kernel(const CombineParams p) 
 // The token's dout pieces are read once per SLOTS slots; with one or two slots two of them are
 // in flight (16384 x 2 rows of 4096 BF16 101 us, 138 with one).  1024 threads an SM: at the 120
 // registers that ptxas takes by itself 512 fit, and 8192 x 8 rows of 4096 BF16 took 197 us, not
-// 170 (1.14 GB: 6.7 TB/s, DRAM 81% busy).
+// 170 (1.14 GB: 6.7 TB/s, DRAM 81% busy).  Under that bound five of the eight-slot kernels spill,
+// 24 bytes a thread in BF16 with 64 and more threads; with a warp a token 200 in BF16, 108 in FP32.
+// k of 3 and 4 take the eight slots too: 16384 x 4 rows of 1024 BF16 62 us for 302 MB.
 template <bool F32, int THREADS, int SLOTS>
 __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS, THREADS == 32 ? 4 : 1024 / THREADS)
     combine_grad_kernel(const CombineParams p) {
@@ -1178,7 +1188,9 @@ __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS, THREADS == 32 ?
   }
 }
 
-// A few tokens: one warp per block, so that they spread over the SMs.
+// A few tokens: one warp per block, so that they spread over the SMs.  128 BF16 experts, k = 8, in
+// rounds: the two are within 0.1 us up to 512 tokens; 1024 take 3.3 us with four warps a block
+// and 3.5 with one, 4096 4.2 and 5.0.
 int route_warps(int64_t T) { return T >= 1024 ? 4 : 1; }
 
 template <bool F32, int V>

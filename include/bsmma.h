@@ -86,14 +86,19 @@ typedef enum { BSMMA_SCALES_A = 0, BSMMA_SCALES_B = 1 } bsmma_scale_role;
  * The scales are first rearranged (mx_scale_relayout, both roles in one launch) into
  * a library-owned device workspace kept per (device, stream), which grows when needed.
  * Growing returns BSMMA_ERR_WORKSPACE if the stream is being captured (call
- * bsmma_reserve_workspace before capture).  Otherwise it allocates a larger buffer
+ * bsmma_reserve_workspace before capture).  Otherwise it allocates a larger buffer (a
+ * quarter more than is needed; it is kept until the process exits or it grows again)
  * and, if no CUDA graph captured a call that used the old buffer, synchronises
  * `stream` once and frees the old one; a buffer that a captured graph uses is kept
  * until the process exits, so replaying that graph stays valid after growth.  Calls
  * on the same stream are ordered; calls on different streams use different
  * workspaces.  The workspace is keyed by the stream handle: let a stream's pending
  * mx_gemm work finish before destroying the stream, since a stream created later
- * may get the same handle and with it the same workspace.
+ * may get the same handle and with it the same workspace.  A captured call uses the
+ * workspaces of the stream it was captured on wherever its graph is replayed: keep
+ * replays in order with that stream's other calls and with other graphs captured on
+ * it.  (cudaStreamPerThread is one handle for each thread's own stream: use it from one
+ * thread at a time.)
  * When the last wave of 256 x 256 output units would leave most SM pairs idle, the
  * kernel splits those units' K range over the idle pairs and the last pair to finish
  * a unit adds the others' FP32 partial sums, in K order (the result does not depend on
@@ -458,17 +463,19 @@ bsmma_status int8_quantize(const void* x, bsmma_dtype x_dtype, int64_t x_rows, i
  * int8_gemm -- D[m][n] = sA[m] * sB[n] * sum_k A[m][k] * B[n][k] (+ bias[n]), the product of
  *   8-bit integers with a scale for each token (row of A) and channel (row of B).
  *   A int8 [M][K], B int8 [N][K], sA FP32 [M], sB FP32 [N], bias BF16 [N] or NULL, D [M][N]
- *   BF16 or FP32 (d_dtype), rounded once.  sm_103a has no INT8 tcgen05 MMA; the operands are
- *   widened to FP16, where an INT8 value and a product of two are exact, and summed in FP32:
- *   the integer sum is exact while its partial sums stay below 2^24 (any K <= 1024; longer K
- *   short of one-sided extremes), else rounded as FP32 sums are, in an order that depends on
- *   the sizes alone (and on whether a captured stream has the workspaces below).
+ *   BF16 or FP32 (d_dtype), rounded to that type once.  sm_103a has no INT8 tcgen05 MMA; the
+ *   operands are widened to FP16, where an INT8 value and a product of two are exact, and
+ *   summed in FP32: the integer sum is exact while its partial sums stay below 2^24 (any
+ *   K <= 1024; longer K short of one-sided extremes).  Beyond, each accumulation step rounds
+ *   or cuts the sum to 24 bits, in an order that depends on the sizes alone (and on whether
+ *   a captured stream has the workspaces below).
  *   The scales and the bias are applied in FP32, without loss where the scales' product alone
  *   would leave FP32's range: a sum of 0 gives the bias (or 0) with any finite scales.
  *   One launch; two where many rows of A are widened to FP16 first, in the stream's workspace
- *   (mx_gemm's; 2 * M * K bytes).  The last wave's units may be split along K, as mx_gemm's
- *   are, in the stream's split workspace.  A call captured on a stream without these
- *   workspaces needs no reservation: it widens in the kernel and splits nothing.
+ *   (mx_gemm's, 2 * M * K bytes, and grown as there: a call that needs more than any before
+ *   it allocates and may synchronise).  The last wave's units may be split along K, as
+ *   mx_gemm's are, in the stream's split workspace.  A call captured on a stream without
+ *   these workspaces needs no reservation: it widens in the kernel and splits nothing.
  * Preconditions: M, N, K >= 0, K % 16 == 0, M, N, K < 2^31 - 512, 16-byte-aligned A, B and D,
  *   4-byte-aligned sA and sB, 2-byte-aligned bias.  N is not restricted.  M == 0 or N == 0
  *   is a no-op; K == 0 writes the bias, or 0.
