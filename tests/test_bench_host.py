@@ -75,3 +75,12 @@ def test_kernel_sources_cover_their_includes():
             with open(os.path.join(csrc, f), encoding="utf-8") as fh:
                 todo += [h for h in re.findall(r'#include "([^"]+)"', fh.read()) if h in local]
         assert seen <= set(files), (workload, sorted(seen - set(files)))
+
+
+def test_committed_traffic_records_are_of_these_sources():
+    """Each record was measured on the kernel sources as they are: a benchmark line whose record
+    is older has no traffic figure."""
+    names = sorted(f[len("traffic_"):-len(".txt")] for f in os.listdir(os.path.join(ROOT, "profiles"))
+                   if f.startswith("traffic_"))
+    assert len(names) == 7
+    assert [n for n in names if bench.recorded_traffic(n) is None] == []
