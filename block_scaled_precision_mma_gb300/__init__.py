@@ -17,6 +17,9 @@ Functions mirror the C names:
   :func:`moe_combine_backward` -- the expert layer around the grouped GEMMs.
 * :func:`int8_quantize`, :func:`int8_gemm`, :func:`grouped_int8_gemm` -- INT8 products with
   scales for each token and channel.
+* :func:`branch_enter`, :func:`branch_leave`, :func:`branch_enter_backward`,
+  :func:`branch_leave_backward`, :func:`dropout` -- a residual branch's norms, gate, dropout and
+  residual, with the next product's operand made on the way.
 * :func:`device_status`, :func:`reserve_workspace`, :func:`set_wait_limit_ns`,
   :func:`launch_count`, :func:`probe_wait_timeout`, :func:`status_string`.
 """
@@ -35,6 +38,8 @@ __all__ = ["mx_gemm", "mx_gemm_tiled", "mx_gemm_noalloc", "grouped_fp8_gemm", "g
            "moe_route", "moe_route_backward", "moe_plan", "moe_plan_workspace_bytes",
            "moe_combine", "moe_combine_backward",
            "int8_quantize", "int8_gemm", "grouped_int8_gemm",
+           "branch_enter", "branch_enter_backward", "branch_leave", "branch_leave_backward",
+           "branch_backward_workspace_bytes", "dropout",
            "mx_scale_relayout",
            "mx_quantize", "fp8_group_quantize", "fp8_block_quantize", "autotune_configure",
            "autotune_lookup",
@@ -117,6 +122,15 @@ def load(path: str | None = None):
         lib.int8_quantize.argtypes = [p, i32, i64, i64, p, i32, i64, p, p, p]
         lib.int8_gemm.argtypes = [p, p, p, p, p, p, i32, i64, i64, i64, p]
         lib.grouped_int8_gemm.argtypes = [p, p, p, p, p, i32, p, i64, i32, i64, i64, p]
+        lib.branch_enter.argtypes = [p, i32, i64, i64, i32, f32, p, p, i32, p, p, p]
+        lib.branch_leave.argtypes = [p, i32, p, i32, i64, i64, i32, f32, p, p, p, i64, f32, f32, f32,
+                                     p, p, i32, f32, p, p, i32, p, p, p]
+        lib.branch_enter_backward.argtypes = [p, i32, p, i32, i64, i64, i32, f32, p, p, p, p, p, p]
+        lib.branch_leave_backward.argtypes = [p, i32, p, i32, i64, i64, i32, f32, p, p, p, i64, f32,
+                                              f32, f32, p, p, p, p, p, p, p]
+        lib.branch_backward_workspace_bytes.argtypes = [i64, i64]
+        lib.branch_backward_workspace_bytes.restype = i64
+        lib.dropout.argtypes = [p, i32, i64, f32, p, p, p]
         for name in ("mx_gemm", "mx_gemm_tiled", "mx_gemm_noalloc", "grouped_fp8_gemm",
                      "grouped_fp8_gemm_packed", "grouped_fp8_pack_weights",
                      "mx_scale_relayout",
@@ -127,7 +141,8 @@ def load(path: str | None = None):
                      "fp8_block_quantize", "mx_gemm_bias_act", "mx_gemm_tiled_bias_act",
                      "bsmma_autotune_configure", "moe_route", "moe_route_backward", "moe_plan",
                      "moe_combine", "moe_combine_backward", "int8_quantize", "int8_gemm",
-                     "grouped_int8_gemm"):
+                     "grouped_int8_gemm", "branch_enter", "branch_leave", "branch_enter_backward",
+                     "branch_leave_backward", "dropout"):
             getattr(lib, name).restype = i32
         _lib = lib
         return lib
@@ -537,6 +552,151 @@ def grouped_int8_gemm(X, sX, W, sW, m_sizes, out=None, dtype=torch.bfloat16, str
                                     _ptr(W), _ptr(sW), _ptr(out) if total_M else None,
                                     _dtype_of(out, "out"), _ptr(m_sizes), total_M, G, N, K,
                                     _stream(stream)), "grouped_int8_gemm")
+    return out
+
+
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+OPERANDS = {"bf16": 0, "f32": 1, "int8": 2, "e4m3": 3, "e5m2": 4, "e2m1": 5}
+_OPERAND_OF = {torch.bfloat16: "bf16", torch.float32: "f32"}
+
+
+def _operand(fmt, T, H, like, out, scales):
+    """Output and scales (None without) of a [T, H] operand, given or new."""
+    if fmt in ("bf16", "f32"):
+        if scales is not None:
+            raise ValueError(f"{fmt} rows have no scales")
+        return _output(out, torch.bfloat16 if fmt == "bf16" else torch.float32, (T, H), like, "out"), None
+    if fmt == "int8":
+        return (_output(out, torch.int8, (T, H), like, "codes"),
+                _output(scales, torch.float32, (T,), like, "scales"))
+    return (_output(out, torch.uint8, (T, H // 2 if fmt == "e2m1" else H), like, "codes"),
+            _output(scales, torch.uint8, (T, H // 32), like, "scales"))
+
+
+def _rng(rng, p: float):
+    _expect(rng, torch.int64, (2,), "rng")
+    if rng is None and p > 0:
+        raise ValueError("dropout needs rng, an int64 tensor (seed, offset) on the device")
+
+
+def _gate(gate, gate_rows, y):
+    """The rows that share a row of the gate (all of them unless said)."""
+    if gate is None:
+        return 1
+    T, H = y.shape
+    rows = max(T, 1) if gate_rows is None else gate_rows
+    if rows < 1:
+        raise ValueError("gate_rows must be at least 1")
+    _expect(gate, y.dtype, (-(-T // rows), H), "gate")
+    return rows
+
+
+def branch_enter(x, weight=None, bias=None, norm="rms", eps=1e-6, fmt=None, out=None, scales=None,
+                 stream=None):
+    """The norm before a block: n(x) * weight + bias for x [T, H] (BF16 or FP32; weight and bias
+    float32 [H]), ``norm`` 'rms' or 'layer'.  ``fmt`` None (x's dtype), 'bf16' or 'f32' ->
+    [T, H]; 'int8' -> (codes, scales) as :func:`int8_quantize`'s, 'e4m3', 'e5m2', 'e2m1' -> as
+    :func:`mx_quantize`'s (rowwise).  See ``branch_enter`` in bsmma.h."""
+    T, H = x.shape
+    dtype = _dtype_of(x, "x")
+    fmt = fmt or _OPERAND_OF[x.dtype]
+    _expect(weight, torch.float32, (H,), "weight")
+    _expect(bias, torch.float32, (H,), "bias")
+    out, scales = _operand(fmt, T, H, x, out, scales)
+    _check(load().branch_enter(_ptr(x), dtype, T, H, NORMS[norm], eps, _ptr(weight), _ptr(bias),
+                               OPERANDS[fmt], _ptr(out), _ptr(scales), _stream(stream)),
+           "branch_enter")
+    return out if scales is None else (out, scales)
+
+
+def branch_enter_backward(dh, x, weight=None, norm="rms", eps=1e-6, dres=None, bias=False, dx=None,
+                          stream=None):
+    """The gradients of :func:`branch_enter` for dh [T, H] (x's dtype, or BF16) -> (dx, dweight,
+    dbias).  ``dres``: a gradient of x to add to dx (what reached the stream past the branch);
+    dweight float32 [H], None without a weight; dbias None unless ``bias``."""
+    T, H = x.shape
+    h_dtype, x_dtype = _dtype_of(dh, "dh"), _dtype_of(x, "x")
+    _expect(dh, dh.dtype, (T, H), "dh")
+    _expect(weight, torch.float32, (H,), "weight")
+    _expect(dres, x.dtype, (T, H), "dres")
+    dx = _output(dx, x.dtype, (T, H), x, "dx")
+    dweight = None if weight is None else torch.empty(H, dtype=torch.float32, device=x.device)
+    dbias = torch.empty(H, dtype=torch.float32, device=x.device) if bias else None
+    _check(load().branch_enter_backward(_ptr(dh), h_dtype, _ptr(x), x_dtype, T, H, NORMS[norm], eps,
+                                        _ptr(weight), _ptr(dres), _ptr(dx), _ptr(dweight), _ptr(dbias),
+                                        _stream(stream)), "branch_enter_backward")
+    return dx, dweight, dbias
+
+
+def branch_leave(x, y, weight=None, bias=None, norm="none", eps=1e-6, gate=None, gate_rows=None,
+                 x_scale=1.0, y_scale=1.0, p=0.0, rng=None, next_norm="none", next_weight=None,
+                 next_bias=None, next_eps=1e-6, fmt=None, out=None, next_out=None, next_scales=None,
+                 stream=None):
+    """The step after a block: out = x_scale * x + y_scale * gate * drop(n(y) * weight + bias),
+    [T, H] of x's dtype; y of x's dtype, or BF16 beside an FP32 x.  ``gate`` (y's dtype) has a row for
+    each ``gate_rows`` rows (None: one row for all).  ``p``, ``rng``: as :func:`dropout`.  With
+    ``next_norm`` also the following block's :func:`branch_enter` of out, in ``fmt`` (None: y's
+    dtype) -> (out, h) or (out, codes, scales).  out may be x.  See ``branch_leave`` in bsmma.h."""
+    T, H = x.shape
+    x_dtype, y_dtype = _dtype_of(x, "x"), _dtype_of(y, "y")
+    _expect(y, y.dtype, (T, H), "y")
+    for t, what in ((weight, "weight"), (bias, "bias"), (next_weight, "next_weight"), (next_bias, "next_bias")):
+        _expect(t, torch.float32, (H,), what)
+    gate_rows = _gate(gate, gate_rows, y)
+    _rng(rng, p)
+    out = _output(out, x.dtype, (T, H), x, "out")
+    fmt = fmt or _OPERAND_OF[y.dtype]
+    if next_norm != "none":
+        next_out, next_scales = _operand(fmt, T, H, x, next_out, next_scales)
+    _check(load().branch_leave(_ptr(x), x_dtype, _ptr(y), y_dtype, T, H, NORMS[norm], eps, _ptr(weight),
+                               _ptr(bias), _ptr(gate), gate_rows, x_scale, y_scale, p, _ptr(rng), _ptr(out),
+                               NORMS[next_norm], next_eps, _ptr(next_weight), _ptr(next_bias),
+                               OPERANDS[fmt], _ptr(next_out), _ptr(next_scales), _stream(stream)),
+           "branch_leave")
+    if next_norm == "none":
+        return out
+    return (out, next_out) if next_scales is None else (out, next_out, next_scales)
+
+
+def branch_leave_backward(dout, y, weight=None, bias=None, norm="none", eps=1e-6, gate=None,
+                          gate_rows=None, x_scale=1.0, y_scale=1.0, p=0.0, rng=None, dy=None, dx=None,
+                          stream=None):
+    """The gradients of :func:`branch_leave` (without its next norm) for dout [T, H] and the forward
+    call's arguments -> (dy, dx, dweight, dbias, dgate): dy of y's dtype; dx = x_scale * dout, dout itself
+    where x_scale is 1; the others float32, None for what was not given.  ``rng`` holds what it
+    held in the forward call."""
+    T, H = y.shape
+    x_dtype, y_dtype = _dtype_of(dout, "dout"), _dtype_of(y, "y")
+    _expect(dout, dout.dtype, (T, H), "dout")
+    _expect(weight, torch.float32, (H,), "weight")
+    _expect(bias, torch.float32, (H,), "bias")
+    gate_rows = _gate(gate, gate_rows, y)
+    _rng(rng, p)
+    dy = _output(dy, y.dtype, (T, H), y, "dy")
+    if x_scale != 1 or dx is not None:
+        dx = _output(dx, dout.dtype, (T, H), y, "dx")
+    new = lambda t: None if t is None else torch.empty(t.shape, dtype=torch.float32, device=y.device)  # noqa: E731
+    dweight, dbias, dgate = new(weight), new(bias), new(gate)
+    _check(load().branch_leave_backward(_ptr(dout), x_dtype, _ptr(y), y_dtype, T, H, NORMS[norm], eps,
+                                        _ptr(weight), _ptr(bias), _ptr(gate), gate_rows, x_scale, y_scale,
+                                        p, _ptr(rng), _ptr(dy), _ptr(dx), _ptr(dweight), _ptr(dbias),
+                                        _ptr(dgate), _stream(stream)), "branch_leave_backward")
+    return dy, dout if dx is None else dx, dweight, dbias, dgate
+
+
+def branch_backward_workspace_bytes(T: int, H: int) -> int:
+    """Workspace of the branch's gradients (reserve it before a capture)."""
+    return int(load().branch_backward_workspace_bytes(T, H))
+
+
+def dropout(x, p, rng, out=None, stream=None):
+    """x with each value dropped with probability p (rounded to 2^-16), the others divided by 1 - p;
+    ``rng`` int64 (seed, offset) on the device.  Its gradient is the same call on the output's.
+    out may be x.  See ``dropout`` in bsmma.h."""
+    _rng(rng, p)
+    out = _output(out, x.dtype, tuple(x.shape), x, "out")
+    _check(load().dropout(_ptr(x), _dtype_of(x, "x"), x.numel(), p, _ptr(rng), _ptr(out), _stream(stream)),
+           "dropout")
     return out
 
 

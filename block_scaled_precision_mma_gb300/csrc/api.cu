@@ -11,11 +11,13 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <deque>
 #include <mutex>
 #include <vector>
 
+#include "branch.h"
 #include "epilogue.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -707,6 +709,210 @@ bsmma_status moe_combine_backward(const void* dout, bsmma_dtype dtype, int64_t H
     return BSMMA_ERR_MISALIGNED;
   return launch_combine_backward(dout, dtype == BSMMA_F32, H, Y, src, pos, weights, T, k, dY,
                                  dweights, reinterpret_cast<cudaStream_t>(stream));
+}
+
+namespace {
+bool known_norm(bsmma_norm n, bool none) {
+  return n == BSMMA_NORM_RMS || n == BSMMA_NORM_LAYER || (none && n == BSMMA_NORM_NONE);
+}
+// The norm's own arguments; `more`: anything else that only a norm has.
+bsmma_status check_norm(bsmma_norm norm, bool none, float eps, const float* weight, const float* bias,
+                        bool more = false) {
+  if (!known_norm(norm, none)) return BSMMA_ERR_INVALID_ARG;
+  if (norm == BSMMA_NORM_NONE) return weight || bias || more ? BSMMA_ERR_INVALID_ARG : BSMMA_OK;
+  if (!(eps > 0.f) || eps > 3.402823466e38f) return BSMMA_ERR_INVALID_ARG;
+  return aligned16(weight) && aligned16(bias) ? BSMMA_OK : BSMMA_ERR_MISALIGNED;
+}
+bsmma_status check_rows(bsmma_dtype stream_dtype, bsmma_dtype branch_dtype, int64_t T, int64_t H) {
+  if (!known_dtype(stream_dtype) || !known_dtype(branch_dtype) || T < 0 || T >= INT32_MAX || H < 8 ||
+      H > 16384)
+    return BSMMA_ERR_INVALID_ARG;
+  if (stream_dtype == BSMMA_BF16 && branch_dtype == BSMMA_F32) return BSMMA_ERR_UNSUPPORTED;
+  return H % 8 == 0 ? BSMMA_OK : BSMMA_ERR_MISALIGNED;
+}
+bool is_mx(bsmma_operand f) {
+  return f == BSMMA_OPERAND_E4M3 || f == BSMMA_OPERAND_E5M2 || f == BSMMA_OPERAND_E2M1;
+}
+bsmma_status check_form(bsmma_operand form, bool f32_stream, int64_t T, int64_t H, const void* out,
+                        const void* scales) {
+  if (form < BSMMA_OPERAND_BF16 || form > BSMMA_OPERAND_E2M1) return BSMMA_ERR_INVALID_ARG;
+  if (form == BSMMA_OPERAND_F32 && !f32_stream) return BSMMA_ERR_UNSUPPORTED;
+  if (is_mx(form) && H % 32 != 0) return BSMMA_ERR_INVALID_ARG;
+  if (T == 0) return BSMMA_OK;
+  const bool coded = form == BSMMA_OPERAND_INT8 || is_mx(form);
+  if (!out || coded != (scales != nullptr)) return BSMMA_ERR_INVALID_ARG;
+  return aligned16(out) && (form != BSMMA_OPERAND_INT8 || aligned_to(scales, 4)) ? BSMMA_OK
+                                                                                 : BSMMA_ERR_MISALIGNED;
+}
+bsmma_status check_gate(const void* gate, int64_t gate_rows) {
+  if (gate && gate_rows < 1) return BSMMA_ERR_INVALID_ARG;
+  return aligned16(gate) ? BSMMA_OK : BSMMA_ERR_MISALIGNED;
+}
+// p in 16 bits, and what keeps the mean.
+bsmma_status make_drop(float p, const int64_t* rng, DropArgs* d) {
+  if (!(p >= 0.f && p < 1.f)) return BSMMA_ERR_INVALID_ARG;
+  const double steps = std::nearbyint(static_cast<double>(p) * 65536.0);
+  d->threshold = steps > 65535.0 ? 65535u : static_cast<uint32_t>(steps);
+  d->scale = static_cast<float>(65536.0 / (65536.0 - d->threshold));
+  d->rng = rng;
+  if (p > 0.f && !rng) return BSMMA_ERR_INVALID_ARG;
+  return aligned_to(rng, 8) ? BSMMA_OK : BSMMA_ERR_MISALIGNED;
+}
+// A gate's rows as the kernels divide by them.
+int64_t bounded_rows(int64_t gate_rows, int64_t T) { return gate_rows < T ? gate_rows : T; }
+
+bsmma_status run_grad(const BranchGradArgs& a, bool leave, cudaStream_t s) {
+  if (!a.dweight && !a.dbias && !a.dgate) return launch_branch_grad(a, leave, nullptr, s);
+  const StreamLock lock(s);
+  void* ws = nullptr;
+  const bsmma_status st = get_workspace(branch_grad_workspace_bytes(a.T, a.H), s, &ws);
+  if (st != BSMMA_OK) return st;
+  return launch_branch_grad(a, leave, ws, s);
+}
+bsmma_status clear_sums(float* dweight, float* dbias, int64_t H, cudaStream_t s) {
+  for (float* p : {dweight, dbias})
+    if (p && cudaMemsetAsync(p, 0, static_cast<size_t>(H) * 4, s) != cudaSuccess) return BSMMA_ERR_CUDA;
+  return BSMMA_OK;
+}
+}  // namespace
+
+#define BSMMA_TRY(expr)                        \
+  do {                                         \
+    const bsmma_status st_ = (expr);           \
+    if (st_ != BSMMA_OK) return st_;           \
+  } while (0)
+
+bsmma_status branch_enter(const void* x, bsmma_dtype x_dtype, int64_t T, int64_t H, bsmma_norm norm,
+                          float eps, const float* weight, const float* bias, bsmma_operand form,
+                          void* out, void* scales, bsmma_stream stream) {
+  BSMMA_TRY(check_rows(x_dtype, x_dtype, T, H));
+  BSMMA_TRY(check_norm(norm, false, eps, weight, bias));
+  BSMMA_TRY(check_form(form, x_dtype == BSMMA_F32, T, H, out, scales));
+  if (T == 0) return BSMMA_OK;
+  if (!x) return BSMMA_ERR_INVALID_ARG;
+  if (!aligned16(x)) return BSMMA_ERR_MISALIGNED;
+  EnterArgs a = {};
+  a.x = x;
+  a.x_f32 = x_dtype == BSMMA_F32;
+  a.T = T;
+  a.H = H;
+  a.norm = {norm, eps, weight, bias};
+  a.to = {form, out, scales};
+  return launch_branch_enter(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+bsmma_status branch_leave(const void* x, bsmma_dtype x_dtype, const void* y, bsmma_dtype y_dtype,
+                          int64_t T, int64_t H, bsmma_norm norm, float eps, const float* weight,
+                          const float* bias, const void* gate, int64_t gate_rows, float x_scale,
+                          float y_scale, float p, const int64_t* rng, void* out, bsmma_norm next,
+                          float next_eps, const float* next_weight, const float* next_bias,
+                          bsmma_operand next_form, void* next_out, void* next_scales,
+                          bsmma_stream stream) {
+  BSMMA_TRY(check_rows(x_dtype, y_dtype, T, H));
+  BSMMA_TRY(check_norm(norm, true, eps, weight, bias));
+  BSMMA_TRY(check_gate(gate, gate_rows));
+  BSMMA_TRY(check_norm(next, true, next_eps, next_weight, next_bias, next_out || next_scales));
+  if (next != BSMMA_NORM_NONE)
+    BSMMA_TRY(check_form(next_form, x_dtype == BSMMA_F32, T, H, next_out, next_scales));
+  LeaveArgs a = {};
+  BSMMA_TRY(make_drop(p, rng, &a.drop));
+  if (T == 0) return BSMMA_OK;
+  if (!x || !y || !out) return BSMMA_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(out)) return BSMMA_ERR_MISALIGNED;
+  a.x = x;
+  a.x_f32 = x_dtype == BSMMA_F32;
+  a.y = y;
+  a.y_f32 = y_dtype == BSMMA_F32;
+  a.T = T;
+  a.H = H;
+  a.norm = {norm, eps, weight, bias};
+  a.gate = gate;
+  a.gate_rows = bounded_rows(gate_rows, T);
+  a.x_scale = x_scale;
+  a.y_scale = y_scale;
+  a.out = out;
+  a.next = {next, next_eps, next_weight, next_bias};
+  a.to = {next_form, next_out, next_scales};
+  return launch_branch_leave(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+bsmma_status branch_enter_backward(const void* dh, bsmma_dtype h_dtype, const void* x,
+                                   bsmma_dtype x_dtype, int64_t T, int64_t H, bsmma_norm norm,
+                                   float eps, const float* weight, const void* dres, void* dx,
+                                   float* dweight, float* dbias, bsmma_stream stream) {
+  BSMMA_TRY(check_rows(x_dtype, h_dtype, T, H));
+  BSMMA_TRY(check_norm(norm, false, eps, weight, nullptr));
+  if (!aligned16(dweight) || !aligned16(dbias)) return BSMMA_ERR_MISALIGNED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) return clear_sums(dweight, dbias, H, s);
+  if (!dh || !x || !dx) return BSMMA_ERR_INVALID_ARG;
+  if (!aligned16(dh) || !aligned16(x) || !aligned16(dres) || !aligned16(dx)) return BSMMA_ERR_MISALIGNED;
+  BranchGradArgs a = {};
+  a.d = dh;
+  a.d_f32 = h_dtype == BSMMA_F32;
+  a.v = x;
+  a.v_f32 = x_dtype == BSMMA_F32;
+  a.T = T;
+  a.H = H;
+  a.norm = {norm, eps, weight, nullptr};
+  a.dres = dres;
+  a.drop = {0u, 1.f, nullptr};
+  a.dv = dx;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  return run_grad(a, false, s);
+}
+
+bsmma_status branch_leave_backward(const void* dout, bsmma_dtype x_dtype, const void* y,
+                                   bsmma_dtype y_dtype, int64_t T, int64_t H, bsmma_norm norm,
+                                   float eps, const float* weight, const float* bias,
+                                   const void* gate, int64_t gate_rows, float x_scale,
+                                   float y_scale, float p, const int64_t* rng, void* dy, void* dx,
+                                   float* dweight, float* dbias, float* dgate, bsmma_stream stream) {
+  BSMMA_TRY(check_rows(x_dtype, y_dtype, T, H));
+  BSMMA_TRY(check_norm(norm, true, eps, weight, bias, dweight || dbias));
+  BSMMA_TRY(check_gate(gate, gate_rows));
+  BranchGradArgs a = {};
+  BSMMA_TRY(make_drop(p, rng, &a.drop));
+  if (dgate && !gate) return BSMMA_ERR_INVALID_ARG;
+  if (!aligned16(dweight) || !aligned16(dbias) || !aligned16(dgate)) return BSMMA_ERR_MISALIGNED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) return clear_sums(dweight, dbias, H, s);
+  if (!dout || !y || !dy) return BSMMA_ERR_INVALID_ARG;
+  if (!aligned16(dout) || !aligned16(y) || !aligned16(dy) || !aligned16(dx)) return BSMMA_ERR_MISALIGNED;
+  a.d = dout;
+  a.d_f32 = x_dtype == BSMMA_F32;
+  a.v = y;
+  a.v_f32 = y_dtype == BSMMA_F32;
+  a.T = T;
+  a.H = H;
+  a.norm = {norm, eps, weight, bias};
+  a.gate = gate;
+  a.gate_rows = bounded_rows(gate_rows, T);
+  a.x_scale = x_scale;
+  a.y_scale = y_scale;
+  a.dv = dy;
+  a.dx = dx;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  a.dgate = dgate;
+  return run_grad(a, true, s);
+}
+
+int64_t branch_backward_workspace_bytes(int64_t T, int64_t H) {
+  if (T <= 0 || T >= INT32_MAX || H < 8 || H > 16384) return 0;
+  return branch_grad_workspace_bytes(T, H);
+}
+
+bsmma_status dropout(const void* x, bsmma_dtype dtype, int64_t n, float p, const int64_t* rng, void* y,
+                     bsmma_stream stream) {
+  if (!known_dtype(dtype) || n < 0 || n >= (int64_t{1} << 40)) return BSMMA_ERR_INVALID_ARG;
+  DropArgs d;
+  BSMMA_TRY(make_drop(p, rng, &d));
+  if (n == 0) return BSMMA_OK;
+  if (!x || !y) return BSMMA_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(y)) return BSMMA_ERR_MISALIGNED;
+  return launch_dropout(x, dtype == BSMMA_F32, n, d, y, reinterpret_cast<cudaStream_t>(stream));
 }
 
 bsmma_status bsmma_reserve_workspace(int64_t bytes, bsmma_stream stream) {

@@ -318,6 +318,16 @@ int bsmma_autotune_lookup(const char* key);
 /* Element type of the high-precision inputs of the quantisers. */
 typedef enum { BSMMA_BF16 = 0, BSMMA_F32 = 1 } bsmma_dtype;
 
+/* The form of a product's operand (branch_enter, branch_leave, moe_step). */
+typedef enum {
+  BSMMA_OPERAND_BF16 = 0,
+  BSMMA_OPERAND_F32 = 1,
+  BSMMA_OPERAND_INT8 = 2,
+  BSMMA_OPERAND_E4M3 = 3,
+  BSMMA_OPERAND_E5M2 = 4,
+  BSMMA_OPERAND_E2M1 = 5
+} bsmma_operand;
+
 /*
  * mx_quantize -- MX quantisation, the step that makes mx_gemm's operands.  Source:
  * "[gfx1250] Add MXFP4 GEMM support to FlyDSL backend", the MXFP4 test helpers and
@@ -516,6 +526,90 @@ bsmma_status moe_combine(const void* Y, bsmma_dtype dtype, int64_t R, int64_t H,
 bsmma_status moe_combine_backward(const void* dout, bsmma_dtype dtype, int64_t H, const void* Y,
                                   const int32_t* src, const int32_t* pos, const float* weights,
                                   int64_t T, int k, void* dY, float* dweights, bsmma_stream stream);
+
+/*
+ * The residual branch.  What a block does to the residual stream x around its products f
+ * (the source pages have no counterpart; their GEMMs' operands are what it makes):
+ *     h = n(x) * weight + bias                                         branch_enter
+ *     out = x_scale * x + y_scale * gate * drop(n(y) * weight + bias)  branch_leave, y = f(h)
+ *   n is RMS (v / sqrt(mean v^2 + eps)), LAYER ((v - mean v) / sqrt(var v + eps), the variance
+ *   around the mean, divided by H) or, for branch_leave, NONE (n(y) = y; no weight, no bias).
+ *   Rows of H values; arithmetic, statistics and sums in FP32 (a row whose squares' sum leaves
+ *   FP32's range is out of the operators' range), results rounded once.  The stream (x, out,
+ *   dout, dres) has one type, the branch (h, y, gate, dh, dy) that type or, with an FP32
+ *   stream, BF16.  weight and bias FP32 [H] or NULL (1, 0).
+ *   gate [ceil(T / gate_rows)][H]: rows g * gate_rows .. of the stream use row g (1: one for
+ *   each token; >= T: one for all; else one for each sequence, the last may be short); NULL: 1.
+ *   drop: dropout with probability p, in [0, 1); rng {seed, offset} int64 [2] in DEVICE memory
+ *   (read by the kernel, so a captured call draws new numbers when the memory changes; NULL
+ *   only where p == 0).  p is rounded to 2^-16 (at most 65535/65536) and kept values are
+ *   multiplied by 1 / (1 - p) of the rounded p.  Value i of the tensor (row-major) is kept or not by 16
+ *   bits of Philox4x32-10, counter (i / 8 as two words, offset as two words), key the seed's
+ *   two words, words in order, low halves first: the mask is made again wherever it is needed
+ *   and never stored.  A dropped value is 0, whatever it was.
+ * A row to write as a product's operand (form): BF16, FP32 (FP32 streams), or codes of the
+ *   FP32 values with the rules of int8_quantize (codes int8 [T][H], scales FP32 [T]) and of
+ *   mx_quantize, rowwise (codes [T][H], E2M1 [T][H/2]; scales E8M0 uint8 [T][H/32]).
+ */
+typedef enum { BSMMA_NORM_NONE = 0, BSMMA_NORM_RMS = 1, BSMMA_NORM_LAYER = 2 } bsmma_norm;
+
+/*
+ * branch_enter -- h from x [T][H]; norm RMS or LAYER.  scales: INT8 and MX forms, else NULL.
+ * branch_leave -- out [T][H] of the stream's type from x and y; out may be x.  With next
+ *   (RMS or LAYER) also the following block's branch_enter of the row as it is stored in out:
+ *   next_out in next_form (and next_scales) with next_weight, next_bias and next_eps, in the
+ *   same pass; next NONE: next_out is not written.
+ * Preconditions (these and the gradients): 0 <= T < 2^31, 8 <= H <= 16384, H % 8 == 0 (MX forms
+ *   H % 32 == 0), eps > 0 and finite where there is a norm, gate_rows >= 1 with a gate;
+ *   16-byte-aligned matrices, weights and biases, 8-byte-aligned rng, 4-byte-aligned FP32
+ *   scales.  Outputs overlap nothing else but as said.  One launch (none when T == 0).
+ */
+bsmma_status branch_enter(const void* x, bsmma_dtype x_dtype, int64_t T, int64_t H, bsmma_norm norm,
+                          float eps, const float* weight, const float* bias, bsmma_operand form,
+                          void* out, void* scales, bsmma_stream stream);
+bsmma_status branch_leave(const void* x, bsmma_dtype x_dtype, const void* y, bsmma_dtype y_dtype,
+                          int64_t T, int64_t H, bsmma_norm norm, float eps, const float* weight,
+                          const float* bias, const void* gate, int64_t gate_rows, float x_scale,
+                          float y_scale, float p, const int64_t* rng, void* out, bsmma_norm next,
+                          float next_eps, const float* next_weight, const float* next_bias,
+                          bsmma_operand next_form, void* next_out, void* next_scales,
+                          bsmma_stream stream);
+
+/*
+ * branch_enter_backward -- dx = (gradient of h in x, for dh) + dres, and dweight and dbias FP32
+ *   [H], the sums over the rows.  dh [T][H] in the branch's type, x, dres (what reaches x past
+ *   the branch; NULL: 0) and dx in the stream's.
+ * branch_leave_backward -- from dout [T][H] of the stream's type and the forward call's y and
+ *   parameters: dy (the branch's type), dx = x_scale * dout (NULL: not wanted), dweight, dbias
+ *   FP32 [H], dgate FP32 in gate's shape.  rng has to hold what it held in the forward call.
+ *   A NULL dweight, dbias or dgate is not computed.  The statistics are taken from x or y
+ *   again, so the forward calls keep nothing.  Sums are FP32, by runs of rows whose number
+ *   depends on T and H alone: the same call gives the same bits.
+ *   Two launches (one when neither dweight, dbias nor a dgate shared by rows is wanted) and, with
+ *   any of them, branch_backward_workspace_bytes(T, H) bytes of the stream's workspace
+ *   (mx_gemm's; reserve it before a capture).  T == 0 writes dweight = dbias = 0.
+ */
+bsmma_status branch_enter_backward(const void* dh, bsmma_dtype h_dtype, const void* x,
+                                   bsmma_dtype x_dtype, int64_t T, int64_t H, bsmma_norm norm,
+                                   float eps, const float* weight, const void* dres, void* dx,
+                                   float* dweight, float* dbias, bsmma_stream stream);
+bsmma_status branch_leave_backward(const void* dout, bsmma_dtype x_dtype, const void* y,
+                                   bsmma_dtype y_dtype, int64_t T, int64_t H, bsmma_norm norm,
+                                   float eps, const float* weight, const float* bias,
+                                   const void* gate, int64_t gate_rows, float x_scale,
+                                   float y_scale, float p, const int64_t* rng, void* dy, void* dx,
+                                   float* dweight, float* dbias, float* dgate, bsmma_stream stream);
+int64_t branch_backward_workspace_bytes(int64_t T, int64_t H);
+
+/*
+ * dropout -- y[i] = kept(i) ? x[i] / (1 - p) : 0 for n values (BF16 or FP32), the mask of
+ *   branch_leave for the same rng and a [T][H] tensor's values in row-major order.  Its gradient is the same
+ *   call on dy.  y may be x.  p == 0 copies (rng may be NULL).
+ * Preconditions: 0 <= n < 2^40, 0 <= p < 1, 16-byte-aligned x and y, 8-byte-aligned rng.  One
+ *   launch (none when n == 0).
+ */
+bsmma_status dropout(const void* x, bsmma_dtype dtype, int64_t n, float p, const int64_t* rng, void* y,
+                     bsmma_stream stream);
 
 /* Grows the current (device, stream) scale workspace to at least `bytes` and allocates
  * the stream's split workspace if it has none (call before capturing mx_gemm or
