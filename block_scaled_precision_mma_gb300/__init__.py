@@ -14,7 +14,8 @@ Functions mirror the C names:
 * :func:`mx_quantize`, :func:`fp8_group_quantize`, :func:`fp8_block_quantize` -- the
   quantisers that make the GEMMs' operands from BF16 / FP32 tensors.
 * :func:`moe_route`, :func:`moe_route_backward`, :func:`moe_plan`, :func:`moe_combine`,
-  :func:`moe_combine_backward` -- the expert layer around the grouped GEMMs.
+  :func:`moe_combine_backward` -- the expert layer around the grouped GEMMs; :func:`moe_step` --
+  its experts and their weighted sum for a few tokens.
 * :func:`int8_quantize`, :func:`int8_gemm`, :func:`grouped_int8_gemm` -- INT8 products with
   scales for each token and channel.
 * :func:`branch_enter`, :func:`branch_leave`, :func:`branch_enter_backward`,
@@ -36,7 +37,7 @@ from .build import LIB_PATH, build
 __all__ = ["mx_gemm", "mx_gemm_tiled", "mx_gemm_noalloc", "grouped_fp8_gemm", "grouped_fp8_pack_weights",
            "grouped_bf16_gemm",
            "moe_route", "moe_route_backward", "moe_plan", "moe_plan_workspace_bytes",
-           "moe_combine", "moe_combine_backward",
+           "moe_combine", "moe_combine_backward", "moe_step", "moe_step_workspace_bytes",
            "int8_quantize", "int8_gemm", "grouped_int8_gemm",
            "branch_enter", "branch_enter_backward", "branch_leave", "branch_leave_backward",
            "branch_backward_workspace_bytes", "dropout",
@@ -122,6 +123,9 @@ def load(path: str | None = None):
         lib.int8_quantize.argtypes = [p, i32, i64, i64, p, i32, i64, p, p, p]
         lib.int8_gemm.argtypes = [p, p, p, p, p, p, i32, i64, i64, i64, p]
         lib.grouped_int8_gemm.argtypes = [p, p, p, p, p, i32, p, i64, i32, i64, i64, p]
+        lib.moe_step.argtypes = [p, i64, i64, p, p, i32, i32, i64, i32, p, p, p, p, i32, p, p]
+        lib.moe_step_workspace_bytes.argtypes = [i64, i32, i64]
+        lib.moe_step_workspace_bytes.restype = i64
         lib.branch_enter.argtypes = [p, i32, i64, i64, i32, f32, p, p, i32, p, p, p]
         lib.branch_leave.argtypes = [p, i32, p, i32, i64, i64, i32, f32, p, p, p, i64, f32, f32, f32,
                                      p, p, i32, f32, p, p, i32, p, p, p]
@@ -141,7 +145,7 @@ def load(path: str | None = None):
                      "fp8_block_quantize", "mx_gemm_bias_act", "mx_gemm_tiled_bias_act",
                      "bsmma_autotune_configure", "moe_route", "moe_route_backward", "moe_plan",
                      "moe_combine", "moe_combine_backward", "int8_quantize", "int8_gemm",
-                     "grouped_int8_gemm", "branch_enter", "branch_leave", "branch_enter_backward",
+                     "grouped_int8_gemm", "moe_step", "branch_enter", "branch_leave", "branch_enter_backward",
                      "branch_leave_backward", "dropout"):
             getattr(lib, name).restype = i32
         _lib = lib
@@ -682,6 +686,43 @@ def branch_leave_backward(dout, y, weight=None, bias=None, norm="none", eps=1e-6
                                         p, _ptr(rng), _ptr(dy), _ptr(dx), _ptr(dweight), _ptr(dbias),
                                         _ptr(dgate), _stream(stream)), "branch_leave_backward")
     return dy, dout if dx is None else dx, dweight, dbias, dgate
+
+
+def moe_step_workspace_bytes(T: int, k: int, F: int) -> int:
+    """Workspace of :func:`moe_step` (reserve it before a capture)."""
+    return int(load().moe_step_workspace_bytes(T, k, F))
+
+
+def moe_step(x, ids, weights, w_in, w_out, s_in=None, s_out=None, fmt="bf16", act="silu", out=None,
+             stream=None):
+    """out[t] = sum_j weights[t, j] * W2[e] (act(Wg[e] x[t]) * (Wu[e] x[t])), e = ids[t, j], for a few
+    tokens (T <= 64, T * k <= 1024) x [T, H] BF16; ids int32 and weights float32 [T, k] from
+    :func:`moe_route`.  w_in [E, 2F, H] has the gate's rows first, w_out is [E, H, F]; ``fmt``:
+    'bf16'; 'int8' with float32 scales [E, 2F] and [E, H]; 'e4m3', 'e5m2' or 'e2m1' (uint8 codes, E2M1
+    packed) with uint8 E8M0 scales [E, 2F, H/32] and [E, H, F/32].  See ``moe_step`` in bsmma.h."""
+    T, H = x.shape
+    k = ids.shape[1]
+    E, F = w_in.shape[0], w_in.shape[1] // 2
+    pack = 2 if fmt == "e2m1" else 1
+    dtype = torch.bfloat16 if fmt == "bf16" else torch.int8 if fmt == "int8" else torch.uint8
+    _expect(x, torch.bfloat16, (T, H), "x")
+    _expect(ids, torch.int32, (T, k), "ids")
+    _expect(weights, torch.float32, (T, k), "weights")
+    _expect(w_in, dtype, (E, 2 * F, H // pack), "w_in")
+    _expect(w_out, dtype, (E, H, F // pack), "w_out")
+    if (fmt == "bf16") != (s_in is None) or (fmt == "bf16") != (s_out is None):
+        raise ValueError("s_in and s_out go with codes, not with BF16 weights")
+    if fmt == "int8":
+        _expect(s_in, torch.float32, (E, 2 * F), "s_in")
+        _expect(s_out, torch.float32, (E, H), "s_out")
+    else:
+        _expect(s_in, torch.uint8, (E, 2 * F, H // 32), "s_in")
+        _expect(s_out, torch.uint8, (E, H, F // 32), "s_out")
+    out = _output(out, torch.bfloat16, (T, H), x, "out")
+    _check(load().moe_step(_ptr(x), T, H, _ptr(ids), _ptr(weights), k, E, F, OPERANDS[fmt], _ptr(w_in),
+                           _ptr(s_in), _ptr(w_out), _ptr(s_out), ACTIVATIONS[act], _ptr(out),
+                           _stream(stream)), "moe_step")
+    return out
 
 
 def branch_backward_workspace_bytes(T: int, H: int) -> int:

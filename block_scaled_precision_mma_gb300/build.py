@@ -15,7 +15,7 @@ SOURCES = ["api.cu", "relayout.cu", "mx_gemm.cu", "grouped_gemm.cu", "noalloc.cu
            "mx_gemm_2sm.cu", "quantize.cu", "autotune.cu", "grouped_bf16.cu",
            "moe.cu", "int8_gemm.cu", "int8_pair.cu",
            "branch.cu", "branch_grad.cu", "branch_grad_bf16.cu", "branch_grad_f32.cu",
-           "branch_grad_mixed.cu"]
+           "branch_grad_mixed.cu", "moe_step.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 

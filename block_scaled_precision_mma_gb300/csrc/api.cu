@@ -20,6 +20,7 @@
 #include "branch.h"
 #include "epilogue.cuh"
 #include "internal.h"
+#include "moe_step.h"
 #include "ptx.cuh"
 #include "store_stage.cuh"
 
@@ -913,6 +914,53 @@ bsmma_status dropout(const void* x, bsmma_dtype dtype, int64_t n, float p, const
   if (!x || !y) return BSMMA_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(y)) return BSMMA_ERR_MISALIGNED;
   return launch_dropout(x, dtype == BSMMA_F32, n, d, y, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int64_t moe_step_workspace_bytes(int64_t T, int k, int64_t F) {
+  if (T <= 0 || T > 64 || k < 1 || T * k > 1024 || F <= 0 || F > 65536) return 0;
+  return T * k * F * 2;
+}
+
+bsmma_status moe_step(const void* x, int64_t T, int64_t H, const int32_t* ids, const float* weights,
+                      int k, int E, int64_t F, bsmma_operand form, const void* w_in,
+                      const void* s_in, const void* w_out, const void* s_out,
+                      bsmma_activation act, void* out, bsmma_stream stream) {
+  if (form == BSMMA_OPERAND_F32) return BSMMA_ERR_UNSUPPORTED;
+  if (form < BSMMA_OPERAND_BF16 || form > BSMMA_OPERAND_E2M1 || act < BSMMA_ACT_NONE || act > BSMMA_ACT_SILU)
+    return BSMMA_ERR_INVALID_ARG;
+  if (T < 0 || T > 64 || k < 1 || k > 1024 || T * k > 1024 || E < 1 || E > 1024 || H <= 0 || H > 65536 ||
+      F <= 0 || F > 65536)
+    return BSMMA_ERR_INVALID_ARG;
+  const int piece = form == BSMMA_OPERAND_BF16 ? 8 : form == BSMMA_OPERAND_INT8 ? 16 : 32;
+  if (H % piece != 0 || F % piece != 0) return BSMMA_ERR_INVALID_ARG;
+  if ((form != BSMMA_OPERAND_BF16) != (s_in != nullptr) || (form != BSMMA_OPERAND_BF16) != (s_out != nullptr))
+    return BSMMA_ERR_INVALID_ARG;
+  if (T == 0) return BSMMA_OK;
+  if (!x || !ids || !weights || !w_in || !w_out || !out) return BSMMA_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w_in) || !aligned16(w_out) || !aligned16(out) || !aligned_to(ids, 4) ||
+      !aligned_to(weights, 4) || (form == BSMMA_OPERAND_INT8 && (!aligned_to(s_in, 4) || !aligned_to(s_out, 4))))
+    return BSMMA_ERR_MISALIGNED;
+  StepArgs a = {};
+  a.x = x;
+  a.T = T;
+  a.H = H;
+  a.ids = ids;
+  a.weights = weights;
+  a.k = k;
+  a.E = E;
+  a.F = F;
+  a.w_in = w_in;
+  a.s_in = s_in;
+  a.w_out = w_out;
+  a.s_out = s_out;
+  a.act = act;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const StreamLock lock(s);
+  void* ws = nullptr;
+  BSMMA_TRY(get_workspace(moe_step_workspace_bytes(T, k, F), s, &ws));
+  a.inner = static_cast<__nv_bfloat16*>(ws);
+  return launch_moe_step(a, form, s);
 }
 
 bsmma_status bsmma_reserve_workspace(int64_t bytes, bsmma_stream stream) {

@@ -186,8 +186,8 @@ constexpr int kBlock = TPR < 128 ? 128 : TPR;
 template <bool F32, int TPR, int V>
 __global__ void __launch_bounds__(kBlock<TPR>) enter_kernel(const EnterArgs p) {
   __shared__ float part[3 * 32];
-  grid_launch_dependents();
   grid_dependency_wait();
+  grid_launch_dependents();
   const int tid = threadIdx.x % TPR, vecs = static_cast<int>(p.H / 8);
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kBlock<TPR> / TPR) + threadIdx.x / TPR;
   if (t >= p.T) return;   // (whole warps, and no barrier where a row is a warp's)
@@ -207,8 +207,8 @@ __global__ void __launch_bounds__(kBlock<TPR>) enter_kernel(const EnterArgs p) {
 template <bool XF, bool YF, int TPR, int V>
 __global__ void __launch_bounds__(kBlock<TPR>) leave_kernel(const LeaveArgs p) {
   __shared__ float part[5 * 32];
-  grid_launch_dependents();
   grid_dependency_wait();
+  grid_launch_dependents();
   const int tid = threadIdx.x % TPR, vecs = static_cast<int>(p.H / 8);
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kBlock<TPR> / TPR) + threadIdx.x / TPR;
   if (t >= p.T) return;
@@ -262,8 +262,8 @@ constexpr int kDropPieces = 4;
 template <bool F32>
 __global__ void __launch_bounds__(256) dropout_kernel(const void* x, int64_t n, const DropArgs drop,
                                                       void* y) {
-  grid_launch_dependents();
   grid_dependency_wait();
+  grid_launch_dependents();
   Philox gen = {};
   if (drop.threshold) gen = philox_of(drop.rng);
   const int64_t whole = n / 8;

@@ -1,5 +1,5 @@
 // branch.h -- host-side interface of the residual branch's operators (branch.cu,
-// branch_grad_*.cu) and of the decoding step's expert layer (moe_step.cu).
+// branch_grad*.cu).
 #pragma once
 #include "internal.h"
 

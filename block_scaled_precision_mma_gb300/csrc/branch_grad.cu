@@ -32,8 +32,8 @@ struct SumParams {
 };
 __global__ void __launch_bounds__(32 * kSumLanes) sum_kernel(const SumParams p) {
   __shared__ float part[kSumLanes][32];
-  grid_launch_dependents();
   grid_dependency_wait();
+  grid_launch_dependents();
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   const float* from;

@@ -44,8 +44,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, 1) grad_kernel(const Gr
   constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
   constexpr int kPart = TPR < 128 ? 1 : 2 * (TPR / 32);
   __shared__ float part[2][2][kPart];   // by the row's parity: one barrier a reduction
-  grid_launch_dependents();
   grid_dependency_wait();
+  grid_launch_dependents();
   const BranchGradArgs& a = p.a;
   const int tid = threadIdx.x % TPR;
   const int worker = static_cast<int>(blockIdx.x) * kRows + static_cast<int>(threadIdx.x) / TPR;

@@ -528,6 +528,38 @@ bsmma_status moe_combine_backward(const void* dout, bsmma_dtype dtype, int64_t H
                                   int64_t T, int k, void* dY, float* dweights, bsmma_stream stream);
 
 /*
+ * moe_step -- the experts and the weighted sum of a few tokens in two launches, without the
+ *   expert order and the gathered rows of the grouped products:
+ *     out[t] = sum_j weights[t][j] * W2[e] (act(Wg[e] x[t]) * (Wu[e] x[t])),  e = ids[t][j]
+ *   Only experts that some token chose are read, each once (their columns in tiles of 8, 16 or
+ *   32 tokens; an expert with more columns is read once a tile).
+ *   x BF16 [T][H]; ids int32 [T][k] and weights FP32 [T][k] as moe_route writes them (a slot
+ *   with an id outside 0..E-1 adds nothing, whatever its weight; a token without any gives a
+ *   row of zeros; an expert may be named twice); out BF16 [T][H].
+ *   w_in [E][2F][H], the gate's F rows (Wg) and then the F of Wu; w_out [E][H][F] (W2), both
+ *   of one form:
+ *     BSMMA_OPERAND_BF16   BF16, no scales (s_in, s_out NULL)
+ *     BSMMA_OPERAND_INT8   INT8 codes, FP32 scale for each row: s_in [E][2F], s_out [E][H]
+ *     BSMMA_OPERAND_E4M3, _E5M2, _E2M1   MX codes and E8M0 scales as mx_quantize writes them
+ *                          rowwise: s_in [E][2F][H/32], s_out [E][H][F/32].  Codes that stand
+ *                          for NaN or infinity are not supported (they count as finite numbers).
+ *   act  a bsmma_activation, in FP32; BSMMA_ACT_NONE leaves the product of the two halves.
+ *   Products are summed in FP32; the inner row act(..) * (..) is rounded to BF16 once, as the
+ *   second product's operand; the sum over j is FP32, rounded once.  The sums' order depends
+ *   on the sizes and the ids alone.
+ * Preconditions: T >= 0, k >= 1, T <= 64, T * k <= 1024, 1 <= E <= 1024; H and F at least one
+ *   piece of 16 bytes of codes and whole ones (BF16: H, F % 8 == 0; INT8: % 16; MX: % 32) and
+ *   at most 65536; 16-byte-aligned x, w_in, w_out and out, 4-byte-aligned ids, weights and
+ *   scales.  out overlaps no input.  Takes moe_step_workspace_bytes(T, k, F) bytes of the
+ *   stream's workspace (mx_gemm's; reserve it before a capture).  T == 0 is a no-op.
+ */
+bsmma_status moe_step(const void* x, int64_t T, int64_t H, const int32_t* ids, const float* weights,
+                      int k, int E, int64_t F, bsmma_operand form, const void* w_in,
+                      const void* s_in, const void* w_out, const void* s_out,
+                      bsmma_activation act, void* out, bsmma_stream stream);
+int64_t moe_step_workspace_bytes(int64_t T, int k, int64_t F);
+
+/*
  * The residual branch.  What a block does to the residual stream x around its products f
  * (the source pages have no counterpart; their GEMMs' operands are what it makes):
  *     h = n(x) * weight + bias                                         branch_enter
