@@ -124,7 +124,7 @@ def load(path: str | None = None):
         lib.int8_gemm.argtypes = [p, p, p, p, p, p, i32, i64, i64, i64, p]
         lib.grouped_int8_gemm.argtypes = [p, p, p, p, p, i32, p, i64, i32, i64, i64, p]
         lib.moe_step.argtypes = [p, i64, i64, p, p, i32, i32, i64, i32, p, p, p, p, i32, p, p]
-        lib.moe_step_workspace_bytes.argtypes = [i64, i32, i64]
+        lib.moe_step_workspace_bytes.argtypes = [i64, i32, i64, i64]
         lib.moe_step_workspace_bytes.restype = i64
         lib.branch_enter.argtypes = [p, i32, i64, i64, i32, f32, p, p, i32, p, p, p]
         lib.branch_leave.argtypes = [p, i32, p, i32, i64, i64, i32, f32, p, p, p, i64, f32, f32, f32,
@@ -688,15 +688,15 @@ def branch_leave_backward(dout, y, weight=None, bias=None, norm="none", eps=1e-6
     return dy, dout if dx is None else dx, dweight, dbias, dgate
 
 
-def moe_step_workspace_bytes(T: int, k: int, F: int) -> int:
+def moe_step_workspace_bytes(T: int, k: int, H: int, F: int) -> int:
     """Workspace of :func:`moe_step` (reserve it before a capture)."""
-    return int(load().moe_step_workspace_bytes(T, k, F))
+    return int(load().moe_step_workspace_bytes(T, k, H, F))
 
 
 def moe_step(x, ids, weights, w_in, w_out, s_in=None, s_out=None, fmt="bf16", act="silu", out=None,
              stream=None):
     """out[t] = sum_j weights[t, j] * W2[e] (act(Wg[e] x[t]) * (Wu[e] x[t])), e = ids[t, j], for a few
-    tokens (T <= 64, T * k <= 1024) x [T, H] BF16; ids int32 and weights float32 [T, k] from
+    tokens (T <= 32, T * k <= 1024) x [T, H] BF16; ids int32 and weights float32 [T, k] from
     :func:`moe_route`.  w_in [E, 2F, H] has the gate's rows first, w_out is [E, H, F]; ``fmt``:
     'bf16'; 'int8' with float32 scales [E, 2F] and [E, H]; 'e4m3', 'e5m2' or 'e2m1' (uint8 codes, E2M1
     packed) with uint8 E8M0 scales [E, 2F, H/32] and [E, H, F/32].  See ``moe_step`` in bsmma.h."""

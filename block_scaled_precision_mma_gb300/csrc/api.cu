@@ -916,9 +916,9 @@ bsmma_status dropout(const void* x, bsmma_dtype dtype, int64_t n, float p, const
   return launch_dropout(x, dtype == BSMMA_F32, n, d, y, reinterpret_cast<cudaStream_t>(stream));
 }
 
-int64_t moe_step_workspace_bytes(int64_t T, int k, int64_t F) {
-  if (T <= 0 || T > 64 || k < 1 || T * k > 1024 || F <= 0 || F > 65536) return 0;
-  return T * k * F * 2;
+int64_t moe_step_workspace_bytes(int64_t T, int k, int64_t H, int64_t F) {
+  if (T <= 0 || T > 32 || k < 1 || T * k > 1024 || H <= 0 || H > 65536 || F <= 0 || F > 65536) return 0;
+  return step_workspace_bytes(T, k, H, F);
 }
 
 bsmma_status moe_step(const void* x, int64_t T, int64_t H, const int32_t* ids, const float* weights,
@@ -928,7 +928,7 @@ bsmma_status moe_step(const void* x, int64_t T, int64_t H, const int32_t* ids, c
   if (form == BSMMA_OPERAND_F32) return BSMMA_ERR_UNSUPPORTED;
   if (form < BSMMA_OPERAND_BF16 || form > BSMMA_OPERAND_E2M1 || act < BSMMA_ACT_NONE || act > BSMMA_ACT_SILU)
     return BSMMA_ERR_INVALID_ARG;
-  if (T < 0 || T > 64 || k < 1 || k > 1024 || T * k > 1024 || E < 1 || E > 1024 || H <= 0 || H > 65536 ||
+  if (T < 0 || T > 32 || k < 1 || k > 1024 || T * k > 1024 || E < 1 || E > 1024 || H <= 0 || H > 65536 ||
       F <= 0 || F > 65536)
     return BSMMA_ERR_INVALID_ARG;
   const int piece = form == BSMMA_OPERAND_BF16 ? 8 : form == BSMMA_OPERAND_INT8 ? 16 : 32;
@@ -958,9 +958,8 @@ bsmma_status moe_step(const void* x, int64_t T, int64_t H, const int32_t* ids, c
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const StreamLock lock(s);
   void* ws = nullptr;
-  BSMMA_TRY(get_workspace(moe_step_workspace_bytes(T, k, F), s, &ws));
-  a.inner = static_cast<__nv_bfloat16*>(ws);
-  return launch_moe_step(a, form, s);
+  BSMMA_TRY(get_workspace(step_workspace_bytes(T, k, H, F), s, &ws));
+  return launch_moe_step(a, form, ws, s);
 }
 
 bsmma_status bsmma_reserve_workspace(int64_t bytes, bsmma_stream stream) {

@@ -1,27 +1,35 @@
-// moe_step.cu -- the experts and the weighted sum of a few tokens, in two launches.
+// moe_step.cu -- the experts and the weighted sum of a few tokens.
 //
-// What bounds it is reading the chosen experts' weights once, so both kernels are built around
-// keeping their bytes in flight: one block of 16 warps an SM, each warp with a ring of
-// asynchronous copies of its own that runs on from one unit of work to the next.  A lane reads
-// back what it copied itself, so the ring needs no barrier, and since both operands of a product
-// may take K in any order, a lane's 16 bytes of a weight row and the same K of a token go into
-// the matrix instruction as they are.
+// What bounds it is reading the chosen experts' weights once, so the two products' kernels are
+// built around keeping their bytes in flight with few instructions a byte: one block of 16 warps
+// an SM, each warp with a ring of asynchronous copies of its own that runs on from one unit of
+// work to the next.
 //
 // The products use mma.sync with the weights as the 16-row operand and up to 8 * NT tokens as
 // columns: with a row or a few an expert the tensor cores wait for memory whatever their
-// instruction, and the few-row form needs no tile of tokens in shared memory.  Weights are widened
-// to BF16 in registers, exactly: INT8 codes are BF16 values, and an MX code's bits, moved into
-// BF16's fields, are the code times a power of two, which one multiplication by another takes
-// to the scaled value.  Sums are FP32.
+// instruction, and this form needs no tile of tokens in shared memory.  BF16 weights meet BF16
+// tokens.  Codes are widened to FP16, which holds every INT8, E4M3, E5M2 and E2M1 value, by
+// one conversion for two values; the tokens are then FP16 too, times a power of two of their
+// own that brings their largest value to 2^14 .. 2^15: a BF16 value's eight bits fit, and only
+// what is below 2^-29 of the largest loses any.  (Widening to BF16 instead, by moving bits and a
+// multiplication, kept the integer pipe busy at 52% with DRAM at 38%: 363 MB of E4M3 experts
+// 115 us.)  The 32 K of a matrix step are one MX block, so a block's scale multiplies its sum,
+// four FMAs for 16 rows, and no weight.  Sums are FP32.
 //
-// First launch: units of 16 inner columns (16 rows of Wg and the 16 of Wu) of one expert; the
-// warps share out K, their sums meet in shared memory, and the inner row leaves in BF16.  Gate and
-// up rows are put into the upper and lower half of the same 16-row operand, so that the lane
-// that has a gate's sum has its up's too.  Second launch: units of 16 output columns over all
-// chosen experts, the warps sharing out (expert, K) in runs; a warp adds an expert's columns, times
-// their tokens' weights, to its tokens' sums, and the warps' sums are added in order.  It starts
-// under the first one (programmatic launch) and has its ring full when the inner rows are done.
+// First launch: who takes what (the chosen experts and their columns), and the tokens in FP16.
+// Second: units of 32 inner columns (32 rows of Wg and the 32 of Wu) of one expert; the warps share
+// out K and the rows, their sums meet in shared memory, and the inner row leaves in BF16, or
+// in FP16 with a power of two for each 32 values.  Gate and up rows are put into the upper and
+// lower half of the same 16-row operand, so that the lane that has a gate's sum has its up's
+// too.  Third: units of 32 output columns over all chosen experts, the warps sharing out
+// (expert, K) in runs; a warp adds an expert's columns, times their tokens' weights, to its
+// tokens' sums, and the warps' sums are added in order.  Each starts under the one before
+// (programmatic launch), the third with its rings full when the inner rows are done.
+#include <cuda_fp16.h>
+
 #include <algorithm>
+#include <cfloat>
+#include <type_traits>
 
 #include "epilogue.cuh"
 #include "moe_step.h"
@@ -33,117 +41,121 @@ namespace {
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kMaxSlots = 1024, kMaxExperts = 1024;
+constexpr int kTableBytes = 8 + kMaxSlots * 10;   // sizeof(WeightedTable)
 
 // ------------------------------------------------------------------------- weights
-// How a form's codes lie in a lane's 16 bytes, by granules of eight consecutive K.
+// A stage is 128 bytes of each of a warp's 32 rows: `kBlocks` blocks of 32 K, of which a row's
+// four lanes have eight consecutive values each, `kLaneBytes`.
+constexpr int kRowStage = 128;
 template <int FORM>
 struct Form {
-  static constexpr bool kMx = FORM >= BSMMA_OPERAND_E4M3;
-  static constexpr int kGranules = FORM == BSMMA_OPERAND_BF16 ? 1 : FORM == BSMMA_OPERAND_E2M1 ? 4 : 2;
-  static constexpr int kLaneK = 8 * kGranules;     // K of a lane's 16 bytes
-  static constexpr int kPieceK = 4 * kLaneK;       // of the four lanes that share a row
-  // a scaled value is its code's bits in BF16's fields times 2^(scale + this - 127) (as a
-  // BF16 exponent field: scale + this)
-  static constexpr int kField = FORM == BSMMA_OPERAND_E4M3 ? 120 : FORM == BSMMA_OPERAND_E5M2 ? 112 : 126;
-};
-
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-// The multiplier(s) of a block's E8M0 scale, twice in a word.  A scale too large for one
-// multiplier (2^8 and more for E4M3) takes a second; 255 is NaN.
-struct MxScale {
-  uint32_t first, second;   // second 0: one multiplier
-};
-template <int FORM>
-__device__ __forceinline__ MxScale mx_scale(uint32_t code) {
-  MxScale m;
-  const uint32_t field = code + Form<FORM>::kField;
-  m.first = field << 7;
-  m.second = 0;
-  if (field > 254) {
-    m.first = static_cast<uint32_t>(Form<FORM>::kField + 127) << 7;
-    m.second = code == 255 ? 0x7FC07FC0u : code << 7 | code << 23;
+  static constexpr bool kMx = FORM >= BSMMA_OPERAND_E4M3, kBf16 = FORM == BSMMA_OPERAND_BF16;
+  static constexpr int kLaneBytes = kBf16 ? 16 : FORM == BSMMA_OPERAND_E2M1 ? 4 : 8;
+  static constexpr int kBlockBytes = 4 * kLaneBytes, kBlocks = kRowStage / kBlockBytes;
+  static constexpr int kStageK = 32 * kBlocks;
+  static constexpr int kStage = 32 * (kRowStage + (kMx ? kBlocks : 0));   // a warp's, scales behind the codes
+  // Block b of row g (of a set of eight) lies at block b ^ g's place of the row, so that the lanes
+  // of one shared-memory access are in different banks.
+  static __device__ __forceinline__ uint32_t place(int g, int byte) {
+    return g * kRowStage + (byte ^ (g & (kBlocks - 1)) * kBlockBytes);
   }
-  m.first |= m.first << 16;
-  return m;
+};
+template <int FORM>
+__device__ __forceinline__ int64_t row_bytes(int64_t K) {
+  return FORM == BSMMA_OPERAND_BF16 ? 2 * K : FORM == BSMMA_OPERAND_E2M1 ? K / 2 : K;
 }
 
-// Granule q of a lane's 16 bytes as four pairs of BF16 values.
+// Four E8M0 codes as FP32 (through BF16, which holds 2^-127 and has a NaN for 255).
+__device__ __forceinline__ void e8m0x4(uint32_t codes, float (&f)[4]) {
+  uint32_t lo, hi;
+  asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.bf16x2.ue8m0x2 %0, a;\n\tcvt.rn.bf16x2.ue8m0x2 %1, b;}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
+  f[0] = __uint_as_float(lo << 16);
+  f[1] = __uint_as_float(lo & 0xFFFF0000u);
+  f[2] = __uint_as_float(hi << 16);
+  f[3] = __uint_as_float(hi & 0xFFFF0000u);
+}
+
+// A lane's eight weights of a block, at shared address `at`, as four pairs (BF16 or FP16).
 template <int FORM>
-__device__ __forceinline__ void decode(const uint4& w, int q, const MxScale& s, uint32_t (&o)[4]) {
+__device__ __forceinline__ void load_weights(uint32_t at, uint32_t (&o)[4]) {
   if constexpr (FORM == BSMMA_OPERAND_BF16) {
-    o[0] = w.x, o[1] = w.y, o[2] = w.z, o[3] = w.w;
-  } else if constexpr (FORM == BSMMA_OPERAND_INT8) {
-    const uint32_t c[2] = {q ? w.z : w.x, q ? w.w : w.y};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // 0x43 above a code's byte: its low seven bits are 128 + those, its sign 128 or 256, and the
-      // difference is the code
-      const uint32_t v = __byte_perm(c[i >> 1], 0x43434343u, i & 1 ? 0x4342 : 0x4140);
-      o[i] = sub_bf16x2(v & 0xFF7FFF7Fu, v & 0xFF80FF80u);
-    }
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+                 : "r"(at));
   } else if constexpr (FORM == BSMMA_OPERAND_E2M1) {
-    const uint32_t c = q == 0 ? w.x : q == 1 ? w.y : q == 2 ? w.z : w.w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {   // K i and i + 4 of the granule
-      const uint32_t t = c >> (4 * i);
-      o[i] = (t & 0x00070007u) << 6 | (t & 0x00080008u) << 12;
-    }
+    uint32_t w;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at));
+    asm("{.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;}"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+        : "r"(w));
   } else {
-    constexpr int kShift = FORM == BSMMA_OPERAND_E4M3 ? 4 : 3;
-    constexpr uint32_t kBits = 0x7F007F00u >> kShift;
-    const uint32_t c[2] = {q ? w.z : w.x, q ? w.w : w.y};
+    uint32_t w[2];
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t v = __byte_perm(c[i >> 1], 0u, i & 1 ? 0x3424 : 0x1404);
-      o[i] = (v >> kShift & kBits) | (v & 0x80008000u);
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (FORM == BSMMA_OPERAND_INT8) {
+        // 0x64 above a byte u is 1024 + u in FP16; u = code + 128
+        const uint32_t u = w[i] ^ 0x80808080u, off = 0x64806480u;   // 1152
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o[2 * i]) : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(off));
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o[2 * i + 1]) : "r"(__byte_perm(u, 0x64646464u, 0x4342)), "r"(off));
+      } else if constexpr (FORM == BSMMA_OPERAND_E4M3) {
+        asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;}"
+            : "=r"(o[2 * i]), "=r"(o[2 * i + 1])
+            : "r"(w[i]));
+      } else {   // E5M2 is the upper byte of FP16
+        o[2 * i] = __byte_perm(w[i], 0u, 0x1404);
+        o[2 * i + 1] = __byte_perm(w[i], 0u, 0x3424);
+      }
     }
   }
-  if constexpr (Form<FORM>::kMx) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = mul_bf16x2(o[i], s.first);
-    if (s.second)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = mul_bf16x2(o[i], s.second);
-  }
-}
-// A token's granule in the order of decode()'s pairs.
-template <int FORM>
-__device__ __forceinline__ void order_token(uint4& x) {
-  if constexpr (FORM == BSMMA_OPERAND_E2M1)
-    x = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
-                   __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t a0, const uint32_t a1,
-                                         const uint32_t a2, const uint32_t a3, const uint32_t b0,
-                                         const uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// d += (or, FIRST, =) the product of a 16-row operand and eight columns over 16 K.
+template <bool BF16, bool FIRST>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else if constexpr (FIRST)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void cp_async_16(uint32_t dst_smem, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src),
                "r"(in ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ uint4 lds16(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr));
-  return v;
+__device__ __forceinline__ void cp_async_16(uint32_t dst_smem, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_word(uint32_t dst_smem, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst_smem), "l"(src), "r"(in ? 4 : 0)
+               : "memory");
+}
+
+// A value's power of two and FP16 form: the largest finite magnitude of a group of values goes to
+// 2^14 .. 2^15 (FP16 ends at 65504).  2^-127 bounds the power below, so that it is a float.
+__device__ __forceinline__ float group_power(float amax) {
+  const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14;
+  return amax > 0.f ? __uint_as_float(static_cast<uint32_t>(max(e, -126) + 127) << 23) : 1.f;
 }
 
 // ------------------------------------------------------------------------- who takes what
@@ -152,11 +164,13 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 struct Table {
   int entries;
   uint16_t expert[kMaxSlots];       // of each tile
-  uint16_t first[kMaxSlots];        // its first column
-  uint16_t count[kMaxSlots];
-  uint16_t slot[kMaxSlots];         // of each column (token * k + choice)
-  float weight[kMaxSlots];
+  uint16_t first[kMaxSlots + 2];    // its first column; it ends where the next begins
+  uint16_t slot[kMaxSlots];         // of each column: token * k + choice
 };
+struct WeightedTable : Table {
+  float weight[kMaxSlots];          // of each column
+};
+static_assert(sizeof(WeightedTable) == kTableBytes, "workspace layout");
 struct TableScratch {
   int start[kMaxExperts];           // counts, then first columns
   int32_t ids[kMaxSlots];
@@ -164,7 +178,7 @@ struct TableScratch {
 };
 constexpr uint16_t kNone = 0xFFFF;
 
-__device__ __forceinline__ void build_table(Table& t, TableScratch& s, const StepArgs& a, int tile) {
+__device__ __forceinline__ void build_table(WeightedTable& t, TableScratch& s, const StepArgs& a, int tile) {
   const int tid = threadIdx.x, lane = tid & 31, slots = static_cast<int>(a.T) * a.k;
   for (int e = tid; e < a.E; e += kThreads) s.start[e] = 0;
   for (int i = tid; i < slots; i += kThreads) {
@@ -206,12 +220,14 @@ __device__ __forceinline__ void build_table(Table& t, TableScratch& s, const Ste
       for (int i = 0; i < tiles; ++i) {
         t.expert[t0 + i] = static_cast<uint16_t>(e);
         t.first[t0 + i] = static_cast<uint16_t>(c0 + i * tile);
-        t.count[t0 + i] = static_cast<uint16_t>(min(tile, n - i * tile));
       }
       column += __shfl_sync(kFull, in, 31);
       entry += __shfl_sync(kFull, it, 31);
     }
-    if (lane == 0) t.entries = entry;
+    if (lane == 0) {
+      t.entries = entry;
+      t.first[entry] = static_cast<uint16_t>(column);
+    }
   }
   __syncthreads();
   for (int i = tid; i < slots; i += kThreads) {
@@ -226,55 +242,191 @@ __device__ __forceinline__ void build_table(Table& t, TableScratch& s, const Ste
   __syncthreads();
 }
 
-// ------------------------------------------------------------------------- products
-// A lane's share of one stage: PIECES * 16 bytes of each of ROWS rows, 512 bytes a piece and warp.
-constexpr int kPieces = 2;
-template <int ROWS>
-constexpr int kStageBytes = ROWS * kPieces * 512;
-
-// Multiplies a stage's weights into acc.  MT operands of 16 rows: operand m has rows
-// 2 m (upper half, lane's row g) and 2 m + 1 (lower half) of the stage's ROWS = 2 * MT.
-// x: rows of the columns (a lane's column of each 8), or nullptr; k: the lane's first K.
-template <int FORM, int MT, int NT>
-__device__ __forceinline__ void multiply(float (&acc)[MT][NT][4], uint32_t ring,
-                                         const __nv_bfloat16* const (&x)[NT], int nt_used, int64_t k,
-                                         int64_t K, const uint8_t* const (&scale)[2 * MT]) {
-  using F = Form<FORM>;
+// Block 0: the table.  Block 1 + t (forms with codes): token t in FP16 and its power of two.
+__global__ void __launch_bounds__(kThreads) step_order_kernel(const StepArgs a, int tile) {
+  __shared__ TableScratch scratch;
+  __shared__ uint32_t part[kWarps];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (blockIdx.x == 0) {
+    build_table(*static_cast<WeightedTable*>(a.table), scratch, a, tile);
+    return;
+  }
+  const int64_t t = blockIdx.x - 1;
+  const uint4* x = static_cast<const uint4*>(a.x) + t * (a.H / 8);
+  uint4* out = reinterpret_cast<uint4*>(a.x16) + t * (a.H / 8);
+  const int vecs = static_cast<int>(a.H / 8);
+  uint32_t amax = 0;   // of the finite values, as bits of a BF16 value
+  for (int v = threadIdx.x; v < vecs; v += kThreads) {
+    const uint4 q = x[v];
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-  for (int p = 0; p < kPieces; ++p) {
-    const int64_t kp = k + p * F::kPieceK;
-    const bool in = kp < K;
-    MxScale s[2 * MT] = {};
-    if constexpr (F::kMx) {
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int r = 0; r < 2 * MT; ++r) s[r] = mx_scale<FORM>(in && scale[r] ? scale[r][kp >> 5] : 127u);
-    }
-    uint4 w[2 * MT];
-#pragma unroll
-    for (int r = 0; r < 2 * MT; ++r) w[r] = lds16(ring + (r * kPieces + p) * 512);
-#pragma unroll
-    for (int q = 0; q < F::kGranules; ++q) {
-      uint4 b[NT];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        b[n] = make_uint4(0, 0, 0, 0);
-        if (in && x[n]) b[n] = *reinterpret_cast<const uint4*>(x[n] + kp + 8 * q);
-        order_token<FORM>(b[n]);
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t m = w[j] >> (16 * h) & 0x7FFFu;
+        if (m < 0x7F80u) amax = max(amax, m);
       }
+  }
+  amax = __reduce_max_sync(kFull, amax);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
+  __syncthreads();
+  amax = __reduce_max_sync(kFull, part[threadIdx.x & (kWarps - 1)]);
+  const float power = group_power(__uint_as_float(amax << 16)), inv = 1.f / power;
+  for (int v = threadIdx.x; v < vecs; v += kThreads) {
+    const uint4 q = x[v];
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint32_t o[4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        uint32_t hi[4], lo[4];
-        decode<FORM>(w[2 * m], q, s[2 * m], hi);
-        decode<FORM>(w[2 * m + 1], q, s[2 * m + 1], lo);
+    for (int j = 0; j < 4; ++j) {
+      const __half2 h = __floats2half2_rn(__uint_as_float(w[j] << 16) * inv,
+                                          __uint_as_float(w[j] & 0xFFFF0000u) * inv);
+      o[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    out[v] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  if (threadIdx.x == 0) a.x_power[t] = power;
+}
+
+// The table in shared memory (every thread of the block).
+__device__ __forceinline__ void copy_table(Table& to, const Table& from, int slots) {
+  const int tid = threadIdx.x;
+  if (tid == 0) to.entries = from.entries;
+  for (int i = tid; i < slots + 1; i += kThreads) {
+    to.first[i] = from.first[i];
+    if (i == slots) break;
+    to.slot[i] = from.slot[i];
+    to.expert[i] = from.expert[i];
+  }
+}
+
+// ------------------------------------------------------------------------- products
+// A run of stages of a warp's 32 rows, four sets of eight: set r starts set_bytes[r] behind
+// the first (a set past the matrix repeats the first: its sums are not used).
+struct Source {
+  const uint8_t* row;       // the lane's row of the first set (lane (g, t): row g), its chunk t
+  const uint8_t* scales;    // the scales of row lane (of 32)
+};
+struct Sets {
+  int64_t bytes[4];         // of codes
+};
+
+// Starts the copies of stage `stage` (from the row's first byte): lane (g, t) copies the 16-byte
+// chunks t and t + 4 of its row in each set, lane l the scales of row l.
+template <int FORM>
+__device__ __forceinline__ void load_stage(uint32_t to, const Source& from, const Sets& sets, int stage,
+                                           int64_t bytes, int64_t blocks, bool words) {
+  using F = Form<FORM>;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int64_t at = static_cast<int64_t>(stage) * kRowStage;
+  const uint32_t d0 = to + F::place(g, 16 * t), d1 = to + F::place(g, 64 + 16 * t);
+  const uint8_t* src = from.row + at;
+  if (at + kRowStage <= bytes) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          if (n < nt_used) {
-            mma_bf16(acc[m][n], hi[0], lo[0], hi[1], lo[1], b[n].x, b[n].y);
-            mma_bf16(acc[m][n], hi[2], lo[2], hi[3], lo[3], b[n].z, b[n].w);
-          }
+    for (int r = 0; r < 4; ++r) {
+      cp_async_16(d0 + r * 1024, src + sets.bytes[r]);
+      cp_async_16(d1 + r * 1024, src + sets.bytes[r] + 64);
+    }
+  } else {   // the end of K: what is past it counts as zero
+    const bool in0 = at + 16 * t < bytes, in1 = at + 64 + 16 * t < bytes;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      cp_async_16(d0 + r * 1024, in0 ? src + sets.bytes[r] : from.row, in0);
+      cp_async_16(d1 + r * 1024, in1 ? src + sets.bytes[r] + 64 : from.row, in1);
+    }
+  }
+  if constexpr (F::kMx) {
+    if (words) {
+      const int64_t b = static_cast<int64_t>(stage) * F::kBlocks;
+#pragma unroll
+      for (int i = 0; i < F::kBlocks; i += 4) {
+        const bool in = b + i < blocks;
+        cp_async_word(to + 4096 + lane * F::kBlocks + i, in ? from.scales + b + i : from.scales, in);
       }
     }
   }
+}
+
+// Multiplies a stage's weights into acc: operand m has set 2 m in its upper and set 2 m + 1 in
+// its lower eight rows.  x: the lane's column (of each eight) from its first K of the stage on; left:
+// K from there to the end; powers (POWERS): of the blocks of the lane's two result columns.
+// scale(r, b): where the scales cannot be copied by words, block b's of the lane's row of set r.
+template <int FORM, int NT, bool POWERS, typename Scale>
+__device__ __forceinline__ void multiply(float (&acc)[2][NT][4], uint32_t ring, const uint16_t* const (&x)[NT],
+                                         int64_t left, const float* const (&powers)[NT][2],
+                                         const Scale& scale, bool words) {
+  using F = Form<FORM>;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const bool whole = left + 8 * t >= F::kStageK;   // (uniform)
+  constexpr int kQuads = F::kMx ? 4 : F::kBlocks;
+#pragma unroll
+  for (int b0 = 0; b0 < F::kBlocks; b0 += kQuads) {
+    float sw[4][4];
+    if constexpr (F::kMx) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        uint32_t codes = 0;
+        if (words)
+          asm volatile("ld.shared.b32 %0, [%1];"
+                       : "=r"(codes)
+                       : "r"(ring + 4096 + (r * 8 + g) * F::kBlocks + b0));
+        else
+          for (int j = 0; j < 4; ++j)
+            if (32 * (b0 + j) < left + 8 * t) codes |= scale(r, b0 + j) << (8 * j);
+        e8m0x4(codes, sw[r]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kQuads; ++j) {
+      const int b = b0 + j;
+      uint4 xv[NT];
+      float p[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        p[n][0] = p[n][1] = 1.f;
+        if (whole) {
+          xv[n] = *reinterpret_cast<const uint4*>(x[n] + 32 * b);
+          if constexpr (POWERS) p[n][0] = powers[n][0][b], p[n][1] = powers[n][1][b];
+        } else {
+          xv[n] = make_uint4(0, 0, 0, 0);
+          if (32 * b < left) xv[n] = *reinterpret_cast<const uint4*>(x[n] + 32 * b);
+          if constexpr (POWERS)
+            if (32 * b < left + 8 * t) p[n][0] = powers[n][0][b], p[n][1] = powers[n][1][b];
+        }
+      }
+      const uint32_t at = ring + F::place(g, b * F::kBlockBytes + t * F::kLaneBytes);
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        uint32_t hi[4], lo[4];
+        load_weights<FORM>(at + 2 * m * 1024, hi);
+        load_weights<FORM>(at + (2 * m + 1) * 1024, lo);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if constexpr (F::kMx || POWERS) {
+            float c[4];
+            mma<F::kBf16, true>(c, hi[0], lo[0], hi[1], lo[1], xv[n].x, xv[n].y);
+            mma<F::kBf16, false>(c, hi[2], lo[2], hi[3], lo[3], xv[n].z, xv[n].w);
+            float s[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              s[i] = F::kMx ? sw[2 * m + (i >> 1)][j] : p[n][i & 1];
+              if (F::kMx && POWERS) s[i] *= p[n][i & 1];
+              acc[m][n][i] = fmaf(c[i], s[i], acc[m][n][i]);
+            }
+          } else {
+            mma<F::kBf16, false>(acc[m][n], hi[0], lo[0], hi[1], lo[1], xv[n].x, xv[n].y);
+            mma<F::kBf16, false>(acc[m][n], hi[2], lo[2], hi[3], lo[3], xv[n].z, xv[n].w);
+          }
+        }
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float load_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ float activate(float x, int act) {
@@ -283,21 +435,32 @@ __device__ __forceinline__ float activate(float x, int act) {
   return act == BSMMA_ACT_SILU ? x / (1.f + expf(-x)) : x;
 }
 
-// Bytes of a row of K codes.
-template <int FORM>
-__device__ __forceinline__ int64_t row_bytes(int64_t K) {
-  return FORM == BSMMA_OPERAND_BF16 ? 2 * K : FORM == BSMMA_OPERAND_E2M1 ? K / 2 : K;
+// Which expert, columns and rows a unit has: an expert's units are its tiles of rows, and
+// within one its tiles of columns, so that what several of those read is read at one time.
+struct Unit {
+  int entry, rows;
+};
+__device__ __forceinline__ Unit unit_of(const Table& table, int u, int tiles) {
+  int lead = u / tiles;
+  const int expert = table.expert[lead];
+  int end = lead + 1;
+  while (lead > 0 && table.expert[lead - 1] == expert) --lead;
+  while (end < table.entries && table.expert[end] == expert) ++end;
+  const int i = u - lead * tiles, c = end - lead;
+  return c == 1 ? Unit{lead, i} : Unit{lead + i % c, i / c};
 }
 
-// The inner rows: [slot][F] BF16.
+// The inner rows.  Warp w has rows of half w & 1 (16 inner columns) and every eighth stage of K
+// from w >> 1 on.
+constexpr int kGroups = kWarps / 2;
 template <int FORM, int NT>
 struct InCfg {
-  static constexpr int kStage = kStageBytes<4>;
-  static constexpr int kStages = NT == 1 ? 3 : 2;
-  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kStage = Form<FORM>::kStage;
   static constexpr int kSums = kWarps * 2 * NT * 512;
+  static constexpr int kStages = (232448 - kSums - static_cast<int>(sizeof(Table))) / (kWarps * kStage);
+  static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kBytes = kRing + kSums + static_cast<int>(sizeof(Table));
-  static_assert(sizeof(TableScratch) <= kRing && kBytes <= 232448, "shared memory budget");
+  static_assert(kStages >= 2, "one stage in flight");
 };
 
 template <int FORM, int NT>
@@ -305,46 +468,45 @@ __global__ void __launch_bounds__(kThreads, 1) step_in_kernel(const StepArgs a) 
   using C = InCfg<FORM, NT>;
   using F = Form<FORM>;
   extern __shared__ __align__(128) uint8_t smem[];
-  float4* sums = reinterpret_cast<float4*>(smem + C::kRing);
+  float4* sums = reinterpret_cast<float4*>(smem + C::kRing);   // [operand of 4][NT][group][lane]
   Table& table = *reinterpret_cast<Table*>(smem + C::kRing + C::kSums);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int half = warp & 1, group = warp >> 1;
   grid_dependency_wait();
   grid_launch_dependents();
-  build_table(table, *reinterpret_cast<TableScratch*>(smem), a, 8 * NT);
+  copy_table(table, *static_cast<const WeightedTable*>(a.table), static_cast<int>(a.T) * a.k);
+  __syncthreads();
 
-  const int64_t K = a.H, bytes = row_bytes<FORM>(K);
-  const int tiles = static_cast<int>((a.F + 15) / 16), units = table.entries * tiles;
-  const int stages = static_cast<int>((K + kPieces * F::kPieceK - 1) / (kPieces * F::kPieceK));
-  const int mine = warp < stages ? (stages - warp + kWarps - 1) / kWarps : 0;   // of a unit
-  const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStage + lane * 16;
-  // row r (0, 2: gate, 1, 3: up) of a unit: its number in the expert, or -1
-  auto row_of = [&](int u, int r) -> int64_t {
-    const int64_t f = static_cast<int64_t>(u % tiles) * 16 + 8 * (r >> 1) + g;
-    return f < a.F ? (r & 1 ? a.F + f : f) : -1;
+  const int64_t K = a.H, bytes = row_bytes<FORM>(K), blocks = K / 32;
+  const bool words = F::kMx && blocks % 4 == 0 && (reinterpret_cast<uintptr_t>(a.s_in) & 3) == 0;
+  const int tiles = static_cast<int>((a.F + 31) / 32), units = table.entries * tiles;
+  const int stages = static_cast<int>((K + F::kStageK - 1) / F::kStageK);
+  const int mine = group < stages ? (stages - group + kGroups - 1) / kGroups : 0;   // of a unit
+  const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStage;
+  // A unit's sets of rows from its first row f of the half on (F % 8 == 0: a set is in the matrix
+  // or not): Wg's f .. f + 7, Wu's, Wg's f + 8 .. f + 15, Wu's.
+  auto set_row = [&](int64_t f, int r) { return (r & 1 ? a.F : 0) + (r >> 1 && f + 8 < a.F ? 8 : 0); };
+  auto first_row = [&](int rows) {
+    const int64_t f = static_cast<int64_t>(rows) * 32 + 16 * half;
+    return f < a.F ? f : 0;
   };
   // the loads run ahead of the products through the block's units
   int lu = blockIdx.x, li = 0, slot = 0;
-  const uint8_t* src[4];
+  Source src = {};
+  Sets sets = {};
   auto enter_unit = [&] {
     if (lu >= units) return;
-    const int64_t e = table.expert[lu / tiles];
+    const Unit w = unit_of(table, lu, tiles);
+    const int64_t f = first_row(w.rows), base = static_cast<int64_t>(table.expert[w.entry]) * 2 * a.F + f;
+    src.row = static_cast<const uint8_t*>(a.w_in) + (base + g) * bytes + 16 * t;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t row = row_of(lu, r);
-      src[r] = row < 0 ? nullptr : static_cast<const uint8_t*>(a.w_in) + (e * 2 * a.F + row) * bytes;
-    }
+    for (int r = 0; r < 4; ++r) sets.bytes[r] = set_row(f, r) * bytes;
+    if constexpr (F::kMx)
+      src.scales = static_cast<const uint8_t*>(a.s_in) + (base + set_row(f, lane >> 3) + (lane & 7)) * blocks;
   };
   auto load = [&] {
     if (mine && lu < units) {
-      const int64_t at = static_cast<int64_t>(warp + li * kWarps) * (kPieces * 64) + t * 16;
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int p = 0; p < kPieces; ++p) {
-          const bool in = src[r] && at + 64 * p < bytes;
-          cp_async_16(ring + slot * C::kStage + (r * kPieces + p) * 512,
-                      in ? src[r] + at + 64 * p : static_cast<const uint8_t*>(a.w_in), in);
-        }
+      load_stage<FORM>(ring + slot * C::kStage, src, sets, group + li * kGroups, bytes, blocks, words);
       if (++li == mine) {
         li = 0;
         lu += gridDim.x;
@@ -360,133 +522,175 @@ __global__ void __launch_bounds__(kThreads, 1) step_in_kernel(const StepArgs a) 
 
   int at = 0;
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int entry = u / tiles, first = table.first[entry], count = table.count[entry];
-    const int nt_used = (count + 7) / 8;
-    const __nv_bfloat16* x[NT];
+    const Unit here = unit_of(table, u, tiles);
+    const int first = table.first[here.entry], count = table.first[here.entry + 1] - first;
+    const int64_t expert = table.expert[here.entry], f_first = first_row(here.rows);
+    const uint8_t* scales = static_cast<const uint8_t*>(a.s_in) + (expert * 2 * a.F + f_first + g) * blocks;
+    // n_cols tiles of eight columns; a column past the entry's repeats its last
+    auto products = [&](auto n_cols) {
+      constexpr int N = decltype(n_cols)::value;
+      const uint16_t* x[N];
+      const float* const no_powers[N][2] = {};
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-      x[n] = 8 * n + g < count
-                 ? static_cast<const __nv_bfloat16*>(a.x) + table.slot[first + 8 * n + g] / a.k * a.H
-                 : nullptr;
-    const uint8_t* scale[4] = {};
-    if constexpr (F::kMx) {
+      for (int n = 0; n < N; ++n)
+        x[n] = (F::kBf16 ? static_cast<const uint16_t*>(a.x) : a.x16) +
+               table.slot[first + min(8 * n + g, count - 1)] / a.k * a.H + group * F::kStageK + 8 * t;
+      int64_t k = group * F::kStageK;
+      float acc[2][N][4] = {};
+      for (int i = 0; i < mine; ++i) {
+        cp_async_wait<C::kStages - 2>();
+        __syncwarp();   // the other lanes' copies, and their reads of the slot that is filled next
+        load();
+        multiply<FORM, N, false>(
+            acc, ring + at * C::kStage, x, K - k - 8 * t, no_powers,
+            [&](int r, int b) -> uint32_t { return scales[set_row(f_first, r) * blocks + k / 32 + b]; }, words);
+        k += kGroups * F::kStageK;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t row = row_of(u, r);
-        if (row >= 0)
-          scale[r] = static_cast<const uint8_t*>(a.s_in) + (table.expert[entry] * 2 * a.F + row) * (K / 32);
+        for (int n = 0; n < N; ++n) x[n] += kGroups * F::kStageK;
+        at = at + 1 == C::kStages ? 0 : at + 1;
       }
-    }
-    float acc[2][NT][4] = {};
-    for (int i = 0; i < mine; ++i) {
-      load();
-      cp_async_wait<C::kStages - 1>();
-      multiply<FORM, 2, NT>(acc, ring + at * C::kStage, x, nt_used,
-                            static_cast<int64_t>(warp + i * kWarps) * (kPieces * F::kPieceK) + t * F::kLaneK,
-                            K, scale);
-      at = at + 1 == C::kStages ? 0 : at + 1;
-    }
-    __syncthreads();   // the sums of the unit before have been read
+      __syncthreads();   // the sums of the unit before have been read
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (n < nt_used)
-          sums[((m * NT + n) * kWarps + warp) * 32 + lane] =
+        for (int n = 0; n < N; ++n)
+          sums[(((2 * half + m) * NT + n) * kGroups + group) * 32 + lane] =
               make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
+    };
+    if (NT == 1 || count <= 8) products(std::integral_constant<int, 1>{});
+    else products(std::integral_constant<int, NT>{});
     __syncthreads();
-    // a warp an operand and eight columns
-    for (int j = warp; j < 2 * NT; j += kWarps) {
-      const int m = j / NT, n = j % NT;
-      if (n >= nt_used) continue;
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    // a warp eight columns: inner values 8 m + g of columns 2 t and 2 t + 1
+    if (8 * warp < count) {
+      const int n = warp;
+      const int64_t f0 = static_cast<int64_t>(here.rows) * 32;
+      int64_t slots[2];
+      float power[2] = {1.f, 1.f};
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 v = sums[(j * kWarps + w) * 32 + lane];
-        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+      for (int c = 0; c < 2; ++c) {
+        const int col = 8 * n + 2 * t + c;
+        slots[c] = col < count ? table.slot[first + col] : -1;
+        if (!F::kBf16 && slots[c] >= 0) power[c] = a.x_power[slots[c] / a.k];
       }
-      const int64_t f = static_cast<int64_t>(u % tiles) * 16 + 8 * m + g;
-      if (f >= a.F) continue;
-      if constexpr (FORM == BSMMA_OPERAND_INT8) {
-        const float* of = static_cast<const float*>(a.s_in) + table.expert[entry] * 2 * a.F;
-        const float sg = of[f], su = of[a.F + f];
-        s.x *= sg, s.y *= sg, s.z *= su, s.w *= su;
-      }
-      const float v[2] = {activate(s.x, a.act) * s.z, activate(s.y, a.act) * s.w};
+      float v[2][4], amax[2] = {0.f, 0.f};
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (8 * n + 2 * t + c < count)
-          a.inner[table.slot[first + 8 * n + 2 * t + c] * a.F + f] = __float2bfloat16_rn(v[c]);
+      for (int m = 0; m < 4; ++m) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kGroups; ++w) {
+          const float4 q = sums[((m * NT + n) * kGroups + w) * 32 + lane];
+          s.x += q.x, s.y += q.y, s.z += q.z, s.w += q.w;
+        }
+        const int64_t f = f0 + 8 * m + g;
+        if constexpr (FORM == BSMMA_OPERAND_INT8) {
+          const float* of = static_cast<const float*>(a.s_in) + expert * 2 * a.F;
+          const float sg = f < a.F ? of[f] : 0.f, su = f < a.F ? of[a.F + f] : 0.f;
+          s.x *= sg, s.y *= sg, s.z *= su, s.w *= su;
+        }
+        v[0][m] = activate(s.x * power[0], a.act) * (s.z * power[0]);
+        v[1][m] = activate(s.y * power[1], a.act) * (s.w * power[1]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (f < a.F && fabsf(v[c][m]) <= FLT_MAX) amax[c] = fmaxf(amax[c], fabsf(v[c][m]));
+      }
+      float inv[2] = {1.f, 1.f};
+      if constexpr (!F::kBf16) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) amax[c] = fmaxf(amax[c], __shfl_xor_sync(kFull, amax[c], o));
+          const float p = group_power(amax[c]);
+          inv[c] = 1.f / p;
+          if (g == 0 && slots[c] >= 0) a.inner_power[slots[c] * tiles + here.rows] = p;
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int64_t f = f0 + 8 * m + g;
+        if (f >= a.F) continue;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (slots[c] < 0) continue;
+          uint16_t* to = a.inner + slots[c] * a.F + f;
+          if constexpr (F::kBf16) *to = __bfloat16_as_ushort(__float2bfloat16_rn(v[c][m]));
+          else *to = __half_as_ushort(__float2half_rn(v[c][m] * inv[c]));
+        }
+      }
     }
   }
   cp_async_wait_all();
 }
 
-// The output rows.
+// The output rows.  A cluster of `kCluster` blocks shares a unit of 32 rows: (expert, K) in runs over
+// all of their warps.
 template <int FORM, int NT>
 struct OutCfg {
-  static constexpr int kStage = kStageBytes<2>;
-  static constexpr int kStages = 4;
+  static constexpr int kStage = Form<FORM>::kStage;
+  static constexpr int kTokens = NT == 1 ? 8 : 32;
+  static constexpr int kSums = (kWarps + 2) * kTokens * 32 * 4;   // of each warp, and twice the block's
+  static constexpr int kStages = (232448 - kSums - kTableBytes) / (kWarps * kStage);
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kFixed = kRing + static_cast<int>(sizeof(Table));
-  static int bytes(int64_t T) { return kFixed + kWarps * static_cast<int>(T) * 16 * 4; }
-  static_assert(sizeof(TableScratch) <= kRing && kFixed + kWarps * 64 * 64 <= 232448, "shared memory budget");
+  static constexpr int kBytes = kRing + kTableBytes + kSums;
+  static_assert(kStages >= 2, "one stage in flight");
 };
 
 template <int FORM, int NT>
-__global__ void __launch_bounds__(kThreads, 1) step_out_kernel(const StepArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) step_out_kernel(const StepArgs a, int cluster) {
   using C = OutCfg<FORM, NT>;
   using F = Form<FORM>;
+  constexpr bool kPowers = !F::kBf16;
   extern __shared__ __align__(128) uint8_t smem[];
-  Table& table = *reinterpret_cast<Table*>(smem + C::kRing);
-  float* sums = reinterpret_cast<float*>(smem + C::kFixed);   // [warp][token][16]
+  WeightedTable& table = *reinterpret_cast<WeightedTable*>(smem + C::kRing);
+  float* sums = reinterpret_cast<float*>(smem + C::kRing + kTableBytes);   // [warp][token][32]
+  const int T = static_cast<int>(a.T), values = T * 32;
+  float* totals = sums + kWarps * values;                                  // [2][token][32]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int T = static_cast<int>(a.T);
-  // ids, weights and w_out were there before the first launch began (it waited for what was
-  // before it); only the inner rows are waited for
-  build_table(table, *reinterpret_cast<TableScratch*>(smem), a, 8 * NT);
-  float* own = sums + warp * T * 16;
-  for (int i = lane; i < T * 16; i += 32) own[i] = 0.f;
-  __syncwarp();
+  const int rank = static_cast<int>(blockIdx.x) % cluster, clusters = static_cast<int>(gridDim.x) / cluster;
+  // the table and w_out were there before the second launch let this one start (it waited for
+  // what was before it); only the inner rows are waited for
+  float* own = sums + warp * values;
+  for (int i = lane; i < values; i += 32) own[i] = 0.f;
+  const WeightedTable& from = *static_cast<const WeightedTable*>(a.table);
+  copy_table(table, from, T * a.k);
+  for (int i = threadIdx.x; i < T * a.k; i += kThreads) table.weight[i] = from.weight[i];
+  __syncthreads();
 
-  const int64_t K = a.F, bytes = row_bytes<FORM>(K);
-  const int units = static_cast<int>((a.H + 15) / 16);
-  const int stages = static_cast<int>((K + kPieces * F::kPieceK - 1) / (kPieces * F::kPieceK));
+  const int64_t K = a.F, bytes = row_bytes<FORM>(K), blocks = K / 32, power_blocks = (K + 31) / 32;
+  const bool words = F::kMx && blocks % 4 == 0 && (reinterpret_cast<uintptr_t>(a.s_out) & 3) == 0;
+  const int units = static_cast<int>((a.H + 31) / 32);
+  const int stages = static_cast<int>((K + F::kStageK - 1) / F::kStageK);
   // the warp's run of (entry, stage)
   const int64_t items = static_cast<int64_t>(table.entries) * stages;
-  const int64_t i0 = items * warp / kWarps, i1 = items * (warp + 1) / kWarps;
+  const int runner = rank * kWarps + warp, runners = cluster * kWarps;
+  const int64_t i0 = items * runner / runners, i1 = items * (runner + 1) / runners;
   const int entry0 = static_cast<int>(i0 / stages), stage0 = static_cast<int>(i0 % stages);
-  const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStage + lane * 16;
+  const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStage;
+  // sets of rows: H % 8 == 0
+  auto set_row = [&](int64_t row0, int r) { return row0 + 8 * r < a.H ? 8 * r : 0; };
 
-  int lu = blockIdx.x, slot = 0, le = entry0, ls = stage0;
+  int lu = static_cast<int>(blockIdx.x) / cluster, slot = 0, le = entry0, ls = stage0;
   int64_t left = i1 - i0;
-  const uint8_t* src[2];
+  Source src = {};
+  Sets sets = {};
   auto rows_of = [&] {
-    const int64_t e = table.expert[le];
+    const int64_t row0 = static_cast<int64_t>(lu) * 32;
+    const int64_t base = static_cast<int64_t>(table.expert[le]) * a.H + row0;
+    src.row = static_cast<const uint8_t*>(a.w_out) + (base + g) * bytes + 16 * t;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int64_t row = static_cast<int64_t>(lu) * 16 + 8 * r + g;
-      src[r] = row < a.H ? static_cast<const uint8_t*>(a.w_out) + (e * a.H + row) * bytes : nullptr;
-    }
+    for (int r = 0; r < 4; ++r) sets.bytes[r] = set_row(row0, r) * bytes;
+    if constexpr (F::kMx)
+      src.scales = static_cast<const uint8_t*>(a.s_out) + (base + set_row(row0, lane >> 3) + (lane & 7)) * blocks;
   };
-  if (i1 > i0) rows_of();
+  if (i1 > i0 && lu < units) rows_of();
   auto load = [&] {
     if (i1 > i0 && lu < units) {
-      const int64_t at = static_cast<int64_t>(ls) * (kPieces * 64) + t * 16;
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int p = 0; p < kPieces; ++p) {
-          const bool in = src[r] && at + 64 * p < bytes;
-          cp_async_16(ring + slot * C::kStage + (r * kPieces + p) * 512,
-                      in ? src[r] + at + 64 * p : static_cast<const uint8_t*>(a.w_out), in);
-        }
+      load_stage<FORM>(ring + slot * C::kStage, src, sets, ls, bytes, blocks, words);
       bool moved = false;
       if (++ls == stages) ls = 0, ++le, moved = true;
       if (--left == 0) {
         left = i1 - i0;
         le = entry0, ls = stage0, moved = true;
-        lu += gridDim.x;
+        lu += clusters;
       }
       if (moved && lu < units) rows_of();
     }
@@ -497,108 +701,201 @@ __global__ void __launch_bounds__(kThreads, 1) step_out_kernel(const StepArgs a)
   for (int i = 0; i < C::kStages - 1; ++i) load();
   grid_dependency_wait();
 
-  int at = 0;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const int64_t row0 = static_cast<int64_t>(u) * 16;
+  int at = 0, turn = 0;
+  for (int u = static_cast<int>(blockIdx.x) / cluster; u < units; u += clusters, turn ^= 1) {
+    const int64_t row0 = static_cast<int64_t>(u) * 32;
     int entry = entry0, stage = stage0;
     int64_t todo = i1 - i0;
     while (todo > 0) {
       const int n_here = static_cast<int>(todo < stages - stage ? todo : stages - stage);
-      const int first = table.first[entry], count = table.count[entry], nt_used = (count + 7) / 8;
-      const int64_t e = table.expert[entry];
-      const __nv_bfloat16* x[NT];
+      const int first = table.first[entry], count = table.first[entry + 1] - first;
+      const int64_t base = static_cast<int64_t>(table.expert[entry]) * a.H + row0;
+      const uint8_t* scales = static_cast<const uint8_t*>(a.s_out) + (base + g) * blocks;
+      auto products = [&](auto n_cols) {
+        constexpr int N = decltype(n_cols)::value;
+        int64_t k = static_cast<int64_t>(stage) * F::kStageK;
+        const uint16_t* x[N];
+        const float* powers[N][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        x[n] = 8 * n + g < count ? a.inner + table.slot[first + 8 * n + g] * a.F : nullptr;
-      const uint8_t* scale[2] = {};
-      if constexpr (F::kMx) {
+        for (int n = 0; n < N; ++n) {
+          x[n] = a.inner + table.slot[first + min(8 * n + g, count - 1)] * a.F + k + 8 * t;
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          if (row0 + 8 * r + g < a.H)
-            scale[r] = static_cast<const uint8_t*>(a.s_out) + (e * a.H + row0 + 8 * r + g) * (K / 32);
-      }
-      float acc[1][NT][4] = {};
-      for (int i = 0; i < n_here; ++i) {
-        load();
-        cp_async_wait<C::kStages - 1>();
-        multiply<FORM, 1, NT>(acc, ring + at * C::kStage, x, nt_used,
-                              static_cast<int64_t>(stage + i) * (kPieces * F::kPieceK) + t * F::kLaneK, K,
-                              scale);
-        at = at + 1 == C::kStages ? 0 : at + 1;
-      }
-      float rs[2] = {1.f, 1.f};
-      if constexpr (FORM == BSMMA_OPERAND_INT8) {
+          for (int c = 0; c < 2; ++c)
+            powers[n][c] = a.inner_power + table.slot[first + min(8 * n + 2 * t + c, count - 1)] * power_blocks + k / 32;
+        }
+        float acc[2][N][4] = {};
+        for (int i = 0; i < n_here; ++i) {
+          cp_async_wait<C::kStages - 2>();
+          __syncwarp();
+          load();
+          multiply<FORM, N, kPowers>(
+              acc, ring + at * C::kStage, x, K - k - 8 * t, powers,
+              [&](int r, int b) -> uint32_t { return scales[set_row(row0, r) * blocks + k / 32 + b]; }, words);
+          k += F::kStageK;
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          if (row0 + 8 * r + g < a.H) rs[r] = static_cast<const float*>(a.s_out)[e * a.H + row0 + 8 * r + g];
-      }
-      // an entry's columns are different tokens, so no two lanes add to one place
+          for (int n = 0; n < N; ++n) {
+            x[n] += F::kStageK;
+            powers[n][0] += F::kBlocks;
+            powers[n][1] += F::kBlocks;
+          }
+          at = at + 1 == C::kStages ? 0 : at + 1;
+        }
+        if constexpr (FORM == BSMMA_OPERAND_INT8) {
+          const float* of = static_cast<const float*>(a.s_out) + base + g;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+          for (int r = 0; r < 4; ++r) {
+            const float s = of[set_row(row0, r)];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int col = 8 * n + 2 * t + c;
-          if (col < count) {
-            const float w = table.weight[first + col];
-            float* to = own + table.slot[first + col] / a.k * 16 + g;
-            to[0] = fmaf(w, acc[0][n][c] * rs[0], to[0]);
-            to[8] = fmaf(w, acc[0][n][2 + c] * rs[1], to[8]);
+            for (int n = 0; n < N; ++n) {
+              acc[r >> 1][n][2 * (r & 1)] *= s;
+              acc[r >> 1][n][2 * (r & 1) + 1] *= s;
+            }
           }
         }
+        // an entry's columns are different tokens, so no two lanes add to one place
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int col = 8 * n + 2 * t + c;
+            if (col < count) {
+              const float w = table.weight[first + col];
+              float* to = own + table.slot[first + col] / a.k * 32 + g;
+#pragma unroll
+              for (int r = 0; r < 4; ++r) to[8 * r] = fmaf(w, acc[r >> 1][n][2 * (r & 1) + c], to[8 * r]);
+            }
+          }
+      };
+      if (NT == 1 || count <= 8) products(std::integral_constant<int, 1>{});
+      else products(std::integral_constant<int, NT>{});
       __syncwarp();
       todo -= n_here;
       stage = 0;
       ++entry;
     }
+    // the warps' sums, then (over the cluster) the blocks'; each block finishes its share of them
     __syncthreads();
-    for (int i = threadIdx.x; i < T * 16; i += kThreads) {
+    float* total = totals + turn * values;
+    for (int i = threadIdx.x; i < values; i += kThreads) {
       float s = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        s += sums[w * T * 16 + i];
-        sums[w * T * 16 + i] = 0.f;
+        s += sums[w * values + i];
+        sums[w * values + i] = 0.f;
       }
-      if (row0 + (i & 15) < a.H) a.out[(i >> 4) * a.H + row0 + (i & 15)] = __float2bfloat16_rn(s);
+      total[i] = s;
     }
-    __syncthreads();
+    if (cluster > 1) cluster_sync();
+    else __syncthreads();
+    for (int i = rank * kThreads + static_cast<int>(threadIdx.x); i < values; i += cluster * kThreads) {
+      float s = 0.f;
+      if (cluster > 1) {
+        for (int b = 0; b < cluster; ++b) s += load_cluster(map_to_cta(smem_u32(total + i), b));
+      } else {
+        s = total[i];
+      }
+      if (row0 + (i & 31) < a.H) a.out[(i >> 5) * a.H + row0 + (i & 31)] = __float2bfloat16_rn(s);
+    }
   }
   cp_async_wait_all();
+  if (cluster > 1) cluster_sync();   // the others have read this block's sums
+}
+
+// Blocks that share a unit of the third launch: as many as make its last wave fullest.
+template <int FORM, int NT>
+bsmma_status launch_out(const StepArgs& a, const DeviceInfo* dev, cudaStream_t stream) {
+  using C = OutCfg<FORM, NT>;
+  static PerDevice smem_set, fit[4];
+  bsmma_status st = smem_set.allow_smem(dev->device, step_out_kernel<FORM, NT>, C::kBytes);
+  if (st != BSMMA_OK) return st;
+  const int64_t units = (a.H + 31) / 32;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {1, 1, 1};
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  double best = 0;
+  int shared = 1, active = 1;
+  for (int i = 0; i < 4; ++i) {
+    const int c = 1 << i;
+    int n = 0;   // clusters that run at one time
+    st = fit[i].get(dev->device, &n, [&](int* v) {
+      if (c == 1) {
+        *v = dev->sm_count;
+        return BSMMA_OK;
+      }
+      cudaLaunchConfig_t q = cfg;
+      q.gridDim = dim3(static_cast<unsigned>(c));
+      attr[1].val.clusterDim.x = static_cast<unsigned>(c);
+      q.attrs = attr + 1;
+      q.numAttrs = 1;
+      return cuda_ok(cudaOccupancyMaxActiveClusters(v, step_out_kernel<FORM, NT>, &q));
+    });
+    if (st != BSMMA_OK) return st;
+    if (n < 1) continue;
+    const double waves = static_cast<double>((units + n - 1) / n) / c;
+    if (i == 0 || waves < 0.95 * best) best = waves, shared = c, active = n;
+  }
+  attr[1].val.clusterDim.x = static_cast<unsigned>(shared);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(units, active) * shared));
+  cfg.numAttrs = 2;
+  return cuda_ok(cudaLaunchKernelEx(&cfg, step_out_kernel<FORM, NT>, a, shared));
 }
 
 template <int FORM, int NT>
 bsmma_status launch_step(const StepArgs& a, const DeviceInfo* dev, cudaStream_t stream) {
-  static PerDevice in_set, out_set;
-  constexpr int kIn = InCfg<FORM, NT>::kBytes, kOut = OutCfg<FORM, NT>::kFixed + kWarps * 64 * 64;
+  static PerDevice in_set;
+  constexpr int kIn = InCfg<FORM, NT>::kBytes;
   bsmma_status st = in_set.allow_smem(dev->device, step_in_kernel<FORM, NT>, kIn);
-  if (st == BSMMA_OK) st = out_set.allow_smem(dev->device, step_out_kernel<FORM, NT>, kOut);
   if (st != BSMMA_OK) return st;
   const int64_t slots = a.T * a.k;   // at most this many entries
-  const int64_t in_units = slots * ((a.F + 15) / 16), out_units = (a.H + 15) / 16;
+  const int64_t in_units = slots * ((a.F + 31) / 32);
   const unsigned in_blocks = static_cast<unsigned>(std::min<int64_t>(in_units, dev->sm_count));
-  const unsigned out_blocks = static_cast<unsigned>(std::min<int64_t>(out_units, dev->sm_count));
-  cudaError_t e = launch_dependent(step_in_kernel<FORM, NT>, dim3(in_blocks), dim3(kThreads), kIn, stream, a);
-  count_launches(1);
+  cudaError_t e = launch_dependent(step_order_kernel, dim3(Form<FORM>::kBf16 ? 1 : 1 + static_cast<unsigned>(a.T)),
+                                   dim3(kThreads), 0, stream, a, 8 * NT);
+  if (e == cudaSuccess)
+    e = launch_dependent(step_in_kernel<FORM, NT>, dim3(in_blocks), dim3(kThreads), kIn, stream, a);
   if (e != cudaSuccess) return BSMMA_ERR_CUDA;
-  e = launch_dependent(step_out_kernel<FORM, NT>, dim3(out_blocks), dim3(kThreads),
-                       OutCfg<FORM, NT>::bytes(a.T), stream, a);
-  count_launches(1);
-  return cuda_ok(e);
+  st = launch_out<FORM, NT>(a, dev, stream);
+  count_launches(3);
+  return st;
 }
 
 template <int FORM>
 bsmma_status launch_step_form(const StepArgs& a, const DeviceInfo* dev, cudaStream_t stream) {
-  // an expert's columns are at most the tokens: tiles no wider than those
-  if (a.T <= 8) return launch_step<FORM, 1>(a, dev, stream);
-  if (a.T <= 16) return launch_step<FORM, 2>(a, dev, stream);
-  return launch_step<FORM, 4>(a, dev, stream);
+  // an expert's columns are at most the tokens
+  return a.T <= 8 ? launch_step<FORM, 1>(a, dev, stream) : launch_step<FORM, 2>(a, dev, stream);
 }
+
+constexpr int64_t round_up(int64_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-bsmma_status launch_moe_step(const StepArgs& a, int form, cudaStream_t stream) {
+int64_t step_workspace_bytes(int64_t T, int k, int64_t H, int64_t F) {
+  return round_up(kTableBytes) + round_up(T * 4) + round_up(T * H * 2) + round_up(T * k * ((F + 31) / 32) * 4) +
+         round_up(T * k * F * 2);
+}
+
+bsmma_status launch_moe_step(StepArgs a, int form, void* workspace, cudaStream_t stream) {
   bsmma_status st;
   const DeviceInfo* dev = current_device(&st);
   if (!dev) return st;
+  uint8_t* p = static_cast<uint8_t*>(workspace);
+  auto take = [&](int64_t n) {
+    uint8_t* q = p;
+    p += round_up(n);
+    return q;
+  };
+  a.table = take(kTableBytes);
+  a.x_power = reinterpret_cast<float*>(take(a.T * 4));
+  a.x16 = reinterpret_cast<uint16_t*>(take(a.T * a.H * 2));
+  a.inner_power = reinterpret_cast<float*>(take(a.T * a.k * ((a.F + 31) / 32) * 4));
+  a.inner = reinterpret_cast<uint16_t*>(take(a.T * a.k * a.F * 2));
   switch (form) {
     case BSMMA_OPERAND_BF16: return launch_step_form<BSMMA_OPERAND_BF16>(a, dev, stream);
     case BSMMA_OPERAND_INT8: return launch_step_form<BSMMA_OPERAND_INT8>(a, dev, stream);

@@ -15,10 +15,16 @@ struct StepArgs {
   int64_t F;
   const void *w_in, *s_in, *w_out, *s_out;
   int act;
-  __nv_bfloat16* inner;          // workspace [T * k][F]
   __nv_bfloat16* out;            // [T][H]
+  // in the workspace
+  void* table;                   // who takes what
+  float* x_power;                // [T], and the tokens in FP16 over it
+  uint16_t* x16;                 // [T][H]
+  float* inner_power;            // [T * k][ceil(F / 32)], and the inner rows in FP16 over it, or
+  uint16_t* inner;               // [T * k][F]             in BF16
 };
 
-bsmma_status launch_moe_step(const StepArgs& a, int form, cudaStream_t stream);
+int64_t step_workspace_bytes(int64_t T, int k, int64_t H, int64_t F);
+bsmma_status launch_moe_step(StepArgs a, int form, void* workspace, cudaStream_t stream);
 
 }  // namespace bsmma

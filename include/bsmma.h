@@ -528,8 +528,9 @@ bsmma_status moe_combine_backward(const void* dout, bsmma_dtype dtype, int64_t H
                                   int64_t T, int k, void* dY, float* dweights, bsmma_stream stream);
 
 /*
- * moe_step -- the experts and the weighted sum of a few tokens in two launches, without the
- *   expert order and the gathered rows of the grouped products:
+ * moe_step -- the experts and the weighted sum of a few tokens, without the expert order and
+ *   the gathered rows of the grouped products (three launches: a small one that finds the chosen
+ *   experts' tokens, and two that hold all of the products):
  *     out[t] = sum_j weights[t][j] * W2[e] (act(Wg[e] x[t]) * (Wu[e] x[t])),  e = ids[t][j]
  *   Only experts that some token chose are read, each once (their columns in tiles of 8, 16 or
  *   32 tokens; an expert with more columns is read once a tile).
@@ -541,23 +542,24 @@ bsmma_status moe_combine_backward(const void* dout, bsmma_dtype dtype, int64_t H
  *     BSMMA_OPERAND_BF16   BF16, no scales (s_in, s_out NULL)
  *     BSMMA_OPERAND_INT8   INT8 codes, FP32 scale for each row: s_in [E][2F], s_out [E][H]
  *     BSMMA_OPERAND_E4M3, _E5M2, _E2M1   MX codes and E8M0 scales as mx_quantize writes them
- *                          rowwise: s_in [E][2F][H/32], s_out [E][H][F/32].  Codes that stand
- *                          for NaN or infinity are not supported (they count as finite numbers).
+ *                          rowwise: s_in [E][2F][H/32], s_out [E][H][F/32].
  *   act  a bsmma_activation, in FP32; BSMMA_ACT_NONE leaves the product of the two halves.
- *   Products are summed in FP32; the inner row act(..) * (..) is rounded to BF16 once, as the
- *   second product's operand; the sum over j is FP32, rounded once.  The sums' order depends
- *   on the sizes and the ids alone.
- * Preconditions: T >= 0, k >= 1, T <= 64, T * k <= 1024, 1 <= E <= 1024; H and F at least one
+ *   Products are summed in FP32; the inner row act(..) * (..) is rounded once, as the second
+ *   product's operand, to BF16 (BF16 weights) or to FP16 over a power of two for each 32 values
+ *   (codes); with codes x is taken as FP16 over a power of two for each token, which loses only
+ *   what is below 2^-29 of the token's largest value.  The sum over j is FP32, rounded once.
+ *   The sums' order depends on the sizes and the ids alone.
+ * Preconditions: T >= 0, k >= 1, T <= 32, T * k <= 1024, 1 <= E <= 1024; H and F at least one
  *   piece of 16 bytes of codes and whole ones (BF16: H, F % 8 == 0; INT8: % 16; MX: % 32) and
  *   at most 65536; 16-byte-aligned x, w_in, w_out and out, 4-byte-aligned ids, weights and
- *   scales.  out overlaps no input.  Takes moe_step_workspace_bytes(T, k, F) bytes of the
+ *   scales.  out overlaps no input.  Takes moe_step_workspace_bytes(T, k, H, F) bytes of the
  *   stream's workspace (mx_gemm's; reserve it before a capture).  T == 0 is a no-op.
  */
 bsmma_status moe_step(const void* x, int64_t T, int64_t H, const int32_t* ids, const float* weights,
                       int k, int E, int64_t F, bsmma_operand form, const void* w_in,
                       const void* s_in, const void* w_out, const void* s_out,
                       bsmma_activation act, void* out, bsmma_stream stream);
-int64_t moe_step_workspace_bytes(int64_t T, int k, int64_t F);
+int64_t moe_step_workspace_bytes(int64_t T, int k, int64_t H, int64_t F);
 
 /*
  * The residual branch.  What a block does to the residual stream x around its products f

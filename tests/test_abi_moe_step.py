@@ -16,7 +16,7 @@ def test_refusals():
     bs.build()
     lib = bs.load()
     for change, want in [
-            (dict(T=-1), ARG), (dict(T=65), ARG), (dict(k=0), ARG), (dict(k=300), ARG), (dict(k=2000), ARG),
+            (dict(T=-1), ARG), (dict(T=33), ARG), (dict(k=0), ARG), (dict(k=300), ARG), (dict(k=2000), ARG),
             (dict(E=0), ARG), (dict(E=1025), ARG), (dict(H=0), ARG), (dict(H=65544), ARG), (dict(F=0), ARG),
             (dict(F=65544), ARG), (dict(H=60), ARG), (dict(F=4), ARG), (dict(form=1), UNSUP), (dict(form=6), ARG),
             (dict(form=-1), ARG), (dict(form=2), ARG), (dict(s_in=A), ARG), (dict(s_out=A), ARG),
@@ -30,9 +30,10 @@ def test_refusals():
 
 
 def test_workspace_bytes():
-    assert bs.moe_step_workspace_bytes(0, 2, 64) == 0
-    assert bs.moe_step_workspace_bytes(4, 2, 64) == 4 * 2 * 64 * 2
-    assert bs.moe_step_workspace_bytes(65, 2, 64) == 0
+    assert bs.moe_step_workspace_bytes(0, 2, 64, 64) == 0
+    # at least the inner rows, and no more than those, the tokens, their powers of two and the table
+    assert 4 * 2 * 64 * 2 <= bs.moe_step_workspace_bytes(4, 2, 64, 64) <= 1 << 15
+    assert bs.moe_step_workspace_bytes(33, 2, 64, 64) == 0
 
 
 def test_binding_refuses():
