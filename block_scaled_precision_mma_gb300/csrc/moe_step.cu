@@ -347,79 +347,124 @@ __device__ __forceinline__ void load_stage(uint32_t to, const Source& from, cons
   }
 }
 
-// Multiplies a stage's weights into acc: operand m has set 2 m in its upper and set 2 m + 1 in
-// its lower eight rows.  x: the lane's column (of each eight) from its first K of the stage on; left:
-// K from there to the end; powers (POWERS): of the blocks of the lane's two result columns.
-// scale(r, b): where the scales cannot be copied by words, block b's of the lane's row of set r.
-template <int FORM, int NT, bool POWERS, typename Scale>
-__device__ __forceinline__ void multiply(float (&acc)[2][NT][4], uint32_t ring, const uint16_t* const (&x)[NT],
-                                         int64_t left, const float* const (&powers)[NT][2],
-                                         const Scale& scale, bool words) {
-  using F = Form<FORM>;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const bool whole = left + 8 * t >= F::kStageK;   // (uniform)
-  constexpr int kQuads = F::kMx ? 4 : F::kBlocks;
+// What the columns bring to a chunk of up to four blocks: the lane's eight values of each
+// block, and the powers of two of the lane's two result columns.  It is read from L2 or L1, so it is
+// asked for ahead of the wait for the weights.
+template <int FORM, int NT, bool POWERS>
+struct Columns {
+  static constexpr int kChunk = Form<FORM>::kBlocks < 4 ? Form<FORM>::kBlocks : 4;
+  uint4 x[kChunk][NT];
+  float p[POWERS ? kChunk : 1][NT][2];
+};
+// x: the lane's column (of each eight) from its first K of the chunk on; left: K from there to the
+// end; powers: of the chunk's blocks.
+template <int FORM, int NT, bool POWERS>
+__device__ __forceinline__ void load_columns(Columns<FORM, NT, POWERS>& c, const uint16_t* const (&x)[NT],
+                                             int64_t left, const float* const (&powers)[NT][2], int b0) {
+  constexpr int kChunk = Columns<FORM, NT, POWERS>::kChunk;
+  const int t = threadIdx.x & 3;
+  if (left + 8 * t >= 32 * (b0 + kChunk)) {   // (uniform)
 #pragma unroll
-  for (int b0 = 0; b0 < F::kBlocks; b0 += kQuads) {
-    float sw[4][4];
-    if constexpr (F::kMx) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        uint32_t codes = 0;
-        if (words)
-          asm volatile("ld.shared.b32 %0, [%1];"
-                       : "=r"(codes)
-                       : "r"(ring + 4096 + (r * 8 + g) * F::kBlocks + b0));
-        else
-          for (int j = 0; j < 4; ++j)
-            if (32 * (b0 + j) < left + 8 * t) codes |= scale(r, b0 + j) << (8 * j);
-        e8m0x4(codes, sw[r]);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kQuads; ++j) {
-      const int b = b0 + j;
-      uint4 xv[NT];
-      float p[NT][2];
+    for (int j = 0; j < kChunk; ++j)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        p[n][0] = p[n][1] = 1.f;
-        if (whole) {
-          xv[n] = *reinterpret_cast<const uint4*>(x[n] + 32 * b);
-          if constexpr (POWERS) p[n][0] = powers[n][0][b], p[n][1] = powers[n][1][b];
-        } else {
-          xv[n] = make_uint4(0, 0, 0, 0);
-          if (32 * b < left) xv[n] = *reinterpret_cast<const uint4*>(x[n] + 32 * b);
-          if constexpr (POWERS)
-            if (32 * b < left + 8 * t) p[n][0] = powers[n][0][b], p[n][1] = powers[n][1][b];
+        c.x[j][n] = *reinterpret_cast<const uint4*>(x[n] + 32 * (b0 + j));
+        if constexpr (POWERS) {
+          c.p[j][n][0] = powers[n][0][b0 + j];
+          c.p[j][n][1] = powers[n][1][b0 + j];
         }
       }
-      const uint32_t at = ring + F::place(g, b * F::kBlockBytes + t * F::kLaneBytes);
+  } else {
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        uint32_t hi[4], lo[4];
-        load_weights<FORM>(at + 2 * m * 1024, hi);
-        load_weights<FORM>(at + (2 * m + 1) * 1024, lo);
+    for (int j = 0; j < kChunk; ++j)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if constexpr (F::kMx || POWERS) {
-            float c[4];
-            mma<F::kBf16, true>(c, hi[0], lo[0], hi[1], lo[1], xv[n].x, xv[n].y);
-            mma<F::kBf16, false>(c, hi[2], lo[2], hi[3], lo[3], xv[n].z, xv[n].w);
-            float s[4];
+      for (int n = 0; n < NT; ++n) {
+        c.x[j][n] = make_uint4(0, 0, 0, 0);
+        if (32 * (b0 + j) < left) c.x[j][n] = *reinterpret_cast<const uint4*>(x[n] + 32 * (b0 + j));
+        if constexpr (POWERS) {
+          const bool in = 32 * (b0 + j) < left + 8 * t;
+          c.p[j][n][0] = in ? powers[n][0][b0 + j] : 0.f;
+          c.p[j][n][1] = in ? powers[n][1][b0 + j] : 0.f;
+        }
+      }
+  }
+}
+
+// Multiplies a chunk's weights into acc: operand m has set 2 m in its upper and set 2 m + 1 in
+// its lower eight rows.  scale(r, b): where the scales cannot be copied by words, block b's of the
+// lane's row of set r (asked for inside K only).
+template <int FORM, int NT, bool POWERS, typename Scale>
+__device__ __forceinline__ void multiply(float (&acc)[2][NT][4], const Columns<FORM, NT, POWERS>& c,
+                                         uint32_t ring, int b0, int64_t left, const Scale& scale, bool words) {
+  using F = Form<FORM>;
+  constexpr int kChunk = Columns<FORM, NT, POWERS>::kChunk;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  float sw[F::kMx ? 4 : 1][4];
+  if constexpr (F::kMx) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              s[i] = F::kMx ? sw[2 * m + (i >> 1)][j] : p[n][i & 1];
-              if (F::kMx && POWERS) s[i] *= p[n][i & 1];
-              acc[m][n][i] = fmaf(c[i], s[i], acc[m][n][i]);
-            }
-          } else {
-            mma<F::kBf16, false>(acc[m][n], hi[0], lo[0], hi[1], lo[1], xv[n].x, xv[n].y);
-            mma<F::kBf16, false>(acc[m][n], hi[2], lo[2], hi[3], lo[3], xv[n].z, xv[n].w);
+    for (int r = 0; r < 4; ++r) {
+      uint32_t codes = 0;
+      if (words)
+        asm volatile("ld.shared.b32 %0, [%1];"
+                     : "=r"(codes)
+                     : "r"(ring + 4096 + (r * 8 + g) * F::kBlocks + b0));
+      else
+        for (int j = 0; j < 4; ++j)
+          if (32 * (b0 + j) < left + 8 * t) codes |= scale(r, b0 + j) << (8 * j);
+      e8m0x4(codes, sw[r]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kChunk; ++j) {
+    const uint32_t at = ring + F::place(g, (b0 + j) * F::kBlockBytes + t * F::kLaneBytes);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      uint32_t hi[4], lo[4];
+      load_weights<FORM>(at + 2 * m * 1024, hi);
+      load_weights<FORM>(at + (2 * m + 1) * 1024, lo);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint4& x = c.x[j][n];
+        if constexpr (F::kMx || POWERS) {
+          float d[4];
+          mma<F::kBf16, true>(d, hi[0], lo[0], hi[1], lo[1], x.x, x.y);
+          mma<F::kBf16, false>(d, hi[2], lo[2], hi[3], lo[3], x.z, x.w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float f;
+            if constexpr (F::kMx && POWERS) f = sw[2 * m + (i >> 1)][j] * c.p[j][n][i & 1];
+            else if constexpr (F::kMx) f = sw[2 * m + (i >> 1)][j];
+            else f = c.p[j][n][i & 1];
+            acc[m][n][i] = fmaf(d[i], f, acc[m][n][i]);
           }
+        } else {
+          mma<F::kBf16, false>(acc[m][n], hi[0], lo[0], hi[1], lo[1], x.x, x.y);
+          mma<F::kBf16, false>(acc[m][n], hi[2], lo[2], hi[3], lo[3], x.z, x.w);
         }
       }
     }
+  }
+}
+
+// A stage of the ring: the columns' first chunk, the wait for the weights, the next stage's load,
+// and the products.
+template <int FORM, int NT, bool POWERS, int PENDING, typename Load, typename Scale>
+__device__ __forceinline__ void stage_products(float (&acc)[2][NT][4], const uint16_t* const (&x)[NT],
+                                               const float* const (&powers)[NT][2], int64_t left, uint32_t ring,
+                                               const Load& load, const Scale& scale, bool words) {
+  using Cols = Columns<FORM, NT, POWERS>;
+  Cols c;
+  load_columns<FORM, NT, POWERS>(c, x, left, powers, 0);
+  cp_async_wait<PENDING>();
+  __syncwarp();   // the other lanes' copies, and their reads of the slot that is filled next
+  load();
+#pragma unroll
+  for (int b0 = 0; b0 < Form<FORM>::kBlocks; b0 += Cols::kChunk) {
+    Cols next;
+    if (b0 + Cols::kChunk < Form<FORM>::kBlocks)
+      load_columns<FORM, NT, POWERS>(next, x, left, powers, b0 + Cols::kChunk);
+    multiply<FORM, NT, POWERS>(acc, c, ring, b0, left, scale, words);
+    c = next;
   }
 }
 
@@ -538,11 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1) step_in_kernel(const StepArgs a) 
       int64_t k = group * F::kStageK;
       float acc[2][N][4] = {};
       for (int i = 0; i < mine; ++i) {
-        cp_async_wait<C::kStages - 2>();
-        __syncwarp();   // the other lanes' copies, and their reads of the slot that is filled next
-        load();
-        multiply<FORM, N, false>(
-            acc, ring + at * C::kStage, x, K - k - 8 * t, no_powers,
+        stage_products<FORM, N, false, C::kStages - 2>(
+            acc, x, no_powers, K - k - 8 * t, ring + at * C::kStage, load,
             [&](int r, int b) -> uint32_t { return scales[set_row(f_first, r) * blocks + k / 32 + b]; }, words);
         k += kGroups * F::kStageK;
 #pragma unroll
@@ -725,11 +767,8 @@ __global__ void __launch_bounds__(kThreads, 1) step_out_kernel(const StepArgs a,
         }
         float acc[2][N][4] = {};
         for (int i = 0; i < n_here; ++i) {
-          cp_async_wait<C::kStages - 2>();
-          __syncwarp();
-          load();
-          multiply<FORM, N, kPowers>(
-              acc, ring + at * C::kStage, x, K - k - 8 * t, powers,
+          stage_products<FORM, N, kPowers, C::kStages - 2>(
+              acc, x, powers, K - k - 8 * t, ring + at * C::kStage, load,
               [&](int r, int b) -> uint32_t { return scales[set_row(row0, r) * blocks + k / 32 + b]; }, words);
           k += F::kStageK;
 #pragma unroll
