@@ -423,6 +423,9 @@ def _expect(t, dtype, shape, what: str):
 def _output(t, dtype, shape, like, what: str):
     """The output to write: `t` if it has this dtype and shape (a tuple), or a new one."""
     if t is None:
+        # empty_like takes half the host time of an empty with its shape and device spelt out
+        if like.shape == shape:
+            return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
         return torch.empty(shape, dtype=dtype, device=like.device)
     _expect(t, dtype, shape, what)
     return t
@@ -585,8 +588,6 @@ def _rng(rng, p: float):
 
 def _gate(gate, gate_rows, y):
     """The rows that share a row of the gate (all of them unless said)."""
-    if gate is None:
-        return 1
     T, H = y.shape
     rows = max(T, 1) if gate_rows is None else gate_rows
     if rows < 1:
@@ -604,8 +605,10 @@ def branch_enter(x, weight=None, bias=None, norm="rms", eps=1e-6, fmt=None, out=
     T, H = x.shape
     dtype = _dtype_of(x, "x")
     fmt = fmt or _OPERAND_OF[x.dtype]
-    _expect(weight, torch.float32, (H,), "weight")
-    _expect(bias, torch.float32, (H,), "bias")
+    if weight is not None:
+        _expect(weight, torch.float32, (H,), "weight")
+    if bias is not None:
+        _expect(bias, torch.float32, (H,), "bias")
     out, scales = _operand(fmt, T, H, x, out, scales)
     _check(load().branch_enter(_ptr(x), dtype, T, H, NORMS[norm], eps, _ptr(weight), _ptr(bias),
                                OPERANDS[fmt], _ptr(out), _ptr(scales), _stream(stream)),
@@ -644,9 +647,15 @@ def branch_leave(x, y, weight=None, bias=None, norm="none", eps=1e-6, gate=None,
     T, H = x.shape
     x_dtype, y_dtype = _dtype_of(x, "x"), _dtype_of(y, "y")
     _expect(y, y.dtype, (T, H), "y")
-    for t, what in ((weight, "weight"), (bias, "bias"), (next_weight, "next_weight"), (next_bias, "next_bias")):
-        _expect(t, torch.float32, (H,), what)
-    gate_rows = _gate(gate, gate_rows, y)
+    if weight is not None:
+        _expect(weight, torch.float32, (H,), "weight")
+    if bias is not None:
+        _expect(bias, torch.float32, (H,), "bias")
+    if next_weight is not None:
+        _expect(next_weight, torch.float32, (H,), "next_weight")
+    if next_bias is not None:
+        _expect(next_bias, torch.float32, (H,), "next_bias")
+    gate_rows = 1 if gate is None else _gate(gate, gate_rows, y)
     _rng(rng, p)
     out = _output(out, x.dtype, (T, H), x, "out")
     fmt = fmt or _OPERAND_OF[y.dtype]
@@ -674,7 +683,7 @@ def branch_leave_backward(dout, y, weight=None, bias=None, norm="none", eps=1e-6
     _expect(dout, dout.dtype, (T, H), "dout")
     _expect(weight, torch.float32, (H,), "weight")
     _expect(bias, torch.float32, (H,), "bias")
-    gate_rows = _gate(gate, gate_rows, y)
+    gate_rows = 1 if gate is None else _gate(gate, gate_rows, y)
     _rng(rng, p)
     dy = _output(dy, y.dtype, (T, H), y, "dy")
     if x_scale != 1 or dx is not None:
@@ -735,7 +744,7 @@ def dropout(x, p, rng, out=None, stream=None):
     ``rng`` int64 (seed, offset) on the device.  Its gradient is the same call on the output's.
     out may be x.  See ``dropout`` in bsmma.h."""
     _rng(rng, p)
-    out = _output(out, x.dtype, tuple(x.shape), x, "out")
+    out = _output(out, x.dtype, x.shape, x, "out")
     _check(load().dropout(_ptr(x), _dtype_of(x, "x"), x.numel(), p, _ptr(rng), _ptr(out), _stream(stream)),
            "dropout")
     return out

@@ -797,6 +797,7 @@ bsmma_status branch_enter(const void* x, bsmma_dtype x_dtype, int64_t T, int64_t
   a.x_f32 = x_dtype == BSMMA_F32;
   a.T = T;
   a.H = H;
+  a.inv_h = 1.f / static_cast<float>(H);
   a.norm = {norm, eps, weight, bias};
   a.to = {form, out, scales};
   return launch_branch_enter(a, reinterpret_cast<cudaStream_t>(stream));
@@ -826,6 +827,7 @@ bsmma_status branch_leave(const void* x, bsmma_dtype x_dtype, const void* y, bsm
   a.y_f32 = y_dtype == BSMMA_F32;
   a.T = T;
   a.H = H;
+  a.inv_h = 1.f / static_cast<float>(H);
   a.norm = {norm, eps, weight, bias};
   a.gate = gate;
   a.gate_rows = bounded_rows(gate_rows, T);
@@ -855,6 +857,7 @@ bsmma_status branch_enter_backward(const void* dh, bsmma_dtype h_dtype, const vo
   a.v_f32 = x_dtype == BSMMA_F32;
   a.T = T;
   a.H = H;
+  a.inv_h = 1.f / static_cast<float>(H);
   a.norm = {norm, eps, weight, nullptr};
   a.dres = dres;
   a.drop = {0u, 1.f, nullptr};
@@ -887,6 +890,7 @@ bsmma_status branch_leave_backward(const void* dout, bsmma_dtype x_dtype, const 
   a.v_f32 = y_dtype == BSMMA_F32;
   a.T = T;
   a.H = H;
+  a.inv_h = 1.f / static_cast<float>(H);
   a.norm = {norm, eps, weight, bias};
   a.gate = gate;
   a.gate_rows = bounded_rows(gate_rows, T);

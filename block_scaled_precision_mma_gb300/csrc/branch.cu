@@ -16,49 +16,65 @@ namespace {
 using namespace branch;
 
 // ------------------------------------------------------------------------- norms
+constexpr int kPieces = 4;   // a thread's, in registers
+template <bool WARP>
+using Row = Place<WARP, kPieces>;
+
 // f (zeros in pieces past the row) -> n(f) * weight + bias.  The variance of a layer norm is
 // summed around the mean, in a second pass over the registers: a row far from zero keeps its
-// digits.
-template <int TPR, int V>
-__device__ __forceinline__ void norm_row(float (&f)[V][8], const NormArgs& a, int tid, int vecs,
-                                         float inv_h, float* part) {
-  float s[1] = {0.f};
+// digits.  part: 64 floats.
+template <bool WARP>
+__device__ __forceinline__ void norm_row(Vals (&f)[kPieces], const NormArgs& a, const Row<WARP>& at, float inv_h,
+                                         float* part) {
+  float s[1];
   if (a.kind == BSMMA_NORM_LAYER) {
+    float2 acc[2] = {both(0.f), both(0.f)};
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int i = 0; i < kPieces; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[0] += f[i][j];
-    row_sums<TPR>(s, part);
-    const float mean = s[0] * inv_h;
-    s[0] = 0.f;
+      for (int j = 0; j < 4; ++j) acc[j & 1] = add2(acc[j & 1], f[i].v[j]);
+    s[0] = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+    row_sums<WARP>(s, part);
+    const float2 minus_mean = both(-s[0] * inv_h);
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (tid + i * TPR < vecs)
+    for (int i = 0; i < kPieces; ++i)
+      if (at.in(i))
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          f[i][j] -= mean;
-          s[0] = fmaf(f[i][j], f[i][j], s[0]);
-        }
-    row_sums<TPR>(s, part + 32);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[0] = fmaf(f[i][j], f[i][j], s[0]);
-    row_sums<TPR>(s, part);
+        for (int j = 0; j < 4; ++j) f[i].v[j] = add2(f[i].v[j], minus_mean);
+    part += 32;
   }
-  const float r = __frsqrt_rn(fmaf(s[0], inv_h, a.eps));
+  float2 acc[2] = {both(0.f), both(0.f)};
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int v = tid + i * TPR;
-    if (v >= vecs) continue;
-    float w[8], b[8];
+  for (int i = 0; i < kPieces; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = 1.f, b[j] = 0.f;
-    if (a.weight) load_columns(a.weight, 8 * v, w);
-    if (a.bias) load_columns(a.bias, 8 * v, b);
+    for (int j = 0; j < 4; ++j) acc[j & 1] = __ffma2_rn(f[i].v[j], f[i].v[j], acc[j & 1]);
+  s[0] = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+  row_sums<WARP>(s, part);
+  const float2 rs = both(inv_sqrt(fmaf(s[0], inv_h, a.eps)));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[i][j] = fmaf(f[i][j] * r, w[j], b[j]);
+  for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[i].v[j] = mul2(f[i].v[j], rs);
+  // what a call may leave out stands in loops of its own, which it jumps over
+  if (a.weight) {
+    const float* w0 = a.weight + 8 * at.base;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (at.in(i)) {
+        const Vals w = load_columns(w0, 256 * i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[i].v[j] = mul2(f[i].v[j], w.v[j]);
+      }
+  }
+  if (a.bias) {
+    const float* b0 = a.bias + 8 * at.base;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (at.in(i)) {
+        const Vals b = load_columns(b0, 256 * i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[i].v[j] = add2(f[i].v[j], b.v[j]);
+      }
   }
 }
 
@@ -81,214 +97,237 @@ __device__ __forceinline__ uint32_t fp4x2(float lo, float hi) {
   return r & 0xFFu;
 }
 
-template <int FMT, int TPR, int V>
-__device__ __forceinline__ void store_mx(const float (&f)[V][8], const OperandArgs& to, int64_t t,
-                                         int64_t H, int tid, int vecs) {
+// One piece's codes at `codes` and, by one lane of four, its block's scale at `scale`; the four lanes
+// that hold a block of 32 are all here (a row has whole blocks).  in: the piece is in the row.
+template <int FMT>
+__device__ __forceinline__ void store_mx(const Vals& f, uint8_t* codes, uint8_t* scale, bool in, bool first) {
   constexpr int kEmax = FMT == BSMMA_OPERAND_E4M3 ? 8 : FMT == BSMMA_OPERAND_E5M2 ? 15 : 2;
-  uint8_t* codes = static_cast<uint8_t*>(to.out) + t * (FMT == BSMMA_OPERAND_E2M1 ? H / 2 : H);
-  uint8_t* scales = static_cast<uint8_t*>(to.scales) + t * (H / 32);
+  float amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int v = tid + i * TPR;
-    float amax = 0.f;
+  for (int j = 0; j < 4; ++j) amax = fmaxf(fmaxf(amax, fabsf(f.v[j].x)), fabsf(f.v[j].y));
+  amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
+  if (!in) return;
+  // floor(log2 amax) - emax + 127, at least 0: the exponent field less emax (a subnormal's
+  // field is 0, and what is below it would be cut to 0 as well); 127 for a block of zeros
+  const int field = static_cast<int>(__float_as_uint(amax) >> 23);
+  const int code = amax == 0.f ? 127 : max(field - kEmax, 0);
+  const float2 inv = both(__uint_as_float(static_cast<uint32_t>(254 - code) << 23));   // 2^(127 - code)
+  float2 y[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[i][j]));
-    // four neighbouring lanes hold a block of 32 (vecs % 4 == 0: all of them in the row or none)
-    amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
-    if (v >= vecs) continue;
-    int e = 0;
-    if (amax > 0.f) {
-      const uint32_t bits = __float_as_uint(amax);
-      const int ef = static_cast<int>(bits >> 23);
-      e = (ef ? ef - 127 : 31 - __clz(static_cast<int>(bits)) - 149) - kEmax;
-      e = max(-127, min(127, e));
-    }
-    // 2^-e; 2^-127 is subnormal
-    const float inv = e < 127 ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23)
-                              : __uint_as_float(0x00400000u);
-    float y[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(f[i][j], inv);
-    if constexpr (FMT == BSMMA_OPERAND_E2M1) {
-      *reinterpret_cast<uint32_t*>(codes + 4 * static_cast<int64_t>(v)) =
-          fp4x2(y[0], y[1]) | fp4x2(y[2], y[3]) << 8 | fp4x2(y[4], y[5]) << 16 | fp4x2(y[6], y[7]) << 24;
-    } else {
-      *reinterpret_cast<uint2*>(codes + 8 * static_cast<int64_t>(v)) =
-          make_uint2(fp8x2<FMT>(y[0], y[1]) | fp8x2<FMT>(y[2], y[3]) << 16,
-                     fp8x2<FMT>(y[4], y[5]) | fp8x2<FMT>(y[6], y[7]) << 16);
-    }
-    if ((v & 3) == 0) scales[v >> 2] = static_cast<uint8_t>(e + 127);
+  for (int j = 0; j < 4; ++j) y[j] = mul2(f.v[j], inv);
+  if constexpr (FMT == BSMMA_OPERAND_E2M1) {
+    *reinterpret_cast<uint32_t*>(codes) = fp4x2(y[0].x, y[0].y) | fp4x2(y[1].x, y[1].y) << 8 |
+                                          fp4x2(y[2].x, y[2].y) << 16 | fp4x2(y[3].x, y[3].y) << 24;
+  } else {
+    *reinterpret_cast<uint2*>(codes) = make_uint2(fp8x2<FMT>(y[0].x, y[0].y) | fp8x2<FMT>(y[1].x, y[1].y) << 16,
+                                                  fp8x2<FMT>(y[2].x, y[2].y) | fp8x2<FMT>(y[3].x, y[3].y) << 16);
   }
+  if (first) *scale = static_cast<uint8_t>(code);
+}
+template <int FMT, bool WARP>
+__device__ __forceinline__ void store_mx_row(const Vals (&f)[kPieces], const OperandArgs& to, int64_t t, int64_t H,
+                                             const Row<WARP>& at) {
+  constexpr int kCodes = FMT == BSMMA_OPERAND_E2M1 ? 4 : 8;   // bytes of a piece
+  uint8_t* codes = static_cast<uint8_t*>(to.out) + t * (H / 8) * kCodes + at.base * kCodes;
+  uint8_t* scales = static_cast<uint8_t*>(to.scales) + t * (H / 32) + (at.base >> 2);
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i)
+    store_mx<FMT>(f[i], codes + 32 * kCodes * i, scales + 8 * i, at.in(i), (at.base & 3) == 0);
 }
 
-template <int TPR, int V>
-__device__ __forceinline__ void store_int8(const float (&f)[V][8], const OperandArgs& to, int64_t t,
-                                           int64_t H, int tid, int vecs, float* part) {
-  uint32_t amax = 0;
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(f[i][j]) & 0x7FFFFFFFu);
-  amax = row_max<TPR>(amax, reinterpret_cast<uint32_t*>(part));
+// The INT8 scale of a row's largest magnitude, and a piece's codes: the quotient rounded once, by
+// two fused corrections on the reciprocal (as int8_quantize takes it) where nothing of them
+// leaves FP32's range.
+struct Int8Scale {
+  float s, inv;   // inv 0: outside that range
+};
+__device__ __forceinline__ Int8Scale int8_scale(uint32_t amax) {
   float s = __fmul_rn(__uint_as_float(amax), 1.f / 127.f);
   if (s == 0.f) s = 1.f;
-  if (tid == 0) static_cast<float*>(to.scales)[t] = s;
-  // the quotient rounded once: two fused corrections on the reciprocal (as int8_quantize takes
-  // it), where nothing of them leaves FP32's range
-  const bool normal = s >= 0x1p-88f && s <= 0x1p100f;
-  const float inv = normal ? __fdiv_rn(1.f, s) : 0.f;
-  int8_t* codes = static_cast<int8_t*>(to.out) + t * H;
+  return Int8Scale{s, s >= 0x1p-88f && s <= 0x1p100f ? __fdiv_rn(1.f, s) : 0.f};
+}
+__device__ __forceinline__ uint32_t magnitude(const Vals& f, uint32_t amax) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int v = tid + i * TPR;
-    if (v >= vecs) continue;
-    uint32_t c[2] = {0, 0};
+  for (int j = 0; j < 4; ++j)
+    amax = max(max(amax, __float_as_uint(f.v[j].x) & 0x7FFFFFFFu), __float_as_uint(f.v[j].y) & 0x7FFFFFFFu);
+  return amax;
+}
+__device__ __forceinline__ uint2 int8_codes(const Vals& f, const Int8Scale& k) {
+  const float2 inv = both(k.inv), minus_s = both(-k.s);
+  uint32_t c[2] = {0, 0};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float x = f[i][j];
-      float q = x * inv;
-      q = fmaf(fmaf(-s, q, x), inv, q);
-      q = fmaf(fmaf(-s, q, x), inv, q);
-      if (!normal) q = __fdiv_rn(x, s);
-      const int n = max(-127, min(127, __float2int_rn(q)));
-      c[j >> 2] |= (static_cast<uint32_t>(n) & 0xFFu) << (8 * (j & 3));
-    }
-    *reinterpret_cast<uint2*>(codes + 8 * static_cast<int64_t>(v)) = make_uint2(c[0], c[1]);
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = f.v[j];
+    float2 q = mul2(x, inv);
+    q = __ffma2_rn(__ffma2_rn(minus_s, q, x), inv, q);
+    q = __ffma2_rn(__ffma2_rn(minus_s, q, x), inv, q);
+    if (k.inv == 0.f) q = make_float2(__fdiv_rn(x.x, k.s), __fdiv_rn(x.y, k.s));
+    const int n0 = max(-127, min(127, __float2int_rn(q.x))), n1 = max(-127, min(127, __float2int_rn(q.y)));
+    c[j >> 1] |= ((static_cast<uint32_t>(n0) & 0xFFu) | (static_cast<uint32_t>(n1) & 0xFFu) << 8) << (16 * (j & 1));
   }
+  return make_uint2(c[0], c[1]);
 }
 
-template <int TPR, int V>
-__device__ __forceinline__ void store_operand(const float (&f)[V][8], const OperandArgs& to, int64_t t,
-                                              int64_t H, int tid, int vecs, float* part) {
+template <bool WARP>
+__device__ __forceinline__ void store_int8(const Vals (&f)[kPieces], const OperandArgs& to, int64_t t, int64_t H,
+                                           const Row<WARP>& at, float* part) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) amax = magnitude(f[i], amax);
+  const Int8Scale k = int8_scale(row_max<WARP>(amax, reinterpret_cast<uint32_t*>(part)));
+  if (at.base == 0) static_cast<float*>(to.scales)[t] = k.s;
+  int8_t* codes = static_cast<int8_t*>(to.out) + t * H + 8 * at.base;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i)
+    if (at.in(i)) *reinterpret_cast<uint2*>(codes + 256 * i) = int8_codes(f[i], k);
+}
+
+template <bool WARP>
+__device__ __forceinline__ void store_operand(const Vals (&f)[kPieces], const OperandArgs& to, int64_t t, int64_t H,
+                                              const Row<WARP>& at, float* part) {
   switch (to.form) {
     case BSMMA_OPERAND_BF16:
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        if (at.in(i)) store_raw<false>(to.out, t * H + 8 * at.base + 256 * i, narrow<false>(f[i]));
+      break;
     case BSMMA_OPERAND_F32:
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (tid + i * TPR < vecs) {
-          const int64_t at = t * H + 8 * (tid + i * TPR);
-          if (to.form == BSMMA_OPERAND_BF16) store_raw<false>(to.out, at, narrow<false>(f[i]));
-          else store_raw<true>(to.out, at, narrow<true>(f[i]));
-        }
+      for (int i = 0; i < kPieces; ++i)
+        if (at.in(i)) store_raw<true>(to.out, t * H + 8 * at.base + 256 * i, narrow<true>(f[i]));
       break;
-    case BSMMA_OPERAND_INT8: store_int8<TPR, V>(f, to, t, H, tid, vecs, part); break;
-    case BSMMA_OPERAND_E4M3: store_mx<BSMMA_OPERAND_E4M3, TPR, V>(f, to, t, H, tid, vecs); break;
-    case BSMMA_OPERAND_E5M2: store_mx<BSMMA_OPERAND_E5M2, TPR, V>(f, to, t, H, tid, vecs); break;
-    default: store_mx<BSMMA_OPERAND_E2M1, TPR, V>(f, to, t, H, tid, vecs); break;
+    case BSMMA_OPERAND_INT8: store_int8<WARP>(f, to, t, H, at, part); break;
+    case BSMMA_OPERAND_E4M3: store_mx_row<BSMMA_OPERAND_E4M3, WARP>(f, to, t, H, at); break;
+    case BSMMA_OPERAND_E5M2: store_mx_row<BSMMA_OPERAND_E5M2, WARP>(f, to, t, H, at); break;
+    default: store_mx_row<BSMMA_OPERAND_E2M1, WARP>(f, to, t, H, at); break;
   }
 }
 
 // ------------------------------------------------------------------------- kernels
-template <int TPR>
-constexpr int kBlock = TPR < 128 ? 128 : TPR;
+// WARP: a row a warp (rows of up to 1024 values), four warps a block; else a row a block, as many
+// warps as give each thread four pieces.
+template <bool WARP>
+__device__ __forceinline__ int64_t row_of() {
+  return WARP ? static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5) : blockIdx.x;
+}
+// Rows of up to 8192 values: at most 256 threads, registers for three or four blocks an SM.
+constexpr int kMaxThreads = 512, kShortThreads = 256;
 
-template <bool F32, int TPR, int V>
-__global__ void __launch_bounds__(kBlock<TPR>) enter_kernel(const EnterArgs p) {
-  __shared__ float part[3 * 32];
+// A row a block (a warp), in registers.  16384 x 7168 BF16 into E4M3: 80 us, 356 MB at 4.4 TB/s, bound by
+// issuing (64% of the slots: 120 instructions for eight values, 40 of them what a row costs each
+// of its warps) and by the weights' loads (57% of the L1 cache's cycles); FP32 into BF16 16384 x 4096
+// 70 us, 403 MB at 5.7 TB/s.  Tried and slower: two rows a block that share the weights (87 us, 14
+// warps an SM), and rows in a ring of asynchronous copies, one (78) or two (86) at a time, which
+// widen the values anew in each pass.
+template <bool F32, bool WARP, bool SHORT>
+__global__ void __launch_bounds__(SHORT ? kShortThreads : kMaxThreads, SHORT ? 4 : 2) enter_kernel(const EnterArgs p) {
+  __shared__ float part[WARP ? 1 : 3 * 32];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int tid = threadIdx.x % TPR, vecs = static_cast<int>(p.H / 8);
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kBlock<TPR> / TPR) + threadIdx.x / TPR;
+  const Row<WARP> at(p.H);
+  const int64_t t = row_of<WARP>();
   if (t >= p.T) return;   // (whole warps, and no barrier where a row is a warp's)
-  Raw<F32> raw[V];
+  Raw<F32> raw[kPieces];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int v = tid + i * TPR;
-    raw[i] = v < vecs ? load_raw<F32>(p.x, t * p.H + 8 * v) : zero_raw<F32>();
-  }
-  float f[V][8];
+  for (int i = 0; i < kPieces; ++i)
+    raw[i] = at.in(i) ? load_raw<F32>(p.x, t * p.H + 8 * at.base + 256 * i) : zero_raw<F32>();
+  Vals f[kPieces];
 #pragma unroll
-  for (int i = 0; i < V; ++i) widen<F32>(raw[i], f[i]);
-  norm_row<TPR, V>(f, p.norm, tid, vecs, 1.f / static_cast<float>(p.H), part);
-  store_operand<TPR, V>(f, p.to, t, p.H, tid, vecs, part + 64);
+  for (int i = 0; i < kPieces; ++i) f[i] = widen<F32>(raw[i]);
+  norm_row<WARP>(f, p.norm, at, p.inv_h, part);
+  store_operand<WARP>(f, p.to, t, p.H, at, part + (WARP ? 0 : 64));
 }
 
-template <bool XF, bool YF, int TPR, int V>
-__global__ void __launch_bounds__(kBlock<TPR>) leave_kernel(const LeaveArgs p) {
-  __shared__ float part[5 * 32];
+template <bool XF, bool YF, bool WARP, bool SHORT>
+__global__ void __launch_bounds__(SHORT ? kShortThreads : kMaxThreads, SHORT ? 3 : 1) leave_kernel(const LeaveArgs p) {
+  __shared__ float part[WARP ? 1 : 5 * 32];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int tid = threadIdx.x % TPR, vecs = static_cast<int>(p.H / 8);
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kBlock<TPR> / TPR) + threadIdx.x / TPR;
+  const Row<WARP> at(p.H);
+  const int64_t t = row_of<WARP>();
   if (t >= p.T) return;
-  const float inv_h = 1.f / static_cast<float>(p.H);
-  Raw<YF> ry[V];
-  Raw<XF> rx[V];
+  const float inv_h = p.inv_h;
+  const int64_t row = t * p.H + 8 * at.base;
+  Raw<YF> ry[kPieces];
+  Raw<XF> rx[kPieces];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int v = tid + i * TPR;
-    ry[i] = v < vecs ? load_raw<YF>(p.y, t * p.H + 8 * v) : zero_raw<YF>();
-    rx[i] = v < vecs ? load_raw<XF>(p.x, t * p.H + 8 * v) : zero_raw<XF>();
+  for (int i = 0; i < kPieces; ++i) {
+    ry[i] = at.in(i) ? load_raw<YF>(p.y, row + 256 * i) : zero_raw<YF>();
+    rx[i] = at.in(i) ? load_raw<XF>(p.x, row + 256 * i) : zero_raw<XF>();
   }
-  float f[V][8];
+  Vals f[kPieces];
 #pragma unroll
-  for (int i = 0; i < V; ++i) widen<YF>(ry[i], f[i]);
-  if (p.norm.kind != BSMMA_NORM_NONE) norm_row<TPR, V>(f, p.norm, tid, vecs, inv_h, part);
-  Philox gen = {};
-  if (p.drop.threshold) gen = philox_of(p.drop.rng);
-  const int64_t gate_row =
-      p.gate ? static_cast<int64_t>(static_cast<uint32_t>(t) / static_cast<uint32_t>(p.gate_rows)) * p.H : 0;
+  for (int i = 0; i < kPieces; ++i) f[i] = widen<YF>(ry[i]);
+  if (p.norm.kind != BSMMA_NORM_NONE) norm_row<WARP>(f, p.norm, at, inv_h, part);
+  if (p.drop.threshold != 0) {
+    const Philox gen = philox_of(p.drop.rng);
+    const uint64_t block = static_cast<uint64_t>(t) * at.vecs + at.base;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int v = tid + i * TPR;
-    if (v >= vecs) continue;
-    if (p.drop.threshold) {
-      const uint32_t keep = kept8(gen, static_cast<uint64_t>(t) * vecs + v, p.drop.threshold);
+    for (int i = 0; i < kPieces; ++i) drop(f[i], philox(gen, block + 32 * i), p.drop.threshold << 16);
+  }
+  if (p.gate) {
+    const int64_t from =
+        static_cast<int64_t>(static_cast<uint32_t>(t) / static_cast<uint32_t>(p.gate_rows)) * p.H + 8 * at.base;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[i][j] = keep >> j & 1u ? f[i][j] * p.drop.scale : 0.f;
-    }
-    if (p.gate) {
-      float g[8];
-      widen<YF>(load_raw<YF>(p.gate, gate_row + 8 * v), g);
+    for (int i = 0; i < kPieces; ++i)
+      if (at.in(i)) {
+        const Vals g = widen<YF>(load_raw<YF>(p.gate, from + 256 * i));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[i][j] *= g[j];
-    }
-    float x[8];
-    widen<XF>(rx[i], x);
+        for (int j = 0; j < 4; ++j) f[i].v[j] = mul2(f[i].v[j], g.v[j]);
+      }
+  }
+  const float2 xs = both(p.x_scale), ys = both(p.y_scale * p.drop.scale);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[i][j] = fmaf(p.y_scale, f[i][j], p.x_scale * x[j]);
+  for (int i = 0; i < kPieces; ++i) {
+    const Vals x = widen<XF>(rx[i]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[i].v[j] = __ffma2_rn(ys, f[i].v[j], mul2(xs, x.v[j]));
     const Raw<XF> o = narrow<XF>(f[i]);
-    store_raw<XF>(p.out, t * p.H + 8 * v, o);
-    widen<XF>(o, f[i]);   // the next norm is of what is stored
+    if (at.in(i)) store_raw<XF>(p.out, row + 256 * i, o);
+    f[i] = widen<XF>(o);   // the next norm is of what is stored
   }
   if (p.next.kind == BSMMA_NORM_NONE) return;
-  norm_row<TPR, V>(f, p.next, tid, vecs, inv_h, part + 64);
-  store_operand<TPR, V>(f, p.to, t, p.H, tid, vecs, part + 128);
+  norm_row<WARP>(f, p.next, at, inv_h, part + (WARP ? 0 : 64));
+  store_operand<WARP>(f, p.to, t, p.H, at, part + (WARP ? 0 : 128));
 }
 
 // Eight values a piece (the last one may be short), kPieces in flight a thread.
-constexpr int kDropPieces = 4;
 template <bool F32>
-__global__ void __launch_bounds__(256) dropout_kernel(const void* x, int64_t n, const DropArgs drop,
-                                                      void* y) {
+__global__ void __launch_bounds__(256) dropout_kernel(const void* x, int64_t n, const DropArgs args, void* y) {
   grid_dependency_wait();
   grid_launch_dependents();
+  const bool dropping = args.threshold != 0;
   Philox gen = {};
-  if (drop.threshold) gen = philox_of(drop.rng);
+  if (dropping) gen = philox_of(args.rng);
+  const uint32_t limit = args.threshold << 16;
+  const float2 scale = both(args.scale);
   const int64_t whole = n / 8;
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * (256 * kDropPieces) + threadIdx.x;
-  Raw<F32> raw[kDropPieces];
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * (256 * kPieces) + threadIdx.x;
+  Raw<F32> raw[kPieces];
 #pragma unroll
-  for (int i = 0; i < kDropPieces; ++i)
+  for (int i = 0; i < kPieces; ++i)
     if (base + 256 * i < whole) raw[i] = load_raw<F32>(x, 8 * (base + 256 * i));
 #pragma unroll
-  for (int i = 0; i < kDropPieces; ++i) {
+  for (int i = 0; i < kPieces; ++i) {
     const int64_t v = base + 256 * i;
-    if (v > whole || 8 * v >= n) continue;
-    const uint32_t keep = drop.threshold ? kept8(gen, static_cast<uint64_t>(v), drop.threshold) : 0xFFu;
     if (v < whole) {
-      float f[8];
-      widen<F32>(raw[i], f);
+      Vals f = widen<F32>(raw[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = keep >> j & 1u ? f[j] * drop.scale : 0.f;
+      for (int j = 0; j < 4; ++j) f.v[j] = mul2(f.v[j], scale);
+      if (dropping) drop(f, philox(gen, static_cast<uint64_t>(v)), limit);
       store_raw<F32>(y, 8 * v, narrow<F32>(f));
-    } else {
-      for (int j = 0; j < static_cast<int>(n - 8 * v); ++j) {
+    } else if (v == whole && 8 * v < n) {
+      uint4 words = make_uint4(0, 0, 0, 0);
+      if (dropping) words = philox(gen, static_cast<uint64_t>(v));
+      const uint32_t w[4] = {words.x, words.y, words.z, words.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (8 * v + j >= n) break;
         float f;
         if constexpr (F32) f = static_cast<const float*>(x)[8 * v + j];
         else f = __bfloat162float(static_cast<const __nv_bfloat16*>(x)[8 * v + j]);
-        f = keep >> j & 1u ? f * drop.scale : 0.f;
+        f = (j & 1 ? w[j >> 1] : w[j >> 1] << 16) >= limit ? f * args.scale : 0.f;
         if constexpr (F32) static_cast<float*>(y)[8 * v + j] = f;
         else static_cast<__nv_bfloat16*>(y)[8 * v + j] = __float2bfloat16_rn(f);
       }
@@ -296,51 +335,52 @@ __global__ void __launch_bounds__(256) dropout_kernel(const void* x, int64_t n, 
   }
 }
 
-// The threads of a row: enough that a thread has at most four pieces of it (32 values in
-// registers); rows of up to 1024 values take a warp, four to a block.
-template <typename Launch>
-void by_length(int64_t H, const Launch& launch) {
-  const int64_t vecs = H / 8;
-  if (vecs <= 32 * 4) launch(std::integral_constant<int, 32>{});
-  else if (vecs <= 128 * 4) launch(std::integral_constant<int, 128>{});
-  else if (vecs <= 256 * 4) launch(std::integral_constant<int, 256>{});
-  else launch(std::integral_constant<int, 512>{});
+constexpr int kWarpRow = 8 * 32 * kPieces;   // values of a row that a warp holds
+unsigned threads_of(int64_t H) {
+  return H <= kWarpRow ? 128u : static_cast<unsigned>(32 * ((H + kWarpRow - 1) / kWarpRow));
+}
+
+template <bool F32>
+bsmma_status launch_enter(const EnterArgs& a, cudaStream_t stream) {
+  const bool warp = a.H <= kWarpRow;
+  const unsigned threads = threads_of(a.H);
+  return cuda_ok(launch_dependent(warp ? enter_kernel<F32, true, true>
+                                  : threads <= kShortThreads ? enter_kernel<F32, false, true>
+                                                             : enter_kernel<F32, false, false>,
+                                  dim3(static_cast<unsigned>(warp ? (a.T + 3) / 4 : a.T)), dim3(threads), 0, stream, a));
+}
+template <bool XF, bool YF>
+bsmma_status launch_leave(const LeaveArgs& a, cudaStream_t stream) {
+  const unsigned threads = threads_of(a.H);
+  const bool warp = a.H <= kWarpRow;
+  return cuda_ok(launch_dependent(warp ? leave_kernel<XF, YF, true, true>
+                                  : threads <= kShortThreads ? leave_kernel<XF, YF, false, true>
+                                                             : leave_kernel<XF, YF, false, false>,
+                                  dim3(static_cast<unsigned>(warp ? (a.T + 3) / 4 : a.T)), dim3(threads), 0, stream, a));
 }
 
 }  // namespace
 
 bsmma_status launch_branch_enter(const EnterArgs& a, cudaStream_t stream) {
-  cudaError_t e = cudaSuccess;
-  by_length(a.H, [&](auto tpr) {
-    constexpr int kTpr = decltype(tpr)::value, kRows = kBlock<kTpr> / kTpr;
-    const unsigned blocks = static_cast<unsigned>((a.T + kRows - 1) / kRows);
-    e = launch_dependent(a.x_f32 ? enter_kernel<true, kTpr, 4> : enter_kernel<false, kTpr, 4>,
-                         dim3(blocks), dim3(kBlock<kTpr>), 0, stream, a);
-  });
+  const bsmma_status st = a.x_f32 ? launch_enter<true>(a, stream) : launch_enter<false>(a, stream);
   count_launches(1);
-  return cuda_ok(e);
+  return st;
 }
 
 bsmma_status launch_branch_leave(const LeaveArgs& a, cudaStream_t stream) {
-  cudaError_t e = cudaSuccess;
-  by_length(a.H, [&](auto tpr) {
-    constexpr int kTpr = decltype(tpr)::value, kRows = kBlock<kTpr> / kTpr;
-    const unsigned blocks = static_cast<unsigned>((a.T + kRows - 1) / kRows);
-    const auto kern = !a.x_f32   ? leave_kernel<false, false, kTpr, 4>
-                      : a.y_f32 ? leave_kernel<true, true, kTpr, 4>
-                                : leave_kernel<true, false, kTpr, 4>;
-    e = launch_dependent(kern, dim3(blocks), dim3(kBlock<kTpr>), 0, stream, a);
-  });
+  const bsmma_status st = !a.x_f32   ? launch_leave<false, false>(a, stream)
+                          : a.y_f32 ? launch_leave<true, true>(a, stream)
+                                    : launch_leave<true, false>(a, stream);
   count_launches(1);
-  return cuda_ok(e);
+  return st;
 }
 
 bsmma_status launch_dropout(const void* x, bool f32, int64_t n, const DropArgs& drop, void* y,
                             cudaStream_t stream) {
   const int64_t pieces = (n + 7) / 8;
-  const unsigned blocks = static_cast<unsigned>((pieces + 256 * kDropPieces - 1) / (256 * kDropPieces));
-  const cudaError_t e = launch_dependent(f32 ? dropout_kernel<true> : dropout_kernel<false>,
-                                         dim3(blocks), dim3(256), 0, stream, x, n, drop, y);
+  const unsigned blocks = static_cast<unsigned>((pieces + 256 * kPieces - 1) / (256 * kPieces));
+  const cudaError_t e = launch_dependent(f32 ? dropout_kernel<true> : dropout_kernel<false>, dim3(blocks),
+                                         dim3(256), 0, stream, x, n, drop, y);
   count_launches(1);
   return cuda_ok(e);
 }

@@ -30,6 +30,7 @@ struct EnterArgs {
   const void* x;
   bool x_f32;
   int64_t T, H;
+  float inv_h;                   // 1 / H
   NormArgs norm;
   OperandArgs to;
 };
@@ -40,6 +41,7 @@ struct LeaveArgs {
   const void* y;
   bool y_f32;
   int64_t T, H;
+  float inv_h;
   NormArgs norm;
   const void* gate;              // of y's type, or nullptr
   int64_t gate_rows;
@@ -57,6 +59,7 @@ struct BranchGradArgs {
   const void* v;
   bool v_f32;
   int64_t T, H;
+  float inv_h;
   NormArgs norm;
   const void* dres;              // entering: added to dv (of v's type), or nullptr
   const void* gate;              // leaving: as forward

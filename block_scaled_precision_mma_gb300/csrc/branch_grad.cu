@@ -9,8 +9,8 @@ namespace branch {
 namespace {
 
 // Workers: runs of rows, as many as fill the GPU's 152 SMs with the blocks that fit one (by
-// registers), fewer rows each for shorter rows.  A fixed number, so that the sums' order, and
-// with it every bit, is the same wherever the call runs.
+// registers), fewer rows each for shorter rows.  A number of T and H alone, so that the sums' order,
+// and with it every bit, is the same wherever the call runs.
 int workers_of(int64_t T, int64_t H) {
   const int64_t vecs = H / 8;
   const int64_t most = vecs <= 128 ? 152 * 16 : vecs <= 512 ? 152 * 2 : 152;

@@ -34,38 +34,57 @@ struct GradParams {
 // Rows r0(w) .. r0(w + 1) - 1 are worker w's.
 __host__ __device__ inline int64_t first_row(int64_t T, int workers, int64_t w) { return T * w / workers; }
 
-__device__ __forceinline__ void store_sums(float* to, const float (&f)[8]) {
-  *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
-  *reinterpret_cast<float4*>(to + 4) = make_float4(f[4], f[5], f[6], f[7]);
+__device__ __forceinline__ void store_sums(float* to, const Vals& f) {
+  *reinterpret_cast<float4*>(to) = make_float4(f.v[0].x, f.v[0].y, f.v[1].x, f.v[1].y);
+  *reinterpret_cast<float4*>(to + 4) = make_float4(f.v[2].x, f.v[2].y, f.v[3].x, f.v[3].y);
+}
+__device__ __forceinline__ float sum_of(const float2 (&a)[2]) { return (a[0].x + a[0].y) + (a[1].x + a[1].y); }
+
+// sum += of * z, where what was dropped (of is 0) adds nothing whatever z is.
+__device__ __forceinline__ void add_gate(Vals& sum, const Vals& of, const Vals& z, bool dropping) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float2 u = z.v[j];
+    if (dropping) u = make_float2(of.v[j].x == 0.f ? 0.f : u.x, of.v[j].y == 0.f ? 0.f : u.y);
+    sum.v[j] = __ffma2_rn(of.v[j], u, sum.v[j]);
+  }
 }
 
-template <bool LEAVE, bool DF, bool VF, bool BIAS, bool GATE, int TPR, int V>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, 1) grad_kernel(const GradParams p) {
-  constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
-  constexpr int kPart = TPR < 128 ? 1 : 2 * (TPR / 32);
+// A thread's pieces of a row: with up to three sums a column the registers hold two (a warp's
+// rows are short, and four of them keep it busy).
+template <bool WARP>
+constexpr int kGradPieces = WARP ? 4 : 2;
+// Blocks of up to 14 warps (rows of 7168) keep 128 registers a thread, longer rows 64.
+template <bool WARP, bool LONG>
+constexpr int kGradThreads = WARP ? 128 : LONG ? 1024 : 512;
+
+template <bool LEAVE, bool DF, bool VF, bool BIAS, bool GATE, bool WARP, bool LONG>
+__global__ void __launch_bounds__(kGradThreads<WARP, LONG>, 1) grad_kernel(const GradParams p) {
+  constexpr int V = kGradPieces<WARP>;
+  constexpr int kPart = WARP ? 1 : 64;
   __shared__ float part[2][2][kPart];   // by the row's parity: one barrier a reduction
   grid_dependency_wait();
   grid_launch_dependents();
   const BranchGradArgs& a = p.a;
-  const int tid = threadIdx.x % TPR;
-  const int worker = static_cast<int>(blockIdx.x) * kRows + static_cast<int>(threadIdx.x) / TPR;
+  const Place<WARP, V> at(a.H);
+  const int worker = WARP ? static_cast<int>(blockIdx.x) * 4 + static_cast<int>(threadIdx.x >> 5)
+                          : static_cast<int>(blockIdx.x);
   if (worker >= p.workers) return;
-  const int vecs = static_cast<int>(a.H / 8);
-  const float inv_h = 1.f / static_cast<float>(a.H);
+  const float inv_h = a.inv_h;
   const int64_t r0 = first_row(a.T, p.workers, worker), r1 = first_row(a.T, p.workers, worker + 1);
   const bool layer = a.norm.kind == BSMMA_NORM_LAYER, normed = a.norm.kind != BSMMA_NORM_NONE;
+  const bool dropping = LEAVE && a.drop.threshold != 0;
   Philox gen = {};
-  if (LEAVE && a.drop.threshold) gen = philox_of(a.drop.rng);
+  if (dropping) gen = philox_of(a.drop.rng);
 
-  float sw[V][8], sb[BIAS ? V : 1][8], sg[GATE ? V : 1][8];
+  Vals sw[V], sb[BIAS ? V : 1], sg[GATE ? V : 1];
+  const Vals none = {};
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      sw[i][j] = 0.f;
-      if constexpr (BIAS) sb[i][j] = 0.f;
-      if constexpr (GATE) sg[i][j] = 0.f;
-    }
+  for (int i = 0; i < V; ++i) {
+    sw[i] = none;
+    if constexpr (BIAS) sb[i] = none;
+    if constexpr (GATE) sg[i] = none;
+  }
   int64_t g = 0, g_end = 0;   // the gate in use and the row after its last
   if constexpr (GATE) {
     g = r0 / a.gate_rows;
@@ -79,9 +98,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, 1) grad_kernel(const Gr
                       : p.part_g + (2 * static_cast<int64_t>(worker) + (begin > r0)) * a.H;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if (tid + i * TPR < vecs) store_sums(to + 8 * (tid + i * TPR), sg[i]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sg[i][j] = 0.f;
+        if (at.in(i)) store_sums(to + 8 * (at.at(i)), sg[i]);
+        sg[i] = none;
       }
     }
   };
@@ -91,8 +109,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, 1) grad_kernel(const Gr
   auto fetch = [&](int64_t r) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = tid + i * TPR;
-      if (c < vecs && r < r1) {
+      const int c = at.at(i);
+      if (at.in(i) && r < r1) {
         next_v[i] = load_raw<VF>(a.v, r * a.H + 8 * c);
         next_d[i] = load_raw<DF>(a.d, r * a.H + 8 * c);
       } else {
@@ -111,160 +129,157 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, 1) grad_kernel(const Gr
       }
     }
     Raw<VF> rv[V], rres[LEAVE ? 1 : V];
-    Raw<DF> rd[V];
+    Vals of[V];   // leaving: y_scale * d * keep, what the gate's sum has of dz; entering: d
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       rv[i] = next_v[i];
-      rd[i] = next_d[i];
-      if constexpr (!LEAVE)
-        rres[i] = a.dres && tid + i * TPR < vecs ? load_raw<VF>(a.dres, r * a.H + 8 * (tid + i * TPR))
-                                                 : zero_raw<VF>();
+      of[i] = widen<DF>(next_d[i]);
+      const int c = at.at(i);
+      if constexpr (LEAVE) {
+        if (a.dx && at.in(i)) {
+          Vals d = of[i];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) d.v[j] = mul2(d.v[j], both(a.x_scale));
+          store_raw<DF>(a.dx, r * a.H + 8 * c, narrow<DF>(d));
+        }
+        const float2 scale = both(a.y_scale * a.drop.scale);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) of[i].v[j] = mul2(of[i].v[j], scale);
+      } else {
+        rres[i] = a.dres && at.in(i) ? load_raw<VF>(a.dres, r * a.H + 8 * c) : zero_raw<VF>();
+      }
     }
     fetch(r + 1);
-    uint32_t keep[LEAVE ? V : 1];
-    if constexpr (LEAVE) {
+    if (dropping) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        keep[i] = a.drop.threshold && tid + i * TPR < vecs
-                      ? kept8(gen, static_cast<uint64_t>(r) * vecs + tid + i * TPR, a.drop.threshold)
-                      : 0xFFu;
+        if (at.in(i))
+          drop(of[i], philox(gen, static_cast<uint64_t>(r) * at.vecs + at.at(i)), a.drop.threshold << 16);
     }
     int64_t gate_row = 0;
     if constexpr (GATE) gate_row = g * a.H;
     else if (LEAVE && a.gate)
       gate_row = static_cast<int64_t>(static_cast<uint32_t>(r) / static_cast<uint32_t>(a.gate_rows)) * a.H;
-    // dz of piece i (0 past the row); of: y_scale * d * keep, what the gate's sum has of it
-    auto piece = [&](int i, float (&dz)[8], float (&of)[8]) {
-      widen<DF>(rd[i], of);
-      if constexpr (LEAVE) {
+    auto dz_of = [&](int i) {
+      Vals dz = of[i];
+      if (LEAVE && (GATE || a.gate)) {
+        const Vals w = widen<VF>(load_raw<VF>(a.gate, gate_row + 8 * (at.at(i))));
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          of[j] = keep[i] >> j & 1u ? of[j] * a.y_scale * a.drop.scale : 0.f;
-        if (a.gate && tid + i * TPR < vecs) {
-          float w[8];
-          widen<VF>(load_raw<VF>(a.gate, gate_row + 8 * (tid + i * TPR)), w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) dz[j] = of[j] * w[j];
-          return;
-        }
+        for (int j = 0; j < 4; ++j) dz.v[j] = mul2(dz.v[j], w.v[j]);
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) dz[j] = of[j];
+      return dz;
     };
-    auto weights = [&](int i, float (&w)[8]) {
+    auto weighted = [&](int i, Vals q) {
+      if (a.norm.weight) {
+        const Vals w = load_columns(a.norm.weight, 8 * (at.at(i)));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = 1.f;
-      if (a.norm.weight && tid + i * TPR < vecs) load_columns(a.norm.weight, 8 * (tid + i * TPR), w);
+        for (int j = 0; j < 4; ++j) q.v[j] = mul2(q.v[j], w.v[j]);
+      }
+      return q;
     };
     float mean = 0.f, qmean = 0.f, rs = 1.f, c1 = 0.f;
     if (normed) {
-      float s[2] = {0.f, 0.f};
+      float s[2];
       float (&shared)[2][kPart] = part[r & 1];
       if (layer) {
+        float2 sv[2] = {both(0.f), both(0.f)}, sq[2] = {both(0.f), both(0.f)};
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          float v[8], dz[8], of[8], w[8];
-          widen<VF>(rv[i], v);
-          piece(i, dz, of);
-          weights(i, w);
+          if (!at.in(i)) continue;
+          const Vals v = widen<VF>(rv[i]), q = weighted(i, dz_of(i));
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            s[0] += v[j];
-            s[1] = fmaf(dz[j], w[j], s[1]);
+          for (int j = 0; j < 4; ++j) {
+            sv[j & 1] = add2(sv[j & 1], v.v[j]);
+            sq[j & 1] = add2(sq[j & 1], q.v[j]);
           }
         }
-        row_sums<TPR>(s, shared[0]);
+        s[0] = sum_of(sv), s[1] = sum_of(sq);
+        row_sums<WARP>(s, shared[0]);
         mean = s[0] * inv_h;
         qmean = s[1] * inv_h;
-        s[0] = s[1] = 0.f;
       }
+      float2 sv[2] = {both(0.f), both(0.f)}, sq[2] = {both(0.f), both(0.f)};
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if (tid + i * TPR >= vecs) continue;
-        float v[8], dz[8], of[8], w[8];
-        widen<VF>(rv[i], v);
-        piece(i, dz, of);
-        weights(i, w);
+        if (!at.in(i)) continue;
+        const Vals v = widen<VF>(rv[i]), q = weighted(i, dz_of(i));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float c = v[j] - mean;
-          s[0] = fmaf(c, c, s[0]);
-          s[1] = fmaf(dz[j] * w[j], c, s[1]);
+        for (int j = 0; j < 4; ++j) {
+          const float2 c = add2(v.v[j], both(-mean));
+          sv[j & 1] = __ffma2_rn(c, c, sv[j & 1]);
+          sq[j & 1] = __ffma2_rn(q.v[j], c, sq[j & 1]);
         }
       }
-      row_sums<TPR>(s, shared[1]);
-      rs = __frsqrt_rn(fmaf(s[0], inv_h, a.norm.eps));
+      s[0] = sum_of(sv), s[1] = sum_of(sq);
+      row_sums<WARP>(s, shared[1]);
+      rs = inv_sqrt(fmaf(s[0], inv_h, a.norm.eps));
       c1 = rs * (s[1] * inv_h);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = tid + i * TPR;
-      if (c >= vecs) continue;
-      float v[8], dz[8], of[8], w[8], o[8], b[8];
-      widen<VF>(rv[i], v);
-      piece(i, dz, of);
-      weights(i, w);
-      if constexpr (GATE) {
+      const int c = at.at(i);
+      if (!at.in(i)) continue;
+      const Vals v = widen<VF>(rv[i]), dz = dz_of(i);
+      Vals o = dz;
+      if (normed) {
+        o = weighted(i, dz);
+        Vals n;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) b[j] = 0.f;
-        if (a.norm.bias) load_columns(a.norm.bias, 8 * c, b);
-      }
+        for (int j = 0; j < 4; ++j) {
+          n.v[j] = mul2(add2(v.v[j], both(-mean)), both(rs));
+          sw[i].v[j] = __ffma2_rn(dz.v[j], n.v[j], sw[i].v[j]);
+          o.v[j] = mul2(__ffma2_rn(n.v[j], both(-c1), add2(o.v[j], both(-qmean))), both(rs));
+        }
+        if constexpr (BIAS) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float n = (v[j] - mean) * rs;
-        o[j] = normed ? rs * (fmaf(dz[j], w[j], -qmean) - n * c1) : dz[j];
-        sw[i][j] = fmaf(dz[j], n, sw[i][j]);
-        if constexpr (BIAS) sb[i][j] += dz[j];
+          for (int j = 0; j < 4; ++j) sb[i].v[j] = add2(sb[i].v[j], dz.v[j]);
+        }
         if constexpr (GATE) {
-          const float z = normed ? fmaf(n, w[j], b[j]) : v[j];
-          if (keep[i] >> j & 1u) sg[i][j] = fmaf(of[j], z, sg[i][j]);
+          n = weighted(i, n);
+          if (a.norm.bias) {
+            const Vals b = load_columns(a.norm.bias, 8 * c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) n.v[j] = add2(n.v[j], b.v[j]);
+          }
+          add_gate(sg[i], of[i], n, dropping);
         }
+      } else {
+        if constexpr (GATE) add_gate(sg[i], of[i], v, dropping);
       }
-      const int64_t at = r * a.H + 8 * c;
       if constexpr (!LEAVE) {
-        float res[8];
-        widen<VF>(rres[i], res);
+        const Vals res = widen<VF>(rres[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] += res[j];
+        for (int j = 0; j < 4; ++j) o.v[j] = add2(o.v[j], res.v[j]);
       }
-      store_raw<VF>(a.dv, at, narrow<VF>(o));
-      if constexpr (LEAVE) {
-        if (a.dx) {
-          float d[8];
-          widen<DF>(rd[i], d);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) d[j] *= a.x_scale;
-          store_raw<DF>(a.dx, at, narrow<DF>(d));
-        }
-      }
+      store_raw<VF>(a.dv, r * a.H + 8 * c, narrow<VF>(o));
     }
   }
   flush_gate();
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = tid + i * TPR;
-    if (c >= vecs) continue;
-    const int64_t at = static_cast<int64_t>(worker) * a.H + 8 * c;
-    if (p.part_w) store_sums(p.part_w + at, sw[i]);
-    if constexpr (BIAS) store_sums(p.part_b + at, sb[i]);
+    const int c = at.at(i);
+    if (!at.in(i)) continue;
+    const int64_t to = static_cast<int64_t>(worker) * a.H + 8 * c;
+    if (p.part_w) store_sums(p.part_w + to, sw[i]);
+    if constexpr (BIAS) store_sums(p.part_b + to, sb[i]);
   }
 }
 
-// The threads of a worker by H, as forward but with at most two pieces a thread (four in a
-// warp): with up to three sums a column the registers do not hold more.
 template <bool LEAVE, bool DF, bool VF, bool BIAS, bool GATE>
 bsmma_status launch_grad_kernel(const GradParams& p, cudaStream_t stream) {
   const int64_t vecs = p.a.H / 8;
   const unsigned blocks = static_cast<unsigned>(p.workers);
   cudaError_t e;
-  if (vecs <= 32 * 4)
-    e = launch_dependent(grad_kernel<LEAVE, DF, VF, BIAS, GATE, 32, 4>, dim3((blocks + 3) / 4), dim3(128), 0, stream, p);
-  else if (vecs <= 256 * 2)
-    e = launch_dependent(grad_kernel<LEAVE, DF, VF, BIAS, GATE, 256, 2>, dim3(blocks), dim3(256), 0, stream, p);
-  else if (vecs <= 512 * 2)
-    e = launch_dependent(grad_kernel<LEAVE, DF, VF, BIAS, GATE, 512, 2>, dim3(blocks), dim3(512), 0, stream, p);
-  else
-    e = launch_dependent(grad_kernel<LEAVE, DF, VF, BIAS, GATE, 1024, 2>, dim3(blocks), dim3(1024), 0, stream, p);
+  if (vecs <= 32 * kGradPieces<true>) {
+    e = launch_dependent(grad_kernel<LEAVE, DF, VF, BIAS, GATE, true, false>, dim3((blocks + 3) / 4), dim3(128), 0,
+                         stream, p);
+  } else {
+    constexpr int kWarpVecs = 32 * kGradPieces<false>;
+    const unsigned threads = static_cast<unsigned>(32 * ((vecs + kWarpVecs - 1) / kWarpVecs));
+    e = launch_dependent(threads <= 512 ? grad_kernel<LEAVE, DF, VF, BIAS, GATE, false, false>
+                                        : grad_kernel<LEAVE, DF, VF, BIAS, GATE, false, true>,
+                         dim3(blocks), dim3(threads), 0, stream, p);
+  }
   return cuda_ok(e);
 }
 
