@@ -144,6 +144,27 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* part) {
       for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kFull, v[i], o);
   }
 }
+// Two sums at once, the lower half-warp on the first and the upper on the second: half the
+// shuffles.
+template <bool WARP>
+__device__ __forceinline__ float2 row_sums2(float2 v, float* part) {
+  const int lane = threadIdx.x & 31;
+  const bool upper = lane & 16;
+  float s = (upper ? v.y : v.x) + __shfl_xor_sync(kFull, upper ? v.x : v.y, 16);
+#pragma unroll
+  for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+  if constexpr (!WARP) {
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    if ((lane & 15) == 0) part[(lane << 1) + warp] = s;   // [sum][32 warps]
+    __syncthreads();
+    const float* from = part + ((lane & 16) << 1) + (lane & 15);
+    s = (lane & 15) < warps ? from[0] : 0.f;
+    if ((lane & 15) + 16 < warps) s += from[16];
+#pragma unroll
+    for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+  }
+  return make_float2(__shfl_sync(kFull, s, 0), __shfl_sync(kFull, s, 16));
+}
 template <bool WARP>
 __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* part) {
   v = __reduce_max_sync(kFull, v);

@@ -38,17 +38,6 @@ __device__ __forceinline__ void store_sums(float* to, const Vals& f) {
   *reinterpret_cast<float4*>(to) = make_float4(f.v[0].x, f.v[0].y, f.v[1].x, f.v[1].y);
   *reinterpret_cast<float4*>(to + 4) = make_float4(f.v[2].x, f.v[2].y, f.v[3].x, f.v[3].y);
 }
-__device__ __forceinline__ float sum_of(const float2 (&a)[2]) { return (a[0].x + a[0].y) + (a[1].x + a[1].y); }
-
-// sum += of * z, where what was dropped (of is 0) adds nothing whatever z is.
-__device__ __forceinline__ void add_gate(Vals& sum, const Vals& of, const Vals& z, bool dropping) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float2 u = z.v[j];
-    if (dropping) u = make_float2(of.v[j].x == 0.f ? 0.f : u.x, of.v[j].y == 0.f ? 0.f : u.y);
-    sum.v[j] = __ffma2_rn(of.v[j], u, sum.v[j]);
-  }
-}
 
 // A thread's pieces of a row: with up to three sums a column the registers hold two (a warp's
 // rows are short, and four of them keep it busy).
@@ -98,28 +87,49 @@ __global__ void __launch_bounds__(kGradThreads<WARP, LONG>, 1) grad_kernel(const
                       : p.part_g + (2 * static_cast<int64_t>(worker) + (begin > r0)) * a.H;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if (at.in(i)) store_sums(to + 8 * (at.at(i)), sg[i]);
+        // without a norm the factor is still to come (with one it came with n)
+        if (!normed)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sg[i].v[j] = mul2(sg[i].v[j], both(a.y_scale * a.drop.scale));
+        if (at.in(i)) store_sums(to + 8 * at.at(i), sg[i]);
         sg[i] = none;
       }
     }
   };
 
+  // dz is linear in d: its constant factor goes into the row's factors and into the sums
+  const float scale = LEAVE ? a.y_scale * a.drop.scale : 1.f;
+  // everything a row is read from and written to lies at these places, a row after the other
+  const int64_t first = r0 * a.H + 8 * at.base;
+  const char* v_at = static_cast<const char*>(a.v) + first * (VF ? 4 : 2);
+  const char* d_at = static_cast<const char*>(a.d) + first * (DF ? 4 : 2);
+  const int64_t v_step = a.H * (VF ? 4 : 2), d_step = a.H * (DF ? 4 : 2);
+  int64_t out = 0;   // rows behind v_at's first, in bytes of v
+  char* dv_at = static_cast<char*>(a.dv) + first * (VF ? 4 : 2);
+  const char* res_at = !LEAVE && a.dres ? static_cast<const char*>(a.dres) + first * (VF ? 4 : 2) : nullptr;
+  char* dx_at = LEAVE && a.dx ? static_cast<char*>(a.dx) + first * (DF ? 4 : 2) : nullptr;
+  const float* w_at = a.norm.weight ? a.norm.weight + 8 * at.base : nullptr;
+  const float* b_at = GATE && a.norm.bias ? a.norm.bias + 8 * at.base : nullptr;
+  const __nv_bfloat16* gate_bf16 = nullptr;   // the gate's row, in its type
+  const float* gate_f32 = nullptr;
+  auto gate_piece = [&](int i) {
+    if constexpr (VF) return widen<true>(load_raw<true>(gate_f32, 256 * i));
+    else return widen<false>(load_raw<false>(gate_bf16, 256 * i));
+  };
+
   Raw<VF> next_v[V];
   Raw<DF> next_d[V];
-  auto fetch = [&](int64_t r) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = at.at(i);
-      if (at.in(i) && r < r1) {
-        next_v[i] = load_raw<VF>(a.v, r * a.H + 8 * c);
-        next_d[i] = load_raw<DF>(a.d, r * a.H + 8 * c);
-      } else {
-        next_v[i] = zero_raw<VF>();
-        next_d[i] = zero_raw<DF>();
+  for (int i = 0; i < V; ++i) next_v[i] = zero_raw<VF>(), next_d[i] = zero_raw<DF>();
+  auto fetch = [&] {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (at.in(i)) {
+        next_v[i] = load_raw<VF>(v_at, 256 * i);
+        next_d[i] = load_raw<DF>(d_at, 256 * i);
       }
-    }
   };
-  fetch(r0);
+  if (r0 < r1) fetch();
   for (int64_t r = r0; r < r1; ++r) {
     if constexpr (GATE) {
       if (r == g_end) {
@@ -128,140 +138,166 @@ __global__ void __launch_bounds__(kGradThreads<WARP, LONG>, 1) grad_kernel(const
         g_end += a.gate_rows;
       }
     }
-    Raw<VF> rv[V], rres[LEAVE ? 1 : V];
-    Vals of[V];   // leaving: y_scale * d * keep, what the gate's sum has of dz; entering: d
+    if (LEAVE && (GATE || a.gate)) {
+      const int64_t row = GATE ? g : static_cast<int64_t>(static_cast<uint32_t>(r) / static_cast<uint32_t>(a.gate_rows));
+      if constexpr (VF) gate_f32 = static_cast<const float*>(a.gate) + row * a.H + 8 * at.base;
+      else gate_bf16 = static_cast<const __nv_bfloat16*>(a.gate) + row * a.H + 8 * at.base;
+    }
+    Vals c[V], of[V];   // the rows, later less their mean; d, without what was dropped
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      rv[i] = next_v[i];
+      c[i] = widen<VF>(next_v[i]);
       of[i] = widen<DF>(next_d[i]);
-      const int c = at.at(i);
-      if constexpr (LEAVE) {
-        if (a.dx && at.in(i)) {
-          Vals d = of[i];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) d.v[j] = mul2(d.v[j], both(a.x_scale));
-          store_raw<DF>(a.dx, r * a.H + 8 * c, narrow<DF>(d));
-        }
-        const float2 scale = both(a.y_scale * a.drop.scale);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) of[i].v[j] = mul2(of[i].v[j], scale);
-      } else {
-        rres[i] = a.dres && at.in(i) ? load_raw<VF>(a.dres, r * a.H + 8 * c) : zero_raw<VF>();
-      }
     }
-    fetch(r + 1);
+    v_at += v_step;
+    d_at += d_step;
+    if (r + 1 < r1) fetch();
+    if (LEAVE && dx_at) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        Vals d;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d.v[j] = mul2(of[i].v[j], both(a.x_scale));
+        if (at.in(i)) store_raw<DF>(dx_at, 256 * i, narrow<DF>(d));
+      }
+      dx_at += d_step;
+    }
     if (dropping) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (at.in(i))
-          drop(of[i], philox(gen, static_cast<uint64_t>(r) * at.vecs + at.at(i)), a.drop.threshold << 16);
+        drop(of[i], philox(gen, static_cast<uint64_t>(r) * at.vecs + at.at(i)), a.drop.threshold << 16);
     }
-    int64_t gate_row = 0;
-    if constexpr (GATE) gate_row = g * a.H;
-    else if (LEAVE && a.gate)
-      gate_row = static_cast<int64_t>(static_cast<uint32_t>(r) / static_cast<uint32_t>(a.gate_rows)) * a.H;
-    auto dz_of = [&](int i) {
-      Vals dz = of[i];
+    // dz / scale, and times the weight
+    auto gated = [&](int i) {
+      Vals z = of[i];
       if (LEAVE && (GATE || a.gate)) {
-        const Vals w = widen<VF>(load_raw<VF>(a.gate, gate_row + 8 * (at.at(i))));
+        const Vals w = gate_piece(i);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) dz.v[j] = mul2(dz.v[j], w.v[j]);
+        for (int j = 0; j < 4; ++j) z.v[j] = mul2(z.v[j], w.v[j]);
       }
-      return dz;
+      return z;
     };
-    auto weighted = [&](int i, Vals q) {
-      if (a.norm.weight) {
-        const Vals w = load_columns(a.norm.weight, 8 * (at.at(i)));
+    auto weighted = [&](int i, Vals z) {
+      if (w_at) {
+        const Vals w = load_columns(w_at, 256 * i);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) q.v[j] = mul2(q.v[j], w.v[j]);
+        for (int j = 0; j < 4; ++j) z.v[j] = mul2(z.v[j], w.v[j]);
       }
-      return q;
+      return z;
     };
-    float mean = 0.f, qmean = 0.f, rs = 1.f, c1 = 0.f;
-    if (normed) {
-      float s[2];
-      float (&shared)[2][kPart] = part[r & 1];
-      if (layer) {
-        float2 sv[2] = {both(0.f), both(0.f)}, sq[2] = {both(0.f), both(0.f)};
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if (!at.in(i)) continue;
-          const Vals v = widen<VF>(rv[i]), q = weighted(i, dz_of(i));
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            sv[j & 1] = add2(sv[j & 1], v.v[j]);
-            sq[j & 1] = add2(sq[j & 1], q.v[j]);
-          }
-        }
-        s[0] = sum_of(sv), s[1] = sum_of(sq);
-        row_sums<WARP>(s, shared[0]);
-        mean = s[0] * inv_h;
-        qmean = s[1] * inv_h;
-      }
-      float2 sv[2] = {both(0.f), both(0.f)}, sq[2] = {both(0.f), both(0.f)};
+    if (!normed) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         if (!at.in(i)) continue;
-        const Vals v = widen<VF>(rv[i]), q = weighted(i, dz_of(i));
+        Vals z = gated(i);
+        if constexpr (GATE) {
+          // a dropped value (of is 0) adds nothing to the gate's sum, whatever it is
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 u = make_float2(of[i].v[j].x == 0.f ? 0.f : c[i].v[j].x, of[i].v[j].y == 0.f ? 0.f : c[i].v[j].y);
+            sg[i].v[j] = __ffma2_rn(of[i].v[j], u, sg[i].v[j]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z.v[j] = mul2(z.v[j], both(scale));
+        store_raw<VF>(dv_at + out, 256 * i, narrow<VF>(z));
+      }
+      out += v_step;
+      continue;
+    }
+    // q is kept where registers hold it (else its factors come from the L1 cache again)
+    constexpr bool kKeep = !GATE && !BIAS && !VF;
+    Vals q[kKeep ? V : 1];
+    float (&shared)[2][kPart] = part[r & 1];
+    float2 s, qmean = both(0.f);
+    if (layer) {
+      float2 sv = both(0.f), sq = both(0.f);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (at.in(i)) {
+          const Vals z = weighted(i, gated(i));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sv = add2(sv, c[i].v[j]), sq = add2(sq, z.v[j]);
+        }
+      s = row_sums2<WARP>(make_float2(sv.x + sv.y, sq.x + sq.y), shared[0]);
+      const float2 minus_mean = both(-s.x * inv_h);
+      qmean = both(s.y * inv_h);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[i].v[j] = add2(c[i].v[j], minus_mean);
+    }
+    float2 sv = both(0.f), sq = both(0.f);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (at.in(i)) {
+        const Vals z = weighted(i, gated(i));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 c = add2(v.v[j], both(-mean));
-          sv[j & 1] = __ffma2_rn(c, c, sv[j & 1]);
-          sq[j & 1] = __ffma2_rn(q.v[j], c, sq[j & 1]);
+          sv = __ffma2_rn(c[i].v[j], c[i].v[j], sv);
+          sq = __ffma2_rn(z.v[j], c[i].v[j], sq);
         }
+        if constexpr (kKeep) q[i] = z;
       }
-      s[0] = sum_of(sv), s[1] = sum_of(sq);
-      row_sums<WARP>(s, shared[1]);
-      rs = inv_sqrt(fmaf(s[0], inv_h, a.norm.eps));
-      c1 = rs * (s[1] * inv_h);
+    Raw<VF> res[LEAVE ? 1 : V];   // on its way during the reduction
+    if constexpr (!LEAVE) {
+      if (res_at) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (at.in(i)) res[i] = load_raw<VF>(res_at + out, 256 * i);
+      }
     }
+    s = row_sums2<WARP>(make_float2(sv.x + sv.y, sq.x + sq.y), shared[1]);
+    // dv = scale * (rs (q - mean q) - c rs^3 mean(q c)); n = c rs
+    const float rs = inv_sqrt(fmaf(s.x, inv_h, a.norm.eps)), rss = rs * scale;
+    const float2 fq = both(rss), fc = both(-(rs * (s.y * inv_h)) * rs * rss), f0 = both(-rss * qmean.x);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = at.at(i);
       if (!at.in(i)) continue;
-      const Vals v = widen<VF>(rv[i]), dz = dz_of(i);
-      Vals o = dz;
-      if (normed) {
-        o = weighted(i, dz);
-        Vals n;
+      const Vals z = gated(i);
+      Vals o;
+      if constexpr (kKeep) o = q[i];
+      else o = weighted(i, z);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          n.v[j] = mul2(add2(v.v[j], both(-mean)), both(rs));
-          sw[i].v[j] = __ffma2_rn(dz.v[j], n.v[j], sw[i].v[j]);
-          o.v[j] = mul2(__ffma2_rn(n.v[j], both(-c1), add2(o.v[j], both(-qmean))), both(rs));
-        }
-        if constexpr (BIAS) {
+      for (int j = 0; j < 4; ++j) {
+        const float2 n = mul2(c[i].v[j], fq);   // n scale
+        o.v[j] = __ffma2_rn(c[i].v[j], fc, __ffma2_rn(o.v[j], fq, f0));
+        sw[i].v[j] = __ffma2_rn(z.v[j], n, sw[i].v[j]);
+        if constexpr (BIAS) sb[i].v[j] = add2(sb[i].v[j], z.v[j]);
+        if constexpr (GATE) c[i].v[j] = n;
+      }
+      if constexpr (GATE) {
+        Vals n = weighted(i, c[i]);
+        if (b_at) {
+          const Vals b = load_columns(b_at, 256 * i);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sb[i].v[j] = add2(sb[i].v[j], dz.v[j]);
+          for (int j = 0; j < 4; ++j) n.v[j] = __ffma2_rn(b.v[j], both(scale), n.v[j]);
         }
-        if constexpr (GATE) {
-          n = weighted(i, n);
-          if (a.norm.bias) {
-            const Vals b = load_columns(a.norm.bias, 8 * c);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) n.v[j] = add2(n.v[j], b.v[j]);
-          }
-          add_gate(sg[i], of[i], n, dropping);
-        }
-      } else {
-        if constexpr (GATE) add_gate(sg[i], of[i], v, dropping);
+        for (int j = 0; j < 4; ++j) sg[i].v[j] = __ffma2_rn(of[i].v[j], n.v[j], sg[i].v[j]);
       }
       if constexpr (!LEAVE) {
-        const Vals res = widen<VF>(rres[i]);
+        if (res_at) {
+          const Vals more = widen<VF>(res[i]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o.v[j] = add2(o.v[j], res.v[j]);
+          for (int j = 0; j < 4; ++j) o.v[j] = add2(o.v[j], more.v[j]);
+        }
       }
-      store_raw<VF>(a.dv, r * a.H + 8 * c, narrow<VF>(o));
+      store_raw<VF>(dv_at + out, 256 * i, narrow<VF>(o));
     }
+    out += v_step;
   }
   flush_gate();
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = at.at(i);
     if (!at.in(i)) continue;
-    const int64_t to = static_cast<int64_t>(worker) * a.H + 8 * c;
+    const int64_t to = static_cast<int64_t>(worker) * a.H + 8 * at.at(i);
     if (p.part_w) store_sums(p.part_w + to, sw[i]);
-    if constexpr (BIAS) store_sums(p.part_b + to, sb[i]);
+    if constexpr (BIAS) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sb[i].v[j] = mul2(sb[i].v[j], both(scale));
+      store_sums(p.part_b + to, sb[i]);
+    }
   }
 }
 
