@@ -44,20 +44,22 @@ constexpr int kMaxSlots = 1024, kMaxExperts = 1024;
 constexpr int kTableBytes = 8 + kMaxSlots * 10;   // sizeof(WeightedTable)
 
 // ------------------------------------------------------------------------- weights
-// A stage is 128 bytes of each of a warp's 32 rows: `kBlocks` blocks of 32 K, of which a row's
-// four lanes have eight consecutive values each, `kLaneBytes`.
-constexpr int kRowStage = 128;
+// A stage is 64 bytes of each of a warp's 32 rows: `kBlocks` blocks of 32 K, of which a row's four
+// lanes have eight consecutive values each, `kLaneBytes`.  (Stages of 128 bytes save a few
+// instructions, but where the sums of many tokens leave room for two of them only one is on its
+// way: 32 tokens of INT8 experts 554 us against 498; one token of E4M3 experts 81 and 84.)
+constexpr int kRowStage = 64, kSetStage = 8 * kRowStage, kCodeStage = 4 * kSetStage;
 template <int FORM>
 struct Form {
   static constexpr bool kMx = FORM >= BSMMA_OPERAND_E4M3, kBf16 = FORM == BSMMA_OPERAND_BF16;
   static constexpr int kLaneBytes = kBf16 ? 16 : FORM == BSMMA_OPERAND_E2M1 ? 4 : 8;
   static constexpr int kBlockBytes = 4 * kLaneBytes, kBlocks = kRowStage / kBlockBytes;
   static constexpr int kStageK = 32 * kBlocks;
-  static constexpr int kStage = 32 * (kRowStage + (kMx ? kBlocks : 0));   // a warp's, scales behind the codes
-  // Block b of row g (of a set of eight) lies at block b ^ g's place of the row, so that the lanes
-  // of one shared-memory access are in different banks.
+  static constexpr int kStage = kCodeStage + (kMx ? 32 * 4 : 0);   // a warp's: codes, then a word of scales a row
+  // Block b of row g (of a set of eight) lies at the place of block b ^ (g / 2) of the row, so that
+  // the lanes of one shared-memory access are in different banks (rows two apart share them).
   static __device__ __forceinline__ uint32_t place(int g, int byte) {
-    return g * kRowStage + (byte ^ (g & (kBlocks - 1)) * kBlockBytes);
+    return g * kRowStage + (byte ^ ((g >> 1) & (kBlocks - 1)) * kBlockBytes);
   }
 };
 template <int FORM>
@@ -65,16 +67,11 @@ __device__ __forceinline__ int64_t row_bytes(int64_t K) {
   return FORM == BSMMA_OPERAND_BF16 ? 2 * K : FORM == BSMMA_OPERAND_E2M1 ? K / 2 : K;
 }
 
-// Four E8M0 codes as FP32 (through BF16, which holds 2^-127 and has a NaN for 255).
-__device__ __forceinline__ void e8m0x4(uint32_t codes, float (&f)[4]) {
-  uint32_t lo, hi;
-  asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.bf16x2.ue8m0x2 %0, a;\n\tcvt.rn.bf16x2.ue8m0x2 %1, b;}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(codes));
-  f[0] = __uint_as_float(lo << 16);
-  f[1] = __uint_as_float(lo & 0xFFFF0000u);
-  f[2] = __uint_as_float(hi << 16);
-  f[3] = __uint_as_float(hi & 0xFFFF0000u);
+// Two E8M0 codes as FP32 (through BF16, which holds 2^-127 and has a NaN for 255).
+__device__ __forceinline__ float2 e8m0x2(uint32_t codes) {
+  uint32_t two;
+  asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, a;}" : "=r"(two) : "r"(codes));
+  return make_float2(__uint_as_float(two << 16), __uint_as_float(two & 0xFFFF0000u));
 }
 
 // A lane's eight weights of a block, at shared address `at`, as four pairs (BF16 or FP16).
@@ -146,9 +143,8 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst_smem, const void* src, 
 __device__ __forceinline__ void cp_async_16(uint32_t dst_smem, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async_word(uint32_t dst_smem, const void* src, bool in) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst_smem), "l"(src), "r"(in ? 4 : 0)
-               : "memory");
+__device__ __forceinline__ void cp_async_4(uint32_t dst_smem, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst_smem), "l"(src) : "memory");
 }
 
 // A value's power of two and FP16 form: the largest finite magnitude of a group of values goes to
@@ -312,159 +308,134 @@ struct Sets {
 };
 
 // Starts the copies of stage `stage` (from the row's first byte): lane (g, t) copies the 16-byte
-// chunks t and t + 4 of its row in each set, lane l the scales of row l.
+// chunk t of its row in each set, lane l the word that has the scales of row l.
 template <int FORM>
 __device__ __forceinline__ void load_stage(uint32_t to, const Source& from, const Sets& sets, int stage,
-                                           int64_t bytes, int64_t blocks, bool words) {
+                                           int64_t bytes, bool words) {
   using F = Form<FORM>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int64_t at = static_cast<int64_t>(stage) * kRowStage;
-  const uint32_t d0 = to + F::place(g, 16 * t), d1 = to + F::place(g, 64 + 16 * t);
+  const uint32_t d = to + F::place(g, 16 * t);
   const uint8_t* src = from.row + at;
   if (at + kRowStage <= bytes) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      cp_async_16(d0 + r * 1024, src + sets.bytes[r]);
-      cp_async_16(d1 + r * 1024, src + sets.bytes[r] + 64);
-    }
+    for (int r = 0; r < 4; ++r) cp_async_16(d + r * kSetStage, src + sets.bytes[r]);
   } else {   // the end of K: what is past it counts as zero
-    const bool in0 = at + 16 * t < bytes, in1 = at + 64 + 16 * t < bytes;
+    const bool in = at + 16 * t < bytes;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      cp_async_16(d0 + r * 1024, in0 ? src + sets.bytes[r] : from.row, in0);
-      cp_async_16(d1 + r * 1024, in1 ? src + sets.bytes[r] + 64 : from.row, in1);
-    }
+    for (int r = 0; r < 4; ++r) cp_async_16(d + r * kSetStage, in ? src + sets.bytes[r] : from.row, in);
   }
-  if constexpr (F::kMx) {
-    if (words) {
-      const int64_t b = static_cast<int64_t>(stage) * F::kBlocks;
-#pragma unroll
-      for (int i = 0; i < F::kBlocks; i += 4) {
-        const bool in = b + i < blocks;
-        cp_async_word(to + 4096 + lane * F::kBlocks + i, in ? from.scales + b + i : from.scales, in);
-      }
-    }
-  }
+  // (a word is four blocks' scales: of two stages where a stage has two)
+  if constexpr (F::kMx)
+    if (words)
+      cp_async_4(to + kCodeStage + 4 * lane, from.scales + (static_cast<int64_t>(stage) * F::kBlocks & ~3));
 }
 
-// What the columns bring to a chunk of up to four blocks: the lane's eight values of each
-// block, and the powers of two of the lane's two result columns.  It is read from L2 or L1, so it is
-// asked for ahead of the wait for the weights.
+// What the columns bring to a stage: the lane's eight values of each block, and the powers of two
+// of the lane's two result columns.  It is read from L2 or L1, so it is asked for ahead of the wait
+// for the weights.
 template <int FORM, int NT, bool POWERS>
 struct Columns {
-  static constexpr int kChunk = Form<FORM>::kBlocks < 4 ? Form<FORM>::kBlocks : 4;
-  uint4 x[kChunk][NT];
-  float p[POWERS ? kChunk : 1][NT][2];
+  uint4 x[Form<FORM>::kBlocks][NT];
+  float p[POWERS ? Form<FORM>::kBlocks : 1][NT][2];
 };
-// x: the lane's column (of each eight) from its first K of the chunk on; left: K from there to the
-// end; powers: of the chunk's blocks.
+// x: the lane's column (of each eight) from its first K of the stage on; left: K from there to the
+// end; powers: of the stage's blocks.
 template <int FORM, int NT, bool POWERS>
 __device__ __forceinline__ void load_columns(Columns<FORM, NT, POWERS>& c, const uint16_t* const (&x)[NT],
-                                             int64_t left, const float* const (&powers)[NT][2], int b0) {
-  constexpr int kChunk = Columns<FORM, NT, POWERS>::kChunk;
+                                             int64_t left, const float* const (&powers)[NT][2]) {
+  constexpr int kBlocks = Form<FORM>::kBlocks;
   const int t = threadIdx.x & 3;
-  if (left + 8 * t >= 32 * (b0 + kChunk)) {   // (uniform)
+  if (left + 8 * t >= 32 * kBlocks) {   // (uniform)
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j)
+    for (int j = 0; j < kBlocks; ++j)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        c.x[j][n] = *reinterpret_cast<const uint4*>(x[n] + 32 * (b0 + j));
+        c.x[j][n] = *reinterpret_cast<const uint4*>(x[n] + 32 * j);
         if constexpr (POWERS) {
-          c.p[j][n][0] = powers[n][0][b0 + j];
-          c.p[j][n][1] = powers[n][1][b0 + j];
+          c.p[j][n][0] = powers[n][0][j];
+          c.p[j][n][1] = powers[n][1][j];
         }
       }
   } else {
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j)
+    for (int j = 0; j < kBlocks; ++j)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         c.x[j][n] = make_uint4(0, 0, 0, 0);
-        if (32 * (b0 + j) < left) c.x[j][n] = *reinterpret_cast<const uint4*>(x[n] + 32 * (b0 + j));
+        if (32 * j < left) c.x[j][n] = *reinterpret_cast<const uint4*>(x[n] + 32 * j);
         if constexpr (POWERS) {
-          const bool in = 32 * (b0 + j) < left + 8 * t;
-          c.p[j][n][0] = in ? powers[n][0][b0 + j] : 0.f;
-          c.p[j][n][1] = in ? powers[n][1][b0 + j] : 0.f;
+          const bool in = 32 * j < left + 8 * t;
+          c.p[j][n][0] = in ? powers[n][0][j] : 0.f;
+          c.p[j][n][1] = in ? powers[n][1][j] : 0.f;
         }
       }
   }
 }
 
-// Multiplies a chunk's weights into acc: operand m has set 2 m in its upper and set 2 m + 1 in
-// its lower eight rows.  scale(r, b): where the scales cannot be copied by words, block b's of the
-// lane's row of set r (asked for inside K only).
-template <int FORM, int NT, bool POWERS, typename Scale>
-__device__ __forceinline__ void multiply(float (&acc)[2][NT][4], const Columns<FORM, NT, POWERS>& c,
-                                         uint32_t ring, int b0, int64_t left, const Scale& scale, bool words) {
+// A stage of the ring: the columns' values asked for, the wait for the weights, the next stage's
+// load, and the products into acc: operand m has set 2 m in its upper and set 2 m + 1 in its lower
+// eight rows.  odd: the stage's scales are the upper half of their word (two blocks a stage);
+// scale(r, b): where the scales cannot be copied by words, block b's of the lane's row of set r (asked
+// for inside K only).
+template <int FORM, int NT, bool POWERS, int PENDING, typename Load, typename Scale>
+__device__ __forceinline__ void stage_products(float (&acc)[2][NT][4], const uint16_t* const (&x)[NT],
+                                               const float* const (&powers)[NT][2], int64_t left, uint32_t ring,
+                                               const Load& load, const Scale& scale, bool words, bool odd) {
   using F = Form<FORM>;
-  constexpr int kChunk = Columns<FORM, NT, POWERS>::kChunk;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  float sw[F::kMx ? 4 : 1][4];
+  Columns<FORM, NT, POWERS> c;
+  load_columns<FORM, NT, POWERS>(c, x, left, powers);
+  cp_async_wait<PENDING>();
+  __syncwarp();   // the other lanes' copies, and their reads of the slot that is filled next
+  load();
+  float2 sw[F::kMx ? 4 : 1][F::kMx ? F::kBlocks / 2 : 1];
   if constexpr (F::kMx) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       uint32_t codes = 0;
-      if (words)
-        asm volatile("ld.shared.b32 %0, [%1];"
-                     : "=r"(codes)
-                     : "r"(ring + 4096 + (r * 8 + g) * F::kBlocks + b0));
-      else
-        for (int j = 0; j < 4; ++j)
-          if (32 * (b0 + j) < left + 8 * t) codes |= scale(r, b0 + j) << (8 * j);
-      e8m0x4(codes, sw[r]);
+      if (words) {
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(codes) : "r"(ring + kCodeStage + 4 * (r * 8 + g)));
+        if (F::kBlocks == 2 && odd) codes >>= 16;
+      } else {
+        for (int j = 0; j < F::kBlocks; ++j)
+          if (32 * j < left + 8 * t) codes |= scale(r, j) << (8 * j);
+      }
+#pragma unroll
+      for (int j = 0; j < F::kBlocks / 2; ++j) sw[r][j] = e8m0x2(codes >> (16 * j));
     }
   }
 #pragma unroll
-  for (int j = 0; j < kChunk; ++j) {
-    const uint32_t at = ring + F::place(g, (b0 + j) * F::kBlockBytes + t * F::kLaneBytes);
+  for (int j = 0; j < F::kBlocks; ++j) {
+    const uint32_t at = ring + F::place(g, j * F::kBlockBytes + t * F::kLaneBytes);
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       uint32_t hi[4], lo[4];
-      load_weights<FORM>(at + 2 * m * 1024, hi);
-      load_weights<FORM>(at + (2 * m + 1) * 1024, lo);
+      load_weights<FORM>(at + 2 * m * kSetStage, hi);
+      load_weights<FORM>(at + (2 * m + 1) * kSetStage, lo);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const uint4& x = c.x[j][n];
+        const uint4& v = c.x[j][n];
         if constexpr (F::kMx || POWERS) {
           float d[4];
-          mma<F::kBf16, true>(d, hi[0], lo[0], hi[1], lo[1], x.x, x.y);
-          mma<F::kBf16, false>(d, hi[2], lo[2], hi[3], lo[3], x.z, x.w);
+          mma<F::kBf16, true>(d, hi[0], lo[0], hi[1], lo[1], v.x, v.y);
+          mma<F::kBf16, false>(d, hi[2], lo[2], hi[3], lo[3], v.z, v.w);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float f;
-            if constexpr (F::kMx && POWERS) f = sw[2 * m + (i >> 1)][j] * c.p[j][n][i & 1];
-            else if constexpr (F::kMx) f = sw[2 * m + (i >> 1)][j];
-            else f = c.p[j][n][i & 1];
+            float f = 1.f;
+            if constexpr (F::kMx) {
+              const float2 two = sw[2 * m + (i >> 1)][j >> 1];
+              f = j & 1 ? two.y : two.x;
+            }
+            if constexpr (POWERS) f *= c.p[j][n][i & 1];
             acc[m][n][i] = fmaf(d[i], f, acc[m][n][i]);
           }
         } else {
-          mma<F::kBf16, false>(acc[m][n], hi[0], lo[0], hi[1], lo[1], x.x, x.y);
-          mma<F::kBf16, false>(acc[m][n], hi[2], lo[2], hi[3], lo[3], x.z, x.w);
+          mma<F::kBf16, false>(acc[m][n], hi[0], lo[0], hi[1], lo[1], v.x, v.y);
+          mma<F::kBf16, false>(acc[m][n], hi[2], lo[2], hi[3], lo[3], v.z, v.w);
         }
       }
     }
-  }
-}
-
-// A stage of the ring: the columns' first chunk, the wait for the weights, the next stage's load,
-// and the products.
-template <int FORM, int NT, bool POWERS, int PENDING, typename Load, typename Scale>
-__device__ __forceinline__ void stage_products(float (&acc)[2][NT][4], const uint16_t* const (&x)[NT],
-                                               const float* const (&powers)[NT][2], int64_t left, uint32_t ring,
-                                               const Load& load, const Scale& scale, bool words) {
-  using Cols = Columns<FORM, NT, POWERS>;
-  Cols c;
-  load_columns<FORM, NT, POWERS>(c, x, left, powers, 0);
-  cp_async_wait<PENDING>();
-  __syncwarp();   // the other lanes' copies, and their reads of the slot that is filled next
-  load();
-#pragma unroll
-  for (int b0 = 0; b0 < Form<FORM>::kBlocks; b0 += Cols::kChunk) {
-    Cols next;
-    if (b0 + Cols::kChunk < Form<FORM>::kBlocks)
-      load_columns<FORM, NT, POWERS>(next, x, left, powers, b0 + Cols::kChunk);
-    multiply<FORM, NT, POWERS>(acc, c, ring, b0, left, scale, words);
-    c = next;
   }
 }
 
@@ -496,25 +467,36 @@ __device__ __forceinline__ Unit unit_of(const Table& table, int u, int tiles) {
 }
 
 // The inner rows.  Warp w has rows of half w & 1 (16 inner columns) and every eighth stage of K
-// from w >> 1 on.
-constexpr int kGroups = kWarps / 2;
+// from w >> 1 on; one more warp adds the sums up and finishes a unit while the others are at the next
+// (done by one of theirs, the other fifteen waited for it a quarter of their time).
+constexpr int kGroups = kWarps / 2, kInThreads = kThreads + 32;
 template <int FORM, int NT>
 struct InCfg {
   static constexpr int kStage = Form<FORM>::kStage;
   static constexpr int kSums = kWarps * 2 * NT * 512;
-  static constexpr int kStages = (232448 - kSums - static_cast<int>(sizeof(Table))) / (kWarps * kStage);
+  static constexpr int kFixed = kSums + static_cast<int>(sizeof(Table)) + 32;
+  static constexpr int kStages = (232448 - kFixed) / (kWarps * kStage);
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kBytes = kRing + kSums + static_cast<int>(sizeof(Table));
+  static constexpr int kBytes = kRing + kFixed;
   static_assert(kStages >= 2, "one stage in flight");
 };
 
 template <int FORM, int NT>
-__global__ void __launch_bounds__(kThreads, 1) step_in_kernel(const StepArgs a) {
+__global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a) {
   using C = InCfg<FORM, NT>;
   using F = Form<FORM>;
   extern __shared__ __align__(128) uint8_t smem[];
   float4* sums = reinterpret_cast<float4*>(smem + C::kRing);   // [operand of 4][NT][group][lane]
-  Table& table = *reinterpret_cast<Table*>(smem + C::kRing + C::kSums);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kRing + C::kSums);   // the sums are there
+  uint64_t* empty = full + 1;                                                 // ... have been read
+  volatile int* abort = reinterpret_cast<volatile int*>(full + 2);
+  Table& table = *reinterpret_cast<Table*>(smem + C::kRing + C::kSums + 32);
+  if (threadIdx.x == 0) {
+    mbar_init(full, kWarps);
+    mbar_init(empty, 1);
+    fence_mbar_init();
+    *abort = 0;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int half = warp & 1, group = warp >> 1;
   grid_dependency_wait();
@@ -535,6 +517,74 @@ __global__ void __launch_bounds__(kThreads, 1) step_in_kernel(const StepArgs a) 
     const int64_t f = static_cast<int64_t>(rows) * 32 + 16 * half;
     return f < a.F ? f : 0;
   };
+  if (warp == kWarps) {
+    int done = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x, ++done) {
+      const Unit here = unit_of(table, u, tiles);
+      const int first = table.first[here.entry], count = table.first[here.entry + 1] - first;
+      const int64_t expert = table.expert[here.entry];
+      if (!mbar_wait(full, done & 1, a.limit_ns, abort, a.status)) return;
+      // eight columns at a time: inner values 8 m + g of columns 2 t and 2 t + 1
+      for (int n = 0; 8 * n < count; ++n) {
+        const int64_t f0 = static_cast<int64_t>(here.rows) * 32;
+        int64_t slots[2];
+        float power[2] = {1.f, 1.f};
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int col = 8 * n + 2 * t + c;
+          slots[c] = col < count ? table.slot[first + col] : -1;
+          if (!F::kBf16 && slots[c] >= 0) power[c] = a.x_power[slots[c] / a.k];
+        }
+        float v[2][4], amax[2] = {0.f, 0.f};
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < kGroups; ++w) {
+            const float4 q = sums[((m * NT + n) * kGroups + w) * 32 + lane];
+            s.x += q.x, s.y += q.y, s.z += q.z, s.w += q.w;
+          }
+          const int64_t f = f0 + 8 * m + g;
+          if constexpr (FORM == BSMMA_OPERAND_INT8) {
+            const float* of = static_cast<const float*>(a.s_in) + expert * 2 * a.F;
+            const float sg = f < a.F ? of[f] : 0.f, su = f < a.F ? of[a.F + f] : 0.f;
+            s.x *= sg, s.y *= sg, s.z *= su, s.w *= su;
+          }
+          v[0][m] = activate(s.x * power[0], a.act) * (s.z * power[0]);
+          v[1][m] = activate(s.y * power[1], a.act) * (s.w * power[1]);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            if (f < a.F && fabsf(v[c][m]) <= FLT_MAX) amax[c] = fmaxf(amax[c], fabsf(v[c][m]));
+        }
+        float inv[2] = {1.f, 1.f};
+        if constexpr (!F::kBf16) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) amax[c] = fmaxf(amax[c], __shfl_xor_sync(kFull, amax[c], o));
+            const float p = group_power(amax[c]);
+            inv[c] = 1.f / p;
+            if (g == 0 && slots[c] >= 0) a.inner_power[slots[c] * tiles + here.rows] = p;
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const int64_t f = f0 + 8 * m + g;
+          if (f >= a.F) continue;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if (slots[c] < 0) continue;
+            uint16_t* to = a.inner + slots[c] * a.F + f;
+            if constexpr (F::kBf16) *to = __bfloat16_as_ushort(__float2bfloat16_rn(v[c][m]));
+            else *to = __half_as_ushort(__float2half_rn(v[c][m] * inv[c]));
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty);
+    }
+    return;
+  }
   // the loads run ahead of the products through the block's units
   int lu = blockIdx.x, li = 0, slot = 0;
   Source src = {};
@@ -551,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_in_kernel(const StepArgs a) 
   };
   auto load = [&] {
     if (mine && lu < units) {
-      load_stage<FORM>(ring + slot * C::kStage, src, sets, group + li * kGroups, bytes, blocks, words);
+      load_stage<FORM>(ring + slot * C::kStage, src, sets, group + li * kGroups, bytes, words);
       if (++li == mine) {
         li = 0;
         lu += gridDim.x;
@@ -565,8 +615,8 @@ __global__ void __launch_bounds__(kThreads, 1) step_in_kernel(const StepArgs a) 
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i) load();
 
-  int at = 0;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+  int at = 0, done = 0;
+  for (int u = blockIdx.x; u < units; u += gridDim.x, ++done) {
     const Unit here = unit_of(table, u, tiles);
     const int first = table.first[here.entry], count = table.first[here.entry + 1] - first;
     const int64_t expert = table.expert[here.entry], f_first = first_row(here.rows);
@@ -585,80 +635,28 @@ __global__ void __launch_bounds__(kThreads, 1) step_in_kernel(const StepArgs a) 
       for (int i = 0; i < mine; ++i) {
         stage_products<FORM, N, false, C::kStages - 2>(
             acc, x, no_powers, K - k - 8 * t, ring + at * C::kStage, load,
-            [&](int r, int b) -> uint32_t { return scales[set_row(f_first, r) * blocks + k / 32 + b]; }, words);
+            [&](int r, int b) -> uint32_t { return scales[set_row(f_first, r) * blocks + k / 32 + b]; }, words,
+            (group + i * kGroups) & 1);
         k += kGroups * F::kStageK;
 #pragma unroll
         for (int n = 0; n < N; ++n) x[n] += kGroups * F::kStageK;
         at = at + 1 == C::kStages ? 0 : at + 1;
       }
-      __syncthreads();   // the sums of the unit before have been read
+      // the sums of the unit before have been read
+      if (done > 0 && !mbar_wait(empty, (done - 1) & 1, a.limit_ns, abort, a.status)) return false;
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int n = 0; n < N; ++n)
           sums[(((2 * half + m) * NT + n) * kGroups + group) * 32 + lane] =
               make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full);
+      return true;
     };
-    if (NT == 1 || count <= 8) products(std::integral_constant<int, 1>{});
-    else products(std::integral_constant<int, NT>{});
-    __syncthreads();
-    // a warp eight columns: inner values 8 m + g of columns 2 t and 2 t + 1
-    if (8 * warp < count) {
-      const int n = warp;
-      const int64_t f0 = static_cast<int64_t>(here.rows) * 32;
-      int64_t slots[2];
-      float power[2] = {1.f, 1.f};
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int col = 8 * n + 2 * t + c;
-        slots[c] = col < count ? table.slot[first + col] : -1;
-        if (!F::kBf16 && slots[c] >= 0) power[c] = a.x_power[slots[c] / a.k];
-      }
-      float v[2][4], amax[2] = {0.f, 0.f};
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kGroups; ++w) {
-          const float4 q = sums[((m * NT + n) * kGroups + w) * 32 + lane];
-          s.x += q.x, s.y += q.y, s.z += q.z, s.w += q.w;
-        }
-        const int64_t f = f0 + 8 * m + g;
-        if constexpr (FORM == BSMMA_OPERAND_INT8) {
-          const float* of = static_cast<const float*>(a.s_in) + expert * 2 * a.F;
-          const float sg = f < a.F ? of[f] : 0.f, su = f < a.F ? of[a.F + f] : 0.f;
-          s.x *= sg, s.y *= sg, s.z *= su, s.w *= su;
-        }
-        v[0][m] = activate(s.x * power[0], a.act) * (s.z * power[0]);
-        v[1][m] = activate(s.y * power[1], a.act) * (s.w * power[1]);
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          if (f < a.F && fabsf(v[c][m]) <= FLT_MAX) amax[c] = fmaxf(amax[c], fabsf(v[c][m]));
-      }
-      float inv[2] = {1.f, 1.f};
-      if constexpr (!F::kBf16) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) amax[c] = fmaxf(amax[c], __shfl_xor_sync(kFull, amax[c], o));
-          const float p = group_power(amax[c]);
-          inv[c] = 1.f / p;
-          if (g == 0 && slots[c] >= 0) a.inner_power[slots[c] * tiles + here.rows] = p;
-        }
-      }
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const int64_t f = f0 + 8 * m + g;
-        if (f >= a.F) continue;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (slots[c] < 0) continue;
-          uint16_t* to = a.inner + slots[c] * a.F + f;
-          if constexpr (F::kBf16) *to = __bfloat16_as_ushort(__float2bfloat16_rn(v[c][m]));
-          else *to = __half_as_ushort(__float2half_rn(v[c][m] * inv[c]));
-        }
-      }
-    }
+    if (!(NT == 1 || count <= 8 ? products(std::integral_constant<int, 1>{})
+                                : products(std::integral_constant<int, NT>{})))
+      break;
   }
   cp_async_wait_all();
 }
@@ -726,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_out_kernel(const StepArgs a,
   if (i1 > i0 && lu < units) rows_of();
   auto load = [&] {
     if (i1 > i0 && lu < units) {
-      load_stage<FORM>(ring + slot * C::kStage, src, sets, ls, bytes, blocks, words);
+      load_stage<FORM>(ring + slot * C::kStage, src, sets, ls, bytes, words);
       bool moved = false;
       if (++ls == stages) ls = 0, ++le, moved = true;
       if (--left == 0) {
@@ -769,7 +767,8 @@ __global__ void __launch_bounds__(kThreads, 1) step_out_kernel(const StepArgs a,
         for (int i = 0; i < n_here; ++i) {
           stage_products<FORM, N, kPowers, C::kStages - 2>(
               acc, x, powers, K - k - 8 * t, ring + at * C::kStage, load,
-              [&](int r, int b) -> uint32_t { return scales[set_row(row0, r) * blocks + k / 32 + b]; }, words);
+              [&](int r, int b) -> uint32_t { return scales[set_row(row0, r) * blocks + k / 32 + b]; }, words,
+              (stage + i) & 1);
           k += F::kStageK;
 #pragma unroll
           for (int n = 0; n < N; ++n) {
@@ -887,7 +886,9 @@ bsmma_status launch_out(const StepArgs& a, const DeviceInfo* dev, cudaStream_t s
 }
 
 template <int FORM, int NT>
-bsmma_status launch_step(const StepArgs& a, const DeviceInfo* dev, cudaStream_t stream) {
+bsmma_status launch_step(StepArgs a, const DeviceInfo* dev, cudaStream_t stream) {
+  a.limit_ns = wait_limit_ns();
+  a.status = dev->status;
   static PerDevice in_set;
   constexpr int kIn = InCfg<FORM, NT>::kBytes;
   bsmma_status st = in_set.allow_smem(dev->device, step_in_kernel<FORM, NT>, kIn);
@@ -895,10 +896,10 @@ bsmma_status launch_step(const StepArgs& a, const DeviceInfo* dev, cudaStream_t 
   const int64_t slots = a.T * a.k;   // at most this many entries
   const int64_t in_units = slots * ((a.F + 31) / 32);
   const unsigned in_blocks = static_cast<unsigned>(std::min<int64_t>(in_units, dev->sm_count));
-  cudaError_t e = launch_dependent(step_order_kernel, dim3(Form<FORM>::kBf16 ? 1 : 1 + static_cast<unsigned>(a.T)),
+  cudaError_t e = launch_dependent(step_order_kernel, dim3(FORM == BSMMA_OPERAND_BF16 ? 1 : 1 + static_cast<unsigned>(a.T)),
                                    dim3(kThreads), 0, stream, a, 8 * NT);
   if (e == cudaSuccess)
-    e = launch_dependent(step_in_kernel<FORM, NT>, dim3(in_blocks), dim3(kThreads), kIn, stream, a);
+    e = launch_dependent(step_in_kernel<FORM, NT>, dim3(in_blocks), dim3(kInThreads), kIn, stream, a);
   if (e != cudaSuccess) return BSMMA_ERR_CUDA;
   st = launch_out<FORM, NT>(a, dev, stream);
   count_launches(3);

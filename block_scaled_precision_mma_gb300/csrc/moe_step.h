@@ -16,6 +16,8 @@ struct StepArgs {
   const void *w_in, *s_in, *w_out, *s_out;
   int act;
   __nv_bfloat16* out;            // [T][H]
+  uint64_t limit_ns;             // of a wait on the device, and where one that ran out is latched
+  int* status;
   // in the workspace
   void* table;                   // who takes what
   float* x_power;                // [T], and the tokens in FP16 over it
