@@ -63,7 +63,7 @@ struct Form {
   }
 };
 template <int FORM>
-__device__ __forceinline__ int64_t row_bytes(int64_t K) {
+__device__ __forceinline__ int row_bytes(int K) {   // (at most 2^17)
   return FORM == BSMMA_OPERAND_BF16 ? 2 * K : FORM == BSMMA_OPERAND_E2M1 ? K / 2 : K;
 }
 
@@ -311,10 +311,10 @@ struct Sets {
 // chunk t of its row in each set, lane l the word that has the scales of row l.
 template <int FORM>
 __device__ __forceinline__ void load_stage(uint32_t to, const Source& from, const Sets& sets, int stage,
-                                           int64_t bytes, bool words) {
+                                           int bytes, bool words) {
   using F = Form<FORM>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int64_t at = static_cast<int64_t>(stage) * kRowStage;
+  const int at = stage * kRowStage;
   const uint32_t d = to + F::place(g, 16 * t);
   const uint8_t* src = from.row + at;
   if (at + kRowStage <= bytes) {
@@ -328,7 +328,7 @@ __device__ __forceinline__ void load_stage(uint32_t to, const Source& from, cons
   // (a word is four blocks' scales: of two stages where a stage has two)
   if constexpr (F::kMx)
     if (words)
-      cp_async_4(to + kCodeStage + 4 * lane, from.scales + (static_cast<int64_t>(stage) * F::kBlocks & ~3));
+      cp_async_4(to + kCodeStage + 4 * lane, from.scales + (stage * F::kBlocks & ~3));
 }
 
 // What the columns bring to a stage: the lane's eight values of each block, and the powers of two
@@ -339,22 +339,24 @@ struct Columns {
   uint4 x[Form<FORM>::kBlocks][NT];
   float p[POWERS ? Form<FORM>::kBlocks : 1][NT][2];
 };
-// x: the lane's column (of each eight) from its first K of the stage on; left: K from there to the
-// end; powers: of the stage's blocks.
+// x: where the lane's column (of each eight) has its first K of the stage, in bytes behind x0; left: K
+// from there to the end; powers: where the stage's first blocks' are, in bytes behind p0.
 template <int FORM, int NT, bool POWERS>
-__device__ __forceinline__ void load_columns(Columns<FORM, NT, POWERS>& c, const uint16_t* const (&x)[NT],
-                                             int64_t left, const float* const (&powers)[NT][2]) {
+__device__ __forceinline__ void load_columns(Columns<FORM, NT, POWERS>& c, const uint8_t* x0, const uint32_t (&x)[NT],
+                                             int left, const uint8_t* p0, const uint32_t (&powers)[NT][2]) {
   constexpr int kBlocks = Form<FORM>::kBlocks;
   const int t = threadIdx.x & 3;
+  auto x_of = [&](int n, int j) { return *reinterpret_cast<const uint4*>(x0 + x[n] + 64 * j); };
+  auto p_of = [&](int n, int c, int j) { return *reinterpret_cast<const float*>(p0 + powers[n][c] + 4 * j); };
   if (left + 8 * t >= 32 * kBlocks) {   // (uniform)
 #pragma unroll
     for (int j = 0; j < kBlocks; ++j)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        c.x[j][n] = *reinterpret_cast<const uint4*>(x[n] + 32 * j);
+        c.x[j][n] = x_of(n, j);
         if constexpr (POWERS) {
-          c.p[j][n][0] = powers[n][0][j];
-          c.p[j][n][1] = powers[n][1][j];
+          c.p[j][n][0] = p_of(n, 0, j);
+          c.p[j][n][1] = p_of(n, 1, j);
         }
       }
   } else {
@@ -363,11 +365,11 @@ __device__ __forceinline__ void load_columns(Columns<FORM, NT, POWERS>& c, const
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         c.x[j][n] = make_uint4(0, 0, 0, 0);
-        if (32 * j < left) c.x[j][n] = *reinterpret_cast<const uint4*>(x[n] + 32 * j);
+        if (32 * j < left) c.x[j][n] = x_of(n, j);
         if constexpr (POWERS) {
           const bool in = 32 * j < left + 8 * t;
-          c.p[j][n][0] = in ? powers[n][0][j] : 0.f;
-          c.p[j][n][1] = in ? powers[n][1][j] : 0.f;
+          c.p[j][n][0] = in ? p_of(n, 0, j) : 0.f;
+          c.p[j][n][1] = in ? p_of(n, 1, j) : 0.f;
         }
       }
   }
@@ -379,13 +381,13 @@ __device__ __forceinline__ void load_columns(Columns<FORM, NT, POWERS>& c, const
 // scale(r, b): where the scales cannot be copied by words, block b's of the lane's row of set r (asked
 // for inside K only).
 template <int FORM, int NT, bool POWERS, int PENDING, typename Load, typename Scale>
-__device__ __forceinline__ void stage_products(float (&acc)[2][NT][4], const uint16_t* const (&x)[NT],
-                                               const float* const (&powers)[NT][2], int64_t left, uint32_t ring,
-                                               const Load& load, const Scale& scale, bool words, bool odd) {
+__device__ __forceinline__ void stage_products(float (&acc)[2][NT][4], const uint8_t* x0, const uint32_t (&x)[NT],
+                                               const uint8_t* p0, const uint32_t (&powers)[NT][2], int left,
+                                               uint32_t ring, const Load& load, const Scale& scale, bool words, bool odd) {
   using F = Form<FORM>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   Columns<FORM, NT, POWERS> c;
-  load_columns<FORM, NT, POWERS>(c, x, left, powers);
+  load_columns<FORM, NT, POWERS>(c, x0, x, left, p0, powers);
   cp_async_wait<PENDING>();
   __syncwarp();   // the other lanes' copies, and their reads of the slot that is filled next
   load();
@@ -504,7 +506,8 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
   copy_table(table, *static_cast<const WeightedTable*>(a.table), static_cast<int>(a.T) * a.k);
   __syncthreads();
 
-  const int64_t K = a.H, bytes = row_bytes<FORM>(K), blocks = K / 32;
+  const int K = static_cast<int>(a.H), bytes = row_bytes<FORM>(K), blocks = K / 32;
+  const uint8_t* x0 = F::kBf16 ? static_cast<const uint8_t*>(a.x) : reinterpret_cast<const uint8_t*>(a.x16);
   const bool words = F::kMx && blocks % 4 == 0 && (reinterpret_cast<uintptr_t>(a.s_in) & 3) == 0;
   const int tiles = static_cast<int>((a.F + 31) / 32), units = table.entries * tiles;
   const int stages = static_cast<int>((K + F::kStageK - 1) / F::kStageK);
@@ -624,22 +627,21 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
     // n_cols tiles of eight columns; a column past the entry's repeats its last
     auto products = [&](auto n_cols) {
       constexpr int N = decltype(n_cols)::value;
-      const uint16_t* x[N];
-      const float* const no_powers[N][2] = {};
+      uint32_t x[N];
+      const uint32_t no_powers[N][2] = {};
+      int k = group * F::kStageK;
 #pragma unroll
       for (int n = 0; n < N; ++n)
-        x[n] = (F::kBf16 ? static_cast<const uint16_t*>(a.x) : a.x16) +
-               table.slot[first + min(8 * n + g, count - 1)] / a.k * a.H + group * F::kStageK + 8 * t;
-      int64_t k = group * F::kStageK;
+        x[n] = 2 * (table.slot[first + min(8 * n + g, count - 1)] / a.k * K + k + 8 * t);
       float acc[2][N][4] = {};
       for (int i = 0; i < mine; ++i) {
         stage_products<FORM, N, false, C::kStages - 2>(
-            acc, x, no_powers, K - k - 8 * t, ring + at * C::kStage, load,
+            acc, x0, x, x0, no_powers, K - k - 8 * t, ring + at * C::kStage, load,
             [&](int r, int b) -> uint32_t { return scales[set_row(f_first, r) * blocks + k / 32 + b]; }, words,
             (group + i * kGroups) & 1);
         k += kGroups * F::kStageK;
 #pragma unroll
-        for (int n = 0; n < N; ++n) x[n] += kGroups * F::kStageK;
+        for (int n = 0; n < N; ++n) x[n] += 2 * kGroups * F::kStageK;
         at = at + 1 == C::kStages ? 0 : at + 1;
       }
       // the sums of the unit before have been read
@@ -695,7 +697,9 @@ __global__ void __launch_bounds__(kThreads, 1) step_out_kernel(const StepArgs a,
   for (int i = threadIdx.x; i < T * a.k; i += kThreads) table.weight[i] = from.weight[i];
   __syncthreads();
 
-  const int64_t K = a.F, bytes = row_bytes<FORM>(K), blocks = K / 32, power_blocks = (K + 31) / 32;
+  const int K = static_cast<int>(a.F), bytes = row_bytes<FORM>(K), blocks = K / 32, power_blocks = (K + 31) / 32;
+  const uint8_t* x0 = reinterpret_cast<const uint8_t*>(a.inner);
+  const uint8_t* p0 = reinterpret_cast<const uint8_t*>(a.inner_power);
   const bool words = F::kMx && blocks % 4 == 0 && (reinterpret_cast<uintptr_t>(a.s_out) & 3) == 0;
   const int units = static_cast<int>((a.H + 31) / 32);
   const int stages = static_cast<int>((K + F::kStageK - 1) / F::kStageK);
@@ -753,28 +757,27 @@ __global__ void __launch_bounds__(kThreads, 1) step_out_kernel(const StepArgs a,
       const uint8_t* scales = static_cast<const uint8_t*>(a.s_out) + (base + g) * blocks;
       auto products = [&](auto n_cols) {
         constexpr int N = decltype(n_cols)::value;
-        int64_t k = static_cast<int64_t>(stage) * F::kStageK;
-        const uint16_t* x[N];
-        const float* powers[N][2];
+        int k = stage * F::kStageK;
+        uint32_t x[N], powers[N][2];   // (at most 2^27 bytes)
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-          x[n] = a.inner + table.slot[first + min(8 * n + g, count - 1)] * a.F + k + 8 * t;
+          x[n] = 2 * (table.slot[first + min(8 * n + g, count - 1)] * K + k + 8 * t);
 #pragma unroll
           for (int c = 0; c < 2; ++c)
-            powers[n][c] = a.inner_power + table.slot[first + min(8 * n + 2 * t + c, count - 1)] * power_blocks + k / 32;
+            powers[n][c] = 4 * (table.slot[first + min(8 * n + 2 * t + c, count - 1)] * power_blocks + k / 32);
         }
         float acc[2][N][4] = {};
         for (int i = 0; i < n_here; ++i) {
           stage_products<FORM, N, kPowers, C::kStages - 2>(
-              acc, x, powers, K - k - 8 * t, ring + at * C::kStage, load,
+              acc, x0, x, p0, powers, K - k - 8 * t, ring + at * C::kStage, load,
               [&](int r, int b) -> uint32_t { return scales[set_row(row0, r) * blocks + k / 32 + b]; }, words,
               (stage + i) & 1);
           k += F::kStageK;
 #pragma unroll
           for (int n = 0; n < N; ++n) {
-            x[n] += F::kStageK;
-            powers[n][0] += F::kBlocks;
-            powers[n][1] += F::kBlocks;
+            x[n] += 2 * F::kStageK;
+            powers[n][0] += 4 * F::kBlocks;
+            powers[n][1] += 4 * F::kBlocks;
           }
           at = at + 1 == C::kStages ? 0 : at + 1;
         }
