@@ -562,6 +562,12 @@ def grouped_int8_gemm(X, sX, W, sW, m_sizes, out=None, dtype=torch.bfloat16, str
     return out
 
 
+def _here(t):
+    """`t` is on the current device, whose stream and kernels a call uses."""
+    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError("expected a CUDA tensor on the current device")
+
+
 NORMS = {"none": 0, "rms": 1, "layer": 2}
 OPERANDS = {"bf16": 0, "f32": 1, "int8": 2, "e4m3": 3, "e5m2": 4, "e2m1": 5}
 _OPERAND_OF = {torch.bfloat16: "bf16", torch.float32: "f32"}
@@ -610,6 +616,7 @@ def branch_enter(x, weight=None, bias=None, norm="rms", eps=1e-6, fmt=None, out=
     if bias is not None:
         _expect(bias, torch.float32, (H,), "bias")
     out, scales = _operand(fmt, T, H, x, out, scales)
+    _here(x)
     _check(load().branch_enter(_ptr(x), dtype, T, H, NORMS[norm], eps, _ptr(weight), _ptr(bias),
                                OPERANDS[fmt], _ptr(out), _ptr(scales), _stream(stream)),
            "branch_enter")
@@ -624,11 +631,16 @@ def branch_enter_backward(dh, x, weight=None, norm="rms", eps=1e-6, dres=None, b
     T, H = x.shape
     h_dtype, x_dtype = _dtype_of(dh, "dh"), _dtype_of(x, "x")
     _expect(dh, dh.dtype, (T, H), "dh")
-    _expect(weight, torch.float32, (H,), "weight")
-    _expect(dres, x.dtype, (T, H), "dres")
+    if weight is not None:
+        _expect(weight, torch.float32, (H,), "weight")
+    if dres is not None:
+        _expect(dres, x.dtype, (T, H), "dres")
     dx = _output(dx, x.dtype, (T, H), x, "dx")
-    dweight = None if weight is None else torch.empty(H, dtype=torch.float32, device=x.device)
-    dbias = torch.empty(H, dtype=torch.float32, device=x.device) if bias else None
+    dweight = None if weight is None else torch.empty_like(weight)
+    dbias = None
+    if bias:
+        dbias = torch.empty(H, dtype=torch.float32, device=x.device) if weight is None else torch.empty_like(weight)
+    _here(x)
     _check(load().branch_enter_backward(_ptr(dh), h_dtype, _ptr(x), x_dtype, T, H, NORMS[norm], eps,
                                         _ptr(weight), _ptr(dres), _ptr(dx), _ptr(dweight), _ptr(dbias),
                                         _stream(stream)), "branch_enter_backward")
@@ -661,6 +673,7 @@ def branch_leave(x, y, weight=None, bias=None, norm="none", eps=1e-6, gate=None,
     fmt = fmt or _OPERAND_OF[y.dtype]
     if next_norm != "none":
         next_out, next_scales = _operand(fmt, T, H, x, next_out, next_scales)
+    _here(x)
     _check(load().branch_leave(_ptr(x), x_dtype, _ptr(y), y_dtype, T, H, NORMS[norm], eps, _ptr(weight),
                                _ptr(bias), _ptr(gate), gate_rows, x_scale, y_scale, p, _ptr(rng), _ptr(out),
                                NORMS[next_norm], next_eps, _ptr(next_weight), _ptr(next_bias),
@@ -681,15 +694,19 @@ def branch_leave_backward(dout, y, weight=None, bias=None, norm="none", eps=1e-6
     T, H = y.shape
     x_dtype, y_dtype = _dtype_of(dout, "dout"), _dtype_of(y, "y")
     _expect(dout, dout.dtype, (T, H), "dout")
-    _expect(weight, torch.float32, (H,), "weight")
-    _expect(bias, torch.float32, (H,), "bias")
+    if weight is not None:
+        _expect(weight, torch.float32, (H,), "weight")
+    if bias is not None:
+        _expect(bias, torch.float32, (H,), "bias")
     gate_rows = 1 if gate is None else _gate(gate, gate_rows, y)
     _rng(rng, p)
     dy = _output(dy, y.dtype, (T, H), y, "dy")
     if x_scale != 1 or dx is not None:
         dx = _output(dx, dout.dtype, (T, H), y, "dx")
-    new = lambda t: None if t is None else torch.empty(t.shape, dtype=torch.float32, device=y.device)  # noqa: E731
-    dweight, dbias, dgate = new(weight), new(bias), new(gate)
+    dweight = None if weight is None else torch.empty_like(weight)
+    dbias = None if bias is None else torch.empty_like(bias)
+    dgate = None if gate is None else torch.empty_like(gate, dtype=torch.float32)
+    _here(y)
     _check(load().branch_leave_backward(_ptr(dout), x_dtype, _ptr(y), y_dtype, T, H, NORMS[norm], eps,
                                         _ptr(weight), _ptr(bias), _ptr(gate), gate_rows, x_scale, y_scale,
                                         p, _ptr(rng), _ptr(dy), _ptr(dx), _ptr(dweight), _ptr(dbias),
@@ -728,6 +745,7 @@ def moe_step(x, ids, weights, w_in, w_out, s_in=None, s_out=None, fmt="bf16", ac
         _expect(s_in, torch.uint8, (E, 2 * F, H // 32), "s_in")
         _expect(s_out, torch.uint8, (E, H, F // 32), "s_out")
     out = _output(out, torch.bfloat16, (T, H), x, "out")
+    _here(x)
     _check(load().moe_step(_ptr(x), T, H, _ptr(ids), _ptr(weights), k, E, F, OPERANDS[fmt], _ptr(w_in),
                            _ptr(s_in), _ptr(w_out), _ptr(s_out), ACTIVATIONS[act], _ptr(out),
                            _stream(stream)), "moe_step")
@@ -745,6 +763,7 @@ def dropout(x, p, rng, out=None, stream=None):
     out may be x.  See ``dropout`` in bsmma.h."""
     _rng(rng, p)
     out = _output(out, x.dtype, x.shape, x, "out")
+    _here(x)
     _check(load().dropout(_ptr(x), _dtype_of(x, "x"), x.numel(), p, _ptr(rng), _ptr(out), _stream(stream)),
            "dropout")
     return out

@@ -91,7 +91,7 @@ def test_binding_refuses():
     """Types and shapes are checked before pointers are taken (CPU tensors suffice)."""
     x, w, h = torch.zeros(4, 64), torch.zeros(64), torch.zeros((4, 64), dtype=torch.bfloat16)
     rng = torch.zeros(2, dtype=torch.int64)
-    for call in (lambda: bs.branch_enter(x.double(), w),
+    calls = [lambda: bs.branch_enter(x.double(), w),
                  lambda: bs.branch_enter(x, w.bfloat16()),
                  lambda: bs.branch_enter(x, torch.zeros(32)),
                  lambda: bs.branch_enter(x, w, out=h),
@@ -108,6 +108,8 @@ def test_binding_refuses():
                  lambda: bs.dropout(x, 0.5, None),
                  lambda: bs.dropout(x, 0.5, torch.zeros(3, dtype=torch.int64)),
                  lambda: bs.dropout(x.half(), 0.5, rng),
-                 lambda: bs.branch_enter(x, w)):          # right types, not on a GPU
-        with pytest.raises(ValueError):
+                 lambda: bs.branch_enter(x, w)]          # the last: right types, not on a GPU
+    for call in calls:
+        with pytest.raises(ValueError) as e:
             call()
+        assert ("current device" in str(e.value)) == (call is calls[-1])

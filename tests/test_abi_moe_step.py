@@ -40,7 +40,7 @@ def test_binding_refuses():
     x, ids, w = torch.zeros(4, 64).bfloat16(), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
     w_in, w_out = torch.zeros(3, 64, 64).bfloat16(), torch.zeros(3, 64, 32).bfloat16()
     s_in, s_out = torch.zeros(3, 64), torch.zeros(3, 64)
-    for call in (lambda: bs.moe_step(x.float(), ids, w, w_in, w_out),
+    calls = [lambda: bs.moe_step(x.float(), ids, w, w_in, w_out),
                  lambda: bs.moe_step(x, ids.long(), w, w_in, w_out),
                  lambda: bs.moe_step(x, ids, w[:3], w_in, w_out),
                  lambda: bs.moe_step(x, ids, w, w_in[:2], w_out),
@@ -51,6 +51,8 @@ def test_binding_refuses():
                                      s_out=s_out, fmt="int8"),
                  lambda: bs.moe_step(x, ids, w, w_in.to(torch.uint8), w_out.to(torch.uint8), s_in=s_in,
                                      s_out=s_out, fmt="e4m3"),
-                 lambda: bs.moe_step(x, ids, w, w_in, w_out)):          # right types, not on a GPU
-        with pytest.raises(ValueError):
+                 lambda: bs.moe_step(x, ids, w, w_in, w_out)]          # the last: right types, not on a GPU
+    for call in calls:
+        with pytest.raises(ValueError) as e:
             call()
+        assert ("current device" in str(e.value)) == (call is calls[-1])
