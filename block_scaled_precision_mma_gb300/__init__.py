@@ -762,9 +762,10 @@ def dropout(x, p, rng, out=None, stream=None):
     ``rng`` int64 (seed, offset) on the device.  Its gradient is the same call on the output's.
     out may be x.  See ``dropout`` in bsmma.h."""
     _rng(rng, p)
+    dtype = _dtype_of(x, "x")
     out = _output(out, x.dtype, x.shape, x, "out")
     _here(x)
-    _check(load().dropout(_ptr(x), _dtype_of(x, "x"), x.numel(), p, _ptr(rng), _ptr(out), _stream(stream)),
+    _check(load().dropout(_ptr(x), dtype, x.numel(), p, _ptr(rng), _ptr(out), _stream(stream)),
            "dropout")
     return out
 
