@@ -41,7 +41,7 @@ namespace {
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kMaxSlots = 1024, kMaxExperts = 1024;
-constexpr int kTableBytes = 8 + kMaxSlots * 10;   // sizeof(WeightedTable)
+constexpr int kTableBytes = 8 + kMaxSlots * 12;   // sizeof(WeightedTable)
 
 // ------------------------------------------------------------------------- weights
 // A stage is 64 bytes of each of a warp's 32 rows: `kBlocks` blocks of 32 K, of which a row's four
@@ -162,6 +162,7 @@ struct Table {
   uint16_t expert[kMaxSlots];       // of each tile
   uint16_t first[kMaxSlots + 2];    // its first column; it ends where the next begins
   uint16_t slot[kMaxSlots];         // of each column: token * k + choice
+  uint16_t token[kMaxSlots];
 };
 struct WeightedTable : Table {
   float weight[kMaxSlots];          // of each column
@@ -233,6 +234,7 @@ __device__ __forceinline__ void build_table(WeightedTable& t, TableScratch& s, c
     for (int j = i + 1; j % a.k; ++j)
       if (s.ids[j] == id) w += a.weights[j];
     t.slot[c] = static_cast<uint16_t>(i);
+    t.token[c] = static_cast<uint16_t>(i / a.k);
     t.weight[c] = w;
   }
   __syncthreads();
@@ -292,6 +294,7 @@ __device__ __forceinline__ void copy_table(Table& to, const Table& from, int slo
     to.first[i] = from.first[i];
     if (i == slots) break;
     to.slot[i] = from.slot[i];
+    to.token[i] = from.token[i];
     to.expert[i] = from.expert[i];
   }
 }
@@ -354,11 +357,23 @@ __device__ __forceinline__ void load_columns(Columns<FORM, NT, POWERS>& c, const
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         c.x[j][n] = x_of(n, j);
-        if constexpr (POWERS) {
-          c.p[j][n][0] = p_of(n, 0, j);
-          c.p[j][n][1] = p_of(n, 1, j);
-        }
       }
+    if constexpr (POWERS) {   // (a slot's powers begin at a multiple of 16 bytes)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint8_t* from = p0 + powers[n][i];
+          if constexpr (kBlocks == 4) {
+            const float4 p = *reinterpret_cast<const float4*>(from);
+            c.p[0][n][i] = p.x, c.p[1][n][i] = p.y, c.p[2][n][i] = p.z, c.p[3][n][i] = p.w;
+          } else {
+            static_assert(kBlocks == 2, "powers go with codes");
+            const float2 p = *reinterpret_cast<const float2*>(from);
+            c.p[0][n][i] = p.x, c.p[1][n][i] = p.y;
+          }
+        }
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < kBlocks; ++j)
@@ -453,20 +468,39 @@ __device__ __forceinline__ float activate(float x, int act) {
   return act == BSMMA_ACT_SILU ? x / (1.f + expf(-x)) : x;
 }
 
-// Which expert, columns and rows a unit has: an expert's units are its tiles of rows, and
-// within one its tiles of columns, so that what several of those read is read at one time.
-struct Unit {
-  int entry, rows;
+// A block's walk over its units (every gridDim-th).  An expert's units are its tiles of rows, and
+// within one its tiles of columns, so that what several of those read is read at one time.  Kept as
+// a place in the expert's units: with few stages a unit its divisions would show.
+struct Walk {
+  int lead, tiles_c, at;   // the expert's first entry, its entries, the unit's number in the expert
+  __device__ __forceinline__ void find(const Table& t) {
+    int end = lead + 1;
+    while (end < t.entries && t.expert[end] == t.expert[lead]) ++end;
+    tiles_c = end - lead;
+  }
+  // step units further; false: past the last
+  __device__ __forceinline__ bool forward(const Table& t, int step, int tiles) {
+    at += step;
+    while (at >= tiles * tiles_c) {
+      at -= tiles * tiles_c;
+      lead += tiles_c;
+      if (lead >= t.entries) return false;
+      find(t);
+    }
+    return true;
+  }
+  __device__ __forceinline__ bool begin(const Table& t, int unit, int tiles) {
+    lead = tiles_c = at = 0;
+    if (t.entries == 0) return false;
+    find(t);
+    return forward(t, unit, tiles);
+  }
+  __device__ __forceinline__ int entry() const { return tiles_c == 1 ? lead : lead + at % tiles_c; }
+  __device__ __forceinline__ int rows() const { return tiles_c == 1 ? at : at / tiles_c; }
 };
-__device__ __forceinline__ Unit unit_of(const Table& table, int u, int tiles) {
-  int lead = u / tiles;
-  const int expert = table.expert[lead];
-  int end = lead + 1;
-  while (lead > 0 && table.expert[lead - 1] == expert) --lead;
-  while (end < table.entries && table.expert[end] == expert) ++end;
-  const int i = u - lead * tiles, c = end - lead;
-  return c == 1 ? Unit{lead, i} : Unit{lead + i % c, i / c};
-}
+
+// Powers of two of an inner row: one for 32 values, whole fours of them.
+__host__ __device__ constexpr int64_t power_stride(int64_t F) { return (F + 127) / 128 * 4; }
 
 // The inner rows.  Warp w has rows of half w & 1 (16 inner columns) and every eighth stage of K
 // from w >> 1 on; one more warp adds the sums up and finishes a unit while the others are at the next
@@ -509,7 +543,7 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
   const int K = static_cast<int>(a.H), bytes = row_bytes<FORM>(K), blocks = K / 32;
   const uint8_t* x0 = F::kBf16 ? static_cast<const uint8_t*>(a.x) : reinterpret_cast<const uint8_t*>(a.x16);
   const bool words = F::kMx && blocks % 4 == 0 && (reinterpret_cast<uintptr_t>(a.s_in) & 3) == 0;
-  const int tiles = static_cast<int>((a.F + 31) / 32), units = table.entries * tiles;
+  const int tiles = static_cast<int>((a.F + 31) / 32), step = static_cast<int>(gridDim.x);
   const int stages = static_cast<int>((K + F::kStageK - 1) / F::kStageK);
   const int mine = group < stages ? (stages - group + kGroups - 1) / kGroups : 0;   // of a unit
   const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStage;
@@ -522,21 +556,22 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
   };
   if (warp == kWarps) {
     int done = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++done) {
-      const Unit here = unit_of(table, u, tiles);
-      const int first = table.first[here.entry], count = table.first[here.entry + 1] - first;
-      const int64_t expert = table.expert[here.entry];
+    Walk here;
+    for (bool more = here.begin(table, blockIdx.x, tiles); more; more = here.forward(table, step, tiles), ++done) {
+      const int entry = here.entry(), rows = here.rows();
+      const int first = table.first[entry], count = table.first[entry + 1] - first;
+      const int64_t expert = table.expert[entry];
       if (!mbar_wait(full, done & 1, a.limit_ns, abort, a.status)) return;
       // eight columns at a time: inner values 8 m + g of columns 2 t and 2 t + 1
       for (int n = 0; 8 * n < count; ++n) {
-        const int64_t f0 = static_cast<int64_t>(here.rows) * 32;
+        const int64_t f0 = static_cast<int64_t>(rows) * 32;
         int64_t slots[2];
         float power[2] = {1.f, 1.f};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int col = 8 * n + 2 * t + c;
           slots[c] = col < count ? table.slot[first + col] : -1;
-          if (!F::kBf16 && slots[c] >= 0) power[c] = a.x_power[slots[c] / a.k];
+          if (!F::kBf16 && slots[c] >= 0) power[c] = a.x_power[table.token[first + col]];
         }
         float v[2][4], amax[2] = {0.f, 0.f};
 #pragma unroll
@@ -567,7 +602,7 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
             for (int o = 4; o < 32; o <<= 1) amax[c] = fmaxf(amax[c], __shfl_xor_sync(kFull, amax[c], o));
             const float p = group_power(amax[c]);
             inv[c] = 1.f / p;
-            if (g == 0 && slots[c] >= 0) a.inner_power[slots[c] * tiles + here.rows] = p;
+            if (g == 0 && slots[c] >= 0) a.inner_power[slots[c] * power_stride(a.F) + rows] = p;
           }
         }
 #pragma unroll
@@ -589,13 +624,14 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
     return;
   }
   // the loads run ahead of the products through the block's units
-  int lu = blockIdx.x, li = 0, slot = 0;
+  Walk ahead;
+  bool to_load = ahead.begin(table, blockIdx.x, tiles) && mine;
+  int li = 0, slot = 0;
   Source src = {};
   Sets sets = {};
   auto enter_unit = [&] {
-    if (lu >= units) return;
-    const Unit w = unit_of(table, lu, tiles);
-    const int64_t f = first_row(w.rows), base = static_cast<int64_t>(table.expert[w.entry]) * 2 * a.F + f;
+    const int64_t f = first_row(ahead.rows());
+    const int64_t base = static_cast<int64_t>(table.expert[ahead.lead]) * 2 * a.F + f;
     src.row = static_cast<const uint8_t*>(a.w_in) + (base + g) * bytes + 16 * t;
 #pragma unroll
     for (int r = 0; r < 4; ++r) sets.bytes[r] = set_row(f, r) * bytes;
@@ -603,26 +639,26 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
       src.scales = static_cast<const uint8_t*>(a.s_in) + (base + set_row(f, lane >> 3) + (lane & 7)) * blocks;
   };
   auto load = [&] {
-    if (mine && lu < units) {
+    if (to_load) {
       load_stage<FORM>(ring + slot * C::kStage, src, sets, group + li * kGroups, bytes, words);
       if (++li == mine) {
         li = 0;
-        lu += gridDim.x;
-        enter_unit();
+        to_load = ahead.forward(table, step, tiles);
+        if (to_load) enter_unit();
       }
     }
     cp_async_commit();
     slot = slot + 1 == C::kStages ? 0 : slot + 1;
   };
-  enter_unit();
+  if (to_load) enter_unit();
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i) load();
 
   int at = 0, done = 0;
-  for (int u = blockIdx.x; u < units; u += gridDim.x, ++done) {
-    const Unit here = unit_of(table, u, tiles);
-    const int first = table.first[here.entry], count = table.first[here.entry + 1] - first;
-    const int64_t expert = table.expert[here.entry], f_first = first_row(here.rows);
+  Walk here;
+  for (bool more = here.begin(table, blockIdx.x, tiles); more; more = here.forward(table, step, tiles), ++done) {
+    const int entry = here.entry(), first = table.first[entry], count = table.first[entry + 1] - first;
+    const int64_t expert = table.expert[entry], f_first = first_row(here.rows());
     const uint8_t* scales = static_cast<const uint8_t*>(a.s_in) + (expert * 2 * a.F + f_first + g) * blocks;
     // n_cols tiles of eight columns; a column past the entry's repeats its last
     auto products = [&](auto n_cols) {
@@ -632,7 +668,7 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
       int k = group * F::kStageK;
 #pragma unroll
       for (int n = 0; n < N; ++n)
-        x[n] = 2 * (table.slot[first + min(8 * n + g, count - 1)] / a.k * K + k + 8 * t);
+        x[n] = 2 * (table.token[first + min(8 * n + g, count - 1)] * K + k + 8 * t);
       float acc[2][N][4] = {};
       for (int i = 0; i < mine; ++i) {
         stage_products<FORM, N, false, C::kStages - 2>(
@@ -697,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_out_kernel(const StepArgs a,
   for (int i = threadIdx.x; i < T * a.k; i += kThreads) table.weight[i] = from.weight[i];
   __syncthreads();
 
-  const int K = static_cast<int>(a.F), bytes = row_bytes<FORM>(K), blocks = K / 32, power_blocks = (K + 31) / 32;
+  const int K = static_cast<int>(a.F), bytes = row_bytes<FORM>(K), blocks = K / 32, powers_at = static_cast<int>(power_stride(K));
   const uint8_t* x0 = reinterpret_cast<const uint8_t*>(a.inner);
   const uint8_t* p0 = reinterpret_cast<const uint8_t*>(a.inner_power);
   const bool words = F::kMx && blocks % 4 == 0 && (reinterpret_cast<uintptr_t>(a.s_out) & 3) == 0;
@@ -764,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_out_kernel(const StepArgs a,
           x[n] = 2 * (table.slot[first + min(8 * n + g, count - 1)] * K + k + 8 * t);
 #pragma unroll
           for (int c = 0; c < 2; ++c)
-            powers[n][c] = 4 * (table.slot[first + min(8 * n + 2 * t + c, count - 1)] * power_blocks + k / 32);
+            powers[n][c] = 4 * (table.slot[first + min(8 * n + 2 * t + c, count - 1)] * powers_at + k / 32);
         }
         float acc[2][N][4] = {};
         for (int i = 0; i < n_here; ++i) {
@@ -801,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_out_kernel(const StepArgs a,
             const int col = 8 * n + 2 * t + c;
             if (col < count) {
               const float w = table.weight[first + col];
-              float* to = own + table.slot[first + col] / a.k * 32 + g;
+              float* to = own + table.token[first + col] * 32 + g;
 #pragma unroll
               for (int r = 0; r < 4; ++r) to[8 * r] = fmaf(w, acc[r >> 1][n][2 * (r & 1) + c], to[8 * r]);
             }
@@ -920,7 +956,7 @@ constexpr int64_t round_up(int64_t n) { return (n + 255) / 256 * 256; }
 }  // namespace
 
 int64_t step_workspace_bytes(int64_t T, int k, int64_t H, int64_t F) {
-  return round_up(kTableBytes) + round_up(T * 4) + round_up(T * H * 2) + round_up(T * k * ((F + 31) / 32) * 4) +
+  return round_up(kTableBytes) + round_up(T * 4) + round_up(T * H * 2) + round_up(T * k * power_stride(F) * 4) +
          round_up(T * k * F * 2);
 }
 
@@ -937,7 +973,7 @@ bsmma_status launch_moe_step(StepArgs a, int form, void* workspace, cudaStream_t
   a.table = take(kTableBytes);
   a.x_power = reinterpret_cast<float*>(take(a.T * 4));
   a.x16 = reinterpret_cast<uint16_t*>(take(a.T * a.H * 2));
-  a.inner_power = reinterpret_cast<float*>(take(a.T * a.k * ((a.F + 31) / 32) * 4));
+  a.inner_power = reinterpret_cast<float*>(take(a.T * a.k * power_stride(a.F) * 4));
   a.inner = reinterpret_cast<uint16_t*>(take(a.T * a.k * a.F * 2));
   switch (form) {
     case BSMMA_OPERAND_BF16: return launch_step_form<BSMMA_OPERAND_BF16>(a, dev, stream);

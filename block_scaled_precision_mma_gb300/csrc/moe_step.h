@@ -22,7 +22,7 @@ struct StepArgs {
   void* table;                   // who takes what
   float* x_power;                // [T], and the tokens in FP16 over it
   uint16_t* x16;                 // [T][H]
-  float* inner_power;            // [T * k][ceil(F / 32)], and the inner rows in FP16 over it, or
+  float* inner_power;            // [T * k][F / 32, in fours], and the inner rows in FP16 over it, or
   uint16_t* inner;               // [T * k][F]             in BF16
 };
 
