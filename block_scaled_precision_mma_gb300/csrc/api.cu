@@ -942,7 +942,7 @@ bsmma_status moe_step(const void* x, int64_t T, int64_t H, const int32_t* ids, c
   if (T == 0) return BSMMA_OK;
   if (!x || !ids || !weights || !w_in || !w_out || !out) return BSMMA_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(w_in) || !aligned16(w_out) || !aligned16(out) || !aligned_to(ids, 4) ||
-      !aligned_to(weights, 4) || (form == BSMMA_OPERAND_INT8 && (!aligned_to(s_in, 4) || !aligned_to(s_out, 4))))
+      !aligned_to(weights, 4) || !aligned_to(s_in, 4) || !aligned_to(s_out, 4))
     return BSMMA_ERR_MISALIGNED;
   StepArgs a = {};
   a.x = x;

@@ -55,7 +55,7 @@ struct Form {
   static constexpr int kLaneBytes = kBf16 ? 16 : FORM == BSMMA_OPERAND_E2M1 ? 4 : 8;
   static constexpr int kBlockBytes = 4 * kLaneBytes, kBlocks = kRowStage / kBlockBytes;
   static constexpr int kStageK = 32 * kBlocks;
-  static constexpr int kStage = kCodeStage + (kMx ? 32 * 4 : 0);   // a warp's: codes, then a word of scales a row
+  static constexpr int kStage = kCodeStage + (kMx ? 32 * 8 : 0);   // a warp's: codes, then two words of scales a row
   // Block b of row g (of a set of eight) lies at the place of block b ^ (g / 2) of the row, so that
   // the lanes of one shared-memory access are in different banks (rows two apart share them).
   static __device__ __forceinline__ uint32_t place(int g, int byte) {
@@ -143,8 +143,9 @@ __device__ __forceinline__ void cp_async_16(uint32_t dst_smem, const void* src, 
 __device__ __forceinline__ void cp_async_16(uint32_t dst_smem, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async_4(uint32_t dst_smem, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst_smem), "l"(src) : "memory");
+// (bytes < 4: the rest is zero; the address is a word's)
+__device__ __forceinline__ void cp_async_4(uint32_t dst_smem, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst_smem), "l"(src), "r"(bytes) : "memory");
 }
 
 // A value's power of two and FP16 form: the largest finite magnitude of a group of values goes to
@@ -306,15 +307,21 @@ struct Source {
   const uint8_t* row;       // the lane's row of the first set (lane (g, t): row g), its chunk t
   const uint8_t* scales;    // the scales of row lane (of 32)
 };
+// A stage's scales are copied as the word that holds its first one and, where rows do not have whole
+// words of them, the next word; never from behind `end`, the last scale of the matrix.
+struct Scales {
+  const uint8_t* end;
+  bool whole;               // a stage's scales lie in one word
+};
 struct Sets {
   int64_t bytes[4];         // of codes
 };
 
 // Starts the copies of stage `stage` (from the row's first byte): lane (g, t) copies the 16-byte
-// chunk t of its row in each set, lane l the word that has the scales of row l.
+// chunk t of its row in each set, lane l the word or words that have the scales of row l.
 template <int FORM>
 __device__ __forceinline__ void load_stage(uint32_t to, const Source& from, const Sets& sets, int stage,
-                                           int bytes, bool words) {
+                                           int bytes, const Scales& all) {
   using F = Form<FORM>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int at = stage * kRowStage;
@@ -328,10 +335,21 @@ __device__ __forceinline__ void load_stage(uint32_t to, const Source& from, cons
 #pragma unroll
     for (int r = 0; r < 4; ++r) cp_async_16(d + r * kSetStage, in ? src + sets.bytes[r] : from.row, in);
   }
-  // (a word is four blocks' scales: of two stages where a stage has two)
-  if constexpr (F::kMx)
-    if (words)
-      cp_async_4(to + kCodeStage + 4 * lane, from.scales + (stage * F::kBlocks & ~3));
+  if constexpr (F::kMx) {
+    const uint8_t* first = from.scales + stage * F::kBlocks;
+    const uint8_t* word = first - (reinterpret_cast<uintptr_t>(first) & 3);
+    const uint32_t d_scales = to + kCodeStage + 8 * lane;
+    if (all.whole) {
+      cp_async_4(d_scales, word, 4);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t here = all.end - (word + 4 * i);
+        cp_async_4(d_scales + 4 * i, here > 0 ? word + 4 * i : word,
+                   here >= 4 ? 4 : here > 0 ? static_cast<int>(here) : 0);
+      }
+    }
+  }
 }
 
 // What the columns bring to a stage: the lane's eight values of each block, and the powers of two
@@ -392,13 +410,13 @@ __device__ __forceinline__ void load_columns(Columns<FORM, NT, POWERS>& c, const
 
 // A stage of the ring: the columns' values asked for, the wait for the weights, the next stage's
 // load, and the products into acc: operand m has set 2 m in its upper and set 2 m + 1 in its lower
-// eight rows.  odd: the stage's scales are the upper half of their word (two blocks a stage);
-// scale(r, b): where the scales cannot be copied by words, block b's of the lane's row of set r (asked
-// for inside K only).
-template <int FORM, int NT, bool POWERS, int PENDING, typename Load, typename Scale>
+// eight rows.  scale_at: the address of the stage's first scale of the lane's row of the first set,
+// of which only the place in its word matters, and set_blocks[r] that of set r behind it.
+template <int FORM, int NT, bool POWERS, int PENDING, typename Load>
 __device__ __forceinline__ void stage_products(float (&acc)[2][NT][4], const uint8_t* x0, const uint32_t (&x)[NT],
                                                const uint8_t* p0, const uint32_t (&powers)[NT][2], int left,
-                                               uint32_t ring, const Load& load, const Scale& scale, bool words, bool odd) {
+                                               uint32_t ring, const Load& load, uint32_t scale_at,
+                                               const uint32_t (&set_blocks)[4], const Scales& all) {
   using F = Form<FORM>;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   Columns<FORM, NT, POWERS> c;
@@ -410,13 +428,15 @@ __device__ __forceinline__ void stage_products(float (&acc)[2][NT][4], const uin
   if constexpr (F::kMx) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      uint32_t codes = 0;
-      if (words) {
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(codes) : "r"(ring + kCodeStage + 4 * (r * 8 + g)));
-        if (F::kBlocks == 2 && odd) codes >>= 16;
+      uint32_t codes;
+      const uint32_t from = ring + kCodeStage + 8 * (r * 8 + g);
+      if (all.whole) {
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(codes) : "r"(from));
+        if (F::kBlocks == 2) codes >>= 8 * (scale_at & 2);
       } else {
-        for (int j = 0; j < F::kBlocks; ++j)
-          if (32 * j < left + 8 * t) codes |= scale(r, j) << (8 * j);
+        uint32_t more;
+        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(codes), "=r"(more) : "r"(from));
+        codes = __funnelshift_r(codes, more, 8 * ((scale_at + set_blocks[r]) & 3));
       }
 #pragma unroll
       for (int j = 0; j < F::kBlocks / 2; ++j) sw[r][j] = e8m0x2(codes >> (16 * j));
@@ -502,12 +522,14 @@ struct Walk {
 // Powers of two of an inner row: one for 32 values, whole fours of them.
 __host__ __device__ constexpr int64_t power_stride(int64_t F) { return (F + 127) / 128 * 4; }
 
-// The inner rows.  Warp w has rows of half w & 1 (16 inner columns) and every eighth stage of K
-// from w >> 1 on; one more warp adds the sums up and finishes a unit while the others are at the next
-// (done by one of theirs, the other fifteen waited for it a quarter of their time).
-constexpr int kGroups = kWarps / 2, kInThreads = kThreads + 32;
-template <int FORM, int NT>
+// The inner rows.  A unit is 16 inner columns for each of kWarps / G parts; warp w has part w % (16 / G)
+// and every G-th stage of K from w / (16 / G) on.  One more warp adds the sums up and finishes a unit
+// while the others are at the next (done by one of theirs, the other fifteen waited for it a quarter
+// of their time).
+constexpr int kInThreads = kThreads + 32;
+template <int FORM, int NT, int G>
 struct InCfg {
+  static constexpr int kParts = kWarps / G, kTile = 16 * kParts;   // a unit's parts and inner columns
   static constexpr int kStage = Form<FORM>::kStage;
   static constexpr int kSums = kWarps * 2 * NT * 512;
   static constexpr int kFixed = kSums + static_cast<int>(sizeof(Table)) + 32;
@@ -517,12 +539,12 @@ struct InCfg {
   static_assert(kStages >= 2, "one stage in flight");
 };
 
-template <int FORM, int NT>
+template <int FORM, int NT, int G>
 __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a) {
-  using C = InCfg<FORM, NT>;
+  using C = InCfg<FORM, NT, G>;
   using F = Form<FORM>;
   extern __shared__ __align__(128) uint8_t smem[];
-  float4* sums = reinterpret_cast<float4*>(smem + C::kRing);   // [operand of 4][NT][group][lane]
+  float4* sums = reinterpret_cast<float4*>(smem + C::kRing);   // [operand: two a part][NT][group][lane]
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kRing + C::kSums);   // the sums are there
   uint64_t* empty = full + 1;                                                 // ... have been read
   volatile int* abort = reinterpret_cast<volatile int*>(full + 2);
@@ -534,7 +556,7 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
     *abort = 0;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int half = warp & 1, group = warp >> 1;
+  const int part = warp % C::kParts, group = warp / C::kParts;
   grid_dependency_wait();
   grid_launch_dependents();
   copy_table(table, *static_cast<const WeightedTable*>(a.table), static_cast<int>(a.T) * a.k);
@@ -542,16 +564,16 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
 
   const int K = static_cast<int>(a.H), bytes = row_bytes<FORM>(K), blocks = K / 32;
   const uint8_t* x0 = F::kBf16 ? static_cast<const uint8_t*>(a.x) : reinterpret_cast<const uint8_t*>(a.x16);
-  const bool words = F::kMx && blocks % 4 == 0 && (reinterpret_cast<uintptr_t>(a.s_in) & 3) == 0;
-  const int tiles = static_cast<int>((a.F + 31) / 32), step = static_cast<int>(gridDim.x);
+  const Scales all = {static_cast<const uint8_t*>(a.s_in) + static_cast<int64_t>(a.E) * 2 * a.F * blocks, blocks % 4 == 0};
+  const int tiles = static_cast<int>((a.F + C::kTile - 1) / C::kTile), step = static_cast<int>(gridDim.x);
   const int stages = static_cast<int>((K + F::kStageK - 1) / F::kStageK);
-  const int mine = group < stages ? (stages - group + kGroups - 1) / kGroups : 0;   // of a unit
+  const int mine = group < stages ? (stages - group + G - 1) / G : 0;   // of a unit
   const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStage;
-  // A unit's sets of rows from its first row f of the half on (F % 8 == 0: a set is in the matrix
+  // A part's sets of rows from its first row f on (F % 8 == 0: a set is in the matrix
   // or not): Wg's f .. f + 7, Wu's, Wg's f + 8 .. f + 15, Wu's.
   auto set_row = [&](int64_t f, int r) { return (r & 1 ? a.F : 0) + (r >> 1 && f + 8 < a.F ? 8 : 0); };
   auto first_row = [&](int rows) {
-    const int64_t f = static_cast<int64_t>(rows) * 32 + 16 * half;
+    const int64_t f = static_cast<int64_t>(rows) * C::kTile + 16 * part;
     return f < a.F ? f : 0;
   };
   if (warp == kWarps) {
@@ -562,9 +584,11 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
       const int first = table.first[entry], count = table.first[entry + 1] - first;
       const int64_t expert = table.expert[entry];
       if (!mbar_wait(full, done & 1, a.limit_ns, abort, a.status)) return;
-      // eight columns at a time: inner values 8 m + g of columns 2 t and 2 t + 1
-      for (int n = 0; 8 * n < count; ++n) {
-        const int64_t f0 = static_cast<int64_t>(rows) * 32;
+      // eight columns and 32 inner values at a time: values 8 m + g of columns 2 t and 2 t + 1
+      for (int qn = 0; qn < C::kTile / 32 * ((count + 7) / 8); ++qn) {
+        const int q = qn % (C::kTile / 32), n = qn / (C::kTile / 32);
+        const int64_t f0 = static_cast<int64_t>(rows) * C::kTile + 32 * q;
+        if (f0 >= a.F) continue;
         int64_t slots[2];
         float power[2] = {1.f, 1.f};
 #pragma unroll
@@ -578,9 +602,9 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
         for (int m = 0; m < 4; ++m) {
           float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int w = 0; w < kGroups; ++w) {
-            const float4 q = sums[((m * NT + n) * kGroups + w) * 32 + lane];
-            s.x += q.x, s.y += q.y, s.z += q.z, s.w += q.w;
+          for (int w = 0; w < G; ++w) {
+            const float4 one = sums[(((4 * q + m) * NT + n) * G + w) * 32 + lane];
+            s.x += one.x, s.y += one.y, s.z += one.z, s.w += one.w;
           }
           const int64_t f = f0 + 8 * m + g;
           if constexpr (FORM == BSMMA_OPERAND_INT8) {
@@ -602,7 +626,7 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
             for (int o = 4; o < 32; o <<= 1) amax[c] = fmaxf(amax[c], __shfl_xor_sync(kFull, amax[c], o));
             const float p = group_power(amax[c]);
             inv[c] = 1.f / p;
-            if (g == 0 && slots[c] >= 0) a.inner_power[slots[c] * power_stride(a.F) + rows] = p;
+            if (g == 0 && slots[c] >= 0) a.inner_power[slots[c] * power_stride(a.F) + f0 / 32] = p;
           }
         }
 #pragma unroll
@@ -640,7 +664,7 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
   };
   auto load = [&] {
     if (to_load) {
-      load_stage<FORM>(ring + slot * C::kStage, src, sets, group + li * kGroups, bytes, words);
+      load_stage<FORM>(ring + slot * C::kStage, src, sets, group + li * G, bytes, all);
       if (++li == mine) {
         li = 0;
         to_load = ahead.forward(table, step, tiles);
@@ -659,7 +683,9 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
   for (bool more = here.begin(table, blockIdx.x, tiles); more; more = here.forward(table, step, tiles), ++done) {
     const int entry = here.entry(), first = table.first[entry], count = table.first[entry + 1] - first;
     const int64_t expert = table.expert[entry], f_first = first_row(here.rows());
-    const uint8_t* scales = static_cast<const uint8_t*>(a.s_in) + (expert * 2 * a.F + f_first + g) * blocks;
+    uint32_t scale_at = static_cast<uint32_t>((expert * 2 * a.F + f_first + g) * blocks), set_blocks[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) set_blocks[r] = static_cast<uint32_t>(set_row(f_first, r) * blocks);
     // n_cols tiles of eight columns; a column past the entry's repeats its last
     auto products = [&](auto n_cols) {
       constexpr int N = decltype(n_cols)::value;
@@ -672,12 +698,11 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
       float acc[2][N][4] = {};
       for (int i = 0; i < mine; ++i) {
         stage_products<FORM, N, false, C::kStages - 2>(
-            acc, x0, x, x0, no_powers, K - k - 8 * t, ring + at * C::kStage, load,
-            [&](int r, int b) -> uint32_t { return scales[set_row(f_first, r) * blocks + k / 32 + b]; }, words,
-            (group + i * kGroups) & 1);
-        k += kGroups * F::kStageK;
+            acc, x0, x, x0, no_powers, K - k - 8 * t, ring + at * C::kStage, load, scale_at + k / 32,
+            set_blocks, all);
+        k += G * F::kStageK;
 #pragma unroll
-        for (int n = 0; n < N; ++n) x[n] += 2 * kGroups * F::kStageK;
+        for (int n = 0; n < N; ++n) x[n] += 2 * G * F::kStageK;
         at = at + 1 == C::kStages ? 0 : at + 1;
       }
       // the sums of the unit before have been read
@@ -686,7 +711,7 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int n = 0; n < N; ++n)
-          sums[(((2 * half + m) * NT + n) * kGroups + group) * 32 + lane] =
+          sums[(((2 * part + m) * NT + n) * G + group) * 32 + lane] =
               make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
       __syncwarp();
       if (lane == 0) mbar_arrive(full);
@@ -736,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_out_kernel(const StepArgs a,
   const int K = static_cast<int>(a.F), bytes = row_bytes<FORM>(K), blocks = K / 32, powers_at = static_cast<int>(power_stride(K));
   const uint8_t* x0 = reinterpret_cast<const uint8_t*>(a.inner);
   const uint8_t* p0 = reinterpret_cast<const uint8_t*>(a.inner_power);
-  const bool words = F::kMx && blocks % 4 == 0 && (reinterpret_cast<uintptr_t>(a.s_out) & 3) == 0;
+  const Scales all = {static_cast<const uint8_t*>(a.s_out) + static_cast<int64_t>(a.E) * a.H * blocks, blocks % 4 == 0};
   const int units = static_cast<int>((a.H + 31) / 32);
   const int stages = static_cast<int>((K + F::kStageK - 1) / F::kStageK);
   // the warp's run of (entry, stage)
@@ -764,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_out_kernel(const StepArgs a,
   if (i1 > i0 && lu < units) rows_of();
   auto load = [&] {
     if (i1 > i0 && lu < units) {
-      load_stage<FORM>(ring + slot * C::kStage, src, sets, ls, bytes, words);
+      load_stage<FORM>(ring + slot * C::kStage, src, sets, ls, bytes, all);
       bool moved = false;
       if (++ls == stages) ls = 0, ++le, moved = true;
       if (--left == 0) {
@@ -790,7 +815,9 @@ __global__ void __launch_bounds__(kThreads, 1) step_out_kernel(const StepArgs a,
       const int n_here = static_cast<int>(todo < stages - stage ? todo : stages - stage);
       const int first = table.first[entry], count = table.first[entry + 1] - first;
       const int64_t base = static_cast<int64_t>(table.expert[entry]) * a.H + row0;
-      const uint8_t* scales = static_cast<const uint8_t*>(a.s_out) + (base + g) * blocks;
+      uint32_t scale_at = static_cast<uint32_t>((base + g) * blocks), set_blocks[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) set_blocks[r] = static_cast<uint32_t>(set_row(row0, r) * blocks);
       auto products = [&](auto n_cols) {
         constexpr int N = decltype(n_cols)::value;
         int k = stage * F::kStageK;
@@ -805,9 +832,8 @@ __global__ void __launch_bounds__(kThreads, 1) step_out_kernel(const StepArgs a,
         float acc[2][N][4] = {};
         for (int i = 0; i < n_here; ++i) {
           stage_products<FORM, N, kPowers, C::kStages - 2>(
-              acc, x0, x, p0, powers, K - k - 8 * t, ring + at * C::kStage, load,
-              [&](int r, int b) -> uint32_t { return scales[set_row(row0, r) * blocks + k / 32 + b]; }, words,
-              (stage + i) & 1);
+              acc, x0, x, p0, powers, K - k - 8 * t, ring + at * C::kStage, load, scale_at + k / 32,
+              set_blocks, all);
           k += F::kStageK;
 #pragma unroll
           for (int n = 0; n < N; ++n) {
@@ -924,23 +950,37 @@ bsmma_status launch_out(const StepArgs& a, const DeviceInfo* dev, cudaStream_t s
   return cuda_ok(cudaLaunchKernelEx(&cfg, step_out_kernel<FORM, NT>, a, shared));
 }
 
+template <int FORM, int NT, int G>
+bsmma_status launch_in(const StepArgs& a, const DeviceInfo* dev, cudaStream_t stream) {
+  using C = InCfg<FORM, NT, G>;
+  static PerDevice set;
+  const bsmma_status st = set.allow_smem(dev->device, step_in_kernel<FORM, NT, G>, C::kBytes);
+  if (st != BSMMA_OK) return st;
+  // at most as many entries as slots
+  const int64_t units = a.T * a.k * ((a.F + C::kTile - 1) / C::kTile);
+  return cuda_ok(launch_dependent(step_in_kernel<FORM, NT, G>,
+                                  dim3(static_cast<unsigned>(std::min<int64_t>(units, dev->sm_count))),
+                                  dim3(kInThreads), C::kBytes, stream, a));
+}
+
 template <int FORM, int NT>
 bsmma_status launch_step(StepArgs a, const DeviceInfo* dev, cudaStream_t stream) {
   a.limit_ns = wait_limit_ns();
   a.status = dev->status;
-  static PerDevice in_set;
-  constexpr int kIn = InCfg<FORM, NT>::kBytes;
-  bsmma_status st = in_set.allow_smem(dev->device, step_in_kernel<FORM, NT>, kIn);
-  if (st != BSMMA_OK) return st;
-  const int64_t slots = a.T * a.k;   // at most this many entries
-  const int64_t in_units = slots * ((a.F + 31) / 32);
-  const unsigned in_blocks = static_cast<unsigned>(std::min<int64_t>(in_units, dev->sm_count));
-  cudaError_t e = launch_dependent(step_order_kernel, dim3(FORM == BSMMA_OPERAND_BF16 ? 1 : 1 + static_cast<unsigned>(a.T)),
-                                   dim3(kThreads), 0, stream, a, 8 * NT);
-  if (e == cudaSuccess)
-    e = launch_dependent(step_in_kernel<FORM, NT>, dim3(in_blocks), dim3(kInThreads), kIn, stream, a);
-  if (e != cudaSuccess) return BSMMA_ERR_CUDA;
-  st = launch_out<FORM, NT>(a, dev, stream);
+  if (launch_dependent(step_order_kernel, dim3(FORM == BSMMA_OPERAND_BF16 ? 1 : 1 + static_cast<unsigned>(a.T)),
+                       dim3(kThreads), 0, stream, a, 8 * NT) != cudaSuccess)
+    return BSMMA_ERR_CUDA;
+  // K over eight groups of warps where that leaves each three stages of a unit or more; short rows over
+  // two, in units of four times the columns (what a unit costs beside its stages, and the groups'
+  // unequal shares: 29 tokens, 63 experts of 8640 x 544 in E5M2 389 and 320 us), as long as those are
+  // units enough to share them evenly (three or four for an SM were slower: 18 tokens, 14 experts of
+  // 4720 x 432 in INT8 65 and 74 us): no more experts than E or slots are chosen
+  using F = Form<FORM>;
+  const int64_t stages = (a.H + F::kStageK - 1) / F::kStageK;
+  const int64_t wide_units = std::min<int64_t>(a.E, a.T * a.k) * ((a.F + 127) / 128);
+  bsmma_status st = stages < 24 && wide_units >= 8 * dev->sm_count ? launch_in<FORM, NT, 2>(a, dev, stream)
+                                                                   : launch_in<FORM, NT, 8>(a, dev, stream);
+  if (st == BSMMA_OK) st = launch_out<FORM, NT>(a, dev, stream);
   count_launches(3);
   return st;
 }

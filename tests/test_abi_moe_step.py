@@ -25,7 +25,7 @@ def test_refusals():
             (dict(ids=None), ARG), (dict(weights=None), ARG), (dict(w_in=None), ARG), (dict(w_out=None), ARG),
             (dict(out=None), ARG), (dict(x=A + 8), ALIGN), (dict(w_in=A + 8), ALIGN), (dict(w_out=A + 2), ALIGN),
             (dict(out=A + 8), ALIGN), (dict(ids=A + 2), ALIGN), (dict(weights=A + 1), ALIGN),
-            (dict(form=2, s_in=A + 2, s_out=A), ALIGN), (dict(T=0, x=None, out=None), OK)]:
+            (dict(form=2, s_in=A + 2, s_out=A), ALIGN), (dict(form=3, s_in=A, s_out=A + 1), ALIGN), (dict(T=0, x=None, out=None), OK)]:
         assert lib.moe_step(*{**BASE, **change}.values()) == want, change
 
 

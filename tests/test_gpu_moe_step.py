@@ -89,6 +89,8 @@ CASES = [
     (31, 2, 2, 128, 96, "silu", False),
     (32, 40, 16, 64, 32, "silu", True),
     (5, 1024, 32, 32, 32, "silu", False),
+    (3, 5, 2, 544, 1120, "silu", False),       # 17 and 35 blocks a row: scales in two words
+    (29, 6, 2, 224, 2080, "relu", True),
 ]
 
 
@@ -106,6 +108,16 @@ def test_odd_sizes(fmt, H, F):
     """Sizes that are whole 16-byte pieces and no more."""
     c = case(H + F, 4, 6, 2, H, F, fmt)
     check(run(c, fmt), c, fmt)
+
+
+@pytest.mark.parametrize("fmt,H", [("bf16", 168), ("int8", 208), ("e4m3", 288), ("e5m2", 32), ("e2m1", 352)])
+@pytest.mark.parametrize("T,k,F", [(5, 8, 4640), (13, 3, 4672)])
+def test_many_short_rows(T, k, F, fmt, H):
+    """Enough units of short rows to take them in wider units."""
+    c = case(T + H, T, 40, k, H, F, fmt, True)
+    got = run(c, fmt)
+    check(got, c, fmt)
+    assert torch.equal(run(c, fmt), got)
 
 
 def test_long_rows():
