@@ -149,7 +149,7 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst_smem, const void* src, i
 }
 
 // A value's power of two and FP16 form: the largest finite magnitude of a group of values goes to
-// 2^14 .. 2^15 (FP16 ends at 65504).  2^-127 bounds the power below, so that it is a float.
+// 2^14 .. 2^15 (FP16 ends at 65504).  2^-126 bounds the power below, so that it is a float.
 __device__ __forceinline__ float group_power(float amax) {
   const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14;
   return amax > 0.f ? __uint_as_float(static_cast<uint32_t>(max(e, -126) + 127) << 23) : 1.f;
@@ -426,6 +426,9 @@ __device__ __forceinline__ void stage_products(float (&acc)[2][NT][4], const uin
   load();
   float2 sw[F::kMx ? 4 : 1][F::kMx ? F::kBlocks / 2 : 1];
   if constexpr (F::kMx) {
+    // a block past K counts as 2^-127 times zero: the scale there is the next row's, which may be NaN
+    const int here = left + 8 * t;
+    const uint32_t in_row = here < F::kStageK ? (1u << (here / 4)) - 1 : kFull;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       uint32_t codes;
@@ -436,7 +439,7 @@ __device__ __forceinline__ void stage_products(float (&acc)[2][NT][4], const uin
       } else {
         uint32_t more;
         asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(codes), "=r"(more) : "r"(from));
-        codes = __funnelshift_r(codes, more, 8 * ((scale_at + set_blocks[r]) & 3));
+        codes = __funnelshift_r(codes, more, 8 * ((scale_at + set_blocks[r]) & 3)) & in_row;
       }
 #pragma unroll
       for (int j = 0; j < F::kBlocks / 2; ++j) sw[r][j] = e8m0x2(codes >> (16 * j));

@@ -532,8 +532,8 @@ bsmma_status moe_combine_backward(const void* dout, bsmma_dtype dtype, int64_t H
  *   the gathered rows of the grouped products (three launches: a small one that finds the chosen
  *   experts' tokens, and two that hold all of the products):
  *     out[t] = sum_j weights[t][j] * W2[e] (act(Wg[e] x[t]) * (Wu[e] x[t])),  e = ids[t][j]
- *   Only experts that some token chose are read, each once (their columns in tiles of 8, 16 or
- *   32 tokens; an expert with more columns is read once a tile).
+ *   Only experts that some token chose are read, each once (their columns in tiles of 8, or
+ *   with more than 8 tokens of 16; an expert with more columns is read once a tile).
  *   x BF16 [T][H]; ids int32 [T][k] and weights FP32 [T][k] as moe_route writes them (a slot
  *   with an id outside 0..E-1 adds nothing, whatever its weight; a token without any gives a
  *   row of zeros; an expert may be named twice); out BF16 [T][H].
@@ -547,7 +547,8 @@ bsmma_status moe_combine_backward(const void* dout, bsmma_dtype dtype, int64_t H
  *   Products are summed in FP32; the inner row act(..) * (..) is rounded once, as the second
  *   product's operand, to BF16 (BF16 weights) or to FP16 over a power of two for each 32 values
  *   (codes); with codes x is taken as FP16 over a power of two for each token, which loses only
- *   what is below 2^-29 of the token's largest value.  The sum over j is FP32, rounded once.
+ *   what is below 2^-29 of the token's largest value (a sum has to stay in FP32's range with that
+ *   value at 2^15).  The sum over j is FP32, rounded once.
  *   The sums' order depends on the sizes and the ids alone.
  * Preconditions: T >= 0, k >= 1, T <= 32, T * k <= 1024, 1 <= E <= 1024; H and F at least one
  *   piece of 16 bytes of codes and whole ones (BF16: H, F % 8 == 0; INT8: % 16; MX: % 32) and
@@ -593,7 +594,7 @@ typedef enum { BSMMA_NORM_NONE = 0, BSMMA_NORM_RMS = 1, BSMMA_NORM_LAYER = 2 } b
  *   (RMS or LAYER) also the following block's branch_enter of the row as it is stored in out:
  *   next_out in next_form (and next_scales) with next_weight, next_bias and next_eps, in the
  *   same pass; next NONE: next_out is not written.
- * Preconditions (these and the gradients): 0 <= T < 2^31, 8 <= H <= 16384, H % 8 == 0 (MX forms
+ * Preconditions (these and the gradients): 0 <= T < 2^31 - 1, 8 <= H <= 16384, H % 8 == 0 (MX forms
  *   H % 32 == 0), eps > 0 and finite where there is a norm, gate_rows >= 1 with a gate;
  *   16-byte-aligned matrices, weights and biases, 8-byte-aligned rng, 4-byte-aligned FP32
  *   scales.  Outputs overlap nothing else but as said.  One launch (none when T == 0).

@@ -158,6 +158,24 @@ def test_unread_values():
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2", "e2m1"])
+@pytest.mark.parametrize("H,F", [(96, 224), (32, 160)])
+def test_unread_scales(fmt, H, F):
+    """Rows whose blocks end inside a stage: the scales behind a row's last are another row's, or
+    another expert's, and a NaN there is not the row's."""
+    c = case(H + F, 6, 4, 1, H, F, fmt)
+    c["ids"][:, 0] = torch.tensor([0, 2, 0, 2, 0, -1])
+    clean = run(c, fmt)
+    for e in (1, 3):
+        c["s_in"][e] = c["s_out"][e] = 255
+    assert torch.equal(run(c, fmt), clean)
+    c["s_out"][0, 5] = 255
+    got = run(c, fmt)
+    assert got[[0, 2, 4], 5].isnan().all()
+    clean[[0, 2, 4], 5] = got[[0, 2, 4], 5] = 0
+    assert torch.equal(got, clean)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2", "e2m1"])
 def test_every_code_and_scale(fmt):
     """Every finite code under every block scale that leaves FP32 finite sums: one weight a row and
     a token of ones reads it back."""
