@@ -16,7 +16,10 @@
 // 115 us.)  The 32 K of a matrix step are one MX block, so a block's scale multiplies its sum,
 // four FMAs for 16 rows, and no weight.  Sums are FP32.
 //
-// First launch: who takes what (the chosen experts and their columns), and the tokens in FP16.
+// First launch, for codes: the tokens in FP16.  Every block of the other two makes the table of who
+// takes what (the chosen experts and their columns) for itself from the ids, in its ring's place; it
+// does so, and fills its ring, before it waits for the launch ahead of it.  (A table made by one
+// block of a launch ahead of them cost a call 1 to 2 us more, and BF16 a launch.)
 // Second: units of 32 inner columns (32 rows of Wg and the 32 of Wu) of one expert; the warps share
 // out K and the rows, their sums meet in shared memory, and the inner row leaves in BF16, or
 // in FP16 with a power of two for each 32 values.  Gate and up rows are put into the upper and
@@ -41,7 +44,6 @@ namespace {
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kMaxSlots = 1024, kMaxExperts = 1024;
-constexpr int kTableBytes = 8 + kMaxSlots * 12;   // sizeof(WeightedTable)
 
 // ------------------------------------------------------------------------- weights
 // A stage is 64 bytes of each of a warp's 32 rows: `kBlocks` blocks of 32 K, of which a row's four
@@ -168,7 +170,6 @@ struct Table {
 struct WeightedTable : Table {
   float weight[kMaxSlots];          // of each column
 };
-static_assert(sizeof(WeightedTable) == kTableBytes, "workspace layout");
 struct TableScratch {
   int start[kMaxExperts];           // counts, then first columns
   int32_t ids[kMaxSlots];
@@ -176,10 +177,13 @@ struct TableScratch {
 };
 constexpr uint16_t kNone = 0xFFFF;
 
-__device__ __forceinline__ void build_table(WeightedTable& t, TableScratch& s, const StepArgs& a, int tile) {
+// By every thread of the block; what is at `s` is free again afterwards.
+template <typename T>
+__device__ __forceinline__ void build_table(T& t, TableScratch& s, const StepArgs& a, int tile) {
   const int tid = threadIdx.x, lane = tid & 31, slots = static_cast<int>(a.T) * a.k;
-  for (int e = tid; e < a.E; e += kThreads) s.start[e] = 0;
-  for (int i = tid; i < slots; i += kThreads) {
+  const int threads = static_cast<int>(blockDim.x);
+  for (int e = tid; e < a.E; e += threads) s.start[e] = 0;
+  for (int i = tid; i < slots; i += threads) {
     const int32_t id = a.ids[i];
     s.ids[i] = id >= 0 && id < a.E ? id : -1;
   }
@@ -228,30 +232,27 @@ __device__ __forceinline__ void build_table(WeightedTable& t, TableScratch& s, c
     }
   }
   __syncthreads();
-  for (int i = tid; i < slots; i += kThreads) {
+  for (int i = tid; i < slots; i += threads) {
     if (s.rank[i] == kNone) continue;
     const int id = s.ids[i], c = s.start[id] + s.rank[i];
-    float w = a.weights[i];
-    for (int j = i + 1; j % a.k; ++j)
-      if (s.ids[j] == id) w += a.weights[j];
     t.slot[c] = static_cast<uint16_t>(i);
     t.token[c] = static_cast<uint16_t>(i / a.k);
-    t.weight[c] = w;
+    if constexpr (std::is_same_v<T, WeightedTable>) {
+      float w = a.weights[i];
+      for (int j = i + 1; j % a.k; ++j)
+        if (s.ids[j] == id) w += a.weights[j];
+      t.weight[c] = w;
+    }
   }
   __syncthreads();
 }
 
-// Block 0: the table.  Block 1 + t (forms with codes): token t in FP16 and its power of two.
-__global__ void __launch_bounds__(kThreads) step_order_kernel(const StepArgs a, int tile) {
-  __shared__ TableScratch scratch;
+// Block t: token t in FP16 and its power of two.
+__global__ void __launch_bounds__(kThreads) step_tokens_kernel(const StepArgs a) {
   __shared__ uint32_t part[kWarps];
   grid_dependency_wait();
   grid_launch_dependents();
-  if (blockIdx.x == 0) {
-    build_table(*static_cast<WeightedTable*>(a.table), scratch, a, tile);
-    return;
-  }
-  const int64_t t = blockIdx.x - 1;
+  const int64_t t = blockIdx.x;
   const uint4* x = static_cast<const uint4*>(a.x) + t * (a.H / 8);
   uint4* out = reinterpret_cast<uint4*>(a.x16) + t * (a.H / 8);
   const int vecs = static_cast<int>(a.H / 8);
@@ -285,19 +286,6 @@ __global__ void __launch_bounds__(kThreads) step_order_kernel(const StepArgs a, 
     out[v] = make_uint4(o[0], o[1], o[2], o[3]);
   }
   if (threadIdx.x == 0) a.x_power[t] = power;
-}
-
-// The table in shared memory (every thread of the block).
-__device__ __forceinline__ void copy_table(Table& to, const Table& from, int slots) {
-  const int tid = threadIdx.x;
-  if (tid == 0) to.entries = from.entries;
-  for (int i = tid; i < slots + 1; i += kThreads) {
-    to.first[i] = from.first[i];
-    if (i == slots) break;
-    to.slot[i] = from.slot[i];
-    to.token[i] = from.token[i];
-    to.expert[i] = from.expert[i];
-  }
 }
 
 // ------------------------------------------------------------------------- products
@@ -560,10 +548,14 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int part = warp % C::kParts, group = warp / C::kParts;
-  grid_dependency_wait();
-  grid_launch_dependents();
-  copy_table(table, *static_cast<const WeightedTable*>(a.table), static_cast<int>(a.T) * a.k);
-  __syncthreads();
+  // BF16: this is the first launch.  Else the one ahead let this one start when all that was before
+  // itself had ended, so only the tokens are waited for, with the ring full.
+  if constexpr (F::kBf16) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+  }
+  build_table(table, *reinterpret_cast<TableScratch*>(smem), a, 8 * NT);
+  static_assert(sizeof(TableScratch) <= C::kRing, "the ring's place");
 
   const int K = static_cast<int>(a.H), bytes = row_bytes<FORM>(K), blocks = K / 32;
   const uint8_t* x0 = F::kBf16 ? static_cast<const uint8_t*>(a.x) : reinterpret_cast<const uint8_t*>(a.x16);
@@ -580,6 +572,7 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
     return f < a.F ? f : 0;
   };
   if (warp == kWarps) {
+    if constexpr (!F::kBf16) grid_dependency_wait();
     int done = 0;
     Walk here;
     for (bool more = here.begin(table, blockIdx.x, tiles); more; more = here.forward(table, step, tiles), ++done) {
@@ -680,6 +673,10 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
   if (to_load) enter_unit();
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i) load();
+  if constexpr (!F::kBf16) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+  }
 
   int at = 0, done = 0;
   Walk here;
@@ -734,9 +731,9 @@ struct OutCfg {
   static constexpr int kStage = Form<FORM>::kStage;
   static constexpr int kTokens = NT == 1 ? 8 : 32;
   static constexpr int kSums = (kWarps + 2) * kTokens * 32 * 4;   // of each warp, and twice the block's
-  static constexpr int kStages = (232448 - kSums - kTableBytes) / (kWarps * kStage);
+  static constexpr int kStages = (232448 - kSums - static_cast<int>(sizeof(WeightedTable))) / (kWarps * kStage);
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kBytes = kRing + kTableBytes + kSums;
+  static constexpr int kBytes = kRing + static_cast<int>(sizeof(WeightedTable)) + kSums;
   static_assert(kStages >= 2, "one stage in flight");
 };
 
@@ -747,19 +744,17 @@ __global__ void __launch_bounds__(kThreads, 1) step_out_kernel(const StepArgs a,
   constexpr bool kPowers = !F::kBf16;
   extern __shared__ __align__(128) uint8_t smem[];
   WeightedTable& table = *reinterpret_cast<WeightedTable*>(smem + C::kRing);
-  float* sums = reinterpret_cast<float*>(smem + C::kRing + kTableBytes);   // [warp][token][32]
+  float* sums = reinterpret_cast<float*>(smem + C::kRing + sizeof(WeightedTable));   // [warp][token][32]
   const int T = static_cast<int>(a.T), values = T * 32;
   float* totals = sums + kWarps * values;                                  // [2][token][32]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(blockIdx.x) % cluster, clusters = static_cast<int>(gridDim.x) / cluster;
-  // the table and w_out were there before the second launch let this one start (it waited for
-  // what was before it); only the inner rows are waited for
+  // what the second launch waited for, the ids and w_out among it, was there before it let this one
+  // start; only the inner rows are waited for
   float* own = sums + warp * values;
   for (int i = lane; i < values; i += 32) own[i] = 0.f;
-  const WeightedTable& from = *static_cast<const WeightedTable*>(a.table);
-  copy_table(table, from, T * a.k);
-  for (int i = threadIdx.x; i < T * a.k; i += kThreads) table.weight[i] = from.weight[i];
-  __syncthreads();
+  build_table(table, *reinterpret_cast<TableScratch*>(smem), a, 8 * NT);
+  static_assert(sizeof(TableScratch) <= C::kRing, "the ring's place");
 
   const int K = static_cast<int>(a.F), bytes = row_bytes<FORM>(K), blocks = K / 32, powers_at = static_cast<int>(power_stride(K));
   const uint8_t* x0 = reinterpret_cast<const uint8_t*>(a.inner);
@@ -970,9 +965,12 @@ template <int FORM, int NT>
 bsmma_status launch_step(StepArgs a, const DeviceInfo* dev, cudaStream_t stream) {
   a.limit_ns = wait_limit_ns();
   a.status = dev->status;
-  if (launch_dependent(step_order_kernel, dim3(FORM == BSMMA_OPERAND_BF16 ? 1 : 1 + static_cast<unsigned>(a.T)),
-                       dim3(kThreads), 0, stream, a, 8 * NT) != cudaSuccess)
-    return BSMMA_ERR_CUDA;
+  if (FORM != BSMMA_OPERAND_BF16) {
+    if (launch_dependent(step_tokens_kernel, dim3(static_cast<unsigned>(a.T)), dim3(kThreads), 0, stream, a) !=
+        cudaSuccess)
+      return BSMMA_ERR_CUDA;
+    count_launches(1);
+  }
   // K over eight groups of warps where that leaves each three stages of a unit or more; short rows over
   // two, in units of four times the columns (what a unit costs beside its stages, and the groups'
   // unequal shares: 29 tokens, 63 experts of 8640 x 544 in E5M2 389 and 320 us), as long as those are
@@ -984,7 +982,7 @@ bsmma_status launch_step(StepArgs a, const DeviceInfo* dev, cudaStream_t stream)
   bsmma_status st = stages < 24 && wide_units >= 8 * dev->sm_count ? launch_in<FORM, NT, 2>(a, dev, stream)
                                                                    : launch_in<FORM, NT, 8>(a, dev, stream);
   if (st == BSMMA_OK) st = launch_out<FORM, NT>(a, dev, stream);
-  count_launches(3);
+  count_launches(2);
   return st;
 }
 
@@ -999,7 +997,7 @@ constexpr int64_t round_up(int64_t n) { return (n + 255) / 256 * 256; }
 }  // namespace
 
 int64_t step_workspace_bytes(int64_t T, int k, int64_t H, int64_t F) {
-  return round_up(kTableBytes) + round_up(T * 4) + round_up(T * H * 2) + round_up(T * k * power_stride(F) * 4) +
+  return round_up(T * 4) + round_up(T * H * 2) + round_up(T * k * power_stride(F) * 4) +
          round_up(T * k * F * 2);
 }
 
@@ -1013,7 +1011,6 @@ bsmma_status launch_moe_step(StepArgs a, int form, void* workspace, cudaStream_t
     p += round_up(n);
     return q;
   };
-  a.table = take(kTableBytes);
   a.x_power = reinterpret_cast<float*>(take(a.T * 4));
   a.x16 = reinterpret_cast<uint16_t*>(take(a.T * a.H * 2));
   a.inner_power = reinterpret_cast<float*>(take(a.T * a.k * power_stride(a.F) * 4));

@@ -19,7 +19,6 @@ struct StepArgs {
   uint64_t limit_ns;             // of a wait on the device, and where one that ran out is latched
   int* status;
   // in the workspace
-  void* table;                   // who takes what
   float* x_power;                // [T], and the tokens in FP16 over it
   uint16_t* x16;                 // [T][H]
   float* inner_power;            // [T * k][F / 32, in fours], and the inner rows in FP16 over it, or

@@ -529,8 +529,8 @@ bsmma_status moe_combine_backward(const void* dout, bsmma_dtype dtype, int64_t H
 
 /*
  * moe_step -- the experts and the weighted sum of a few tokens, without the expert order and
- *   the gathered rows of the grouped products (three launches: a small one that finds the chosen
- *   experts' tokens, and two that hold all of the products):
+ *   the gathered rows of the grouped products (two launches that hold all of the products and,
+ *   with codes, a small one ahead of them for the tokens):
  *     out[t] = sum_j weights[t][j] * W2[e] (act(Wg[e] x[t]) * (Wu[e] x[t])),  e = ids[t][j]
  *   Only experts that some token chose are read, each once (their columns in tiles of 8, or
  *   with more than 8 tokens of 16; an expert with more columns is read once a tile).
