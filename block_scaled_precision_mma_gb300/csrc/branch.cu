@@ -16,28 +16,26 @@ namespace {
 using namespace branch;
 
 // ------------------------------------------------------------------------- norms
-constexpr int kPieces = 4;   // a thread's, in registers
-template <bool WARP>
-using Row = Place<WARP, kPieces>;
+constexpr int kPieces = 4;   // a thread's, in registers (rows of up to 256 values: one, up to 512: two)
 
 // f (zeros in pieces past the row) -> n(f) * weight + bias.  The variance of a layer norm is
 // summed around the mean, in a second pass over the registers: a row far from zero keeps its
 // digits.  part: 64 floats.
-template <bool WARP>
-__device__ __forceinline__ void norm_row(Vals (&f)[kPieces], const NormArgs& a, const Row<WARP>& at, float inv_h,
+template <bool WARP, int V>
+__device__ __forceinline__ void norm_row(Vals (&f)[V], const NormArgs& a, const Place<WARP, V>& at, float inv_h,
                                          float* part) {
   float s[1];
   if (a.kind == BSMMA_NORM_LAYER) {
     float2 acc[2] = {both(0.f), both(0.f)};
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i)
+    for (int i = 0; i < V; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[j & 1] = add2(acc[j & 1], f[i].v[j]);
     s[0] = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
     row_sums<WARP>(s, part);
     const float2 minus_mean = both(-s[0] * inv_h);
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i)
+    for (int i = 0; i < V; ++i)
       if (at.in(i))
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[i].v[j] = add2(f[i].v[j], minus_mean);
@@ -45,21 +43,21 @@ __device__ __forceinline__ void norm_row(Vals (&f)[kPieces], const NormArgs& a, 
   }
   float2 acc[2] = {both(0.f), both(0.f)};
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i)
+  for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j & 1] = __ffma2_rn(f[i].v[j], f[i].v[j], acc[j & 1]);
   s[0] = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
   row_sums<WARP>(s, part);
   const float2 rs = both(inv_sqrt(fmaf(s[0], inv_h, a.eps)));
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i)
+  for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) f[i].v[j] = mul2(f[i].v[j], rs);
   // what a call may leave out stands in loops of its own, which it jumps over
   if (a.weight) {
     const float* w0 = a.weight + 8 * at.base;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i)
+    for (int i = 0; i < V; ++i)
       if (at.in(i)) {
         const Vals w = load_columns(w0, 256 * i);
 #pragma unroll
@@ -69,7 +67,7 @@ __device__ __forceinline__ void norm_row(Vals (&f)[kPieces], const NormArgs& a, 
   if (a.bias) {
     const float* b0 = a.bias + 8 * at.base;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i)
+    for (int i = 0; i < V; ++i)
       if (at.in(i)) {
         const Vals b = load_columns(b0, 256 * i);
 #pragma unroll
@@ -125,14 +123,14 @@ __device__ __forceinline__ void store_mx(const Vals& f, uint8_t* codes, uint8_t*
   }
   if (first) *scale = static_cast<uint8_t>(code);
 }
-template <int FMT, bool WARP>
-__device__ __forceinline__ void store_mx_row(const Vals (&f)[kPieces], const OperandArgs& to, int64_t t, int64_t H,
-                                             const Row<WARP>& at) {
+template <int FMT, bool WARP, int V>
+__device__ __forceinline__ void store_mx_row(const Vals (&f)[V], const OperandArgs& to, int64_t t, int64_t H,
+                                             const Place<WARP, V>& at) {
   constexpr int kCodes = FMT == BSMMA_OPERAND_E2M1 ? 4 : 8;   // bytes of a piece
   uint8_t* codes = static_cast<uint8_t*>(to.out) + t * (H / 8) * kCodes + at.base * kCodes;
   uint8_t* scales = static_cast<uint8_t*>(to.scales) + t * (H / 32) + (at.base >> 2);
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i)
+  for (int i = 0; i < V; ++i)
     store_mx<FMT>(f[i], codes + 32 * kCodes * i, scales + 8 * i, at.in(i), (at.base & 3) == 0);
 }
 
@@ -169,32 +167,32 @@ __device__ __forceinline__ uint2 int8_codes(const Vals& f, const Int8Scale& k) {
   return make_uint2(c[0], c[1]);
 }
 
-template <bool WARP>
-__device__ __forceinline__ void store_int8(const Vals (&f)[kPieces], const OperandArgs& to, int64_t t, int64_t H,
-                                           const Row<WARP>& at, float* part) {
+template <bool WARP, int V>
+__device__ __forceinline__ void store_int8(const Vals (&f)[V], const OperandArgs& to, int64_t t, int64_t H,
+                                           const Place<WARP, V>& at, float* part) {
   uint32_t amax = 0;
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) amax = magnitude(f[i], amax);
+  for (int i = 0; i < V; ++i) amax = magnitude(f[i], amax);
   const Int8Scale k = int8_scale(row_max<WARP>(amax, reinterpret_cast<uint32_t*>(part)));
   if (at.base == 0) static_cast<float*>(to.scales)[t] = k.s;
   int8_t* codes = static_cast<int8_t*>(to.out) + t * H + 8 * at.base;
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i)
+  for (int i = 0; i < V; ++i)
     if (at.in(i)) *reinterpret_cast<uint2*>(codes + 256 * i) = int8_codes(f[i], k);
 }
 
-template <bool WARP>
-__device__ __forceinline__ void store_operand(const Vals (&f)[kPieces], const OperandArgs& to, int64_t t, int64_t H,
-                                              const Row<WARP>& at, float* part) {
+template <bool WARP, int V>
+__device__ __forceinline__ void store_operand(const Vals (&f)[V], const OperandArgs& to, int64_t t, int64_t H,
+                                              const Place<WARP, V>& at, float* part) {
   switch (to.form) {
     case BSMMA_OPERAND_BF16:
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i)
+      for (int i = 0; i < V; ++i)
         if (at.in(i)) store_raw<false>(to.out, t * H + 8 * at.base + 256 * i, narrow<false>(f[i]));
       break;
     case BSMMA_OPERAND_F32:
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i)
+      for (int i = 0; i < V; ++i)
         if (at.in(i)) store_raw<true>(to.out, t * H + 8 * at.base + 256 * i, narrow<true>(f[i]));
       break;
     case BSMMA_OPERAND_INT8: store_int8<WARP>(f, to, t, H, at, part); break;
@@ -220,57 +218,57 @@ constexpr int kMaxThreads = 512, kShortThreads = 256;
 // 70 us, 403 MB at 5.7 TB/s.  Tried and slower: two rows a block that share the weights (87 us, 14
 // warps an SM), and rows in a ring of asynchronous copies, one (78) or two (86) at a time, which
 // widen the values anew in each pass.
-template <bool F32, bool WARP, bool SHORT>
+template <bool F32, bool WARP, bool SHORT, int V>
 __global__ void __launch_bounds__(SHORT ? kShortThreads : kMaxThreads, SHORT ? 4 : 2) enter_kernel(const EnterArgs p) {
   __shared__ float part[WARP ? 1 : 3 * 32];
   grid_dependency_wait();
   grid_launch_dependents();
-  const Row<WARP> at(p.H);
+  const Place<WARP, V> at(p.H);
   const int64_t t = row_of<WARP>();
   if (t >= p.T) return;   // (whole warps, and no barrier where a row is a warp's)
-  Raw<F32> raw[kPieces];
+  Raw<F32> raw[V];
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i)
+  for (int i = 0; i < V; ++i)
     raw[i] = at.in(i) ? load_raw<F32>(p.x, t * p.H + 8 * at.base + 256 * i) : zero_raw<F32>();
-  Vals f[kPieces];
+  Vals f[V];
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) f[i] = widen<F32>(raw[i]);
+  for (int i = 0; i < V; ++i) f[i] = widen<F32>(raw[i]);
   norm_row<WARP>(f, p.norm, at, p.inv_h, part);
   store_operand<WARP>(f, p.to, t, p.H, at, part + (WARP ? 0 : 64));
 }
 
-template <bool XF, bool YF, bool WARP, bool SHORT>
+template <bool XF, bool YF, bool WARP, bool SHORT, int V>
 __global__ void __launch_bounds__(SHORT ? kShortThreads : kMaxThreads, SHORT ? 3 : 1) leave_kernel(const LeaveArgs p) {
   __shared__ float part[WARP ? 1 : 5 * 32];
   grid_dependency_wait();
   grid_launch_dependents();
-  const Row<WARP> at(p.H);
+  const Place<WARP, V> at(p.H);
   const int64_t t = row_of<WARP>();
   if (t >= p.T) return;
   const float inv_h = p.inv_h;
   const int64_t row = t * p.H + 8 * at.base;
-  Raw<YF> ry[kPieces];
-  Raw<XF> rx[kPieces];
+  Raw<YF> ry[V];
+  Raw<XF> rx[V];
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
+  for (int i = 0; i < V; ++i) {
     ry[i] = at.in(i) ? load_raw<YF>(p.y, row + 256 * i) : zero_raw<YF>();
     rx[i] = at.in(i) ? load_raw<XF>(p.x, row + 256 * i) : zero_raw<XF>();
   }
-  Vals f[kPieces];
+  Vals f[V];
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) f[i] = widen<YF>(ry[i]);
+  for (int i = 0; i < V; ++i) f[i] = widen<YF>(ry[i]);
   if (p.norm.kind != BSMMA_NORM_NONE) norm_row<WARP>(f, p.norm, at, inv_h, part);
   if (p.drop.threshold != 0) {
     const Philox gen = philox_of(p.drop.rng);
     const uint64_t block = static_cast<uint64_t>(t) * at.vecs + at.base;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) drop(f[i], philox(gen, block + 32 * i), p.drop.threshold << 16);
+    for (int i = 0; i < V; ++i) drop(f[i], philox(gen, block + 32 * i), p.drop.threshold << 16);
   }
   if (p.gate) {
     const int64_t from =
         static_cast<int64_t>(static_cast<uint32_t>(t) / static_cast<uint32_t>(p.gate_rows)) * p.H + 8 * at.base;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i)
+    for (int i = 0; i < V; ++i)
       if (at.in(i)) {
         const Vals g = widen<YF>(load_raw<YF>(p.gate, from + 256 * i));
 #pragma unroll
@@ -279,7 +277,7 @@ __global__ void __launch_bounds__(SHORT ? kShortThreads : kMaxThreads, SHORT ? 3
   }
   const float2 xs = both(p.x_scale), ys = both(p.y_scale * p.drop.scale);
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
+  for (int i = 0; i < V; ++i) {
     const Vals x = widen<XF>(rx[i]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) f[i].v[j] = __ffma2_rn(ys, f[i].v[j], mul2(xs, x.v[j]));
@@ -344,18 +342,22 @@ template <bool F32>
 bsmma_status launch_enter(const EnterArgs& a, cudaStream_t stream) {
   const bool warp = a.H <= kWarpRow;
   const unsigned threads = threads_of(a.H);
-  return cuda_ok(launch_dependent(warp ? enter_kernel<F32, true, true>
-                                  : threads <= kShortThreads ? enter_kernel<F32, false, true>
-                                                             : enter_kernel<F32, false, false>,
+  return cuda_ok(launch_dependent(a.H <= kWarpRow / 4        ? enter_kernel<F32, true, true, 1>
+                                  : a.H <= kWarpRow / 2      ? enter_kernel<F32, true, true, 2>
+                                  : warp                     ? enter_kernel<F32, true, true, kPieces>
+                                  : threads <= kShortThreads ? enter_kernel<F32, false, true, kPieces>
+                                                             : enter_kernel<F32, false, false, kPieces>,
                                   dim3(static_cast<unsigned>(warp ? (a.T + 3) / 4 : a.T)), dim3(threads), 0, stream, a));
 }
 template <bool XF, bool YF>
 bsmma_status launch_leave(const LeaveArgs& a, cudaStream_t stream) {
   const unsigned threads = threads_of(a.H);
   const bool warp = a.H <= kWarpRow;
-  return cuda_ok(launch_dependent(warp ? leave_kernel<XF, YF, true, true>
-                                  : threads <= kShortThreads ? leave_kernel<XF, YF, false, true>
-                                                             : leave_kernel<XF, YF, false, false>,
+  return cuda_ok(launch_dependent(a.H <= kWarpRow / 4        ? leave_kernel<XF, YF, true, true, 1>
+                                  : a.H <= kWarpRow / 2      ? leave_kernel<XF, YF, true, true, 2>
+                                  : warp                     ? leave_kernel<XF, YF, true, true, kPieces>
+                                  : threads <= kShortThreads ? leave_kernel<XF, YF, false, true, kPieces>
+                                                             : leave_kernel<XF, YF, false, false, kPieces>,
                                   dim3(static_cast<unsigned>(warp ? (a.T + 3) / 4 : a.T)), dim3(threads), 0, stream, a));
 }
 

@@ -17,8 +17,7 @@ int workers_of(int64_t T, int64_t H) {
   return static_cast<int>(std::min(T, most));
 }
 
-// The workers' sums of 32 columns, added by eight threads a column, each a run of workers.
-constexpr int kSumLanes = 8;
+// The workers' sums of 32 columns, added by LANES threads a column, each a run of workers.
 // The worker that has a row: the last one whose first row is not after it.
 __device__ __forceinline__ int worker_of(int64_t T, int workers, int64_t row) {
   return static_cast<int>(((row + 1) * workers - 1) / T);
@@ -30,8 +29,9 @@ struct SumParams {
   int workers, fixed;   // fixed: blockIdx.y below it are dweight and dbias
   bool by_worker;
 };
-__global__ void __launch_bounds__(32 * kSumLanes) sum_kernel(const SumParams p) {
-  __shared__ float part[kSumLanes][32];
+template <int LANES>
+__global__ void __launch_bounds__(32 * LANES) sum_kernel(const SumParams p) {
+  __shared__ float part[LANES][32];
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
@@ -68,15 +68,15 @@ __global__ void __launch_bounds__(32 * kSumLanes) sum_kernel(const SumParams p) 
   }
   float s = 0.f;
   if (c < p.H) {
-    const int n = w1 - w0, a = w0 + n * run / kSumLanes, e = w0 + n * (run + 1) / kSumLanes;
-#pragma unroll 4
+    const int n = w1 - w0, a = w0 + n * run / LANES, e = w0 + n * (run + 1) / LANES;
+#pragma unroll 8
     for (int w = a; w < e; ++w) s += from[w * step + (w == w0 ? first : 0) + c];
   }
   part[run][lane] = s;
   __syncthreads();
   if (run == 0 && c < p.H) {
 #pragma unroll
-    for (int i = 1; i < kSumLanes; ++i) s += part[i][lane];
+    for (int i = 1; i < LANES; ++i) s += part[i][lane];
     to[c] = s;
   }
 }
@@ -134,9 +134,12 @@ bsmma_status launch_branch_grad(const BranchGradArgs& a, bool leave, void* works
   const int shared = static_cast<int>(std::min<int64_t>(gates, p.workers - 1));
   s.by_worker = gates > p.workers - 1;
   if (s.fixed + shared == 0) return BSMMA_OK;
-  const cudaError_t e =
-      launch_dependent(sum_kernel, dim3(static_cast<unsigned>((a.H + 31) / 32), s.fixed + shared),
-                       dim3(32 * kSumLanes), 0, stream, s);
+  // Eight threads a column where the blocks fill the GPU, else 32: few columns have as many workers as
+  // many have (5499 rows of 128, both directions 58 and 43 us; 16383 of
+  // 4096, 242 and 237)
+  const dim3 grid(static_cast<unsigned>((a.H + 31) / 32), s.fixed + shared);
+  const cudaError_t e = grid.x * grid.y < 4 * 152 ? launch_dependent(sum_kernel<32>, grid, dim3(1024), 0, stream, s)
+                                                  : launch_dependent(sum_kernel<8>, grid, dim3(256), 0, stream, s);
   count_launches(1);
   return cuda_ok(e);
 }

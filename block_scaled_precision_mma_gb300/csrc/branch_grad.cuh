@@ -17,6 +17,8 @@
 // others' pieces (each worker has at most a first and a last such gate) are added by the
 // second launch.  Nothing depends on the order in which blocks run.
 #pragma once
+#include <type_traits>
+
 #include "branch.cuh"
 #include "branch.h"
 
@@ -39,17 +41,21 @@ __device__ __forceinline__ void store_sums(float* to, const Vals& f) {
   *reinterpret_cast<float4*>(to + 4) = make_float4(f.v[2].x, f.v[2].y, f.v[3].x, f.v[3].y);
 }
 
-// A thread's pieces of a row: with up to three sums a column the registers hold two (a warp's
-// rows are short, and four of them keep it busy).
-template <bool WARP>
-constexpr int kGradPieces = WARP ? 4 : 2;
-// Blocks of up to 14 warps (rows of 7168) keep 128 registers a thread, longer rows 64.
-template <bool WARP, bool LONG>
-constexpr int kGradThreads = WARP ? 128 : LONG ? 1024 : 512;
+// How a row is held: by a warp (rows of up to 256, 512 or 1024 values) or by a block.  A thread's
+// pieces: with up to three sums a column the registers hold two; a warp's rows are short, and four of
+// them keep it busy, or as many as there are (a step of 65536 rows of 256 values with dropout, a gate a row and
+// two norms, both directions, 144 us, and 275 in warps that go through four).
+// Blocks of up to 16 warps (rows of 8192) keep 128 registers a thread, longer rows 64.
+enum RowKind { ROW_WARP_1, ROW_WARP_2, ROW_WARP, ROW_BLOCK, ROW_LONG };
+template <RowKind ROW>
+constexpr int kGradPieces = ROW == ROW_WARP_1 ? 1 : ROW == ROW_WARP ? 4 : 2;
+template <RowKind ROW>
+constexpr int kGradThreads = ROW <= ROW_WARP ? 128 : ROW == ROW_LONG ? 1024 : 512;
 
-template <bool LEAVE, bool DF, bool VF, bool BIAS, bool GATE, bool WARP, bool LONG>
-__global__ void __launch_bounds__(kGradThreads<WARP, LONG>, 1) grad_kernel(const GradParams p) {
-  constexpr int V = kGradPieces<WARP>;
+template <bool LEAVE, bool DF, bool VF, bool BIAS, bool GATE, RowKind ROW>
+__global__ void __launch_bounds__(kGradThreads<ROW>, 1) grad_kernel(const GradParams p) {
+  constexpr int V = kGradPieces<ROW>;
+  constexpr bool WARP = ROW <= ROW_WARP, LONG = ROW == ROW_LONG;
   constexpr int kPart = WARP ? 1 : 64;
   __shared__ float part[2][2][kPart];   // by the row's parity: one barrier a reduction
   grid_dependency_wait();
@@ -79,24 +85,6 @@ __global__ void __launch_bounds__(kGradThreads<WARP, LONG>, 1) grad_kernel(const
     g = r0 / a.gate_rows;
     g_end = (g + 1) * a.gate_rows;
   }
-  auto flush_gate = [&] {
-    if constexpr (GATE) {
-      const int64_t begin = g * a.gate_rows, end = g_end < a.T ? g_end : a.T;
-      float* to = begin >= r0 && end <= r1
-                      ? a.dgate + g * a.H
-                      : p.part_g + (2 * static_cast<int64_t>(worker) + (begin > r0)) * a.H;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        // without a norm the factor is still to come (with one it came with n)
-        if (!normed)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sg[i].v[j] = mul2(sg[i].v[j], both(a.y_scale * a.drop.scale));
-        if (at.in(i)) store_sums(to + 8 * at.at(i), sg[i]);
-        sg[i] = none;
-      }
-    }
-  };
-
   // dz is linear in d: its constant factor goes into the row's factors and into the sums
   const float scale = LEAVE ? a.y_scale * a.drop.scale : 1.f;
   // everything a row is read from and written to lies at these places, a row after the other
@@ -116,6 +104,46 @@ __global__ void __launch_bounds__(kGradThreads<WARP, LONG>, 1) grad_kernel(const
     if constexpr (VF) return widen<true>(load_raw<true>(gate_f32, 256 * i));
     else return widen<false>(load_raw<false>(gate_bf16, 256 * i));
   };
+  auto weighted = [&](int i, Vals z) {
+    if (w_at) {
+      const Vals w = load_columns(w_at, 256 * i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z.v[j] = mul2(z.v[j], w.v[j]);
+    }
+    return z;
+  };
+
+  // Where registers allow, gate * weight (a factor of 1 without either), by which d becomes q, is held for
+  // a gate's rows, or for all.  With a gate's gradient sg is then the sum of d n, which over a
+  // gate's rows gives dgate, times the weight, and its part of dweight, times the gate.  (Taken from the L1
+  // cache for every row: 20000 rows of 5120 with dropout and a gate for 2048 of them 221 us, and 172.)
+  constexpr bool HOLD = !LONG && !(BIAS && (GATE || VF));
+  Vals gw[HOLD ? V : 1];
+  auto flush_gate = [&] {
+    if constexpr (GATE) {
+      const int64_t begin = g * a.gate_rows, end = g_end < a.T ? g_end : a.T;
+      float* to = begin >= r0 && end <= r1
+                      ? a.dgate + g * a.H
+                      : p.part_g + (2 * static_cast<int64_t>(worker) + (begin > r0)) * a.H;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        // without a norm the factor is still to come (with one it came with n)
+        if (!normed)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sg[i].v[j] = mul2(sg[i].v[j], both(a.y_scale * a.drop.scale));
+        if (at.in(i)) {
+          if (HOLD && normed) {
+            const Vals one = gate_piece(i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sw[i].v[j] = __ffma2_rn(one.v[j], sg[i].v[j], sw[i].v[j]);
+            sg[i] = weighted(i, sg[i]);
+          }
+          store_sums(to + 8 * at.at(i), sg[i]);
+        }
+        sg[i] = none;
+      }
+    }
+  };
 
   Raw<VF> next_v[V];
   Raw<DF> next_d[V];
@@ -129,19 +157,35 @@ __global__ void __launch_bounds__(kGradThreads<WARP, LONG>, 1) grad_kernel(const
         next_d[i] = load_raw<DF>(d_at, 256 * i);
       }
   };
+  // the factors of a gate's rows (no gate: of all rows)
+  auto use_gate = [&](int64_t row) {
+    const bool gates = LEAVE && (GATE || a.gate);
+    if (gates) {
+      if constexpr (VF) gate_f32 = static_cast<const float*>(a.gate) + row * a.H + 8 * at.base;
+      else gate_bf16 = static_cast<const __nv_bfloat16*>(a.gate) + row * a.H + 8 * at.base;
+    }
+    if constexpr (HOLD) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        gw[i] = Vals{{both(1.f), both(1.f), both(1.f), both(1.f)}};
+        if (!at.in(i)) continue;
+        if (gates) gw[i] = gate_piece(i);
+        gw[i] = weighted(i, gw[i]);
+      }
+    }
+  };
   if (r0 < r1) fetch();
+  use_gate(GATE ? g : 0);
   for (int64_t r = r0; r < r1; ++r) {
     if constexpr (GATE) {
       if (r == g_end) {
         flush_gate();
         ++g;
         g_end += a.gate_rows;
+        use_gate(g);
       }
-    }
-    if (LEAVE && (GATE || a.gate)) {
-      const int64_t row = GATE ? g : static_cast<int64_t>(static_cast<uint32_t>(r) / static_cast<uint32_t>(a.gate_rows));
-      if constexpr (VF) gate_f32 = static_cast<const float*>(a.gate) + row * a.H + 8 * at.base;
-      else gate_bf16 = static_cast<const __nv_bfloat16*>(a.gate) + row * a.H + 8 * at.base;
+    } else if (LEAVE && a.gate) {
+      use_gate(static_cast<uint32_t>(r) / static_cast<uint32_t>(a.gate_rows));
     }
     Vals c[V], of[V];   // the rows, later less their mean; d, without what was dropped
 #pragma unroll
@@ -167,7 +211,7 @@ __global__ void __launch_bounds__(kGradThreads<WARP, LONG>, 1) grad_kernel(const
       for (int i = 0; i < V; ++i)
         drop(of[i], philox(gen, static_cast<uint64_t>(r) * at.vecs + at.at(i)), a.drop.threshold << 16);
     }
-    // dz / scale, and times the weight
+    // dz / scale, and times the weight (q / scale)
     auto gated = [&](int i) {
       Vals z = of[i];
       if (LEAVE && (GATE || a.gate)) {
@@ -177,13 +221,15 @@ __global__ void __launch_bounds__(kGradThreads<WARP, LONG>, 1) grad_kernel(const
       }
       return z;
     };
-    auto weighted = [&](int i, Vals z) {
-      if (w_at) {
-        const Vals w = load_columns(w_at, 256 * i);
+    auto q_of = [&](int i) {
+      if constexpr (HOLD) {
+        Vals z = of[i];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) z.v[j] = mul2(z.v[j], w.v[j]);
+        for (int j = 0; j < 4; ++j) z.v[j] = mul2(z.v[j], gw[i].v[j]);
+        return z;
+      } else {
+        return weighted(i, gated(i));
       }
-      return z;
     };
     if (!normed) {
 #pragma unroll
@@ -205,9 +251,6 @@ __global__ void __launch_bounds__(kGradThreads<WARP, LONG>, 1) grad_kernel(const
       out += v_step;
       continue;
     }
-    // q is kept where registers hold it (else its factors come from the L1 cache again)
-    constexpr bool kKeep = !GATE && !BIAS && !VF;
-    Vals q[kKeep ? V : 1];
     float (&shared)[2][kPart] = part[r & 1];
     float2 s, qmean = both(0.f);
     if (layer) {
@@ -215,7 +258,7 @@ __global__ void __launch_bounds__(kGradThreads<WARP, LONG>, 1) grad_kernel(const
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (at.in(i)) {
-          const Vals z = weighted(i, gated(i));
+          const Vals z = q_of(i);
 #pragma unroll
           for (int j = 0; j < 4; ++j) sv = add2(sv, c[i].v[j]), sq = add2(sq, z.v[j]);
         }
@@ -231,13 +274,12 @@ __global__ void __launch_bounds__(kGradThreads<WARP, LONG>, 1) grad_kernel(const
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (at.in(i)) {
-        const Vals z = weighted(i, gated(i));
+        const Vals z = q_of(i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           sv = __ffma2_rn(c[i].v[j], c[i].v[j], sv);
           sq = __ffma2_rn(z.v[j], c[i].v[j], sq);
         }
-        if constexpr (kKeep) q[i] = z;
       }
     Raw<VF> res[LEAVE ? 1 : V];   // on its way during the reduction
     if constexpr (!LEAVE) {
@@ -254,19 +296,18 @@ __global__ void __launch_bounds__(kGradThreads<WARP, LONG>, 1) grad_kernel(const
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if (!at.in(i)) continue;
-      const Vals z = gated(i);
-      Vals o;
-      if constexpr (kKeep) o = q[i];
-      else o = weighted(i, z);
+      Vals o = q_of(i), z;
+      if constexpr (!(HOLD && GATE)) z = gated(i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 n = mul2(c[i].v[j], fq);   // n scale
         o.v[j] = __ffma2_rn(c[i].v[j], fc, __ffma2_rn(o.v[j], fq, f0));
-        sw[i].v[j] = __ffma2_rn(z.v[j], n, sw[i].v[j]);
+        if constexpr (HOLD && GATE) sg[i].v[j] = __ffma2_rn(of[i].v[j], n, sg[i].v[j]);
+        else sw[i].v[j] = __ffma2_rn(z.v[j], n, sw[i].v[j]);
         if constexpr (BIAS) sb[i].v[j] = add2(sb[i].v[j], z.v[j]);
-        if constexpr (GATE) c[i].v[j] = n;
+        if constexpr (!HOLD) c[i].v[j] = n;
       }
-      if constexpr (GATE) {
+      if constexpr (!HOLD) {
         Vals n = weighted(i, c[i]);
         if (b_at) {
           const Vals b = load_columns(b_at, 256 * i);
@@ -296,7 +337,7 @@ __global__ void __launch_bounds__(kGradThreads<WARP, LONG>, 1) grad_kernel(const
     if constexpr (BIAS) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) sb[i].v[j] = mul2(sb[i].v[j], both(scale));
-      store_sums(p.part_b + to, sb[i]);
+      if (p.part_b) store_sums(p.part_b + to, sb[i]);
     }
   }
 }
@@ -304,18 +345,21 @@ __global__ void __launch_bounds__(kGradThreads<WARP, LONG>, 1) grad_kernel(const
 template <bool LEAVE, bool DF, bool VF, bool BIAS, bool GATE>
 bsmma_status launch_grad_kernel(const GradParams& p, cudaStream_t stream) {
   const int64_t vecs = p.a.H / 8;
-  const unsigned blocks = static_cast<unsigned>(p.workers);
-  cudaError_t e;
-  if (vecs <= 32 * kGradPieces<true>) {
-    e = launch_dependent(grad_kernel<LEAVE, DF, VF, BIAS, GATE, true, false>, dim3((blocks + 3) / 4), dim3(128), 0,
-                         stream, p);
-  } else {
-    constexpr int kWarpVecs = 32 * kGradPieces<false>;
+  const unsigned workers = static_cast<unsigned>(p.workers);
+  auto launch = [&](auto kind) {
+    constexpr RowKind ROW = decltype(kind)::value;
+    constexpr int kWarpVecs = 32 * kGradPieces<ROW>;
     const unsigned threads = static_cast<unsigned>(32 * ((vecs + kWarpVecs - 1) / kWarpVecs));
-    e = launch_dependent(threads <= 512 ? grad_kernel<LEAVE, DF, VF, BIAS, GATE, false, false>
-                                        : grad_kernel<LEAVE, DF, VF, BIAS, GATE, false, true>,
-                         dim3(blocks), dim3(threads), 0, stream, p);
-  }
+    return ROW <= ROW_WARP ? launch_dependent(grad_kernel<LEAVE, DF, VF, BIAS, GATE, ROW>, dim3((workers + 3) / 4),
+                                              dim3(128), 0, stream, p)
+                           : launch_dependent(grad_kernel<LEAVE, DF, VF, BIAS, GATE, ROW>, dim3(workers),
+                                              dim3(threads), 0, stream, p);
+  };
+  const cudaError_t e = vecs <= 32     ? launch(std::integral_constant<RowKind, ROW_WARP_1>{})
+                        : vecs <= 64   ? launch(std::integral_constant<RowKind, ROW_WARP_2>{})
+                        : vecs <= 128  ? launch(std::integral_constant<RowKind, ROW_WARP>{})
+                        : vecs <= 1024 ? launch(std::integral_constant<RowKind, ROW_BLOCK>{})
+                                       : launch(std::integral_constant<RowKind, ROW_LONG>{});
   return cuda_ok(e);
 }
 
@@ -327,7 +371,8 @@ bsmma_status grad_leave_mixed(const GradParams& p, cudaStream_t stream);
 
 template <bool DF, bool VF>
 bsmma_status launch_leave_grad(const GradParams& p, cudaStream_t stream) {
-  const bool bias = p.part_b != nullptr, gate = p.a.dgate != nullptr;
+  // (a bias is part of what the gate's gradient sums)
+  const bool gate = p.a.dgate != nullptr, bias = p.part_b != nullptr || (gate && p.a.norm.bias);
   if (bias && gate) return launch_grad_kernel<true, DF, VF, true, true>(p, stream);
   if (bias) return launch_grad_kernel<true, DF, VF, true, false>(p, stream);
   if (gate) return launch_grad_kernel<true, DF, VF, false, true>(p, stream);
