@@ -763,7 +763,7 @@ bsmma_status make_drop(float p, const int64_t* rng, DropArgs* d) {
 int64_t bounded_rows(int64_t gate_rows, int64_t T) { return gate_rows < T ? gate_rows : T; }
 
 bsmma_status run_grad(const BranchGradArgs& a, bool leave, cudaStream_t s) {
-  if (!a.dweight && !a.dbias && !a.dgate) return launch_branch_grad(a, leave, nullptr, s);
+  if (!a.dweight && !a.dbias && !(a.dgate && a.gate_rows > 1)) return launch_branch_grad(a, leave, nullptr, s);
   const StreamLock lock(s);
   void* ws = nullptr;
   const bsmma_status st = get_workspace(branch_grad_workspace_bytes(a.T, a.H), s, &ws);

@@ -9,11 +9,12 @@ namespace branch {
 namespace {
 
 // Workers: runs of rows, as many as fill the GPU's 152 SMs with the blocks that fit one (by
-// registers), fewer rows each for shorter rows.  A number of T and H alone, so that the sums' order,
+// registers; at most two of them, 46479 rows of 1136 in BF16 took 181 us for 94).  A number of T and H alone, so that the sums' order,
 // and with it every bit, is the same wherever the call runs.
 int workers_of(int64_t T, int64_t H) {
   const int64_t vecs = H / 8;
-  const int64_t most = vecs <= 128 ? 152 * 16 : vecs <= 512 ? 152 * 2 : 152;
+  const int64_t warps = (vecs + 63) / 64;   // of a block; 16 with 128 registers a thread fit an SM
+  const int64_t most = 152 * (vecs <= 128 ? 16 : std::max<int64_t>(16 / warps, 1));
   return static_cast<int>(std::min(T, most));
 }
 
@@ -110,7 +111,7 @@ bsmma_status launch_branch_grad(const BranchGradArgs& a, bool leave, void* works
   const int64_t plane = a.H * p.workers;
   if (a.dweight) p.part_w = ws;
   if (a.dbias) p.part_b = ws + plane;
-  if (a.dgate) p.part_g = ws + 2 * plane;
+  if (a.dgate && a.gate_rows > 1) p.part_g = ws + 2 * plane;
   bsmma_status st;
   if (!leave) st = grad_enter(p, stream);
   else if (!a.d_f32) st = grad_leave_bf16(p, stream);

@@ -97,7 +97,9 @@ __global__ void __launch_bounds__(kGradThreads<ROW>, 1) grad_kernel(const GradPa
   const char* res_at = !LEAVE && a.dres ? static_cast<const char*>(a.dres) + first * (VF ? 4 : 2) : nullptr;
   char* dx_at = LEAVE && a.dx ? static_cast<char*>(a.dx) + first * (DF ? 4 : 2) : nullptr;
   const float* w_at = a.norm.weight ? a.norm.weight + 8 * at.base : nullptr;
-  const float* b_at = GATE && a.norm.bias ? a.norm.bias + 8 * at.base : nullptr;
+  const float* b_at = LEAVE && a.dgate && a.norm.bias ? a.norm.bias + 8 * at.base : nullptr;
+  // a gate for each row (never with GATE): its gradient is a row
+  float* dgate_at = LEAVE && !GATE && a.dgate ? a.dgate + first : nullptr;
   const __nv_bfloat16* gate_bf16 = nullptr;   // the gate's row, in its type
   const float* gate_f32 = nullptr;
   auto gate_piece = [&](int i) {
@@ -117,7 +119,21 @@ __global__ void __launch_bounds__(kGradThreads<ROW>, 1) grad_kernel(const GradPa
   // a gate's rows, or for all.  With a gate's gradient sg is then the sum of d n, which over a
   // gate's rows gives dgate, times the weight, and its part of dweight, times the gate.  (Taken from the L1
   // cache for every row: 20000 rows of 5120 with dropout and a gate for 2048 of them 221 us, and 172.)
-  constexpr bool HOLD = !LONG && !(BIAS && (GATE || VF));
+  constexpr bool HOLD = !LONG && !(BIAS && VF && !GATE);
+  // With a bias there is the sum of d too, in sw's place; the parts of dweight and dbias are then added to
+  // the worker's sums in memory after each gate's rows.
+  constexpr bool OUT = HOLD && GATE && BIAS;
+  bool fresh = true;   // nothing is there yet
+  auto add_sums = [&](float* to, Vals f) {
+    if (!to) return;
+    to += static_cast<int64_t>(worker) * a.H;
+    if (!fresh) {
+      const Vals more = load_columns(to, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f.v[j] = add2(f.v[j], more.v[j]);
+    }
+    store_sums(to, f);
+  };
   Vals gw[HOLD ? V : 1];
   auto flush_gate = [&] {
     if constexpr (GATE) {
@@ -134,14 +150,33 @@ __global__ void __launch_bounds__(kGradThreads<ROW>, 1) grad_kernel(const GradPa
         if (at.in(i)) {
           if (HOLD && normed) {
             const Vals one = gate_piece(i);
+            if constexpr (OUT) {
+              Vals dw, db;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sw[i].v[j] = __ffma2_rn(one.v[j], sg[i].v[j], sw[i].v[j]);
+              for (int j = 0; j < 4; ++j) {
+                sw[i].v[j] = mul2(sw[i].v[j], both(scale));
+                dw.v[j] = mul2(one.v[j], sg[i].v[j]);
+                db.v[j] = mul2(one.v[j], sw[i].v[j]);
+              }
+              add_sums(p.part_w ? p.part_w + 8 * at.at(i) : nullptr, dw);
+              add_sums(p.part_b ? p.part_b + 8 * at.at(i) : nullptr, db);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) sw[i].v[j] = __ffma2_rn(one.v[j], sg[i].v[j], sw[i].v[j]);
+            }
             sg[i] = weighted(i, sg[i]);
+            if (OUT && b_at) {
+              const Vals b = load_columns(b_at, 256 * i);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) sg[i].v[j] = __ffma2_rn(b.v[j], sw[i].v[j], sg[i].v[j]);
+            }
           }
           store_sums(to + 8 * at.at(i), sg[i]);
         }
         sg[i] = none;
+        if constexpr (OUT) sw[i] = none;
       }
+      fresh = false;
     }
   };
 
@@ -149,43 +184,68 @@ __global__ void __launch_bounds__(kGradThreads<ROW>, 1) grad_kernel(const GradPa
   Raw<DF> next_d[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) next_v[i] = zero_raw<VF>(), next_d[i] = zero_raw<DF>();
-  auto fetch = [&] {
+  // Without sums of a gate's rows the gate may be another for each: it is fetched with the row (15000 x
+  // 7168, a gate a row, 272 us, and 356 when it is read at the row's turn) where registers allow.
+  constexpr bool AHEAD = LEAVE && !GATE && HOLD && !VF;
+  const bool each = LEAVE && !GATE && a.gate;
+  Raw<VF> next_g[AHEAD ? V : 1];
+  auto gate_at = [&](int64_t row) {
+    if constexpr (VF) gate_f32 = static_cast<const float*>(a.gate) + row * a.H + 8 * at.base;
+    else gate_bf16 = static_cast<const __nv_bfloat16*>(a.gate) + row * a.H + 8 * at.base;
+  };
+  auto gate_of = [&](int64_t r) {
+    return static_cast<int64_t>(static_cast<uint32_t>(r) / static_cast<uint32_t>(a.gate_rows)) * a.H + 8 * at.base;
+  };
+  auto fetch = [&](int64_t r) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (at.in(i)) {
         next_v[i] = load_raw<VF>(v_at, 256 * i);
         next_d[i] = load_raw<DF>(d_at, 256 * i);
       }
-  };
-  // the factors of a gate's rows (no gate: of all rows)
-  auto use_gate = [&](int64_t row) {
-    const bool gates = LEAVE && (GATE || a.gate);
-    if (gates) {
-      if constexpr (VF) gate_f32 = static_cast<const float*>(a.gate) + row * a.H + 8 * at.base;
-      else gate_bf16 = static_cast<const __nv_bfloat16*>(a.gate) + row * a.H + 8 * at.base;
+    if constexpr (AHEAD) {
+      if (each) {
+        const int64_t from = gate_of(r);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (at.in(i)) next_g[i] = load_raw<VF>(a.gate, from + 256 * i);
+      }
     }
+  };
+  // the factors of a gate's rows, of a row with its own (fetched), or of all
+  auto use_gate = [&] {
     if constexpr (HOLD) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         gw[i] = Vals{{both(1.f), both(1.f), both(1.f), both(1.f)}};
         if (!at.in(i)) continue;
-        if (gates) gw[i] = gate_piece(i);
+        if constexpr (GATE) gw[i] = gate_piece(i);
+        else if constexpr (LEAVE) {
+          if constexpr (AHEAD) {
+            if (each) gw[i] = widen<VF>(next_g[i]);
+          } else {
+            if (each) gw[i] = gate_piece(i);
+          }
+        }
         gw[i] = weighted(i, gw[i]);
       }
     }
   };
-  if (r0 < r1) fetch();
-  use_gate(GATE ? g : 0);
+  if (r0 < r1) fetch(r0);
+  if (GATE) gate_at(g);
+  use_gate();
   for (int64_t r = r0; r < r1; ++r) {
     if constexpr (GATE) {
       if (r == g_end) {
         flush_gate();
         ++g;
         g_end += a.gate_rows;
-        use_gate(g);
+        gate_at(g);
+        use_gate();
       }
-    } else if (LEAVE && a.gate) {
-      use_gate(static_cast<uint32_t>(r) / static_cast<uint32_t>(a.gate_rows));
+    } else if (each) {
+      gate_at(static_cast<uint32_t>(r) / static_cast<uint32_t>(a.gate_rows));
+      use_gate();
     }
     Vals c[V], of[V];   // the rows, later less their mean; d, without what was dropped
 #pragma unroll
@@ -195,7 +255,7 @@ __global__ void __launch_bounds__(kGradThreads<ROW>, 1) grad_kernel(const GradPa
     }
     v_at += v_step;
     d_at += d_step;
-    if (r + 1 < r1) fetch();
+    if (r + 1 < r1) fetch(r + 1);
     if (LEAVE && dx_at) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -236,12 +296,19 @@ __global__ void __launch_bounds__(kGradThreads<ROW>, 1) grad_kernel(const GradPa
       for (int i = 0; i < V; ++i) {
         if (!at.in(i)) continue;
         Vals z = gated(i);
-        if constexpr (GATE) {
+        if (LEAVE && (GATE || dgate_at)) {
           // a dropped value (of is 0) adds nothing to the gate's sum, whatever it is
+          Vals u;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 u = make_float2(of[i].v[j].x == 0.f ? 0.f : c[i].v[j].x, of[i].v[j].y == 0.f ? 0.f : c[i].v[j].y);
-            sg[i].v[j] = __ffma2_rn(of[i].v[j], u, sg[i].v[j]);
+          for (int j = 0; j < 4; ++j)
+            u.v[j] = make_float2(of[i].v[j].x == 0.f ? 0.f : c[i].v[j].x, of[i].v[j].y == 0.f ? 0.f : c[i].v[j].y);
+          if constexpr (GATE) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sg[i].v[j] = __ffma2_rn(of[i].v[j], u.v[j], sg[i].v[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u.v[j] = mul2(mul2(of[i].v[j], u.v[j]), both(scale));
+            store_sums(dgate_at + 256 * i, u);
           }
         }
 #pragma unroll
@@ -249,6 +316,7 @@ __global__ void __launch_bounds__(kGradThreads<ROW>, 1) grad_kernel(const GradPa
         store_raw<VF>(dv_at + out, 256 * i, narrow<VF>(z));
       }
       out += v_step;
+      if (LEAVE && !GATE && dgate_at) dgate_at += a.H;
       continue;
     }
     float (&shared)[2][kPart] = part[r & 1];
@@ -304,10 +372,11 @@ __global__ void __launch_bounds__(kGradThreads<ROW>, 1) grad_kernel(const GradPa
         o.v[j] = __ffma2_rn(c[i].v[j], fc, __ffma2_rn(o.v[j], fq, f0));
         if constexpr (HOLD && GATE) sg[i].v[j] = __ffma2_rn(of[i].v[j], n, sg[i].v[j]);
         else sw[i].v[j] = __ffma2_rn(z.v[j], n, sw[i].v[j]);
-        if constexpr (BIAS) sb[i].v[j] = add2(sb[i].v[j], z.v[j]);
-        if constexpr (!HOLD) c[i].v[j] = n;
+        if constexpr (OUT) sw[i].v[j] = add2(sw[i].v[j], of[i].v[j]);
+        else if constexpr (BIAS) sb[i].v[j] = add2(sb[i].v[j], z.v[j]);
+        if constexpr (!HOLD && GATE) c[i].v[j] = n;
       }
-      if constexpr (!HOLD) {
+      if constexpr (!HOLD && GATE) {
         Vals n = weighted(i, c[i]);
         if (b_at) {
           const Vals b = load_columns(b_at, 256 * i);
@@ -316,6 +385,20 @@ __global__ void __launch_bounds__(kGradThreads<ROW>, 1) grad_kernel(const GradPa
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) sg[i].v[j] = __ffma2_rn(of[i].v[j], n.v[j], sg[i].v[j]);
+      }
+      if (LEAVE && !GATE && dgate_at) {
+        Vals n;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) n.v[j] = mul2(c[i].v[j], fq);
+        n = weighted(i, n);
+        if (b_at) {
+          const Vals b = load_columns(b_at, 256 * i);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) n.v[j] = __ffma2_rn(b.v[j], both(scale), n.v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) n.v[j] = mul2(of[i].v[j], n.v[j]);
+        store_sums(dgate_at + 256 * i, n);
       }
       if constexpr (!LEAVE) {
         if (res_at) {
@@ -327,8 +410,10 @@ __global__ void __launch_bounds__(kGradThreads<ROW>, 1) grad_kernel(const GradPa
       store_raw<VF>(dv_at + out, 256 * i, narrow<VF>(o));
     }
     out += v_step;
+    if (LEAVE && !GATE && dgate_at) dgate_at += a.H;
   }
   flush_gate();
+  if constexpr (OUT) return;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     if (!at.in(i)) continue;
@@ -371,8 +456,8 @@ bsmma_status grad_leave_mixed(const GradParams& p, cudaStream_t stream);
 
 template <bool DF, bool VF>
 bsmma_status launch_leave_grad(const GradParams& p, cudaStream_t stream) {
-  // (a bias is part of what the gate's gradient sums)
-  const bool gate = p.a.dgate != nullptr, bias = p.part_b != nullptr || (gate && p.a.norm.bias);
+  // a gate for each row has no sums; where it has, a bias is part of them
+  const bool gate = p.a.dgate != nullptr && p.a.gate_rows > 1, bias = p.part_b != nullptr || (gate && p.a.norm.bias);
   if (bias && gate) return launch_grad_kernel<true, DF, VF, true, true>(p, stream);
   if (bias) return launch_grad_kernel<true, DF, VF, true, false>(p, stream);
   if (gate) return launch_grad_kernel<true, DF, VF, false, true>(p, stream);

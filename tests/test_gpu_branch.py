@@ -75,7 +75,7 @@ def normed_size(v, kind, weight, bias, eps=1e-6):
 
 
 SIZES = [(1, 8), (3, 264), (6, 1024), (5, 1032), (33, 4096), (2, 4104), (9, 7168), (4, 8200), (3, 16384),
-         (700, 520)]
+         (700, 520), (2500, 192), (1300, 408)]
 
 
 @pytest.mark.parametrize("T,H", SIZES)
@@ -140,6 +140,12 @@ LEAVES = [
     (1000, 2048, "layer", 300, 0.75, 0.5, 0.1),
     (5000, 264, "none", 2, 1.0, 1.0, 0.1),
     (700, 7168, "rms", 650, 1.0, 1.0, 0.1),
+    (600, 104, "layer", 7, 1.0, 0.5, 0.1),
+    (2600, 256, "layer", 1, 1.0, 0.5, 0.1),
+    (900, 480, "layer", 350, 0.75, 1.0, 0.2),
+    (3000, 72, "rms", 1000, 1.0, 1.0, 0.0),
+    (800, 2992, "layer", 1, 1.0, 1.0, 0.1),
+    (500, 6144, "layer", 170, 1.0, 0.5, 0.1),
 ]
 
 
@@ -207,6 +213,28 @@ def test_leave_backward(T, H, kind, gate_rows, xs, ys, p, dtype, ydtype):
     again = call()
     for a, e in zip(again, (dy, dx, dw, db, dgate)):
         assert (a is None and e is None) or torch.equal(a, e)
+
+
+@pytest.mark.parametrize("T,H,gate_rows", [(40, 192, 7), (300, 1040, 1), (300, 4096, 130), (20, 8224, 3)])
+def test_a_gates_gradient_alone(T, H, gate_rows):
+    """A sum that is not wanted changes no other."""
+    c = leave_case(torch.Generator().manual_seed(T + H), T, H, "bf16", "bf16", "layer", gate_rows, 0.1)
+    dout, y, w, b, gate, rng = (dev(c[k]) for k in ("x", "y", "w", "b", "gate", "rng"))
+    dy, dx, dw, db, dgate = bs.branch_leave_backward(dout, y, w, b, norm="layer", gate=gate, gate_rows=gate_rows,
+                                                     x_scale=0.5, y_scale=0.5, p=0.1, rng=rng)
+    for keep in ((), (2,), (3,), (4,), (2, 3), (2, 4), (3, 4)):
+        raw = [guarded(t.shape, t.dtype) for t in (dy, dx, dw, db, dgate)]
+        ptr = lambda t: t.data_ptr()  # noqa: E731
+        got = [r[1] if i < 2 or i in keep else None for i, r in enumerate(raw)]
+        status = bs.load().branch_leave_backward(
+            ptr(dout), 0, ptr(y), 0, T, H, 2, 1e-6, ptr(w), ptr(b), ptr(gate), gate_rows, 0.5, 0.5, 0.1, ptr(rng),
+            *(None if t is None else ptr(t) for t in got), torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert status == 0
+        for t, e, r in zip(got, (dy, dx, dw, db, dgate), raw):
+            assert intact(r[0])
+            if t is not None:   # (a kernel for fewer sums may round another way)
+                near(t, e.double().cpu(), 2.0 ** -14 * e.double().cpu().abs().amax(), t.dtype)
 
 
 @pytest.mark.parametrize("T,H", SIZES + [(1000, 1024), (900, 4096), (500, 7168), (400, 16384)])
