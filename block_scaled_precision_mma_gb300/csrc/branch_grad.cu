@@ -9,8 +9,8 @@ namespace branch {
 namespace {
 
 // Workers: runs of rows, as many as fill the GPU's 152 SMs with the blocks that fit one (by
-// registers; at most two of them, 46479 rows of 1136 in BF16 took 181 us for 94).  A number of T and H alone, so that the sums' order,
-// and with it every bit, is the same wherever the call runs.
+// registers; at most two of them, 46479 rows of 1136 in BF16 took 181 us for 94).  A number of T and
+// H alone, so that the sums' order, and with it every bit, is the same wherever the call runs.
 int workers_of(int64_t T, int64_t H) {
   const int64_t vecs = H / 8;
   const int64_t warps = (vecs + 63) / 64;   // of a block; 16 with 128 registers a thread fit an SM
@@ -18,7 +18,6 @@ int workers_of(int64_t T, int64_t H) {
   return static_cast<int>(std::min(T, most));
 }
 
-// The workers' sums of 32 columns, added by LANES threads a column, each a run of workers.
 // The worker that has a row: the last one whose first row is not after it.
 __device__ __forceinline__ int worker_of(int64_t T, int workers, int64_t row) {
   return static_cast<int>(((row + 1) * workers - 1) / T);
@@ -30,6 +29,7 @@ struct SumParams {
   int workers, fixed;   // fixed: blockIdx.y below it are dweight and dbias
   bool by_worker;
 };
+// The workers' sums of 32 columns, added by LANES threads a column, each a run of workers.
 template <int LANES>
 __global__ void __launch_bounds__(32 * LANES) sum_kernel(const SumParams p) {
   __shared__ float part[LANES][32];
