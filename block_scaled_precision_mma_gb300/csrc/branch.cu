@@ -212,12 +212,13 @@ __device__ __forceinline__ int64_t row_of() {
 // Rows of up to 8192 values: at most 256 threads, registers for three or four blocks an SM.
 constexpr int kMaxThreads = 512, kShortThreads = 256;
 
-// A row a block (a warp), in registers.  16384 x 7168 BF16 into E4M3: 80 us, 356 MB at 4.4 TB/s, bound by
+// A row a block (a warp), in registers.  16384 x 7168 BF16 into E4M3: 76 us, 356 MB at 4.7 TB/s, bound by
 // issuing (64% of the slots: 120 instructions for eight values, 40 of them what a row costs each
 // of its warps) and by the weights' loads (57% of the L1 cache's cycles); FP32 into BF16 16384 x 4096
-// 70 us, 403 MB at 5.7 TB/s.  Tried and slower: two rows a block that share the weights (87 us, 14
-// warps an SM), and rows in a ring of asynchronous copies, one (78) or two (86) at a time, which
-// widen the values anew in each pass.
+// 69 us, 403 MB at 5.8 TB/s.  Tried and slower: two pieces a thread (twice the warps, each with a row's
+// costs: 104 us, and a step with dropout, gate and two norms 208 for 179), two rows a block that share
+// the weights (87 us, 14 warps an SM), and rows in a ring of asynchronous copies, one (78) or two (86)
+// at a time, which widen the values anew in each pass.
 template <bool F32, bool WARP, bool SHORT, int V>
 __global__ void __launch_bounds__(SHORT ? kShortThreads : kMaxThreads, SHORT ? 4 : 2) enter_kernel(const EnterArgs p) {
   __shared__ float part[WARP ? 1 : 3 * 32];
