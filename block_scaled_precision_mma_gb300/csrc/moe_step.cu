@@ -514,10 +514,10 @@ struct Walk {
 __host__ __device__ constexpr int64_t power_stride(int64_t F) { return (F + 127) / 128 * 4; }
 
 // The inner rows.  A unit is 16 inner columns for each of kWarps / G parts; warp w has part w % (16 / G)
-// and every G-th stage of K from w / (16 / G) on.  One more warp adds the sums up and finishes a unit
-// while the others are at the next (done by one of theirs, the other fifteen waited for it a quarter
-// of their time).
-constexpr int kInThreads = kThreads + 32;
+// and every G-th stage of K from w / (16 / G) on.  More warps, one for each eight columns and 32 inner
+// values, at most four, add the sums up and finish a unit while the others are at the next (done by one of
+// theirs, the other fifteen waited for it a quarter of their time; with one for all of a unit 32 tokens,
+// 32 experts of 2048 x 2048 in INT8 took 77 us for 69).
 template <int FORM, int NT, int G>
 struct InCfg {
   static constexpr int kParts = kWarps / G, kTile = 16 * kParts;   // a unit's parts and inner columns
@@ -528,10 +528,12 @@ struct InCfg {
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kBytes = kRing + kFixed;
   static_assert(kStages >= 2, "one stage in flight");
+  static constexpr int kEnds = kTile / 32 * NT < 4 ? kTile / 32 * NT : 4;   // warps that finish units
+  static constexpr int kThreadsIn = kThreads + 32 * kEnds;
 };
 
 template <int FORM, int NT, int G>
-__global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a) {
+__global__ void __launch_bounds__(InCfg<FORM, NT, G>::kThreadsIn, 1) step_in_kernel(const StepArgs a) {
   using C = InCfg<FORM, NT, G>;
   using F = Form<FORM>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
   Table& table = *reinterpret_cast<Table*>(smem + C::kRing + C::kSums + 32);
   if (threadIdx.x == 0) {
     mbar_init(full, kWarps);
-    mbar_init(empty, 1);
+    mbar_init(empty, C::kEnds);
     fence_mbar_init();
     *abort = 0;
   }
@@ -571,27 +573,43 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
     const int64_t f = static_cast<int64_t>(rows) * C::kTile + 16 * part;
     return f < a.F ? f : 0;
   };
-  if (warp == kWarps) {
+  if (warp >= kWarps) {
     if constexpr (!F::kBf16) grid_dependency_wait();
+    // What a unit's end needs beside the sums is asked for before them: lane t has the power of token t,
+    // and the rows' INT8 scales are read ahead of the wait (read after it: 32 tokens, 32 experts of
+    // 2048 x 2048 96 us for 77).
+    const float powers = !F::kBf16 && lane < a.T ? a.x_power[lane] : 1.f;
+    constexpr bool AHEAD = FORM == BSMMA_OPERAND_INT8 && C::kTile == 32;
+    float row_scales[2][4];   // of the gate's rows and the up's
     int done = 0;
     Walk here;
     for (bool more = here.begin(table, blockIdx.x, tiles); more; more = here.forward(table, step, tiles), ++done) {
       const int entry = here.entry(), rows = here.rows();
       const int first = table.first[entry], count = table.first[entry + 1] - first;
       const int64_t expert = table.expert[entry];
+      auto load_scales = [&](int64_t f0) {
+        const float* of = static_cast<const float*>(a.s_in) + expert * 2 * a.F;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const int64_t f = f0 + 8 * m + g;
+          row_scales[0][m] = f < a.F ? of[f] : 0.f, row_scales[1][m] = f < a.F ? of[a.F + f] : 0.f;
+        }
+      };
+      if constexpr (AHEAD) load_scales(static_cast<int64_t>(rows) * C::kTile);
       if (!mbar_wait(full, done & 1, a.limit_ns, abort, a.status)) return;
       // eight columns and 32 inner values at a time: values 8 m + g of columns 2 t and 2 t + 1
-      for (int qn = 0; qn < C::kTile / 32 * ((count + 7) / 8); ++qn) {
+      for (int qn = warp - kWarps; qn < C::kTile / 32 * ((count + 7) / 8); qn += C::kEnds) {
         const int q = qn % (C::kTile / 32), n = qn / (C::kTile / 32);
         const int64_t f0 = static_cast<int64_t>(rows) * C::kTile + 32 * q;
         if (f0 >= a.F) continue;
+        if constexpr (FORM == BSMMA_OPERAND_INT8 && !AHEAD) load_scales(f0);
         int64_t slots[2];
         float power[2] = {1.f, 1.f};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int col = 8 * n + 2 * t + c;
           slots[c] = col < count ? table.slot[first + col] : -1;
-          if (!F::kBf16 && slots[c] >= 0) power[c] = a.x_power[table.token[first + col]];
+          if constexpr (!F::kBf16) power[c] = __shfl_sync(kFull, powers, table.token[first + min(col, count - 1)]);
         }
         float v[2][4], amax[2] = {0.f, 0.f};
 #pragma unroll
@@ -604,9 +622,8 @@ __global__ void __launch_bounds__(kInThreads, 1) step_in_kernel(const StepArgs a
           }
           const int64_t f = f0 + 8 * m + g;
           if constexpr (FORM == BSMMA_OPERAND_INT8) {
-            const float* of = static_cast<const float*>(a.s_in) + expert * 2 * a.F;
-            const float sg = f < a.F ? of[f] : 0.f, su = f < a.F ? of[a.F + f] : 0.f;
-            s.x *= sg, s.y *= sg, s.z *= su, s.w *= su;
+            s.x *= row_scales[0][m], s.y *= row_scales[0][m];
+            s.z *= row_scales[1][m], s.w *= row_scales[1][m];
           }
           v[0][m] = activate(s.x * power[0], a.act) * (s.z * power[0]);
           v[1][m] = activate(s.y * power[1], a.act) * (s.w * power[1]);
@@ -958,7 +975,7 @@ bsmma_status launch_in(const StepArgs& a, const DeviceInfo* dev, cudaStream_t st
   const int64_t units = a.T * a.k * ((a.F + C::kTile - 1) / C::kTile);
   return cuda_ok(launch_dependent(step_in_kernel<FORM, NT, G>,
                                   dim3(static_cast<unsigned>(std::min<int64_t>(units, dev->sm_count))),
-                                  dim3(kInThreads), C::kBytes, stream, a));
+                                  dim3(C::kThreadsIn), C::kBytes, stream, a));
 }
 
 template <int FORM, int NT>
@@ -972,14 +989,14 @@ bsmma_status launch_step(StepArgs a, const DeviceInfo* dev, cudaStream_t stream)
     count_launches(1);
   }
   // K over eight groups of warps where that leaves each three stages of a unit or more; short rows over
-  // two, in units of four times the columns (what a unit costs beside its stages, and the groups'
-  // unequal shares: 29 tokens, 63 experts of 8640 x 544 in E5M2 389 and 320 us), as long as those are
-  // units enough to share them evenly (three or four for an SM were slower: 18 tokens, 14 experts of
-  // 4720 x 432 in INT8 65 and 74 us): no more experts than E or slots are chosen
+  // two, in units of four times the columns (what a unit costs beside its stages, and the groups' unequal
+  // shares: 29 tokens, 63 experts of 8640 x 544 in E5M2 392 and 288 us; 18 tokens, 14 experts of 4720 x
+  // 432 in INT8 69 and 54), as long as those are two for an SM or more: no more experts than E or slots
+  // are chosen
   using F = Form<FORM>;
   const int64_t stages = (a.H + F::kStageK - 1) / F::kStageK;
   const int64_t wide_units = std::min<int64_t>(a.E, a.T * a.k) * ((a.F + 127) / 128);
-  bsmma_status st = stages < 24 && wide_units >= 8 * dev->sm_count ? launch_in<FORM, NT, 2>(a, dev, stream)
+  bsmma_status st = stages < 24 && wide_units >= 2 * dev->sm_count ? launch_in<FORM, NT, 2>(a, dev, stream)
                                                                    : launch_in<FORM, NT, 8>(a, dev, stream);
   if (st == BSMMA_OK) st = launch_out<FORM, NT>(a, dev, stream);
   count_launches(2);
