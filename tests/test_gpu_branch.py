@@ -314,6 +314,39 @@ def test_dropout_is_the_branchs():
     assert abs(share - drop) < 5 * (drop * (1 - drop) / (T * H)) ** 0.5
 
 
+def test_rows_past_32_bits_of_values():
+    """The last rows of more than 2^31 values give what they give by themselves."""
+    T, H, n = 270000, 8192, 5
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x, y = (torch.empty(T, H, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    x.normal_(generator=g), y.normal_(generator=g)
+    w = torch.randn(H, generator=g, device="cuda")
+    gate = torch.randn(2, H, generator=g, device="cuda").bfloat16()
+    rows_ = T - 1000    # of the first gate
+    form = dict(norm="layer", x_scale=0.75, y_scale=0.5)
+    codes, scales = bs.branch_enter(x, w, fmt="e4m3")
+    want = bs.branch_enter(x[-n:].contiguous(), w, fmt="e4m3")
+    assert torch.equal(codes[-n:], want[0]) and torch.equal(scales[-n:], want[1])
+    out, h = bs.branch_leave(x, y, w, w, gate=gate, gate_rows=rows_, next_norm="rms", next_weight=w, **form)
+    want = bs.branch_leave(x[-n:].contiguous(), y[-n:].contiguous(), w, w, gate=gate[1:], gate_rows=n, next_norm="rms",
+                           next_weight=w, **form)
+    assert torch.equal(out[-n:], want[0]) and torch.equal(h[-n:], want[1])
+    dy, dx, dw, db, dgate = bs.branch_leave_backward(x, y, w, w, gate=gate, gate_rows=rows_, **form)
+    want = bs.branch_leave_backward(x[-n:].contiguous(), y[-n:].contiguous(), w, w, gate=gate[1:], gate_rows=n, **form)
+    assert torch.equal(dy[-n:], want[0]) and torch.equal(dx[-n:], want[1])
+    # the second gate's rows by themselves: other runs of rows, so only as near as the sums are
+    part = bs.branch_leave_backward(x[rows_:].contiguous(), y[rows_:].contiguous(), w, w, gate=gate[1:], gate_rows=T,
+                                    **form)[4]
+    near(dgate[1:], part.cpu(), 2.0 ** -14 * 1000 ** 0.5 * part.cpu().abs().amax(), torch.float32)
+    del codes, scales, h, dy, dx
+    rng = torch.tensor([3, 5], device="cuda")
+    kept = bs.branch_leave(x, y, p=0.25, rng=rng, x_scale=0.0)
+    assert torch.equal(kept.view(-1)[-n * H:], bs.dropout(y, 0.25, rng).view(-1)[-n * H:])
+    assert abs((kept[-n:] == 0).float().mean().item() - 0.25) < 0.02
+    # another row has another mask
+    assert not torch.equal(kept[-1] == 0, kept[T - 1 - (1 << 32) // H // 2] == 0)
+
+
 def test_special_values_stay_in_their_rows():
     """Infinities and NaN: a dropped one is 0, a kept one is the row's own matter."""
     T, H = 6, 1024

@@ -126,6 +126,40 @@ def test_long_rows():
         check(run(c, fmt), c, fmt)
 
 
+@pytest.mark.parametrize("fmt,H,F", [("bf16", 65536, 8), ("bf16", 8, 65536), ("int8", 65536, 16), ("int8", 16, 65536),
+                                     ("e4m3", 65536, 32), ("e5m2", 32, 65536), ("e2m1", 65536, 32)])
+def test_longest_rows(fmt, H, F):
+    c = case(H % 1000 + F, 2, 2, 1, H, F, fmt)
+    check(run(c, fmt), c, fmt)
+
+
+@pytest.mark.parametrize("T,E,k", [(32, 64, 32), (1, 1024, 1024), (32, 1024, 32)])
+def test_most_choices(T, E, k):
+    c = case(T + E, T, E, k, 32, 32, "int8")
+    check(run(c, "int8"), c, "int8")
+
+
+def test_weights_past_32_bits_of_bytes():
+    """The last expert of more than 2^32 bytes gives what it gives as one of two."""
+    E, H, F = 700, 8192, 512
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda *s: torch.randint(-127, 128, s, generator=g, device="cuda", dtype=torch.int8)  # noqa: E731
+    w_in, w_out = rnd(2, 2 * F, H), rnd(2, H, F)
+    s_in, s_out = (torch.rand(s, generator=g, device="cuda") / 1024 for s in ((2, 2 * F), (2, H)))
+    x = torch.randn(3, H, generator=g, device="cuda").bfloat16()
+    ids = torch.tensor([[0, 1], [1, -1], [1, 0]], device="cuda", dtype=torch.int32)
+    weights = torch.rand(3, 2, generator=g, device="cuda")
+    want = bs.moe_step(x, ids, weights, w_in, w_out, s_in, s_out, fmt="int8")
+    many = []
+    for t in (w_in, w_out, s_in, s_out):
+        all_ = torch.zeros((E,) + t.shape[1:], dtype=t.dtype, device="cuda")
+        all_[3], all_[E - 1] = t[0], t[1]
+        many.append(all_)
+    assert many[0].numel() > 1 << 32
+    ids = torch.where(ids == 0, 3, torch.where(ids == 1, E - 1, ids))
+    assert torch.equal(bs.moe_step(x, ids, weights, *many, fmt="int8"), want) and want.isfinite().all() and want.any()
+
+
 def test_same_expert_twice_and_no_expert():
     """A token that names an expert twice, one whose choices are all dropped, and every token on one
     expert (more columns than a tile)."""
