@@ -232,8 +232,8 @@ __global__ void __launch_bounds__(kGradThreads<ROW>, 1) grad_kernel(const GradPa
     }
   };
   if (r0 < r1) fetch(r0);
-  if (GATE) gate_at(g);
-  use_gate();
+  if constexpr (GATE) gate_at(g);
+  if (!each) use_gate();   // (a gate for each row: at its row's turn, when gate_at() has been there)
   for (int64_t r = r0; r < r1; ++r) {
     if constexpr (GATE) {
       if (r == g_end) {
