@@ -84,8 +84,8 @@ __global__ void __launch_bounds__(32 * LANES) sum_kernel(const SumParams p) {
 
 template <bool DF, bool VF>
 bsmma_status launch_enter_grad(const GradParams& p, cudaStream_t stream) {
-  return p.part_b ? launch_grad_kernel<false, DF, VF, true, false>(p, stream)
-                  : launch_grad_kernel<false, DF, VF, false, false>(p, stream);
+  return p.part_b ? launch_grad_kernel<false, DF, VF, true, true, false>(p, stream)
+                  : launch_grad_kernel<false, DF, VF, true, false, false>(p, stream);
 }
 
 }  // namespace

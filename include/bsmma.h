@@ -581,7 +581,8 @@ int64_t moe_step_workspace_bytes(int64_t T, int k, int64_t H, int64_t F);
  *   multiplied by 1 / (1 - p) of the rounded p.  Value i of the tensor (row-major) is kept or not by 16
  *   bits of Philox4x32-10, counter (i / 8 as two words, offset as two words), key the seed's
  *   two words, words in order, low halves first: the mask is made again wherever it is needed
- *   and never stored.  A dropped value is 0, whatever it was.
+ *   and never stored.  A dropped value is 0, whatever it was, and adds nothing to the sums of
+ *   dweight, dbias and dgate (weight and bias finite).
  * A row to write as a product's operand (form): BF16, FP32 (FP32 streams), or codes of the
  *   FP32 values with the rules of int8_quantize (codes int8 [T][H], scales FP32 [T]) and of
  *   mx_quantize, rowwise (codes [T][H], E2M1 [T][H/2]; scales E8M0 uint8 [T][H/32]).
