@@ -12,6 +12,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cstdint>
 
 #include "bsmma.h"
@@ -114,10 +115,11 @@ struct Place {
   __device__ __forceinline__ bool in(int i) const { return at(i) < vecs; }
 };
 
-// 1 / sqrt(v) to the last place or so: the fast root and one step of Newton's.
+// 1 / sqrt(v) to the last place or so: the fast root and one step of Newton's, which would make
+// infinity times 0 of an infinite v (0).
 __device__ __forceinline__ float inv_sqrt(float v) {
   const float r = rsqrtf(v);
-  return r * fmaf(-0.5f * v * r, r, 1.5f);
+  return v <= FLT_MAX ? r * fmaf(-0.5f * (v * r), r, 1.5f) : r;
 }
 
 // The sums of N values over the row's threads, in all of them and in an order that does not

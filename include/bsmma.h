@@ -569,8 +569,9 @@ int64_t moe_step_workspace_bytes(int64_t T, int k, int64_t H, int64_t F);
  *     out = x_scale * x + y_scale * gate * drop(n(y) * weight + bias)  branch_leave, y = f(h)
  *   n is RMS (v / sqrt(mean v^2 + eps)), LAYER ((v - mean v) / sqrt(var v + eps), the variance
  *   around the mean, divided by H) or, for branch_leave, NONE (n(y) = y; no weight, no bias).
- *   Rows of H values; arithmetic, statistics and sums in FP32 (a row whose squares' sum leaves
- *   FP32's range is out of the operators' range), results rounded once.  The stream (x, out,
+ *   Rows of H values; arithmetic, statistics and sums in FP32, results rounded once.  (A row whose
+ *   squares' sum leaves FP32's range is out of the operators' range: an infinite sum is a factor of 0,
+ *   so that RMS makes 0 of the row's finite values and NaN of its infinities.)  The stream (x, out,
  *   dout, dres) has one type, the branch (h, y, gate, dh, dy) that type or, with an FP32
  *   stream, BF16.  weight and bias FP32 [H] or NULL (1, 0).
  *   gate [ceil(T / gate_rows)][H]: rows g * gate_rows .. of the stream use row g (1: one for

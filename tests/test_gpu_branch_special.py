@@ -80,3 +80,34 @@ def test_a_kept_nan_without_a_gradient(rows, p):
         dgate = bs.branch_leave_backward(dev(dout), dev(y), norm=kind, gate=dev(c["gate"]), gate_rows=rows, p=p,
                                          rng=dev(c["rng"]))[4]
         assert dgate[4 // rows, at].isnan()
+
+
+@pytest.mark.parametrize("T,H", [(7, 200), (7, 512), (7, 1024), (5, 4096), (5, 16384)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("value", [INF, -INF, 1e30])
+def test_an_infinite_sum_of_squares(T, H, dtype, value):
+    """RMS: the factor is 0, a finite value becomes 0 (the bias), an infinity NaN; other rows keep theirs."""
+    g = torch.Generator().manual_seed(H)
+    x, w, b = (torch.randn(s, generator=g) for s in ((T, H), (H,), (H,)))
+    x = dev(x.to(DT[dtype]))
+    w, b = dev(w), dev(b)
+    bad = x.clone()
+    bad[3, H // 2] = value
+    finite = bad[3].isfinite()
+    out = bs.branch_enter(bad, w, b)
+    clean = bs.branch_enter(x, w, b)
+    rows = [t for t in range(T) if t != 3]
+    assert torch.equal(out[rows], clean[rows])
+    assert torch.equal(out[3, finite], b.to(DT[dtype])[finite]) and out[3, ~finite].isnan().all()
+    left, h = bs.branch_leave(x, bad, w, b, norm="rms", next_norm="rms", next_weight=w)
+    assert torch.equal(left[3, finite], (x[3].float() + b).to(DT[dtype])[finite]) and left[3, ~finite].isnan().all()
+    assert h[rows].isfinite().all() and h[3].isfinite().all() == bool(finite.all())
+    # with the row's n of 0 nothing is added to its gradient or to the weight's
+    dh = torch.randn(T, H, generator=g).to(DT[dtype]).cuda()
+    dx, dw, _ = bs.branch_enter_backward(dh, bad, w, dres=x)
+    want = bs.branch_enter_backward(dh, x, w, dres=x)
+    assert torch.equal(dx[rows], want[0][rows])
+    if finite.all():
+        assert torch.equal(dx[3], x[3]) and dw.isfinite().all()
+    else:
+        assert dx[3].isnan().all()
