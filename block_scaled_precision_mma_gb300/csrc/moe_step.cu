@@ -17,9 +17,8 @@
 // four FMAs for 16 rows, and no weight.  Sums are FP32.
 //
 // First launch, for codes: the tokens in FP16.  Every block of the other two makes the table of who
-// takes what (the chosen experts and their columns) for itself from the ids, in its ring's place; it
-// does so, and fills its ring, before it waits for the launch ahead of it.  (A table made by one
-// block of a launch ahead of them cost a call 1 to 2 us more, and BF16 a launch.)
+// takes what (the chosen experts and their columns) for itself from the ids, in its ring's place.  (A
+// table made by one block of a launch ahead of them cost a call 1 to 2 us more, and BF16 a launch.)
 // Second: units of 32 inner columns (32 rows of Wg and the 32 of Wu) of one expert; the warps share
 // out K and the rows, their sums meet in shared memory, and the inner row leaves in BF16, or
 // in FP16 with a power of two for each 32 values.  Gate and up rows are put into the upper and
@@ -27,7 +26,8 @@
 // too.  Third: units of 32 output columns over all chosen experts, the warps sharing out
 // (expert, K) in runs; a warp adds an expert's columns, times their tokens' weights, to its
 // tokens' sums, and the warps' sums are added in order.  Each starts under the one before
-// (programmatic launch), the third with its rings full when the inner rows are done.
+// (programmatic launch), but reads nothing before its own wait for it, not the ids nor the weights
+// either: what a launch further ahead wrote is there for certain only then.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -550,12 +550,8 @@ __global__ void __launch_bounds__(InCfg<FORM, NT, G>::kThreadsIn, 1) step_in_ker
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int part = warp % C::kParts, group = warp / C::kParts;
-  // BF16: this is the first launch.  Else the one ahead let this one start when all that was before
-  // itself had ended, so only the tokens are waited for, with the ring full.
-  if constexpr (F::kBf16) {
-    grid_dependency_wait();
-    grid_launch_dependents();
-  }
+  grid_dependency_wait();
+  grid_launch_dependents();
   build_table(table, *reinterpret_cast<TableScratch*>(smem), a, 8 * NT);
   static_assert(sizeof(TableScratch) <= C::kRing, "the ring's place");
 
@@ -574,7 +570,6 @@ __global__ void __launch_bounds__(InCfg<FORM, NT, G>::kThreadsIn, 1) step_in_ker
     return f < a.F ? f : 0;
   };
   if (warp >= kWarps) {
-    if constexpr (!F::kBf16) grid_dependency_wait();
     // What a unit's end needs beside the sums is asked for before them: lane t has the power of token t,
     // and the rows' INT8 scales are read ahead of the wait (read after it: 32 tokens, 32 experts of
     // 2048 x 2048 96 us for 77).
@@ -690,10 +685,6 @@ __global__ void __launch_bounds__(InCfg<FORM, NT, G>::kThreadsIn, 1) step_in_ker
   if (to_load) enter_unit();
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i) load();
-  if constexpr (!F::kBf16) {
-    grid_dependency_wait();
-    grid_launch_dependents();
-  }
 
   int at = 0, done = 0;
   Walk here;
@@ -766,10 +757,9 @@ __global__ void __launch_bounds__(kThreads, 1) step_out_kernel(const StepArgs a,
   float* totals = sums + kWarps * values;                                  // [2][token][32]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(blockIdx.x) % cluster, clusters = static_cast<int>(gridDim.x) / cluster;
-  // what the second launch waited for, the ids and w_out among it, was there before it let this one
-  // start; only the inner rows are waited for
   float* own = sums + warp * values;
   for (int i = lane; i < values; i += 32) own[i] = 0.f;
+  grid_dependency_wait();
   build_table(table, *reinterpret_cast<TableScratch*>(smem), a, 8 * NT);
   static_assert(sizeof(TableScratch) <= C::kRing, "the ring's place");
 
@@ -819,7 +809,6 @@ __global__ void __launch_bounds__(kThreads, 1) step_out_kernel(const StepArgs a,
   };
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i) load();
-  grid_dependency_wait();
 
   int at = 0, turn = 0;
   for (int u = static_cast<int>(blockIdx.x) / cluster; u < units; u += clusters, turn ^= 1) {
