@@ -908,7 +908,22 @@ __global__ void __launch_bounds__(kThreads, 1) step_out_kernel(const StepArgs a,
   if (cluster > 1) cluster_sync();   // the others have read this block's sums
 }
 
+// How the work is cut goes by a GB300's room, SMs and clusters of 1, 2, 4 and 8 blocks that run at one
+// time, as numbers: sizes and ids alone give the sums' order, and with it every bit, on a device with
+// more or less of it too, which only takes the units in other waves.
+constexpr int kRoom[4] = {152, 76, 36, 15};
+
 // Blocks that share a unit of the third launch: as many as make its last wave fullest.
+inline int cluster_shift(int64_t units) {
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < 4; ++i) {
+    const double waves = static_cast<double>((units + kRoom[i] - 1) / kRoom[i]) / (1 << i);
+    if (i == 0 || waves < 0.95 * least) least = waves, best = i;
+  }
+  return best;
+}
+
 template <int FORM, int NT>
 bsmma_status launch_out(const StepArgs& a, const DeviceInfo* dev, cudaStream_t stream) {
   using C = OutCfg<FORM, NT>;
@@ -926,28 +941,22 @@ bsmma_status launch_out(const StepArgs& a, const DeviceInfo* dev, cudaStream_t s
   cfg.dynamicSmemBytes = C::kBytes;
   cfg.stream = stream;
   cfg.attrs = attr;
-  double best = 0;
-  int shared = 1, active = 1;
-  for (int i = 0; i < 4; ++i) {
-    const int c = 1 << i;
-    int n = 0;   // clusters that run at one time
-    st = fit[i].get(dev->device, &n, [&](int* v) {
-      if (c == 1) {
-        *v = dev->sm_count;
-        return BSMMA_OK;
-      }
-      cudaLaunchConfig_t q = cfg;
-      q.gridDim = dim3(static_cast<unsigned>(c));
-      attr[1].val.clusterDim.x = static_cast<unsigned>(c);
-      q.attrs = attr + 1;
-      q.numAttrs = 1;
-      return cuda_ok(cudaOccupancyMaxActiveClusters(v, step_out_kernel<FORM, NT>, &q));
-    });
-    if (st != BSMMA_OK) return st;
-    if (n < 1) continue;
-    const double waves = static_cast<double>((units + n - 1) / n) / c;
-    if (i == 0 || waves < 0.95 * best) best = waves, shared = c, active = n;
-  }
+  const int shift = cluster_shift(units), shared = 1 << shift;
+  int active = 0;   // clusters that run at one time here
+  st = fit[shift].get(dev->device, &active, [&](int* v) {
+    if (shared == 1) {
+      *v = dev->sm_count;
+      return BSMMA_OK;
+    }
+    cudaLaunchConfig_t q = cfg;
+    q.gridDim = dim3(static_cast<unsigned>(shared));
+    attr[1].val.clusterDim.x = static_cast<unsigned>(shared);
+    q.attrs = attr + 1;
+    q.numAttrs = 1;
+    return cuda_ok(cudaOccupancyMaxActiveClusters(v, step_out_kernel<FORM, NT>, &q));
+  });
+  if (st != BSMMA_OK) return st;
+  if (active < 1) return BSMMA_ERR_CUDA;
   attr[1].val.clusterDim.x = static_cast<unsigned>(shared);
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(units, active) * shared));
   cfg.numAttrs = 2;
@@ -985,8 +994,8 @@ bsmma_status launch_step(StepArgs a, const DeviceInfo* dev, cudaStream_t stream)
   using F = Form<FORM>;
   const int64_t stages = (a.H + F::kStageK - 1) / F::kStageK;
   const int64_t wide_units = std::min<int64_t>(a.E, a.T * a.k) * ((a.F + 127) / 128);
-  bsmma_status st = stages < 24 && wide_units >= 2 * dev->sm_count ? launch_in<FORM, NT, 2>(a, dev, stream)
-                                                                   : launch_in<FORM, NT, 8>(a, dev, stream);
+  bsmma_status st = stages < 24 && wide_units >= 2 * kRoom[0] ? launch_in<FORM, NT, 2>(a, dev, stream)
+                                                              : launch_in<FORM, NT, 8>(a, dev, stream);
   if (st == BSMMA_OK) st = launch_out<FORM, NT>(a, dev, stream);
   count_launches(2);
   return st;

@@ -3,7 +3,8 @@
 // the entry points do on the host: which kernels they launch, in which order, from which
 // thread, on which device, and whether a kernel was set up on that device first.
 //
-// Device 0 has 152 SMs and room for 76 clusters, device 1 has 20 and 10.  As in CUDA, a kernel's
+// Device 0 has 152 SMs and room for 76 clusters, device 1 has 20 and 10 (or what a test says for
+// clusters of a size).  As in CUDA, a kernel's
 // shared-memory attribute belongs to one device, and a launch that asks for more than 48 KB
 // without it fails.
 #include <unistd.h>
@@ -24,6 +25,7 @@ enum { kLookup = 0, kLaunch = 1, kMalloc = 2, kFree = 3 };
 struct Event {
   int kind, thread, device;
   int64_t value;   // a launch's blocks, an allocation's address
+  int cluster;     // blocks of a launch's clusters
   std::string name;
 };
 struct Dim3 {
@@ -43,8 +45,24 @@ struct LaunchConfig {
   unsigned num_attrs;
 };
 
+// cudaLaunchAttribute
+struct LaunchAttribute {
+  int id, pad;
+  union {
+    Dim3 dim;
+    char bytes[64];
+  };
+};
+int cluster_of(const LaunchConfig* c) {
+  const LaunchAttribute* a = static_cast<const LaunchAttribute*>(c->attrs);
+  for (unsigned i = 0; i < c->num_attrs; ++i)
+    if (a[i].id == 4) return static_cast<int>(a[i].dim.x);   // cudaLaunchAttributeClusterDimension
+  return 1;
+}
+
 struct State {
   std::mutex mu;
+  std::map<std::pair<int, int>, int> clusters;       // (device, blocks) -> room for them
   std::map<const void*, std::string> names;
   std::map<std::pair<int, const void*>, int> smem;   // (device, kernel) -> attribute
   std::vector<Event> log;
@@ -67,10 +85,10 @@ int fail(int e) {
 void pause_thread() {
   if (g_delay_us) usleep(g_delay_us);
 }
-void record(int kind, int64_t value, const std::string& name) {
+void record(int kind, int64_t value, const std::string& name, int cluster = 1) {
   State& s = state();
   std::lock_guard<std::mutex> lk(s.mu);
-  s.log.push_back(Event{kind, t_thread, t_device, value, name});
+  s.log.push_back(Event{kind, t_thread, t_device, value, cluster, name});
 }
 bool set_up(const void* f, size_t smem) {
   State& s = state();
@@ -78,7 +96,7 @@ bool set_up(const void* f, size_t smem) {
   const auto it = s.smem.find({t_device, f});
   return smem <= 48 * 1024 || (it != s.smem.end() && static_cast<size_t>(it->second) >= smem);
 }
-int launch(const void* f, Dim3 grid, size_t smem) {
+int launch(const void* f, Dim3 grid, size_t smem, int cluster = 1) {
   if (!set_up(f, smem)) return fail(1);
   std::string name;
   {
@@ -86,7 +104,7 @@ int launch(const void* f, Dim3 grid, size_t smem) {
     std::lock_guard<std::mutex> lk(s.mu);
     name = s.names[f];
   }
-  record(kLaunch, grid.x, name);
+  record(kLaunch, grid.x, name, cluster);
   pause_thread();
   return 0;
 }
@@ -100,6 +118,12 @@ extern "C" {
 void fake_set_device(int d) { t_device = d; }
 void fake_set_delay_us(int us) { g_delay_us = us; }
 int fake_thread() { return t_thread; }
+void fake_set_clusters(int device, int blocks, int n) {
+  State& s = state();
+  std::lock_guard<std::mutex> lk(s.mu);
+  s.clusters[{device, blocks}] = n;
+}
+int fake_event_cluster(int i) { return state().log[i].cluster; }
 void fake_clear() {
   State& s = state();
   std::lock_guard<std::mutex> lk(s.mu);
@@ -151,7 +175,7 @@ int __cudaLaunchKernel(const void* f, Dim3 grid, Dim3, void**, size_t smem, void
 
 // ---- the runtime
 int cudaLaunchKernelExC(const LaunchConfig* c, const void* f, void**) {
-  return launch(f, c->grid, c->smem);
+  return launch(f, c->grid, c->smem, cluster_of(c));
 }
 int cudaGetLastError() {
   const int e = t_error;
@@ -174,7 +198,10 @@ int cudaFuncSetAttribute(const void* f, int, int value) {
 }
 int cudaOccupancyMaxActiveClusters(int* n, const void* f, const LaunchConfig* c) {
   if (!set_up(f, c->smem)) return fail(1);
-  *n = kSms[t_device] / 2;
+  State& s = state();
+  std::lock_guard<std::mutex> lk(s.mu);
+  const auto it = s.clusters.find({t_device, cluster_of(c)});
+  *n = it != s.clusters.end() ? it->second : kSms[t_device] / 2;
   return 0;
 }
 int cudaOccupancyMaxActiveBlocksPerMultiprocessorWithFlags(int* n, const void* f, int, size_t smem,
