@@ -562,10 +562,23 @@ def grouped_int8_gemm(X, sX, W, sW, m_sizes, out=None, dtype=torch.bfloat16, str
     return out
 
 
-def _here(t):
-    """`t` is on the current device, whose stream and kernels a call uses."""
-    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError("expected a CUDA tensor on the current device")
+def _here(*tensors):
+    """The addresses of tensors (None: none), all contiguous and on the current device, whose stream and
+    kernels a call uses."""
+    here, at = None, []
+    for t in tensors:
+        if t is None:
+            at.append(None)
+            continue
+        device = t.get_device()
+        if here is None and device >= 0:
+            here = torch._C._cuda_getDevice()
+        if device != here:
+            raise ValueError("expected a CUDA tensor on the current device")
+        if not t.is_contiguous():
+            raise ValueError("expected a contiguous tensor")
+        at.append(t.data_ptr())
+    return at
 
 
 NORMS = {"none": 0, "rms": 1, "layer": 2}
@@ -616,10 +629,9 @@ def branch_enter(x, weight=None, bias=None, norm="rms", eps=1e-6, fmt=None, out=
     if bias is not None:
         _expect(bias, torch.float32, (H,), "bias")
     out, scales = _operand(fmt, T, H, x, out, scales)
-    _here(x)
-    _check(load().branch_enter(_ptr(x), dtype, T, H, NORMS[norm], eps, _ptr(weight), _ptr(bias),
-                               OPERANDS[fmt], _ptr(out), _ptr(scales), _stream(stream)),
-           "branch_enter")
+    x_at, w_at, b_at, out_at, scales_at = _here(x, weight, bias, out, scales)
+    _check(load().branch_enter(x_at, dtype, T, H, NORMS[norm], eps, w_at, b_at, OPERANDS[fmt], out_at, scales_at,
+                               _stream(stream)), "branch_enter")
     return out if scales is None else (out, scales)
 
 
@@ -640,9 +652,8 @@ def branch_enter_backward(dh, x, weight=None, norm="rms", eps=1e-6, dres=None, b
     dbias = None
     if bias:
         dbias = torch.empty(H, dtype=torch.float32, device=x.device) if weight is None else torch.empty_like(weight)
-    _here(x)
-    _check(load().branch_enter_backward(_ptr(dh), h_dtype, _ptr(x), x_dtype, T, H, NORMS[norm], eps,
-                                        _ptr(weight), _ptr(dres), _ptr(dx), _ptr(dweight), _ptr(dbias),
+    dh_at, x_at, w_at, *rest = _here(dh, x, weight, dres, dx, dweight, dbias)
+    _check(load().branch_enter_backward(dh_at, h_dtype, x_at, x_dtype, T, H, NORMS[norm], eps, w_at, *rest,
                                         _stream(stream)), "branch_enter_backward")
     return dx, dweight, dbias
 
@@ -673,12 +684,11 @@ def branch_leave(x, y, weight=None, bias=None, norm="none", eps=1e-6, gate=None,
     fmt = fmt or _OPERAND_OF[y.dtype]
     if next_norm != "none":
         next_out, next_scales = _operand(fmt, T, H, x, next_out, next_scales)
-    _here(x)
-    _check(load().branch_leave(_ptr(x), x_dtype, _ptr(y), y_dtype, T, H, NORMS[norm], eps, _ptr(weight),
-                               _ptr(bias), _ptr(gate), gate_rows, x_scale, y_scale, p, _ptr(rng), _ptr(out),
-                               NORMS[next_norm], next_eps, _ptr(next_weight), _ptr(next_bias),
-                               OPERANDS[fmt], _ptr(next_out), _ptr(next_scales), _stream(stream)),
-           "branch_leave")
+    x_at, y_at, w_at, b_at, gate_at, rng_at, out_at, nw_at, nb_at, no_at, ns_at = _here(
+        x, y, weight, bias, gate, rng, out, next_weight, next_bias, next_out, next_scales)
+    _check(load().branch_leave(x_at, x_dtype, y_at, y_dtype, T, H, NORMS[norm], eps, w_at, b_at, gate_at, gate_rows,
+                               x_scale, y_scale, p, rng_at, out_at, NORMS[next_norm], next_eps, nw_at, nb_at,
+                               OPERANDS[fmt], no_at, ns_at, _stream(stream)), "branch_leave")
     if next_norm == "none":
         return out
     return (out, next_out) if next_scales is None else (out, next_out, next_scales)
@@ -706,11 +716,11 @@ def branch_leave_backward(dout, y, weight=None, bias=None, norm="none", eps=1e-6
     dweight = None if weight is None else torch.empty_like(weight)
     dbias = None if bias is None else torch.empty_like(bias)
     dgate = None if gate is None else torch.empty_like(gate, dtype=torch.float32)
-    _here(y)
-    _check(load().branch_leave_backward(_ptr(dout), x_dtype, _ptr(y), y_dtype, T, H, NORMS[norm], eps,
-                                        _ptr(weight), _ptr(bias), _ptr(gate), gate_rows, x_scale, y_scale,
-                                        p, _ptr(rng), _ptr(dy), _ptr(dx), _ptr(dweight), _ptr(dbias),
-                                        _ptr(dgate), _stream(stream)), "branch_leave_backward")
+    dout_at, y_at, w_at, b_at, gate_at, rng_at, *grads = _here(dout, y, weight, bias, gate, rng, dy, dx, dweight, dbias,
+                                                               dgate)
+    _check(load().branch_leave_backward(dout_at, x_dtype, y_at, y_dtype, T, H, NORMS[norm], eps, w_at, b_at, gate_at,
+                                        gate_rows, x_scale, y_scale, p, rng_at, *grads, _stream(stream)),
+           "branch_leave_backward")
     return dy, dout if dx is None else dx, dweight, dbias, dgate
 
 
@@ -745,9 +755,8 @@ def moe_step(x, ids, weights, w_in, w_out, s_in=None, s_out=None, fmt="bf16", ac
         _expect(s_in, torch.uint8, (E, 2 * F, H // 32), "s_in")
         _expect(s_out, torch.uint8, (E, H, F // 32), "s_out")
     out = _output(out, torch.bfloat16, (T, H), x, "out")
-    _here(x)
-    _check(load().moe_step(_ptr(x), T, H, _ptr(ids), _ptr(weights), k, E, F, OPERANDS[fmt], _ptr(w_in),
-                           _ptr(s_in), _ptr(w_out), _ptr(s_out), ACTIVATIONS[act], _ptr(out),
+    x_at, ids_at, weights_at, *experts, out_at = _here(x, ids, weights, w_in, s_in, w_out, s_out, out)
+    _check(load().moe_step(x_at, T, H, ids_at, weights_at, k, E, F, OPERANDS[fmt], *experts, ACTIVATIONS[act], out_at,
                            _stream(stream)), "moe_step")
     return out
 
@@ -764,9 +773,8 @@ def dropout(x, p, rng, out=None, stream=None):
     _rng(rng, p)
     dtype = _dtype_of(x, "x")
     out = _output(out, x.dtype, x.shape, x, "out")
-    _here(x)
-    _check(load().dropout(_ptr(x), dtype, x.numel(), p, _ptr(rng), _ptr(out), _stream(stream)),
-           "dropout")
+    x_at, rng_at, out_at = _here(x, rng, out)
+    _check(load().dropout(x_at, dtype, x.numel(), p, rng_at, out_at, _stream(stream)), "dropout")
     return out
 
 
