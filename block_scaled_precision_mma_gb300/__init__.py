@@ -606,12 +606,13 @@ def _rng(rng, p: float):
 
 
 def _gate(gate, gate_rows, y):
-    """The rows that share a row of the gate (all of them unless said)."""
+    """The rows that share a row of the gate (all of them unless said).  No rows need no gate, but the
+    one that all of them would share may be there."""
     T, H = y.shape
     rows = max(T, 1) if gate_rows is None else gate_rows
     if rows < 1:
         raise ValueError("gate_rows must be at least 1")
-    _expect(gate, y.dtype, (-(-T // rows), H), "gate")
+    _expect(gate, y.dtype, (1 if T == 0 and gate.shape == (1, H) else -(-T // rows), H), "gate")
     return rows
 
 
@@ -716,6 +717,8 @@ def branch_leave_backward(dout, y, weight=None, bias=None, norm="none", eps=1e-6
     dweight = None if weight is None else torch.empty_like(weight)
     dbias = None if bias is None else torch.empty_like(bias)
     dgate = None if gate is None else torch.empty_like(gate, dtype=torch.float32)
+    if T == 0 and gate is not None:
+        dgate.zero_()
     dout_at, y_at, w_at, b_at, gate_at, rng_at, *grads = _here(dout, y, weight, bias, gate, rng, dy, dx, dweight, dbias,
                                                                dgate)
     _check(load().branch_leave_backward(dout_at, x_dtype, y_at, y_dtype, T, H, NORMS[norm], eps, w_at, b_at, gate_at,

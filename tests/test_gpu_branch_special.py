@@ -111,3 +111,12 @@ def test_an_infinite_sum_of_squares(T, H, dtype, value):
         assert torch.equal(dx[3], x[3]) and dw.isfinite().all()
     else:
         assert dx[3].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_an_empty_batch_with_the_gate_of_all_rows(dtype):
+    x, gate, w = torch.empty(0, 64, dtype=DT[dtype]).cuda(), torch.ones(1, 64, dtype=DT[dtype]).cuda(), torch.ones(64).cuda()
+    out, h = bs.branch_leave(x, x, w, norm="rms", gate=gate, next_norm="rms")
+    assert out.shape == h.shape == (0, 64)
+    _, _, dw, _, dgate = bs.branch_leave_backward(x, x, w, norm="rms", gate=gate)
+    assert dgate.shape == (1, 64) and not dgate.any() and not dw.any()

@@ -92,3 +92,20 @@ def test_a_strided_tensor_is_refused(calls, name, bad):
     with pytest.raises(ValueError, match="contiguous"):
         getattr(bs, name)(**t, **more)
     assert not calls
+
+
+@pytest.mark.parametrize("rows", [None, 1, 100])
+def test_an_empty_batch_takes_the_gate_of_all_rows(calls, rows):
+    here = lambda *s, dtype=bf16: torch.ones(*s, dtype=dtype).as_subclass(Here)  # noqa: E731
+    x = here(0, H)
+    for gates in (0, 1):
+        gate = here(gates, H)
+        assert bs.branch_leave(x, x, gate=gate, gate_rows=rows).shape == (0, H)
+        dgate = bs.branch_leave_backward(x, x, gate=gate, gate_rows=rows)[4]
+        assert dgate.shape == (gates, H) and dgate.dtype == f32 and not dgate.any()
+    for bad in (here(2, H), here(1, H + 8), here(1, H, dtype=f32)):
+        with pytest.raises(ValueError, match="gate must be"):
+            bs.branch_leave(x, x, gate=bad, gate_rows=rows)
+    y = here(5, H)
+    with pytest.raises(ValueError, match="gate must be"):
+        bs.branch_leave(y, y, gate=here(1, H), gate_rows=4)
