@@ -86,3 +86,39 @@ def test_each_gradient_left_out(T, H, rows, kind, dtype, ydtype):
         for n, (buffer, got) in raw.items():
             assert intact(buffer)
             near(got, *want[n], got.dtype)
+
+
+@pytest.mark.parametrize("T,H,rows", [(30400, 1536, 7), (30400, 1536, 64), (30400, 4096, 7), (30400, 7168, 64),
+                                      (30400, 7168, 3000), (60000, 264, 3), (121600, 1000, 13), (6000, 8200, 7)])
+@pytest.mark.parametrize("kind,bias", [("rms", False), ("layer", True)])
+@pytest.mark.parametrize("dtype,ydtype", TYPES)
+def test_many_rows_and_gates_a_worker(T, H, rows, kind, bias, dtype, ydtype):
+    """A worker (at least 152 of them, at most 16 an SM) adds R <= T / 152 + 1 rows in a run, over several gates, and
+    a thread of the second launch at most 304 runs, eight threads a column: a sum's own error is below
+    (R + 312) 2^-24 of its terms' sizes, and a term's 2^-18, as a normed value's (3 products: 2^-22)."""
+    g = torch.Generator(device="cuda").manual_seed(T + H + rows)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    y = (rnd(T, H) * torch.exp(0.5 * rnd(H)) + 0.3 * rnd(H)).to(DT[ydtype])
+    w, b, gate = rnd(H), rnd(H) if bias else None, rnd(-(-T // rows), H).to(DT[ydtype])
+    dout = rnd(T, H).to(DT[dtype])
+    _, _, dw, db, dgate = bs.branch_leave_backward(dout, y, w, b, norm=kind, gate=gate, gate_rows=rows, y_scale=0.5)
+    v, at = y.double(), torch.arange(T, device="cuda") // rows
+    mean, r = ref.stats(v, kind, 1e-6)
+    n, size = (v - mean) * r, (v.abs() + v.abs().mean(1, keepdim=True)) * r
+    of = 0.5 * dout.double()
+    dz = of * gate.double()[at]
+    run = lambda rows: (rows + 312) * 2.0 ** -24 + 2.0 ** -18 + 2.0 ** -22  # noqa: E731
+
+    def close(got, want, tol):
+        bad = ~((got.double() - want).abs() <= tol + 2.0 ** -24 * want.abs())
+        assert not bad.any(), (int(bad.sum()), got[bad][:3], want[bad][:3], tol[bad][:3])
+
+    most = T // 152 + 1
+    close(dw, (dz * n).sum(0), run(most) * (dz.abs() * size).sum(0))
+    if bias:
+        close(db, dz.sum(0), run(most) * dz.abs().sum(0))
+    z, zsize = n * w, size * w.abs()
+    if bias:
+        z, zsize = z + b, zsize + b.abs()
+    sums = [torch.zeros_like(gate, dtype=torch.float64).index_add_(0, at, t) for t in (of * z, of.abs() * zsize)]
+    close(dgate, sums[0], run(rows) * sums[1])
