@@ -1,11 +1,12 @@
 // branch.cu -- the residual branch forward: the norm before a block (branch_enter), the step
 // after it (branch_leave) and dropout by itself.
 //
-// All of them are bound by DRAM, so every row is read once, kept in registers through its
-// reductions, and written once.  The norm of the next block is taken from the row while it is
-// there, and a product's operand (INT8 rows, MX codes with their scales) is made from the FP32
-// values of the norm, so that neither the normed row nor a second reading of the stream costs
-// any bytes.
+// DRAM is their floor, so every row is read once, kept in registers through its reductions, and
+// written once.  It bounds the others; rows of BF16 that become codes, or pass through two norms and
+// dropout, are held up by their instructions and by the chain of a row's reductions (half to two thirds
+// of the issue slots).  The norm of the next block is taken from the row while it is there, and a
+// product's operand (INT8 rows, MX codes with their scales) is made from the FP32 values of the norm,
+// so that neither the normed row nor a second reading of the stream costs any bytes.
 #include <algorithm>
 
 #include "branch.cuh"
@@ -135,7 +136,7 @@ __device__ __forceinline__ void store_mx_row(const Vals (&f)[V], const OperandAr
 }
 
 // The INT8 scale of a row's largest magnitude, and a piece's codes: the quotient rounded once, by
-// two fused corrections on the reciprocal (as int8_quantize takes it) where nothing of them
+// two fused corrections on the reciprocal (Markstein's, as int8_quantize takes it) where nothing of them
 // leaves FP32's range.
 struct Int8Scale {
   float s, inv;   // inv 0: outside that range
@@ -212,13 +213,14 @@ __device__ __forceinline__ int64_t row_of() {
 // Rows of up to 8192 values: at most 256 threads, registers for three or four blocks an SM.
 constexpr int kMaxThreads = 512, kShortThreads = 256;
 
-// A row a block (a warp), in registers.  16384 x 7168 BF16 into E4M3: 76 us, 356 MB at 4.7 TB/s, bound by
-// issuing (64% of the slots: 120 instructions for eight values, 40 of them what a row costs each
-// of its warps) and by the weights' loads (57% of the L1 cache's cycles); FP32 into BF16 16384 x 4096
-// 69 us, 403 MB at 5.8 TB/s.  Tried and slower: two pieces a thread (twice the warps, each with a row's
-// costs: 104 us, and a step with dropout, gate and two norms 208 for 179), two rows a block that share
-// the weights (87 us, 14 warps an SM), and rows in a ring of asynchronous copies, one (78) or two (86)
-// at a time, which widen the values anew in each pass.
+// A row a block (a warp), in registers.  16384 x 7168 BF16 into E4M3: 75 to 79 us, 356 MB at 4.5 to 4.7 TB/s
+// (E2M1 78; INT8, whose maximum is one more reduction of the row, 105).  What holds it up is a row's chain,
+// two reductions and a barrier, at 64% of the issue slots (120 instructions for eight values, 40 of them what
+// a row costs each of its warps), and the weights' loads (57% of the L1 cache's cycles); FP32 into
+// BF16 16384 x 4096 69 us, 403 MB at 5.8 TB/s.  Tried and slower: two pieces a thread (twice the warps, each
+// with a row's costs: 104 us, and a step with dropout, gate and two norms 208 for 179), two rows a block
+// that share the weights (87 us, 14 warps an SM), and rows in a ring of asynchronous copies, one (78) or
+// two (86) at a time, which widen the values anew in each pass.
 template <bool F32, bool WARP, bool SHORT, int V>
 __global__ void __launch_bounds__(SHORT ? kShortThreads : kMaxThreads, SHORT ? 4 : 2) enter_kernel(const EnterArgs p) {
   __shared__ float part[WARP ? 1 : 3 * 32];

@@ -9,7 +9,7 @@ namespace branch {
 namespace {
 
 // Workers: runs of rows, as many as fill the GPU's 152 SMs with the blocks that fit one (by
-// registers; at most two of them, 46479 rows of 1136 in BF16 took 181 us for 94).  A number of T and
+// registers; at most two of them, 46479 rows of 1136 in BF16 took 181 us for 96).  A number of T and
 // H alone, so that the sums' order, and with it every bit, is the same wherever the call runs.
 int workers_of(int64_t T, int64_t H) {
   const int64_t vecs = H / 8;

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kGradThreads<ROW>, 1) grad_kernel(const GradPa
   // Where registers allow, gate * weight (a factor of 1 without either), by which d becomes q, is held for
   // a gate's rows, or for all.  With a gate's gradient sg is then the sum of d n, which over a
   // gate's rows gives dgate, times the weight, and its part of dweight, times the gate.  (Taken from the L1
-  // cache for every row: 20000 rows of 5120 with dropout and a gate for 2048 of them 221 us, and 172.)
+  // cache for every row: 20000 rows of 5120 with dropout and a gate for 2048 of them 221 us, and 179.)
   constexpr bool HOLD = !LONG && !(BIAS && VF && !GATE);
   // With a bias there is the sum of d too, in sw's place; the parts of dweight and dbias are then added to
   // the worker's sums in memory after each gate's rows.
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kGradThreads<ROW>, 1) grad_kernel(const GradPa
 #pragma unroll
   for (int i = 0; i < V; ++i) next_v[i] = zero_raw<VF>(), next_d[i] = zero_raw<DF>();
   // Without sums of a gate's rows the gate may be another for each: it is fetched with the row (15000 x
-  // 7168, a gate a row, 272 us, and 356 when it is read at the row's turn) where registers allow.
+  // 7168, a gate a row, 275 us, and 356 when it is read at the row's turn) where registers allow.
   constexpr bool AHEAD = LEAVE && !GATE && HOLD && !VF;
   const bool each = LEAVE && !GATE && a.gate;
   Raw<VF> next_g[AHEAD ? V : 1];

@@ -3,7 +3,7 @@
 // What bounds it is reading the chosen experts' weights once, so the two products' kernels are
 // built around keeping their bytes in flight with few instructions a byte: one block of 16 warps
 // an SM, each warp with a ring of asynchronous copies of its own that runs on from one unit of
-// work to the next.
+// work to the next (and, in the first product, up to four warps more that finish units).
 //
 // The products use mma.sync with the weights as the 16-row operand and up to 8 * NT tokens as
 // columns: with a row or a few an expert the tensor cores wait for memory whatever their
@@ -14,15 +14,18 @@
 // what is below 2^-29 of the largest loses any.  (Widening to BF16 instead, by moving bits and a
 // multiplication, kept the integer pipe busy at 52% with DRAM at 38%: 363 MB of E4M3 experts
 // 115 us.)  The 32 K of a matrix step are one MX block, so a block's scale multiplies its sum,
-// four FMAs for 16 rows, and no weight.  Sums are FP32.
+// four FMAs for 16 rows, and no weight.  Sums are FP32.  The inner row is rounded once, to what the second
+// product's operand can be beside its weights: FP16 over a power of two for each 32 values with codes,
+// BF16 with BF16 weights, as it is between the grouped products (2 tokens, 1024 x 2048: 0.0024 off the 64-bit
+// value, and 0.0017 with an FP32 inner row, which is the output's own rounding).
 //
 // First launch, for codes: the tokens in FP16.  Every block of the other two makes the table of who
 // takes what (the chosen experts and their columns) for itself from the ids, in its ring's place.  (A
 // table made by one block of a launch ahead of them cost a call 1 to 2 us more, and BF16 a launch.)
-// Second: units of 32 inner columns (32 rows of Wg and the 32 of Wu) of one expert; the warps share
-// out K and the rows, their sums meet in shared memory, and the inner row leaves in BF16, or
-// in FP16 with a power of two for each 32 values.  Gate and up rows are put into the upper and
-// lower half of the same 16-row operand, so that the lane that has a gate's sum has its up's
+// Second: units of 32 inner columns (32 rows of Wg and the 32 of Wu) of one expert, or of 128 where
+// rows are short and units many; the warps share out K and the rows, their sums meet in shared
+// memory, and the inner row leaves in BF16, or in FP16 with a power of two for each 32 values.  Gate and
+// up rows are put into the upper and lower half of the same 16-row operand, so that the lane that has a gate's sum has its up's
 // too.  Third: units of 32 output columns over all chosen experts, the warps sharing out
 // (expert, K) in runs; a warp adds an expert's columns, times their tokens' weights, to its
 // tokens' sums, and the warps' sums are added in order.  Each starts under the one before
@@ -988,9 +991,10 @@ bsmma_status launch_step(StepArgs a, const DeviceInfo* dev, cudaStream_t stream)
   }
   // K over eight groups of warps where that leaves each three stages of a unit or more; short rows over
   // two, in units of four times the columns (what a unit costs beside its stages, and the groups' unequal
-  // shares: 29 tokens, 63 experts of 8640 x 544 in E5M2 392 and 288 us; 18 tokens, 14 experts of 4720 x
-  // 432 in INT8 69 and 54), as long as those are two for an SM or more: no more experts than E or slots
-  // are chosen
+  // shares: 29 tokens, 8 of 63 experts of 8640 x 544 in E5M2 494 and 369 us; 18 tokens, 7 of 14 experts of
+  // 4720 x 432 in INT8 72 and 60), as long as those are two for an SM or more: no more experts than E or
+  // slots are chosen.  (Longer rows in wide units: 32 tokens of INT8 experts of 2048 x 7168 500 and 535 us, 8
+  // of E2M1 experts of 14336 x 4096 199 and 222.)
   using F = Form<FORM>;
   const int64_t stages = (a.H + F::kStageK - 1) / F::kStageK;
   const int64_t wide_units = std::min<int64_t>(a.E, a.T * a.k) * ((a.F + 127) / 128);

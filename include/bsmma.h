@@ -548,8 +548,9 @@ bsmma_status moe_combine_backward(const void* dout, bsmma_dtype dtype, int64_t H
  *   product's operand, to BF16 (BF16 weights) or to FP16 over a power of two for each 32 values
  *   (codes); with codes x is taken as FP16 over a power of two for each token, which loses only
  *   what is below 2^-29 of the token's largest value (a sum has to stay in FP32's range with that
- *   value at 2^15).  The sum over j is FP32, rounded once.
- *   The sums' order depends on the sizes and the ids alone.
+ *   value at 2^15, and so has a block scale of w_out times the power of two of the inner values that it
+ *   meets).  The sum over j is FP32, rounded once.
+ *   The sums' order depends on the sizes and the ids alone, on every device.
  * Preconditions: T >= 0, k >= 1, T <= 32, T * k <= 1024, 1 <= E <= 1024; H and F at least one
  *   piece of 16 bytes of codes and whole ones (BF16: H, F % 8 == 0; INT8: % 16; MX: % 32) and
  *   at most 65536; 16-byte-aligned x, w_in, w_out and out, 4-byte-aligned ids, weights and
